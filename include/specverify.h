@@ -71,7 +71,8 @@ enum {
   SPEC_DEV_BAD_TOKEN = 5,    /* token id outside [0, vocab)                 */
   SPEC_DEV_TIMEOUT = 6,      /* a bounded device-side wait gave up          */
   SPEC_DEV_INTERNAL = 7,     /* a kernel's own layout precondition failed   */
-  SPEC_DEV_BAD_BLOCK = 8     /* a block-table entry outside the block pool  */
+  SPEC_DEV_BAD_BLOCK = 8,    /* a block-table entry outside the block pool  */
+  SPEC_DEV_BAD_PROB = 9      /* a probability outside [0, 1], or a row of 0 */
 };
 
 /* dtype codes */
@@ -376,6 +377,53 @@ int tree_attn_verify_paged(const void *q, const void *k_pages, const void *v_pag
                            size_t workspace_bytes, int32_t *dev_status, spec_stream_t stream);
 
 /* --------------------------------------------------------------------
+ * tree_attn_verify_window -- tree_attn_verify with a sliding window and
+ * sinks.  The pages have no counterpart to it: it serves target models whose
+ * layers attend to the last positions only, and caches that keep only those.
+ *   depth    [batch, n_nodes] int32 (from spec_build_tree*): node i sits at
+ *            position prefix_len[b] + depth[b,i] (a depth outside
+ *            [0, n_nodes) counts as the nearest bound)
+ *   window   >= 1: a node at position x sees the positions x - window + 1 ..
+ *            x (itself included), and
+ *   sinks    >= 0: the positions 0 .. sinks - 1, whatever its own
+ * among the keys tree_attn_verify shows it: prefix rows 0 .. prefix_len[b]-1
+ * (positions of the same number) and its ancestors-or-itself (anc_mask).  A
+ * node that sees nothing (an empty anc_mask and an empty prefix) gets zeros.
+ * Prefix rows that no node sees, [sinks, prefix_len[b] - window], are not
+ * read for the result and may hold anything.  One token of ordinary decoding
+ * is a tree of one node.
+ * The work is that of the visible keys.  bf16 with head_dim 128 and up to
+ * 128 query heads per KV head runs on the tensor cores, all else on CUDA
+ * cores.  Everything else as tree_attn_verify; in addition batch * hkv <=
+ * 65535 and batch * hkv * s_max <= 2^30 (SPEC_ERR_UNSUPPORTED).
+ *   workspace  device scratch of tree_attn_window_workspace_bytes() bytes
+ *            (16-byte aligned, uninitialised; may be NULL when that size is
+ *            0; calls that may overlap on the GPU, two captured graphs among
+ *            them, need separate ones)
+ *
+ * tree_attn_verify_window_paged -- the same over a paged prefix cache with
+ * the arguments of tree_attn_verify_paged.  Entries of blocks that hold no
+ * visible position are not read (kv_pages_free drops them).
+ * ------------------------------------------------------------------ */
+size_t tree_attn_window_workspace_bytes(int dtype, int batch, int n_nodes, int hq, int hkv,
+                                        int head_dim, int max_prefix, int window, int sinks);
+int tree_attn_verify_window(const void *q, const void *k_cache, const void *v_cache,
+                            const void *k_tree, const void *v_tree, const int32_t *prefix_len,
+                            const int32_t *depth, const uint64_t *anc_mask, void *out, int dtype,
+                            int batch, int n_nodes, int hq, int hkv, int head_dim, int s_max,
+                            int max_prefix, int window, int sinks, float scale, void *workspace,
+                            size_t workspace_bytes, int32_t *dev_status, spec_stream_t stream);
+int tree_attn_verify_window_paged(const void *q, const void *k_pages, const void *v_pages,
+                                  const int32_t *block_table, int block_size, int num_blocks,
+                                  int max_blocks, const void *k_tree, const void *v_tree,
+                                  const int32_t *prefix_len, const int32_t *depth,
+                                  const uint64_t *anc_mask, void *out, int dtype, int batch,
+                                  int n_nodes, int hq, int hkv, int head_dim, int max_prefix,
+                                  int window, int sinks, float scale, void *workspace,
+                                  size_t workspace_bytes, int32_t *dev_status,
+                                  spec_stream_t stream);
+
+/* --------------------------------------------------------------------
  * tree_attn_verify_noalloc -- tree_attn_verify without a caller workspace.
  * The pages have no counterpart to this entry point; it exists for callers
  * that cannot allocate device memory: a plugin inside a host runtime that
@@ -509,6 +557,50 @@ int spec_accept(int mode, const void *logits, const void *draft_logits, int dtyp
                 int32_t *bonus, int32_t *dev_status, spec_stream_t stream);
 
 /* --------------------------------------------------------------------
+ * spec_verify_probs -- the rejection modes of spec_accept from given
+ * probabilities and given uniform numbers ("Drafters: ...", section "Why the
+ * answer does not change"): for callers whose target and draft distributions
+ * have been cut or renormalised (temperature, top-k, top-p), or whose random
+ * numbers come from a generator of their own.  A chain of drafted tokens is
+ * a tree whose nodes have one child each.
+ *
+ *   target_probs [batch, n_nodes, vocab] (f32 or bf16), 16-byte aligned: the
+ *            target's distribution after each node, values in [0, 1], rows
+ *            taken to sum to 1 as they are
+ *   draft_probs  the same for the drafter, where the children of a node are
+ *            independent draws from its row; or NULL where they are
+ *            deterministic
+ *   tok, parents, first_child, next_sibling [batch, n_nodes] int32 (as
+ *            spec_accept)
+ *   u_accept [batch, n_nodes] f32 in [0, 1): the number node c is tested with
+ *   u_bonus  [batch] f32 in [0, 1): the bonus token's
+ * Rule, from the root, the children c of node v in their order, with the
+ * residual weights w = target_probs[b,v], their mass W = 1:
+ *   draft_probs NULL: c is accepted iff u_c * W < w(tok[c]); otherwise W <-
+ *       W - w(tok[c]) and w(tok[c]) <- 0;
+ *   else: c is accepted iff u_c * W * q_v(tok[c]) < w(tok[c]); otherwise w <-
+ *       max(0, w / W - q_v), W <- sum of w.
+ * An accepted child is the next v.  Where none is accepted, the bonus is the
+ * lowest token x with w(0) + .. + w(x) > u_bonus[b] * (sum of w); weights
+ * that are all zero give way to target_probs[b,v].
+ * Outputs as spec_accept.  Sums are exact to 2^-60 a value and independent
+ * of their order; the tests of the drafts are float64.  Numbers outside
+ * [0, 1) count as the nearest number inside, NaN as 0.
+ * dev_status: SPEC_DEV_BAD_TOKEN (a child's token outside [0, vocab): never
+ * accepted, nothing subtracted), SPEC_DEV_BAD_PARENTS (links that disagree
+ * with parents[]: the node is taken to have no further child),
+ * SPEC_DEV_CAPACITY (a path longer than path_cap: the path ends there),
+ * SPEC_DEV_BAD_PROB (a value outside [0, 1], NaN among them: counts as 0; or
+ * a row of zeros to draw the bonus from: token 0).
+ * ------------------------------------------------------------------ */
+int spec_verify_probs(const void *target_probs, const void *draft_probs, int dtype, int batch,
+                      int n_nodes, int vocab, const int32_t *tok, const int32_t *parents,
+                      const int32_t *first_child, const int32_t *next_sibling,
+                      const float *u_accept, const float *u_bonus, int path_cap, int32_t *acc_len,
+                      int32_t *acc_path, int32_t *bonus, int32_t *dev_status,
+                      spec_stream_t stream);
+
+/* --------------------------------------------------------------------
  * spec_accept_commit -- spec_accept and kv_commit (contiguous cache) in one
  * launch: each sequence's cluster, once it has taken its path, copies that
  * path's K/V rows into the cache and advances prefix_len.  The pages'
@@ -568,6 +660,89 @@ int kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table, in
                     const int32_t *acc_len, const int32_t *acc_path, int path_cap,
                     const int32_t *prefix_len, int32_t *prefix_len_out, int32_t *dev_status,
                     spec_stream_t stream);
+
+/* --------------------------------------------------------------------
+ * kv_pages_* -- the life of a paged cache's blocks on the device (block
+ * tables of paged KV: "5.3 Medusa、EAGLE 与 MTP", section 8): what
+ * kv_commit_paged leaves to the caller's allocator, without a round trip to
+ * the host.  All calls are asynchronous and capturable.
+ *
+ *   block_table [batch, max_blocks] int32: entry j of a sequence names the
+ *            block of positions [j * block_size, (j + 1) * block_size);
+ *            negative: none.  batch <= SPEC_PAGES_MAX_BATCH
+ *   ref_count   [num_blocks] int32: the table entries that name a block, and
+ *            whatever else the caller counts (a pinned prompt); <= 0: free
+ *   prefix_len  [batch] int32
+ * Every call reads a table and counts and writes table_out and ref_count_out,
+ * which may be the same buffers (where a call says so) or others, but may
+ * not overlap them in part (SPEC_ERR_INVALID_ARG).  Results depend on the
+ * inputs alone: blocks are handed out lowest id first.  An entry at or past
+ * num_blocks sets SPEC_DEV_BAD_BLOCK; fork, free and compact drop it.
+ *
+ * kv_pages_fork -- sequence i of the new batch continues sequence parent[i]
+ * of the old one and shares its blocks; parent[i] < 0: an empty slot.  One
+ * call forks samples, reorders beams and ends requests (an old sequence that
+ * no new one continues loses its references).
+ *   parent   [batch_out] int32 (at or past batch: SPEC_DEV_BAD_PARENTS, an
+ *            empty slot)
+ *   table_out [batch_out, max_blocks] and prefix_len_out [batch_out]: not
+ *            their inputs; ref_count_out may be ref_count
+ *
+ * kv_pages_free -- drops every entry whose page begins at or past position
+ * prefix_len + spare, and with a window (0: none) every entry whose page
+ * holds neither a sink (a position below sinks) nor a position past
+ * prefix_len - window (one that a node at prefix_len sees, or the next to be
+ * written).  So it lets go of what has left the window, of pages reserved
+ * and not used, and of everything of a sequence of length 0.
+ * Both outputs may be their inputs.
+ *
+ * kv_pages_reserve -- makes positions prefix_len .. prefix_len + need - 1 of
+ * every sequence writable: entries without a block get a free one, and a
+ * block that other entries share is replaced by a copy (the rows of
+ * positions below prefix_len; all layers, heads, K and V), in the order of
+ * (sequence, page), so that the last of a block's holders keeps it.  What
+ * kv_commit_paged and the model's own K/V writes need before them.
+ *   need     [batch] int32 (<= 0: nothing for that sequence)
+ * A sequence that would pass max_blocks * block_size is left out
+ * (SPEC_DEV_CAPACITY); with too few free blocks for all of the others the
+ * call changes nothing (SPEC_DEV_CAPACITY).  Both outputs may be their
+ * inputs.
+ *
+ * kv_pages_compact -- moves the used blocks at or past U = number of used
+ * blocks into the free ones below U, both in order of id, and renames the
+ * table's entries: the pool past U is then unused.  An entry naming a block
+ * of count 0 is dropped (SPEC_DEV_BAD_BLOCK).
+ *   n_used   [1] int32 out: U
+ *   remap    [num_blocks] int32 out: new id of each block, -1 if unused (may
+ *            be NULL; for holders outside the table)
+ * Both outputs may be their inputs.
+ *
+ * k_pages, v_pages [n_layers, num_blocks, hkv, block_size, head_dim] (16-byte
+ * aligned, elem_bytes 2 or 4, head_dim * elem_bytes % 16 == 0).  workspace:
+ * kv_pages_workspace_bytes() bytes, 16-byte aligned, uninitialised; calls
+ * that may overlap on the GPU need separate ones.
+ * ------------------------------------------------------------------ */
+#define SPEC_PAGES_MAX_BATCH 4096
+size_t kv_pages_workspace_bytes(int batch, int max_blocks, int num_blocks);
+int kv_pages_fork(const int32_t *block_table, const int32_t *prefix_len, const int32_t *parent,
+                  int batch, int batch_out, int max_blocks, int num_blocks,
+                  const int32_t *ref_count, int32_t *table_out, int32_t *prefix_len_out,
+                  int32_t *ref_count_out, int32_t *dev_status, spec_stream_t stream);
+int kv_pages_free(const int32_t *block_table, const int32_t *prefix_len, int batch, int max_blocks,
+                  int block_size, int num_blocks, int window, int sinks, int spare,
+                  const int32_t *ref_count, int32_t *table_out, int32_t *ref_count_out,
+                  int32_t *dev_status, spec_stream_t stream);
+int kv_pages_reserve(void *k_pages, void *v_pages, int elem_bytes, int n_layers, int hkv,
+                     int head_dim, int block_size, int num_blocks, const int32_t *block_table,
+                     int batch, int max_blocks, const int32_t *prefix_len, const int32_t *need,
+                     const int32_t *ref_count, int32_t *table_out, int32_t *ref_count_out,
+                     void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                     spec_stream_t stream);
+int kv_pages_compact(void *k_pages, void *v_pages, int elem_bytes, int n_layers, int hkv,
+                     int head_dim, int block_size, int num_blocks, const int32_t *block_table,
+                     int batch, int max_blocks, const int32_t *ref_count, int32_t *table_out,
+                     int32_t *ref_count_out, int32_t *n_used, int32_t *remap, void *workspace,
+                     size_t workspace_bytes, int32_t *dev_status, spec_stream_t stream);
 
 #ifdef __cplusplus
 }

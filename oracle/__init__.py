@@ -16,6 +16,7 @@ heads      Medusa residual heads, LM head, top-s selection
 attention  tree attention, explicit per node over prefix + ancestors
 accept     greedy / typical / rejection acceptance and the bonus token
 commit     copy of the accepted path's K/V rows into the cache
+pages      forking, reserving, freeing and compacting a paged cache's blocks
 expand     one confidence-product expansion round (EAGLE-2 style)
 expected   expected accepted length (closed forms on the pages)
 rng        Philox4x32-10 counter-based generator

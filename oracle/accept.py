@@ -349,3 +349,41 @@ def accept_reject_stochastic(logits, draft_logits, tok, first_child, next_siblin
         paths.append(path)
     acc_len, acc_path, bon = _pack(paths, bonus, path_cap)
     return acc_len, acc_path, bon, near
+
+
+def accept_probs(probs, draft_probs, tok, first_child, next_sibling, u_accept, u_bonus, path_cap):
+    """The rejection rule from given probabilities [B,N,V] (draft_probs None:
+    deterministic siblings) and given uniform numbers u_accept [B,N], u_bonus
+    [B], float64: from the root, child c of v is kept iff u_c * W * q(tok) <
+    w(tok), w = p_v and W = 1 on arrival (q = 1 for deterministic siblings);
+    a rejection removes tok (W loses its probability), or leaves w = max(0,
+    w / W - q), W = sum w.  The bonus is the lowest token whose running sum
+    of w exceeds u * sum w (w = p_v where nothing is left)."""
+    B = probs.shape[0]
+    paths, bonus = [], []
+    for b in range(B):
+        v, path = 0, [0]
+        while True:
+            p = probs[b, v].astype(np.float64)
+            w, W, hit = p.copy(), 1.0, None
+            for c in _children(first_child[b], next_sibling[b], v):
+                t, u = int(tok[b, c]), float(u_accept[b, c])
+                q = None if draft_probs is None else draft_probs[b, v].astype(np.float64)
+                if u * W * (1.0 if q is None else q[t]) < w[t]:
+                    hit = c
+                    break
+                if q is None:
+                    W, w[t] = max(0.0, W - w[t]), 0.0
+                else:
+                    w = np.maximum(0.0, w / W - q) if W > 0 else np.zeros_like(w)
+                    W = w.sum()
+            if hit is None:
+                break
+            v = hit
+            path.append(v)
+        if not w.sum() > 0:
+            w = p
+        run = np.cumsum(w)
+        bonus.append(int(np.searchsorted(run, float(u_bonus[b]) * run[-1], side="right")))
+        paths.append(path)
+    return _pack(paths, bonus, path_cap)

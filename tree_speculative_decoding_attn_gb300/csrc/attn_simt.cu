@@ -54,13 +54,17 @@ __device__ __forceinline__ void stage_rows(float *dst, const T *src, int nrows) 
   }
 }
 
-template <typename T, int D, int MW>
+// WIN: only the sinks and the window of the prefix are staged, and each row
+// masks them (and, for windows shorter than the tree, its ancestors) by its
+// own position.  Splits then share out those tiles: chunk keys of them each.
+template <typename T, int D, int MW, bool WIN>
 __global__ void __launch_bounds__(kWarps * 32)
     attn_simt_kernel(const T *__restrict__ q, const T *__restrict__ kc, const T *__restrict__ vc,
                      const T *__restrict__ kt, const T *__restrict__ vt,
                      const int32_t *__restrict__ prefix_len, const uint64_t *__restrict__ anc,
                      T *__restrict__ out, int N, int Hq, int Hkv, int s_max, int max_prefix,
-                     int splits, int chunk, float scale_log2, float *ws, int32_t *status, const sv::KvPages pg) {
+                     int splits, int chunk, float scale_log2, float *ws, int32_t *status, const sv::KvPages pg,
+                     const sv::Window win) {
   constexpr int DL = D / 32;  // output dims per lane
   __shared__ float sK[kKeyTile * (D + 1)];
   __shared__ float sV[kKeyTile * D];
@@ -102,15 +106,30 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int k0 = split * chunk;
   const int k1 = min(P, k0 + chunk);
   const bool with_tree = split == splits - 1;
-  const int n_prefix_tiles = k1 > k0 ? (k1 - k0 + kKeyTile - 1) / kKeyTile : 0;
+  int n_prefix_tiles = k1 > k0 ? (k1 - k0 + kKeyTile - 1) / kKeyTile : 0;
+  sv::WinSpan span{};
+  int pos[kRowsPerWarp];  // WIN: the rows' positions
+  if constexpr (WIN) {
+    span = sv::win_span(win.window, win.sinks, P, kKeyTile, pg.table ? kKeyTile : 1);
+    n_prefix_tiles = max(0, min(span.n_tiles - k0 / kKeyTile, chunk / kKeyTile));
+#pragma unroll
+    for (int k = 0; k < kRowsPerWarp; ++k) {
+      const int r = rg * kRowsPerCta + warp * kRowsPerWarp + k;
+      pos[k] = P + (r < R ? sv::win_depth(win, (int64_t)b * N + r / G, N) : 0);
+    }
+  }
   const int n_tree_tiles = with_tree ? (N + kKeyTile - 1) / kKeyTile : 0;
   const int64_t kv_base = ((int64_t)b * Hkv + kvh) * s_max * D;
   const int64_t kt_base = ((int64_t)b * Hkv + kvh) * N * D;
 
   for (int tile = 0; tile < n_prefix_tiles + n_tree_tiles; ++tile) {
     const bool tree = tile >= n_prefix_tiles;
-    const int t0 = tree ? (tile - n_prefix_tiles) * kKeyTile : k0 + tile * kKeyTile;
-    const int nvalid = tree ? min(kKeyTile, N - t0) : min(kKeyTile, k1 - t0);
+    const int t0 = tree  ? (tile - n_prefix_tiles) * kKeyTile
+                   : WIN ? sv::win_key0(span, k0 / kKeyTile + tile, kKeyTile)
+                         : k0 + tile * kKeyTile;
+    const int nvalid = tree  ? min(kKeyTile, N - t0)
+                       : WIN ? sv::win_keys(span, P, k0 / kKeyTile + tile, kKeyTile)
+                             : min(kKeyTile, k1 - t0);
     __syncthreads();  // previous tile fully consumed (and sQ written on entry)
     if (tree) {
       stage_rows<T, D, D + 1>(sK, kt + kt_base + (int64_t)t0 * D, nvalid);
@@ -122,6 +141,17 @@ __global__ void __launch_bounds__(kWarps * 32)
       const T *vs = pg.table ? vc + (int64_t)(row < 0 ? 0 : row) * D : vc + kv_base + (int64_t)t0 * D;
       stage_rows<T, D, D + 1>(sK, ks, row < 0 ? 0 : nvalid);
       stage_rows<T, D, D>(sV, vs, row < 0 ? 0 : nvalid);
+    }
+    int kpos = 0;  // WIN: this lane's key's position
+    if constexpr (WIN) {
+      kpos = !tree ? t0 + lane : lane < nvalid ? P + sv::win_depth(win, (int64_t)b * N + t0 + lane, N) : 0;
+      // a key of the tile's first block that the root no longer sees: its V
+      // may be anything, and 0 * V has to be 0
+      if (!tree && t0 < span.lo) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < (min(span.lo, t0 + kKeyTile) - max(t0, win.sinks)) * D; e += kWarps * 32)
+          sV[(max(t0, win.sinks) - t0) * D + e] = 0.f;
+      }
     }
     __syncthreads();
     // The warp's rows go through each step together, so their dot products,
@@ -147,7 +177,8 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
       for (int w = 1; w < MW; ++w)
         if ((t0 >> 6) == w) word = am[k][w];
-      const bool vis = lane < nvalid && (!tree || ((word >> ((t0 & 63) + lane)) & 1ull));
+      bool vis = lane < nvalid && (!tree || ((word >> ((t0 & 63) + lane)) & 1ull));
+      if constexpr (WIN) vis = vis && (kpos < win.sinks || pos[k] - kpos < win.window);
       sc[k] = vis ? sc[k] * scale_log2 : -INFINITY;
       mx[k] = sc[k];
     }
@@ -252,11 +283,13 @@ int launch_simt(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const 
                 cudaStream_t stream) {
   const int R = s.n_nodes * (s.hq / s.hkv);
   dim3 grid((R + kRowsPerCta - 1) / kRowsPerCta, p.splits, s.batch * s.hkv);
-  auto kern = s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1> : attn_simt_kernel<T, D, 4>;
+  auto kern = s.window > 0 ? (s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1, true> : attn_simt_kernel<T, D, 4, true>)
+                           : (s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1, false> : attn_simt_kernel<T, D, 4, false>);
   kern<<<grid, kWarps * 32, 0, stream>>>((const T *)q, (const T *)kc, (const T *)vc, (const T *)kt, (const T *)vt,
                                          prefix_len, anc, (T *)out, s.n_nodes, s.hq, s.hkv, s.s_max, s.max_prefix,
                                          p.splits, p.chunk, scale * 1.4426950408889634f, (float *)ws, status,
-                                         sv::KvPages{s.block_table, s.block_size, s.max_blocks, s.num_blocks});
+                                         sv::KvPages{s.block_table, s.block_size, s.max_blocks, s.num_blocks},
+                                         sv::Window{s.depth, s.window, s.sinks});
   return sv_launch_status();
 }
 
@@ -278,11 +311,17 @@ SvAttnPlan sv_attn_simt_plan(const SvAttnShape &s, int num_splits) {
   p.use_tc = 0;
   const int R = s.n_nodes * (s.hq / s.hkv);
   const int base = ((R + kRowsPerCta - 1) / kRowsPerCta) * s.batch * s.hkv;
-  const int max_useful = s.max_prefix > 0 ? (s.max_prefix + kKeyTile - 1) / kKeyTile : 1;
+  // prefix keys that are read: with a window its own and the sinks, rounded up
+  // to the tiles that may hold them (each kind ends in a cut tile of its own)
+  const long long most = s.window > 0 ? (long long)s.window - 1 + kKeyTile + ((long long)s.sinks + kKeyTile - 1) / kKeyTile * kKeyTile
+                                      : s.max_prefix;
+  const long long all = s.window > 0 && s.max_prefix > 0 ? (long long)s.max_prefix + kKeyTile : s.max_prefix;
+  const int keys = (int)(most < all ? most : all);
+  const int max_useful = keys > 0 ? (keys + kKeyTile - 1) / kKeyTile : 1;
   int splits = num_splits > 0 ? num_splits : (2 * kSms + base - 1) / base;
   splits = splits < 1 ? 1 : (splits > max_useful ? max_useful : splits);
   if (splits > 64) splits = 64;
-  int chunk = s.max_prefix > 0 ? (s.max_prefix + splits - 1) / splits : 0;
+  int chunk = keys > 0 ? (keys + splits - 1) / splits : 0;
   chunk = (chunk + kKeyTile - 1) / kKeyTile * kKeyTile;
   p.splits = splits;
   p.chunk = chunk;

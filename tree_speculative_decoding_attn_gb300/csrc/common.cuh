@@ -132,6 +132,44 @@ __device__ __forceinline__ int kv_row(const KvPages &pg, int b, int hkv, int h, 
   return (blk * hkv + h) * pg.block_size + key % pg.block_size;
 }
 
+// Sliding window with sinks.  A node at depth d of a sequence with P
+// committed tokens sits at position P + d and sees position x iff x < sinks
+// or P + d - x < window.  The prefix keys that some node sees are then the
+// sinks [0, s_end) and the window [w0, P) of the root (deeper nodes see a
+// later part of it): both are cut into tiles, sinks first, and nothing in
+// between is read.  `align`: a window tile starts at a multiple of it (1, or
+// the tile size when a tile must not leave a cache block).
+struct Window {
+  const int32_t *depth;  // [batch, n_nodes]
+  int window, sinks;     // window >= 1, sinks >= 0
+};
+struct WinSpan {
+  int lo;     // first prefix key inside the root's window (<= P)
+  int w0;     // first key of the window tiles (<= lo)
+  int s_end;  // keys of the sink tiles (<= w0)
+  int n_sink, n_tiles;
+};
+__device__ __forceinline__ WinSpan win_span(int window, int sinks, int P, int tile, int align) {
+  WinSpan v;
+  v.lo = max(0, P - window + 1);
+  v.w0 = v.lo >= P ? P : v.lo / align * align;
+  v.s_end = min(sinks, v.w0);
+  v.n_sink = (v.s_end + tile - 1) / tile;
+  v.n_tiles = v.n_sink + (P - v.w0 + tile - 1) / tile;
+  return v;
+}
+// First key and key count of prefix tile i (0 <= i < n_tiles).
+__device__ __forceinline__ int win_key0(const WinSpan &v, int i, int tile) {
+  return i < v.n_sink ? i * tile : v.w0 + (i - v.n_sink) * tile;
+}
+__device__ __forceinline__ int win_keys(const WinSpan &v, int P, int i, int tile) {
+  return min(tile, (i < v.n_sink ? v.s_end : P) - win_key0(v, i, tile));
+}
+// Depths are 0 .. n_nodes - 1; anything else counts as the nearest of them.
+__device__ __forceinline__ int win_depth(const Window &w, int64_t i, int n_nodes) {
+  return min(max(__ldg(w.depth + i), 0), n_nodes - 1);
+}
+
 }  // namespace sv
 
 // Launch wrapper status helper (host).

@@ -35,6 +35,10 @@ struct SvAttnShape {
   // paged: s_max = max_blocks * block_size is each sequence's capacity)
   const int32_t *block_table;
   int block_size, max_blocks, num_blocks;
+  // sliding window (0: none) with `sinks` first positions always visible, and
+  // the nodes' depths [batch, n_nodes]
+  int window, sinks;
+  const int32_t *depth;
 };
 struct SvAttnPlan {
   int use_tc;        // 2 = pair (cta_group::2) kernel, 1 = tcgen05 kernel, 0 = CUDA-core kernel
@@ -43,6 +47,7 @@ struct SvAttnPlan {
   size_t ws_bytes;   // partials (0 when splits == 1)
 };
 SvAttnPlan sv_attn_plan(const SvAttnShape &s, int num_splits);
+SvAttnPlan sv_attn_window_plan(const SvAttnShape &s);  // s.window > 0
 bool sv_attn_tc_supported(const SvAttnShape &s);
 int sv_attn_tc_ragged_splits(const SvAttnShape &s, const int32_t *host_prefix);
 int sv_attn_simt(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const void *kc,
@@ -138,3 +143,26 @@ int sv_kv_commit(void *kc, void *vc, const void *kt, const void *vt, int elem_by
                  int batch, int hkv, int s_max, int n_nodes, int head_dim, const int32_t *acc_len,
                  const int32_t *acc_path, int path_cap, const int32_t *prefix_len,
                  int32_t *prefix_len_out, int32_t *status, cudaStream_t stream, SvPages pages = SvPages{});
+
+int sv_verify_probs(const void *p, const void *q, int dtype, int batch, int n_nodes, int vocab, const int32_t *tok,
+                    const int32_t *parents, const int32_t *first_child, const int32_t *next_sibling,
+                    const float *u_accept, const float *u_bonus, int path_cap, int32_t *acc_len, int32_t *acc_path,
+                    int32_t *bonus, int32_t *status, cudaStream_t stream);
+
+// The life of a paged cache's blocks (pages.cu).  vec_per_row = head_dim *
+// elem_bytes / 16.
+size_t sv_pages_ws_bytes(int batch, int max_blocks, int num_blocks);
+int sv_pages_fork(const int32_t *table, const int32_t *prefix_len, const int32_t *parent, int batch, int batch_out,
+                  int max_blocks, int num_blocks, const int32_t *ref, int32_t *table_out, int32_t *prefix_out,
+                  int32_t *ref_out, int32_t *status, cudaStream_t stream);
+int sv_pages_free(const int32_t *table, const int32_t *prefix_len, int batch, int max_blocks, int block_size,
+                  int num_blocks, int window, int sinks, int spare, const int32_t *ref, int32_t *table_out,
+                  int32_t *ref_out, int32_t *status, cudaStream_t stream);
+int sv_pages_reserve(void *k, void *v, int vec_per_row, int n_layers, int hkv, int block_size, int num_blocks,
+                     const int32_t *table, int32_t *table_out, int batch, int max_blocks, const int32_t *prefix_len,
+                     const int32_t *need, const int32_t *ref, int32_t *ref_out, void *workspace, int32_t *status,
+                     cudaStream_t stream);
+int sv_pages_compact(void *k, void *v, int vec_per_row, int n_layers, int hkv, int block_size, int num_blocks,
+                     const int32_t *table, int32_t *table_out, int batch, int max_blocks, const int32_t *ref,
+                     int32_t *ref_out, int32_t *n_used, int32_t *remap, void *workspace, int32_t *status,
+                     cudaStream_t stream);

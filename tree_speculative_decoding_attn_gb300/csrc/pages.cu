@@ -1,0 +1,475 @@
+// The pages of a paged K/V cache: forking, reserving (with copy-on-write),
+// freeing and compacting.  "5.3 Medusa、EAGLE 与 MTP", section 8, closing
+// remarks (block tables of paged KV); what the commit leaves to "the caller's
+// allocator".
+//
+// State, all in device memory and owned by the caller: block tables [batch,
+// max_blocks] (negative entry: no block) and one reference count per block
+// (the table entries that name it, plus whatever the caller adds).  A block
+// of count 0 is free; there is no free list, so the lowest free ids are found
+// by a scan and every result is a function of the inputs alone: integer
+// atomics count, their order changes nothing.
+//
+// fork and free move no rows: 4 bytes per table entry and per block, a few
+// microseconds of latency.  reserve and compact plan in one CTA (counts,
+// block-wide scans, a list of moves) and copy in a second launch over the
+// whole GPU, a programmatic dependent of the first; that one is bound by
+// HBM: two bytes moved per byte copied.
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kMaxBatch = 4096;   // rows of a table (a shared-memory word each)
+constexpr int kRange = 4096;      // blocks whose counts one CTA owns
+
+__device__ __forceinline__ int ld_relaxed(const int32_t *p) {
+  int v;
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Does a page of positions [r0, r0 + block_size) of a sequence of P rows
+// stay: does it begin below P + spare and, in a window, hold a sink or a
+// position that a node at P sees or that comes after it?
+__device__ __forceinline__ bool page_stays(long long r0, int block_size, long long P, int window, int sinks,
+                                           int spare) {
+  if (r0 >= P + spare) return false;
+  return window <= 0 || r0 < sinks || r0 + block_size > P - window + 1;
+}
+
+// fork (FORK) and free.  CTA c owns the counts of blocks [c kRange, +kRange):
+// it scans the whole table once, collects its blocks' changes in shared
+// memory and writes their counts.  free: the owner of an entry's block also
+// writes the entry, so the table may be changed in place: another CTA sees
+// the block's id, which is not its own, or -1.
+template <bool FORK>
+__global__ void __launch_bounds__(kThreads)
+    pages_refs_kernel(const int32_t *table, const int32_t *prefix_len, const int32_t *__restrict__ parent, int batch,
+                      int batch_out, int max_blocks, int block_size, int num_blocks, int window, int sinks, int spare,
+                      const int32_t *ref, int32_t *table_out, int32_t *prefix_out, int32_t *ref_out, int32_t *status) {
+  __shared__ int s_delta[kRange];
+  __shared__ int s_mult[FORK ? kMaxBatch : 1];  // continuations of an old sequence
+  const int lo = blockIdx.x * kRange, n = min(kRange, num_blocks - lo);
+  for (int i = threadIdx.x; i < n; i += kThreads) s_delta[i] = 0;
+  if constexpr (FORK)
+    for (int i = threadIdx.x; i < batch; i += kThreads) s_mult[i] = 0;
+  __syncthreads();
+  if constexpr (FORK) {
+    for (int i = threadIdx.x; i < batch_out; i += kThreads) {
+      const int p = parent[i];
+      if (p >= batch) {
+        sv::report(status, SPEC_DEV_BAD_PARENTS);
+      } else if (p >= 0) {
+        atomicAdd(&s_mult[p], 1);
+      }
+    }
+    __syncthreads();
+    // the new tables' rows, shared out over the CTAs
+    for (int i = blockIdx.x; i < batch_out; i += gridDim.x) {
+      const int p = parent[i];
+      const bool live = p >= 0 && p < batch;
+      for (int j = threadIdx.x; j < max_blocks; j += kThreads) {
+        int blk = live ? table[(int64_t)p * max_blocks + j] : -1;
+        if (blk < 0 || blk >= num_blocks) blk = -1;
+        table_out[(int64_t)i * max_blocks + j] = blk;
+      }
+      if (threadIdx.x == 0) prefix_out[i] = live ? prefix_len[p] : 0;
+    }
+  }
+  const int64_t total = (int64_t)batch * max_blocks;
+  for (int64_t e = threadIdx.x; e < total; e += kThreads) {
+    const int blk = FORK ? table[e] : ld_relaxed(table + e);
+    const int b = (int)(e / max_blocks);
+    const bool mine = blk >= lo && blk < lo + n;
+    if (blk >= num_blocks) sv::report(status, SPEC_DEV_BAD_BLOCK);
+    if constexpr (FORK) {
+      const int d = s_mult[b] - 1;
+      if (mine && d) atomicAdd(&s_delta[blk - lo], d);
+    } else {
+      const int j = (int)(e - (int64_t)b * max_blocks);
+      if (mine) {
+        const bool stays = page_stays((long long)j * block_size, block_size, prefix_len[b], window, sinks, spare);
+        if (!stays) atomicSub(&s_delta[blk - lo], 1);
+        table_out[e] = stays ? blk : -1;
+      } else if (blockIdx.x == 0 && (blk < 0 || blk >= num_blocks)) {
+        table_out[e] = -1;
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) ref_out[lo + i] = ref[lo + i] + s_delta[i];
+}
+
+// ---------------------------------------------------------------------------
+// reserve and compact
+// ---------------------------------------------------------------------------
+struct Move {
+  int src, dst, rows, pad;
+};
+// The workspace: header (number of moves), moves, then words per block and
+// per table entry.
+struct Space {
+  int *n_moves;
+  Move *moves;
+  int *a, *b, *c;  // [num_blocks] each
+  int *flag;       // [batch * max_blocks]
+};
+__host__ __device__ inline size_t space_layout(Space *s, void *base, long long batch, long long max_blocks,
+                                               long long num_blocks) {
+  uint8_t *p = static_cast<uint8_t *>(base);
+  size_t off = 16;
+  const size_t moves = off;
+  off += (size_t)(num_blocks > batch ? num_blocks : batch) * sizeof(Move);
+  const size_t words = off;
+  off += (size_t)num_blocks * 3 * 4;
+  const size_t flag = off;
+  off += (size_t)batch * max_blocks * 4;
+  if (s) {
+    s->n_moves = reinterpret_cast<int *>(p);
+    s->moves = reinterpret_cast<Move *>(p + moves);
+    s->a = reinterpret_cast<int *>(p + words);
+    s->b = s->a + num_blocks;
+    s->c = s->b + num_blocks;
+    s->flag = reinterpret_cast<int *>(p + flag);
+  }
+  return (off + 15) / 16 * 16;
+}
+
+// Exclusive prefix sum of v over the CTA's threads and the CTA's total.
+__device__ int cta_scan(int v, int *total) {
+  __shared__ int s_warp[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  *total = s_warp[kThreads / 32 - 1];
+  return x - v + (warp ? s_warp[warp - 1] : 0);
+}
+
+// The entries a call writes: the pages holding rows P .. P + need - 1 of each
+// sequence, numbered in (sequence, page) order.
+struct Writes {
+  const int *off;  // [batch + 1] in shared memory
+  int batch;
+  __device__ int seq_of(int i) const {  // the last sequence whose first entry is <= i (and that has any)
+    int lo = 0, hi = batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (off[mid] <= i) lo = mid; else hi = mid;
+    }
+    return lo;
+  }
+};
+
+constexpr int kKeep = 0, kFresh = 1, kCopy = 2;
+
+__global__ void __launch_bounds__(kThreads)
+    reserve_plan_kernel(const int32_t *table, int32_t *table_out, int batch, int max_blocks, int block_size,
+                        int num_blocks, const int32_t *__restrict__ prefix_len, const int32_t *__restrict__ need,
+                        const int32_t *ref, int32_t *ref_out, const Space ws, int32_t *status) {
+  __shared__ int s_off[kMaxBatch + 1];
+  __shared__ int s_moves;
+  sv::ptx::grid_dep_launch();
+  const int tid = threadIdx.x;
+  if (tid == 0) s_moves = 0;
+
+  // 1. how many entries each sequence writes
+  int n = 0;
+  for (int b0 = 0; b0 < batch; b0 += kThreads) {
+    const int b = b0 + tid;
+    int k = 0;
+    if (b < batch && need[b] > 0) {
+      const long long P = prefix_len[b], end = P + need[b];
+      if (P < 0 || end > (long long)max_blocks * block_size)
+        sv::report(status, SPEC_DEV_CAPACITY);
+      else
+        k = (int)((end - 1) / block_size - P / block_size) + 1;
+    }
+    int total;
+    const int at = cta_scan(k, &total);
+    if (b < batch) s_off[b] = n + at;
+    n += total;
+  }
+  if (tid == 0) s_off[batch] = n;
+  __syncthreads();
+  const Writes wr{s_off, batch};
+  auto entry = [&](int i, int *b, int *j) -> int64_t {
+    *b = wr.seq_of(i);
+    *j = prefix_len[*b] / block_size + (i - s_off[*b]);
+    return (int64_t)*b * max_blocks + *j;
+  };
+
+  // 2. the writers of each shared block: how many, and which is the last
+  for (int i = tid; i < n; i += kThreads) {
+    int b, j;
+    const int blk = table[entry(i, &b, &j)];
+    if (blk >= num_blocks) sv::report(status, SPEC_DEV_BAD_BLOCK);
+    if (blk >= 0 && blk < num_blocks && ref[blk] > 1) {
+      ws.a[blk] = 0;
+      ws.b[blk] = -1;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    int b, j;
+    const int blk = table[entry(i, &b, &j)];
+    if (blk >= 0 && blk < num_blocks && ref[blk] > 1) {
+      atomicAdd(&ws.a[blk], 1);
+      atomicMax(&ws.b[blk], i);
+    }
+  }
+  __syncthreads();
+  // 3. what becomes of each entry.  Taken in order, a writer copies a block
+  // that others still hold: all of them if some other holder does not write,
+  // else all but the last.
+  int mine = 0;
+  for (int i = tid; i < n; i += kThreads) {
+    int b, j;
+    const int blk = table[entry(i, &b, &j)];
+    int f = kFresh;
+    if (blk >= 0 && blk < num_blocks) {
+      const int r = ref[blk];
+      f = r > 1 && !(__ldcg(&ws.a[blk]) >= r && __ldcg(&ws.b[blk]) == i) ? kCopy : kKeep;
+    }
+    ws.flag[i] = f;
+    mine += f != kKeep;
+  }
+  int wanted;
+  cta_scan(mine, &wanted);
+  // 4. the lowest free blocks, in order, as many as are wanted (each thread
+  // looks at one contiguous piece of the counts)
+  const int per = (num_blocks + kThreads - 1) / kThreads;
+  const int lo = min(num_blocks, tid * per), hi = min(num_blocks, lo + per);
+  int nfree = 0;
+  for (int i = lo; i < hi; ++i) nfree += ref[i] <= 0;
+  int all_free;
+  int at = cta_scan(nfree, &all_free);
+  const bool fits = wanted <= all_free;
+  if (!fits && tid == 0) sv::report(status, SPEC_DEV_CAPACITY);
+  for (int i = lo; i < hi && at < wanted; ++i)
+    if (ref[i] <= 0) ws.c[at++] = i;
+  // 5. tables and counts as they were, where they are not changed in place
+  if (table_out != table)
+    for (int64_t e = tid; e < (int64_t)batch * max_blocks; e += kThreads) table_out[e] = table[e];
+  if (ref_out != ref)
+    for (int i = tid; i < num_blocks; i += kThreads) ref_out[i] = ref[i];
+  __syncthreads();
+  // 6. hand the blocks out in entry order
+  if (fits) {
+    int base = 0;
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+      const int i = i0 + tid;
+      const int f = i < n ? ws.flag[i] : kKeep;
+      int total;
+      const int k = base + cta_scan(f != kKeep, &total);
+      base += total;
+      if (f == kKeep) continue;
+      int b, j;
+      const int64_t e = entry(i, &b, &j);
+      const int blk = ws.c[k];
+      const int old = table[e];
+      table_out[e] = blk;
+      ref_out[blk] = 1;
+      if (f == kCopy) {
+        atomicSub(&ref_out[old], 1);
+        const int rows = prefix_len[b] % block_size;
+        if (j == prefix_len[b] / block_size && rows > 0)  // rows in use before the first new one
+          ws.moves[atomicAdd(&s_moves, 1)] = Move{old, blk, rows, 0};
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) *ws.n_moves = s_moves;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    compact_plan_kernel(int block_size, int num_blocks, const int32_t *ref, int32_t *ref_out, int32_t *n_used,
+                        int32_t *remap, const Space ws) {
+  sv::ptx::grid_dep_launch();
+  const int tid = threadIdx.x;
+  const int per = (num_blocks + kThreads - 1) / kThreads;
+  const int lo = min(num_blocks, tid * per), hi = min(num_blocks, lo + per);
+  int used = 0;
+  for (int i = lo; i < hi; ++i) used += ref[i] > 0;
+  int U;
+  cta_scan(used, &U);
+  // the holes below U and the used blocks from U on, in order: as many of one as of the other
+  int holes = 0, high = 0;
+  for (int i = lo; i < hi; ++i) {
+    const bool u = ref[i] > 0;
+    holes += !u && i < U;
+    high += u && i >= U;
+  }
+  int m, m2;
+  int h = cta_scan(holes, &m), s = cta_scan(high, &m2);
+  for (int i = lo; i < hi; ++i) {
+    const bool u = ref[i] > 0;
+    if (!u && i < U) ws.moves[h++].dst = i;
+    if (u && i >= U) {
+      ws.moves[s].rows = block_size;
+      ws.moves[s++].src = i;
+    }
+    ws.a[i] = u ? i : -1;  // the new id of block i (those that move: below)
+  }
+  for (int i = lo; i < hi; ++i) ref_out[i] = max(ref[i], 0);
+  __syncthreads();
+  for (int k = tid; k < m; k += kThreads) {
+    const int src = ws.moves[k].src, dst = ws.moves[k].dst;
+    ws.a[src] = dst;
+    ref_out[dst] = ref[src];
+    ref_out[src] = 0;
+  }
+  if (tid == 0) {
+    *ws.n_moves = m;
+    *n_used = U;
+  }
+  if (remap) {
+    __syncthreads();
+    for (int i = lo; i < hi; ++i) remap[i] = ws.a[i];
+  }
+}
+
+// Copies the planned rows of every layer and KV head, K and V, 16 bytes a
+// thread and load; REMAP: also renames the table's entries.  A unit is up to
+// kPiece vectors of one (move, K or V, layer, head); the CTAs take them in
+// turn.
+constexpr int kCopyThreads = 256;
+constexpr int kInFlight = 4;
+constexpr int kPiece = kCopyThreads * kInFlight;
+template <bool REMAP>
+__global__ void __launch_bounds__(kCopyThreads)
+    pages_copy_kernel(uint4 *k_pages, uint4 *v_pages, int n_layers, int hkv, int block_size, int num_blocks,
+                      int vec_per_row, const Space ws, const int32_t *table, int32_t *table_out, int64_t n_entries,
+                      int32_t *status) {
+  sv::ptx::grid_dep_wait();
+  const int n_moves = *ws.n_moves;
+  const int64_t page_vec = (int64_t)block_size * vec_per_row;
+  const int pieces = (int)((page_vec + kPiece - 1) / kPiece);
+  const int64_t units = (int64_t)n_moves * 2 * n_layers * hkv * pieces;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int piece = (int)(u % pieces);
+    int64_t x = u / pieces;
+    const int h = (int)(x % hkv);
+    x /= hkv;
+    const int layer = (int)(x % n_layers);
+    x /= n_layers;
+    const int is_v = (int)(x & 1);
+    const Move mv = ws.moves[x >> 1];
+    const int64_t n = (int64_t)mv.rows * vec_per_row;
+    uint4 *pool = is_v ? v_pages : k_pages;
+    const int64_t layer0 = (int64_t)layer * num_blocks;
+    const uint4 *src = pool + ((layer0 + mv.src) * hkv + h) * page_vec;
+    uint4 *dst = pool + ((layer0 + mv.dst) * hkv + h) * page_vec;
+    const int64_t i0 = (int64_t)piece * kPiece + threadIdx.x;
+    uint4 r[kInFlight];
+#pragma unroll
+    for (int j = 0; j < kInFlight; ++j)
+      if (i0 + j * kCopyThreads < n) r[j] = src[i0 + j * kCopyThreads];
+#pragma unroll
+    for (int j = 0; j < kInFlight; ++j)
+      if (i0 + j * kCopyThreads < n) dst[i0 + j * kCopyThreads] = r[j];
+  }
+  if constexpr (REMAP) {
+    for (int64_t e = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; e < n_entries;
+         e += (int64_t)gridDim.x * kCopyThreads) {
+      const int blk = table[e];
+      int to = -1;
+      if (blk >= 0) {
+        to = blk < num_blocks ? ws.a[blk] : -1;
+        if (to < 0) sv::report(status, SPEC_DEV_BAD_BLOCK);
+      }
+      table_out[e] = to;
+    }
+  }
+}
+
+template <bool REMAP>
+int launch_copy(void *k, void *v, int n_layers, int hkv, int block_size, int num_blocks, int vec_per_row,
+                long long most_moves, const Space &ws, const int32_t *table, int32_t *table_out, int64_t n_entries,
+                int32_t *status, cudaStream_t stream) {
+  const long long page_vec = (long long)block_size * vec_per_row;
+  const long long units = most_moves * 2 * n_layers * hkv * ((page_vec + kPiece - 1) / kPiece);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units < 1 ? 1 : units > 152 * 8 ? 152 * 8 : units));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pages_copy_kernel<REMAP>, (uint4 *)k, (uint4 *)v, n_layers, hkv, block_size,
+                            num_blocks, vec_per_row, ws, table, table_out, n_entries, status) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t sv_pages_ws_bytes(int batch, int max_blocks, int num_blocks) {
+  return space_layout(nullptr, nullptr, batch, max_blocks, num_blocks);
+}
+
+static_assert(kMaxBatch == SPEC_PAGES_MAX_BATCH, "the header's limit");
+
+int sv_pages_fork(const int32_t *table, const int32_t *prefix_len, const int32_t *parent, int batch, int batch_out,
+                  int max_blocks, int num_blocks, const int32_t *ref, int32_t *table_out, int32_t *prefix_out,
+                  int32_t *ref_out, int32_t *status, cudaStream_t stream) {
+  pages_refs_kernel<true><<<(num_blocks + kRange - 1) / kRange, kThreads, 0, stream>>>(
+      table, prefix_len, parent, batch, batch_out, max_blocks, 1, num_blocks, 0, 0, 0, ref, table_out, prefix_out,
+      ref_out, status);
+  return sv_launch_status();
+}
+
+int sv_pages_free(const int32_t *table, const int32_t *prefix_len, int batch, int max_blocks, int block_size,
+                  int num_blocks, int window, int sinks, int spare, const int32_t *ref, int32_t *table_out,
+                  int32_t *ref_out, int32_t *status, cudaStream_t stream) {
+  pages_refs_kernel<false><<<(num_blocks + kRange - 1) / kRange, kThreads, 0, stream>>>(
+      table, prefix_len, nullptr, batch, 0, max_blocks, block_size, num_blocks, window, sinks, spare, ref, table_out,
+      nullptr, ref_out, status);
+  return sv_launch_status();
+}
+
+int sv_pages_reserve(void *k, void *v, int vec_per_row, int n_layers, int hkv, int block_size, int num_blocks,
+                     const int32_t *table, int32_t *table_out, int batch, int max_blocks, const int32_t *prefix_len,
+                     const int32_t *need, const int32_t *ref, int32_t *ref_out, void *workspace, int32_t *status,
+                     cudaStream_t stream) {
+  Space ws;
+  space_layout(&ws, workspace, batch, max_blocks, num_blocks);
+  reserve_plan_kernel<<<1, kThreads, 0, stream>>>(table, table_out, batch, max_blocks, block_size, num_blocks,
+                                                  prefix_len, need, ref, ref_out, ws, status);
+  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  return launch_copy<false>(k, v, n_layers, hkv, block_size, num_blocks, vec_per_row, batch, ws, nullptr, nullptr, 0,
+                            status, stream);
+}
+
+int sv_pages_compact(void *k, void *v, int vec_per_row, int n_layers, int hkv, int block_size, int num_blocks,
+                     const int32_t *table, int32_t *table_out, int batch, int max_blocks, const int32_t *ref,
+                     int32_t *ref_out, int32_t *n_used, int32_t *remap, void *workspace, int32_t *status,
+                     cudaStream_t stream) {
+  Space ws;
+  space_layout(&ws, workspace, batch, max_blocks, num_blocks);
+  compact_plan_kernel<<<1, kThreads, 0, stream>>>(block_size, num_blocks, ref, ref_out, n_used, remap, ws);
+  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  return launch_copy<true>(k, v, n_layers, hkv, block_size, num_blocks, vec_per_row, (num_blocks + 1) / 2, ws, table,
+                           table_out, (int64_t)batch * max_blocks, status, stream);
+}

@@ -12,6 +12,14 @@ namespace {
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline cudaStream_t cs(spec_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
+// Whether [a, a + na) and [b, b + nb) share a byte.
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+// A buffer that may be its own input (the very same address), but not lie across it.
+inline bool same_or_apart(const void *a, const void *b, size_t n) { return a == b || !overlap(a, n, b, n); }
+
 }  // namespace
 
 SvAttnPlan sv_attn_simt_plan(const SvAttnShape &s, int num_splits);
@@ -30,6 +38,8 @@ SvAttnPlan sv_attn_plan(const SvAttnShape &s, int num_splits) {
   if (ok) return p;
   return sv_attn_simt_plan(s, num_splits);
 }
+
+SvAttnPlan sv_attn_window_plan(const SvAttnShape &s) { return sv_attn_simt_plan(s, 0); }
 
 // Run the planned attention kernel (and its combine) for shape s.
 int sv_attn_run(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const void *kc, const void *vc,
@@ -230,6 +240,81 @@ int tree_attn_verify_paged(const void *q, const void *k_pages, const void *v_pag
                      workspace_bytes, dev_status, cs(stream));
 }
 
+// Limits of the window entry points beyond attn_check: 32-bit row indices.
+static int window_check(const SvAttnShape &s) {
+  if (s.window < 1 || s.sinks < 0) return SPEC_ERR_INVALID_ARG;
+  const int rc = attn_check(s.dtype, s.batch, s.n_nodes, s.hq, s.hkv, s.head_dim, s.s_max, s.max_prefix);
+  if (rc != SPEC_OK) return rc;
+  const long long most = 1 << 30;
+  if (s.s_max > most || (long long)s.batch * s.hkv > 65535 || (long long)s.batch * s.hkv * s.n_nodes > most ||
+      (!s.block_table && (long long)s.batch * s.hkv * s.s_max > most))
+    return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+size_t tree_attn_window_workspace_bytes(int dtype, int batch, int n_nodes, int hq, int hkv, int head_dim,
+                                        int max_prefix, int window, int sinks) {
+  SvAttnShape s{dtype, batch, n_nodes, hq, hkv, head_dim, max_prefix, max_prefix};
+  s.window = window;
+  s.sinks = sinks;
+  // (the cache's own limits are the call's; a paged pool may be smaller than batch * max_prefix)
+  if (window < 1 || sinks < 0 || attn_check(dtype, batch, n_nodes, hq, hkv, head_dim, max_prefix, max_prefix) != SPEC_OK)
+    return 0;
+  return sv_attn_window_plan(s).ws_bytes;
+}
+
+static int window_run(SvAttnShape &s, const void *q, const void *k, const void *v, const void *k_tree,
+                      const void *v_tree, const int32_t *prefix_len, const int32_t *depth, const uint64_t *anc_mask,
+                      void *out, float scale, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                      spec_stream_t stream) {
+  if (!q || !k || !v || !k_tree || !v_tree || !prefix_len || !depth || !anc_mask || !out) return SPEC_ERR_INVALID_ARG;
+  const int rc = window_check(s);
+  if (rc != SPEC_OK) return rc;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(out))
+    return SPEC_ERR_INVALID_ARG;
+  s.depth = depth;
+  const SvAttnPlan p = sv_attn_window_plan(s);
+  if (p.ws_bytes > 0 && (!workspace || workspace_bytes < p.ws_bytes || !aligned16(workspace)))
+    return SPEC_ERR_CAPACITY;
+  if (!(scale > 0.f)) scale = 1.0f / sqrtf((float)s.head_dim);
+  return sv_attn_run(s, p, q, k, v, k_tree, v_tree, prefix_len, anc_mask, out, scale, workspace, workspace_bytes,
+                     dev_status, cs(stream));
+}
+
+int tree_attn_verify_window(const void *q, const void *k_cache, const void *v_cache, const void *k_tree,
+                            const void *v_tree, const int32_t *prefix_len, const int32_t *depth,
+                            const uint64_t *anc_mask, void *out, int dtype, int batch, int n_nodes, int hq, int hkv,
+                            int head_dim, int s_max, int max_prefix, int window, int sinks, float scale,
+                            void *workspace, size_t workspace_bytes, int32_t *dev_status, spec_stream_t stream) {
+  SvAttnShape s{dtype, batch, n_nodes, hq, hkv, head_dim, s_max, max_prefix};
+  s.window = window;
+  s.sinks = sinks;
+  return window_run(s, q, k_cache, v_cache, k_tree, v_tree, prefix_len, depth, anc_mask, out, scale, workspace,
+                    workspace_bytes, dev_status, stream);
+}
+
+int tree_attn_verify_window_paged(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
+                                  int block_size, int num_blocks, int max_blocks, const void *k_tree,
+                                  const void *v_tree, const int32_t *prefix_len, const int32_t *depth,
+                                  const uint64_t *anc_mask, void *out, int dtype, int batch, int n_nodes, int hq,
+                                  int hkv, int head_dim, int max_prefix, int window, int sinks, float scale,
+                                  void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                  spec_stream_t stream) {
+  if (!block_table || block_size < 128 || block_size % 128 || num_blocks < 1 || max_blocks < 1 || hkv < 1)
+    return SPEC_ERR_INVALID_ARG;
+  if ((long long)max_blocks * block_size > (1 << 30) || (long long)num_blocks * hkv * block_size > (1 << 30))
+    return SPEC_ERR_UNSUPPORTED;
+  SvAttnShape s{dtype, batch, n_nodes, hq, hkv, head_dim, max_blocks * block_size, max_prefix};
+  s.block_table = block_table;
+  s.block_size = block_size;
+  s.max_blocks = max_blocks;
+  s.num_blocks = num_blocks;
+  s.window = window;
+  s.sinks = sinks;
+  return window_run(s, q, k_pages, v_pages, k_tree, v_tree, prefix_len, depth, anc_mask, out, scale, workspace,
+                    workspace_bytes, dev_status, stream);
+}
+
 static bool eagle_shape_ok(int batch, int n_front, int hidden, int hq, int hkv, int head_dim, int ffn, int vocab) {
   return batch >= 1 && n_front >= 1 && hidden >= 64 && hidden % 64 == 0 && hidden <= 8192 && hq >= 1 && hkv >= 1 && hq % hkv == 0 &&
          (head_dim == 64 || head_dim == 128) && (hq * head_dim) % 64 == 0 && ffn >= 64 && ffn % 64 == 0 &&
@@ -426,6 +511,119 @@ int kv_commit(void *k_cache, void *v_cache, const void *k_tree, const void *v_tr
   return sv_kv_commit(k_cache, v_cache, k_tree, v_tree, elem_bytes, n_layers, batch, hkv, s_max,
                       n_nodes, head_dim, acc_len, acc_path, path_cap, prefix_len, prefix_len_out,
                       dev_status, cs(stream));
+}
+
+int spec_verify_probs(const void *target_probs, const void *draft_probs, int dtype, int batch, int n_nodes, int vocab,
+                      const int32_t *tok, const int32_t *parents, const int32_t *first_child,
+                      const int32_t *next_sibling, const float *u_accept, const float *u_bonus, int path_cap,
+                      int32_t *acc_len, int32_t *acc_path, int32_t *bonus, int32_t *dev_status, spec_stream_t stream) {
+  if (!target_probs || !tok || !parents || !first_child || !next_sibling || !u_accept || !u_bonus || !acc_len ||
+      !acc_path || !bonus)
+    return SPEC_ERR_INVALID_ARG;
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
+  if (batch < 1 || n_nodes < 1 || vocab < 1 || path_cap < 1) return SPEC_ERR_INVALID_ARG;
+  if (n_nodes > SPEC_MAX_NODES || path_cap > SPEC_MAX_NODES + 1 || batch > 65535 || vocab > (1 << 30))
+    return SPEC_ERR_UNSUPPORTED;
+  if (!aligned16(target_probs) || !aligned16(draft_probs)) return SPEC_ERR_INVALID_ARG;
+  return sv_verify_probs(target_probs, draft_probs, dtype, batch, n_nodes, vocab, tok, parents, first_child,
+                         next_sibling, u_accept, u_bonus, path_cap, acc_len, acc_path, bonus, dev_status, cs(stream));
+}
+
+// Limits of the page entry points: sizes of the table and of the block pool.
+static int pages_check(int batch, int max_blocks, int num_blocks) {
+  if (batch < 1 || max_blocks < 1 || num_blocks < 1) return SPEC_ERR_INVALID_ARG;
+  if (batch > SPEC_PAGES_MAX_BATCH || (long long)batch * max_blocks > (1 << 28) || num_blocks > (1 << 28))
+    return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+static int pool_check(const void *k, const void *v, int elem_bytes, int n_layers, int hkv, int head_dim,
+                      int block_size, int num_blocks, int max_blocks) {
+  if (!k || !v) return SPEC_ERR_INVALID_ARG;
+  if (elem_bytes != 2 && elem_bytes != 4) return SPEC_ERR_UNSUPPORTED;
+  if (n_layers < 1 || hkv < 1 || head_dim < 1 || block_size < 1) return SPEC_ERR_INVALID_ARG;
+  if (((long long)head_dim * elem_bytes) % 16) return SPEC_ERR_UNSUPPORTED;
+  if ((long long)max_blocks * block_size > (1 << 30) || (long long)hkv * block_size > (1 << 30) ||
+      (long long)num_blocks * hkv * block_size > (1 << 30) || head_dim > (1 << 20) || n_layers > (1 << 20))
+    return SPEC_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v)) return SPEC_ERR_INVALID_ARG;
+  return SPEC_OK;
+}
+
+size_t kv_pages_workspace_bytes(int batch, int max_blocks, int num_blocks) {
+  if (pages_check(batch, max_blocks, num_blocks) != SPEC_OK) return 0;
+  return sv_pages_ws_bytes(batch, max_blocks, num_blocks);
+}
+
+int kv_pages_fork(const int32_t *block_table, const int32_t *prefix_len, const int32_t *parent, int batch,
+                  int batch_out, int max_blocks, int num_blocks, const int32_t *ref_count, int32_t *table_out,
+                  int32_t *prefix_len_out, int32_t *ref_count_out, int32_t *dev_status, spec_stream_t stream) {
+  if (!block_table || !prefix_len || !parent || !ref_count || !table_out || !prefix_len_out || !ref_count_out)
+    return SPEC_ERR_INVALID_ARG;
+  int rc = pages_check(batch, max_blocks, num_blocks);
+  if (rc == SPEC_OK) rc = pages_check(batch_out, max_blocks, num_blocks);
+  if (rc != SPEC_OK) return rc;
+  const size_t row = (size_t)max_blocks * 4;
+  if (overlap(block_table, batch * row, table_out, batch_out * row) ||
+      overlap(prefix_len, (size_t)batch * 4, prefix_len_out, (size_t)batch_out * 4) ||
+      overlap(parent, (size_t)batch_out * 4, prefix_len_out, (size_t)batch_out * 4) ||
+      !same_or_apart(ref_count, ref_count_out, (size_t)num_blocks * 4))
+    return SPEC_ERR_INVALID_ARG;
+  return sv_pages_fork(block_table, prefix_len, parent, batch, batch_out, max_blocks, num_blocks, ref_count,
+                       table_out, prefix_len_out, ref_count_out, dev_status, cs(stream));
+}
+
+int kv_pages_free(const int32_t *block_table, const int32_t *prefix_len, int batch, int max_blocks, int block_size,
+                  int num_blocks, int window, int sinks, int spare, const int32_t *ref_count, int32_t *table_out,
+                  int32_t *ref_count_out, int32_t *dev_status, spec_stream_t stream) {
+  if (!block_table || !prefix_len || !ref_count || !table_out || !ref_count_out) return SPEC_ERR_INVALID_ARG;
+  const int rc = pages_check(batch, max_blocks, num_blocks);
+  if (rc != SPEC_OK) return rc;
+  if (block_size < 1 || window < 0 || sinks < 0 || spare < 0) return SPEC_ERR_INVALID_ARG;
+  if (!same_or_apart(block_table, table_out, (size_t)batch * max_blocks * 4) ||
+      !same_or_apart(ref_count, ref_count_out, (size_t)num_blocks * 4))
+    return SPEC_ERR_INVALID_ARG;
+  return sv_pages_free(block_table, prefix_len, batch, max_blocks, block_size, num_blocks, window, sinks, spare,
+                       ref_count, table_out, ref_count_out, dev_status, cs(stream));
+}
+
+int kv_pages_reserve(void *k_pages, void *v_pages, int elem_bytes, int n_layers, int hkv, int head_dim,
+                     int block_size, int num_blocks, const int32_t *block_table, int batch, int max_blocks,
+                     const int32_t *prefix_len, const int32_t *need, const int32_t *ref_count, int32_t *table_out,
+                     int32_t *ref_count_out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                     spec_stream_t stream) {
+  if (!block_table || !prefix_len || !need || !ref_count || !table_out || !ref_count_out) return SPEC_ERR_INVALID_ARG;
+  int rc = pages_check(batch, max_blocks, num_blocks);
+  if (rc == SPEC_OK)
+    rc = pool_check(k_pages, v_pages, elem_bytes, n_layers, hkv, head_dim, block_size, num_blocks, max_blocks);
+  if (rc != SPEC_OK) return rc;
+  if (!same_or_apart(block_table, table_out, (size_t)batch * max_blocks * 4) ||
+      !same_or_apart(ref_count, ref_count_out, (size_t)num_blocks * 4))
+    return SPEC_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < sv_pages_ws_bytes(batch, max_blocks, num_blocks))
+    return SPEC_ERR_CAPACITY;
+  return sv_pages_reserve(k_pages, v_pages, head_dim * elem_bytes / 16, n_layers, hkv, block_size, num_blocks,
+                          block_table, table_out, batch, max_blocks, prefix_len, need, ref_count, ref_count_out,
+                          workspace, dev_status, cs(stream));
+}
+
+int kv_pages_compact(void *k_pages, void *v_pages, int elem_bytes, int n_layers, int hkv, int head_dim,
+                     int block_size, int num_blocks, const int32_t *block_table, int batch, int max_blocks,
+                     const int32_t *ref_count, int32_t *table_out, int32_t *ref_count_out, int32_t *n_used,
+                     int32_t *remap, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                     spec_stream_t stream) {
+  if (!block_table || !ref_count || !table_out || !ref_count_out || !n_used) return SPEC_ERR_INVALID_ARG;
+  int rc = pages_check(batch, max_blocks, num_blocks);
+  if (rc == SPEC_OK)
+    rc = pool_check(k_pages, v_pages, elem_bytes, n_layers, hkv, head_dim, block_size, num_blocks, max_blocks);
+  if (rc != SPEC_OK) return rc;
+  if (!same_or_apart(block_table, table_out, (size_t)batch * max_blocks * 4) ||
+      !same_or_apart(ref_count, ref_count_out, (size_t)num_blocks * 4))
+    return SPEC_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < sv_pages_ws_bytes(batch, max_blocks, num_blocks))
+    return SPEC_ERR_CAPACITY;
+  return sv_pages_compact(k_pages, v_pages, head_dim * elem_bytes / 16, n_layers, hkv, block_size, num_blocks,
+                          block_table, table_out, batch, max_blocks, ref_count, ref_count_out, n_used, remap,
+                          workspace, dev_status, cs(stream));
 }
 
 }  // extern "C"

@@ -19,10 +19,11 @@ LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CAPACITY, ERR_CUDA = range(5)
 (DEV_OK, DEV_BAD_PARENTS, DEV_CAPACITY, DEV_BAD_PATH, DEV_BAD_POOL, DEV_BAD_TOKEN, DEV_TIMEOUT, DEV_INTERNAL,
- DEV_BAD_BLOCK) = range(9)
+ DEV_BAD_BLOCK, DEV_BAD_PROB) = range(10)
 F32, BF16 = 0, 1
 GREEDY, TYPICAL, REJECT, REJECT_STOCHASTIC = 0, 1, 2, 3
 MAX_NODES = 256
+PAGES_MAX_BATCH = 4096
 
 
 def mask_words(n_nodes):
@@ -52,6 +53,9 @@ _SIGS = {
                           _vp, _sz, _vp, _vp], _i),
     "tree_attn_verify_paged": ([_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
                                 _i, _f, _i, _vp, _sz, _vp, _vp], _i),
+    "tree_attn_window_workspace_bytes": ([_i] * 9, _sz),
+    "tree_attn_verify_window": ([_vp] * 9 + [_i] * 10 + [_f, _vp, _sz, _vp, _vp], _i),
+    "tree_attn_verify_window_paged": ([_vp] * 4 + [_i] * 3 + [_vp] * 6 + [_i] * 9 + [_f, _vp, _sz, _vp, _vp], _i),
     "tree_attn_verify_noalloc": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                   _i, _vp, _vp], _i),
     "spec_lm_head_workspace_bytes": ([_i, _i, _i], _sz),
@@ -61,6 +65,12 @@ _SIGS = {
                              _vp, _vp], _i),
     "spec_accept": ([_i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _f, _f, _f, _u64, _u64, _i, _vp, _vp,
                      _vp, _vp, _vp], _i),
+    "spec_verify_probs": ([_vp, _vp] + [_i] * 4 + [_vp] * 6 + [_i] + [_vp] * 5, _i),
+    "kv_pages_workspace_bytes": ([_i, _i, _i], _sz),
+    "kv_pages_fork": ([_vp] * 3 + [_i] * 4 + [_vp] * 6, _i),
+    "kv_pages_free": ([_vp] * 2 + [_i] * 7 + [_vp] * 5, _i),
+    "kv_pages_reserve": ([_vp, _vp] + [_i] * 6 + [_vp, _i, _i] + [_vp] * 6 + [_sz, _vp, _vp], _i),
+    "kv_pages_compact": ([_vp, _vp] + [_i] * 6 + [_vp, _i, _i] + [_vp] * 6 + [_sz, _vp, _vp], _i),
     "kv_commit_paged": ([_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp,
                          _vp], _i),
     "kv_commit": ([_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp], _i),
@@ -108,6 +118,35 @@ def _p(t):
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return C.c_void_p(t.data_ptr())
+
+
+class _Args:
+    """Device pointers of one call's tensors, each checked: on the call's
+    device (which has to be the current one, whose stream the call goes to),
+    contiguous, and of the dtype and shape (or element count) the C entry
+    point will take it for."""
+
+    def __init__(self, device):
+        if device.type != "cuda":
+            raise ValueError("expected a CUDA tensor")
+        if device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+        self.index = device.index
+
+    def __call__(self, t, dtype=None, shape=None, numel=None):
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
+            raise ValueError(f"expected a tensor on cuda:{self.index}")
+        if not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"dtype {t.dtype}, expected {dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if numel is not None and t.numel() != numel:
+            raise ValueError(f"{t.numel()} elements, expected {numel}")
+        return t.data_ptr()
 
 
 def _want(t, *dtypes):
@@ -309,6 +348,55 @@ def tree_attn_verify_paged(q, k_pages, v_pages, block_table, k_tree, v_tree, pre
         int(num_splits), _p(workspace), ws_bytes, _p(dev_status), _stream()))
 
 
+def tree_attn_window_workspace_bytes(dtype, batch, n_nodes, hq, hkv, head_dim, max_prefix, window, sinks=0):
+    code = _DT[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(load().tree_attn_window_workspace_bytes(code, batch, n_nodes, hq, hkv, head_dim, int(max_prefix),
+                                                       int(window), int(sinks)))
+
+
+def tree_attn_verify_window(q, k_cache, v_cache, k_tree, v_tree, prefix_len, depth, anc_mask, out, max_prefix, window,
+                            sinks=0, scale=0.0, workspace=None, dev_status=None):
+    """tree_attn_verify over the last ``window`` positions and the first
+    ``sinks`` ones; depth [B, N] int32 gives the nodes' positions.
+    ``workspace`` (uint8, tree_attn_window_workspace_bytes) is allocated per
+    call when not given."""
+    B, N, Hq, D = q.shape
+    _, Hkv, S, _ = k_cache.shape
+    code = _DT.get(q.dtype, -1)
+    if workspace is None:
+        workspace = _scratch(tree_attn_window_workspace_bytes(code, B, N, Hq, Hkv, D, max_prefix, window, sinks), q)
+    ptr = _Args(q.device)
+    kv, tree = (B, Hkv, S, D), (B, Hkv, N, D)
+    args = (ptr(q, q.dtype, (B, N, Hq, D)), ptr(k_cache, q.dtype, kv), ptr(v_cache, q.dtype, kv),
+            ptr(k_tree, q.dtype, tree), ptr(v_tree, q.dtype, tree), ptr(prefix_len, torch.int32, (B,)),
+            ptr(depth, torch.int32, (B, N)), ptr(anc_mask, torch.int64, None, B * N * mask_words(N)),
+            ptr(out, q.dtype, (B, N, Hq, D)))
+    _check("tree_attn_verify_window", load().tree_attn_verify_window(
+        *args, code, B, N, Hq, Hkv, D, S, int(max_prefix), int(window), int(sinks), float(scale), ptr(workspace),
+        workspace.numel() * workspace.element_size(), ptr(dev_status, torch.int32), _stream()))
+
+
+def tree_attn_verify_window_paged(q, k_pages, v_pages, block_table, k_tree, v_tree, prefix_len, depth, anc_mask, out,
+                                  max_prefix, window, sinks=0, scale=0.0, workspace=None, dev_status=None):
+    """tree_attn_verify_window over a paged prefix cache: k_pages/v_pages
+    [num_blocks, Hkv, block_size, D], block_table [B, max_blocks] int32."""
+    B, N, Hq, D = q.shape
+    nb, Hkv, bs, _ = k_pages.shape
+    mb = block_table.shape[1]
+    code = _DT.get(q.dtype, -1)
+    if workspace is None:
+        workspace = _scratch(tree_attn_window_workspace_bytes(code, B, N, Hq, Hkv, D, max_prefix, window, sinks), q)
+    ptr = _Args(q.device)
+    kv, tree = (nb, Hkv, bs, D), (B, Hkv, N, D)
+    args = (ptr(q, q.dtype, (B, N, Hq, D)), ptr(k_pages, q.dtype, kv), ptr(v_pages, q.dtype, kv),
+            ptr(block_table, torch.int32, (B, mb)), bs, nb, mb, ptr(k_tree, q.dtype, tree), ptr(v_tree, q.dtype, tree),
+            ptr(prefix_len, torch.int32, (B,)), ptr(depth, torch.int32, (B, N)),
+            ptr(anc_mask, torch.int64, None, B * N * mask_words(N)), ptr(out, q.dtype, (B, N, Hq, D)))
+    _check("tree_attn_verify_window_paged", load().tree_attn_verify_window_paged(
+        *args, code, B, N, Hq, Hkv, D, int(max_prefix), int(window), int(sinks), float(scale), ptr(workspace),
+        workspace.numel() * workspace.element_size(), ptr(dev_status, torch.int32), _stream()))
+
+
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -423,3 +511,87 @@ def kv_commit_paged(k_pages, v_pages, block_table, k_tree, v_tree, acc_len, acc_
         _p(k_pages), _p(v_pages), _p(block_table), bs, nb, block_table.shape[1], _p(k_tree), _p(v_tree),
         k_pages.element_size(), L, B, Hkv, N, D, _p(acc_len), _p(acc_path), acc_path.shape[1], _p(prefix_len),
         _p(prefix_len_out), _p(dev_status), _stream()))
+
+
+def spec_verify_probs(target_probs, tok, parents, first_child, next_sibling, u_accept, u_bonus, acc_len, acc_path,
+                      bonus, draft_probs=None, dev_status=None):
+    """Acceptance from given probabilities [B, N, V] (float32 or bf16) and
+    given uniform numbers u_accept [B, N], u_bonus [B] (float32); draft_probs
+    where siblings are draws of the drafter.  Outputs as spec_accept."""
+    B, N, V = target_probs.shape
+    dt, i32, f32 = target_probs.dtype, torch.int32, torch.float32
+    ptr = _Args(target_probs.device)
+    node, cap = (B, N), acc_path.shape[1]
+    _check("spec_verify_probs", load().spec_verify_probs(
+        ptr(target_probs), ptr(draft_probs, dt, (B, N, V)), _DT.get(dt, -1), B, N, V, ptr(tok, i32, node),
+        ptr(parents, i32, node), ptr(first_child, i32, node), ptr(next_sibling, i32, node), ptr(u_accept, f32, node),
+        ptr(u_bonus, f32, (B,)), cap, ptr(acc_len, i32, (B,)), ptr(acc_path, i32, (B, cap)), ptr(bonus, i32, (B,)),
+        ptr(dev_status, i32), _stream()))
+
+
+def kv_pages_workspace_bytes(batch, max_blocks, num_blocks):
+    return int(load().kv_pages_workspace_bytes(batch, max_blocks, num_blocks))
+
+
+def kv_pages_fork(block_table, prefix_len, parent, ref_count, table_out, prefix_len_out, ref_out, dev_status=None):
+    """Sequence i of the new batch continues sequence parent[i] (< 0: empty)."""
+    B, mb = block_table.shape
+    out, nb, i32 = parent.shape[0], ref_count.shape[0], torch.int32
+    ptr = _Args(block_table.device)
+    _check("kv_pages_fork", load().kv_pages_fork(
+        ptr(block_table, i32), ptr(prefix_len, i32, (B,)), ptr(parent, i32, (out,)), B, out, mb, nb,
+        ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (out, mb)), ptr(prefix_len_out, i32, (out,)),
+        ptr(ref_out, i32, (nb,)), ptr(dev_status, i32), _stream()))
+
+
+def kv_pages_free(block_table, prefix_len, ref_count, table_out, ref_out, block_size, window=0, sinks=0, spare=0,
+                  dev_status=None):
+    """Drops the entries whose pages no later step needs (window 0: none has left)."""
+    B, mb = block_table.shape
+    nb, i32 = ref_count.shape[0], torch.int32
+    ptr = _Args(block_table.device)
+    _check("kv_pages_free", load().kv_pages_free(
+        ptr(block_table, i32), ptr(prefix_len, i32, (B,)), B, mb, int(block_size), nb, int(window), int(sinks),
+        int(spare), ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)), ptr(ref_out, i32, (nb,)),
+        ptr(dev_status, i32), _stream()))
+
+
+def _pool(ptr, k_pages, v_pages):
+    """(K, V, element bytes, layers, KV heads, head_dim, block size, blocks) of a pool with or without the layer axis."""
+    L, (nb, Hkv, bs, D) = (1, k_pages.shape) if k_pages.dim() == 4 else (k_pages.shape[0], k_pages.shape[1:])
+    return ptr(k_pages), ptr(v_pages, k_pages.dtype, k_pages.shape), k_pages.element_size(), L, Hkv, D, bs, nb
+
+
+def kv_pages_reserve(k_pages, v_pages, block_table, prefix_len, need, ref_count, table_out, ref_out, workspace=None,
+                     dev_status=None):
+    """Makes the next need[b] rows of every sequence writable (new blocks,
+    copies of shared ones).  ``workspace`` (uint8, kv_pages_workspace_bytes)
+    is allocated per call when not given."""
+    B, mb = block_table.shape
+    i32 = torch.int32
+    ptr = _Args(block_table.device)
+    pool = _pool(ptr, k_pages, v_pages)
+    nb = pool[-1]
+    if workspace is None:
+        workspace = _scratch(kv_pages_workspace_bytes(B, mb, nb), block_table)
+    _check("kv_pages_reserve", load().kv_pages_reserve(
+        *pool, ptr(block_table, i32), B, mb, ptr(prefix_len, i32, (B,)), ptr(need, i32, (B,)),
+        ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)), ptr(ref_out, i32, (nb,)), ptr(workspace),
+        workspace.numel() * workspace.element_size(), ptr(dev_status, i32), _stream()))
+
+
+def kv_pages_compact(k_pages, v_pages, block_table, ref_count, table_out, ref_out, n_used, remap=None, workspace=None,
+                     dev_status=None):
+    """Packs the used blocks into the pool's low end; n_used [1] int32 and
+    remap [num_blocks] int32 (optional) are outputs."""
+    B, mb = block_table.shape
+    i32 = torch.int32
+    ptr = _Args(block_table.device)
+    pool = _pool(ptr, k_pages, v_pages)
+    nb = pool[-1]
+    if workspace is None:
+        workspace = _scratch(kv_pages_workspace_bytes(B, mb, nb), block_table)
+    _check("kv_pages_compact", load().kv_pages_compact(
+        *pool, ptr(block_table, i32), B, mb, ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)),
+        ptr(ref_out, i32, (nb,)), ptr(n_used, i32, (1,)), ptr(remap, i32, (nb,)), ptr(workspace),
+        workspace.numel() * workspace.element_size(), ptr(dev_status, i32), _stream()))
