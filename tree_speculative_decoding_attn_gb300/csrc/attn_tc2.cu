@@ -100,8 +100,14 @@ constexpr float kSumBound = 65536.f;  // 2^kTau
 constexpr uint16_t kBoth = 3;                // CTA mask of the pair
 constexpr int kStoreThread = 64;             // softmax thread that issues the output stores (warp 2, lane 0)
 // A partial row: 128 bf16 of unnormalised O (256 B), then the running max
-// (log2 units) and the sum as float32, padded to 272 B.
-constexpr int kPartialBytes = kD * 2 + 16;
+// (log2 units) and the sum as float32, padded to 272 B.  In a window, where a
+// call has few bytes and one more rounding to bf16 would show beside those of
+// P and of the output, O stays float32: 528 B.
+template <bool WIN>
+constexpr int kPartialBytes = kD * (WIN ? 4 : 2) + 16;
+// The running max before a row has seen a key: finite, so that a part of a
+// row group may start on tiles that show a row none of its keys (a window's).
+constexpr float kUnseen = -3.0e38f;
 
 struct Bars {
   uint64_t kland[kKS], kempty[kKS], kfull[kKS];
@@ -123,12 +129,27 @@ constexpr uint32_t kIdescPV = idesc_bf16_f32(256, 128, 0, 1);  // V MN-major (di
 // ---------------------------------------------------------------------------
 // Work schedule
 // ---------------------------------------------------------------------------
-struct Sched {
+struct SchedBase {
   const int32_t *prefix_len;
   int batch, hkv, pairs, n_nodes, s_max, max_prefix, n_clusters;
   int nt, mw;                                              // tree tiles; ancestor-mask words per node
   sv::KvPages pg;                                          // prefix cache addressing
   __device__ int gpb() const { return hkv * pairs; }  // row groups per sequence
+};
+// WIN: a sliding window with sinks (sv::Window).  The prefix tiles of a row
+// group are then the sink tiles and the window's (sv::win_span); groups of
+// query heads that do not divide 128 take gp rows per node, gp the next power
+// of two (the rows past the group are padding: the tensor maps read them as
+// zero and drop them on the way out).
+template <bool WIN>
+struct Sched : SchedBase {};
+template <>
+struct Sched<true> : SchedBase {
+  sv::Window win;
+  int gp;
+  __device__ sv::WinSpan span(int P) const {
+    return sv::win_span(win.window, win.sinks, P, kBN, pg.table ? kBN : 1);
+  }
 };
 
 // A row group's fixed cost (the pipeline drain and epilogue at its end, the
@@ -141,11 +162,16 @@ __device__ __forceinline__ int unit_start_w(int t, int nt) { return t < nt ? 0 :
 
 // A prefix length out of bounds counts as 0 (the sequence is reported and
 // its output left unwritten).
-__device__ __forceinline__ bool prefix_ok(const Sched &s, int raw) {
+__device__ __forceinline__ bool prefix_ok(const SchedBase &s, int raw) {
   return raw >= 0 && raw <= s.max_prefix && raw <= s.s_max;
 }
-__device__ __forceinline__ int seq_tiles(const Sched &s, int P) { return s.nt + (P + kBN - 1) / kBN; }
-__device__ __forceinline__ int tiles_of(const Sched &s, int raw) { return seq_tiles(s, prefix_ok(s, raw) ? raw : 0); }
+template <bool WIN>
+__device__ __forceinline__ int seq_tiles(const Sched<WIN> &s, int P) {
+  if constexpr (WIN) return s.nt + s.span(P).n_tiles;
+  return s.nt + (P + kBN - 1) / kBN;
+}
+template <bool WIN>
+__device__ __forceinline__ int tiles_of(const Sched<WIN> &s, int raw) { return seq_tiles(s, prefix_ok(s, raw) ? raw : 0); }
 
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
@@ -169,7 +195,7 @@ constexpr int kTabSeqs = 128;
 struct SeqTab {
   int raw[4];
 };
-__device__ __forceinline__ void tab_load(const Sched &s, SeqTab &tb) {
+__device__ __forceinline__ void tab_load(const SchedBase &s, SeqTab &tb) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < 4; ++i) tb.raw[i] = 32 * i + lane < s.batch ? s.prefix_len[32 * i + lane] : 0;
@@ -177,7 +203,7 @@ __device__ __forceinline__ void tab_load(const Sched &s, SeqTab &tb) {
 // f(i, raw) for the chunks i of 32 sequences in order (raw: the lane's
 // sequence 32 i + lane, 0 past the batch) until f returns true (uniform).
 template <typename F>
-__device__ __forceinline__ void for_chunks(const Sched &s, const SeqTab &tb, F f) {
+__device__ __forceinline__ void for_chunks(const SchedBase &s, const SeqTab &tb, F f) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -187,7 +213,7 @@ __device__ __forceinline__ void for_chunks(const Sched &s, const SeqTab &tb, F f
     if (f(i, 32 * i + lane < s.batch ? s.prefix_len[32 * i + lane] : 0)) return;
 }
 // prefix_len[b] for a warp-uniform b (0 past the batch).
-__device__ __forceinline__ int warp_raw(const Sched &s, const SeqTab &tb, int b) {
+__device__ __forceinline__ int warp_raw(const SchedBase &s, const SeqTab &tb, int b) {
   if (b >= s.batch) return 0;
   if (b >= kTabSeqs) return s.prefix_len[b];
   int v = 0;
@@ -199,7 +225,8 @@ __device__ __forceinline__ int warp_raw(const Sched &s, const SeqTab &tb, int b)
   return v;
 }
 // Total weight W and units U of all row groups.
-__device__ __forceinline__ void warp_totals(const Sched &s, const SeqTab &tb, long long *W, long long *U) {
+template <bool WIN>
+__device__ __forceinline__ void warp_totals(const Sched<WIN> &s, const SeqTab &tb, long long *W, long long *U) {
   const int lane = threadIdx.x & 31;
   long long n = 0;
   for_chunks(s, tb, [&](int i, int raw) {
@@ -219,7 +246,8 @@ struct Pos {
 };
 // The first units whose start weights are >= x0 and >= x1 (past the last
 // unit: b = batch, u = U, wrg = W), in one walk over the sequences.
-__device__ void warp_seek2(const Sched &s, const SeqTab &tb, long long x0, long long x1, Pos *p0, Pos *p1) {
+template <bool WIN>
+__device__ void warp_seek2(const Sched<WIN> &s, const SeqTab &tb, long long x0, long long x1, Pos *p0, Pos *p1) {
   const int lane = threadIdx.x & 31;
   const int gpb = s.gpb();
   long long W0 = 0, U0 = 0;
@@ -275,7 +303,7 @@ __device__ void warp_seek2(const Sched &s, const SeqTab &tb, long long x0, long 
 // Clusters in use: each range is at least as wide as the heaviest run of
 // units with one start weight (a row group's tree tiles), so every range
 // holds a unit's start.
-__device__ __forceinline__ long long clusters_used(const Sched &s, long long W) {
+__device__ __forceinline__ long long clusters_used(const SchedBase &s, long long W) {
   return max(1ll, min((long long)s.n_clusters, W / (s.nt + kSegW)));
 }
 __device__ __forceinline__ long long range_start(long long c, long long W, long long C) { return c * W / C; }
@@ -291,28 +319,38 @@ __device__ __forceinline__ int cluster_of(long long x, long long W, long long C)
 struct CutDesc {
   int usable, b, gi, c_hi;
 };
+template <bool WIN>
 __device__ __forceinline__ CutDesc *cut_descs(void *ws, int n_clusters) {
   return reinterpret_cast<CutDesc *>(reinterpret_cast<uint8_t *>(ws) +
-                                     (size_t)n_clusters * 2 * kPairRows * kPartialBytes);
+                                     (size_t)n_clusters * 2 * kPairRows * kPartialBytes<WIN>);
 }
 
 // Walks the tiles of a cluster's range in order.  The next sequence's
 // prefix length is loaded one sequence ahead: a global load waited for at a
 // sequence boundary would stall the walk for a full memory latency.
+template <bool WIN>
 struct Cur {
   int b, gi, t;   // sequence, row group within it, tile within the row group
   int n, P;       // tiles of the row group, effective prefix
   bool ok;        // prefix within bounds
   int raw_next;   // prefix_len[b + 1] (0 past the batch)
+  sv::WinSpan sp; // WIN: the prefix tiles
 };
-__device__ __forceinline__ int load_prefix(const Sched &s, int b) { return b < s.batch ? s.prefix_len[b] : 0; }
-__device__ __forceinline__ void cur_apply(Cur &c, const Sched &s, int raw) {
+__device__ __forceinline__ int load_prefix(const SchedBase &s, int b) { return b < s.batch ? s.prefix_len[b] : 0; }
+template <bool WIN>
+__device__ __forceinline__ void cur_apply(Cur<WIN> &c, const Sched<WIN> &s, int raw) {
   c.ok = prefix_ok(s, raw);
   c.P = c.ok ? raw : 0;
-  c.n = seq_tiles(s, c.P);
+  if constexpr (WIN) {
+    c.sp = s.span(c.P);
+    c.n = s.nt + c.sp.n_tiles;
+  } else {
+    c.n = seq_tiles(s, c.P);
+  }
 }
-__device__ __forceinline__ Cur cur_begin(const Bars *bars, const Sched &s) {
-  Cur c;
+template <bool WIN>
+__device__ __forceinline__ Cur<WIN> cur_begin(const Bars *bars, const Sched<WIN> &s) {
+  Cur<WIN> c;
   c.b = bars->start_b;
   c.gi = bars->start_gi;
   c.t = bars->start_t;
@@ -320,7 +358,8 @@ __device__ __forceinline__ Cur cur_begin(const Bars *bars, const Sched &s) {
   c.raw_next = bars->start_raw_next;
   return c;
 }
-__device__ __forceinline__ void cur_next(Cur &c, const Sched &s) {
+template <bool WIN>
+__device__ __forceinline__ void cur_next(Cur<WIN> &c, const Sched<WIN> &s) {
   if (++c.t == c.n) {
     c.t = 0;
     if (++c.gi == s.gpb()) {
@@ -332,8 +371,18 @@ __device__ __forceinline__ void cur_next(Cur &c, const Sched &s) {
   }
 }
 // Valid keys of tile t: a tree tile (t < nt) or a prefix tile.
-__device__ __forceinline__ int tile_keys(const Cur &c, const Sched &s) {
+template <bool WIN>
+__device__ __forceinline__ int tile_keys(const Cur<WIN> &c, const Sched<WIN> &s) {
+  if constexpr (WIN)
+    return c.t < s.nt ? min(kBN, s.n_nodes - c.t * kBN) : sv::win_keys(c.sp, c.P, c.t - s.nt, kBN);
   return c.t < s.nt ? min(kBN, s.n_nodes - c.t * kBN) : min(kBN, c.P - (c.t - s.nt) * kBN);
+}
+
+// First key of prefix tile t (t >= nt).
+template <bool WIN>
+__device__ __forceinline__ int tile_key0(const Cur<WIN> &c, const Sched<WIN> &s) {
+  if constexpr (WIN) return sv::win_key0(c.sp, c.t - s.nt, kBN);
+  return (c.t - s.nt) * kBN;
 }
 
 __device__ __forceinline__ void give_up(Bars *bars, int32_t *status) {
@@ -351,10 +400,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // Waits for this CTA's V half of tile g to land and zeroes its rows past the
 // last key of a partial tile, up to the next multiple of 16 (the last PV
 // k-step reads them with zero probabilities; stale cache rows need not be
-// finite).  Full warp; false on timeout.
-__device__ __forceinline__ bool v_ready(Bars *bars, uint8_t *sV, int g, int nkeys) {
-  const int st = g % kVS;
+// finite).  WIN: likewise the rows between the sinks and the root's window,
+// which a tile starting at a block's boundary may hold.  Full warp; false on
+// timeout.
+template <bool WIN>
+__device__ __forceinline__ bool v_ready(Bars *bars, uint8_t *sV, int g, const Cur<WIN> &c, const Sched<WIN> &s) {
+  const int st = g % kVS, nkeys = tile_keys(c, s);
   if (!warp_wait(&bars->vland[st], (g / kVS) & 1)) return false;
+  if constexpr (WIN) {
+    const int key0 = c.t < s.nt ? c.sp.lo : tile_key0(c, s);
+    const int d0 = max(0, s.win.sinks - key0), d1 = min(nkeys, c.sp.lo - key0);
+    if (d0 < d1) {
+      uint4 *v = reinterpret_cast<uint4 *>(sV + st * kVBytes);
+      for (int e = d0 * 8 + (int)(threadIdx.x & 31); e < d1 * 8; e += 32) v[e] = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+    }
+  }
   if (nkeys < kBN) {
     uint4 *v = reinterpret_cast<uint4 *>(sV + st * kVBytes);
     const int end = min(kBN, (nkeys + 15) & ~15) * 8;
@@ -367,16 +428,16 @@ __device__ __forceinline__ bool v_ready(Bars *bars, uint8_t *sV, int g, int nkey
 
 // MAXW: ancestor-mask words per node, rounded up to 1, 2 or 4 (trees of up
 // to 64, 128 or 256 nodes; one, one or two tree tiles).
-template <int MAXW>
+template <int MAXW, bool WIN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attn_tc2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kc,
                     const __grid_constant__ CUtensorMap tm_vc, const __grid_constant__ CUtensorMap tm_kt,
                     const __grid_constant__ CUtensorMap tm_vt, const __grid_constant__ CUtensorMap tm_o,
-                    const Sched s_in, const uint64_t *__restrict__ anc, void *__restrict__ ws, int Hq,
+                    const Sched<WIN> s_in, const uint64_t *__restrict__ anc, void *__restrict__ ws, int Hq,
                     float scale_log2, int32_t *status) {
   // the tree-tile count as a compile-time constant in every schedule step
-  const Sched s = [&] {
-    Sched t = s_in;
+  const Sched<WIN> s = [&] {
+    Sched<WIN> t = s_in;
     t.nt = (MAXW + 1) / 2;
     return t;
   }();
@@ -386,7 +447,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t *sV = sK + kKS * kKBytes;
   Bars *bars = reinterpret_cast<Bars *>(sV + kVS * kVBytes);
 
-  const int N = s.n_nodes, G = Hq / s.hkv, R = N * G;
+  const int N = s.n_nodes;
+  const int G = [&] {
+    if constexpr (WIN) return s.gp;
+    return Hq / s.hkv;
+  }();
+  const int R = N * G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cluster = blockIdx.x >> 1;
@@ -434,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           d.gi = p0.gi;
           d.c_hi = cluster_of(p0.wrg + unit_start_w(tiles_of(s, raw0) - 1, s.nt), W, C);
         }
-        cut_descs(ws, s.n_clusters)[cluster] = d;
+        cut_descs<WIN>(ws, s.n_clusters)[cluster] = d;
       }
     }
   } else if (warp == 1) {
@@ -488,9 +554,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ loads
     if (lane == 0) {
       const bool is_v = warp == 10;
-      Cur c = cur_begin(bars, s);
+      Cur<WIN> c = cur_begin(bars, s);
       int seg = 0, issued = 0, q_issued = 0;
-      Cur cpf = c;  // kPrefetch tiles ahead of c
+      Cur<WIN> cpf = c;  // kPrefetch tiles ahead of c
       for (int i = 0; i < kPrefetch && i < T; ++i) cur_next(cpf, s);
       for (int g = 0; g < T; ++g) {
         const bool first = g == 0 || c.t == 0;
@@ -502,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int pbh = cpf.b * s.hkv + cpf.gi / pairs;
           const bool ptree = cpf.t < s.nt;
           const int prow = ptree ? pbh * N + cpf.t * kBN
-                                 : sv::kv_row(s.pg, cpf.b, s.hkv, cpf.gi / pairs, s.s_max, (cpf.t - s.nt) * kBN, nullptr);
+                                 : sv::kv_row(s.pg, cpf.b, s.hkv, cpf.gi / pairs, s.s_max, tile_key0(cpf, s), nullptr);
           if (is_v) {
             tma_prefetch_2d(ptree ? &tm_vt : &tm_vc, 64 * (int)rank, prow);
           } else {
@@ -537,7 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // (a 128-key tile lies inside one cache block: block sizes are
         // multiples of 128; a bad block id gives row -1, read as zeros)
         const int row0 =
-            tree ? bh * N + c.t * kBN : sv::kv_row(s.pg, c.b, s.hkv, kvh, s.s_max, (c.t - s.nt) * kBN, status);
+            tree ? bh * N + c.t * kBN : sv::kv_row(s.pg, c.b, s.hkv, kvh, s.s_max, tile_key0(c, s), status);
         if (is_v) {
           mbar_expect_tx(land, kVBytes);
           tma_load_2d(sV + st * kVBytes, tree ? &tm_vt : &tm_vc, 64 * (int)rank, row0, land);
@@ -567,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0) {
       const uint32_t qa = smem_u32(sQ), ka = smem_u32(sK);
-      Cur cs = cur_begin(bars, s);
+      Cur<WIN> cs = cur_begin(bars, s);
       int seg_s = 0;
       // S(g) = Q K(g)^T into S buffer g % kSB; called for g = 0, 1, 2, ...
       // in order.  Descriptors are a base plus constant offsets (the start
@@ -607,7 +673,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
       // odd CTA: its Q and K halves have landed -> arrive on the even CTA's
       // full barriers
-      Cur c = cur_begin(bars, s);
+      Cur<WIN> c = cur_begin(bars, s);
       int seg = 0;
       for (int g = 0; g < T; ++g) {
         const bool first = g == 0 || c.t == 0;
@@ -637,13 +703,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ PV issuer
     if (rank == 0) {
       const uint32_t va = smem_u32(sV);
-      Cur cp = cur_begin(bars, s);
+      Cur<WIN> cp = cur_begin(bars, s);
       bool ok = true;
       for (int g = 0; ok && g < T; ++g) {
         // O += P(g) V(g) once P of both CTAs is ready (which also covers both
         // V halves of tile g)
         const int nkeys = tile_keys(cp, s);
-        if (!(ok = warp_wait(&bars->pfull[g % kSB], (g / kSB) & 1) && v_ready(bars, sV, g, nkeys))) break;
+        if (!(ok = warp_wait(&bars->pfull[g % kSB], (g / kSB) & 1) && v_ready(bars, sV, g, cp, s))) break;
         tc_fence_after();
         const bool first = g == 0 || cp.t == 0;
         const int st = g % kVS;
@@ -678,9 +744,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // PV(g-kSB) completed, i.e. after the barrier's phase for tile g-kSB,
       // so the arrival cannot fall into that earlier phase.
       const uint32_t pfull_even0 = mapa_cluster(&bars->pfull[0], 0);  // pfull[i] at + 8 i
-      Cur c = cur_begin(bars, s);
+      Cur<WIN> c = cur_begin(bars, s);
       for (int g = 0; g < T; ++g) {
-        if (!warp_wait(&bars->sfull[g % kSB], (g / kSB) & 1) || !v_ready(bars, sV, g, tile_keys(c, s)) ||
+        if (!warp_wait(&bars->sfull[g % kSB], (g / kSB) & 1) || !v_ready(bars, sV, g, c, s) ||
             bars->abort) {
           give_up(bars, status);
           break;
@@ -705,11 +771,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto softmax_sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     const uint32_t pfull_even0 = mapa_cluster(&bars->pfull[0], 0);  // pfull[i] at + 8 i
     const float NEG_INF = -INFINITY;
-    Cur c = cur_begin(bars, s);
+    Cur<WIN> c = cur_begin(bars, s);
     int seg = 0;        // segment (row group part) of this range: Q buffer seg % kQB
     int q_pending = 0;  // 1 + the Q buffer the last output store reads (store thread)
     bool from_start = c.t == 0;
-    float ma = NEG_INF, mb = NEG_INF;  // running max of rows ra, rb (log2 units)
+    constexpr float M0 = WIN ? kUnseen : -INFINITY;
+    float ma = M0, mb = M0;            // running max of rows ra, rb (log2 units)
     float la = 0.f, lb_sum = 0.f;      // this thread's part of their sums
     // Ancestor bits of a row for tree tile tt (words 2 tt and 2 tt + 1 of its
     // node; padding rows: all tree keys): the first tree tile's loaded one
@@ -731,6 +798,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return m;
     };
     Mask amask_a{}, amask_b{}, next_a{}, next_b{};
+    // WIN: first prefix key inside a row's window, less the prefix length
+    // (depth - window + 1; rows of nodes at most as deep as the tree), the
+    // next segment's loaded with its masks
+    auto load_from = [&](int b, int gi, int lane_row) -> int {
+      if constexpr (WIN) {
+        const int rr = grow(gi, lane_row);
+        return (rr < R ? sv::win_depth(s.win, (int64_t)b * N + rr / G, N) : 0) - s.win.window + 1;
+      }
+      return 0;
+    };
+    int from_a = load_from(c.b, c.gi, ra), from_b = load_from(c.b, c.gi, rb), next_from_a = 0, next_from_b = 0;
     if (c.t < NT) {
       amask_a = load_mask(c.b, c.gi, ra, c.t);
       amask_b = load_mask(c.b, c.gi, rb, c.t);
@@ -749,21 +827,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         from_start = true;
         amask_a = next_a;
         amask_b = next_b;
+        from_a = next_from_a;
+        from_b = next_from_b;
       }
-      ma = mb = NEG_INF;
+      ma = mb = M0;
       la = lb_sum = 0.f;
       if (g + (c.n - 1 - c.t) + 1 < T) {  // the next segment's ancestor bits, a segment ahead
         const bool same_b = c.gi + 1 < s.gpb();
         next_a = load_mask(same_b ? c.b : c.b + 1, same_b ? c.gi + 1 : 0, ra, 0);
         next_b = load_mask(same_b ? c.b : c.b + 1, same_b ? c.gi + 1 : 0, rb, 0);
+        next_from_a = load_from(same_b ? c.b : c.b + 1, same_b ? c.gi + 1 : 0, ra);
+        next_from_b = load_from(same_b ? c.b : c.b + 1, same_b ? c.gi + 1 : 0, rb);
       }
       bool first = true;
+      // WIN: a warp of padding rows (calls of few rows have many) only keeps
+      // the barriers' pace; its P and O are never read
+      const bool idle = WIN && grow(c.gi, lb) >= R;
       for (;;) {
         if (ok && !s_ready && !warp_wait(&bars->sfull[g % kSB], (g / kSB) & 1)) ok = false;
         const uint32_t s_addr = tmem + lane_off + (uint32_t)(g % kSB) * 128u;
         // sv[4j + e]: row ra, key 8j + 2 tq + e;  sv[4j + 2 + e]: row rb
         uint32_t sv[64];
-        if (ok) {
+        if (ok && !idle) {
           tc_fence_after();
           tmem_ld_16x256b_x16(s_addr, sv);
           tmem_wait_ld();
@@ -782,10 +867,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // keys below nvalid are a prefix of these bits (they increase with
             // the bit index); on a tree tile also the ancestor bits (keys 0-63
             // of the tile from its first mask word, 64-127 from its second).
-            const int m8 = nvalid - 2 * tq;
-            const int nb = m8 <= 0 ? 0 : min(32, 2 * (m8 >> 3) + min(2, m8 & 7));
-            const uint32_t in = nb >= 32 ? 0xFFFFFFFFu : ((1u << nb) - 1u);
+            auto below = [&](int n) -> uint32_t {  // bits of this thread's keys below n
+              const int m8 = n - 2 * tq;
+              const int nb = m8 <= 0 ? 0 : min(32, 2 * (m8 >> 3) + min(2, m8 & 7));
+              return nb >= 32 ? 0xFFFFFFFFu : ((1u << nb) - 1u);
+            };
+            const uint32_t in = below(nvalid);
             uint32_t va = in, vb = in;
+            if constexpr (WIN) {
+              if (!tree) {
+                const int key0 = tile_key0(c, s);
+                const uint32_t sink = below(s.win.sinks - key0);
+                va &= sink | ~below(c.P - key0 + from_a);
+                vb &= sink | ~below(c.P - key0 + from_b);
+              }
+            }
             if (tree) {
               auto mine = [&](uint64_t m) -> uint32_t {
                 uint64_t x = (m >> (2 * tq)) & 0x0303030303030303ull;
@@ -918,7 +1014,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           s_ready = __all_sync(0xffffffffu, next_done);
         };
-        if (__builtin_expect(tree || nvalid < kBN, 0))
+        // (WIN: no row masks a full tile of sinks, nor one inside the window of
+        // the deepest node a tree may have)
+        bool edge = tree || nvalid < kBN;
+        if constexpr (WIN) {
+          const int key0 = tile_key0(c, s);
+          edge = edge || (key0 + kBN > s.win.sinks && key0 - c.P < N - s.win.window);
+        }
+        if (idle) {
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive_cluster(pfull_even0 + (uint32_t)(g % kSB) * (uint32_t)sizeof(uint64_t));
+          s_ready = false;
+        } else if (__builtin_expect(edge, 0))
           tile(std::true_type{});
         else
           tile(std::false_type{});
@@ -973,20 +1080,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else if (live) {
           // a part cut at the range end: slot 2c + 1; the one cut at its start: 2c
           const int slot = cluster * 2 + (g == T - 1 && c.t != c.n - 1 ? 1 : 0);
-          uint8_t *w = reinterpret_cast<uint8_t *>(ws) + ((int64_t)slot * kPairRows + (int)rank * 128) * kPartialBytes;
+          constexpr int PB = kPartialBytes<WIN>;
+          uint8_t *w = reinterpret_cast<uint8_t *>(ws) + ((int64_t)slot * kPairRows + (int)rank * 128) * PB;
           const bool oka = grow(c.gi, ra) < R, okb = grow(c.gi, rb) < R;
+          if constexpr (WIN) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (oka) *reinterpret_cast<uint2 *>(w + ra * PB + 32 * j + 8 * tq) = make_uint2(ov[4 * j], ov[4 * j + 1]);
+              if (okb) *reinterpret_cast<uint2 *>(w + rb * PB + 32 * j + 8 * tq) = make_uint2(ov[4 * j + 2], ov[4 * j + 3]);
+            }
+          } else
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             if (oka)
-              *reinterpret_cast<uint32_t *>(w + ra * kPartialBytes + 16 * j + 4 * tq) =
+              *reinterpret_cast<uint32_t *>(w + ra * PB + 16 * j + 4 * tq) =
                   pack_bf16(__uint_as_float(ov[4 * j]), __uint_as_float(ov[4 * j + 1]));
             if (okb)
-              *reinterpret_cast<uint32_t *>(w + rb * kPartialBytes + 16 * j + 4 * tq) =
+              *reinterpret_cast<uint32_t *>(w + rb * PB + 16 * j + 4 * tq) =
                   pack_bf16(__uint_as_float(ov[4 * j + 2]), __uint_as_float(ov[4 * j + 3]));
           }
           if (tq == 0) {
-            if (oka) *reinterpret_cast<float2 *>(w + ra * kPartialBytes + kD * 2) = make_float2(ma, sa);
-            if (okb) *reinterpret_cast<float2 *>(w + rb * kPartialBytes + kD * 2) = make_float2(mb, sb);
+            if (oka) *reinterpret_cast<float2 *>(w + ra * PB + PB - 16) = make_float2(ma, sa);
+            if (okb) *reinterpret_cast<float2 *>(w + rb * PB + PB - 16) = make_float2(mb, sb);
           }
         }
         softmax_sync();  // every row of this CTA staged
@@ -1036,24 +1151,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // as a programmatic dependent of the main kernel: its blocks become
 // resident as the main kernel's CTAs leave and wait for it to complete.
 constexpr int kCombRows = 32;
-constexpr int kCombBatch = 3;
+template <bool WIN>
 __global__ void __launch_bounds__(256, 4) attn_tc2_combine_kernel(void *__restrict__ ws, __nv_bfloat16 *__restrict__ out,
-                                                                  const Sched s, int Hq) {
+                                                                  const Sched<WIN> s, int Hq) {
+  constexpr int PB = kPartialBytes<WIN>;
+  constexpr int OV = WIN ? 4 : 2;  // 16-byte vectors of a thread's 16 dims
+  constexpr int kCombBatch = WIN ? 2 : 3;  // contributors loaded together (what 64 registers hold)
   const int k = blockIdx.x + 1;                 // boundary between clusters k-1 and k
   const int rr = blockIdx.y * kCombRows + (threadIdx.x >> 3);  // row of the pair
   const int d0 = (threadIdx.x & 7) * 16;        // first head dim
   grid_dep_wait();  // the main kernel's partials and descriptors are written and visible
-  const CutDesc d = cut_descs(ws, s.n_clusters)[k];
+  const CutDesc d = cut_descs<WIN>(ws, s.n_clusters)[k];
   if (!d.usable) return;
-  const int G = Hq / s.hkv, R = s.n_nodes * G;
+  const int heads = Hq / s.hkv;
+  int G = heads;  // rows per node
+  if constexpr (WIN) G = s.gp;
+  const int R = s.n_nodes * G;
   const int kvh = d.gi / s.pairs, pair = d.gi % s.pairs;
   const int rg = pair * kPairRows + rr;
-  if (rg >= R) return;
+  if (rg >= R || rg % G >= heads) return;
   const int c_lo = k - 1, nc = d.c_hi - c_lo + 1;
   // cluster c's part: slot 2c + 1 when cut at its range end (all but the last)
   auto row_of = [&](int c) -> const uint8_t * {
     const int slot = 2 * c + (c < d.c_hi ? 1 : 0);
-    return reinterpret_cast<const uint8_t *>(ws) + ((int64_t)slot * kPairRows + rr) * kPartialBytes;
+    return reinterpret_cast<const uint8_t *>(ws) + ((int64_t)slot * kPairRows + rr) * PB;
   };
   float M = -INFINITY, L = 0.f;
   float acc[16];
@@ -1061,17 +1182,18 @@ __global__ void __launch_bounds__(256, 4) attn_tc2_combine_kernel(void *__restri
   for (int j = 0; j < 16; ++j) acc[j] = 0.f;
   for (int c0 = 0; c0 < nc; c0 += kCombBatch) {
     float2 ml[kCombBatch];
-    uint4 o[kCombBatch][2];
+    uint4 o[kCombBatch][OV];
 #pragma unroll
     for (int i = 0; i < kCombBatch; ++i) {
       if (c0 + i < nc) {
         const uint8_t *row = row_of(c_lo + c0 + i);
-        ml[i] = *reinterpret_cast<const float2 *>(row + kD * 2);
-        o[i][0] = *reinterpret_cast<const uint4 *>(row + d0 * 2);
-        o[i][1] = *reinterpret_cast<const uint4 *>(row + d0 * 2 + 16);
+        ml[i] = *reinterpret_cast<const float2 *>(row + PB - 16);
+#pragma unroll
+        for (int j = 0; j < OV; ++j) o[i][j] = *reinterpret_cast<const uint4 *>(row + d0 * (OV / 2) * 2 + 16 * j);
       } else {
         ml[i] = make_float2(-INFINITY, 0.f);
-        o[i][0] = o[i][1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < OV; ++j) o[i][j] = make_uint4(0, 0, 0, 0);
       }
     }
     float Mb = M;
@@ -1086,11 +1208,21 @@ __global__ void __launch_bounds__(256, 4) attn_tc2_combine_kernel(void *__restri
     for (int i = 0; i < kCombBatch; ++i) {
       const float f = c0 + i < nc ? exp2f(ml[i].x - Mb) : 0.f;
       L = fmaf(f, ml[i].y, L);
-      const uint32_t w[8] = {o[i][0].x, o[i][0].y, o[i][0].z, o[i][0].w, o[i][1].x, o[i][1].y, o[i][1].z, o[i][1].w};
+      if constexpr (WIN) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        acc[2 * j] = fmaf(f, __uint_as_float(w[j] << 16), acc[2 * j]);
-        acc[2 * j + 1] = fmaf(f, __uint_as_float(w[j] & 0xFFFF0000u), acc[2 * j + 1]);
+        for (int j = 0; j < 4; ++j) {
+          acc[4 * j] = fmaf(f, __uint_as_float(o[i][j].x), acc[4 * j]);
+          acc[4 * j + 1] = fmaf(f, __uint_as_float(o[i][j].y), acc[4 * j + 1]);
+          acc[4 * j + 2] = fmaf(f, __uint_as_float(o[i][j].z), acc[4 * j + 2]);
+          acc[4 * j + 3] = fmaf(f, __uint_as_float(o[i][j].w), acc[4 * j + 3]);
+        }
+      } else {
+        const uint32_t w[8] = {o[i][0].x, o[i][0].y, o[i][0].z, o[i][0].w, o[i][1].x, o[i][1].y, o[i][1].z, o[i][1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          acc[2 * j] = fmaf(f, __uint_as_float(w[j] << 16), acc[2 * j]);
+          acc[2 * j + 1] = fmaf(f, __uint_as_float(w[j] & 0xFFFF0000u), acc[2 * j + 1]);
+        }
       }
     }
     M = Mb;
@@ -1105,9 +1237,29 @@ __global__ void __launch_bounds__(256, 4) attn_tc2_combine_kernel(void *__restri
   v1.y = pack_bf16(acc[10] * inv, acc[11] * inv);
   v1.z = pack_bf16(acc[12] * inv, acc[13] * inv);
   v1.w = pack_bf16(acc[14] * inv, acc[15] * inv);
-  uint4 *dst = reinterpret_cast<uint4 *>(out + (((int64_t)d.b * s.n_nodes + rg / G) * Hq + kvh * G + rg % G) * kD + d0);
+  uint4 *dst = reinterpret_cast<uint4 *>(out + (((int64_t)d.b * s.n_nodes + rg / G) * Hq + kvh * heads + rg % G) * kD + d0);
   dst[0] = v0;
   dst[1] = v1;
+}
+
+// Ancestor masks for a window shorter than the tree: drops the ancestors of a
+// node that its window has left (and that are no sinks).  Wider windows never
+// hide an ancestor and use the caller's masks as they are.
+__global__ void __launch_bounds__(256)
+    window_mask_kernel(const uint64_t *__restrict__ anc, const int32_t *__restrict__ prefix_len, const sv::Window win,
+                       int N, uint64_t *__restrict__ out) {
+  __shared__ int s_depth[SPEC_MAX_NODES];
+  const int b = blockIdx.x, words = (N + 63) / 64;
+  if (threadIdx.x < N) s_depth[threadIdx.x] = sv::win_depth(win, (int64_t)b * N + threadIdx.x, N);
+  __syncthreads();
+  const long long P = prefix_len[b];
+  for (int e = threadIdx.x; e < N * words; e += 256) {
+    const int d = s_depth[e / words], t0 = e % words * 64;
+    uint64_t m = anc[(int64_t)b * N * words + e], keep = 0;
+    for (int t = 0; t < 64 && t0 + t < N; ++t)
+      if (d - s_depth[t0 + t] < win.window || P + s_depth[t0 + t] < win.sinks) keep |= 1ull << t;
+    out[(int64_t)b * N * words + e] = m & keep;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1154,7 +1306,7 @@ int tc2_clusters() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   int n = g_clusters[dev].load();
   if (n > 0) return n;
-  if (cudaFuncSetAttribute(attn_tc2_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+  if (cudaFuncSetAttribute(attn_tc2_kernel<1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
       cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
@@ -1162,46 +1314,42 @@ int tc2_clusters() {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   int clusters = 0;
-  if (cudaOccupancyMaxActiveClusters(&clusters, attn_tc2_kernel<1>, &cfg) != cudaSuccess || clusters < 1) return 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, attn_tc2_kernel<1, false>, &cfg) != cudaSuccess || clusters < 1) return 0;
   g_clusters[dev].store(clusters);
   return clusters;
 }
 
-}  // namespace
-
-bool sv_attn_tc2_supported(const SvAttnShape &s) {
-  if (s.dtype != SPEC_BF16 || s.head_dim != kD || s.hkv < 1) return false;
-  const int G = s.hq / s.hkv;
-  return s.n_nodes <= SPEC_MAX_NODES && G <= 128 && (128 % G) == 0 && (s.n_nodes * G > 128 || s.n_nodes > 64);
+int pow2_at_least(int x) {
+  int p = 1;
+  while (p < x) p *= 2;
+  return p;
 }
 
-size_t sv_attn_tc2_ws_bytes() {
-  const int c = tc2_clusters();
-  return c > 0 ? (size_t)c * (2 * kPairRows * kPartialBytes + sizeof(CutDesc)) : 0;
-}
-
-int sv_attn_tc2(const SvAttnShape &s, const void *q, const void *kc, const void *vc, const void *kt, const void *vt,
-                const int32_t *prefix_len, const uint64_t *anc, void *out, float scale, void *ws, size_t ws_bytes,
-                int32_t *status, cudaStream_t stream) {
+// The tensor maps, the schedule and the two launches of one call.  rows_g:
+// rows per node (the group's query heads, or the next power of two).
+template <bool WIN>
+int tc2_run(const SvAttnShape &s, Sched<WIN> &sc, int rows_g, const void *q, const void *kc, const void *vc,
+            const void *kt, const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out, float scale,
+            void *ws, int32_t *status, cudaStream_t stream) {
   const int C = tc2_clusters();
   if (C < 1) return SPEC_ERR_CUDA;
-  if (!ws || ws_bytes < sv_attn_tc2_ws_bytes()) return SPEC_ERR_CAPACITY;
-  const int G = s.hq / s.hkv, R = s.n_nodes * G;
+  const int G = s.hq / s.hkv, R = s.n_nodes * rows_g;
   CUtensorMap mq, mkc, mvc, mkt, mvt, mo;
   {
     const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)G, (cuuint64_t)s.hkv, (cuuint64_t)s.batch * s.n_nodes};
     const cuuint64_t strides[3] = {(cuuint64_t)kD * 2, (cuuint64_t)G * kD * 2, (cuuint64_t)s.hq * kD * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)(128 / G)};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows_g, 1, (cuuint32_t)(128 / rows_g)};
     if (make_map(&mq, q, 4, dims, strides, box) != SPEC_OK) return SPEC_ERR_CUDA;
   }
   {
-    // output rows of a CTA: 128 / G nodes x the G heads of a KV head; nodes
-    // past the sequence's last are outside the map and not written
+    // output rows of a CTA: 128 / rows_g nodes x the G heads of a KV head;
+    // nodes past the sequence's last, and rows past the last head, are outside
+    // the map and not written
     const cuuint64_t dims[5] = {(cuuint64_t)kD, (cuuint64_t)G, (cuuint64_t)s.hkv, (cuuint64_t)s.n_nodes,
                                 (cuuint64_t)s.batch};
     const cuuint64_t strides[4] = {(cuuint64_t)kD * 2, (cuuint64_t)G * kD * 2, (cuuint64_t)s.hq * kD * 2,
                                    (cuuint64_t)s.n_nodes * s.hq * kD * 2};
-    const cuuint32_t box[5] = {64, (cuuint32_t)G, 1, (cuuint32_t)(128 / G), 1};
+    const cuuint32_t box[5] = {64, (cuuint32_t)rows_g, 1, (cuuint32_t)(128 / rows_g), 1};
     if (make_map(&mo, out, 5, dims, strides, box) != SPEC_OK) return SPEC_ERR_CUDA;
   }
   {
@@ -1222,7 +1370,6 @@ int sv_attn_tc2(const SvAttnShape &s, const void *q, const void *kc, const void 
     if (make_map(&mkt, kt, 2, dims, strides, kbox) != SPEC_OK) return SPEC_ERR_CUDA;
     if (make_map(&mvt, vt, 2, dims, strides, vbox) != SPEC_OK) return SPEC_ERR_CUDA;
   }
-  Sched sc;
   sc.prefix_len = prefix_len;
   sc.batch = s.batch;
   sc.hkv = s.hkv;
@@ -1236,7 +1383,9 @@ int sv_attn_tc2(const SvAttnShape &s, const void *q, const void *kc, const void 
   sc.pg = sv::KvPages{s.block_table, s.block_size, s.max_blocks, s.num_blocks};
   // (every instance has the same shared memory and one CTA per SM, so the
   // cluster count looked up for one holds for all)
-  auto kern = sc.mw == 1 ? attn_tc2_kernel<1> : sc.mw == 2 ? attn_tc2_kernel<2> : attn_tc2_kernel<4>;
+  auto kern = sc.mw == 1   ? attn_tc2_kernel<1, WIN>
+              : sc.mw == 2 ? attn_tc2_kernel<2, WIN>
+                           : attn_tc2_kernel<4, WIN>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess)
     return SPEC_ERR_CUDA;
   kern<<<2 * C, kThreads, kSmemBytes, stream>>>(mq, mkc, mvc, mkt, mvt, mo, sc, anc, ws, s.hq,
@@ -1255,9 +1404,67 @@ int sv_attn_tc2(const SvAttnShape &s, const void *q, const void *kc, const void 
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_tc2_combine_kernel, ws, (__nv_bfloat16 *)out, sc, s.hq) !=
+    if (cudaLaunchKernelEx(&cfg, attn_tc2_combine_kernel<WIN>, ws, (__nv_bfloat16 *)out, sc, s.hq) !=
         cudaSuccess)
       return SPEC_ERR_CUDA;
   }
   return sv_launch_status();
+}
+}  // namespace
+
+bool sv_attn_tc2_supported(const SvAttnShape &s) {
+  if (s.dtype != SPEC_BF16 || s.head_dim != kD || s.hkv < 1) return false;
+  const int G = s.hq / s.hkv;
+  return s.n_nodes <= SPEC_MAX_NODES && G <= 128 && (128 % G) == 0 && (s.n_nodes * G > 128 || s.n_nodes > 64);
+}
+
+size_t sv_attn_tc2_ws_bytes() {
+  const int c = tc2_clusters();
+  return c > 0 ? (size_t)c * (2 * kPairRows * kPartialBytes<false> + sizeof(CutDesc)) : 0;
+}
+
+int sv_attn_tc2(const SvAttnShape &s, const void *q, const void *kc, const void *vc, const void *kt, const void *vt,
+                const int32_t *prefix_len, const uint64_t *anc, void *out, float scale, void *ws, size_t ws_bytes,
+                int32_t *status, cudaStream_t stream) {
+  if (tc2_clusters() < 1) return SPEC_ERR_CUDA;
+  if (!ws || ws_bytes < sv_attn_tc2_ws_bytes()) return SPEC_ERR_CAPACITY;
+  Sched<false> sc;
+  return tc2_run<false>(s, sc, s.hq / s.hkv, q, kc, vc, kt, vt, prefix_len, anc, out, scale, ws, status, stream);
+}
+
+bool sv_attn_tc2_window_supported(const SvAttnShape &s) {
+  return s.window > 0 && s.dtype == SPEC_BF16 && s.head_dim == kD && s.hkv >= 1 && s.hq / s.hkv <= 128 &&
+         s.n_nodes <= SPEC_MAX_NODES;
+}
+
+// Partials and descriptors, then the masks of windows shorter than the tree.
+static size_t window_masks_at(int clusters) {
+  return (size_t)clusters * (2 * kPairRows * kPartialBytes<true> + sizeof(CutDesc));
+}
+size_t sv_attn_tc2_window_ws_bytes(const SvAttnShape &s) {
+  const int c = tc2_clusters();
+  if (c < 1) return 0;
+  const size_t masks = s.window < s.n_nodes ? (size_t)s.batch * s.n_nodes * ((s.n_nodes + 63) / 64) * 8 : 0;
+  return window_masks_at(c) + masks;
+}
+
+int sv_attn_tc2_window(const SvAttnShape &s, const void *q, const void *kc, const void *vc, const void *kt,
+                       const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out, float scale,
+                       void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream) {
+  const int c = tc2_clusters();
+  if (c < 1) return SPEC_ERR_CUDA;
+  if (!ws || ws_bytes < sv_attn_tc2_window_ws_bytes(s)) return SPEC_ERR_CAPACITY;
+  Sched<true> sc;
+  // (positions stay below 2^30 + 256, so a wider window or more sinks hide
+  // nothing either, and sums with them fit in 32 bits)
+  constexpr int kAll = (1 << 30) + SPEC_MAX_NODES;
+  sc.win = sv::Window{s.depth, s.window < kAll ? s.window : kAll, s.sinks < kAll ? s.sinks : kAll};
+  sc.gp = pow2_at_least(s.hq / s.hkv);
+  if (s.window < s.n_nodes) {
+    uint64_t *masks = reinterpret_cast<uint64_t *>(static_cast<uint8_t *>(ws) + window_masks_at(c));
+    window_mask_kernel<<<s.batch, 256, 0, stream>>>(anc, prefix_len, sc.win, s.n_nodes, masks);
+    if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+    anc = masks;
+  }
+  return tc2_run<true>(s, sc, sc.gp, q, kc, vc, kt, vt, prefix_len, anc, out, scale, ws, status, stream);
 }

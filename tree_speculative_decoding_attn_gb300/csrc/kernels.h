@@ -66,6 +66,13 @@ size_t sv_attn_tc2_ws_bytes();
 int sv_attn_tc2(const SvAttnShape &s, const void *q, const void *kc, const void *vc, const void *kt,
                 const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out,
                 float scale, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream);
+// The same in a sliding window (s.window > 0), for any group of up to 128
+// query heads and any number of rows.
+bool sv_attn_tc2_window_supported(const SvAttnShape &s);
+size_t sv_attn_tc2_window_ws_bytes(const SvAttnShape &s);
+int sv_attn_tc2_window(const SvAttnShape &s, const void *q, const void *kc, const void *vc, const void *kt,
+                       const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out, float scale,
+                       void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream);
 int sv_attn_run(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const void *kc, const void *vc,
                 const void *kt, const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out,
                 float scale, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream);

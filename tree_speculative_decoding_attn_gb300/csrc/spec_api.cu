@@ -39,7 +39,14 @@ SvAttnPlan sv_attn_plan(const SvAttnShape &s, int num_splits) {
   return sv_attn_simt_plan(s, num_splits);
 }
 
-SvAttnPlan sv_attn_window_plan(const SvAttnShape &s) { return sv_attn_simt_plan(s, 0); }
+SvAttnPlan sv_attn_window_plan(const SvAttnShape &s) {
+  if (!sv_attn_tc2_window_supported(s)) return sv_attn_simt_plan(s, 0);
+  SvAttnPlan p{};
+  p.use_tc = 2;
+  p.splits = 1;
+  p.ws_bytes = sv_attn_tc2_window_ws_bytes(s);
+  return p;
+}
 
 // Run the planned attention kernel (and its combine) for shape s.
 int sv_attn_run(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const void *kc, const void *vc,
@@ -47,6 +54,8 @@ int sv_attn_run(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const 
                 float scale, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream) {
   if (p.use_tc == 2) {
     if (p.ws_bytes == 0) return SPEC_ERR_CUDA;
+    if (s.window > 0)
+      return sv_attn_tc2_window(s, q, kc, vc, kt, vt, prefix_len, anc, out, scale, ws, ws_bytes, status, stream);
     return sv_attn_tc2(s, q, kc, vc, kt, vt, prefix_len, anc, out, scale, ws, ws_bytes, status, stream);
   }
   const int rc = p.use_tc ? sv_attn_tc(s, p, q, kc, vc, kt, vt, prefix_len, anc, out, scale, ws, status, stream)
