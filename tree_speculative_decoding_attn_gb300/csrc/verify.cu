@@ -26,8 +26,10 @@
 // walk in shared memory, one row, one cluster exchange), the rows' bytes at
 // large batch.  One cluster per sequence; each warp owns one contiguous piece
 // of the row, so the bonus is found from the per-warp sums by rereading one
-// warp's piece (at most a few KB, in L2).
+// warp's piece (a few KB, in L2), a vector a thread.
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -44,17 +46,22 @@ constexpr int kInFlight = 4;  // 16-byte loads of one lane in flight (twice that
 typedef unsigned long long u64;
 constexpr u64 kOne = 1ull << 60;
 
-// x in [0, 1] in units of 2^-60, cut; anything else (NaN too) sets *bad and
-// counts as 0.
-__device__ __forceinline__ u64 fixed60(float x, bool *bad) {
-  if (!(x >= 0.f && x <= 1.f)) {
-    *bad = true;
-    return 0;
-  }
-  const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
-  const u64 m = (b & 0x7FFFFFu) | 0x800000u;
-  const int sh = (int)(b >> 23) - 90;  // x = m * 2^(e - 150)
-  return sh >= 0 ? m << sh : sh > -24 ? m >> -sh : 0;
+// The bits of a float in [0, 1] as a number of units of 2^-60, cut: the 24
+// bits of the significand at the top of 64, shifted right by what the
+// exponent leaves (m 2^(e - 150) = (m 2^40 >> (130 - e)) 2^-60; PTX gives 0
+// for shifts past 63).
+__device__ __forceinline__ u64 fixed60(uint32_t b) {
+  const u64 m = (u64)(((b & 0x7FFFFFu) | 0x800000u) << 8) << 32;
+  u64 r;
+  asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(m), "r"(130u - (b >> 23)));
+  return r;
+}
+constexpr uint32_t kOneBits = 0x3F800000u;  // 1.f: bits of the floats in [0, 1] are at most these
+// Anything but a float in [0, 1] (NaN too) sets *bad and counts as 0.
+__device__ __forceinline__ uint32_t checked(uint32_t b, bool *bad) {
+  if (b <= kOneBits) return b;
+  if (b != 0x80000000u) *bad = true;  // (-0 is 0)
+  return 0;
 }
 // A uniform number as the rule takes it: in [0, 1).
 __device__ __forceinline__ float uniform(float u) { return u >= 0.f ? fminf(u, 0.99999994f) : 0.f; }
@@ -87,7 +94,9 @@ __device__ __forceinline__ u64 warp_incl_u64(u64 v) {
 struct Shared {
   int fc[SPEC_MAX_NODES], ns[SPEC_MAX_NODES], tok[SPEC_MAX_NODES], par[SPEC_MAX_NODES];
   float u[SPEC_MAX_NODES], p[SPEC_MAX_NODES], q[SPEC_MAX_NODES];
-  int removed[SPEC_MAX_NODES];  // deterministic siblings: distinct rejected tokens of the current node
+  uint8_t keep[SPEC_MAX_NODES];    // deterministic siblings: kept if the walk gets to it
+  uint8_t again[SPEC_MAX_NODES];   // its token is an earlier sibling's
+  int removed[SPEC_MAX_NODES];     // the distinct rejected tokens of the last node
   int path[SPEC_MAX_NODES + 1];
   u64 wsum[kWarps];
   u64 part[2];                  // this CTA's sum, double-buffered by exchange
@@ -123,29 +132,40 @@ struct Row {
       }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ static float at(const uint4 &v, int i) {
+  // float32 bits of element i; values outside [0, 1] are made 0 and reported
+  __device__ static uint32_t at(const uint4 &v, int i) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-    return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    if constexpr (sizeof(T) == 4) return w[i];
+    return (i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16;
+  }
+  __device__ static void unpack(const uint4 &v, uint32_t (&x)[VEC], bool *bad) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) most = max(most, x[i] = at(v, i));
+    if (most > kOneBits) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) x[i] = checked(x[i], bad);
+    }
   }
 };
 
-// max(0, p - c q), c = ci + cf * 2^-60.
-template <bool DRAFT>
-__device__ __forceinline__ u64 weight(float p, float q, uint32_t ci, u64 cf, bool *bad) {
-  const u64 fp = fixed60(p, bad);
-  if constexpr (DRAFT) {
-    if (ci | cf) {
-      const u64 fq = fixed60(q, bad);
-      const u64 cq = fq * ci + (cf ? __umul64hi(cf << 4, fq) : 0);
-      return fp > cq ? fp - cq : 0;
-    }
+// max(0, p - c q) of a vector's elements, c = ci + cf * 2^-60.  MODE: 0
+// c = 0, 1 c = 1, 2 any c.
+template <int MODE, int VEC>
+__device__ __forceinline__ void weights(const uint32_t (&p)[VEC], const uint32_t (&q)[VEC], uint32_t ci, u64 cf,
+                                        u64 (&x)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    x[i] = fixed60(p[i]);
+    if (MODE == 0) continue;
+    u64 fq = fixed60(q[i]);
+    if (MODE == 2) fq = fq * ci + __umul64hi(cf << 4, fq);
+    x[i] = x[i] > fq ? x[i] - fq : 0;
   }
-  return fp;
 }
 
 template <typename T, bool DRAFT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     verify_kernel(const T *__restrict__ p_all, const T *__restrict__ q_all, int N, int V,
                   const int32_t *__restrict__ tok, const int32_t *__restrict__ parents,
                   const int32_t *__restrict__ first_child, const int32_t *__restrict__ next_sibling,
@@ -170,29 +190,56 @@ __global__ void __launch_bounds__(kThreads)
     sh.tok[tid] = t;
     if (par >= 0 && par < N && t >= 0 && t < V) {
       const int64_t at = ((int64_t)b * N + par) * V + t;
-      const float pv = sv::to_f32(p_all[at]);
-      const float qv = DRAFT ? sv::to_f32(q_all[at]) : 1.f;
-      bad = !(pv >= 0.f && pv <= 1.f) || !(qv >= 0.f && qv <= 1.f);
-      sh.p[tid] = pv >= 0.f && pv <= 1.f ? pv : 0.f;
-      sh.q[tid] = qv >= 0.f && qv <= 1.f ? qv : 0.f;
+      sh.p[tid] = __uint_as_float(checked(__float_as_uint(sv::to_f32(p_all[at])), &bad));
+      sh.q[tid] = DRAFT ? __uint_as_float(checked(__float_as_uint(sv::to_f32(q_all[at])), &bad)) : 1.f;
     }
   }
   __syncthreads();
+  if constexpr (!DRAFT) {
+    // The walk gets to a child only past its rejected earlier siblings, so
+    // what they have left is known without walking: every child is tested at
+    // once (a thread each), and the walk below reads the answers.  (Children
+    // of a node are numbered in the order of their links; links that are not
+    // a tree's are found by the walk.)
+    const int par = tid < N ? sh.par[tid] : -1;
+    const bool real = par >= 0 && par < N && sh.tok[tid] >= 0 && sh.tok[tid] < V;
+    auto siblings = [&](auto f) {  // the ones before this child, in order
+      int c = sh.fc[par];
+      for (int n = 0; n < N && c >= 0 && c < N && c != tid; ++n) {
+        if (sh.par[c] == par && sh.tok[c] >= 0 && sh.tok[c] < V) f(c);
+        c = sh.ns[c];
+      }
+    };
+    if (real) {
+      bool again = false;
+      siblings([&](int c) { again = again || sh.tok[c] == sh.tok[tid]; });
+      sh.again[tid] = again;
+    }
+    __syncthreads();
+    if (real) {
+      double W = 1.0;
+      siblings([&](int c) {
+        if (!sh.again[c]) W = fmax(0.0, W - (double)sh.p[c]);
+      });
+      sh.keep[tid] = !sh.again[tid] && (double)sh.u[tid] * W < (double)sh.p[tid];
+    }
+    __syncthreads();
+  }
 
   // thread 0's walk, kept across the passes it asks for
   int v = 0, child = sh.fc[0], len = 0, steps = 0, n_removed = 0;
   uint32_t ci = 0;
   u64 cf = 0, D = kOne;       // drafter: c, and the residual's mass
-  double W = 1.0;             // deterministic: what the removals have left
   if (tid == 0) sh.path[0] = 0;
 
-  auto row_sum = [&](int node, uint32_t rci, u64 rcf, int removals) {
-    // this warp's piece of the row: its sum
+  // vectors of a warp's piece of a row (all rows are cut alike)
+  auto piece_of = [&](int nvec) { return ((nvec + nc * kWarps - 1) / (nc * kWarps) + 31) / 32 * 32; };
+  // this warp's piece of the row: its sum, in sh.wsum
+  auto row_sum = [&](auto mode, int node, uint32_t rci, u64 rcf, int removals) {
+    constexpr int MODE = decltype(mode)::value;
     const int64_t off = ((int64_t)b * N + node) * V;
-    const Row<T> rp(p_all, off, V), rq(DRAFT ? q_all : p_all, off, V);
-    const bool with_q = DRAFT && (rci | rcf);
-    const int nvec = rp.vectors(), pieces = nc * kWarps;
-    const int seg = ((nvec + pieces - 1) / pieces + 31) / 32 * 32;
+    const Row<T> rp(p_all, off, V), rq(MODE ? q_all : p_all, off, V);
+    const int nvec = rp.vectors(), seg = piece_of(nvec);
     const int w = rank * kWarps + warp;
     const int k1 = min(nvec, (w + 1) * seg);
     u64 s = 0;
@@ -202,23 +249,35 @@ __global__ void __launch_bounds__(kThreads)
       for (int j = 0; j < kInFlight; ++j) {
         const int k = k0 + 32 * j + lane;
         a[j] = k < k1 ? rp.load(k) : make_uint4(0, 0, 0, 0);
-        if (DRAFT) c[j] = with_q && k < k1 ? rq.load(k) : make_uint4(0, 0, 0, 0);
+        if (MODE) c[j] = k < k1 ? rq.load(k) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int j = 0; j < kInFlight; ++j)
+      for (int j = 0; j < kInFlight; ++j) {
+        uint32_t pb[VEC], qb[VEC] = {};
+        Row<T>::unpack(a[j], pb, &bad);
+        if (MODE) Row<T>::unpack(c[j], qb, &bad);
+        u64 x[VEC];
+        weights<MODE>(pb, qb, rci, rcf, x);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          s += weight<DRAFT>(Row<T>::at(a[j], i), DRAFT ? Row<T>::at(c[j], i) : 0.f, rci, rcf, &bad);
+        for (int i = 0; i < VEC; ++i) s += x[i];
+      }
     }
     if (!DRAFT) {
       for (int r = lane; r < removals; r += 32) {
         const int t = sh.removed[r], k = (t + rp.mis) / VEC;
         bool ignore;
-        if (k >= w * seg && k < k1) s -= fixed60(sv::to_f32(rp.row[t]), &ignore);
+        if (k >= w * seg && k < k1) s -= fixed60(checked(__float_as_uint(sv::to_f32(rp.row[t])), &ignore));
       }
     }
     s = warp_sum_u64(s);
     if (lane == 0) sh.wsum[warp] = s;
+  };
+  auto with_mode = [&](uint32_t rci, u64 rcf, auto f) {
+    if (!DRAFT || !(rci | rcf)) return f(std::integral_constant<int, 0>{});
+    if constexpr (DRAFT) {
+      if (rci == 1 && rcf == 0) return f(std::integral_constant<int, 1>{});
+      f(std::integral_constant<int, 2>{});
+    }
   };
   // the cluster's sum of the CTAs' wsum; sh.all holds the CTAs' own
   int parity = 0;
@@ -257,14 +316,8 @@ __global__ void __launch_bounds__(kThreads)
           keep = D > 0 && (double)sh.u[child] * q * ((double)D * 0x1p-60) < w;
           counted = true;
         } else {
-          bool again = false;
-          for (int r = 0; r < n_removed; ++r) again = again || sh.removed[r] == t;
-          const double w = again ? 0.0 : (double)sh.p[child];
-          keep = (double)sh.u[child] * W < w;
-          if (!keep && !again) {
-            sh.removed[n_removed++] = t;
-            W = fmax(0.0, W - w);
-          }
+          keep = sh.keep[child];
+          if (!keep && !sh.again[child]) sh.removed[n_removed++] = t;
         }
         if (keep) {
           if (len + 1 >= path_cap) {
@@ -277,7 +330,6 @@ __global__ void __launch_bounds__(kThreads)
           ci = 0;
           cf = 0;
           D = kOne;
-          W = 1.0;
           n_removed = 0;
           continue;
         }
@@ -297,7 +349,7 @@ __global__ void __launch_bounds__(kThreads)
       sh.len = len;
     }
     __syncthreads();
-    row_sum(sh.node, sh.ci, sh.cf, sh.n_removed);
+    with_mode(sh.ci, sh.cf, [&](auto mode) { row_sum(mode, sh.node, sh.ci, sh.cf, sh.n_removed); });
     total = cluster_total();
     if (sh.last) break;
     D = total;  // (thread 0's)
@@ -313,53 +365,65 @@ __global__ void __launch_bounds__(kThreads)
     bcf = 0;
     removals = 0;
     __syncthreads();
-    row_sum(node, 0, 0, 0);
+    row_sum(std::integral_constant<int, 0>{}, node, 0, 0, 0);
     total = cluster_total();
   }
 
-  // the bonus: the CTA, then the warp, then the element whose sum passes u * total
+  // the bonus: the CTA, then the warp whose piece's sum passes u * total; its
+  // piece is read again by the whole CTA, a vector a thread
   const u64 thr = part_of(uniform(u_bonus[b]), total);
   u64 before = 0;
   for (int i = 0; i < rank; ++i) before += sh.all[i];
   if (total > 0 && before <= thr && thr < before + sh.all[rank]) {
-    for (int i = 0; i < warp; ++i) before += sh.wsum[i];
-    if (before <= thr && thr < before + sh.wsum[warp]) {
+    int owner = 0;
+    while (before + sh.wsum[owner] <= thr) before += sh.wsum[owner++];
+    __syncthreads();  // wsum is read; it takes the warps' sums of the piece's rounds from here on
+    with_mode(bci, bcf, [&](auto mode) {
+      constexpr int MODE = decltype(mode)::value;
       const int64_t off = ((int64_t)b * N + node) * V;
-      const Row<T> rp(p_all, off, V), rq(DRAFT ? q_all : p_all, off, V);
-      const int nvec = rp.vectors(), pieces = nc * kWarps;
-      const int seg = ((nvec + pieces - 1) / pieces + 31) / 32 * 32;
-      const int w = rank * kWarps + warp;
+      const Row<T> rp(p_all, off, V), rq(MODE ? q_all : p_all, off, V);
+      const int nvec = rp.vectors(), seg = piece_of(nvec);
+      const int w = rank * kWarps + owner;
       const int k1 = min(nvec, (w + 1) * seg);
-      for (int k0 = w * seg; k0 < k1; k0 += 32) {
-        const int k = k0 + lane;
-        const uint4 a = k < k1 ? rp.load(k) : make_uint4(0, 0, 0, 0);
-        const uint4 c = DRAFT && (bci | bcf) && k < k1 ? rq.load(k) : make_uint4(0, 0, 0, 0);
+      for (int k0 = w * seg; k0 < k1; k0 += kThreads) {
+        const int k = k0 + tid;
+        uint32_t pb[VEC], qb[VEC] = {};
+        Row<T>::unpack(k < k1 ? rp.load(k) : make_uint4(0, 0, 0, 0), pb, &bad);
+        if (MODE) Row<T>::unpack(k < k1 ? rq.load(k) : make_uint4(0, 0, 0, 0), qb, &bad);
         u64 x[VEC], s = 0;
+        weights<MODE>(pb, qb, bci, bcf, x);
+        if (!DRAFT) {
+          for (int r = 0; r < removals; ++r) {
+            const int at = sh.removed[r] + rp.mis - k * VEC;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          x[i] = weight<DRAFT>(Row<T>::at(a, i), Row<T>::at(c, i), bci, bcf, &bad);
-          if (!DRAFT)
-            for (int r = 0; r < removals; ++r)
-              if (sh.removed[r] == k * VEC - rp.mis + i) x[i] = 0;
-          s += x[i];
-        }
-        const u64 incl = warp_incl_u64(s);
-        if (__any_sync(0xffffffffu, before + incl > thr)) {
-          u64 run = before + incl - s;
-          if (run <= thr && thr < before + incl) {
-            int hit = -1;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              run += x[i];
-              if (hit < 0 && run > thr) hit = k * VEC - rp.mis + i;
-            }
-            bonus[b] = hit;
+            for (int i = 0; i < VEC; ++i)
+              if (i == at) x[i] = 0;
           }
-          break;
         }
-        before += __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s += x[i];
+        const u64 incl = warp_incl_u64(s);
+        if (lane == 31) sh.wsum[warp] = incl;
+        __syncthreads();
+        u64 run = before + incl - s, round = 0;
+        for (int i = 0; i < kWarps; ++i) {
+          if (i < warp) run += sh.wsum[i];
+          round += sh.wsum[i];
+        }
+        if (run <= thr && thr < run + s) {
+          int hit = -1;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            run += x[i];
+            if (hit < 0 && run > thr) hit = k * VEC - rp.mis + i;
+          }
+          bonus[b] = hit;
+        }
+        before += round;
+        if (before > thr) break;
+        __syncthreads();
       }
-    }
+    });
   }
   if (rank == 0) {
     if (tid == 0) {
@@ -385,8 +449,12 @@ int launch_verify(const void *p, const void *q, int batch, int N, int V, const i
                   cudaStream_t stream) {
   constexpr int VEC = 16 / (int)sizeof(T);
   auto kern = verify_kernel<T, DRAFT>;
-  int nc = 8;
+  int nc = kMaxCluster;
   while (nc > 1 && (batch * nc > 304 || (nc / 2) * kThreads * VEC >= V)) nc /= 2;
+  if (nc > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+    (void)cudaGetLastError();
+    nc = 8;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nc, batch);
   cfg.blockDim = dim3(kThreads);

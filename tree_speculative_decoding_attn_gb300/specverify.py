@@ -126,27 +126,34 @@ class _Args:
     contiguous, and of the dtype and shape (or element count) the C entry
     point will take it for."""
 
-    def __init__(self, device):
-        if device.type != "cuda":
-            raise ValueError("expected a CUDA tensor")
-        if device.index != torch.cuda.current_device():
-            raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
-        self.index = device.index
+    __slots__ = ("index",)
 
-    def __call__(self, t, dtype=None, shape=None, numel=None):
-        if t is None:
-            return None
-        if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
-            raise ValueError(f"expected a tensor on cuda:{self.index}")
-        if not t.is_contiguous():
-            raise ValueError("expected a contiguous tensor")
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"dtype {t.dtype}, expected {dtype}")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if numel is not None and t.numel() != numel:
-            raise ValueError(f"{t.numel()} elements, expected {numel}")
-        return t.data_ptr()
+    def __init__(self, device):
+        self.index = torch.cuda.current_device()
+        if device.type != "cuda" or device.index != self.index:
+            raise ValueError(f"tensors on {device}, but the current device is cuda:{self.index}")
+
+    def __call__(self, t, dtype, shape):
+        if t.dtype is dtype and t.shape == shape and t.get_device() == self.index and t.is_contiguous():
+            return t.data_ptr()
+        raise self.error(t, dtype, shape)
+
+    def sized(self, t, dtype, numel):
+        """A tensor of any shape of numel elements (None: any number)."""
+        if t.get_device() == self.index and t.is_contiguous() and t.dtype is dtype and numel in (None, t.numel()):
+            return t.data_ptr()
+        raise self.error(t, dtype, (numel,))
+
+    def status(self, t):
+        """The optional device status word."""
+        return None if t is None else self.sized(t, torch.int32, None)
+
+    def error(self, t, dtype, shape):
+        if t.get_device() != self.index:
+            return ValueError(f"expected a tensor on cuda:{self.index}, not {t.device}")
+        if t.dtype is not dtype:
+            return TypeError(f"dtype {t.dtype}, expected {dtype}")
+        return ValueError(f"expected a contiguous tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _want(t, *dtypes):
@@ -156,7 +163,8 @@ def _want(t, *dtypes):
 
 
 def _stream():
-    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # (torch.cuda.current_stream() builds a Stream object: 3 us a call)
+    return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _check(fn, code):
@@ -369,11 +377,11 @@ def tree_attn_verify_window(q, k_cache, v_cache, k_tree, v_tree, prefix_len, dep
     kv, tree = (B, Hkv, S, D), (B, Hkv, N, D)
     args = (ptr(q, q.dtype, (B, N, Hq, D)), ptr(k_cache, q.dtype, kv), ptr(v_cache, q.dtype, kv),
             ptr(k_tree, q.dtype, tree), ptr(v_tree, q.dtype, tree), ptr(prefix_len, torch.int32, (B,)),
-            ptr(depth, torch.int32, (B, N)), ptr(anc_mask, torch.int64, None, B * N * mask_words(N)),
+            ptr(depth, torch.int32, (B, N)), ptr.sized(anc_mask, torch.int64, B * N * mask_words(N)),
             ptr(out, q.dtype, (B, N, Hq, D)))
     _check("tree_attn_verify_window", load().tree_attn_verify_window(
-        *args, code, B, N, Hq, Hkv, D, S, int(max_prefix), int(window), int(sinks), float(scale), ptr(workspace),
-        workspace.numel() * workspace.element_size(), ptr(dev_status, torch.int32), _stream()))
+        *args, code, B, N, Hq, Hkv, D, S, int(max_prefix), int(window), int(sinks), float(scale),
+        ptr.sized(workspace, torch.uint8, None), workspace.numel(), ptr.status(dev_status), _stream()))
 
 
 def tree_attn_verify_window_paged(q, k_pages, v_pages, block_table, k_tree, v_tree, prefix_len, depth, anc_mask, out,
@@ -391,10 +399,10 @@ def tree_attn_verify_window_paged(q, k_pages, v_pages, block_table, k_tree, v_tr
     args = (ptr(q, q.dtype, (B, N, Hq, D)), ptr(k_pages, q.dtype, kv), ptr(v_pages, q.dtype, kv),
             ptr(block_table, torch.int32, (B, mb)), bs, nb, mb, ptr(k_tree, q.dtype, tree), ptr(v_tree, q.dtype, tree),
             ptr(prefix_len, torch.int32, (B,)), ptr(depth, torch.int32, (B, N)),
-            ptr(anc_mask, torch.int64, None, B * N * mask_words(N)), ptr(out, q.dtype, (B, N, Hq, D)))
+            ptr.sized(anc_mask, torch.int64, B * N * mask_words(N)), ptr(out, q.dtype, (B, N, Hq, D)))
     _check("tree_attn_verify_window_paged", load().tree_attn_verify_window_paged(
-        *args, code, B, N, Hq, Hkv, D, int(max_prefix), int(window), int(sinks), float(scale), ptr(workspace),
-        workspace.numel() * workspace.element_size(), ptr(dev_status, torch.int32), _stream()))
+        *args, code, B, N, Hq, Hkv, D, int(max_prefix), int(window), int(sinks), float(scale),
+        ptr.sized(workspace, torch.uint8, None), workspace.numel(), ptr.status(dev_status), _stream()))
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -523,10 +531,10 @@ def spec_verify_probs(target_probs, tok, parents, first_child, next_sibling, u_a
     ptr = _Args(target_probs.device)
     node, cap = (B, N), acc_path.shape[1]
     _check("spec_verify_probs", load().spec_verify_probs(
-        ptr(target_probs), ptr(draft_probs, dt, (B, N, V)), _DT.get(dt, -1), B, N, V, ptr(tok, i32, node),
-        ptr(parents, i32, node), ptr(first_child, i32, node), ptr(next_sibling, i32, node), ptr(u_accept, f32, node),
-        ptr(u_bonus, f32, (B,)), cap, ptr(acc_len, i32, (B,)), ptr(acc_path, i32, (B, cap)), ptr(bonus, i32, (B,)),
-        ptr(dev_status, i32), _stream()))
+        ptr(target_probs, dt, (B, N, V)), None if draft_probs is None else ptr(draft_probs, dt, (B, N, V)),
+        _DT.get(dt, -1), B, N, V, ptr(tok, i32, node), ptr(parents, i32, node), ptr(first_child, i32, node),
+        ptr(next_sibling, i32, node), ptr(u_accept, f32, node), ptr(u_bonus, f32, (B,)), cap,
+        ptr(acc_len, i32, (B,)), ptr(acc_path, i32, (B, cap)), ptr(bonus, i32, (B,)), ptr.status(dev_status), _stream()))
 
 
 def kv_pages_workspace_bytes(batch, max_blocks, num_blocks):
@@ -539,9 +547,9 @@ def kv_pages_fork(block_table, prefix_len, parent, ref_count, table_out, prefix_
     out, nb, i32 = parent.shape[0], ref_count.shape[0], torch.int32
     ptr = _Args(block_table.device)
     _check("kv_pages_fork", load().kv_pages_fork(
-        ptr(block_table, i32), ptr(prefix_len, i32, (B,)), ptr(parent, i32, (out,)), B, out, mb, nb,
+        ptr(block_table, i32, (B, mb)), ptr(prefix_len, i32, (B,)), ptr(parent, i32, (out,)), B, out, mb, nb,
         ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (out, mb)), ptr(prefix_len_out, i32, (out,)),
-        ptr(ref_out, i32, (nb,)), ptr(dev_status, i32), _stream()))
+        ptr(ref_out, i32, (nb,)), ptr.status(dev_status), _stream()))
 
 
 def kv_pages_free(block_table, prefix_len, ref_count, table_out, ref_out, block_size, window=0, sinks=0, spare=0,
@@ -551,15 +559,17 @@ def kv_pages_free(block_table, prefix_len, ref_count, table_out, ref_out, block_
     nb, i32 = ref_count.shape[0], torch.int32
     ptr = _Args(block_table.device)
     _check("kv_pages_free", load().kv_pages_free(
-        ptr(block_table, i32), ptr(prefix_len, i32, (B,)), B, mb, int(block_size), nb, int(window), int(sinks),
+        ptr(block_table, i32, (B, mb)), ptr(prefix_len, i32, (B,)), B, mb, int(block_size), nb, int(window), int(sinks),
         int(spare), ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)), ptr(ref_out, i32, (nb,)),
-        ptr(dev_status, i32), _stream()))
+        ptr.status(dev_status), _stream()))
 
 
 def _pool(ptr, k_pages, v_pages):
-    """(K, V, element bytes, layers, KV heads, head_dim, block size, blocks) of a pool with or without the layer axis."""
+    """(K, V, element bytes, layers, KV heads, head_dim, block size, blocks)
+    of a pool with or without the layer axis."""
     L, (nb, Hkv, bs, D) = (1, k_pages.shape) if k_pages.dim() == 4 else (k_pages.shape[0], k_pages.shape[1:])
-    return ptr(k_pages), ptr(v_pages, k_pages.dtype, k_pages.shape), k_pages.element_size(), L, Hkv, D, bs, nb
+    dt, shape = k_pages.dtype, k_pages.shape
+    return ptr(k_pages, dt, shape), ptr(v_pages, dt, shape), k_pages.element_size(), L, Hkv, D, bs, nb
 
 
 def kv_pages_reserve(k_pages, v_pages, block_table, prefix_len, need, ref_count, table_out, ref_out, workspace=None,
@@ -575,9 +585,9 @@ def kv_pages_reserve(k_pages, v_pages, block_table, prefix_len, need, ref_count,
     if workspace is None:
         workspace = _scratch(kv_pages_workspace_bytes(B, mb, nb), block_table)
     _check("kv_pages_reserve", load().kv_pages_reserve(
-        *pool, ptr(block_table, i32), B, mb, ptr(prefix_len, i32, (B,)), ptr(need, i32, (B,)),
-        ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)), ptr(ref_out, i32, (nb,)), ptr(workspace),
-        workspace.numel() * workspace.element_size(), ptr(dev_status, i32), _stream()))
+        *pool, ptr(block_table, i32, (B, mb)), B, mb, ptr(prefix_len, i32, (B,)), ptr(need, i32, (B,)),
+        ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)), ptr(ref_out, i32, (nb,)),
+        ptr.sized(workspace, torch.uint8, None), workspace.numel(), ptr.status(dev_status), _stream()))
 
 
 def kv_pages_compact(k_pages, v_pages, block_table, ref_count, table_out, ref_out, n_used, remap=None, workspace=None,
@@ -592,6 +602,6 @@ def kv_pages_compact(k_pages, v_pages, block_table, ref_count, table_out, ref_ou
     if workspace is None:
         workspace = _scratch(kv_pages_workspace_bytes(B, mb, nb), block_table)
     _check("kv_pages_compact", load().kv_pages_compact(
-        *pool, ptr(block_table, i32), B, mb, ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)),
-        ptr(ref_out, i32, (nb,)), ptr(n_used, i32, (1,)), ptr(remap, i32, (nb,)), ptr(workspace),
-        workspace.numel() * workspace.element_size(), ptr(dev_status, i32), _stream()))
+        *pool, ptr(block_table, i32, (B, mb)), B, mb, ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)),
+        ptr(ref_out, i32, (nb,)), ptr(n_used, i32, (1,)), None if remap is None else ptr(remap, i32, (nb,)),
+        ptr.sized(workspace, torch.uint8, None), workspace.numel(), ptr.status(dev_status), _stream()))
