@@ -141,14 +141,29 @@ struct SchedBase {
 // query heads that do not divide 128 take gp rows per node, gp the next power
 // of two (the rows past the group are padding: the tensor maps read them as
 // zero and drop them on the way out).
+//
+// Up to 64 sink keys ride in the upper half of a tree tile of up to 64 nodes
+// (keys 64 .. 64 + fold - 1 of the tile) instead of filling a tile of their
+// own: one tile less per row group, and half the bytes.
+//
+// whole: a row group is never cut, cluster c takes an equal share of them
+// and there is nothing to merge (the host's choice, tc2_whole).
+constexpr int kFold = 64;  // keys of half a tile
 template <bool WIN>
 struct Sched : SchedBase {};
 template <>
 struct Sched<true> : SchedBase {
   sv::Window win;
   int gp;
+  int whole;
   __device__ sv::WinSpan span(int P) const {
-    return sv::win_span(win.window, win.sinks, P, kBN, pg.table ? kBN : 1);
+    sv::WinSpan v = sv::win_span(win.window, win.sinks, P, kBN, pg.table ? kBN : 1);
+    if (n_nodes <= kFold && v.s_end <= kFold) {
+      v.fold = v.s_end;
+      v.n_tiles -= v.n_sink;
+      v.n_sink = 0;
+    }
+    return v;
   }
 };
 
@@ -374,7 +389,9 @@ __device__ __forceinline__ void cur_next(Cur<WIN> &c, const Sched<WIN> &s) {
 template <bool WIN>
 __device__ __forceinline__ int tile_keys(const Cur<WIN> &c, const Sched<WIN> &s) {
   if constexpr (WIN)
-    return c.t < s.nt ? min(kBN, s.n_nodes - c.t * kBN) : sv::win_keys(c.sp, c.P, c.t - s.nt, kBN);
+    return c.t >= s.nt ? sv::win_keys(c.sp, c.P, c.t - s.nt, kBN)
+           : c.sp.fold ? kFold + c.sp.fold
+                       : min(kBN, s.n_nodes - c.t * kBN);
   return c.t < s.nt ? min(kBN, s.n_nodes - c.t * kBN) : min(kBN, c.P - (c.t - s.nt) * kBN);
 }
 
@@ -401,15 +418,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // last key of a partial tile, up to the next multiple of 16 (the last PV
 // k-step reads them with zero probabilities; stale cache rows need not be
 // finite).  WIN: likewise the rows between the sinks and the root's window,
-// which a tile starting at a block's boundary may hold.  Full warp; false on
-// timeout.
+// which a tile starting at a block's boundary may hold, and those between the
+// last node and the sinks of a tree tile that holds both.  Full warp; false
+// on timeout.
 template <bool WIN>
 __device__ __forceinline__ bool v_ready(Bars *bars, uint8_t *sV, int g, const Cur<WIN> &c, const Sched<WIN> &s) {
   const int st = g % kVS, nkeys = tile_keys(c, s);
   if (!warp_wait(&bars->vland[st], (g / kVS) & 1)) return false;
   if constexpr (WIN) {
-    const int key0 = c.t < s.nt ? c.sp.lo : tile_key0(c, s);
-    const int d0 = max(0, s.win.sinks - key0), d1 = min(nkeys, c.sp.lo - key0);
+    int d0, d1;
+    if (c.t < s.nt) {
+      d0 = s.n_nodes;
+      d1 = c.sp.fold ? kFold : 0;
+    } else {
+      const int key0 = tile_key0(c, s);
+      d0 = max(0, s.win.sinks - key0);
+      d1 = min(nkeys, c.sp.lo - key0);
+    }
     if (d0 < d1) {
       uint4 *v = reinterpret_cast<uint4 *>(sV + st * kVBytes);
       for (int e = d0 * 8 + (int)(threadIdx.x & 31); e < d1 * 8; e += 32) v[e] = make_uint4(0, 0, 0, 0);
@@ -426,6 +451,15 @@ __device__ __forceinline__ bool v_ready(Bars *bars, uint8_t *sV, int g, const Cu
   return true;
 }
 
+// V maps whose box is half a tile (64 keys x 64 dims), for tree tiles that
+// also hold sinks.
+template <bool WIN>
+struct Halves {};
+template <>
+struct Halves<true> {
+  CUtensorMap vc, vt;
+};
+
 // MAXW: ancestor-mask words per node, rounded up to 1, 2 or 4 (trees of up
 // to 64, 128 or 256 nodes; one, one or two tree tiles).
 template <int MAXW, bool WIN>
@@ -433,6 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attn_tc2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kc,
                     const __grid_constant__ CUtensorMap tm_vc, const __grid_constant__ CUtensorMap tm_kt,
                     const __grid_constant__ CUtensorMap tm_vt, const __grid_constant__ CUtensorMap tm_o,
+                    const __grid_constant__ Halves<WIN> tm_half,
                     const Sched<WIN> s_in, const uint64_t *__restrict__ anc, void *__restrict__ ws, int Hq,
                     float scale_log2, int32_t *status) {
   // the tree-tile count as a compile-time constant in every schedule step
@@ -470,9 +505,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_kt);
     tma_prefetch_desc(&tm_vt);
     tma_prefetch_desc(&tm_o);
+    if constexpr (WIN) {
+      tma_prefetch_desc(&tm_half.vc);
+      tma_prefetch_desc(&tm_half.vt);
+    }
   }
   // The range lookup (warp 0) overlaps the barrier and TMEM set-up (warp 1).
-  if (warp == 0) {
+  bool whole = false;
+  if constexpr (WIN) whole = s.whole;
+  if (warp == 0 && whole) {
+    // this cluster's row groups [r0, r1): the tiles of their sequences
+    const long long rgs = (long long)s.batch * s.gpb();
+    const long long r0 = rgs * cluster / s.n_clusters, r1 = rgs * (cluster + 1) / s.n_clusters;
+    const int b0 = (int)(r0 / s.gpb());
+    long long T = 0;
+    int raw0 = 0, raw1 = 0;
+    for (int i = 0; (long long)(b0 + i) * s.gpb() < r1; i += 32) {
+      const int b = b0 + i + lane;
+      const int raw = b < s.batch ? s.prefix_len[b] : 0;
+      const long long first = max(r0, (long long)b * s.gpb()), last = min(r1, (long long)(b + 1) * s.gpb());
+      if (last > first) T += (last - first) * tiles_of(s, raw);
+      if (i == 0) {
+        raw0 = __shfl_sync(0xffffffffu, raw, 0);
+        raw1 = __shfl_sync(0xffffffffu, raw, 1);
+      }
+    }
+    T = warp_sum_ll(T);
+    if (lane == 0) {
+      bars->start_b = b0;
+      bars->start_gi = (int)(r0 % s.gpb());
+      bars->start_t = 0;
+      bars->n_tiles = (int)T;
+      bars->start_raw = raw0;
+      bars->start_raw_next = raw1;
+    }
+  } else if (warp == 0) {
     SeqTab tb;
     tab_load(s, tb);
     long long W, U;
@@ -604,14 +671,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // multiples of 128; a bad block id gives row -1, read as zeros)
         const int row0 =
             tree ? bh * N + c.t * kBN : sv::kv_row(s.pg, c.b, s.hkv, kvh, s.s_max, tile_key0(c, s), status);
+        const bool both = WIN && tree && c.sp.fold > 0;  // nodes, then sinks
+        const int sink0 = both ? sv::kv_row(s.pg, c.b, s.hkv, kvh, s.s_max, 0, status) : 0;
         if (is_v) {
           mbar_expect_tx(land, kVBytes);
-          tma_load_2d(sV + st * kVBytes, tree ? &tm_vt : &tm_vc, 64 * (int)rank, row0, land);
+          if constexpr (WIN) {
+            if (both) {
+              tma_load_2d(sV + st * kVBytes, &tm_half.vt, 64 * (int)rank, row0, land);
+              tma_load_2d(sV + st * kVBytes + kVBytes / 2, &tm_half.vc, 64 * (int)rank, sink0, land);
+            }
+          }
+          if (!both) tma_load_2d(sV + st * kVBytes, tree ? &tm_vt : &tm_vc, 64 * (int)rank, row0, land);
         } else {
           mbar_expect_tx(land, kKBytes);
-          const CUtensorMap *m = tree ? &tm_kt : &tm_kc;
-          tma_load_2d(sK + st * kKBytes, m, 0, row0 + 64 * (int)rank, land);
-          tma_load_2d(sK + st * kKBytes + kKHalf, m, 64, row0 + 64 * (int)rank, land);
+          const CUtensorMap *m = tree && !(both && rank == 1) ? &tm_kt : &tm_kc;
+          const int row = both ? (rank == 1 ? sink0 : row0) : row0 + 64 * (int)rank;
+          tma_load_2d(sK + st * kKBytes, m, 0, row, land);
+          tma_load_2d(sK + st * kKBytes + kKHalf, m, 64, row, land);
         }
         ++issued;
         cur_next(c, s);
@@ -890,8 +966,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 return (uint32_t)((x | (x >> 24)) & 0xFFFFull);
               };
               if constexpr (MP == 1) {
-                va &= mine(amask_a.w[0]);
-                vb &= mine(amask_b.w[0]);
+                uint32_t sink = 0;  // WIN: the sinks behind the nodes, visible to every row
+                if constexpr (WIN) sink = c.sp.fold ? in & 0xFFFF0000u : 0;
+                const uint32_t nodes = WIN ? in & below(N) : in;
+                va = (nodes & mine(amask_a.w[0])) | sink;
+                vb = (nodes & mine(amask_b.w[0])) | sink;
               } else {
                 va &= mine(amask_a.w[0]) | (mine(amask_a.w[1]) << 16);
                 vb &= mine(amask_b.w[0]) | (mine(amask_b.w[1]) << 16);
@@ -1319,6 +1398,34 @@ int tc2_clusters() {
   return clusters;
 }
 
+// Whether a window call keeps its row groups whole.  In tiles of 128 keys
+// (about 0.9 us each): cut in equal ranges, the clusters take the average and
+// then the merge; kept whole, the busiest takes its number of row groups,
+// each at the longest a prefix may be, and no merge is launched.
+constexpr int kMergeTiles = 6;
+bool tc2_whole(const SvAttnShape &s, const Sched<true> &sc, int clusters) {
+  const long long span = (long long)sc.win.window - 1 + (s.block_table ? kBN - 1 : 0);
+  const long long keys = span < s.max_prefix ? span : s.max_prefix;
+  const long long sinks = s.n_nodes <= kFold && sc.win.sinks <= kFold ? 0 : sc.win.sinks < s.max_prefix ? sc.win.sinks : s.max_prefix;
+  const long long n = (s.n_nodes + kBN - 1) / kBN + (keys + kBN - 1) / kBN + (sinks + kBN - 1) / kBN + kSegW;
+  const long long rgs = (long long)s.batch * s.hkv * ((s.n_nodes * sc.gp + kPairRows - 1) / kPairRows);
+  return (rgs + clusters - 1) / clusters * n <= rgs * n / clusters + kMergeTiles;
+}
+
+// Sets an instance's shared-memory size, once per device.
+template <typename K>
+bool tc2_set_smem(K kern, int instance, bool win) {
+  static std::atomic<uint64_t> done[2][3];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  std::atomic<uint64_t> &d = done[win][instance];
+  if (d.load() >> dev & 1) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess)
+    return false;
+  d.fetch_or(1ull << dev);
+  return true;
+}
+
 int pow2_at_least(int x) {
   int p = 1;
   while (p < x) p *= 2;
@@ -1370,6 +1477,17 @@ int tc2_run(const SvAttnShape &s, Sched<WIN> &sc, int rows_g, const void *q, con
     if (make_map(&mkt, kt, 2, dims, strides, kbox) != SPEC_OK) return SPEC_ERR_CUDA;
     if (make_map(&mvt, vt, 2, dims, strides, vbox) != SPEC_OK) return SPEC_ERR_CUDA;
   }
+  Halves<WIN> half;
+  if constexpr (WIN) {
+    const cuuint64_t rows = s.block_table ? (cuuint64_t)s.num_blocks * s.hkv * s.block_size
+                                          : (cuuint64_t)s.batch * s.hkv * s.s_max;
+    const cuuint64_t dims[2] = {(cuuint64_t)kD, rows > 0 ? rows : 1};
+    const cuuint64_t tree_dims[2] = {(cuuint64_t)kD, (cuuint64_t)s.batch * s.hkv * s.n_nodes};
+    const cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)kFold};
+    if (make_map(&half.vc, vc, 2, dims, strides, box) != SPEC_OK) return SPEC_ERR_CUDA;
+    if (make_map(&half.vt, vt, 2, tree_dims, strides, box) != SPEC_OK) return SPEC_ERR_CUDA;
+  }
   sc.prefix_len = prefix_len;
   sc.batch = s.batch;
   sc.hkv = s.hkv;
@@ -1386,12 +1504,13 @@ int tc2_run(const SvAttnShape &s, Sched<WIN> &sc, int rows_g, const void *q, con
   auto kern = sc.mw == 1   ? attn_tc2_kernel<1, WIN>
               : sc.mw == 2 ? attn_tc2_kernel<2, WIN>
                            : attn_tc2_kernel<4, WIN>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess)
-    return SPEC_ERR_CUDA;
-  kern<<<2 * C, kThreads, kSmemBytes, stream>>>(mq, mkc, mvc, mkt, mvt, mo, sc, anc, ws, s.hq,
+  if (!tc2_set_smem(kern, sc.mw == 1 ? 0 : sc.mw == 2 ? 1 : 2, WIN)) return SPEC_ERR_CUDA;
+  kern<<<2 * C, kThreads, kSmemBytes, stream>>>(mq, mkc, mvc, mkt, mvt, mo, half, sc, anc, ws, s.hq,
                                                scale * 1.4426950408889634f, status);
   if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
-  if (C > 1) {
+  bool merge = C > 1;
+  if constexpr (WIN) merge = merge && !sc.whole;
+  if (merge) {
     // programmatic dependent launch: the merge blocks locate their row groups
     // while the main kernel runs (it triggers its dependents after setup)
     cudaLaunchAttribute attr[1];
@@ -1460,6 +1579,7 @@ int sv_attn_tc2_window(const SvAttnShape &s, const void *q, const void *kc, cons
   constexpr int kAll = (1 << 30) + SPEC_MAX_NODES;
   sc.win = sv::Window{s.depth, s.window < kAll ? s.window : kAll, s.sinks < kAll ? s.sinks : kAll};
   sc.gp = pow2_at_least(s.hq / s.hkv);
+  sc.whole = tc2_whole(s, sc, c);
   if (s.window < s.n_nodes) {
     uint64_t *masks = reinterpret_cast<uint64_t *>(static_cast<uint8_t *>(ws) + window_masks_at(c));
     window_mask_kernel<<<s.batch, 256, 0, stream>>>(anc, prefix_len, sc.win, s.n_nodes, masks);

@@ -148,6 +148,7 @@ struct WinSpan {
   int w0;     // first key of the window tiles (<= lo)
   int s_end;  // keys of the sink tiles (<= w0)
   int n_sink, n_tiles;
+  int fold;   // sink keys that ride in the tree tile instead (attn_tc2; 0 here)
 };
 __device__ __forceinline__ WinSpan win_span(int window, int sinks, int P, int tile, int align) {
   WinSpan v;
@@ -156,6 +157,7 @@ __device__ __forceinline__ WinSpan win_span(int window, int sinks, int P, int ti
   v.s_end = min(sinks, v.w0);
   v.n_sink = (v.s_end + tile - 1) / tile;
   v.n_tiles = v.n_sink + (P - v.w0 + tile - 1) / tile;
+  v.fold = 0;
   return v;
 }
 // First key and key count of prefix tile i (0 <= i < n_tiles).
