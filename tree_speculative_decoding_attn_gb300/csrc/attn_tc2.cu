@@ -417,38 +417,87 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // Waits for this CTA's V half of tile g to land and zeroes its rows past the
 // last key of a partial tile, up to the next multiple of 16 (the last PV
 // k-step reads them with zero probabilities; stale cache rows need not be
-// finite).  WIN: likewise the rows between the sinks and the root's window,
-// which a tile starting at a block's boundary may hold, and those between the
-// last node and the sinks of a tree tile that holds both.  Full warp; false
-// on timeout.
-template <bool WIN>
-__device__ __forceinline__ bool v_ready(Bars *bars, uint8_t *sV, int g, const Cur<WIN> &c, const Sched<WIN> &s) {
-  const int st = g % kVS, nkeys = tile_keys(c, s);
+// finite).  Full warp; false on timeout.
+__device__ __forceinline__ void zero_v_rows(uint8_t *v_tile, int r0, int r1) {
+  uint4 *v = reinterpret_cast<uint4 *>(v_tile);
+  for (int e = r0 * 8 + (int)(threadIdx.x & 31); e < r1 * 8; e += 32) v[e] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+}
+__device__ __forceinline__ bool v_ready(Bars *bars, uint8_t *sV, int g, int nkeys) {
+  const int st = g % kVS;
   if (!warp_wait(&bars->vland[st], (g / kVS) & 1)) return false;
-  if constexpr (WIN) {
-    int d0, d1;
-    if (c.t < s.nt) {
-      d0 = s.n_nodes;
-      d1 = c.sp.fold ? kFold : 0;
-    } else {
-      const int key0 = tile_key0(c, s);
-      d0 = max(0, s.win.sinks - key0);
-      d1 = min(nkeys, c.sp.lo - key0);
-    }
-    if (d0 < d1) {
-      uint4 *v = reinterpret_cast<uint4 *>(sV + st * kVBytes);
-      for (int e = d0 * 8 + (int)(threadIdx.x & 31); e < d1 * 8; e += 32) v[e] = make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
-    }
-  }
-  if (nkeys < kBN) {
-    uint4 *v = reinterpret_cast<uint4 *>(sV + st * kVBytes);
-    const int end = min(kBN, (nkeys + 15) & ~15) * 8;
-    for (int e = nkeys * 8 + (int)(threadIdx.x & 31); e < end; e += 32) v[e] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-  }
+  if (nkeys < kBN) zero_v_rows(sV + st * kVBytes, nkeys, min(kBN, (nkeys + 15) & ~15));
   __syncwarp();
   return true;
+}
+
+// ---------------------------------------------------------------------------
+// WIN: what the scalar warps (loads, MMA issue) run per tile is on the way of
+// every tile, a chain of dependent instructions of one thread: with each
+// tile's place and extent computed from the schedule per tile, the 64-sequence
+// serving shape took 1.25 us per tile of a range; with loops per segment that
+// only step (below), and barriers tested before they are waited for (a wait
+// for a phase that is long complete costs some 290 cycles), 0.9 us.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ bool thread_ready(uint64_t *bar, uint32_t parity) {
+  return mbar_test(bar, parity) || mbar_wait_cluster(bar, parity, kWaitLimit);
+}
+__device__ __forceinline__ bool warp_ready(uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_test(bar, parity)) || warp_wait(bar, parity);
+}
+// A place in a ring of N buffers and the parity of its use.
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t parity = 0;
+  bool again = false;  // past the first round
+  __device__ void next() {
+    if (++i == N) {
+      i = 0;
+      parity ^= 1;
+      again = true;
+    }
+  }
+};
+// f(te, last) for the segments of a cluster's range in order: tiles c.t ..
+// te - 1 of row group (c.b, c.gi); last: the range ends there.  f leaves c.t
+// at te; false ends the walk.
+template <typename F>
+__device__ __forceinline__ bool for_segments(Cur<true> &c, const Sched<true> &s, int T, F f) {
+  while (T > 0) {
+    const int te = min(c.n, c.t + T);
+    T -= te - c.t;
+    if (!f(te, T == 0)) return false;
+    if (T > 0) {
+      c.t = c.n - 1;
+      cur_next(c, s);
+    }
+  }
+  return true;
+}
+// Keys of tile c.t, whose V half has landed, if it is one that may hold rows
+// to be zeroed: those past its last key up to the next multiple of 16, those
+// between the sinks and the root's window (the first window tile, where it
+// starts at a block's boundary), those between the last node and the sinks of
+// a tree tile that holds both.
+__device__ __forceinline__ int special_keys(uint8_t *v_tile, const Cur<true> &c, const Sched<true> &s) {
+  const int nkeys = tile_keys(c, s);
+  int d0, d1;
+  if (c.t < s.nt) {
+    d0 = s.n_nodes;
+    d1 = c.sp.fold ? kFold : 0;
+  } else {
+    const int key0 = tile_key0(c, s);
+    d0 = max(0, s.win.sinks - key0);
+    d1 = min(nkeys, c.sp.lo - key0);
+  }
+  if (d0 < d1) zero_v_rows(v_tile, d0, d1);
+  if (nkeys < kBN) zero_v_rows(v_tile, nkeys, min(kBN, (nkeys + 15) & ~15));
+  __syncwarp();
+  return nkeys;
+}
+__device__ __forceinline__ bool is_special(const Cur<true> &c, const Sched<true> &s) {
+  return c.t <= s.nt + c.sp.n_sink || c.t == c.n - 1;
 }
 
 // V maps whose box is half a tile (64 keys x 64 dims), for tree tiles that
@@ -621,8 +670,116 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ loads
     if (lane == 0) {
       const bool is_v = warp == 10;
+      int issued = 0, q_issued = 0;
+      if constexpr (WIN) {
+        Cur<true> c = cur_begin(bars, s);
+        Ring<kQB> qr;
+        const CUtensorMap *tree_map = is_v ? &tm_vt : &tm_kt, *prefix_map = is_v ? &tm_vc : &tm_kc;
+        // the tiles' ring (this thread's: K's or V's), its barriers side by side
+        Ring<kKS> r;
+        static_assert(kKS == kVS, "one ring type for both");
+        uint64_t *const empty0 = is_v ? bars->vempty : bars->kempty;
+        uint64_t *const land0 = is_v ? bars->vland : rank == 0 ? bars->kfull : bars->kland;
+        uint8_t *const ring0 = is_v ? sV : sK;
+        constexpr uint32_t kBytes = kKBytes;
+        static_assert(kKBytes == kVBytes, "one tile size for both");
+        auto slot = [&]() -> bool {
+          if ((r.again && !thread_ready(&empty0[r.i], r.parity ^ 1)) || bars->abort) {
+            give_up(bars, status);
+            return false;
+          }
+          mbar_expect_tx(&land0[r.i], kBytes);
+          return true;
+        };
+        // a bad block's tile lies outside the map and reads as zeros
+        auto read_row = [](int row) { return row < 0 ? 0x7FFF0000 : row; };
+        // this CTA's half of a tile of 128 rows from row0 on
+        auto load = [&](const CUtensorMap *m, int row0) -> bool {
+          if (!slot()) return false;
+          uint8_t *dst = ring0 + r.i * kBytes;
+          uint64_t *land = &land0[r.i];
+          if (is_v) {
+            tma_load_2d(dst, m, 64 * (int)rank, row0, land);
+          } else {
+            tma_load_2d(dst, m, 0, row0 + 64 * (int)rank, land);
+            tma_load_2d(dst + kKHalf, m, 64, row0 + 64 * (int)rank, land);
+          }
+          ++issued;
+          r.next();
+          return true;
+        };
+        for_segments(c, s, T, [&](int te, bool) -> bool {
+          const int kvh = c.gi / pairs, pair = c.gi % pairs;
+          const int bh = c.b * s.hkv + kvh;
+          if (!is_v) {
+            if ((qr.again && !thread_ready(&bars->qempty[qr.i], qr.parity ^ 1)) || bars->abort) {
+              give_up(bars, status);
+              return false;
+            }
+            uint64_t *qbar = rank == 0 ? &bars->qfull[qr.i] : &bars->qland[qr.i];
+            mbar_expect_tx(qbar, kQBytes);
+            const int node0 = c.b * N + (pair * kPairRows + (int)rank * 128) / G;
+            tma_load_4d(sQ + qr.i * kQBytes, &tm_q, 0, 0, kvh, node0, qbar);
+            tma_load_4d(sQ + qr.i * kQBytes + kQHalf, &tm_q, 64, 0, kvh, node0, qbar);
+            ++q_issued;
+            qr.next();
+          }
+          if (c.t == 0 && c.sp.fold) {  // the nodes in the tile's lower half, the sinks in its upper
+            const int sink0 = read_row(sv::kv_row(s.pg, c.b, s.hkv, kvh, s.s_max, 0, status));
+            if (!slot()) return false;
+            uint8_t *dst = ring0 + r.i * kBytes;
+            uint64_t *land = &land0[r.i];
+            if (is_v) {
+              tma_load_2d(dst, &tm_half.vt, 64 * (int)rank, bh * N, land);
+              tma_load_2d(dst + kBytes / 2, &tm_half.vc, 64 * (int)rank, sink0, land);
+            } else {
+              const CUtensorMap *m = rank == 1 ? &tm_kc : &tm_kt;
+              const int row = rank == 1 ? sink0 : bh * N;
+              tma_load_2d(dst, m, 0, row, land);
+              tma_load_2d(dst + kKHalf, m, 64, row, land);
+            }
+            ++issued;
+            r.next();
+            ++c.t;
+          }
+          for (; c.t < te && c.t < s.nt; ++c.t)
+            if (!load(tree_map, bh * N + c.t * kBN)) return false;
+          for (; c.t < te && c.t < s.nt + c.sp.n_sink; ++c.t)
+            if (!load(prefix_map, read_row(sv::kv_row(s.pg, c.b, s.hkv, kvh, s.s_max, (c.t - s.nt) * kBN, status))))
+              return false;
+          if (c.t >= te) return true;
+          const int key = c.sp.w0 + (c.t - s.nt - c.sp.n_sink) * kBN;
+          if (!s.pg.table) {
+            int row = bh * s.s_max + key;
+            for (; c.t < te; ++c.t, row += kBN)
+              if (!load(prefix_map, row)) return false;
+          } else {
+            // (a tile lies inside one block; the next block's id is loaded a tile ahead)
+            const int32_t *tab = s.pg.table + (int64_t)c.b * s.pg.max_blocks;
+            int j = key / s.pg.block_size, off = key - j * s.pg.block_size;
+            int blk = __ldg(tab + j);
+            for (; c.t < te; ++c.t) {
+              const bool step = off + kBN == s.pg.block_size;
+              const int next = step && c.t + 1 < te ? __ldg(tab + j + 1) : 0;
+              int row = read_row(-1);
+              if (blk >= 0 && blk < s.pg.num_blocks)
+                row = (blk * s.hkv + kvh) * s.pg.block_size + off;
+              else
+                sv::report(status, SPEC_DEV_BAD_BLOCK);
+              if (!load(prefix_map, row)) return false;
+              off += kBN;
+              if (step) {
+                off = 0;
+                ++j;
+                blk = next;
+              }
+            }
+          }
+          return true;
+        });
+      } else {
       Cur<WIN> c = cur_begin(bars, s);
-      int seg = 0, issued = 0, q_issued = 0;
+      int seg = 0;
       Cur<WIN> cpf = c;  // kPrefetch tiles ahead of c
       for (int i = 0; i < kPrefetch && i < T; ++i) cur_next(cpf, s);
       for (int g = 0; g < T; ++g) {
@@ -635,7 +792,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int pbh = cpf.b * s.hkv + cpf.gi / pairs;
           const bool ptree = cpf.t < s.nt;
           const int prow = ptree ? pbh * N + cpf.t * kBN
-                                 : sv::kv_row(s.pg, cpf.b, s.hkv, cpf.gi / pairs, s.s_max, tile_key0(cpf, s), nullptr);
+                                 : sv::kv_row(s.pg, cpf.b, s.hkv, cpf.gi / pairs, s.s_max, (cpf.t - s.nt) * kBN, nullptr);
           if (is_v) {
             tma_prefetch_2d(ptree ? &tm_vt : &tm_vc, 64 * (int)rank, prow);
           } else {
@@ -670,27 +827,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // (a 128-key tile lies inside one cache block: block sizes are
         // multiples of 128; a bad block id gives row -1, read as zeros)
         const int row0 =
-            tree ? bh * N + c.t * kBN : sv::kv_row(s.pg, c.b, s.hkv, kvh, s.s_max, tile_key0(c, s), status);
-        const bool both = WIN && tree && c.sp.fold > 0;  // nodes, then sinks
-        const int sink0 = both ? sv::kv_row(s.pg, c.b, s.hkv, kvh, s.s_max, 0, status) : 0;
+            tree ? bh * N + c.t * kBN : sv::kv_row(s.pg, c.b, s.hkv, kvh, s.s_max, (c.t - s.nt) * kBN, status);
         if (is_v) {
           mbar_expect_tx(land, kVBytes);
-          if constexpr (WIN) {
-            if (both) {
-              tma_load_2d(sV + st * kVBytes, &tm_half.vt, 64 * (int)rank, row0, land);
-              tma_load_2d(sV + st * kVBytes + kVBytes / 2, &tm_half.vc, 64 * (int)rank, sink0, land);
-            }
-          }
-          if (!both) tma_load_2d(sV + st * kVBytes, tree ? &tm_vt : &tm_vc, 64 * (int)rank, row0, land);
+          tma_load_2d(sV + st * kVBytes, tree ? &tm_vt : &tm_vc, 64 * (int)rank, row0, land);
         } else {
           mbar_expect_tx(land, kKBytes);
-          const CUtensorMap *m = tree && !(both && rank == 1) ? &tm_kt : &tm_kc;
-          const int row = both ? (rank == 1 ? sink0 : row0) : row0 + 64 * (int)rank;
-          tma_load_2d(sK + st * kKBytes, m, 0, row, land);
-          tma_load_2d(sK + st * kKBytes + kKHalf, m, 64, row, land);
+          const CUtensorMap *m = tree ? &tm_kt : &tm_kc;
+          tma_load_2d(sK + st * kKBytes, m, 0, row0 + 64 * (int)rank, land);
+          tma_load_2d(sK + st * kKBytes + kKHalf, m, 64, row0 + 64 * (int)rank, land);
         }
         ++issued;
         cur_next(c, s);
+      }
       }
       if (bars->abort) {  // let the copies into this CTA land before it exits (bounded)
         // (a full barrier of the even CTA completes only with the odd CTA's
@@ -709,6 +858,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0) {
       const uint32_t qa = smem_u32(sQ), ka = smem_u32(sK);
+      bool ok = true;
+      if constexpr (WIN) {
+        Cur<true> c = cur_begin(bars, s);
+        Ring<kKS> kr;
+        Ring<kSB> sr;
+        Ring<kQB> qr;
+        ok = for_segments(c, s, T, [&](int te, bool) -> bool {
+          if (!warp_ready(&bars->qfull[qr.i], qr.parity)) return false;
+          const uint64_t qd = smem_desc_sw128(qa + (uint32_t)qr.i * kQBytes, 16, 1024);
+          for (; c.t < te; ++c.t) {
+            // S(g) overwrites the buffer whose P PV(g - kSB) read
+            if (sr.again && !warp_ready(&bars->ofull[sr.i], sr.parity ^ 1)) return false;
+            if (!warp_ready(&bars->kfull[kr.i], kr.parity)) return false;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint64_t kd = smem_desc_sw128(ka + (uint32_t)kr.i * kKBytes, 16, 1024);
+              const uint32_t d = tmem + (uint32_t)sr.i * 128u;
+#pragma unroll
+              for (int kk = 0; kk < kD / 16; ++kk)
+                mma_ss_pair(d, qd + (uint64_t)(((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4),
+                            kd + (uint64_t)(((kk >> 2) * kKHalf + (kk & 3) * 32) >> 4), kIdescS, kk > 0);
+              mma_commit_pair_mc(&bars->sfull[sr.i], kBoth);
+              mma_commit_pair_mc(&bars->kempty[kr.i], kBoth);
+              if (c.t == te - 1) mma_commit_pair_mc(&bars->qempty[qr.i], kBoth);
+            }
+            __syncwarp();
+            kr.next();
+            sr.next();
+          }
+          qr.next();
+          return true;
+        });
+      } else {
       Cur<WIN> cs = cur_begin(bars, s);
       int seg_s = 0;
       // S(g) = Q K(g)^T into S buffer g % kSB; called for g = 0, 1, 2, ...
@@ -737,11 +919,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         cur_next(cs, s);
         return true;
       };
-      bool ok = true;
       for (int g = 0; ok && g < T; ++g) {
         // S(g) overwrites the buffer whose P PV(g - kSB) read
         if (g >= kSB && !(ok = warp_wait(&bars->ofull[g % kSB], ((g - kSB) / kSB) & 1))) break;
         ok = issue_s(g);
+      }
       }
       if (!ok) give_up(bars, status);
       if (lane == 0) mma_commit_pair_mc(&bars->drain, kBoth);  // after every MMA issued above
@@ -749,6 +931,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
       // odd CTA: its Q and K halves have landed -> arrive on the even CTA's
       // full barriers
+      if constexpr (WIN) {
+        Cur<true> c = cur_begin(bars, s);
+        Ring<kKS> kr;
+        Ring<kQB> qr;
+        const uint32_t kfull_even = mapa_cluster(&bars->kfull[0], 0), qfull_even = mapa_cluster(&bars->qfull[0], 0);
+        const bool done = for_segments(c, s, T, [&](int te, bool) -> bool {
+          if (!warp_ready(&bars->qland[qr.i], qr.parity) || bars->abort) return false;
+          if (lane == 0) mbar_arrive_cluster(qfull_even + (uint32_t)qr.i * (uint32_t)sizeof(uint64_t));
+          qr.next();
+          for (; c.t < te; ++c.t) {
+            if (!warp_ready(&bars->kland[kr.i], kr.parity) || bars->abort) return false;
+            if (lane == 0) mbar_arrive_cluster(kfull_even + (uint32_t)kr.i * (uint32_t)sizeof(uint64_t));
+            kr.next();
+          }
+          return true;
+        });
+        if (!done) give_up(bars, status);
+      } else {
       Cur<WIN> c = cur_begin(bars, s);
       int seg = 0;
       for (int g = 0; g < T; ++g) {
@@ -770,6 +970,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_cluster(mapa_cluster(&bars->kfull[st], 0));
         cur_next(c, s);
       }
+      }
       __syncwarp();
     }
     // both CTAs: every pair MMA (and its commits into this CTA) done
@@ -779,13 +980,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ PV issuer
     if (rank == 0) {
       const uint32_t va = smem_u32(sV);
-      Cur<WIN> cp = cur_begin(bars, s);
       bool ok = true;
+      if constexpr (WIN) {
+        Cur<true> c = cur_begin(bars, s);
+        Ring<kVS> vr;
+        Ring<kSB> sr;
+        ok = for_segments(c, s, T, [&](int te, bool) -> bool {
+          uint32_t acc = 0;  // the segment's first tile starts O
+          for (; c.t < te; ++c.t) {
+            if (!warp_ready(&bars->vland[vr.i], vr.parity)) return false;
+            const int nkeys = is_special(c, s) ? special_keys(sV + vr.i * kVBytes, c, s) : kBN;
+            if (!warp_ready(&bars->pfull[sr.i], sr.parity)) return false;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint64_t vd = smem_desc_sw128(va + (uint32_t)vr.i * kVBytes, kVBytes, 1024);
+              const uint32_t pbase = tmem + (uint32_t)sr.i * 128u;
+              if (nkeys == kBN) {
+#pragma unroll
+                for (int kk = 0; kk < kBN / 16; ++kk)
+                  mma_ts_pair(tmem + kColO, pbase + (uint32_t)kk * 8u, vd + (uint64_t)((kk * 2048) >> 4), kIdescPV,
+                              kk > 0 ? 1u : acc);
+              } else {
+                const int ksteps = (nkeys + 15) >> 4;
+                for (int kk = 0; kk < ksteps; ++kk)
+                  mma_ts_pair(tmem + kColO, pbase + (uint32_t)kk * 8u, vd + (uint64_t)((kk * 2048) >> 4), kIdescPV,
+                              kk > 0 ? 1u : acc);
+              }
+              mma_commit_pair_mc(&bars->vempty[vr.i], kBoth);
+              mma_commit_pair_mc(&bars->ofull[sr.i], kBoth);
+            }
+            __syncwarp();
+            acc = 1;
+            vr.next();
+            sr.next();
+          }
+          return true;
+        });
+      } else {
+      Cur<WIN> cp = cur_begin(bars, s);
       for (int g = 0; ok && g < T; ++g) {
         // O += P(g) V(g) once P of both CTAs is ready (which also covers both
         // V halves of tile g)
         const int nkeys = tile_keys(cp, s);
-        if (!(ok = warp_wait(&bars->pfull[g % kSB], (g / kSB) & 1) && v_ready(bars, sV, g, cp, s))) break;
+        if (!(ok = warp_wait(&bars->pfull[g % kSB], (g / kSB) & 1) && v_ready(bars, sV, g, nkeys))) break;
         tc_fence_after();
         const bool first = g == 0 || cp.t == 0;
         const int st = g % kVS;
@@ -810,6 +1047,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         cur_next(cp, s);
       }
+      }
       if (!ok) give_up(bars, status);
       if (lane == 0) mma_commit_pair_mc(&bars->drain, kBoth);  // after every MMA issued above
       __syncwarp();
@@ -820,15 +1058,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // PV(g-kSB) completed, i.e. after the barrier's phase for tile g-kSB,
       // so the arrival cannot fall into that earlier phase.
       const uint32_t pfull_even0 = mapa_cluster(&bars->pfull[0], 0);  // pfull[i] at + 8 i
+      if constexpr (WIN) {
+        Cur<true> c = cur_begin(bars, s);
+        Ring<kVS> vr;
+        Ring<kSB> sr;
+        const bool done = for_segments(c, s, T, [&](int te, bool) -> bool {
+          for (; c.t < te; ++c.t) {
+            if (!warp_ready(&bars->vland[vr.i], vr.parity)) return false;
+            if (is_special(c, s)) special_keys(sV + vr.i * kVBytes, c, s);
+            if (!warp_ready(&bars->sfull[sr.i], sr.parity) || bars->abort) return false;
+            if (lane == 0) mbar_arrive_cluster(pfull_even0 + (uint32_t)sr.i * (uint32_t)sizeof(uint64_t));
+            vr.next();
+            sr.next();
+          }
+          return true;
+        });
+        if (!done) give_up(bars, status);
+      } else {
       Cur<WIN> c = cur_begin(bars, s);
       for (int g = 0; g < T; ++g) {
-        if (!warp_wait(&bars->sfull[g % kSB], (g / kSB) & 1) || !v_ready(bars, sV, g, c, s) ||
+        if (!warp_wait(&bars->sfull[g % kSB], (g / kSB) & 1) || !v_ready(bars, sV, g, tile_keys(c, s)) ||
             bars->abort) {
           give_up(bars, status);
           break;
         }
         if (lane == 0) mbar_arrive_cluster(pfull_even0 + (uint32_t)(g % kSB) * (uint32_t)sizeof(uint64_t));
         cur_next(c, s);
+      }
       }
     }
   } else {
@@ -916,15 +1172,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         next_from_b = load_from(same_b ? c.b : c.b + 1, same_b ? c.gi + 1 : 0, rb);
       }
       bool first = true;
-      // WIN: a warp of padding rows (calls of few rows have many) only keeps
-      // the barriers' pace; its P and O are never read
-      const bool idle = WIN && grow(c.gi, lb) >= R;
+      // releases the Q buffer that the previous output store has read
+      auto release_q = [&]() {
+        if (q_pending && threadIdx.x == kStoreThread) {  // (the store has long read its buffer)
+          bulk_wait_read();
+          mbar_arrive(&bars->qempty[q_pending - 1]);
+          q_pending = 0;
+        }
+      };
+      // WIN: the tiles from t_clear on lie behind the sinks and inside the
+      // window of the deepest node a tree may have: no row masks them
+      int t_clear = s.nt, key_base = -s.nt * kBN;  // (key_base + t kBN: first key of tile t >= t_clear)
+      if constexpr (WIN) {
+        const int t_win = s.nt + c.sp.n_sink;
+        t_clear = t_win + max(0, (c.P + N - s.win.window - c.sp.w0 + kBN - 1) / kBN);
+        key_base = c.sp.w0 - t_win * kBN;
+        if (grow(c.gi, lb) >= R) {
+          // a warp of padding rows (calls of few rows have many) only keeps
+          // the barriers' pace; its P and O are never read
+          for (;;) {
+            if (ok && !warp_wait(&bars->sfull[g % kSB], (g / kSB) & 1)) ok = false;
+            if (ok && lane == 0)
+              mbar_arrive_cluster(pfull_even0 + (uint32_t)(g % kSB) * (uint32_t)sizeof(uint64_t));
+            release_q();
+            if (g == T - 1 || c.t == c.n - 1) break;
+            cur_next(c, s);
+            ++g;
+          }
+          s_ready = false;
+          first = false;
+        }
+      }
+      if (!WIN || grow(c.gi, lb) < R)
       for (;;) {
         if (ok && !s_ready && !warp_wait(&bars->sfull[g % kSB], (g / kSB) & 1)) ok = false;
         const uint32_t s_addr = tmem + lane_off + (uint32_t)(g % kSB) * 128u;
         // sv[4j + e]: row ra, key 8j + 2 tq + e;  sv[4j + 2 + e]: row rb
         uint32_t sv[64];
-        if (ok && !idle) {
+        if (ok) {
           tc_fence_after();
           tmem_ld_16x256b_x16(s_addr, sv);
           tmem_wait_ld();
@@ -933,7 +1218,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 64; ++i) sv[i] = __float_as_uint(0.f);
         }
         const bool tree = c.t < s.nt;
-        const int nvalid = tile_keys(c, s);
         // The tile body comes in two instances so that full prefix tiles, the
         // steady state, carry no masking code: the masked one serves the tree
         // tiles and the last, partial prefix tile.
@@ -948,7 +1232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const int nb = m8 <= 0 ? 0 : min(32, 2 * (m8 >> 3) + min(2, m8 & 7));
               return nb >= 32 ? 0xFFFFFFFFu : ((1u << nb) - 1u);
             };
-            const uint32_t in = below(nvalid);
+            const uint32_t in = below(tile_keys(c, s));
             uint32_t va = in, vb = in;
             if constexpr (WIN) {
               if (!tree) {
@@ -1093,26 +1377,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           s_ready = __all_sync(0xffffffffu, next_done);
         };
-        // (WIN: no row masks a full tile of sinks, nor one inside the window of
-        // the deepest node a tree may have)
-        bool edge = tree || nvalid < kBN;
-        if constexpr (WIN) {
-          const int key0 = tile_key0(c, s);
-          edge = edge || (key0 + kBN > s.win.sinks && key0 - c.P < N - s.win.window);
-        }
-        if (idle) {
-          __syncwarp();
-          if (ok && lane == 0) mbar_arrive_cluster(pfull_even0 + (uint32_t)(g % kSB) * (uint32_t)sizeof(uint64_t));
-          s_ready = false;
-        } else if (__builtin_expect(edge, 0))
+        if (__builtin_expect(c.t < t_clear || c.P - key_base - c.t * kBN < kBN, 0))
           tile(std::true_type{});
         else
           tile(std::false_type{});
-        if (q_pending && threadIdx.x == kStoreThread) {  // the previous output store has long read its buffer
-          bulk_wait_read();
-          mbar_arrive(&bars->qempty[q_pending - 1]);
-          q_pending = 0;
-        }
+        release_q();
         if (g == T - 1 || c.t == c.n - 1) break;
         cur_next(c, s);
         ++g;
