@@ -500,15 +500,6 @@ __device__ __forceinline__ bool is_special(const Cur<true> &c, const Sched<true>
   return c.t <= s.nt + c.sp.n_sink || c.t == c.n - 1;
 }
 
-// V maps whose box is half a tile (64 keys x 64 dims), for tree tiles that
-// also hold sinks.
-template <bool WIN>
-struct Halves {};
-template <>
-struct Halves<true> {
-  CUtensorMap vc, vt;
-};
-
 // MAXW: ancestor-mask words per node, rounded up to 1, 2 or 4 (trees of up
 // to 64, 128 or 256 nodes; one, one or two tree tiles).
 template <int MAXW, bool WIN>
@@ -516,7 +507,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attn_tc2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kc,
                     const __grid_constant__ CUtensorMap tm_vc, const __grid_constant__ CUtensorMap tm_kt,
                     const __grid_constant__ CUtensorMap tm_vt, const __grid_constant__ CUtensorMap tm_o,
-                    const __grid_constant__ Halves<WIN> tm_half,
                     const Sched<WIN> s_in, const uint64_t *__restrict__ anc, void *__restrict__ ws, int Hq,
                     float scale_log2, int32_t *status) {
   // the tree-tile count as a compile-time constant in every schedule step
@@ -554,10 +544,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_kt);
     tma_prefetch_desc(&tm_vt);
     tma_prefetch_desc(&tm_o);
-    if constexpr (WIN) {
-      tma_prefetch_desc(&tm_half.vc);
-      tma_prefetch_desc(&tm_half.vt);
-    }
   }
   // The range lookup (warp 0) overlaps the barrier and TMEM set-up (warp 1).
   bool whole = false;
@@ -698,8 +684,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!slot()) return false;
           uint8_t *dst = ring0 + r.i * kBytes;
           uint64_t *land = &land0[r.i];
-          if (is_v) {
+          if (is_v) {  // (boxes of 64 keys, as K's: a tree tile may hold sinks behind the nodes)
             tma_load_2d(dst, m, 64 * (int)rank, row0, land);
+            tma_load_2d(dst + kBytes / 2, m, 64 * (int)rank, row0 + kFold, land);
           } else {
             tma_load_2d(dst, m, 0, row0 + 64 * (int)rank, land);
             tma_load_2d(dst + kKHalf, m, 64, row0 + 64 * (int)rank, land);
@@ -730,8 +717,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint8_t *dst = ring0 + r.i * kBytes;
             uint64_t *land = &land0[r.i];
             if (is_v) {
-              tma_load_2d(dst, &tm_half.vt, 64 * (int)rank, bh * N, land);
-              tma_load_2d(dst + kBytes / 2, &tm_half.vc, 64 * (int)rank, sink0, land);
+              tma_load_2d(dst, &tm_vt, 64 * (int)rank, bh * N, land);
+              tma_load_2d(dst + kBytes / 2, &tm_vc, 64 * (int)rank, sink0, land);
             } else {
               const CUtensorMap *m = rank == 1 ? &tm_kc : &tm_kt;
               const int row = rank == 1 ? sink0 : bh * N;
@@ -1735,27 +1722,16 @@ int tc2_run(const SvAttnShape &s, Sched<WIN> &sc, int rows_g, const void *q, con
                                           : (cuuint64_t)s.batch * s.hkv * s.s_max;
     const cuuint64_t dims[2] = {(cuuint64_t)kD, rows > 0 ? rows : 1};
     const cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
-    const cuuint32_t kbox[2] = {64, 64}, vbox[2] = {64, (cuuint32_t)kBN};
+    const cuuint32_t kbox[2] = {64, 64}, vbox[2] = {64, (cuuint32_t)(WIN ? kFold : kBN)};
     if (make_map(&mkc, kc, 2, dims, strides, kbox) != SPEC_OK) return SPEC_ERR_CUDA;
     if (make_map(&mvc, vc, 2, dims, strides, vbox) != SPEC_OK) return SPEC_ERR_CUDA;
   }
   {
     const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)s.batch * s.hkv * s.n_nodes};
     const cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
-    const cuuint32_t kbox[2] = {64, 64}, vbox[2] = {64, (cuuint32_t)kBN};
+    const cuuint32_t kbox[2] = {64, 64}, vbox[2] = {64, (cuuint32_t)(WIN ? kFold : kBN)};
     if (make_map(&mkt, kt, 2, dims, strides, kbox) != SPEC_OK) return SPEC_ERR_CUDA;
     if (make_map(&mvt, vt, 2, dims, strides, vbox) != SPEC_OK) return SPEC_ERR_CUDA;
-  }
-  Halves<WIN> half;
-  if constexpr (WIN) {
-    const cuuint64_t rows = s.block_table ? (cuuint64_t)s.num_blocks * s.hkv * s.block_size
-                                          : (cuuint64_t)s.batch * s.hkv * s.s_max;
-    const cuuint64_t dims[2] = {(cuuint64_t)kD, rows > 0 ? rows : 1};
-    const cuuint64_t tree_dims[2] = {(cuuint64_t)kD, (cuuint64_t)s.batch * s.hkv * s.n_nodes};
-    const cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)kFold};
-    if (make_map(&half.vc, vc, 2, dims, strides, box) != SPEC_OK) return SPEC_ERR_CUDA;
-    if (make_map(&half.vt, vt, 2, tree_dims, strides, box) != SPEC_OK) return SPEC_ERR_CUDA;
   }
   sc.prefix_len = prefix_len;
   sc.batch = s.batch;
@@ -1774,7 +1750,7 @@ int tc2_run(const SvAttnShape &s, Sched<WIN> &sc, int rows_g, const void *q, con
               : sc.mw == 2 ? attn_tc2_kernel<2, WIN>
                            : attn_tc2_kernel<4, WIN>;
   if (!tc2_set_smem(kern, sc.mw == 1 ? 0 : sc.mw == 2 ? 1 : 2, WIN)) return SPEC_ERR_CUDA;
-  kern<<<2 * C, kThreads, kSmemBytes, stream>>>(mq, mkc, mvc, mkt, mvt, mo, half, sc, anc, ws, s.hq,
+  kern<<<2 * C, kThreads, kSmemBytes, stream>>>(mq, mkc, mvc, mkt, mvt, mo, sc, anc, ws, s.hq,
                                                scale * 1.4426950408889634f, status);
   if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
   bool merge = C > 1;
