@@ -1117,17 +1117,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return m;
     };
     Mask amask_a{}, amask_b{}, next_a{}, next_b{};
-    // WIN: first prefix key inside a row's window, less the prefix length
-    // (depth - window + 1; rows of nodes at most as deep as the tree), the
-    // next segment's loaded with its masks
-    auto load_from = [&](int b, int gi, int lane_row) -> int {
+    // WIN: the depths of the rows' nodes, the next segment's loaded with its
+    // masks (and not touched before they are needed)
+    auto load_depth = [&](int b, int gi, int lane_row) -> int {
       if constexpr (WIN) {
         const int rr = grow(gi, lane_row);
-        return (rr < R ? sv::win_depth(s.win, (int64_t)b * N + rr / G, N) : 0) - s.win.window + 1;
+        if (rr < R) return __ldg(s.win.depth + (int64_t)b * N + rr / G);
       }
       return 0;
     };
-    int from_a = load_from(c.b, c.gi, ra), from_b = load_from(c.b, c.gi, rb), next_from_a = 0, next_from_b = 0;
+    int depth_a = load_depth(c.b, c.gi, ra), depth_b = load_depth(c.b, c.gi, rb), next_depth_a = 0, next_depth_b = 0;
     if (c.t < NT) {
       amask_a = load_mask(c.b, c.gi, ra, c.t);
       amask_b = load_mask(c.b, c.gi, rb, c.t);
@@ -1146,8 +1145,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         from_start = true;
         amask_a = next_a;
         amask_b = next_b;
-        from_a = next_from_a;
-        from_b = next_from_b;
+        depth_a = next_depth_a;
+        depth_b = next_depth_b;
       }
       ma = mb = M0;
       la = lb_sum = 0.f;
@@ -1155,8 +1154,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool same_b = c.gi + 1 < s.gpb();
         next_a = load_mask(same_b ? c.b : c.b + 1, same_b ? c.gi + 1 : 0, ra, 0);
         next_b = load_mask(same_b ? c.b : c.b + 1, same_b ? c.gi + 1 : 0, rb, 0);
-        next_from_a = load_from(same_b ? c.b : c.b + 1, same_b ? c.gi + 1 : 0, ra);
-        next_from_b = load_from(same_b ? c.b : c.b + 1, same_b ? c.gi + 1 : 0, rb);
+        next_depth_a = load_depth(same_b ? c.b : c.b + 1, same_b ? c.gi + 1 : 0, ra);
+        next_depth_b = load_depth(same_b ? c.b : c.b + 1, same_b ? c.gi + 1 : 0, rb);
       }
       bool first = true;
       // releases the Q buffer that the previous output store has read
@@ -1225,8 +1224,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (!tree) {
                 const int key0 = tile_key0(c, s);
                 const uint32_t sink = below(s.win.sinks - key0);
-                va &= sink | ~below(c.P - key0 + from_a);
-                vb &= sink | ~below(c.P - key0 + from_b);
+                // the first key inside a row's window: P + depth - window + 1
+                const int from = c.P - key0 - s.win.window + 1;
+                va &= sink | ~below(from + min(max(depth_a, 0), N - 1));
+                vb &= sink | ~below(from + min(max(depth_b, 0), N - 1));
               }
             }
             if (tree) {
