@@ -1173,23 +1173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int t_win = s.nt + c.sp.n_sink;
         t_clear = t_win + max(0, (c.P + N - s.win.window - c.sp.w0 + kBN - 1) / kBN);
         key_base = c.sp.w0 - t_win * kBN;
-        if (grow(c.gi, lb) >= R) {
-          // a warp of padding rows (calls of few rows have many) only keeps
-          // the barriers' pace; its P and O are never read
-          for (;;) {
-            if (ok && !warp_wait(&bars->sfull[g % kSB], (g / kSB) & 1)) ok = false;
-            if (ok && lane == 0)
-              mbar_arrive_cluster(pfull_even0 + (uint32_t)(g % kSB) * (uint32_t)sizeof(uint64_t));
-            release_q();
-            if (g == T - 1 || c.t == c.n - 1) break;
-            cur_next(c, s);
-            ++g;
-          }
-          s_ready = false;
-          first = false;
-        }
       }
-      if (!WIN || grow(c.gi, lb) < R)
       for (;;) {
         if (ok && !s_ready && !warp_wait(&bars->sfull[g % kSB], (g / kSB) & 1)) ok = false;
         const uint32_t s_addr = tmem + lane_off + (uint32_t)(g % kSB) * 128u;

@@ -137,8 +137,9 @@ __device__ __forceinline__ int kv_row(const KvPages &pg, int b, int hkv, int h, 
 // or P + d - x < window.  The prefix keys that some node sees are then the
 // sinks [0, s_end) and the window [w0, P) of the root (deeper nodes see a
 // later part of it): both are cut into tiles, sinks first, and nothing in
-// between is read.  `align`: a window tile starts at a multiple of it (1, or
-// the tile size when a tile must not leave a cache block).
+// between is read.  `align`: a window tile starts at a multiple of it (the
+// tile size when a tile must not leave a cache block; 1: the tiles end at P,
+// so that only the first is cut).
 struct Window {
   const int32_t *depth;  // [batch, n_nodes]
   int window, sinks;     // window >= 1, sinks >= 0
@@ -153,7 +154,9 @@ struct WinSpan {
 __device__ __forceinline__ WinSpan win_span(int window, int sinks, int P, int tile, int align) {
   WinSpan v;
   v.lo = max(0, P - window + 1);
-  v.w0 = v.lo >= P ? P : v.lo / align * align;
+  v.w0 = v.lo >= P    ? P
+         : align == 1 ? max(0, P - (P - v.lo + tile - 1) / tile * tile)
+                      : v.lo / align * align;
   v.s_end = min(sinks, v.w0);
   v.n_sink = (v.s_end + tile - 1) / tile;
   v.n_tiles = v.n_sink + (P - v.w0 + tile - 1) / tile;
