@@ -1640,17 +1640,26 @@ int tc2_clusters() {
 }
 
 // Whether a window call keeps its row groups whole.  In tiles of 128 keys
-// (about 0.9 us each): cut in equal ranges, the clusters take the average and
-// then the merge; kept whole, the busiest takes its number of row groups,
-// each at the longest a prefix may be, and no merge is launched.
-constexpr int kMergeTiles = 6;
+// (about 0.85 us each), a row group weighing its tiles and kSegW: cut in equal
+// ranges (of a tree tile's weight at least), a cluster takes the average, and
+// the range lookup, the partials and the merge cost kMergeTiles more; kept
+// whole, the busiest cluster takes its number of row groups, each at the
+// longest a prefix may be.  Measured cut / whole, 4 heads per KV head, 32
+// nodes, paged, by row groups and window: 8, 1024: 16.3 / 15.6 us; 8, 2048:
+// 17.2 / 21.7; 32, 2048: 27.0 / 22.1; 80, 1024: 28.7 / 27.5; 80, 2048: 35.4 /
+// 39.5; 128, 2048: 49.7 / 43.5; 128, 4096: 70.9 / 68.9; 240, 2048: 75.1 /
+// 77.6.  The rule takes the faster side of each.
+constexpr int kMergeTiles = 13;
 bool tc2_whole(const SvAttnShape &s, const Sched<true> &sc, int clusters) {
   const long long span = (long long)sc.win.window - 1 + (s.block_table ? kBN - 1 : 0);
   const long long keys = span < s.max_prefix ? span : s.max_prefix;
-  const long long sinks = s.n_nodes <= kFold && sc.win.sinks <= kFold ? 0 : sc.win.sinks < s.max_prefix ? sc.win.sinks : s.max_prefix;
-  const long long n = (s.n_nodes + kBN - 1) / kBN + (keys + kBN - 1) / kBN + (sinks + kBN - 1) / kBN + kSegW;
+  const long long most_sinks = sc.win.sinks < s.max_prefix ? sc.win.sinks : s.max_prefix;
+  const long long sinks = s.n_nodes <= kFold && sc.win.sinks <= kFold ? 0 : most_sinks;
+  const int nt = (s.n_nodes + kBN - 1) / kBN;
+  const long long n = nt + kSegW + (keys + kBN - 1) / kBN + (sinks + kBN - 1) / kBN;
   const long long rgs = (long long)s.batch * s.hkv * ((s.n_nodes * sc.gp + kPairRows - 1) / kPairRows);
-  return (rgs + clusters - 1) / clusters * n <= rgs * n / clusters + kMergeTiles;
+  const long long mean = rgs * n / clusters > nt + kSegW ? rgs * n / clusters : nt + kSegW;
+  return (rgs + clusters - 1) / clusters * n <= mean + kMergeTiles;
 }
 
 // Sets an instance's shared-memory size, once per device.
