@@ -120,40 +120,42 @@ def _p(t):
     return C.c_void_p(t.data_ptr())
 
 
-class _Args:
-    """Device pointers of one call's tensors, each checked: on the call's
-    device (which has to be the current one, whose stream the call goes to),
-    contiguous, and of the dtype and shape (or element count) the C entry
-    point will take it for."""
+def _args(device):
+    """(ptr, index, stream) of one call: its device, which has to be the
+    current one, that device's current stream, and ptr(t, dtype, shape), the
+    device pointer of a tensor once it is checked: on that device,
+    contiguous, and of the dtype and shape the C entry point takes it for.
+    (A closure: a method call would cost twice as much, a dozen times.)"""
+    index = torch.cuda.current_device()
+    if device.type != "cuda" or device.index != index:
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{index}")
 
-    __slots__ = ("index",)
-
-    def __init__(self, device):
-        self.index = torch.cuda.current_device()
-        if device.type != "cuda" or device.index != self.index:
-            raise ValueError(f"tensors on {device}, but the current device is cuda:{self.index}")
-
-    def __call__(self, t, dtype, shape):
-        if t.dtype is dtype and t.shape == shape and t.get_device() == self.index and t.is_contiguous():
+    def ptr(t, dtype, shape):
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
             return t.data_ptr()
-        raise self.error(t, dtype, shape)
+        raise _refusal(t, index, dtype, shape)
 
-    def sized(self, t, dtype, numel):
-        """A tensor of any shape of numel elements (None: any number)."""
-        if t.get_device() == self.index and t.is_contiguous() and t.dtype is dtype and numel in (None, t.numel()):
-            return t.data_ptr()
-        raise self.error(t, dtype, (numel,))
+    return ptr, index, torch._C._cuda_getCurrentRawStream(index)
 
-    def status(self, t):
-        """The optional device status word."""
-        return None if t is None else self.sized(t, torch.int32, None)
 
-    def error(self, t, dtype, shape):
-        if t.get_device() != self.index:
-            return ValueError(f"expected a tensor on cuda:{self.index}, not {t.device}")
-        if t.dtype is not dtype:
-            return TypeError(f"dtype {t.dtype}, expected {dtype}")
-        return ValueError(f"expected a contiguous tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
+def _sized(t, index, dtype, numel=None):
+    """As ptr, for a tensor of any shape (of numel elements, if given)."""
+    if t.get_device() == index and t.is_contiguous() and t.dtype is dtype and numel in (None, t.numel()):
+        return t.data_ptr()
+    raise _refusal(t, index, dtype, (numel,))
+
+
+def _word(t, index):
+    """The optional device status word."""
+    return None if t is None else _sized(t, index, torch.int32)
+
+
+def _refusal(t, index, dtype, shape):
+    if t.get_device() != index:
+        return ValueError(f"expected a tensor on cuda:{index}, not {t.device}")
+    if t.dtype is not dtype:
+        return TypeError(f"dtype {t.dtype}, expected {dtype}")
+    return ValueError(f"expected a contiguous tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _want(t, *dtypes):
@@ -373,15 +375,14 @@ def tree_attn_verify_window(q, k_cache, v_cache, k_tree, v_tree, prefix_len, dep
     code = _DT.get(q.dtype, -1)
     if workspace is None:
         workspace = _scratch(tree_attn_window_workspace_bytes(code, B, N, Hq, Hkv, D, max_prefix, window, sinks), q)
-    ptr = _Args(q.device)
-    kv, tree = (B, Hkv, S, D), (B, Hkv, N, D)
-    args = (ptr(q, q.dtype, (B, N, Hq, D)), ptr(k_cache, q.dtype, kv), ptr(v_cache, q.dtype, kv),
-            ptr(k_tree, q.dtype, tree), ptr(v_tree, q.dtype, tree), ptr(prefix_len, torch.int32, (B,)),
-            ptr(depth, torch.int32, (B, N)), ptr.sized(anc_mask, torch.int64, B * N * mask_words(N)),
-            ptr(out, q.dtype, (B, N, Hq, D)))
+    ptr, index, stream = _args(q.device)
+    dt, i32, kv, tree = q.dtype, torch.int32, (B, Hkv, S, D), (B, Hkv, N, D)
+    args = (ptr(q, dt, q.shape), ptr(k_cache, dt, kv), ptr(v_cache, dt, kv), ptr(k_tree, dt, tree),
+            ptr(v_tree, dt, tree), ptr(prefix_len, i32, (B,)), ptr(depth, i32, (B, N)),
+            _sized(anc_mask, index, torch.int64, B * N * mask_words(N)), ptr(out, dt, q.shape))
     _check("tree_attn_verify_window", load().tree_attn_verify_window(
         *args, code, B, N, Hq, Hkv, D, S, int(max_prefix), int(window), int(sinks), float(scale),
-        ptr.sized(workspace, torch.uint8, None), workspace.numel(), ptr.status(dev_status), _stream()))
+        _sized(workspace, index, torch.uint8), workspace.numel(), _word(dev_status, index), stream))
 
 
 def tree_attn_verify_window_paged(q, k_pages, v_pages, block_table, k_tree, v_tree, prefix_len, depth, anc_mask, out,
@@ -394,15 +395,14 @@ def tree_attn_verify_window_paged(q, k_pages, v_pages, block_table, k_tree, v_tr
     code = _DT.get(q.dtype, -1)
     if workspace is None:
         workspace = _scratch(tree_attn_window_workspace_bytes(code, B, N, Hq, Hkv, D, max_prefix, window, sinks), q)
-    ptr = _Args(q.device)
-    kv, tree = (nb, Hkv, bs, D), (B, Hkv, N, D)
-    args = (ptr(q, q.dtype, (B, N, Hq, D)), ptr(k_pages, q.dtype, kv), ptr(v_pages, q.dtype, kv),
-            ptr(block_table, torch.int32, (B, mb)), bs, nb, mb, ptr(k_tree, q.dtype, tree), ptr(v_tree, q.dtype, tree),
-            ptr(prefix_len, torch.int32, (B,)), ptr(depth, torch.int32, (B, N)),
-            ptr.sized(anc_mask, torch.int64, B * N * mask_words(N)), ptr(out, q.dtype, (B, N, Hq, D)))
+    ptr, index, stream = _args(q.device)
+    dt, i32, kv, tree = q.dtype, torch.int32, (nb, Hkv, bs, D), (B, Hkv, N, D)
+    args = (ptr(q, dt, q.shape), ptr(k_pages, dt, kv), ptr(v_pages, dt, kv), ptr(block_table, i32, (B, mb)), bs, nb, mb,
+            ptr(k_tree, dt, tree), ptr(v_tree, dt, tree), ptr(prefix_len, i32, (B,)), ptr(depth, i32, (B, N)),
+            _sized(anc_mask, index, torch.int64, B * N * mask_words(N)), ptr(out, dt, q.shape))
     _check("tree_attn_verify_window_paged", load().tree_attn_verify_window_paged(
         *args, code, B, N, Hq, Hkv, D, int(max_prefix), int(window), int(sinks), float(scale),
-        ptr.sized(workspace, torch.uint8, None), workspace.numel(), ptr.status(dev_status), _stream()))
+        _sized(workspace, index, torch.uint8), workspace.numel(), _word(dev_status, index), stream))
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -528,13 +528,13 @@ def spec_verify_probs(target_probs, tok, parents, first_child, next_sibling, u_a
     where siblings are draws of the drafter.  Outputs as spec_accept."""
     B, N, V = target_probs.shape
     dt, i32, f32 = target_probs.dtype, torch.int32, torch.float32
-    ptr = _Args(target_probs.device)
+    ptr, index, stream = _args(target_probs.device)
     node, cap = (B, N), acc_path.shape[1]
     _check("spec_verify_probs", load().spec_verify_probs(
         ptr(target_probs, dt, (B, N, V)), None if draft_probs is None else ptr(draft_probs, dt, (B, N, V)),
         _DT.get(dt, -1), B, N, V, ptr(tok, i32, node), ptr(parents, i32, node), ptr(first_child, i32, node),
         ptr(next_sibling, i32, node), ptr(u_accept, f32, node), ptr(u_bonus, f32, (B,)), cap,
-        ptr(acc_len, i32, (B,)), ptr(acc_path, i32, (B, cap)), ptr(bonus, i32, (B,)), ptr.status(dev_status), _stream()))
+        ptr(acc_len, i32, (B,)), ptr(acc_path, i32, (B, cap)), ptr(bonus, i32, (B,)), _word(dev_status, index), stream))
 
 
 def kv_pages_workspace_bytes(batch, max_blocks, num_blocks):
@@ -545,11 +545,11 @@ def kv_pages_fork(block_table, prefix_len, parent, ref_count, table_out, prefix_
     """Sequence i of the new batch continues sequence parent[i] (< 0: empty)."""
     B, mb = block_table.shape
     out, nb, i32 = parent.shape[0], ref_count.shape[0], torch.int32
-    ptr = _Args(block_table.device)
+    ptr, index, stream = _args(block_table.device)
     _check("kv_pages_fork", load().kv_pages_fork(
         ptr(block_table, i32, (B, mb)), ptr(prefix_len, i32, (B,)), ptr(parent, i32, (out,)), B, out, mb, nb,
         ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (out, mb)), ptr(prefix_len_out, i32, (out,)),
-        ptr(ref_out, i32, (nb,)), ptr.status(dev_status), _stream()))
+        ptr(ref_out, i32, (nb,)), _word(dev_status, index), stream))
 
 
 def kv_pages_free(block_table, prefix_len, ref_count, table_out, ref_out, block_size, window=0, sinks=0, spare=0,
@@ -557,11 +557,11 @@ def kv_pages_free(block_table, prefix_len, ref_count, table_out, ref_out, block_
     """Drops the entries whose pages no later step needs (window 0: none has left)."""
     B, mb = block_table.shape
     nb, i32 = ref_count.shape[0], torch.int32
-    ptr = _Args(block_table.device)
+    ptr, index, stream = _args(block_table.device)
     _check("kv_pages_free", load().kv_pages_free(
         ptr(block_table, i32, (B, mb)), ptr(prefix_len, i32, (B,)), B, mb, int(block_size), nb, int(window), int(sinks),
         int(spare), ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)), ptr(ref_out, i32, (nb,)),
-        ptr.status(dev_status), _stream()))
+        _word(dev_status, index), stream))
 
 
 def _pool(ptr, k_pages, v_pages):
@@ -579,7 +579,7 @@ def kv_pages_reserve(k_pages, v_pages, block_table, prefix_len, need, ref_count,
     is allocated per call when not given."""
     B, mb = block_table.shape
     i32 = torch.int32
-    ptr = _Args(block_table.device)
+    ptr, index, stream = _args(block_table.device)
     pool = _pool(ptr, k_pages, v_pages)
     nb = pool[-1]
     if workspace is None:
@@ -587,7 +587,7 @@ def kv_pages_reserve(k_pages, v_pages, block_table, prefix_len, need, ref_count,
     _check("kv_pages_reserve", load().kv_pages_reserve(
         *pool, ptr(block_table, i32, (B, mb)), B, mb, ptr(prefix_len, i32, (B,)), ptr(need, i32, (B,)),
         ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)), ptr(ref_out, i32, (nb,)),
-        ptr.sized(workspace, torch.uint8, None), workspace.numel(), ptr.status(dev_status), _stream()))
+        _sized(workspace, index, torch.uint8), workspace.numel(), _word(dev_status, index), stream))
 
 
 def kv_pages_compact(k_pages, v_pages, block_table, ref_count, table_out, ref_out, n_used, remap=None, workspace=None,
@@ -596,7 +596,7 @@ def kv_pages_compact(k_pages, v_pages, block_table, ref_count, table_out, ref_ou
     remap [num_blocks] int32 (optional) are outputs."""
     B, mb = block_table.shape
     i32 = torch.int32
-    ptr = _Args(block_table.device)
+    ptr, index, stream = _args(block_table.device)
     pool = _pool(ptr, k_pages, v_pages)
     nb = pool[-1]
     if workspace is None:
@@ -604,4 +604,4 @@ def kv_pages_compact(k_pages, v_pages, block_table, ref_count, table_out, ref_ou
     _check("kv_pages_compact", load().kv_pages_compact(
         *pool, ptr(block_table, i32, (B, mb)), B, mb, ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)),
         ptr(ref_out, i32, (nb,)), ptr(n_used, i32, (1,)), None if remap is None else ptr(remap, i32, (nb,)),
-        ptr.sized(workspace, torch.uint8, None), workspace.numel(), ptr.status(dev_status), _stream()))
+        _sized(workspace, index, torch.uint8), workspace.numel(), _word(dev_status, index), stream))
