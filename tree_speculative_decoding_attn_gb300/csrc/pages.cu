@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kMaxBatch = 4096;   // rows of a table (a shared-memory word each)
-constexpr int kRange = 4096;      // blocks whose counts one CTA owns
+constexpr int kRange = 1024;      // blocks whose counts one CTA owns
 
 __device__ __forceinline__ int ld_relaxed(const int32_t *p) {
   int v;
@@ -67,31 +67,35 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     __syncthreads();
-    // the new tables' rows, shared out over the CTAs
-    for (int i = blockIdx.x; i < batch_out; i += gridDim.x) {
+    // the new tables' entries and lengths, shared out over the CTAs
+    const uint32_t fresh = (uint32_t)batch_out * max_blocks, step = gridDim.x * kThreads;
+#pragma unroll 4
+    for (uint32_t e = blockIdx.x * kThreads + threadIdx.x; e < fresh; e += step) {
+      const uint32_t i = e / max_blocks;
       const int p = parent[i];
-      const bool live = p >= 0 && p < batch;
-      for (int j = threadIdx.x; j < max_blocks; j += kThreads) {
-        int blk = live ? table[(int64_t)p * max_blocks + j] : -1;
-        if (blk < 0 || blk >= num_blocks) blk = -1;
-        table_out[(int64_t)i * max_blocks + j] = blk;
-      }
-      if (threadIdx.x == 0) prefix_out[i] = live ? prefix_len[p] : 0;
+      int blk = p >= 0 && p < batch ? table[(uint32_t)p * max_blocks + (e - i * max_blocks)] : -1;
+      if (blk < 0 || blk >= num_blocks) blk = -1;
+      table_out[e] = blk;
+    }
+    for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < (uint32_t)batch_out; i += step) {
+      const int p = parent[i];
+      prefix_out[i] = p >= 0 && p < batch ? prefix_len[p] : 0;
     }
   }
-  const int64_t total = (int64_t)batch * max_blocks;
-  for (int64_t e = threadIdx.x; e < total; e += kThreads) {
+  const uint32_t total = (uint32_t)batch * max_blocks;
+#pragma unroll 4
+  for (uint32_t e = threadIdx.x; e < total; e += kThreads) {
     const int blk = FORK ? table[e] : ld_relaxed(table + e);
-    const int b = (int)(e / max_blocks);
+    const uint32_t b = e / max_blocks;
     const bool mine = blk >= lo && blk < lo + n;
     if (blk >= num_blocks) sv::report(status, SPEC_DEV_BAD_BLOCK);
     if constexpr (FORK) {
       const int d = s_mult[b] - 1;
       if (mine && d) atomicAdd(&s_delta[blk - lo], d);
     } else {
-      const int j = (int)(e - (int64_t)b * max_blocks);
       if (mine) {
-        const bool stays = page_stays((long long)j * block_size, block_size, prefix_len[b], window, sinks, spare);
+        const bool stays =
+            page_stays((long long)(e - b * max_blocks) * block_size, block_size, prefix_len[b], window, sinks, spare);
         if (!stays) atomicSub(&s_delta[blk - lo], 1);
         table_out[e] = stays ? blk : -1;
       } else if (blockIdx.x == 0 && (blk < 0 || blk >= num_blocks)) {
@@ -139,30 +143,31 @@ __host__ __device__ inline size_t space_layout(Space *s, void *base, long long b
 }
 
 // Exclusive prefix sum of v over the CTA's threads and the CTA's total.
-__device__ int cta_scan(int v, int *total) {
-  __shared__ int s_warp[kThreads / 32];
+template <typename V>
+__device__ V cta_scan(V v, V *total) {
+  __shared__ V s_warp[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  V x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const V y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int w = s_warp[lane];
+    V w = s_warp[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      const V y = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += y;
     }
     s_warp[lane] = w;
   }
   __syncthreads();
   *total = s_warp[kThreads / 32 - 1];
-  return x - v + (warp ? s_warp[warp - 1] : 0);
+  return x - v + (warp ? s_warp[warp - 1] : V(0));
 }
 
 // The entries a call writes: the pages holding rows P .. P + need - 1 of each
@@ -192,108 +197,112 @@ __global__ void __launch_bounds__(kThreads)
   const int tid = threadIdx.x;
   if (tid == 0) s_moves = 0;
 
-  // 1. how many entries each sequence writes
-  int n = 0;
-  for (int b0 = 0; b0 < batch; b0 += kThreads) {
-    const int b = b0 + tid;
-    int k = 0;
-    if (b < batch && need[b] > 0) {
-      const long long P = prefix_len[b], end = P + need[b];
-      if (P < 0 || end > (long long)max_blocks * block_size)
-        sv::report(status, SPEC_DEV_CAPACITY);
-      else
-        k = (int)((end - 1) / block_size - P / block_size) + 1;
+  // 1. how many entries each sequence writes, and how many blocks are free
+  // (each thread looks at one contiguous piece of either): one scan for both
+  const int sper = (batch + kThreads - 1) / kThreads, per = (num_blocks + kThreads - 1) / kThreads;
+  const int b0 = min(batch, tid * sper), b1 = min(batch, b0 + sper);
+  const int lo = min(num_blocks, tid * per), hi = min(num_blocks, lo + per);
+  auto writes_of = [&](int b, bool tell) -> int {
+    const int nd = need[b];
+    if (nd <= 0) return 0;
+    const long long P = prefix_len[b], end = P + nd;
+    if (P < 0 || end > (long long)max_blocks * block_size) {
+      if (tell) sv::report(status, SPEC_DEV_CAPACITY);
+      return 0;
     }
-    int total;
-    const int at = cta_scan(k, &total);
-    if (b < batch) s_off[b] = n + at;
-    n += total;
+    return (int)((uint32_t)(end - 1) / (uint32_t)block_size - (uint32_t)P / (uint32_t)block_size) + 1;
+  };
+  unsigned long long v = 0, sums;
+  for (int i = lo; i < hi; ++i) v += ref[i] <= 0;
+  for (int b = b0; b < b1; ++b) v += (unsigned long long)writes_of(b, true) << 32;
+  const unsigned long long before = cta_scan(v, &sums);
+  const int n = (int)(sums >> 32), all_free = (int)(uint32_t)sums;
+  int at = (int)(before >> 32);
+  for (int b = b0; b < b1; ++b) {
+    s_off[b] = at;
+    at += writes_of(b, false);
   }
   if (tid == 0) s_off[batch] = n;
-  __syncthreads();
-  const Writes wr{s_off, batch};
-  auto entry = [&](int i, int *b, int *j) -> int64_t {
-    *b = wr.seq_of(i);
-    *j = prefix_len[*b] / block_size + (i - s_off[*b]);
-    return (int64_t)*b * max_blocks + *j;
-  };
-
-  // 2. the writers of each shared block: how many, and which is the last
-  for (int i = tid; i < n; i += kThreads) {
-    int b, j;
-    const int blk = table[entry(i, &b, &j)];
-    if (blk >= num_blocks) sv::report(status, SPEC_DEV_BAD_BLOCK);
-    if (blk >= 0 && blk < num_blocks && ref[blk] > 1) {
-      ws.a[blk] = 0;
-      ws.b[blk] = -1;
-    }
+  // the lowest free blocks in order, as many as could be wanted; and the
+  // tables and counts as they were, where they are not changed in place
+  at = (int)(uint32_t)before;
+  for (int i = lo; i < hi; ++i) {
+    const int r = ref[i];
+    if (r <= 0 && at < n) ws.c[at++] = i;
+    ws.a[i] = 0;
+    ws.b[i] = -1;
+    if (ref_out != ref) ref_out[i] = r;
   }
-  __syncthreads();
-  for (int i = tid; i < n; i += kThreads) {
-    int b, j;
-    const int blk = table[entry(i, &b, &j)];
-    if (blk >= 0 && blk < num_blocks && ref[blk] > 1) {
-      atomicAdd(&ws.a[blk], 1);
-      atomicMax(&ws.b[blk], i);
-    }
-  }
-  __syncthreads();
-  // 3. what becomes of each entry.  Taken in order, a writer copies a block
-  // that others still hold: all of them if some other holder does not write,
-  // else all but the last.
-  int mine = 0;
-  for (int i = tid; i < n; i += kThreads) {
-    int b, j;
-    const int blk = table[entry(i, &b, &j)];
-    int f = kFresh;
-    if (blk >= 0 && blk < num_blocks) {
-      const int r = ref[blk];
-      f = r > 1 && !(__ldcg(&ws.a[blk]) >= r && __ldcg(&ws.b[blk]) == i) ? kCopy : kKeep;
-    }
-    ws.flag[i] = f;
-    mine += f != kKeep;
-  }
-  int wanted;
-  cta_scan(mine, &wanted);
-  // 4. the lowest free blocks, in order, as many as are wanted (each thread
-  // looks at one contiguous piece of the counts)
-  const int per = (num_blocks + kThreads - 1) / kThreads;
-  const int lo = min(num_blocks, tid * per), hi = min(num_blocks, lo + per);
-  int nfree = 0;
-  for (int i = lo; i < hi; ++i) nfree += ref[i] <= 0;
-  int all_free;
-  int at = cta_scan(nfree, &all_free);
-  const bool fits = wanted <= all_free;
-  if (!fits && tid == 0) sv::report(status, SPEC_DEV_CAPACITY);
-  for (int i = lo; i < hi && at < wanted; ++i)
-    if (ref[i] <= 0) ws.c[at++] = i;
-  // 5. tables and counts as they were, where they are not changed in place
   if (table_out != table)
     for (int64_t e = tid; e < (int64_t)batch * max_blocks; e += kThreads) table_out[e] = table[e];
-  if (ref_out != ref)
-    for (int i = tid; i < num_blocks; i += kThreads) ref_out[i] = ref[i];
   __syncthreads();
-  // 6. hand the blocks out in entry order
+  const Writes wr{s_off, batch};
+  struct Entry {
+    int b, j, blk, r;  // sequence, page, its block (-1: none) and that block's count
+    int64_t e;
+  };
+  auto entry = [&](int i) -> Entry {
+    Entry x;
+    x.b = wr.seq_of(i);
+    x.j = prefix_len[x.b] / block_size + (i - s_off[x.b]);
+    x.e = (int64_t)x.b * max_blocks + x.j;
+    x.blk = table[x.e];
+    if (x.blk >= num_blocks) sv::report(status, SPEC_DEV_BAD_BLOCK);
+    if (x.blk < 0 || x.blk >= num_blocks) x.blk = -1;
+    x.r = x.blk < 0 ? 0 : ref[x.blk];
+    return x;
+  };
+  // 2. the writers of each shared block: how many, and which is the last
+  // (a thread's first entry stays in its registers through all steps)
+  const Entry mine = tid < n ? entry(tid) : Entry{0, 0, -1, 0, 0};
+  for (int i = tid; i < n; i += kThreads) {
+    const Entry x = i == tid ? mine : entry(i);
+    if (x.r > 1) {
+      atomicAdd(&ws.a[x.blk], 1);
+      atomicMax(&ws.b[x.blk], i);
+    }
+  }
+  __syncthreads();
+  // 3. what becomes of each entry, and its number among those that get a
+  // block.  Taken in order, a writer copies a block that others still hold:
+  // all of them if some other holder does not write, else all but the last.
+  int wanted = 0, my_flag = kKeep, my_rank = 0;
+  for (int i0 = 0; i0 < n; i0 += kThreads) {
+    const int i = i0 + tid;
+    int f = kKeep;
+    if (i < n) {
+      const Entry x = i0 == 0 ? mine : entry(i);
+      if (x.blk < 0)
+        f = kFresh;
+      else if (x.r > 1 && !(__ldcg(&ws.a[x.blk]) >= x.r && __ldcg(&ws.b[x.blk]) == i))
+        f = kCopy;
+    }
+    int sum;
+    const int rank = wanted + cta_scan((int)(f != kKeep), &sum);
+    wanted += sum;
+    if (i0 == 0) {
+      my_flag = f;
+      my_rank = rank;
+    } else if (i < n) {
+      ws.flag[i] = rank << 2 | f;
+    }
+  }
+  const bool fits = wanted <= all_free;
+  if (!fits && tid == 0) sv::report(status, SPEC_DEV_CAPACITY);
+  // 4. hand the blocks out in entry order
   if (fits) {
-    int base = 0;
-    for (int i0 = 0; i0 < n; i0 += kThreads) {
-      const int i = i0 + tid;
-      const int f = i < n ? ws.flag[i] : kKeep;
-      int total;
-      const int k = base + cta_scan(f != kKeep, &total);
-      base += total;
+    for (int i = tid; i < n; i += kThreads) {
+      const int f = i == tid ? my_flag : ws.flag[i] & 3, rank = i == tid ? my_rank : ws.flag[i] >> 2;
       if (f == kKeep) continue;
-      int b, j;
-      const int64_t e = entry(i, &b, &j);
-      const int blk = ws.c[k];
-      const int old = table[e];
-      table_out[e] = blk;
+      const Entry x = i == tid ? mine : entry(i);
+      const int blk = ws.c[rank];
+      table_out[x.e] = blk;
       ref_out[blk] = 1;
       if (f == kCopy) {
-        atomicSub(&ref_out[old], 1);
-        const int rows = prefix_len[b] % block_size;
-        if (j == prefix_len[b] / block_size && rows > 0)  // rows in use before the first new one
-          ws.moves[atomicAdd(&s_moves, 1)] = Move{old, blk, rows, 0};
+        atomicSub(&ref_out[x.blk], 1);
+        const int P = prefix_len[x.b], rows = P % block_size;
+        if (x.j == P / block_size && rows > 0)  // rows in use before the first new one
+          ws.moves[atomicAdd(&s_moves, 1)] = Move{x.blk, blk, rows, 0};
       }
     }
   }
