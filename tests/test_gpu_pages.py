@@ -33,7 +33,7 @@ def filled(g, B, mb, nb, bs, share=0.3):
     return table, prefix, counts(table, nb)
 
 
-SHAPES = [(1, 1, 1, 1), (5, 7, 40, 16), (64, 33, 1500, 128), (300, 5, 9001, 4), (4096, 2, 5000, 2)]
+SHAPES = [(1, 1, 1, 1), (5, 7, 40, 16), (64, 33, 1500, 128), (300, 5, 9001, 4), (4096, 2, 5000, 2), (2000, 9, 30011, 3)]
 
 
 @pytest.mark.parametrize("B,mb,nb,bs", SHAPES)
@@ -68,6 +68,41 @@ def test_free_matches_the_oracle(B, mb, nb, bs, window, sinks, spare):
         assert int(st.item()) == 0
         for x, y in zip(o, want):
             np.testing.assert_array_equal(host(x), y)
+
+
+@pytest.mark.parametrize("nb", [1024, 1025, 8192, 8193, 70001])
+@pytest.mark.parametrize("fill", [0.0, 0.5, 0.999, 1.0])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plans_over_pools_of_every_size(nb, fill, in_place):
+    """Pools around the sizes at which a plan takes another scan or another
+    CTA, from empty to full, with the free blocks bunched at either end."""
+    g = np.random.default_rng(nb)
+    mb, bs = 8, 4
+    ref = (g.random(nb) < fill).astype(np.int32)
+    ref[: nb // 3] = (np.arange(nb // 3) % 97 != 5) if fill > 0.4 else 0
+    held = np.flatnonzero(ref)
+    B = 40
+    table = np.full((B, mb), -1, np.int32)
+    if len(held):
+        table[:, :4] = g.choice(held, (B, 4))
+        ref = np.maximum(ref, counts(table, nb))
+    prefix, need = np.full(B, 14, np.int32), g.integers(0, 17, B).astype(np.int32)
+    k, v = pool(1, 1, nb, 1, bs, 8, torch.bfloat16)
+    pools = [host(k), host(v)]
+    for op in ("reserve", "compact"):
+        d_table, d_ref, st, used = i32(table), i32(ref), zeros_i32(1), zeros_i32(1)
+        o = [d_table, d_ref] if in_place else [torch.full_like(d_table, 77), torch.full_like(d_ref, 77)]
+        if op == "reserve":
+            want, t, r, fits = PG.reserve(pools, table, prefix, need, ref, bs)
+            sv.kv_pages_reserve(k, v, d_table, i32(prefix), i32(need), d_ref, *o, dev_status=st)
+            assert int(st.item()) == (0 if fits else sv.DEV_CAPACITY)
+        else:
+            want, t, r, n, _ = PG.compact(pools, table, ref)
+            sv.kv_pages_compact(k, v, d_table, d_ref, *o, used, dev_status=st)
+            assert int(st.item()) == 0 and int(used.item()) == n
+        for x, y in zip([*o, k, v], [t, r, *want]):
+            np.testing.assert_array_equal(host(x), y)
+        table, ref, pools = t, r, want
 
 
 POOLS = [  # layers, hkv, block size, head_dim, dtype

@@ -11,19 +11,24 @@
 // atomics count, their order changes nothing.
 //
 // fork and free move no rows: 4 bytes per table entry and per block, a few
-// microseconds of latency.  reserve and compact plan in one CTA (counts,
-// block-wide scans, a list of moves) and copy in a second launch over the
-// whole GPU, a programmatic dependent of the first; that one is bound by
-// HBM: two bytes moved per byte copied.
+// microseconds of latency.  reserve and compact plan in one cluster (counts,
+// scans, a list of moves) and copy in a second launch over the whole GPU, a
+// programmatic dependent of the first; that one is bound by HBM: two bytes
+// moved per byte copied.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
 
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kThreads = 1024;
 constexpr int kMaxBatch = 4096;   // rows of a table (a shared-memory word each)
 constexpr int kRange = 1024;      // blocks whose counts one CTA owns
+constexpr long long kScanEntries = 8192;  // table entries up to which every CTA scans the whole table
 
 __device__ __forceinline__ int ld_relaxed(const int32_t *p) {
   int v;
@@ -40,6 +45,41 @@ __device__ __forceinline__ bool page_stays(long long r0, int block_size, long lo
   return window <= 0 || r0 < sinks || r0 + block_size > P - window + 1;
 }
 
+// How many of the new sequences continue each old one.
+__device__ __forceinline__ void count_parents(const int32_t *__restrict__ parent, int batch, int batch_out,
+                                              int *s_mult, int32_t *status) {
+  for (int i = threadIdx.x; i < batch; i += kThreads) s_mult[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < batch_out; i += kThreads) {
+    const int p = parent[i];
+    if (p >= batch) {
+      sv::report(status, SPEC_DEV_BAD_PARENTS);
+    } else if (p >= 0) {
+      atomicAdd(&s_mult[p], 1);
+    }
+  }
+  __syncthreads();
+}
+// The new tables' entries and lengths, this thread's share of them.
+__device__ __forceinline__ void fork_rows(const int32_t *table, const int32_t *prefix_len,
+                                          const int32_t *__restrict__ parent, int batch, int batch_out,
+                                          int max_blocks, int num_blocks, int32_t *table_out, int32_t *prefix_out,
+                                          uint32_t first, uint32_t step) {
+  const uint32_t fresh = (uint32_t)batch_out * max_blocks;
+#pragma unroll 4
+  for (uint32_t e = first; e < fresh; e += step) {
+    const uint32_t i = e / max_blocks;
+    const int p = parent[i];
+    int blk = p >= 0 && p < batch ? table[(uint32_t)p * max_blocks + (e - i * max_blocks)] : -1;
+    if (blk < 0 || blk >= num_blocks) blk = -1;
+    table_out[e] = blk;
+  }
+  for (uint32_t i = first; i < (uint32_t)batch_out; i += step) {
+    const int p = parent[i];
+    prefix_out[i] = p >= 0 && p < batch ? prefix_len[p] : 0;
+  }
+}
+
 // fork (FORK) and free.  CTA c owns the counts of blocks [c kRange, +kRange):
 // it scans the whole table once, collects its blocks' changes in shared
 // memory and writes their counts.  free: the owner of an entry's block also
@@ -54,33 +94,11 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ int s_mult[FORK ? kMaxBatch : 1];  // continuations of an old sequence
   const int lo = blockIdx.x * kRange, n = min(kRange, num_blocks - lo);
   for (int i = threadIdx.x; i < n; i += kThreads) s_delta[i] = 0;
-  if constexpr (FORK)
-    for (int i = threadIdx.x; i < batch; i += kThreads) s_mult[i] = 0;
   __syncthreads();
   if constexpr (FORK) {
-    for (int i = threadIdx.x; i < batch_out; i += kThreads) {
-      const int p = parent[i];
-      if (p >= batch) {
-        sv::report(status, SPEC_DEV_BAD_PARENTS);
-      } else if (p >= 0) {
-        atomicAdd(&s_mult[p], 1);
-      }
-    }
-    __syncthreads();
-    // the new tables' entries and lengths, shared out over the CTAs
-    const uint32_t fresh = (uint32_t)batch_out * max_blocks, step = gridDim.x * kThreads;
-#pragma unroll 4
-    for (uint32_t e = blockIdx.x * kThreads + threadIdx.x; e < fresh; e += step) {
-      const uint32_t i = e / max_blocks;
-      const int p = parent[i];
-      int blk = p >= 0 && p < batch ? table[(uint32_t)p * max_blocks + (e - i * max_blocks)] : -1;
-      if (blk < 0 || blk >= num_blocks) blk = -1;
-      table_out[e] = blk;
-    }
-    for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < (uint32_t)batch_out; i += step) {
-      const int p = parent[i];
-      prefix_out[i] = p >= 0 && p < batch ? prefix_len[p] : 0;
-    }
+    count_parents(parent, batch, batch_out, s_mult, status);
+    fork_rows(table, prefix_len, parent, batch, batch_out, max_blocks, num_blocks, table_out, prefix_out,
+              blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
   }
   const uint32_t total = (uint32_t)batch * max_blocks;
 #pragma unroll 4
@@ -105,6 +123,46 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kThreads) ref_out[lo + i] = ref[lo + i] + s_delta[i];
+}
+
+// The same for tables of more entries than a CTA scans quickly: every entry
+// is looked at once, and its block's count changed by an atomic (in ref_out,
+// which holds the old counts by then: counts_copy_kernel, where it is not
+// changed in place).
+__global__ void __launch_bounds__(kThreads)
+    counts_copy_kernel(const int32_t *__restrict__ ref, int32_t *__restrict__ ref_out, int num_blocks) {
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  if (i < num_blocks) ref_out[i] = ref[i];
+}
+template <bool FORK>
+__global__ void __launch_bounds__(kThreads)
+    pages_refs_spread_kernel(const int32_t *table, const int32_t *prefix_len, const int32_t *__restrict__ parent,
+                             int batch, int batch_out, int max_blocks, int block_size, int num_blocks, int window,
+                             int sinks, int spare, int32_t *table_out, int32_t *prefix_out, int32_t *ref_out,
+                             int32_t *status) {
+  __shared__ int s_mult[FORK ? kMaxBatch : 1];
+  const uint32_t first = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
+  if constexpr (FORK) {
+    count_parents(parent, batch, batch_out, s_mult, status);
+    fork_rows(table, prefix_len, parent, batch, batch_out, max_blocks, num_blocks, table_out, prefix_out, first, step);
+  }
+  const uint32_t total = (uint32_t)batch * max_blocks;
+#pragma unroll 4
+  for (uint32_t e = first; e < total; e += step) {
+    const int blk = table[e];
+    const uint32_t b = e / max_blocks;
+    const bool good = blk >= 0 && blk < num_blocks;
+    if (blk >= num_blocks) sv::report(status, SPEC_DEV_BAD_BLOCK);
+    if constexpr (FORK) {
+      const int d = s_mult[b] - 1;
+      if (good && d) atomicAdd(&ref_out[blk], d);
+    } else {
+      const bool stays = good && page_stays((long long)(e - b * max_blocks) * block_size, block_size, prefix_len[b],
+                                            window, sinks, spare);
+      if (good && !stays) atomicSub(&ref_out[blk], 1);
+      table_out[e] = stays ? blk : -1;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -170,6 +228,52 @@ __device__ V cta_scan(V v, V *total) {
   return x - v + (warp ? s_warp[warp - 1] : V(0));
 }
 
+// The plans run on one cluster: CTA c owns the contiguous blocks [lo, hi) of
+// the pool, so a pool of a million blocks is read by eight SMs and a small
+// one by a single CTA.
+constexpr int kPlanCtas = 8;
+constexpr int kPlanBlocks = 8192;  // blocks that a CTA of a plan takes on before the cluster grows
+struct Span {
+  int lo, hi;
+};
+__device__ __forceinline__ Span my_span(int num_blocks) {
+  const int per = (num_blocks + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int lo = min(num_blocks, (int)blockIdx.x * per);
+  return Span{lo, min(num_blocks, lo + per)};
+}
+__device__ __forceinline__ void plan_sync(cg::cluster_group &cluster) {
+  if (gridDim.x > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+}
+// Sums a number of each CTA over the cluster: the CTAs before this one, and all.
+__device__ void cluster_sums(cg::cluster_group &cluster, int *s_mine, int mine, int *before, int *all) {
+  *before = 0;
+  *all = mine;
+  if (gridDim.x == 1) return;
+  if (threadIdx.x == 0) *s_mine = mine;
+  cluster.sync();
+  int b = 0, a = 0;
+  for (int i = 0; i < (int)gridDim.x; ++i) {
+    const int v = *cluster.map_shared_rank(s_mine, i);
+    a += v;
+    if (i < (int)blockIdx.x) b += v;
+  }
+  *before = b;
+  *all = a;
+}
+// Sum over the CTA of f(i), i in [lo, hi).
+template <typename F>
+__device__ int cta_count(int lo, int hi, F f) {
+  if (lo >= hi) return 0;
+  int v = 0, total;
+#pragma unroll 8
+  for (int i = lo + (int)threadIdx.x; i < hi; i += kThreads) v += f(i);
+  cta_scan(v, &total);
+  return total;
+}
+
 // The entries a call writes: the pages holding rows P .. P + need - 1 of each
 // sequence, numbered in (sequence, page) order.
 struct Writes {
@@ -192,16 +296,17 @@ __global__ void __launch_bounds__(kThreads)
                         int num_blocks, const int32_t *__restrict__ prefix_len, const int32_t *__restrict__ need,
                         const int32_t *ref, int32_t *ref_out, const Space ws, int32_t *status) {
   __shared__ int s_off[kMaxBatch + 1];
-  __shared__ int s_moves;
+  __shared__ int s_moves, s_free;
+  cg::cluster_group cluster = cg::this_cluster();
   sv::ptx::grid_dep_launch();
   const int tid = threadIdx.x;
+  const Span own = my_span(num_blocks);
   if (tid == 0) s_moves = 0;
 
-  // 1. how many entries each sequence writes, and how many blocks are free
-  // (each thread looks at one contiguous piece of either): one scan for both
-  const int sper = (batch + kThreads - 1) / kThreads, per = (num_blocks + kThreads - 1) / kThreads;
+  // 1. how many entries each sequence writes (a thread takes consecutive
+  // ones; every CTA counts them all)
+  const int sper = (batch + kThreads - 1) / kThreads;
   const int b0 = min(batch, tid * sper), b1 = min(batch, b0 + sper);
-  const int lo = min(num_blocks, tid * per), hi = min(num_blocks, lo + per);
   auto writes_of = [&](int b, bool tell) -> int {
     const int nd = need[b];
     if (nd <= 0) return 0;
@@ -212,30 +317,49 @@ __global__ void __launch_bounds__(kThreads)
     }
     return (int)((uint32_t)(end - 1) / (uint32_t)block_size - (uint32_t)P / (uint32_t)block_size) + 1;
   };
-  unsigned long long v = 0, sums;
-  for (int i = lo; i < hi; ++i) v += ref[i] <= 0;
+  // (in the same scan: the free ones among this CTA's first kThreads blocks;
+  // on the way over its blocks: the writers' counts at their start, and the
+  // counts as they were, where they are not changed in place)
+  auto visit = [&](int i) -> int {
+    const int r = ref[i];
+    ws.a[i] = 0;
+    ws.b[i] = -1;
+    if (ref_out != ref) ref_out[i] = r;
+    return r <= 0;
+  };
+  const int first = own.lo + tid;
+  const int first_free = first < own.hi ? visit(first) : 0;
+  unsigned long long v = first_free, sums;
   for (int b = b0; b < b1; ++b) v += (unsigned long long)writes_of(b, true) << 32;
-  const unsigned long long before = cta_scan(v, &sums);
-  const int n = (int)(sums >> 32), all_free = (int)(uint32_t)sums;
-  int at = (int)(before >> 32);
+  const unsigned long long sofar = cta_scan(v, &sums);
+  const int n = (int)(sums >> 32);
+  int at = (int)(sofar >> 32);
   for (int b = b0; b < b1; ++b) {
     s_off[b] = at;
     at += writes_of(b, false);
   }
   if (tid == 0) s_off[batch] = n;
-  // the lowest free blocks in order, as many as could be wanted; and the
-  // tables and counts as they were, where they are not changed in place
-  at = (int)(uint32_t)before;
-  for (int i = lo; i < hi; ++i) {
-    const int r = ref[i];
-    if (r <= 0 && at < n) ws.c[at++] = i;
-    ws.a[i] = 0;
-    ws.b[i] = -1;
-    if (ref_out != ref) ref_out[i] = r;
-  }
+  const int nfree = (int)(uint32_t)sums + cta_count(own.lo + kThreads, own.hi, visit);
   if (table_out != table)
-    for (int64_t e = tid; e < (int64_t)batch * max_blocks; e += kThreads) table_out[e] = table[e];
-  __syncthreads();
+    for (int64_t e = (int64_t)blockIdx.x * kThreads + tid; e < (int64_t)batch * max_blocks;
+         e += (int64_t)gridDim.x * kThreads)
+      table_out[e] = table[e];
+  int base, all_free;
+  cluster_sums(cluster, &s_free, nfree, &base, &all_free);
+  // the lowest free blocks in order, as many as could be wanted
+  const int k0 = base + (int)(uint32_t)sofar;
+  if (first_free && k0 < n) ws.c[k0] = first;
+  base += (int)(uint32_t)sums;
+  for (int i0 = own.lo + kThreads; i0 < own.hi && base < n; i0 += kThreads) {
+    const int i = i0 + tid;
+    const bool f = i < own.hi && ref[i] <= 0;
+    int sum;
+    const int k = base + cta_scan((int)f, &sum);
+    if (f && k < n) ws.c[k] = i;
+    base += sum;
+  }
+  plan_sync(cluster);  // the CTAs' parts are in place (and their sums read)
+  if (blockIdx.x != 0) return;
   const Writes wr{s_off, batch};
   struct Entry {
     int b, j, blk, r;  // sequence, page, its block (-1: none) and that block's count
@@ -295,7 +419,7 @@ __global__ void __launch_bounds__(kThreads)
       const int f = i == tid ? my_flag : ws.flag[i] & 3, rank = i == tid ? my_rank : ws.flag[i] >> 2;
       if (f == kKeep) continue;
       const Entry x = i == tid ? mine : entry(i);
-      const int blk = ws.c[rank];
+      const int blk = __ldcg(&ws.c[rank]);
       table_out[x.e] = blk;
       ref_out[blk] = 1;
       if (f == kCopy) {
@@ -313,48 +437,60 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(kThreads)
     compact_plan_kernel(int block_size, int num_blocks, const int32_t *ref, int32_t *ref_out, int32_t *n_used,
                         int32_t *remap, const Space ws) {
+  __shared__ int s_sum[2];
+  cg::cluster_group cluster = cg::this_cluster();
   sv::ptx::grid_dep_launch();
   const int tid = threadIdx.x;
-  const int per = (num_blocks + kThreads - 1) / kThreads;
-  const int lo = min(num_blocks, tid * per), hi = min(num_blocks, lo + per);
-  int used = 0;
-  for (int i = lo; i < hi; ++i) used += ref[i] > 0;
-  int U;
-  cta_scan(used, &U);
-  // the holes below U and the used blocks from U on, in order: as many of one as of the other
-  int holes = 0, high = 0;
-  for (int i = lo; i < hi; ++i) {
-    const bool u = ref[i] > 0;
-    holes += !u && i < U;
-    high += u && i >= U;
+  const Span own = my_span(num_blocks);
+  // U, and the used blocks before this CTA's (the first kThreads of its
+  // blocks by a scan that is needed later anyway)
+  int before, U, low_before, low, first_sum;
+  const int first = own.lo + tid, first_r = first < own.hi ? ref[first] : 0;
+  const int first_ub = cta_scan((int)(first_r > 0), &first_sum);
+  const int used = first_sum + cta_count(own.lo + kThreads, own.hi, [&](int i) { return (int)(ref[i] > 0); });
+  cluster_sums(cluster, &s_sum[0], used, &before, &U);
+  // used blocks below U
+  if (num_blocks <= kThreads) {
+    if (first == U) s_sum[1] = first_ub;
+    __syncthreads();
+    low = U < num_blocks && U < kThreads ? s_sum[1] : U;
+  } else {
+    const int mine = cta_count(own.lo, min(own.hi, max(own.lo, U)), [&](int i) { return (int)(ref[i] > 0); });
+    cluster_sums(cluster, &s_sum[1], mine, &low_before, &low);
   }
-  int m, m2;
-  int h = cta_scan(holes, &m), s = cta_scan(high, &m2);
-  for (int i = lo; i < hi; ++i) {
-    const bool u = ref[i] > 0;
-    if (!u && i < U) ws.moves[h++].dst = i;
-    if (u && i >= U) {
-      ws.moves[s].rows = block_size;
-      ws.moves[s++].src = i;
+  const int m = U - low;  // holes below U, and as many used blocks from U on
+  for (int i0 = own.lo; i0 < own.hi; i0 += kThreads) {
+    const int i = i0 + tid;
+    const int r = i < own.hi ? ref[i] : 0;
+    int sum = first_sum;
+    const int ub = before + (i0 == own.lo ? first_ub : cta_scan((int)(r > 0), &sum));  // used blocks before block i
+    before += sum;
+    if (i < own.hi) {
+      if (r <= 0 && i < U) ws.moves[i - ub].dst = i;
+      if (r > 0 && i >= U) {
+        ws.moves[ub - low].rows = block_size;
+        ws.moves[ub - low].src = i;
+      }
+      ws.a[i] = r > 0 ? i : -1;  // the new id of block i (those that move: below)
+      ref_out[i] = max(r, 0);
     }
-    ws.a[i] = u ? i : -1;  // the new id of block i (those that move: below)
   }
-  for (int i = lo; i < hi; ++i) ref_out[i] = max(ref[i], 0);
-  __syncthreads();
-  for (int k = tid; k < m; k += kThreads) {
-    const int src = ws.moves[k].src, dst = ws.moves[k].dst;
+  plan_sync(cluster);
+  for (int k = (int)blockIdx.x * kThreads + tid; k < m; k += (int)gridDim.x * kThreads) {
+    const int src = __ldcg(&ws.moves[k].src), dst = __ldcg(&ws.moves[k].dst);
     ws.a[src] = dst;
-    ref_out[dst] = ref[src];
+    ref_out[dst] = __ldcg(&ref[src]);
     ref_out[src] = 0;
   }
-  if (tid == 0) {
+  if (tid == 0 && blockIdx.x == 0) {
     *ws.n_moves = m;
     *n_used = U;
   }
   if (remap) {
-    __syncthreads();
-    for (int i = lo; i < hi; ++i) remap[i] = ws.a[i];
+    plan_sync(cluster);
+    for (int i = own.lo + tid; i < own.hi; i += kThreads) remap[i] = __ldcg(&ws.a[i]);
   }
+  plan_sync(cluster);  // the partners' reads of this CTA's sums are done
 }
 
 // Copies the planned rows of every layer and KV head, K and V, 16 bytes a
@@ -432,6 +568,53 @@ int launch_copy(void *k, void *v, int n_layers, int hkv, int block_size, int num
              : SPEC_ERR_CUDA;
 }
 
+// Launches a plan kernel on a cluster as the pool needs it.
+template <typename... P, typename... A>
+int launch_plan(void (*kern)(P...), int num_blocks, cudaStream_t stream, A... args) {
+  int nc = 1;
+  while (nc < kPlanCtas && (long long)nc * kPlanBlocks < num_blocks) nc *= 2;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = nc;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(nc);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+// fork and free.  A CTA that owns its blocks' counts has one launch to do and
+// no atomics in memory, but looks at every entry; measured fork / free, us,
+// against one look and an atomic per entry (two launches out of place): 64
+// entries 3.0 / 1.9 against 3.3 / 2.3, 4096: 3.6 / 3.9 against 5.3 / 5.7,
+// 8192: 4.5 / 6.2 against 5.4 / 5.7, 16384: 6.0 / 9.4 against 5.5 / 5.8,
+// 262144: 79 / 77 against 6.8 / 6.8.
+template <bool FORK>
+int launch_refs(const int32_t *table, const int32_t *prefix_len, const int32_t *parent, int batch, int batch_out,
+                int max_blocks, int block_size, int num_blocks, int window, int sinks, int spare, const int32_t *ref,
+                int32_t *table_out, int32_t *prefix_out, int32_t *ref_out, int32_t *status, cudaStream_t stream) {
+  const long long entries = (long long)(batch_out > batch ? batch_out : batch) * max_blocks;
+  if (entries <= kScanEntries) {
+    pages_refs_kernel<FORK><<<(num_blocks + kRange - 1) / kRange, kThreads, 0, stream>>>(
+        table, prefix_len, parent, batch, batch_out, max_blocks, block_size, num_blocks, window, sinks, spare, ref,
+        table_out, prefix_out, ref_out, status);
+    return sv_launch_status();
+  }
+  if (ref_out != ref) {
+    counts_copy_kernel<<<(num_blocks + kThreads - 1) / kThreads, kThreads, 0, stream>>>(ref, ref_out, num_blocks);
+    if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  }
+  const long long ctas = (entries + 4 * kThreads - 1) / (4 * kThreads);
+  pages_refs_spread_kernel<FORK><<<(unsigned)(ctas < 304 ? ctas : 304), kThreads, 0, stream>>>(
+      table, prefix_len, parent, batch, batch_out, max_blocks, block_size, num_blocks, window, sinks, spare, table_out,
+      prefix_out, ref_out, status);
+  return sv_launch_status();
+}
+
 }  // namespace
 
 size_t sv_pages_ws_bytes(int batch, int max_blocks, int num_blocks) {
@@ -443,19 +626,15 @@ static_assert(kMaxBatch == SPEC_PAGES_MAX_BATCH, "the header's limit");
 int sv_pages_fork(const int32_t *table, const int32_t *prefix_len, const int32_t *parent, int batch, int batch_out,
                   int max_blocks, int num_blocks, const int32_t *ref, int32_t *table_out, int32_t *prefix_out,
                   int32_t *ref_out, int32_t *status, cudaStream_t stream) {
-  pages_refs_kernel<true><<<(num_blocks + kRange - 1) / kRange, kThreads, 0, stream>>>(
-      table, prefix_len, parent, batch, batch_out, max_blocks, 1, num_blocks, 0, 0, 0, ref, table_out, prefix_out,
-      ref_out, status);
-  return sv_launch_status();
+  return launch_refs<true>(table, prefix_len, parent, batch, batch_out, max_blocks, 1, num_blocks, 0, 0, 0, ref,
+                           table_out, prefix_out, ref_out, status, stream);
 }
 
 int sv_pages_free(const int32_t *table, const int32_t *prefix_len, int batch, int max_blocks, int block_size,
                   int num_blocks, int window, int sinks, int spare, const int32_t *ref, int32_t *table_out,
                   int32_t *ref_out, int32_t *status, cudaStream_t stream) {
-  pages_refs_kernel<false><<<(num_blocks + kRange - 1) / kRange, kThreads, 0, stream>>>(
-      table, prefix_len, nullptr, batch, 0, max_blocks, block_size, num_blocks, window, sinks, spare, ref, table_out,
-      nullptr, ref_out, status);
-  return sv_launch_status();
+  return launch_refs<false>(table, prefix_len, nullptr, batch, 0, max_blocks, block_size, num_blocks, window, sinks,
+                            spare, ref, table_out, nullptr, ref_out, status, stream);
 }
 
 int sv_pages_reserve(void *k, void *v, int vec_per_row, int n_layers, int hkv, int block_size, int num_blocks,
@@ -464,9 +643,9 @@ int sv_pages_reserve(void *k, void *v, int vec_per_row, int n_layers, int hkv, i
                      cudaStream_t stream) {
   Space ws;
   space_layout(&ws, workspace, batch, max_blocks, num_blocks);
-  reserve_plan_kernel<<<1, kThreads, 0, stream>>>(table, table_out, batch, max_blocks, block_size, num_blocks,
-                                                  prefix_len, need, ref, ref_out, ws, status);
-  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  const int rc = launch_plan(reserve_plan_kernel, num_blocks, stream, table, table_out, batch, max_blocks, block_size,
+                             num_blocks, prefix_len, need, ref, ref_out, ws, status);
+  if (rc != SPEC_OK) return rc;
   return launch_copy<false>(k, v, n_layers, hkv, block_size, num_blocks, vec_per_row, batch, ws, nullptr, nullptr, 0,
                             status, stream);
 }
@@ -477,8 +656,9 @@ int sv_pages_compact(void *k, void *v, int vec_per_row, int n_layers, int hkv, i
                      cudaStream_t stream) {
   Space ws;
   space_layout(&ws, workspace, batch, max_blocks, num_blocks);
-  compact_plan_kernel<<<1, kThreads, 0, stream>>>(block_size, num_blocks, ref, ref_out, n_used, remap, ws);
-  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  const int rc = launch_plan(compact_plan_kernel, num_blocks, stream, block_size, num_blocks, ref, ref_out, n_used,
+                             remap, ws);
+  if (rc != SPEC_OK) return rc;
   return launch_copy<true>(k, v, n_layers, hkv, block_size, num_blocks, vec_per_row, (num_blocks + 1) / 2, ws, table,
                            table_out, (int64_t)batch * max_blocks, status, stream);
 }
