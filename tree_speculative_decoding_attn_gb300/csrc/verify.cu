@@ -27,8 +27,6 @@
 // large batch.  One cluster per sequence; each warp owns one contiguous piece
 // of the row, so the bonus is found from the per-warp sums by rereading one
 // warp's piece (a few KB, in L2), a vector a thread.
-#include <cooperative_groups.h>
-
 #include <type_traits>
 
 #include "common.cuh"
@@ -37,7 +35,7 @@
 
 namespace {
 
-namespace cg = cooperative_groups;
+using namespace sv::ptx;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
@@ -45,6 +43,16 @@ constexpr int kMaxCluster = 16;
 constexpr int kInFlight = 4;  // 16-byte loads of one lane in flight (twice that with a drafter's row)
 typedef unsigned long long u64;
 constexpr u64 kOne = 1ull << 60;
+
+// Cluster barrier in two halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Writes v to another CTA's shared memory and counts its 8 bytes on a barrier there.
+__device__ __forceinline__ void send_u64(uint32_t dst, u64 v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u64 [%0], %1, [%2];" ::"r"(dst), "l"(v), "r"(bar)
+               : "memory");
+}
+constexpr uint32_t kWaitLimit = 1u << 22;
 
 // The bits of a float in [0, 1] as a number of units of 2^-60, cut: the 24
 // bits of the significand at the top of 64, shifted right by what the
@@ -99,8 +107,8 @@ struct Shared {
   int removed[SPEC_MAX_NODES];     // the distinct rejected tokens of the last node
   int path[SPEC_MAX_NODES + 1];
   u64 wsum[kWarps];
-  u64 part[2];                  // this CTA's sum, double-buffered by exchange
-  u64 all[kMaxCluster];
+  u64 all[2][kMaxCluster];      // the CTAs' sums, double-buffered by exchange, and
+  uint64_t bar[2];              // the barriers that count their arrival
   // the walk's next pass over a row: node, c = ci + cf * 2^-60, whether it is the bonus
   int node, n_removed, last, len;
   uint32_t ci;
@@ -175,8 +183,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nc = gridDim.x, rank = blockIdx.x, b = blockIdx.y;  // the cluster spans x
-  cg::cluster_group cluster = cg::this_cluster();
   bool bad = false;
+  if (tid == 0) {
+    mbar_init(&sh.bar[0], 1);
+    mbar_init(&sh.bar[1], 1);
+    mbar_fence_init();
+  }
+  __syncthreads();
+  cluster_arrive();  // (waited for before the first sum is sent)
 
   // every node's test needs one value of its parent's row (every CTA of the
   // cluster walks the tree itself, from the same values)
@@ -279,20 +293,27 @@ __global__ void __launch_bounds__(kThreads, 2)
       f(std::integral_constant<int, 2>{});
     }
   };
-  // the cluster's sum of the CTAs' wsum; sh.all holds the CTAs' own
-  int parity = 0;
+  // The cluster's sum of the CTAs' wsum; all[] holds the CTAs' own.  Each CTA
+  // sends its sum to every CTA and waits for theirs: one trip, where a cluster
+  // barrier and a read of the others' memory take two (1.1 us).
+  int turn = 0;
+  const u64 *all = nullptr;
   auto cluster_total = [&]() -> u64 {
+    if (turn == 0) cluster_wait();  // every CTA's barriers exist
+    const int buf = turn & 1;
+    const uint32_t parity = (turn >> 1) & 1;
+    ++turn;
     __syncthreads();
     if (warp == 0) {
       const u64 s = warp_sum_u64(lane < kWarps ? sh.wsum[lane] : 0);
-      if (lane == 0) sh.part[parity] = s;
+      if (lane == 0) mbar_expect_tx(&sh.bar[buf], nc * (uint32_t)sizeof(u64));
+      __syncwarp();
+      if (lane < nc) send_u64(mapa_cluster(&sh.all[buf][rank], lane), s, mapa_cluster(&sh.bar[buf], lane));
     }
-    cluster.sync();
-    if (tid < nc) sh.all[tid] = *cluster.map_shared_rank(&sh.part[parity], tid);
-    parity ^= 1;
-    __syncthreads();
+    if (!mbar_wait_cluster(&sh.bar[buf], parity, kWaitLimit)) sv::report(status, SPEC_DEV_TIMEOUT);
+    all = sh.all[buf];
     u64 s = 0;
-    for (int i = 0; i < nc; ++i) s += sh.all[i];
+    for (int i = 0; i < nc; ++i) s += all[i];
     return s;
   };
 
@@ -369,12 +390,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     total = cluster_total();
   }
 
+  cluster_arrive();  // no more is sent; at the kernel's end every CTA has got this far
   // the bonus: the CTA, then the warp whose piece's sum passes u * total; its
   // piece is read again by the whole CTA, a vector a thread
   const u64 thr = part_of(uniform(u_bonus[b]), total);
   u64 before = 0;
-  for (int i = 0; i < rank; ++i) before += sh.all[i];
-  if (total > 0 && before <= thr && thr < before + sh.all[rank]) {
+  for (int i = 0; i < rank; ++i) before += all[i];
+  if (total > 0 && before <= thr && thr < before + all[rank]) {
     int owner = 0;
     while (before + sh.wsum[owner] <= thr) before += sh.wsum[owner++];
     __syncthreads();  // wsum is read; it takes the warps' sums of the piece's rounds from here on
@@ -436,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = tid; i < path_cap; i += kThreads) acc_path[(int64_t)b * path_cap + i] = i <= sh.len ? sh.path[i] : -1;
   }
   if (bad) sv::report(status, SPEC_DEV_BAD_PROB);
-  cluster.sync();  // the partners' reads of this CTA's sums are done
+  __syncwarp();
+  cluster_wait();
 }
 
 // CTAs per sequence: as many as give every warp a full load round of its
