@@ -102,7 +102,7 @@ __device__ __forceinline__ u64 warp_incl_u64(u64 v) {
 struct Shared {
   int fc[SPEC_MAX_NODES], ns[SPEC_MAX_NODES], tok[SPEC_MAX_NODES], par[SPEC_MAX_NODES];
   float u[SPEC_MAX_NODES], p[SPEC_MAX_NODES], q[SPEC_MAX_NODES];
-  uint8_t keep[SPEC_MAX_NODES];    // deterministic siblings: kept if the walk gets to it
+  uint8_t keep[SPEC_MAX_NODES];    // kept if the walk gets to it (drafter's siblings: to it first)
   uint8_t again[SPEC_MAX_NODES];   // its token is an earlier sibling's
   int removed[SPEC_MAX_NODES];     // the distinct rejected tokens of the last node
   int path[SPEC_MAX_NODES + 1];
@@ -206,6 +206,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int64_t at = ((int64_t)b * N + par) * V + t;
       sh.p[tid] = __uint_as_float(checked(__float_as_uint(sv::to_f32(p_all[at])), &bad));
       sh.q[tid] = DRAFT ? __uint_as_float(checked(__float_as_uint(sv::to_f32(q_all[at])), &bad)) : 1.f;
+      // drafter's siblings: the test of a first sibling
+      sh.keep[tid] = (double)sh.u[tid] * (double)sh.q[tid] < (double)sh.p[tid];
     }
   }
   __syncthreads();
@@ -332,9 +334,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (t < 0 || t >= V) {
           if (rank == 0) sv::report(status, SPEC_DEV_BAD_TOKEN);
         } else if (DRAFT) {
-          const double c = (double)ci + (double)cf * 0x1p-60;
-          const double q = (double)sh.q[child], w = fmax(0.0, (double)sh.p[child] - c * q);
-          keep = D > 0 && (double)sh.u[child] * q * ((double)D * 0x1p-60) < w;
+          if (!(ci | cf)) {
+            keep = sh.keep[child];
+          } else {
+            const double c = (double)ci + (double)cf * 0x1p-60;
+            const double q = (double)sh.q[child], w = fmax(0.0, (double)sh.p[child] - c * q);
+            keep = D > 0 && (double)sh.u[child] * q * ((double)D * 0x1p-60) < w;
+          }
           counted = true;
         } else {
           keep = sh.keep[child];
