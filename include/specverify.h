@@ -583,7 +583,7 @@ int spec_accept(int mode, const void *logits, const void *draft_logits, int dtyp
  * An accepted child is the next v.  Where none is accepted, the bonus is the
  * lowest token x with w(0) + .. + w(x) > u_bonus[b] * (sum of w); weights
  * that are all zero give way to target_probs[b,v].
- * Outputs as spec_accept.  Sums are exact to 2^-60 a value and independent
+ * Outputs as spec_accept.  Sums are exact to 2^-58 a value and independent
  * of their order; the tests of the drafts are float64.  Numbers outside
  * [0, 1) count as the nearest number inside, NaN as 0.
  * dev_status: SPEC_DEV_BAD_TOKEN (a child's token outside [0, vocab): never
@@ -591,7 +591,7 @@ int spec_accept(int mode, const void *logits, const void *draft_logits, int dtyp
  * with parents[]: the node is taken to have no further child),
  * SPEC_DEV_CAPACITY (a path longer than path_cap: the path ends there),
  * SPEC_DEV_BAD_PROB (a value outside [0, 1], NaN among them: counts as 0; or
- * a row of zeros to draw the bonus from: token 0).
+ * a row to draw the bonus from whose sum is 0, or 4 and more: token 0).
  * ------------------------------------------------------------------ */
 int spec_verify_probs(const void *target_probs, const void *draft_probs, int dtype, int batch,
                       int n_nodes, int vocab, const int32_t *tok, const int32_t *parents,

@@ -16,9 +16,9 @@
 // lowest token x with sum_{y <= x} r(y) > u * sum r.
 //
 // Exactness.  The answer is a set of integers, so no sum may depend on its
-// order.  Probabilities are turned into 64-bit fixed point in units of 2^-60
-// (exact from 2^-37 up, cut below), and every sum is an integer sum: the
-// same for any split over lanes, warps and CTAs, and within V * 2^-60 of the
+// order.  Probabilities are turned into 64-bit fixed point in units of 2^-58
+// (exact from 2^-35 up, cut below), and every sum is an integer sum: the
+// same for any split over lanes, warps and CTAs, and within V * 2^-58 of the
 // real one, where float32 sums would move the border of every token by up to
 // 2^-24.  The tests of single drafts use float64 (one thread, a few products).
 //
@@ -42,7 +42,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kInFlight = 4;  // 16-byte loads of one lane in flight (twice that with a drafter's row)
 typedef unsigned long long u64;
-constexpr u64 kOne = 1ull << 60;
+constexpr int kBits = 58;
+constexpr u64 kOne = 1ull << kBits;
+// Sums stop below a mass of 4: a row that gets there is no distribution (its
+// bonus is token 0, reported), and no sum of a million ones wraps: between
+// two stops lie the 32 values of a load round, or 16 stopped sums.
+constexpr u64 kMost = 4 * kOne - 1;
 
 // Cluster barrier in two halves.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -54,14 +59,14 @@ __device__ __forceinline__ void send_u64(uint32_t dst, u64 v, uint32_t bar) {
 }
 constexpr uint32_t kWaitLimit = 1u << 22;
 
-// The bits of a float in [0, 1] as a number of units of 2^-60, cut: the 24
+// The bits of a float in [0, 1] as a number of units of 2^-58, cut: the 24
 // bits of the significand at the top of 64, shifted right by what the
-// exponent leaves (m 2^(e - 150) = (m 2^40 >> (130 - e)) 2^-60; PTX gives 0
+// exponent leaves (m 2^(e - 150) = (m 2^40 >> (132 - e)) 2^-58; PTX gives 0
 // for shifts past 63).
-__device__ __forceinline__ u64 fixed60(uint32_t b) {
+__device__ __forceinline__ u64 fixed(uint32_t b) {
   const u64 m = (u64)(((b & 0x7FFFFFu) | 0x800000u) << 8) << 32;
   u64 r;
-  asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(m), "r"(130u - (b >> 23)));
+  asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(m), "r"(132u - (b >> 23)));
   return r;
 }
 constexpr uint32_t kOneBits = 0x3F800000u;  // 1.f: bits of the floats in [0, 1] are at most these
@@ -86,8 +91,9 @@ __device__ __forceinline__ u64 part_of(float u, u64 s) {
 }
 __device__ __forceinline__ u64 warp_sum_u64(u64 v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = 16; o > 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  v = min(v, kMost);
+  return min(v + __shfl_xor_sync(0xffffffffu, v, 1), kMost);
 }
 __device__ __forceinline__ u64 warp_incl_u64(u64 v) {
   const int lane = threadIdx.x & 31;
@@ -109,7 +115,7 @@ struct Shared {
   u64 wsum[kWarps];
   u64 all[2][kMaxCluster];      // the CTAs' sums, double-buffered by exchange, and
   uint64_t bar[2];              // the barriers that count their arrival
-  // the walk's next pass over a row: node, c = ci + cf * 2^-60, whether it is the bonus
+  // the walk's next pass over a row: node, c = ci + cf * 2^-58, whether it is the bonus
   int node, n_removed, last, len;
   uint32_t ci;
   u64 cf;
@@ -157,17 +163,18 @@ struct Row {
   }
 };
 
-// max(0, p - c q) of a vector's elements, c = ci + cf * 2^-60.  MODE: 0
-// c = 0, 1 c = 1, 2 any c.
+// max(0, p - c q) of a vector's elements, c = ci + cf * 2^-58.  MODE: 0
+// c = 0, 1 c = 1, 2 c < 16, 3 any c (c q past 4 is past any p).
 template <int MODE, int VEC>
 __device__ __forceinline__ void weights(const uint32_t (&p)[VEC], const uint32_t (&q)[VEC], uint32_t ci, u64 cf,
                                         u64 (&x)[VEC]) {
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
-    x[i] = fixed60(p[i]);
+    x[i] = fixed(p[i]);
     if (MODE == 0) continue;
-    u64 fq = fixed60(q[i]);
-    if (MODE == 2) fq = fq * ci + __umul64hi(cf << 4, fq);
+    u64 fq = fixed(q[i]);
+    if (MODE == 3) fq = min(fq, kMost / ci);
+    if (MODE >= 2) fq = fq * ci + __umul64hi(cf << (64 - kBits), fq);
     x[i] = x[i] > fq ? x[i] - fq : 0;
   }
 }
@@ -267,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         a[j] = k < k1 ? rp.load(k) : make_uint4(0, 0, 0, 0);
         if (MODE) c[j] = k < k1 ? rq.load(k) : make_uint4(0, 0, 0, 0);
       }
+      u64 xs = 0;
 #pragma unroll
       for (int j = 0; j < kInFlight; ++j) {
         uint32_t pb[VEC], qb[VEC] = {};
@@ -275,24 +283,29 @@ __global__ void __launch_bounds__(kThreads, 2)
         u64 x[VEC];
         weights<MODE>(pb, qb, rci, rcf, x);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) s += x[i];
+        for (int i = 0; i < VEC; ++i) xs += x[i];
       }
+      s = min(s + xs, kMost);
     }
-    if (!DRAFT) {
+    s = warp_sum_u64(s);
+    if (!DRAFT && removals) {
+      u64 gone = 0;
       for (int r = lane; r < removals; r += 32) {
         const int t = sh.removed[r], k = (t + rp.mis) / VEC;
         bool ignore;
-        if (k >= w * seg && k < k1) s -= fixed60(checked(__float_as_uint(sv::to_f32(rp.row[t])), &ignore));
+        if (k >= w * seg && k < k1) gone += fixed(checked(__float_as_uint(sv::to_f32(rp.row[t])), &ignore));
       }
+      gone = warp_sum_u64(gone);
+      s = s > gone ? s - gone : 0;
     }
-    s = warp_sum_u64(s);
     if (lane == 0) sh.wsum[warp] = s;
   };
   auto with_mode = [&](uint32_t rci, u64 rcf, auto f) {
     if (!DRAFT || !(rci | rcf)) return f(std::integral_constant<int, 0>{});
     if constexpr (DRAFT) {
       if (rci == 1 && rcf == 0) return f(std::integral_constant<int, 1>{});
-      f(std::integral_constant<int, 2>{});
+      if (rci < 16) return f(std::integral_constant<int, 2>{});
+      f(std::integral_constant<int, 3>{});
     }
   };
   // The cluster's sum of the CTAs' wsum; all[] holds the CTAs' own.  Each CTA
@@ -316,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     all = sh.all[buf];
     u64 s = 0;
     for (int i = 0; i < nc; ++i) s += all[i];
-    return s;
+    return min(s, kMost);
   };
 
   u64 total;
@@ -337,9 +350,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (!(ci | cf)) {
             keep = sh.keep[child];
           } else {
-            const double c = (double)ci + (double)cf * 0x1p-60;
+            const double c = (double)ci + (double)cf * 0x1p-58;
             const double q = (double)sh.q[child], w = fmax(0.0, (double)sh.p[child] - c * q);
-            keep = D > 0 && (double)sh.u[child] * q * ((double)D * 0x1p-60) < w;
+            keep = D > 0 && (double)sh.u[child] * q * ((double)D * 0x1p-58) < w;
           }
           counted = true;
         } else {
@@ -363,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         child = sh.ns[child];
         if (counted) {
           cf += D;  // c += D (below 2 in a row that sums to 1)
-          ci += (uint32_t)(cf >> 60);
+          ci += (uint32_t)(cf >> kBits);
           cf &= kOne - 1;
           want = child >= 0;  // its test needs the mass of the new residual
         }
@@ -396,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     total = cluster_total();
   }
 
+  if (total == kMost) total = 0;
   cluster_arrive();  // no more is sent; at the kernel's end every CTA has got this far
   // the bonus: the CTA, then the warp whose piece's sum passes u * total; its
   // piece is read again by the whole CTA, a vector a thread
@@ -404,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int i = 0; i < rank; ++i) before += all[i];
   if (total > 0 && before <= thr && thr < before + all[rank]) {
     int owner = 0;
-    while (before + sh.wsum[owner] <= thr) before += sh.wsum[owner++];
+    while (owner < kWarps - 1 && before + sh.wsum[owner] <= thr) before += sh.wsum[owner++];
     __syncthreads();  // wsum is read; it takes the warps' sums of the piece's rounds from here on
     with_mode(bci, bcf, [&](auto mode) {
       constexpr int MODE = decltype(mode)::value;
@@ -456,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (rank == 0) {
     if (tid == 0) {
       acc_len[b] = sh.len;
-      if (total == 0) {  // a row without any probability
+      if (total == 0) {  // a row without any probability, or with far too much
         bonus[b] = 0;
         bad = true;
       }
@@ -468,9 +482,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster_wait();
 }
 
-// CTAs per sequence: as many as give every warp a full load round of its
-// piece, up to 16 (a size the device may refuse: then 8), and no more than
-// keep the whole batch resident at once.
+// CTAs per sequence: up to 16 (a size the device may refuse: then 8), no more
+// than give every warp a full load round of its piece, and no more than keep
+// the whole batch resident at two CTAs a SM.
 template <typename T, bool DRAFT>
 int launch_verify(const void *p, const void *q, int batch, int N, int V, const int32_t *tok, const int32_t *parents,
                   const int32_t *first_child, const int32_t *next_sibling, const float *u_accept, const float *u_bonus,
@@ -479,7 +493,7 @@ int launch_verify(const void *p, const void *q, int batch, int N, int V, const i
   constexpr int VEC = 16 / (int)sizeof(T);
   auto kern = verify_kernel<T, DRAFT>;
   int nc = kMaxCluster;
-  while (nc > 1 && (batch * nc > 304 || (nc / 2) * kThreads * VEC >= V)) nc /= 2;
+  while (nc > 1 && (batch * nc > 2 * 152 || (nc / 2) * kThreads * VEC >= V)) nc /= 2;
   if (nc > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
     (void)cudaGetLastError();
     nc = 8;
