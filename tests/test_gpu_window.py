@@ -120,6 +120,9 @@ CASES = [
     ("bf16", 2, 8, 2, 128, [260, 5], R(11, 16, (4, 3)), 1, 0, 0),           # itself only
     ("bf16", 2, 8, 1, 128, [77, 1024], R(12, 64, (8, 4, 3, 2, 2)), 100000, 9, 0),  # a window over everything
     ("bf16", 1, 8, 1, 128, [9000], R(13, 32, (4, 3, 2)), 8000, 16, 0),      # one row group across every SM
+    ("bf16", 3, 16, 2, 128, [3000, 40, 900], R(15, 40, (6, 4, 2)), 2500, 200, 128),  # many parts, few, one
+    ("bf16", 2, 8, 2, 128, [4000, 1], R(16, 200, (8, 6, 4, 3)), 3000, 7, 0),  # parts of four row groups a KV head
+    ("bf16", 5, 64, 8, 128, [6000, 5000, 0, 300, 6100], R(17, 24, (4, 3, 2)), 5000, 4, 128),  # equal ranges
     ("bf16", 70, 4, 2, 128, [(37 * i) % 300 for i in range(70)], R(14, 8, (3, 2)), 90, 4, 0),
 ]
 

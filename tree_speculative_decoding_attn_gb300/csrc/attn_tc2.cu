@@ -146,8 +146,10 @@ struct SchedBase {
 // (keys 64 .. 64 + fold - 1 of the tile) instead of filling a tile of their
 // own: one tile less per row group, and half the bytes.
 //
-// whole: a row group is never cut, cluster c takes an equal share of them
-// and there is nothing to merge (the host's choice, tc2_whole).
+// The host (tc2_share) picks how row groups meet clusters: whole, never cut,
+// each cluster an equal number of them and nothing to merge; or parts > 0,
+// each cut alike into that many parts, one a cluster; or, with neither, the
+// stream of units cut into equal ranges.
 constexpr int kFold = 64;  // keys of half a tile
 template <bool WIN>
 struct Sched : SchedBase {};
@@ -155,7 +157,7 @@ template <>
 struct Sched<true> : SchedBase {
   sv::Window win;
   int gp;
-  int whole;
+  int whole, parts;
   __device__ sv::WinSpan span(int P) const {
     sv::WinSpan v = sv::win_span(win.window, win.sinks, P, kBN, pg.table ? kBN : 1);
     if (n_nodes <= kFold && v.s_end <= kFold) {
@@ -187,6 +189,10 @@ __device__ __forceinline__ int seq_tiles(const Sched<WIN> &s, int P) {
 }
 template <bool WIN>
 __device__ __forceinline__ int tiles_of(const Sched<WIN> &s, int raw) { return seq_tiles(s, prefix_ok(s, raw) ? raw : 0); }
+
+// Parts of a row group of n tiles: short ones have fewer, of four tiles at
+// least, so that none starts between the tree tiles and none is empty.
+__device__ __forceinline__ int part_count(int parts, int n) { return max(1, min(parts, n / 4)); }
 
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
@@ -547,8 +553,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   // The range lookup (warp 0) overlaps the barrier and TMEM set-up (warp 1).
   bool whole = false;
-  if constexpr (WIN) whole = s.whole;
-  if (warp == 0 && whole) {
+  int parts = 0;
+  if constexpr (WIN) {
+    whole = s.whole;
+    parts = s.parts;
+  }
+  if (warp == 0 && parts > 0) {
+    // part q of row group rg: of w = n + kSegW weights, those from q w / k on
+    const int rg = cluster / parts, q = cluster % parts;
+    const bool live = rg < s.batch * s.gpb();
+    const int b = live ? rg / s.gpb() : 0;
+    const int raw = s.prefix_len[b], n = tiles_of(s, raw);
+    const int k = part_count(parts, n);
+    auto first = [&](int i) { return i == 0 ? 0 : i >= k ? n : max(s.nt, i * (n + kSegW) / k - kSegW); };
+    if (lane == 0) {
+      bars->start_b = b;
+      bars->start_gi = live ? rg % s.gpb() : 0;
+      bars->start_t = live && q < k ? first(q) : 0;
+      bars->n_tiles = live && q < k ? first(q + 1) - first(q) : 0;
+      bars->start_raw = raw;
+      bars->start_raw_next = 0;  // (not reached)
+      if (rank == 0 && cluster >= 1) {
+        CutDesc d{0, 0, 0, 0};
+        if (live && q == 1 && k > 1) d = CutDesc{1, b, rg % s.gpb(), rg * parts + k - 1};
+        cut_descs<WIN>(ws, s.n_clusters)[cluster] = d;
+      }
+    }
+  } else if (warp == 0 && whole) {
     // this cluster's row groups [r0, r1): the tiles of their sequences
     const long long rgs = (long long)s.batch * s.gpb();
     const long long r0 = rgs * cluster / s.n_clusters, r1 = rgs * (cluster + 1) / s.n_clusters;
@@ -1471,30 +1502,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // as a programmatic dependent of the main kernel: its blocks become
 // resident as the main kernel's CTAs leave and wait for it to complete.
 constexpr int kCombRows = 32;
-template <bool WIN>
+constexpr int kCombBatch = 3;
 __global__ void __launch_bounds__(256, 4) attn_tc2_combine_kernel(void *__restrict__ ws, __nv_bfloat16 *__restrict__ out,
-                                                                  const Sched<WIN> s, int Hq) {
-  constexpr int PB = kPartialBytes<WIN>;
-  constexpr int OV = WIN ? 4 : 2;  // 16-byte vectors of a thread's 16 dims
-  constexpr int kCombBatch = WIN ? 2 : 3;  // contributors loaded together (what 64 registers hold)
+                                                                  const Sched<false> s, int Hq) {
   const int k = blockIdx.x + 1;                 // boundary between clusters k-1 and k
   const int rr = blockIdx.y * kCombRows + (threadIdx.x >> 3);  // row of the pair
   const int d0 = (threadIdx.x & 7) * 16;        // first head dim
   grid_dep_wait();  // the main kernel's partials and descriptors are written and visible
-  const CutDesc d = cut_descs<WIN>(ws, s.n_clusters)[k];
+  const CutDesc d = cut_descs<false>(ws, s.n_clusters)[k];
   if (!d.usable) return;
-  const int heads = Hq / s.hkv;
-  int G = heads;  // rows per node
-  if constexpr (WIN) G = s.gp;
-  const int R = s.n_nodes * G;
+  const int G = Hq / s.hkv, R = s.n_nodes * G;
   const int kvh = d.gi / s.pairs, pair = d.gi % s.pairs;
   const int rg = pair * kPairRows + rr;
-  if (rg >= R || rg % G >= heads) return;
+  if (rg >= R) return;
   const int c_lo = k - 1, nc = d.c_hi - c_lo + 1;
   // cluster c's part: slot 2c + 1 when cut at its range end (all but the last)
   auto row_of = [&](int c) -> const uint8_t * {
     const int slot = 2 * c + (c < d.c_hi ? 1 : 0);
-    return reinterpret_cast<const uint8_t *>(ws) + ((int64_t)slot * kPairRows + rr) * PB;
+    return reinterpret_cast<const uint8_t *>(ws) + ((int64_t)slot * kPairRows + rr) * kPartialBytes<false>;
   };
   float M = -INFINITY, L = 0.f;
   float acc[16];
@@ -1502,18 +1527,17 @@ __global__ void __launch_bounds__(256, 4) attn_tc2_combine_kernel(void *__restri
   for (int j = 0; j < 16; ++j) acc[j] = 0.f;
   for (int c0 = 0; c0 < nc; c0 += kCombBatch) {
     float2 ml[kCombBatch];
-    uint4 o[kCombBatch][OV];
+    uint4 o[kCombBatch][2];
 #pragma unroll
     for (int i = 0; i < kCombBatch; ++i) {
       if (c0 + i < nc) {
         const uint8_t *row = row_of(c_lo + c0 + i);
-        ml[i] = *reinterpret_cast<const float2 *>(row + PB - 16);
-#pragma unroll
-        for (int j = 0; j < OV; ++j) o[i][j] = *reinterpret_cast<const uint4 *>(row + d0 * (OV / 2) * 2 + 16 * j);
+        ml[i] = *reinterpret_cast<const float2 *>(row + kD * 2);
+        o[i][0] = *reinterpret_cast<const uint4 *>(row + d0 * 2);
+        o[i][1] = *reinterpret_cast<const uint4 *>(row + d0 * 2 + 16);
       } else {
         ml[i] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int j = 0; j < OV; ++j) o[i][j] = make_uint4(0, 0, 0, 0);
+        o[i][0] = o[i][1] = make_uint4(0, 0, 0, 0);
       }
     }
     float Mb = M;
@@ -1528,21 +1552,11 @@ __global__ void __launch_bounds__(256, 4) attn_tc2_combine_kernel(void *__restri
     for (int i = 0; i < kCombBatch; ++i) {
       const float f = c0 + i < nc ? exp2f(ml[i].x - Mb) : 0.f;
       L = fmaf(f, ml[i].y, L);
-      if constexpr (WIN) {
+      const uint32_t w[8] = {o[i][0].x, o[i][0].y, o[i][0].z, o[i][0].w, o[i][1].x, o[i][1].y, o[i][1].z, o[i][1].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[4 * j] = fmaf(f, __uint_as_float(o[i][j].x), acc[4 * j]);
-          acc[4 * j + 1] = fmaf(f, __uint_as_float(o[i][j].y), acc[4 * j + 1]);
-          acc[4 * j + 2] = fmaf(f, __uint_as_float(o[i][j].z), acc[4 * j + 2]);
-          acc[4 * j + 3] = fmaf(f, __uint_as_float(o[i][j].w), acc[4 * j + 3]);
-        }
-      } else {
-        const uint32_t w[8] = {o[i][0].x, o[i][0].y, o[i][0].z, o[i][0].w, o[i][1].x, o[i][1].y, o[i][1].z, o[i][1].w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          acc[2 * j] = fmaf(f, __uint_as_float(w[j] << 16), acc[2 * j]);
-          acc[2 * j + 1] = fmaf(f, __uint_as_float(w[j] & 0xFFFF0000u), acc[2 * j + 1]);
-        }
+      for (int j = 0; j < 8; ++j) {
+        acc[2 * j] = fmaf(f, __uint_as_float(w[j] << 16), acc[2 * j]);
+        acc[2 * j + 1] = fmaf(f, __uint_as_float(w[j] & 0xFFFF0000u), acc[2 * j + 1]);
       }
     }
     M = Mb;
@@ -1557,9 +1571,92 @@ __global__ void __launch_bounds__(256, 4) attn_tc2_combine_kernel(void *__restri
   v1.y = pack_bf16(acc[10] * inv, acc[11] * inv);
   v1.z = pack_bf16(acc[12] * inv, acc[13] * inv);
   v1.w = pack_bf16(acc[14] * inv, acc[15] * inv);
-  uint4 *dst = reinterpret_cast<uint4 *>(out + (((int64_t)d.b * s.n_nodes + rg / G) * Hq + kvh * heads + rg % G) * kD + d0);
+  uint4 *dst = reinterpret_cast<uint4 *>(out + (((int64_t)d.b * s.n_nodes + rg / G) * Hq + kvh * G + rg % G) * kD + d0);
   dst[0] = v0;
   dst[1] = v1;
+}
+
+// The same for window calls, whose partials are float32: thread = (row, 8 head
+// dims), 16 threads per row, block (x, y) rows [16 y, +16).  parts > 0: x is
+// the row group, whose contributors follow from its prefix length (an input
+// of the call: read before the wait); else boundary x + 1, as above.
+constexpr int kWinCombRows = 16;
+constexpr int kWinCombBatch = 4;
+__global__ void __launch_bounds__(256, 4)
+    attn_tc2_window_combine_kernel(void *__restrict__ ws, __nv_bfloat16 *__restrict__ out, const Sched<true> s,
+                                   int Hq) {
+  constexpr int PB = kPartialBytes<true>;
+  const int rr = blockIdx.y * kWinCombRows + (threadIdx.x >> 4);  // row of the pair
+  const int d0 = (threadIdx.x & 15) * 8;                          // first head dim
+  int b, gi, c_lo, c_hi;
+  if (s.parts > 0) {
+    b = blockIdx.x / s.gpb();
+    gi = blockIdx.x % s.gpb();
+    const int k = part_count(s.parts, tiles_of(s, s.prefix_len[b]));
+    if (k == 1) return;  // written by its cluster
+    c_lo = blockIdx.x * s.parts;
+    c_hi = c_lo + k - 1;
+    grid_dep_wait();  // the main kernel's partials are written and visible
+  } else {
+    grid_dep_wait();
+    const CutDesc d = cut_descs<true>(ws, s.n_clusters)[blockIdx.x + 1];
+    if (!d.usable) return;
+    b = d.b;
+    gi = d.gi;
+    c_lo = blockIdx.x;
+    c_hi = d.c_hi;
+  }
+  const int heads = Hq / s.hkv, R = s.n_nodes * s.gp;
+  const int kvh = gi / s.pairs;
+  const int row = (gi % s.pairs) * kPairRows + rr;
+  if (row >= R || row % s.gp >= heads) return;
+  const int nc = c_hi - c_lo + 1;
+  float M = kUnseen, L = 0.f;
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+  for (int c0 = 0; c0 < nc; c0 += kWinCombBatch) {
+    float2 ml[kWinCombBatch];
+    float4 o[kWinCombBatch][2];
+#pragma unroll
+    for (int i = 0; i < kWinCombBatch; ++i) {
+      const int c = c_lo + c0 + i;
+      if (c <= c_hi) {
+        // cluster c's part: slot 2c + 1 when cut at its range end (all but the last)
+        const uint8_t *p =
+            reinterpret_cast<const uint8_t *>(ws) + ((int64_t)(2 * c + (c < c_hi ? 1 : 0)) * kPairRows + rr) * PB;
+        ml[i] = *reinterpret_cast<const float2 *>(p + PB - 16);
+        o[i][0] = *reinterpret_cast<const float4 *>(p + d0 * 4);
+        o[i][1] = *reinterpret_cast<const float4 *>(p + d0 * 4 + 16);
+      } else {
+        ml[i] = make_float2(kUnseen, 0.f);
+        o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    float Mb = M;
+#pragma unroll
+    for (int i = 0; i < kWinCombBatch; ++i) Mb = fmaxf(Mb, ml[i].x);
+    const float r = exp2f(M - Mb);
+    L *= r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] *= r;
+#pragma unroll
+    for (int i = 0; i < kWinCombBatch; ++i) {
+      const float f = exp2f(ml[i].x - Mb);  // (1 where no part has seen a key: its sum and O are 0)
+      L = fmaf(f, ml[i].y, L);
+      const float v[8] = {o[i][0].x, o[i][0].y, o[i][0].z, o[i][0].w, o[i][1].x, o[i][1].y, o[i][1].z, o[i][1].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = fmaf(f, v[j], acc[j]);
+    }
+    M = Mb;
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  uint4 v;
+  v.x = pack_bf16(acc[0] * inv, acc[1] * inv);
+  v.y = pack_bf16(acc[2] * inv, acc[3] * inv);
+  v.z = pack_bf16(acc[4] * inv, acc[5] * inv);
+  v.w = pack_bf16(acc[6] * inv, acc[7] * inv);
+  *reinterpret_cast<uint4 *>(out + (((int64_t)b * s.n_nodes + row / s.gp) * Hq + kvh * heads + row % s.gp) * kD + d0) = v;
 }
 
 // Ancestor masks for a window shorter than the tree: drops the ancestors of a
@@ -1639,27 +1736,43 @@ int tc2_clusters() {
   return clusters;
 }
 
-// Whether a window call keeps its row groups whole.  In tiles of 128 keys
-// (about 0.85 us each), a row group weighing its tiles and kSegW: cut in equal
-// ranges (of a tree tile's weight at least), a cluster takes the average, and
-// the range lookup, the partials and the merge cost kMergeTiles more; kept
-// whole, the busiest cluster takes its number of row groups, each at the
-// longest a prefix may be.  Measured cut / whole, 4 heads per KV head, 32
-// nodes, paged, by row groups and window: 8, 1024: 16.3 / 15.6 us; 8, 2048:
-// 17.2 / 21.7; 32, 2048: 27.0 / 22.1; 80, 1024: 28.7 / 27.5; 80, 2048: 35.4 /
-// 39.5; 128, 2048: 49.7 / 43.5; 128, 4096: 70.9 / 68.9; 240, 2048: 75.1 /
-// 77.6.  The rule takes the faster side of each.
-constexpr int kMergeTiles = 13;
-bool tc2_whole(const SvAttnShape &s, const Sched<true> &sc, int clusters) {
+// How the row groups of a window call meet the clusters.  In tiles of 128 keys
+// (about 0.8 us each), a row group weighing its tiles and kSegW, at the longest
+// a prefix may be:
+//   whole  the busiest cluster's number of row groups; no merge is launched
+//   parts  (half the clusters' row groups or fewer) one part, and a merge of
+//          kPartTiles
+//   ranges the average (a tree tile's weight at least), and kMergeTiles for
+//          the range lookup, two partials a cluster and the merge
+// Measured whole / parts, 4 heads per KV head, 32 nodes, paged, by row groups
+// and window, us: 8, 1024: 16.0 / 15.6; 8, 2048: 21.9 / 14.9; 16, 4096: 34.4 /
+// 21.5 (ranges 24.7); 32, 1024: 16.7 / 17.7; 32, 2048: 22.8 / 20.8 (25.8); 32,
+// 8192: 62.4 / 43.6 (45.5).  Whole / ranges: 40, 1024: 16.4 / 23.9; 64, 8192:
+// 64.0 / 67.0; 80, 1024: 27.9 / 27.6; 80, 2048: 40.5 / 34.5; 128, 2048: 44.8 /
+// 49.1; 128, 8192: 119 / 114; 512, 256: 63.5 / 70.9; 512, 1024: 86.4 / 90.5.
+constexpr int kPartTiles = 8;
+constexpr int kMergeTiles = 12;
+void tc2_share(const SvAttnShape &s, Sched<true> &sc, int clusters) {
   const long long span = (long long)sc.win.window - 1 + (s.block_table ? kBN - 1 : 0);
   const long long keys = span < s.max_prefix ? span : s.max_prefix;
   const long long most_sinks = sc.win.sinks < s.max_prefix ? sc.win.sinks : s.max_prefix;
   const long long sinks = s.n_nodes <= kFold && sc.win.sinks <= kFold ? 0 : most_sinks;
   const int nt = (s.n_nodes + kBN - 1) / kBN;
-  const long long n = nt + kSegW + (keys + kBN - 1) / kBN + (sinks + kBN - 1) / kBN;
+  const long long tiles = nt + (keys + kBN - 1) / kBN + (sinks + kBN - 1) / kBN, n = tiles + kSegW;
   const long long rgs = (long long)s.batch * s.hkv * ((s.n_nodes * sc.gp + kPairRows - 1) / kPairRows);
-  const long long mean = rgs * n / clusters > nt + kSegW ? rgs * n / clusters : nt + kSegW;
-  return (rgs + clusters - 1) / clusters * n <= mean + kMergeTiles;
+  const long long whole = (rgs + clusters - 1) / clusters * n;
+  sc.whole = sc.parts = 0;
+  if (2 * rgs <= clusters) {
+    const int most = (int)(clusters / rgs);
+    const long long k = tiles / 4 < most ? (tiles / 4 > 1 ? tiles / 4 : 1) : most;  // (part_count of the longest)
+    if (whole <= n / k + kPartTiles)
+      sc.whole = 1;
+    else
+      sc.parts = most;
+  } else {
+    const long long mean = rgs * n / clusters > nt + kSegW ? rgs * n / clusters : nt + kSegW;
+    sc.whole = whole <= mean + kMergeTiles;
+  }
 }
 
 // Sets an instance's shared-memory size, once per device.
@@ -1762,9 +1875,15 @@ int tc2_run(const SvAttnShape &s, Sched<WIN> &sc, int rows_g, const void *q, con
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_tc2_combine_kernel<WIN>, ws, (__nv_bfloat16 *)out, sc, s.hq) !=
-        cudaSuccess)
-      return SPEC_ERR_CUDA;
+    cudaError_t e;
+    if constexpr (WIN) {
+      const int rows = R < kPairRows ? R : kPairRows;
+      cfg.gridDim = dim3(sc.parts > 0 ? s.batch * s.hkv * sc.pairs : C - 1, (rows + kWinCombRows - 1) / kWinCombRows);
+      e = cudaLaunchKernelEx(&cfg, attn_tc2_window_combine_kernel, ws, (__nv_bfloat16 *)out, sc, s.hq);
+    } else {
+      e = cudaLaunchKernelEx(&cfg, attn_tc2_combine_kernel, ws, (__nv_bfloat16 *)out, sc, s.hq);
+    }
+    if (e != cudaSuccess) return SPEC_ERR_CUDA;
   }
   return sv_launch_status();
 }
@@ -1818,7 +1937,7 @@ int sv_attn_tc2_window(const SvAttnShape &s, const void *q, const void *kc, cons
   constexpr int kAll = (1 << 30) + SPEC_MAX_NODES;
   sc.win = sv::Window{s.depth, s.window < kAll ? s.window : kAll, s.sinks < kAll ? s.sinks : kAll};
   sc.gp = pow2_at_least(s.hq / s.hkv);
-  sc.whole = tc2_whole(s, sc, c);
+  tc2_share(s, sc, c);
   if (s.window < s.n_nodes) {
     uint64_t *masks = reinterpret_cast<uint64_t *>(static_cast<uint8_t *>(ws) + window_masks_at(c));
     window_mask_kernel<<<s.batch, 256, 0, stream>>>(anc, prefix_len, sc.win, s.n_nodes, masks);
