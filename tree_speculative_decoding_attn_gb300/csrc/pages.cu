@@ -496,9 +496,13 @@ __global__ void __launch_bounds__(kThreads)
 // Copies the planned rows of every layer and KV head, K and V, 16 bytes a
 // thread and load; REMAP: also renames the table's entries.  A unit is up to
 // kPiece vectors of one (move, K or V, layer, head); the CTAs take them in
-// turn.
+// turn.  Measured with the plan, eight loads in flight, streaming accesses and
+// up to sixteen CTAs a SM against four loads, plain accesses and eight: a
+// compaction that reads and writes 0.73 GB 113 us (6.5 TB/s, 0.96 of a plain
+// copy's rate) against 121, a reservation whose copies are 0.11 GB 20.6
+// against 23.4.
 constexpr int kCopyThreads = 256;
-constexpr int kInFlight = 4;
+constexpr int kInFlight = 8;
 constexpr int kPiece = kCopyThreads * kInFlight;
 template <bool REMAP>
 __global__ void __launch_bounds__(kCopyThreads)
@@ -528,10 +532,10 @@ __global__ void __launch_bounds__(kCopyThreads)
     uint4 r[kInFlight];
 #pragma unroll
     for (int j = 0; j < kInFlight; ++j)
-      if (i0 + j * kCopyThreads < n) r[j] = src[i0 + j * kCopyThreads];
+      if (i0 + j * kCopyThreads < n) r[j] = __ldcs(src + i0 + j * kCopyThreads);
 #pragma unroll
     for (int j = 0; j < kInFlight; ++j)
-      if (i0 + j * kCopyThreads < n) dst[i0 + j * kCopyThreads] = r[j];
+      if (i0 + j * kCopyThreads < n) __stcs(dst + i0 + j * kCopyThreads, r[j]);
   }
   if constexpr (REMAP) {
     for (int64_t e = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; e < n_entries;
@@ -557,7 +561,7 @@ int launch_copy(void *k, void *v, int n_layers, int hkv, int block_size, int num
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units < 1 ? 1 : units > 152 * 8 ? 152 * 8 : units));
+  cfg.gridDim = dim3((unsigned)(units < 1 ? 1 : units > 152 * 16 ? 152 * 16 : units));
   cfg.blockDim = dim3(kCopyThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
