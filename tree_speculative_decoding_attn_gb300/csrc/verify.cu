@@ -22,9 +22,17 @@
 // real one, where float32 sums would move the border of every token by up to
 // 2^-24.  The tests of single drafts use float64 (one thread, a few products).
 //
-// What bounds it: nothing but latency at batch 1 (two dependent gathers, the
-// walk in shared memory, one row, one cluster exchange), the rows' bytes at
-// large batch.  One cluster per sequence; each warp owns one contiguous piece
+// What bounds it: latency.  One sequence of a six-node chain over 32000 tokens
+// takes 7.0 us (two dependent gathers 1.3, the walk in shared memory 0.6, its
+// row 1.2, the exchange 0.6, the bonus 1.1, the launch the rest); 64 trees of
+// 32 nodes over 128256 bf16 tokens 15 us (16.8 MB, 1.1 TB/s: the two dependent
+// gathers then miss the TLB, 2.6, and the rows' integer sums, ten 32-bit
+// operations a value, take 3 to 6 where a SM holds two CTAs); eight trees of
+// 60 nodes whose siblings a drafter drew 21.5 (a rejected sibling costs 4 us:
+// its row pair 2.5, the exchange 0.6, the next test 0.8).  Kept: all the tests
+// that need no row at once, one thread a child (serial float64 tests cost 0.9
+// each); the whole CTA on the piece that holds the bonus (its own warp alone
+// took up to 20).  One cluster per sequence; each warp owns one contiguous piece
 // of the row, so the bonus is found from the per-warp sums by rereading one
 // warp's piece (a few KB, in L2), a vector a thread.
 #include <type_traits>
@@ -509,10 +517,18 @@ int launch_verify(const void *p, const void *q, int batch, int N, int V, const i
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, (const T *)p, (const T *)q, N, V, tok, parents, first_child, next_sibling,
-                            u_accept, u_bonus, path_cap, acc_len, acc_path, bonus, status) == cudaSuccess
-             ? SPEC_OK
-             : SPEC_ERR_CUDA;
+  auto launch = [&]() {
+    return cudaLaunchKernelEx(&cfg, kern, (const T *)p, (const T *)q, N, V, tok, parents, first_child, next_sibling,
+                              u_accept, u_bonus, path_cap, acc_len, acc_path, bonus, status);
+  };
+  cudaError_t e = launch();
+  if (e == cudaErrorInvalidClusterSize && nc > 8) {
+    (void)cudaGetLastError();
+    attr[0].val.clusterDim.x = 8;
+    cfg.gridDim = dim3(8, batch);
+    e = launch();
+  }
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // namespace
