@@ -109,6 +109,9 @@ CASES = [
     ("f32", 2, 6, 2, 128, [300, 0], R(2, 20, (4, 3, 2)), 128, 0, 128),
     ("f32", 2, 4, 1, 64, [90, 257], R(3, 70, (6, 5, 4)), 3, 1, 0),          # a window shorter than the tree is deep
     ("bf16", 2, 8, 2, 64, [500, 33], R(4, 12, (3, 3)), 100, 70, 0),
+    ("bf16", 3, 24, 4, 64, [900, 4, 2000], R(18, 100, (6, 5, 3)), 700, 130, 128),  # head_dim 64, two mask words, ranges
+    ("bf16", 1, 4, 4, 64, [5000], R(19, 200, (8, 6, 4, 3)), 3000, 30, 0),   # ... parts, two tree tiles
+    ("bf16", 9, 32, 8, 64, [(211 * i) % 1500 for i in range(9)], synth.chain(1), 300, 4, 128),
     ("bf16", 1, 32, 8, 128, [2000], synth.chain(1), 1024, 4, 0),            # one token
     ("bf16", 3, 8, 8, 128, [1, 0, 700], synth.chain(1), 256, 0, 128),
     ("bf16", 4, 32, 8, 128, [900, 128, 4, 1500], R(5, 60, (10, 4, 3, 2, 2)), 512, 4, 128),
@@ -137,7 +140,7 @@ def test_window_matches_the_oracle(case):
     c.check(t)
 
 
-@pytest.mark.parametrize("case", [3, 6, 7, 8, 10, 11])
+@pytest.mark.parametrize("case", [3, 4, 5, 9, 10, 11, 13, 14])
 def test_peaky_scores(case):
     c = Case(*CASES[case], q_scale=4.0, seed=100 + case)
     t = c.tensors()
@@ -145,7 +148,7 @@ def test_peaky_scores(case):
     c.check(t)
 
 
-@pytest.mark.parametrize("case", [0, 3, 4, 7, 8, 9, 11])
+@pytest.mark.parametrize("case", [0, 3, 4, 6, 7, 10, 11, 12, 14])
 @pytest.mark.parametrize("fill", [float("nan"), float("inf"), -3e38])
 def test_rows_nobody_sees_may_hold_anything(case, fill):
     c = Case(*CASES[case], seed=200 + case, fill=(fill, fill))

@@ -146,6 +146,13 @@ struct SchedBase {
 // (keys 64 .. 64 + fold - 1 of the tile) instead of filling a tile of their
 // own: one tile less per row group, and half the bytes.
 //
+// head_dim 64 (hd) runs as the lower half of 128: the tensor maps end at dim
+// 64, so the upper halves of Q, K and V read as zeros without touching memory,
+// and O's upper columns are not stored.  Half of its MMAs are for nothing, but
+// the softmax sets the tile rate: 124 us at 64 x 64/8 heads, 32 nodes, window
+// 2048 (128 dims 131 us; CUDA cores some 3500).  Not loading those halves took
+// branches in the load warps, and 128 dims 2 to 8 % more time.
+//
 // The host (tc2_share) picks how row groups meet clusters: whole, never cut,
 // each cluster an equal number of them and nothing to merge; or parts > 0,
 // each cut alike into that many parts, one a cluster; or, with neither, the
@@ -157,7 +164,7 @@ template <>
 struct Sched<true> : SchedBase {
   sv::Window win;
   int gp;
-  int whole, parts;
+  int whole, parts, hd;
   __device__ sv::WinSpan span(int P) const {
     sv::WinSpan v = sv::win_span(win.window, win.sinks, P, kBN, pg.table ? kBN : 1);
     if (n_nodes <= kFold && v.s_end <= kFold) {
@@ -533,6 +540,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return Hq / s.hkv;
   }();
   const int R = N * G;
+  int head_dim = kD;
+  if constexpr (WIN) head_dim = s.hd;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cluster = blockIdx.x >> 1;
@@ -1461,7 +1470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (live && complete && c.ok && node0 < N) {  // (a CTA past the last node has no rows to write)
             const int kvh = c.gi / pairs;
             tma_store_5d(&tm_o, stage, 0, 0, kvh, node0, c.b);
-            tma_store_5d(&tm_o, stage + kQHalf, 64, 0, kvh, node0, c.b);
+            if (!WIN || head_dim > 64) tma_store_5d(&tm_o, stage + kQHalf, 64, 0, kvh, node0, c.b);
             bulk_commit();
             q_pending = qb + 1;  // Q buffer released once the store has read it
           } else {
@@ -1609,7 +1618,7 @@ __global__ void __launch_bounds__(256, 4)
   const int heads = Hq / s.hkv, R = s.n_nodes * s.gp;
   const int kvh = gi / s.pairs;
   const int row = (gi % s.pairs) * kPairRows + rr;
-  if (row >= R || row % s.gp >= heads) return;
+  if (row >= R || row % s.gp >= heads || d0 >= s.hd) return;
   const int nc = c_hi - c_lo + 1;
   float M = kUnseen, L = 0.f;
   float acc[8];
@@ -1656,7 +1665,8 @@ __global__ void __launch_bounds__(256, 4)
   v.y = pack_bf16(acc[2] * inv, acc[3] * inv);
   v.z = pack_bf16(acc[4] * inv, acc[5] * inv);
   v.w = pack_bf16(acc[6] * inv, acc[7] * inv);
-  *reinterpret_cast<uint4 *>(out + (((int64_t)b * s.n_nodes + row / s.gp) * Hq + kvh * heads + row % s.gp) * kD + d0) = v;
+  const int64_t head = ((int64_t)b * s.n_nodes + row / s.gp) * Hq + kvh * heads + row % s.gp;
+  *reinterpret_cast<uint4 *>(out + head * s.hd + d0) = v;
 }
 
 // Ancestor masks for a window shorter than the tree: drops the ancestors of a
@@ -1803,11 +1813,11 @@ int tc2_run(const SvAttnShape &s, Sched<WIN> &sc, int rows_g, const void *q, con
             void *ws, int32_t *status, cudaStream_t stream) {
   const int C = tc2_clusters();
   if (C < 1) return SPEC_ERR_CUDA;
-  const int G = s.hq / s.hkv, R = s.n_nodes * rows_g;
+  const int G = s.hq / s.hkv, R = s.n_nodes * rows_g, D = s.head_dim;
   CUtensorMap mq, mkc, mvc, mkt, mvt, mo;
   {
-    const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)G, (cuuint64_t)s.hkv, (cuuint64_t)s.batch * s.n_nodes};
-    const cuuint64_t strides[3] = {(cuuint64_t)kD * 2, (cuuint64_t)G * kD * 2, (cuuint64_t)s.hq * kD * 2};
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)G, (cuuint64_t)s.hkv, (cuuint64_t)s.batch * s.n_nodes};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)G * D * 2, (cuuint64_t)s.hq * D * 2};
     const cuuint32_t box[4] = {64, (cuuint32_t)rows_g, 1, (cuuint32_t)(128 / rows_g)};
     if (make_map(&mq, q, 4, dims, strides, box) != SPEC_OK) return SPEC_ERR_CUDA;
   }
@@ -1815,10 +1825,10 @@ int tc2_run(const SvAttnShape &s, Sched<WIN> &sc, int rows_g, const void *q, con
     // output rows of a CTA: 128 / rows_g nodes x the G heads of a KV head;
     // nodes past the sequence's last, and rows past the last head, are outside
     // the map and not written
-    const cuuint64_t dims[5] = {(cuuint64_t)kD, (cuuint64_t)G, (cuuint64_t)s.hkv, (cuuint64_t)s.n_nodes,
+    const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)G, (cuuint64_t)s.hkv, (cuuint64_t)s.n_nodes,
                                 (cuuint64_t)s.batch};
-    const cuuint64_t strides[4] = {(cuuint64_t)kD * 2, (cuuint64_t)G * kD * 2, (cuuint64_t)s.hq * kD * 2,
-                                   (cuuint64_t)s.n_nodes * s.hq * kD * 2};
+    const cuuint64_t strides[4] = {(cuuint64_t)D * 2, (cuuint64_t)G * D * 2, (cuuint64_t)s.hq * D * 2,
+                                   (cuuint64_t)s.n_nodes * s.hq * D * 2};
     const cuuint32_t box[5] = {64, (cuuint32_t)rows_g, 1, (cuuint32_t)(128 / rows_g), 1};
     if (make_map(&mo, out, 5, dims, strides, box) != SPEC_OK) return SPEC_ERR_CUDA;
   }
@@ -1827,15 +1837,15 @@ int tc2_run(const SvAttnShape &s, Sched<WIN> &sc, int rows_g, const void *q, con
     // loaded; a paged cache is one pool of blocks)
     const cuuint64_t rows = s.block_table ? (cuuint64_t)s.num_blocks * s.hkv * s.block_size
                                           : (cuuint64_t)s.batch * s.hkv * s.s_max;
-    const cuuint64_t dims[2] = {(cuuint64_t)kD, rows > 0 ? rows : 1};
-    const cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
+    const cuuint64_t dims[2] = {(cuuint64_t)D, rows > 0 ? rows : 1};
+    const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
     const cuuint32_t kbox[2] = {64, 64}, vbox[2] = {64, (cuuint32_t)(WIN ? kFold : kBN)};
     if (make_map(&mkc, kc, 2, dims, strides, kbox) != SPEC_OK) return SPEC_ERR_CUDA;
     if (make_map(&mvc, vc, 2, dims, strides, vbox) != SPEC_OK) return SPEC_ERR_CUDA;
   }
   {
-    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)s.batch * s.hkv * s.n_nodes};
-    const cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)s.batch * s.hkv * s.n_nodes};
+    const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
     const cuuint32_t kbox[2] = {64, 64}, vbox[2] = {64, (cuuint32_t)(WIN ? kFold : kBN)};
     if (make_map(&mkt, kt, 2, dims, strides, kbox) != SPEC_OK) return SPEC_ERR_CUDA;
     if (make_map(&mvt, vt, 2, dims, strides, vbox) != SPEC_OK) return SPEC_ERR_CUDA;
@@ -1910,7 +1920,7 @@ int sv_attn_tc2(const SvAttnShape &s, const void *q, const void *kc, const void 
 }
 
 bool sv_attn_tc2_window_supported(const SvAttnShape &s) {
-  return s.window > 0 && s.dtype == SPEC_BF16 && s.head_dim == kD && s.hkv >= 1 && s.hq / s.hkv <= 128 &&
+  return s.window > 0 && s.dtype == SPEC_BF16 && s.hkv >= 1 && s.hq / s.hkv <= 128 &&
          s.n_nodes <= SPEC_MAX_NODES;
 }
 
@@ -1937,6 +1947,7 @@ int sv_attn_tc2_window(const SvAttnShape &s, const void *q, const void *kc, cons
   constexpr int kAll = (1 << 30) + SPEC_MAX_NODES;
   sc.win = sv::Window{s.depth, s.window < kAll ? s.window : kAll, s.sinks < kAll ? s.sinks : kAll};
   sc.gp = pow2_at_least(s.hq / s.hkv);
+  sc.hd = s.head_dim;
   tc2_share(s, sc, c);
   if (s.window < s.n_nodes) {
     uint64_t *masks = reinterpret_cast<uint64_t *>(static_cast<uint8_t *>(ws) + window_masks_at(c));
