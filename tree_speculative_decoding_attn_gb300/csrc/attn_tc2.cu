@@ -150,7 +150,7 @@ struct SchedBase {
 // 64, so the upper halves of Q, K and V read as zeros without touching memory,
 // and O's upper columns are not stored.  Half of its MMAs are for nothing, but
 // the softmax sets the tile rate: 124 us at 64 x 64/8 heads, 32 nodes, window
-// 2048 (128 dims 131 us; CUDA cores some 3500).  Not loading those halves took
+// 2048 (128 dims 131 us; on CUDA cores 3975).  Not loading those halves took
 // branches in the load warps, and 128 dims 2 to 8 % more time.
 //
 // The host (tc2_share) picks how row groups meet clusters: whole, never cut,
