@@ -805,68 +805,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           return true;
         });
       } else {
-      Cur<WIN> c = cur_begin(bars, s);
-      int seg = 0;
-      Cur<WIN> cpf = c;  // kPrefetch tiles ahead of c
-      for (int i = 0; i < kPrefetch && i < T; ++i) cur_next(cpf, s);
-      for (int g = 0; g < T; ++g) {
-        const bool first = g == 0 || c.t == 0;
-        if (first && g > 0) ++seg;
-        const int kvh = c.gi / pairs, pair = c.gi % pairs;
-        const int bh = c.b * s.hkv + kvh;
-        if (kPrefetch > 0 && g + kPrefetch < T) {
-          // warm L2 with this CTA's half of tile g + kPrefetch
-          const int pbh = cpf.b * s.hkv + cpf.gi / pairs;
-          const bool ptree = cpf.t < s.nt;
-          const int prow = ptree ? pbh * N + cpf.t * kBN
-                                 : sv::kv_row(s.pg, cpf.b, s.hkv, cpf.gi / pairs, s.s_max, (cpf.t - s.nt) * kBN, nullptr);
-          if (is_v) {
-            tma_prefetch_2d(ptree ? &tm_vt : &tm_vc, 64 * (int)rank, prow);
-          } else {
-            tma_prefetch_2d(ptree ? &tm_kt : &tm_kc, 0, prow + 64 * (int)rank);
-            tma_prefetch_2d(ptree ? &tm_kt : &tm_kc, 64, prow + 64 * (int)rank);
+        Cur<WIN> c = cur_begin(bars, s);
+        int seg = 0;
+        Cur<WIN> cpf = c;  // kPrefetch tiles ahead of c
+        for (int i = 0; i < kPrefetch && i < T; ++i) cur_next(cpf, s);
+        for (int g = 0; g < T; ++g) {
+          const bool first = g == 0 || c.t == 0;
+          if (first && g > 0) ++seg;
+          const int kvh = c.gi / pairs, pair = c.gi % pairs;
+          const int bh = c.b * s.hkv + kvh;
+          if (kPrefetch > 0 && g + kPrefetch < T) {
+            // warm L2 with this CTA's half of tile g + kPrefetch
+            const int pbh = cpf.b * s.hkv + cpf.gi / pairs;
+            const bool ptree = cpf.t < s.nt;
+            const int prow = ptree ? pbh * N + cpf.t * kBN
+                                   : sv::kv_row(s.pg, cpf.b, s.hkv, cpf.gi / pairs, s.s_max, (cpf.t - s.nt) * kBN, nullptr);
+            if (is_v) {
+              tma_prefetch_2d(ptree ? &tm_vt : &tm_vc, 64 * (int)rank, prow);
+            } else {
+              tma_prefetch_2d(ptree ? &tm_kt : &tm_kc, 0, prow + 64 * (int)rank);
+              tma_prefetch_2d(ptree ? &tm_kt : &tm_kc, 64, prow + 64 * (int)rank);
+            }
+            cur_next(cpf, s);
           }
-          cur_next(cpf, s);
-        }
-        if (!is_v && first) {
-          const int qb = seg % kQB;
-          // (a buffer's first use needs no wait: a completed-phase poll still costs a few hundred cycles)
-          if ((seg >= kQB && !mbar_wait_cluster(&bars->qempty[qb], ((seg / kQB) & 1) ^ 1, kWaitLimit)) || bars->abort) {
+          if (!is_v && first) {
+            const int qb = seg % kQB;
+            // (a buffer's first use needs no wait: a completed-phase poll still costs a few hundred cycles)
+            if ((seg >= kQB && !mbar_wait_cluster(&bars->qempty[qb], ((seg / kQB) & 1) ^ 1, kWaitLimit)) || bars->abort) {
+              give_up(bars, status);
+              break;
+            }
+            uint64_t *qbar = rank == 0 ? &bars->qfull[qb] : &bars->qland[qb];
+            mbar_expect_tx(qbar, kQBytes);
+            const int node0 = c.b * N + (pair * kPairRows + (int)rank * 128) / G;
+            tma_load_4d(sQ + qb * kQBytes, &tm_q, 0, 0, kvh, node0, qbar);
+            tma_load_4d(sQ + qb * kQBytes + kQHalf, &tm_q, 64, 0, kvh, node0, qbar);
+            ++q_issued;
+          }
+          const int st = g % (is_v ? kVS : kKS);
+          const int use = g / (is_v ? kVS : kKS);
+          uint64_t *empty = is_v ? &bars->vempty[st] : &bars->kempty[st];
+          uint64_t *land = is_v ? &bars->vland[st] : (rank == 0 ? &bars->kfull[st] : &bars->kland[st]);
+          if ((use > 0 && !mbar_wait_cluster(empty, (use & 1) ^ 1, kWaitLimit)) || bars->abort) {
             give_up(bars, status);
             break;
           }
-          uint64_t *qbar = rank == 0 ? &bars->qfull[qb] : &bars->qland[qb];
-          mbar_expect_tx(qbar, kQBytes);
-          const int node0 = c.b * N + (pair * kPairRows + (int)rank * 128) / G;
-          tma_load_4d(sQ + qb * kQBytes, &tm_q, 0, 0, kvh, node0, qbar);
-          tma_load_4d(sQ + qb * kQBytes + kQHalf, &tm_q, 64, 0, kvh, node0, qbar);
-          ++q_issued;
+          const bool tree = c.t < s.nt;
+          // (a 128-key tile lies inside one cache block: block sizes are
+          // multiples of 128; a bad block id gives row -1, read as zeros)
+          const int row0 =
+              tree ? bh * N + c.t * kBN : sv::kv_row(s.pg, c.b, s.hkv, kvh, s.s_max, (c.t - s.nt) * kBN, status);
+          if (is_v) {
+            mbar_expect_tx(land, kVBytes);
+            tma_load_2d(sV + st * kVBytes, tree ? &tm_vt : &tm_vc, 64 * (int)rank, row0, land);
+          } else {
+            mbar_expect_tx(land, kKBytes);
+            const CUtensorMap *m = tree ? &tm_kt : &tm_kc;
+            tma_load_2d(sK + st * kKBytes, m, 0, row0 + 64 * (int)rank, land);
+            tma_load_2d(sK + st * kKBytes + kKHalf, m, 64, row0 + 64 * (int)rank, land);
+          }
+          ++issued;
+          cur_next(c, s);
         }
-        const int st = g % (is_v ? kVS : kKS);
-        const int use = g / (is_v ? kVS : kKS);
-        uint64_t *empty = is_v ? &bars->vempty[st] : &bars->kempty[st];
-        uint64_t *land = is_v ? &bars->vland[st] : (rank == 0 ? &bars->kfull[st] : &bars->kland[st]);
-        if ((use > 0 && !mbar_wait_cluster(empty, (use & 1) ^ 1, kWaitLimit)) || bars->abort) {
-          give_up(bars, status);
-          break;
-        }
-        const bool tree = c.t < s.nt;
-        // (a 128-key tile lies inside one cache block: block sizes are
-        // multiples of 128; a bad block id gives row -1, read as zeros)
-        const int row0 =
-            tree ? bh * N + c.t * kBN : sv::kv_row(s.pg, c.b, s.hkv, kvh, s.s_max, (c.t - s.nt) * kBN, status);
-        if (is_v) {
-          mbar_expect_tx(land, kVBytes);
-          tma_load_2d(sV + st * kVBytes, tree ? &tm_vt : &tm_vc, 64 * (int)rank, row0, land);
-        } else {
-          mbar_expect_tx(land, kKBytes);
-          const CUtensorMap *m = tree ? &tm_kt : &tm_kc;
-          tma_load_2d(sK + st * kKBytes, m, 0, row0 + 64 * (int)rank, land);
-          tma_load_2d(sK + st * kKBytes + kKHalf, m, 64, row0 + 64 * (int)rank, land);
-        }
-        ++issued;
-        cur_next(c, s);
-      }
       }
       if (bars->abort) {  // let the copies into this CTA land before it exits (bounded)
         // (a full barrier of the even CTA completes only with the odd CTA's
@@ -918,39 +918,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           return true;
         });
       } else {
-      Cur<WIN> cs = cur_begin(bars, s);
-      int seg_s = 0;
-      // S(g) = Q K(g)^T into S buffer g % kSB; called for g = 0, 1, 2, ...
-      // in order.  Descriptors are a base plus constant offsets (the start
-      // address field is the low 14 bits, in 16-byte units).
-      auto issue_s = [&](int g) -> bool {
-        const bool first = g == 0 || cs.t == 0;
-        if (first && g > 0) ++seg_s;
-        const int qb = seg_s % kQB, st = g % kKS;
-        if (first && !warp_wait(&bars->qfull[qb], (seg_s / kQB) & 1)) return false;
-        if (!warp_wait(&bars->kfull[st], (g / kKS) & 1)) return false;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t qd = smem_desc_sw128(qa + (uint32_t)qb * kQBytes, 16, 1024);
-          const uint64_t kd = smem_desc_sw128(ka + (uint32_t)st * kKBytes, 16, 1024);
-          const uint32_t d = tmem + (uint32_t)(g % kSB) * 128u;
+        Cur<WIN> cs = cur_begin(bars, s);
+        int seg_s = 0;
+        // S(g) = Q K(g)^T into S buffer g % kSB; called for g = 0, 1, 2, ...
+        // in order.  Descriptors are a base plus constant offsets (the start
+        // address field is the low 14 bits, in 16-byte units).
+        auto issue_s = [&](int g) -> bool {
+          const bool first = g == 0 || cs.t == 0;
+          if (first && g > 0) ++seg_s;
+          const int qb = seg_s % kQB, st = g % kKS;
+          if (first && !warp_wait(&bars->qfull[qb], (seg_s / kQB) & 1)) return false;
+          if (!warp_wait(&bars->kfull[st], (g / kKS) & 1)) return false;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t qd = smem_desc_sw128(qa + (uint32_t)qb * kQBytes, 16, 1024);
+            const uint64_t kd = smem_desc_sw128(ka + (uint32_t)st * kKBytes, 16, 1024);
+            const uint32_t d = tmem + (uint32_t)(g % kSB) * 128u;
 #pragma unroll
-          for (int kk = 0; kk < kD / 16; ++kk)
-            mma_ss_pair(d, qd + (uint64_t)(((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4),
-                        kd + (uint64_t)(((kk >> 2) * kKHalf + (kk & 3) * 32) >> 4), kIdescS, kk > 0);
-          mma_commit_pair_mc(&bars->sfull[g % kSB], kBoth);
-          mma_commit_pair_mc(&bars->kempty[st], kBoth);
-          if (g == T - 1 || cs.t == cs.n - 1) mma_commit_pair_mc(&bars->qempty[qb], kBoth);
+            for (int kk = 0; kk < kD / 16; ++kk)
+              mma_ss_pair(d, qd + (uint64_t)(((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4),
+                          kd + (uint64_t)(((kk >> 2) * kKHalf + (kk & 3) * 32) >> 4), kIdescS, kk > 0);
+            mma_commit_pair_mc(&bars->sfull[g % kSB], kBoth);
+            mma_commit_pair_mc(&bars->kempty[st], kBoth);
+            if (g == T - 1 || cs.t == cs.n - 1) mma_commit_pair_mc(&bars->qempty[qb], kBoth);
+          }
+          __syncwarp();
+          cur_next(cs, s);
+          return true;
+        };
+        for (int g = 0; ok && g < T; ++g) {
+          // S(g) overwrites the buffer whose P PV(g - kSB) read
+          if (g >= kSB && !(ok = warp_wait(&bars->ofull[g % kSB], ((g - kSB) / kSB) & 1))) break;
+          ok = issue_s(g);
         }
-        __syncwarp();
-        cur_next(cs, s);
-        return true;
-      };
-      for (int g = 0; ok && g < T; ++g) {
-        // S(g) overwrites the buffer whose P PV(g - kSB) read
-        if (g >= kSB && !(ok = warp_wait(&bars->ofull[g % kSB], ((g - kSB) / kSB) & 1))) break;
-        ok = issue_s(g);
-      }
       }
       if (!ok) give_up(bars, status);
       if (lane == 0) mma_commit_pair_mc(&bars->drain, kBoth);  // after every MMA issued above
@@ -976,27 +976,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         });
         if (!done) give_up(bars, status);
       } else {
-      Cur<WIN> c = cur_begin(bars, s);
-      int seg = 0;
-      for (int g = 0; g < T; ++g) {
-        const bool first = g == 0 || c.t == 0;
-        if (first && g > 0) ++seg;
-        if (first) {
-          const int qb = seg % kQB;
-          if (!warp_wait(&bars->qland[qb], (seg / kQB) & 1) || bars->abort) {
+        Cur<WIN> c = cur_begin(bars, s);
+        int seg = 0;
+        for (int g = 0; g < T; ++g) {
+          const bool first = g == 0 || c.t == 0;
+          if (first && g > 0) ++seg;
+          if (first) {
+            const int qb = seg % kQB;
+            if (!warp_wait(&bars->qland[qb], (seg / kQB) & 1) || bars->abort) {
+              give_up(bars, status);
+              break;
+            }
+            if (lane == 0) mbar_arrive_cluster(mapa_cluster(&bars->qfull[qb], 0));
+          }
+          const int st = g % kKS;
+          if (!warp_wait(&bars->kland[st], (g / kKS) & 1) || bars->abort) {
             give_up(bars, status);
             break;
           }
-          if (lane == 0) mbar_arrive_cluster(mapa_cluster(&bars->qfull[qb], 0));
+          if (lane == 0) mbar_arrive_cluster(mapa_cluster(&bars->kfull[st], 0));
+          cur_next(c, s);
         }
-        const int st = g % kKS;
-        if (!warp_wait(&bars->kland[st], (g / kKS) & 1) || bars->abort) {
-          give_up(bars, status);
-          break;
-        }
-        if (lane == 0) mbar_arrive_cluster(mapa_cluster(&bars->kfull[st], 0));
-        cur_next(c, s);
-      }
       }
       __syncwarp();
     }
@@ -1044,36 +1044,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           return true;
         });
       } else {
-      Cur<WIN> cp = cur_begin(bars, s);
-      for (int g = 0; ok && g < T; ++g) {
-        // O += P(g) V(g) once P of both CTAs is ready (which also covers both
-        // V halves of tile g)
-        const int nkeys = tile_keys(cp, s);
-        if (!(ok = warp_wait(&bars->pfull[g % kSB], (g / kSB) & 1) && v_ready(bars, sV, g, nkeys))) break;
-        tc_fence_after();
-        const bool first = g == 0 || cp.t == 0;
-        const int st = g % kVS;
-        const int ksteps = (nkeys + 15) >> 4;
-        if (lane == 0) {
-          const uint64_t vd = smem_desc_sw128(va + (uint32_t)st * kVBytes, kVBytes, 1024);
-          const uint32_t pbase = tmem + (uint32_t)(g % kSB) * 128u;  // P of keys [16kk, +16) at + 8kk
-          const uint32_t acc0 = first ? 0u : 1u;
-          if (ksteps == kBN / 16) {
+        Cur<WIN> cp = cur_begin(bars, s);
+        for (int g = 0; ok && g < T; ++g) {
+          // O += P(g) V(g) once P of both CTAs is ready (which also covers both
+          // V halves of tile g)
+          const int nkeys = tile_keys(cp, s);
+          if (!(ok = warp_wait(&bars->pfull[g % kSB], (g / kSB) & 1) && v_ready(bars, sV, g, nkeys))) break;
+          tc_fence_after();
+          const bool first = g == 0 || cp.t == 0;
+          const int st = g % kVS;
+          const int ksteps = (nkeys + 15) >> 4;
+          if (lane == 0) {
+            const uint64_t vd = smem_desc_sw128(va + (uint32_t)st * kVBytes, kVBytes, 1024);
+            const uint32_t pbase = tmem + (uint32_t)(g % kSB) * 128u;  // P of keys [16kk, +16) at + 8kk
+            const uint32_t acc0 = first ? 0u : 1u;
+            if (ksteps == kBN / 16) {
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)
-              mma_ts_pair(tmem + kColO, pbase + (uint32_t)kk * 8u, vd + (uint64_t)((kk * 2048) >> 4), kIdescPV,
-                          kk > 0 ? 1u : acc0);
-          } else {
-            for (int kk = 0; kk < ksteps; ++kk)
-              mma_ts_pair(tmem + kColO, pbase + (uint32_t)kk * 8u, vd + (uint64_t)((kk * 2048) >> 4), kIdescPV,
-                          kk > 0 ? 1u : acc0);
+              for (int kk = 0; kk < kBN / 16; ++kk)
+                mma_ts_pair(tmem + kColO, pbase + (uint32_t)kk * 8u, vd + (uint64_t)((kk * 2048) >> 4), kIdescPV,
+                            kk > 0 ? 1u : acc0);
+            } else {
+              for (int kk = 0; kk < ksteps; ++kk)
+                mma_ts_pair(tmem + kColO, pbase + (uint32_t)kk * 8u, vd + (uint64_t)((kk * 2048) >> 4), kIdescPV,
+                            kk > 0 ? 1u : acc0);
+            }
+            mma_commit_pair_mc(&bars->vempty[st], kBoth);
+            mma_commit_pair_mc(&bars->ofull[g % kSB], kBoth);
           }
-          mma_commit_pair_mc(&bars->vempty[st], kBoth);
-          mma_commit_pair_mc(&bars->ofull[g % kSB], kBoth);
+          __syncwarp();
+          cur_next(cp, s);
         }
-        __syncwarp();
-        cur_next(cp, s);
-      }
       }
       if (!ok) give_up(bars, status);
       if (lane == 0) mma_commit_pair_mc(&bars->drain, kBoth);  // after every MMA issued above
@@ -1102,16 +1102,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         });
         if (!done) give_up(bars, status);
       } else {
-      Cur<WIN> c = cur_begin(bars, s);
-      for (int g = 0; g < T; ++g) {
-        if (!warp_wait(&bars->sfull[g % kSB], (g / kSB) & 1) || !v_ready(bars, sV, g, tile_keys(c, s)) ||
-            bars->abort) {
-          give_up(bars, status);
-          break;
+        Cur<WIN> c = cur_begin(bars, s);
+        for (int g = 0; g < T; ++g) {
+          if (!warp_wait(&bars->sfull[g % kSB], (g / kSB) & 1) || !v_ready(bars, sV, g, tile_keys(c, s)) ||
+              bars->abort) {
+            give_up(bars, status);
+            break;
+          }
+          if (lane == 0) mbar_arrive_cluster(pfull_even0 + (uint32_t)(g % kSB) * (uint32_t)sizeof(uint64_t));
+          cur_next(c, s);
         }
-        if (lane == 0) mbar_arrive_cluster(pfull_even0 + (uint32_t)(g % kSB) * (uint32_t)sizeof(uint64_t));
-        cur_next(c, s);
-      }
       }
     }
   } else {
