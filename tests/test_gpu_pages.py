@@ -268,6 +268,8 @@ def test_wrapper_refuses():
         lambda: sv.kv_pages_fork(t, p, i32([0, 1]), r, t2[:1], torch.empty_like(p), r2),
         lambda: sv.kv_pages_free(t.long(), p, r, t2, r2, 4),
         lambda: sv.kv_pages_free(t, p[:1], r, t2, r2, 4),
+        lambda: sv.kv_pages_free(t, None, r, t2, r2, 4),
+        lambda: sv.kv_pages_free(t.cpu(), p, r, t2, r2, 4),
         lambda: sv.kv_pages_free(t, p, r, t2, r2, 0),
         lambda: sv.kv_pages_free(t, p, r, t2, r2, 4, window=-1),
         lambda: sv.kv_pages_reserve(k, v[:, :4], t, p, p, r, t2, r2),

@@ -120,26 +120,28 @@ def _p(t):
     return C.c_void_p(t.data_ptr())
 
 
-def _args(device):
-    """(ptr, index, stream) of one call: its device, which has to be the
-    current one, that device's current stream, and ptr(t, dtype, shape), the
-    device pointer of a tensor once it is checked: on that device,
-    contiguous, and of the dtype and shape the C entry point takes it for.
-    (A closure: a method call would cost twice as much, a dozen times.)"""
-    index = torch.cuda.current_device()
-    if device.type != "cuda" or device.index != index:
-        raise ValueError(f"tensors on {device}, but the current device is cuda:{index}")
+def _device(t):
+    """(index, stream) of a call by its first tensor: its device, which has to
+    be the current one, and that device's current stream."""
+    index = t.get_device()
+    if index < 0 or index != torch._C._cuda_getDevice():
+        raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return index, torch._C._cuda_getCurrentRawStream(index)
 
-    def ptr(t, dtype, shape):
+
+def _ptr(t, index, dtype, shape):
+    """Device pointer of a tensor once it is checked: on the call's device,
+    contiguous, and of the dtype and shape the C entry point takes it for."""
+    try:
         if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
             return t.data_ptr()
-        raise _refusal(t, index, dtype, shape)
-
-    return ptr, index, torch._C._cuda_getCurrentRawStream(index)
+    except AttributeError:
+        raise ValueError(f"expected a CUDA tensor, not {type(t).__name__}") from None
+    raise _refusal(t, index, dtype, shape)
 
 
 def _sized(t, index, dtype, numel=None):
-    """As ptr, for a tensor of any shape (of numel elements, if given)."""
+    """As _ptr, for a tensor of any shape (of numel elements, if given)."""
     if t.get_device() == index and t.is_contiguous() and t.dtype is dtype and numel in (None, t.numel()):
         return t.data_ptr()
     raise _refusal(t, index, dtype, (numel,))
@@ -375,14 +377,14 @@ def tree_attn_verify_window(q, k_cache, v_cache, k_tree, v_tree, prefix_len, dep
     code = _DT.get(q.dtype, -1)
     if workspace is None:
         workspace = _scratch(tree_attn_window_workspace_bytes(code, B, N, Hq, Hkv, D, max_prefix, window, sinks), q)
-    ptr, index, stream = _args(q.device)
+    i, stream = _device(q)
     dt, i32, kv, tree = q.dtype, torch.int32, (B, Hkv, S, D), (B, Hkv, N, D)
-    args = (ptr(q, dt, q.shape), ptr(k_cache, dt, kv), ptr(v_cache, dt, kv), ptr(k_tree, dt, tree),
-            ptr(v_tree, dt, tree), ptr(prefix_len, i32, (B,)), ptr(depth, i32, (B, N)),
-            _sized(anc_mask, index, torch.int64, B * N * mask_words(N)), ptr(out, dt, q.shape))
+    args = (_ptr(q, i, dt, q.shape), _ptr(k_cache, i, dt, kv), _ptr(v_cache, i, dt, kv), _ptr(k_tree, i, dt, tree),
+            _ptr(v_tree, i, dt, tree), _ptr(prefix_len, i, i32, (B,)), _ptr(depth, i, i32, (B, N)),
+            _sized(anc_mask, i, torch.int64, B * N * mask_words(N)), _ptr(out, i, dt, q.shape))
     _check("tree_attn_verify_window", load().tree_attn_verify_window(
         *args, code, B, N, Hq, Hkv, D, S, int(max_prefix), int(window), int(sinks), float(scale),
-        _sized(workspace, index, torch.uint8), workspace.numel(), _word(dev_status, index), stream))
+        _sized(workspace, i, torch.uint8), workspace.numel(), _word(dev_status, i), stream))
 
 
 def tree_attn_verify_window_paged(q, k_pages, v_pages, block_table, k_tree, v_tree, prefix_len, depth, anc_mask, out,
@@ -395,14 +397,15 @@ def tree_attn_verify_window_paged(q, k_pages, v_pages, block_table, k_tree, v_tr
     code = _DT.get(q.dtype, -1)
     if workspace is None:
         workspace = _scratch(tree_attn_window_workspace_bytes(code, B, N, Hq, Hkv, D, max_prefix, window, sinks), q)
-    ptr, index, stream = _args(q.device)
+    i, stream = _device(q)
     dt, i32, kv, tree = q.dtype, torch.int32, (nb, Hkv, bs, D), (B, Hkv, N, D)
-    args = (ptr(q, dt, q.shape), ptr(k_pages, dt, kv), ptr(v_pages, dt, kv), ptr(block_table, i32, (B, mb)), bs, nb, mb,
-            ptr(k_tree, dt, tree), ptr(v_tree, dt, tree), ptr(prefix_len, i32, (B,)), ptr(depth, i32, (B, N)),
-            _sized(anc_mask, index, torch.int64, B * N * mask_words(N)), ptr(out, dt, q.shape))
+    args = (_ptr(q, i, dt, q.shape), _ptr(k_pages, i, dt, kv), _ptr(v_pages, i, dt, kv),
+            _ptr(block_table, i, i32, (B, mb)), bs, nb, mb, _ptr(k_tree, i, dt, tree), _ptr(v_tree, i, dt, tree),
+            _ptr(prefix_len, i, i32, (B,)), _ptr(depth, i, i32, (B, N)),
+            _sized(anc_mask, i, torch.int64, B * N * mask_words(N)), _ptr(out, i, dt, q.shape))
     _check("tree_attn_verify_window_paged", load().tree_attn_verify_window_paged(
         *args, code, B, N, Hq, Hkv, D, int(max_prefix), int(window), int(sinks), float(scale),
-        _sized(workspace, index, torch.uint8), workspace.numel(), _word(dev_status, index), stream))
+        _sized(workspace, i, torch.uint8), workspace.numel(), _word(dev_status, i), stream))
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -528,13 +531,14 @@ def spec_verify_probs(target_probs, tok, parents, first_child, next_sibling, u_a
     where siblings are draws of the drafter.  Outputs as spec_accept."""
     B, N, V = target_probs.shape
     dt, i32, f32 = target_probs.dtype, torch.int32, torch.float32
-    ptr, index, stream = _args(target_probs.device)
+    i, stream = _device(target_probs)
     node, cap = (B, N), acc_path.shape[1]
     _check("spec_verify_probs", load().spec_verify_probs(
-        ptr(target_probs, dt, (B, N, V)), None if draft_probs is None else ptr(draft_probs, dt, (B, N, V)),
-        _DT.get(dt, -1), B, N, V, ptr(tok, i32, node), ptr(parents, i32, node), ptr(first_child, i32, node),
-        ptr(next_sibling, i32, node), ptr(u_accept, f32, node), ptr(u_bonus, f32, (B,)), cap,
-        ptr(acc_len, i32, (B,)), ptr(acc_path, i32, (B, cap)), ptr(bonus, i32, (B,)), _word(dev_status, index), stream))
+        _ptr(target_probs, i, dt, (B, N, V)), None if draft_probs is None else _ptr(draft_probs, i, dt, (B, N, V)),
+        _DT.get(dt, -1), B, N, V, _ptr(tok, i, i32, node), _ptr(parents, i, i32, node), _ptr(first_child, i, i32, node),
+        _ptr(next_sibling, i, i32, node), _ptr(u_accept, i, f32, node), _ptr(u_bonus, i, f32, (B,)), cap,
+        _ptr(acc_len, i, i32, (B,)), _ptr(acc_path, i, i32, (B, cap)), _ptr(bonus, i, i32, (B,)),
+        _word(dev_status, i), stream))
 
 
 def kv_pages_workspace_bytes(batch, max_blocks, num_blocks):
@@ -545,11 +549,12 @@ def kv_pages_fork(block_table, prefix_len, parent, ref_count, table_out, prefix_
     """Sequence i of the new batch continues sequence parent[i] (< 0: empty)."""
     B, mb = block_table.shape
     out, nb, i32 = parent.shape[0], ref_count.shape[0], torch.int32
-    ptr, index, stream = _args(block_table.device)
+    i, stream = _device(block_table)
     _check("kv_pages_fork", load().kv_pages_fork(
-        ptr(block_table, i32, (B, mb)), ptr(prefix_len, i32, (B,)), ptr(parent, i32, (out,)), B, out, mb, nb,
-        ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (out, mb)), ptr(prefix_len_out, i32, (out,)),
-        ptr(ref_out, i32, (nb,)), _word(dev_status, index), stream))
+        _ptr(block_table, i, i32, (B, mb)), _ptr(prefix_len, i, i32, (B,)), _ptr(parent, i, i32, (out,)), B, out,
+        mb, nb,
+        _ptr(ref_count, i, i32, (nb,)), _ptr(table_out, i, i32, (out, mb)), _ptr(prefix_len_out, i, i32, (out,)),
+        _ptr(ref_out, i, i32, (nb,)), _word(dev_status, i), stream))
 
 
 def kv_pages_free(block_table, prefix_len, ref_count, table_out, ref_out, block_size, window=0, sinks=0, spare=0,
@@ -557,19 +562,19 @@ def kv_pages_free(block_table, prefix_len, ref_count, table_out, ref_out, block_
     """Drops the entries whose pages no later step needs (window 0: none has left)."""
     B, mb = block_table.shape
     nb, i32 = ref_count.shape[0], torch.int32
-    ptr, index, stream = _args(block_table.device)
+    i, stream = _device(block_table)
     _check("kv_pages_free", load().kv_pages_free(
-        ptr(block_table, i32, (B, mb)), ptr(prefix_len, i32, (B,)), B, mb, int(block_size), nb, int(window), int(sinks),
-        int(spare), ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)), ptr(ref_out, i32, (nb,)),
-        _word(dev_status, index), stream))
+        _ptr(block_table, i, i32, (B, mb)), _ptr(prefix_len, i, i32, (B,)), B, mb, int(block_size), nb, int(window),
+        int(sinks), int(spare), _ptr(ref_count, i, i32, (nb,)), _ptr(table_out, i, i32, (B, mb)), _ptr(ref_out, i, i32, (nb,)),
+        _word(dev_status, i), stream))
 
 
-def _pool(ptr, k_pages, v_pages):
+def _pool(i, k_pages, v_pages):
     """(K, V, element bytes, layers, KV heads, head_dim, block size, blocks)
     of a pool with or without the layer axis."""
     L, (nb, Hkv, bs, D) = (1, k_pages.shape) if k_pages.dim() == 4 else (k_pages.shape[0], k_pages.shape[1:])
     dt, shape = k_pages.dtype, k_pages.shape
-    return ptr(k_pages, dt, shape), ptr(v_pages, dt, shape), k_pages.element_size(), L, Hkv, D, bs, nb
+    return _ptr(k_pages, i, dt, shape), _ptr(v_pages, i, dt, shape), k_pages.element_size(), L, Hkv, D, bs, nb
 
 
 def kv_pages_reserve(k_pages, v_pages, block_table, prefix_len, need, ref_count, table_out, ref_out, workspace=None,
@@ -579,15 +584,15 @@ def kv_pages_reserve(k_pages, v_pages, block_table, prefix_len, need, ref_count,
     is allocated per call when not given."""
     B, mb = block_table.shape
     i32 = torch.int32
-    ptr, index, stream = _args(block_table.device)
-    pool = _pool(ptr, k_pages, v_pages)
+    i, stream = _device(block_table)
+    pool = _pool(i, k_pages, v_pages)
     nb = pool[-1]
     if workspace is None:
         workspace = _scratch(kv_pages_workspace_bytes(B, mb, nb), block_table)
     _check("kv_pages_reserve", load().kv_pages_reserve(
-        *pool, ptr(block_table, i32, (B, mb)), B, mb, ptr(prefix_len, i32, (B,)), ptr(need, i32, (B,)),
-        ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)), ptr(ref_out, i32, (nb,)),
-        _sized(workspace, index, torch.uint8), workspace.numel(), _word(dev_status, index), stream))
+        *pool, _ptr(block_table, i, i32, (B, mb)), B, mb, _ptr(prefix_len, i, i32, (B,)), _ptr(need, i, i32, (B,)),
+        _ptr(ref_count, i, i32, (nb,)), _ptr(table_out, i, i32, (B, mb)), _ptr(ref_out, i, i32, (nb,)),
+        _sized(workspace, i, torch.uint8), workspace.numel(), _word(dev_status, i), stream))
 
 
 def kv_pages_compact(k_pages, v_pages, block_table, ref_count, table_out, ref_out, n_used, remap=None, workspace=None,
@@ -596,12 +601,12 @@ def kv_pages_compact(k_pages, v_pages, block_table, ref_count, table_out, ref_ou
     remap [num_blocks] int32 (optional) are outputs."""
     B, mb = block_table.shape
     i32 = torch.int32
-    ptr, index, stream = _args(block_table.device)
-    pool = _pool(ptr, k_pages, v_pages)
+    i, stream = _device(block_table)
+    pool = _pool(i, k_pages, v_pages)
     nb = pool[-1]
     if workspace is None:
         workspace = _scratch(kv_pages_workspace_bytes(B, mb, nb), block_table)
     _check("kv_pages_compact", load().kv_pages_compact(
-        *pool, ptr(block_table, i32, (B, mb)), B, mb, ptr(ref_count, i32, (nb,)), ptr(table_out, i32, (B, mb)),
-        ptr(ref_out, i32, (nb,)), ptr(n_used, i32, (1,)), None if remap is None else ptr(remap, i32, (nb,)),
-        _sized(workspace, index, torch.uint8), workspace.numel(), _word(dev_status, index), stream))
+        *pool, _ptr(block_table, i, i32, (B, mb)), B, mb, _ptr(ref_count, i, i32, (nb,)),
+        _ptr(table_out, i, i32, (B, mb)), _ptr(ref_out, i, i32, (nb,)), _ptr(n_used, i, i32, (1,)), None if remap is None else _ptr(remap, i, i32, (nb,)),
+        _sized(workspace, i, torch.uint8), workspace.numel(), _word(dev_status, i), stream))
