@@ -552,9 +552,8 @@ def kv_pages_fork(block_table, prefix_len, parent, ref_count, table_out, prefix_
     i, stream = _device(block_table)
     _check("kv_pages_fork", load().kv_pages_fork(
         _ptr(block_table, i, i32, (B, mb)), _ptr(prefix_len, i, i32, (B,)), _ptr(parent, i, i32, (out,)), B, out,
-        mb, nb,
-        _ptr(ref_count, i, i32, (nb,)), _ptr(table_out, i, i32, (out, mb)), _ptr(prefix_len_out, i, i32, (out,)),
-        _ptr(ref_out, i, i32, (nb,)), _word(dev_status, i), stream))
+        mb, nb, _ptr(ref_count, i, i32, (nb,)), _ptr(table_out, i, i32, (out, mb)),
+        _ptr(prefix_len_out, i, i32, (out,)), _ptr(ref_out, i, i32, (nb,)), _word(dev_status, i), stream))
 
 
 def kv_pages_free(block_table, prefix_len, ref_count, table_out, ref_out, block_size, window=0, sinks=0, spare=0,
@@ -565,8 +564,8 @@ def kv_pages_free(block_table, prefix_len, ref_count, table_out, ref_out, block_
     i, stream = _device(block_table)
     _check("kv_pages_free", load().kv_pages_free(
         _ptr(block_table, i, i32, (B, mb)), _ptr(prefix_len, i, i32, (B,)), B, mb, int(block_size), nb, int(window),
-        int(sinks), int(spare), _ptr(ref_count, i, i32, (nb,)), _ptr(table_out, i, i32, (B, mb)), _ptr(ref_out, i, i32, (nb,)),
-        _word(dev_status, i), stream))
+        int(sinks), int(spare), _ptr(ref_count, i, i32, (nb,)), _ptr(table_out, i, i32, (B, mb)),
+        _ptr(ref_out, i, i32, (nb,)), _word(dev_status, i), stream))
 
 
 def _pool(i, k_pages, v_pages):
@@ -608,5 +607,6 @@ def kv_pages_compact(k_pages, v_pages, block_table, ref_count, table_out, ref_ou
         workspace = _scratch(kv_pages_workspace_bytes(B, mb, nb), block_table)
     _check("kv_pages_compact", load().kv_pages_compact(
         *pool, _ptr(block_table, i, i32, (B, mb)), B, mb, _ptr(ref_count, i, i32, (nb,)),
-        _ptr(table_out, i, i32, (B, mb)), _ptr(ref_out, i, i32, (nb,)), _ptr(n_used, i, i32, (1,)), None if remap is None else _ptr(remap, i, i32, (nb,)),
+        _ptr(table_out, i, i32, (B, mb)), _ptr(ref_out, i, i32, (nb,)), _ptr(n_used, i, i32, (1,)),
+        None if remap is None else _ptr(remap, i, i32, (nb,)),
         _sized(workspace, i, torch.uint8), workspace.numel(), _word(dev_status, i), stream))
