@@ -45,6 +45,7 @@ struct SvAttnPlan {
   int splits;        // KV splits per (sequence, KV head)
   int chunk;         // prefix keys per split (multiple of the key tile)
   size_t ws_bytes;   // partials (0 when splits == 1)
+  bool join;         // CUDA-core window kernel whose splits are one cluster (no workspace)
 };
 SvAttnPlan sv_attn_plan(const SvAttnShape &s, int num_splits);
 SvAttnPlan sv_attn_window_plan(const SvAttnShape &s);  // s.window > 0

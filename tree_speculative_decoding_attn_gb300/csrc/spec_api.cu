@@ -23,6 +23,7 @@ inline bool same_or_apart(const void *a, const void *b, size_t n) { return a == 
 }  // namespace
 
 SvAttnPlan sv_attn_simt_plan(const SvAttnShape &s, int num_splits);
+SvAttnPlan sv_attn_simt_window_plan(const SvAttnShape &s);
 SvAttnPlan sv_attn_tc_plan(const SvAttnShape &s, int num_splits, bool *ok);
 
 SvAttnPlan sv_attn_plan(const SvAttnShape &s, int num_splits) {
@@ -40,7 +41,7 @@ SvAttnPlan sv_attn_plan(const SvAttnShape &s, int num_splits) {
 }
 
 SvAttnPlan sv_attn_window_plan(const SvAttnShape &s) {
-  if (!sv_attn_tc2_window_supported(s)) return sv_attn_simt_plan(s, 0);
+  if (!sv_attn_tc2_window_supported(s)) return sv_attn_simt_window_plan(s);
   SvAttnPlan p{};
   p.use_tc = 2;
   p.splits = 1;
@@ -60,7 +61,7 @@ int sv_attn_run(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const 
   }
   const int rc = p.use_tc ? sv_attn_tc(s, p, q, kc, vc, kt, vt, prefix_len, anc, out, scale, ws, status, stream)
                           : sv_attn_simt(s, p, q, kc, vc, kt, vt, prefix_len, anc, out, scale, ws, status, stream);
-  if (rc != SPEC_OK || p.splits == 1) return rc;
+  if (rc != SPEC_OK || p.splits == 1 || p.join) return rc;
   return sv_attn_combine(s, p, ws, out, prefix_len, stream);
 }
 
