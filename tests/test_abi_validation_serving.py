@@ -34,7 +34,7 @@ def _paged(lib, table=P, bs=128, nb=64, mb=8, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(q=NULL), INV), (dict(depth=NULL), INV), (dict(k=MIS), INV), (dict(w=0), INV), (dict(w=-5), INV), (dict(s=-1), INV),
     (dict(dtype=9), UNS), (dict(hq=15), INV), (dict(D=96), UNS), (dict(N=257), UNS), (dict(N=64, hq=128), UNS),
-    (dict(N=65, hq=130, hkv=1), UNS),
+    (dict(N=65, hq=130, hkv=1), UNS), (dict(N=256, hq=1 << 24, hkv=1), UNS),
     (dict(B=0), INV), (dict(mp=2048), CAP), (dict(mp=-1), INV), (dict(B=1 << 15, hkv=4), UNS),
     (dict(B=1024, hkv=2, s_max=1 << 20), UNS),
     (dict(B=1, N=1, hq=2, mp=1000, w=2000), CAP),                       # splits need a workspace

@@ -167,7 +167,7 @@ static int attn_check(int dtype, int batch, int n_nodes, int hq, int hkv, int he
     return SPEC_ERR_INVALID_ARG;
   if (hq % hkv) return SPEC_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return SPEC_ERR_UNSUPPORTED;
-  if (n_nodes > SPEC_MAX_NODES || (hq / hkv) * n_nodes > (n_nodes <= 64 ? 512 : 2048))
+  if (n_nodes > SPEC_MAX_NODES || (long long)(hq / hkv) * n_nodes > (n_nodes <= 64 ? 512 : 2048))
     return SPEC_ERR_UNSUPPORTED;
   if (max_prefix > s_max) return SPEC_ERR_CAPACITY;
   return SPEC_OK;
