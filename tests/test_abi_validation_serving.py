@@ -37,8 +37,8 @@ def _paged(lib, table=P, bs=128, nb=64, mb=8, **kw):
     (dict(N=65, hq=130, hkv=1), UNS), (dict(N=256, hq=1 << 24, hkv=1), UNS),
     (dict(B=0), INV), (dict(mp=2048), CAP), (dict(mp=-1), INV), (dict(B=1 << 15, hkv=4), UNS),
     (dict(B=1024, hkv=2, s_max=1 << 20), UNS),
-    (dict(B=1, N=1, hq=2, mp=1000, w=2000), CAP),                       # splits need a workspace
-    (dict(B=1, N=1, hq=2, mp=1000, w=2000, ws=MIS, ws_bytes=1 << 30), CAP),
+    (dict(B=1, N=1, hq=2, mp=60000, s_max=60000, w=60000), CAP),         # splits need a workspace
+    (dict(B=1, N=1, hq=2, mp=60000, s_max=60000, w=60000, ws=MIS, ws_bytes=1 << 30), CAP),
 ])
 def test_window_refuses(lib, kw, code):
     assert _window(lib, **kw) == code
@@ -55,13 +55,13 @@ def test_paged_window_refuses(lib, kw, code):
 def test_window_workspace_is_zero_for_bad_shapes(lib):
     f = lib.tree_attn_window_workspace_bytes
     assert f(sv.F32, 2, 8, 15, 2, 128, 512, 100, 4) == 0 and f(sv.F32, 2, 8, 16, 2, 128, 512, 0, 4) == 0
-    assert f(sv.F32, 1, 1, 2, 2, 128, 1000, 2000, 4) > 0
+    assert f(sv.F32, 1, 1, 2, 2, 128, 60000, 60000, 4) > 0
 
 
 def test_short_window_calls_need_no_workspace(lib):
     f = lib.tree_attn_window_workspace_bytes
     assert f(sv.F32, 1, 5, 4, 4, 64, 1001, 333, 4) == 0
-    assert f(sv.F32, 1, 5, 4, 4, 64, 1001, 1001, 4) > 0
+    assert f(sv.F32, 1, 5, 4, 4, 64, 60000, 5000, 4) > 0 and f(sv.BF16, 1, 1, 32, 8, 128, 60000, 1024, 4) == 0
 
 
 def _verify(lib, p=P, q=NULL, dtype=sv.F32, B=2, N=8, V=100, u=P, cap=4):

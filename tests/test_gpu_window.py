@@ -127,14 +127,20 @@ CASES = [
     ("bf16", 2, 8, 2, 128, [4000, 1], R(16, 200, (8, 6, 4, 3)), 3000, 7, 0),  # parts of four row groups a KV head
     ("bf16", 5, 64, 8, 128, [6000, 5000, 0, 300, 6100], R(17, 24, (4, 3, 2)), 5000, 4, 128),  # equal ranges
     ("bf16", 70, 4, 2, 128, [(37 * i) % 300 for i in range(70)], R(14, 8, (3, 2)), 90, 4, 0),
-    # CUDA cores, splits joined by a cluster: 13 and 16 CTAs, one CTA, idle CTAs beside short prefixes, two tree tiles
+    # few rows and keys, joined by a cluster: sixteen CTAs, short prefixes that leave CTAs idle, one CTA, two rounds
     ("f32", 1, 4, 4, 64, [1001], R(20, 5, (2, 2)), 333, 4, 0),
     ("f32", 2, 6, 3, 128, [470, 3], R(21, 16, (5, 3)), 450, 7, 128),
     ("f32", 1, 8, 1, 128, [0], R(22, 7, (3, 2)), 9, 2, 0),
     ("f32", 1, 2, 2, 64, [2000], R(23, 40, (5, 3, 2)), 400, 33, 0),
-    # ... groups of heads too wide for the tensor cores, joined and split
+    # ... groups of heads too wide for the tensor cores
     ("bf16", 1, 160, 1, 64, [800], synth.chain(1), 300, 4, 0),
     ("bf16", 2, 130, 1, 128, [500, 90], synth.chain(3), 2000, 4, 128),
+    ("bf16", 1, 32, 8, 128, [5000], synth.chain(1), 4000, 4, 128),          # 251 keys a CTA
+    ("bf16", 40, 16, 8, 128, [(97 * i) % 700 for i in range(40)], synth.chain(1), 256, 4, 0),  # clusters of one
+    ("f32", 1, 8, 2, 128, [1500], R(25, 100, (6, 5, 3)), 900, 30, 128),     # row groups, two mask words
+    # past what a cluster takes: tiles on CUDA cores and a merge, and one token on the tensor cores
+    ("f32", 1, 2, 1, 64, [9000], R(26, 30, (5, 3, 2)), 5000, 4, 0),
+    ("bf16", 8, 32, 8, 128, [3000, 1, 2950, 0, 130, 2000, 2999, 257], synth.chain(1), 2900, 4, 128),
 ]
 
 

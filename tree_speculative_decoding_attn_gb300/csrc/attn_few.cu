@@ -1,0 +1,404 @@
+// Window tree attention of few rows over few keys, in one launch: a decode
+// step, a short chain, a small tree.
+//
+// out = sum_k 2^(s_k - M) v_k / sum_k 2^(s_k - M) with s = scale log2(e) q.k
+// over the sinks, the window and the tree's keys that the row's position and
+// ancestor mask show it.  Sums, probabilities and accumulators are float32.
+//
+// What bounds it: latency.  Work split: one cluster per (16 query rows, KV
+// head, sequence), whose CTAs share its visible keys evenly, key by key (no
+// tiles: every key's row is looked up by itself, so pages and cut windows
+// need no care).  A CTA's keys are few enough to be in flight at once: K into
+// registers (four lanes a key, a pair of keys 64 apart per lane group), V by
+// asynchronous copies into shared memory.  So the softmax needs one pass and
+// no running max: scores to shared memory, a warp a row for max, exp2 and sum,
+// then P V with two dims and four rows a thread.  The partial results are
+// pushed into the shared memory of the CTAs that own slices of the output
+// (one cluster barrier; a pull would add a trip), which weigh and write them.
+#include <cooperative_groups.h>
+#include <math.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 16;                // query rows of a cluster
+constexpr int kLanes = 4;                // that share a key
+constexpr int kGroups = kThreads / kLanes;  // keys taken at once, half of a round
+constexpr int kMaxCtas = 16;
+constexpr int kSms = 152;
+constexpr int kMaxKeys = 264;            // of one CTA: 256 with a few sinks and nodes; two CTAs share an SM
+
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sv::ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4 &u, float (&f)[16 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 2) {
+    sv::bf16x8_to_f32(u, f);
+  } else {
+    f[0] = __uint_as_float(u.x);
+    f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z);
+    f[3] = __uint_as_float(u.w);
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    attn_few_kernel(const T *__restrict__ q, const T *__restrict__ kc, const T *__restrict__ vc,
+                    const T *__restrict__ kt, const T *__restrict__ vt, const int32_t *__restrict__ prefix_len,
+                    const uint64_t *__restrict__ anc, T *__restrict__ out, int N, int Hq, int Hkv, int s_max,
+                    int max_prefix, int cap, float scale_log2, int32_t *status, const sv::KvPages pg,
+                    const sv::Window win) {
+  constexpr int VEC = 16 / (int)sizeof(T);
+  constexpr int LC = D / VEC / kLanes;      // 16-byte pieces of a key that a lane holds
+  constexpr int PG = kThreads / (D / 2);  // thread groups of P V
+  constexpr int MW = SPEC_MAX_NODES / 64;
+  extern __shared__ uint4 dyn[];
+  __shared__ __align__(16) float s_q[kRows][D];
+  __shared__ __align__(16) float s_acc[PG][4][D];
+  __shared__ float4 s_in[kRows * D / 4 + kMaxCtas];   // [CTA][its slice of this CTA's outputs]
+  __shared__ float2 s_ml[kMaxCtas][kRows];            // the CTAs' max and sum of each row
+  __shared__ float2 s_own[kRows];
+  __shared__ uint64_t s_anc[kRows][MW];
+  __shared__ int s_pos[kRows];
+  T *sV = reinterpret_cast<T *>(dyn);                 // [cap][D]
+  float *sS = reinterpret_cast<float *>(sV + (size_t)cap * D);  // [kRows][ld]
+  const int ld = cap + 4;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = gridDim.x, rank = blockIdx.x, b = blockIdx.z / Hkv, kvh = blockIdx.z % Hkv;
+  const int G = Hq / Hkv, r0 = blockIdx.y * kRows, nr = min(kRows, N * G - r0);
+  const int P = prefix_len[b];
+  if (P < 0 || P > max_prefix || P > s_max) {  // (the whole cluster)
+    if (tid == 0) sv::report(status, SPEC_DEV_CAPACITY);
+    return;
+  }
+  cluster_arrive();  // (waited for before the first push: the partners run)
+
+  // the rows: queries, positions, ancestors
+  for (int e = tid; e < nr * (D / VEC); e += kThreads) {
+    const int rr = e / (D / VEC), c = e % (D / VEC), r = r0 + rr;
+    float f[VEC];
+    unpack<T>(*reinterpret_cast<const uint4 *>(q + (((int64_t)b * N + r / G) * Hq + kvh * G + r % G) * D + c * VEC), f);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s_q[rr][c * VEC + i] = f[i];
+  }
+  const int nw = (N + 63) >> 6;
+  for (int e = tid; e < nr * nw; e += kThreads) {
+    const int rr = e / nw;
+    const int64_t node = (int64_t)b * N + (r0 + rr) / G;
+    s_anc[rr][e - rr * nw] = anc[node * nw + e - rr * nw];
+    if (e == rr * nw) s_pos[rr] = P + sv::win_depth(win, node, N);
+  }
+
+  // the visible keys: sinks [0, n_sink), window [lo, P), tree
+  const int lo = max(0, P - win.window + 1), n_sink = min(win.sinks, lo), n_prefix = n_sink + P - lo;
+  const int total = n_prefix + N, per_cta = (total + C - 1) / C;
+  const int first = rank * per_cta, n = max(0, min(per_cta, total - first)), n4 = (n + 3) & ~3;
+  const int group = tid / kLanes, l = tid % kLanes;
+  const int nq = (nr + 3) >> 2;
+  bool synced = false;
+  for (int base = 0; base < n4; base += 2 * kGroups) {
+    uint4 kv[2][LC];
+    int pos[2], node[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = base + h * kGroups + group, slot = first + i;
+      pos[h] = 0;
+      node[h] = -1;
+#pragma unroll
+      for (int j = 0; j < LC; ++j) kv[h][j] = make_uint4(0, 0, 0, 0);
+      if (i >= n4) continue;
+      const T *kp = nullptr, *vp = nullptr;
+      if (i < n && slot < n_prefix) {
+        pos[h] = slot < n_sink ? slot : lo + slot - n_sink;
+        const int row = sv::kv_row(pg, b, Hkv, kvh, s_max, pos[h], status);
+        if (row >= 0) {
+          kp = kc + (int64_t)row * D;
+          vp = vc + (int64_t)row * D;
+        }
+      } else if (i < n) {
+        node[h] = slot - n_prefix;
+        const int64_t row = ((int64_t)b * Hkv + kvh) * N + node[h];
+        kp = kt + row * D;
+        vp = vt + row * D;
+        pos[h] = P + sv::win_depth(win, (int64_t)b * N + node[h], N);
+      }
+      // (a key past the CTA's, or of a bad block: zeros)
+#pragma unroll
+      for (int j = 0; j < LC; ++j) {
+        const int c = (l + kLanes * j) * VEC;
+        if (kp) kv[h][j] = *reinterpret_cast<const uint4 *>(kp + c);
+      }
+#pragma unroll
+      for (int j = 0; j < LC; ++j) {
+        const int c = (l + kLanes * j) * VEC;
+        if (vp)
+          copy16(sV + (size_t)i * D + c, vp + c);
+        else
+          *reinterpret_cast<uint4 *>(sV + (size_t)i * D + c) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    if (!synced) __syncthreads();  // the rows are in place
+    synced = true;
+    // four rows at a time, two keys a lane group (one, where the second is
+    // past the end)
+    const int i0 = base + warp * (32 / kLanes);
+    auto scores = [&](auto two) {
+      constexpr int H = decltype(two)::value;
+      for (int qd = 0; qd < nq; ++qd) {
+        float a[2][4] = {};
+#pragma unroll
+        for (int j = 0; j < LC; ++j) {
+          float k[H][VEC];
+#pragma unroll
+          for (int h = 0; h < H; ++h) unpack<T>(kv[h][j], k[h]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float4 *qp = reinterpret_cast<const float4 *>(&s_q[qd * 4 + r][(l + kLanes * j) * VEC]);
+#pragma unroll
+            for (int v = 0; v < VEC / 4; ++v) {
+              const float4 x = qp[v];
+#pragma unroll
+              for (int h = 0; h < H; ++h)
+                a[h][r] = fmaf(x.x, k[h][4 * v], fmaf(x.y, k[h][4 * v + 1], fmaf(x.z, k[h][4 * v + 2], fmaf(x.w, k[h][4 * v + 3], a[h][r]))));
+            }
+          }
+        }
+        // sums over the lanes of a key: one row each
+        const bool up = l & 2, odd = l & 1;
+        const int rr = qd * 4 + l;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          if (kLanes == 8)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) a[h][r] += __shfl_xor_sync(0xffffffffu, a[h][r], 4);
+          const float x0 = (up ? a[h][2] : a[h][0]) + __shfl_xor_sync(0xffffffffu, up ? a[h][0] : a[h][2], 2);
+          const float x1 = (up ? a[h][3] : a[h][1]) + __shfl_xor_sync(0xffffffffu, up ? a[h][1] : a[h][3], 2);
+          const float y = (odd ? x1 : x0) + __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
+          const int i = base + h * kGroups + group;
+          if (l >= 4 || i >= n4 || rr >= nr) continue;
+          bool vis = i < n && (pos[h] < win.sinks || s_pos[rr] - pos[h] < win.window);
+          if (node[h] >= 0) vis = vis && ((s_anc[rr][node[h] >> 6] >> (node[h] & 63)) & 1ull);
+          sS[rr * ld + i] = vis ? y * scale_log2 : -INFINITY;
+        }
+      }
+    };
+    if (i0 + kGroups < n4)
+      scores(std::integral_constant<int, 2>{});
+    else if (i0 < n4)
+      scores(std::integral_constant<int, 1>{});
+  }
+  __syncthreads();
+  // softmax over the CTA's keys, a warp a row
+  for (int rr = warp; rr < nr; rr += kWarps) {
+    float *s = sS + rr * ld;
+    float m = -INFINITY, sum = 0.f;
+#pragma unroll 2
+    for (int i = lane; i < n4; i += 32) m = fmaxf(m, s[i]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll 2
+    for (int i = lane; i < n4; i += 32) {
+      const float x = s[i], p = x == -INFINITY ? 0.f : exp2f(x - m);
+      s[i] = p;
+      sum += p;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_own[rr] = make_float2(m, sum);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  // P V: two dims and four rows a thread; the groups that are left over share
+  // out the keys
+  const int quads = nq > 2 ? 4 : nq, parts = PG / quads;
+  const int pg_i = tid / (D / 2), quad = pg_i % quads, d = tid % (D / 2) * 2;
+  {
+    float acc[4][2] = {};
+    if (quad < nq) {
+      const float *sp = sS + quad * 4 * ld;
+#pragma unroll 2
+      for (int k = pg_i / quads * 4; k < n4; k += parts * 4) {
+        float4 p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4 *>(sp + r * ld + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 v;
+          if constexpr (sizeof(T) == 2) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(sV + (size_t)(k + i) * D + d);
+            v = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+          } else {
+            v = *reinterpret_cast<const float2 *>(sV + (size_t)(k + i) * D + d);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float w = i == 0 ? p[r].x : i == 1 ? p[r].y : i == 2 ? p[r].z : p[r].w;
+            acc[r][0] = fmaf(w, v.x, acc[r][0]);
+            acc[r][1] = fmaf(w, v.y, acc[r][1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) *reinterpret_cast<float2 *>(&s_acc[pg_i][r][d]) = make_float2(acc[r][0], acc[r][1]);
+  }
+  __syncthreads();
+  cluster_wait();
+  // push: slices of the outputs to the CTAs that own them, the rows' max and
+  // sum to everyone
+  const int pieces = nr * (D / 4), per = (pieces + C - 1) / C;
+  for (int i = tid; i < pieces; i += kThreads) {
+    const int rr = i / (D / 4), c = i % (D / 4) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < parts; ++p) {
+      const float4 y = *reinterpret_cast<const float4 *>(&s_acc[p * quads + (rr >> 2)][rr & 3][c]);
+      x.x += y.x;
+      x.y += y.y;
+      x.z += y.z;
+      x.w += y.w;
+    }
+    const int to = i / per;
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                     sv::ptx::mapa_cluster(&s_in[rank * per + i - to * per], to)),
+                 "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
+                 : "memory");
+  }
+  if (tid < nr * C) {
+    const int rr = tid / C, to = tid % C;
+    const float2 x = s_own[rr];
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(sv::ptx::mapa_cluster(&s_ml[rank][rr], to)),
+                 "f"(x.x), "f"(x.y)
+                 : "memory");
+  }
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  // the outputs that this CTA owns
+  for (int j = tid; j < min(per, pieces - rank * per); j += kThreads) {
+    const int i = rank * per + j, rr = i / (D / 4), c = i % (D / 4) * 4, r = r0 + rr;
+    float M = -INFINITY, L = 0.f;
+    for (int s = 0; s < C; ++s) M = fmaxf(M, s_ml[s][rr].x);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < C; ++s) {
+      const float2 ml = s_ml[s][rr];
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);  // (a CTA that saw no key of the row)
+      const float4 x = s_in[s * per + j];
+      L = fmaf(f, ml.y, L);
+      o.x = fmaf(f, x.x, o.x);
+      o.y = fmaf(f, x.y, o.y);
+      o.z = fmaf(f, x.z, o.z);
+      o.w = fmaf(f, x.w, o.w);
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;  // (a row that sees nothing: zeros)
+    T *to = out + (((int64_t)b * N + r / G) * Hq + kvh * G + r % G) * D + c;
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162 w0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), w1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      *reinterpret_cast<uint2 *>(to) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&w0), *reinterpret_cast<const uint32_t *>(&w1));
+    } else {
+      *reinterpret_cast<float4 *>(to) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    }
+  }
+}
+
+template <typename T, int D>
+int launch_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const void *kc, const void *vc,
+               const void *kt, const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out, float scale,
+               int32_t *status, cudaStream_t stream) {
+  auto kern = attn_few_kernel<T, D>;
+  const auto bytes = [](int cap) { return cap * D * (int)sizeof(T) + kRows * (cap + 4) * 4; };
+  // cluster and shared-memory sizes that have to be asked for, once per device
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (dev > 63 || !(done.load() >> dev & 1)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxKeys)) != cudaSuccess)
+      return SPEC_ERR_CUDA;
+    if (dev <= 63) done.fetch_or(1ull << dev);
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int R = s.n_nodes * (s.hq / s.hkv);
+  cfg.gridDim = dim3(p.splits, (R + kRows - 1) / kRows, s.batch * s.hkv);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes(p.chunk);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, (const T *)q, (const T *)kc, (const T *)vc, (const T *)kt, (const T *)vt,
+                            prefix_len, anc, (T *)out, s.n_nodes, s.hq, s.hkv, s.s_max, s.max_prefix, p.chunk,
+                            scale * 1.4426950408889634f, status,
+                            sv::KvPages{s.block_table, s.block_size, s.max_blocks, s.num_blocks},
+                            sv::Window{s.depth, s.window, s.sinks}) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+// CTAs a cluster: enough for 32 keys each, but no more than run at once (two a
+// SM; clusters of 16 fit a GPC each, so that 256 CTAs in sixteens take 16 us
+// where eights take 10).  Taken for every shape that the SM-pair kernel does
+// not take, and else by an estimate of both, ns: a wave of clusters costs its
+// start and 29 per key and four rows of a CTA; the SM-pair kernel about eight
+// tiles' time beside its tiles (830), spread over the pairs in parts of at
+// least eight.  Measured this / the SM-pair kernel, bf16, 32/8 heads of 128, us:
+// one node, batch 1, window 256: 5.5 / 10.5, 1024: 7.3 / 15.2, 4000: 11.4 /
+// 14.4; batch 8: 7.3 / 12.4, 12.5 / 17.8, 61 / 39; batch 32: 12.7 / 34, 51 /
+// 51, 222 / 112; batch 64: 24 / 60, 93 / 86 (the estimate errs); 4 nodes,
+// batch 1: 8.6 / 10.9, 13.9 / 15.7, 27 / 15; 60 nodes, window 256: 20 / 11.
+// f32 against the CUDA-core tiles: 5 nodes, 4 heads of 64, window 333: 5.7 /
+// 12.6, 4000: 9.9 / 28; 32/8 heads of 128, window 1024: one node 8.1 / 21.4,
+// 60 nodes 73 / 92, batch 64 169 / 362.
+bool sv_attn_few_plan(const SvAttnShape &s, bool pairs, SvAttnPlan *p) {
+  const long long seen = (long long)s.window - 1 + s.sinks;
+  const long long keys = (seen < s.max_prefix ? seen : s.max_prefix) + s.n_nodes;  // at most
+  const int R = s.n_nodes * (s.hq / s.hkv);
+  const long long clusters = (long long)s.batch * s.hkv * ((R + kRows - 1) / kRows);
+  const auto at_once = [](int c) { return c == kMaxCtas ? kSms : 2 * kSms; };
+  int c = 1;
+  while (c < kMaxCtas && (long long)c * 32 < keys) c *= 2;
+  while (c > 1 && clusters * c > at_once(c) && keys <= (long long)c / 2 * kMaxKeys) c /= 2;
+  const long long each = (keys + c - 1) / c;
+  if (each > kMaxKeys) return false;
+  *p = SvAttnPlan{};
+  p->few = true;
+  p->splits = c;
+  p->chunk = (int)(each + 7) / 8 * 8;
+  if (!pairs) return true;
+  const long long waves = (clusters * c + at_once(c) - 1) / at_once(c);
+  const long long few = waves * (5000 + 29 * each * (((R < kRows ? R : kRows) + 3) / 4));
+  const long long groups = (long long)s.batch * s.hkv * ((R + 255) / 256), tiles = (keys + 127) / 128 + 1;
+  const long long share = tiles * groups / (kSms / 2), part = tiles < 8 ? tiles : 8;
+  const long long pair = groups >= kSms / 2 ? 1500 + (6500 + 830 * tiles) * groups / (kSms / 2)
+                                            : 8000 + 830 * (share > part ? share : part);
+  return few <= pair;
+}
+
+int sv_attn_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const void *kc, const void *vc,
+                const void *kt, const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out, float scale,
+                int32_t *status, cudaStream_t stream) {
+  auto run = [&](auto launch) { return launch(s, p, q, kc, vc, kt, vt, prefix_len, anc, out, scale, status, stream); };
+  if (s.dtype == SPEC_BF16) return s.head_dim == 128 ? run(launch_few<__nv_bfloat16, 128>) : run(launch_few<__nv_bfloat16, 64>);
+  return s.head_dim == 128 ? run(launch_few<float, 128>) : run(launch_few<float, 64>);
+}

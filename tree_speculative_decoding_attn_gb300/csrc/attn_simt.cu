@@ -13,10 +13,7 @@
 // sequence are cut into `splits` chunks; the last split also takes the
 // tree keys, whose visibility comes from the node's ancestor bitmask.
 // Online softmax in base 2 (scores pre-multiplied by log2 e).
-#include <cooperative_groups.h>
 #include <math.h>
-
-#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -28,7 +25,6 @@ constexpr int kRowsPerWarp = 4;
 constexpr int kRowsPerCta = kWarps * kRowsPerWarp;
 constexpr int kKeyTile = 32;
 constexpr int kSms = 152;
-constexpr int kJoin = 16;  // most splits of a row that one cluster joins
 
 // Stage `nrows` rows of [.., D] starting at `src` (row stride D) into
 // shared memory as float32; rows past nrows are zero.
@@ -61,9 +57,7 @@ __device__ __forceinline__ void stage_rows(float *dst, const T *src, int nrows) 
 // WIN: only the sinks and the window of the prefix are staged, and each row
 // masks them (and, for windows shorter than the tree, its ancestors) by its
 // own position.  Splits then share out those tiles: chunk keys of them each.
-// JOIN: the splits of a row group are one cluster, which joins its partials
-// through distributed shared memory: no workspace, no second launch.
-template <typename T, int D, int MW, bool WIN, bool JOIN>
+template <typename T, int D, int MW, bool WIN>
 __global__ void __launch_bounds__(kWarps * 32)
     attn_simt_kernel(const T *__restrict__ q, const T *__restrict__ kc, const T *__restrict__ vc,
                      const T *__restrict__ kt, const T *__restrict__ vt,
@@ -223,49 +217,6 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
   }
 
-  if constexpr (JOIN) {
-    namespace cg = cooperative_groups;
-    cg::cluster_group cluster = cg::this_cluster();
-    constexpr int PS = D + 2;  // a row's partial: D accumulators, the max, the sum
-    static_assert(kRowsPerCta * PS <= kKeyTile * (D + 1), "the K tile holds the partials");
-    __syncthreads();  // the last tile is consumed
-#pragma unroll
-    for (int k = 0; k < kRowsPerWarp; ++k) {
-      float *pr = sK + (warp * kRowsPerWarp + k) * PS;
-#pragma unroll
-      for (int dd = 0; dd < DL; ++dd) pr[lane + 32 * dd] = acc[k][dd];
-      if (lane == 0) {
-        pr[D] = m[k];
-        pr[D + 1] = l[k];
-      }
-    }
-    cluster.sync();
-    // rows shared out over the CTAs, dims over the threads
-    for (int rr = split; rr < kRowsPerCta; rr += splits) {
-      const int r = rg * kRowsPerCta + rr;
-      if (r >= R || (int)threadIdx.x >= D) break;
-      float ms[kJoin], ls[kJoin], as[kJoin], M = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kJoin; ++i) {
-        const float *pr = cluster.map_shared_rank(sK, i < splits ? i : 0) + rr * PS;
-        ms[i] = i < splits ? pr[D] : -INFINITY;
-        ls[i] = pr[D + 1];
-        as[i] = pr[threadIdx.x];
-      }
-#pragma unroll
-      for (int i = 0; i < kJoin; ++i) M = fmaxf(M, ms[i]);
-      float L = 0.f, o = 0.f;
-#pragma unroll
-      for (int i = 0; i < kJoin; ++i) {
-        const float f = ms[i] == -INFINITY ? 0.f : exp2f(ms[i] - M);  // (a split that saw no key of the row)
-        L = fmaf(f, ls[i], L);
-        o = fmaf(f, as[i], o);
-      }
-      out[(((int64_t)b * N + r / G) * Hq + kvh * G + r % G) * D + threadIdx.x] = sv::from_f32<T>(L > 0.f ? o / L : 0.f);
-    }
-    cluster.sync();  // the partners have read this CTA's partials
-    return;
-  }
 #pragma unroll
   for (int k = 0; k < kRowsPerWarp; ++k) {
     const int r = rg * kRowsPerCta + warp * kRowsPerWarp + k;
@@ -332,41 +283,8 @@ int launch_simt(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const 
                 cudaStream_t stream) {
   const int R = s.n_nodes * (s.hq / s.hkv);
   dim3 grid((R + kRowsPerCta - 1) / kRowsPerCta, p.splits, s.batch * s.hkv);
-  if (p.join) {
-    auto kern = s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1, true, true> : attn_simt_kernel<T, D, 4, true, true>;
-    if (p.splits > 8) {  // a cluster size that has to be asked for, once per device
-      static std::atomic<uint64_t> done[2];
-      std::atomic<uint64_t> &d = done[s.n_nodes <= 64];
-      int dev = 0;
-      if (cudaGetDevice(&dev) != cudaSuccess) return SPEC_ERR_CUDA;
-      if (dev > 63 || !(d.load() >> dev & 1)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-          return SPEC_ERR_CUDA;
-        if (dev <= 63) d.fetch_or(1ull << dev);
-      }
-    }
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1;
-    attr[0].val.clusterDim.y = p.splits;
-    attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, (const T *)q, (const T *)kc, (const T *)vc, (const T *)kt, (const T *)vt,
-                              prefix_len, anc, (T *)out, s.n_nodes, s.hq, s.hkv, s.s_max, s.max_prefix, p.splits,
-                              p.chunk, scale * 1.4426950408889634f, (float *)nullptr, status,
-                              sv::KvPages{s.block_table, s.block_size, s.max_blocks, s.num_blocks},
-                              sv::Window{s.depth, s.window, s.sinks}) == cudaSuccess
-               ? SPEC_OK
-               : SPEC_ERR_CUDA;
-  }
-  auto kern = s.window > 0
-                  ? (s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1, true, false> : attn_simt_kernel<T, D, 4, true, false>)
-                  : (s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1, false, false> : attn_simt_kernel<T, D, 4, false, false>);
+  auto kern = s.window > 0 ? (s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1, true> : attn_simt_kernel<T, D, 4, true>)
+                           : (s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1, false> : attn_simt_kernel<T, D, 4, false>);
   kern<<<grid, kWarps * 32, 0, stream>>>((const T *)q, (const T *)kc, (const T *)vc, (const T *)kt, (const T *)vt,
                                          prefix_len, anc, (T *)out, s.n_nodes, s.hq, s.hkv, s.s_max, s.max_prefix,
                                          p.splits, p.chunk, scale * 1.4426950408889634f, (float *)ws, status,
@@ -388,22 +306,17 @@ int launch_combine(const SvAttnShape &s, const SvAttnPlan &p, const void *ws, vo
 
 }  // namespace
 
-// Prefix keys that are read at most: with a window its own and the sinks,
-// rounded up to the tiles that may hold them (each kind ends in a cut tile of
-// its own).
-static int simt_keys(const SvAttnShape &s) {
-  if (s.window <= 0 || s.max_prefix <= 0) return s.max_prefix;
-  const long long sinks = ((long long)s.sinks + kKeyTile - 1) / kKeyTile * kKeyTile;
-  const long long most = (long long)s.window - 1 + kKeyTile + sinks, all = (long long)s.max_prefix + kKeyTile;
-  return (int)(most < all ? most : all);
-}
-
 SvAttnPlan sv_attn_simt_plan(const SvAttnShape &s, int num_splits) {
   SvAttnPlan p{};
   p.use_tc = 0;
   const int R = s.n_nodes * (s.hq / s.hkv);
   const int base = ((R + kRowsPerCta - 1) / kRowsPerCta) * s.batch * s.hkv;
-  const int keys = simt_keys(s);
+  // prefix keys that are read: with a window its own and the sinks, rounded up
+  // to the tiles that may hold them (each kind ends in a cut tile of its own)
+  const long long most = s.window > 0 ? (long long)s.window - 1 + kKeyTile + ((long long)s.sinks + kKeyTile - 1) / kKeyTile * kKeyTile
+                                      : s.max_prefix;
+  const long long all = s.window > 0 && s.max_prefix > 0 ? (long long)s.max_prefix + kKeyTile : s.max_prefix;
+  const int keys = (int)(most < all ? most : all);
   const int max_useful = keys > 0 ? (keys + kKeyTile - 1) / kKeyTile : 1;
   int splits = num_splits > 0 ? num_splits : (2 * kSms + base - 1) / base;
   splits = splits < 1 ? 1 : (splits > max_useful ? max_useful : splits);
@@ -414,27 +327,6 @@ SvAttnPlan sv_attn_simt_plan(const SvAttnShape &s, int num_splits) {
   p.chunk = chunk;
   p.ws_bytes = splits > 1 ? (size_t)s.batch * s.hkv * splits * R * sv_partial_stride(s.head_dim) * sizeof(float) : 0;
   return p;
-}
-
-// Few rows and a short window: one tile per split, up to kJoin of them, and the
-// cluster joins them in the same launch.  Measured, f32, us, one launch against
-// main kernel and combine, by the 32-key tiles that follow one another on the
-// busiest SM: 2 (5 nodes, 4 heads of 64, window 333) 8.2 against 12.4, 3 (64
-// nodes) 15.3 against 18.7 and (8 nodes, 8/2 heads of 128, window 512) 18.4
-// against 18.6, 4 (one node, 8 heads of 128, window 1024) 21.8 against 20.1,
-// 9 (32/8 heads, window 4000) 52 against 40.
-constexpr long long kJoinTiles = 3;
-SvAttnPlan sv_attn_simt_window_plan(const SvAttnShape &s) {
-  SvAttnPlan p{};
-  const int n = (simt_keys(s) + kKeyTile - 1) / kKeyTile;
-  p.join = true;
-  p.splits = n < 1 ? 1 : n < kJoin ? n : kJoin;
-  p.chunk = (n + p.splits - 1) / p.splits * kKeyTile;
-  const int R = s.n_nodes * (s.hq / s.hkv);
-  const long long ctas = (long long)((R + kRowsPerCta - 1) / kRowsPerCta) * p.splits * s.batch * s.hkv;
-  const long long waves = (ctas + 2 * kSms - 1) / (2 * kSms);
-  const long long tiles = waves * (p.chunk / kKeyTile + (s.n_nodes + kKeyTile - 1) / kKeyTile);
-  return tiles <= kJoinTiles ? p : sv_attn_simt_plan(s, 0);
 }
 
 int sv_attn_simt(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const void *kc,

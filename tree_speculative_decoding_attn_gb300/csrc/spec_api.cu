@@ -23,7 +23,6 @@ inline bool same_or_apart(const void *a, const void *b, size_t n) { return a == 
 }  // namespace
 
 SvAttnPlan sv_attn_simt_plan(const SvAttnShape &s, int num_splits);
-SvAttnPlan sv_attn_simt_window_plan(const SvAttnShape &s);
 SvAttnPlan sv_attn_tc_plan(const SvAttnShape &s, int num_splits, bool *ok);
 
 SvAttnPlan sv_attn_plan(const SvAttnShape &s, int num_splits) {
@@ -41,8 +40,11 @@ SvAttnPlan sv_attn_plan(const SvAttnShape &s, int num_splits) {
 }
 
 SvAttnPlan sv_attn_window_plan(const SvAttnShape &s) {
-  if (!sv_attn_tc2_window_supported(s)) return sv_attn_simt_window_plan(s);
   SvAttnPlan p{};
+  const bool pairs = sv_attn_tc2_window_supported(s);
+  if (sv_attn_few_plan(s, pairs, &p)) return p;
+  if (!pairs) return sv_attn_simt_plan(s, 0);
+  p = SvAttnPlan{};
   p.use_tc = 2;
   p.splits = 1;
   p.ws_bytes = sv_attn_tc2_window_ws_bytes(s);
@@ -53,6 +55,7 @@ SvAttnPlan sv_attn_window_plan(const SvAttnShape &s) {
 int sv_attn_run(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const void *kc, const void *vc,
                 const void *kt, const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out,
                 float scale, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream) {
+  if (p.few) return sv_attn_few(s, p, q, kc, vc, kt, vt, prefix_len, anc, out, scale, status, stream);
   if (p.use_tc == 2) {
     if (p.ws_bytes == 0) return SPEC_ERR_CUDA;
     if (s.window > 0)
@@ -61,7 +64,7 @@ int sv_attn_run(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const 
   }
   const int rc = p.use_tc ? sv_attn_tc(s, p, q, kc, vc, kt, vt, prefix_len, anc, out, scale, ws, status, stream)
                           : sv_attn_simt(s, p, q, kc, vc, kt, vt, prefix_len, anc, out, scale, ws, status, stream);
-  if (rc != SPEC_OK || p.splits == 1 || p.join) return rc;
+  if (rc != SPEC_OK || p.splits == 1) return rc;
   return sv_attn_combine(s, p, ws, out, prefix_len, stream);
 }
 
