@@ -5,17 +5,23 @@
 // over the sinks, the window and the tree's keys that the row's position and
 // ancestor mask show it.  Sums, probabilities and accumulators are float32.
 //
-// What bounds it: latency.  Work split: one cluster per (16 query rows, KV
-// head, sequence), whose CTAs share its visible keys evenly, key by key (no
-// tiles: every key's row is looked up by itself, so pages and cut windows
-// need no care).  A CTA's keys are few enough to be in flight at once: K into
-// registers (four lanes a key, a pair of keys 64 apart per lane group), V by
-// asynchronous copies into shared memory.  So the softmax needs one pass and
-// no running max: scores to shared memory, a warp a row for max, exp2 and sum,
-// then P V with two dims and four rows a thread.  The partial results are
-// pushed into the shared memory of the CTAs that own slices of the output
-// (one cluster barrier; a pull would add a trip), which weigh and write them.
-#include <cooperative_groups.h>
+// What bounds it: latency.  A decode step (32/8 heads of 128, window 1024,
+// paged) takes 7.6 us from a graph, five float32 nodes of 4 heads over a window
+// of 333 5.3: the launch 2 of it, then prefix length, block table and keys one
+// after another, and a cluster barrier.
+//
+// Work split: one cluster per (16 query rows, KV head, sequence), whose CTAs
+// share its visible keys evenly, key by key (no tiles: every key's row is
+// looked up by itself, so pages and cut windows need no care).  A CTA's keys
+// are few enough to be in flight at once: K into registers (four lanes a key,
+// two keys a lane group), V by asynchronous copies into shared memory.  So the
+// softmax needs one pass and no running max: scores to shared memory, a warp a
+// row for max, exp2 and sum, then P V with two dims and four rows a thread.
+// The partial results are pushed into the shared memory of the CTAs that own
+// slices of the output (one cluster barrier; a pull would add a trip), which
+// weigh and write them.  Measured against this, decode step: 512 threads and
+// eight lanes a key 8.6 to 7.1 us (contiguous cache), partials in a
+// workspace and a second launch (tiles of 32 keys) 22.
 #include <math.h>
 
 #include <atomic>
@@ -39,6 +45,7 @@ constexpr int kMaxKeys = 264;            // of one CTA: 256 with a few sinks and
 __device__ __forceinline__ void copy16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sv::ptx::smem_u32(dst)), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
@@ -85,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (tid == 0) sv::report(status, SPEC_DEV_CAPACITY);
     return;
   }
-  cluster_arrive();  // (waited for before the first push: the partners run)
+  cluster_arrive_relaxed();  // (waited for before the first push: the partners run)
 
   // the rows: queries, positions, ancestors
   for (int e = tid; e < nr * (D / VEC); e += kThreads) {
@@ -363,13 +370,13 @@ int launch_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const v
 // start and 29 per key and four rows of a CTA; the SM-pair kernel about eight
 // tiles' time beside its tiles (830), spread over the pairs in parts of at
 // least eight.  Measured this / the SM-pair kernel, bf16, 32/8 heads of 128, us:
-// one node, batch 1, window 256: 5.5 / 10.5, 1024: 7.3 / 15.2, 4000: 11.4 /
-// 14.4; batch 8: 7.3 / 12.4, 12.5 / 17.8, 61 / 39; batch 32: 12.7 / 34, 51 /
-// 51, 222 / 112; batch 64: 24 / 60, 93 / 86 (the estimate errs); 4 nodes,
-// batch 1: 8.6 / 10.9, 13.9 / 15.7, 27 / 15; 60 nodes, window 256: 20 / 11.
-// f32 against the CUDA-core tiles: 5 nodes, 4 heads of 64, window 333: 5.7 /
-// 12.6, 4000: 9.9 / 28; 32/8 heads of 128, window 1024: one node 8.1 / 21.4,
-// 60 nodes 73 / 92, batch 64 169 / 362.
+// one node, batch 1, window 256: 5.2 / 10.5, 1024: 7.0 / 15.2, 4000: 11.1 /
+// 14.4; batch 8: 7.1 / 12.4, 12.2 / 17.8, 61 / 38; batch 32: 12.2 / 34, 50 /
+// 51, 222 / 112; batch 64: 23 / 60, 91 / 86 (the estimate errs); 4 nodes,
+// batch 1: 8.3 / 10.9, 13.7 / 15.7, 27 / 15; 60 nodes, window 256: 20 / 11.
+// f32 against the CUDA-core tiles: 5 nodes, 4 heads of 64, window 333: 5.5 /
+// 12.6, 4000: 9.4 / 28; 32/8 heads of 128, window 1024: one node 7.8 / 21.4,
+// 60 nodes 72 / 92, batch 64 162 / 362.
 bool sv_attn_few_plan(const SvAttnShape &s, bool pairs, SvAttnPlan *p) {
   const long long seen = (long long)s.window - 1 + s.sinks;
   const long long keys = (seen < s.max_prefix ? seen : s.max_prefix) + s.n_nodes;  // at most

@@ -23,13 +23,14 @@
 // 2^-24.  The tests of single drafts use float64 (one thread, a few products).
 //
 // What bounds it: latency.  One sequence of a six-node chain over 32000 tokens
-// takes 7.0 us (two dependent gathers 1.3, the walk in shared memory 0.6, its
+// takes 6.3 us (two dependent gathers 1.3, the walk in shared memory 0.6, its
 // row 1.2, the exchange 0.6, the bonus 1.1, the launch the rest); 64 trees of
-// 32 nodes over 128256 bf16 tokens 15 us (16.8 MB, 1.1 TB/s: the two dependent
+// 32 nodes over 128256 bf16 tokens 14.7 us (16.8 MB, 1.1 TB/s: the two dependent
 // gathers then miss the TLB, 2.6, and the rows' integer sums, ten 32-bit
 // operations a value, take 3 to 6 where a SM holds two CTAs); eight trees of
-// 60 nodes whose siblings a drafter drew 21.5 (a rejected sibling costs 4 us:
-// its row pair 2.5, the exchange 0.6, the next test 0.8).  Kept: all the tests
+// 60 nodes whose siblings a drafter drew 19.9 (a rejected sibling costs 3.7 us:
+// its row pair 2.2, the exchange 0.6, the next test 0.8; keeping the rows in
+// shared memory from pass to pass gains nothing).  Kept: all the tests
 // that need no row at once, one thread a child (serial float64 tests cost 0.9
 // each); the whole CTA on the piece that holds the bonus (its own warp alone
 // took up to 20).  One cluster per sequence; each warp owns one contiguous piece
@@ -57,8 +58,10 @@ constexpr u64 kOne = 1ull << kBits;
 // two stops lie the 32 values of a load round, or 16 stopped sums.
 constexpr u64 kMost = 4 * kOne - 1;
 
-// Cluster barrier in two halves.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// Cluster barrier in two halves.  It tells that the CTAs run and have their
+// barriers set up (fenced), later that they are done; the sums are ordered by
+// their mbarriers, so the arrival need not wait for memory (0.2 us each).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Writes v to another CTA's shared memory and counts its 8 bytes on a barrier there.
 __device__ __forceinline__ void send_u64(uint32_t dst, u64 v, uint32_t bar) {
@@ -171,6 +174,17 @@ struct Row {
   }
 };
 
+// floor(c q) in units of 2^-58 for the bits b of a q in [0, 1] and c2 = c 2^59
+// < 2^63: (c2 * (24-bit significand * 2^8) >> 32) >> (127 - e), half the
+// instructions of a product of two 64-bit numbers.
+__device__ __forceinline__ u64 scaled(uint32_t b, u64 c2) {
+  const uint32_t m = ((b & 0x7FFFFFu) | 0x800000u) << 8;
+  const u64 t = (u64)(uint32_t)(c2 >> 32) * m + ((u64)(uint32_t)c2 * m >> 32);
+  u64 r;
+  asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(t), "r"(127u - (b >> 23)));
+  return r;
+}
+
 // max(0, p - c q) of a vector's elements, c = ci + cf * 2^-58.  MODE: 0
 // c = 0, 1 c = 1, 2 c < 16, 3 any c (c q past 4 is past any p).
 template <int MODE, int VEC>
@@ -180,9 +194,11 @@ __device__ __forceinline__ void weights(const uint32_t (&p)[VEC], const uint32_t
   for (int i = 0; i < VEC; ++i) {
     x[i] = fixed(p[i]);
     if (MODE == 0) continue;
-    u64 fq = fixed(q[i]);
-    if (MODE == 3) fq = min(fq, kMost / ci);
-    if (MODE >= 2) fq = fq * ci + __umul64hi(cf << (64 - kBits), fq);
+    u64 fq = MODE == 2 ? scaled(q[i], ((u64)ci << kBits | cf) << 1) : fixed(q[i]);
+    if (MODE == 3) {
+      fq = min(fq, kMost / ci);
+      fq = fq * ci + __umul64hi(cf << (64 - kBits), fq);
+    }
     x[i] = x[i] > fq ? x[i] - fq : 0;
   }
 }
