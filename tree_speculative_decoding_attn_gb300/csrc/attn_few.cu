@@ -45,9 +45,15 @@ constexpr int kMaxKeys = 264;            // of one CTA: 256 with a few sinks and
 __device__ __forceinline__ void copy16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sv::ptx::smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 template <typename T>
 __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[16 / sizeof(T)]) {
@@ -59,6 +65,10 @@ __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[16 / sizeof(T)
     f[2] = __uint_as_float(u.z);
     f[3] = __uint_as_float(u.w);
   }
+}
+
+__device__ __forceinline__ float dot4(const float4 &x, const float *k, float a) {
+  return fmaf(x.x, k[0], fmaf(x.y, k[1], fmaf(x.z, k[2], fmaf(x.w, k[3], a))));
 }
 
 template <typename T, int D>
@@ -180,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               const float4 x = qp[v];
 #pragma unroll
               for (int h = 0; h < H; ++h)
-                a[h][r] = fmaf(x.x, k[h][4 * v], fmaf(x.y, k[h][4 * v + 1], fmaf(x.z, k[h][4 * v + 2], fmaf(x.w, k[h][4 * v + 3], a[h][r]))));
+                a[h][r] = dot4(x, &k[h][4 * v], a[h][r]);
             }
           }
         }
@@ -189,14 +199,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int rr = qd * 4 + l;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-          if (kLanes == 8)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) a[h][r] += __shfl_xor_sync(0xffffffffu, a[h][r], 4);
           const float x0 = (up ? a[h][2] : a[h][0]) + __shfl_xor_sync(0xffffffffu, up ? a[h][0] : a[h][2], 2);
           const float x1 = (up ? a[h][3] : a[h][1]) + __shfl_xor_sync(0xffffffffu, up ? a[h][1] : a[h][3], 2);
           const float y = (odd ? x1 : x0) + __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
           const int i = base + h * kGroups + group;
-          if (l >= 4 || i >= n4 || rr >= nr) continue;
+          if (i >= n4 || rr >= nr) continue;
           bool vis = i < n && (pos[h] < win.sinks || s_pos[rr] - pos[h] < win.window);
           if (node[h] >= 0) vis = vis && ((s_anc[rr][node[h] >> 6] >> (node[h] & 63)) & 1ull);
           sS[rr * ld + i] = vis ? y * scale_log2 : -INFINITY;
@@ -314,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float inv = L > 0.f ? 1.f / L : 0.f;  // (a row that sees nothing: zeros)
     T *to = out + (((int64_t)b * N + r / G) * Hq + kvh * G + r % G) * D + c;
     if constexpr (sizeof(T) == 2) {
-      const __nv_bfloat162 w0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), w1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      const __nv_bfloat162 w0 = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+      const __nv_bfloat162 w1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
       *reinterpret_cast<uint2 *>(to) =
           make_uint2(*reinterpret_cast<const uint32_t *>(&w0), *reinterpret_cast<const uint32_t *>(&w1));
     } else {
@@ -406,6 +414,7 @@ int sv_attn_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const 
                 const void *kt, const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out, float scale,
                 int32_t *status, cudaStream_t stream) {
   auto run = [&](auto launch) { return launch(s, p, q, kc, vc, kt, vt, prefix_len, anc, out, scale, status, stream); };
-  if (s.dtype == SPEC_BF16) return s.head_dim == 128 ? run(launch_few<__nv_bfloat16, 128>) : run(launch_few<__nv_bfloat16, 64>);
+  if (s.dtype == SPEC_BF16)
+    return s.head_dim == 128 ? run(launch_few<__nv_bfloat16, 128>) : run(launch_few<__nv_bfloat16, 64>);
   return s.head_dim == 128 ? run(launch_few<float, 128>) : run(launch_few<float, 64>);
 }

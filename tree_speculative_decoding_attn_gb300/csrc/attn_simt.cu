@@ -313,8 +313,8 @@ SvAttnPlan sv_attn_simt_plan(const SvAttnShape &s, int num_splits) {
   const int base = ((R + kRowsPerCta - 1) / kRowsPerCta) * s.batch * s.hkv;
   // prefix keys that are read: with a window its own and the sinks, rounded up
   // to the tiles that may hold them (each kind ends in a cut tile of its own)
-  const long long most = s.window > 0 ? (long long)s.window - 1 + kKeyTile + ((long long)s.sinks + kKeyTile - 1) / kKeyTile * kKeyTile
-                                      : s.max_prefix;
+  const long long sinks = ((long long)s.sinks + kKeyTile - 1) / kKeyTile * kKeyTile;
+  const long long most = s.window > 0 ? (long long)s.window - 1 + kKeyTile + sinks : s.max_prefix;
   const long long all = s.window > 0 && s.max_prefix > 0 ? (long long)s.max_prefix + kKeyTile : s.max_prefix;
   const int keys = (int)(most < all ? most : all);
   const int max_useful = keys > 0 ? (keys + kKeyTile - 1) / kKeyTile : 1;
