@@ -138,9 +138,14 @@ CASES = [
     ("bf16", 1, 32, 8, 128, [5000], synth.chain(1), 4000, 4, 128),          # 251 keys a CTA
     ("bf16", 40, 16, 8, 128, [(97 * i) % 700 for i in range(40)], synth.chain(1), 256, 4, 0),  # clusters of one
     ("f32", 1, 8, 2, 128, [1500], R(25, 100, (6, 5, 3)), 900, 30, 128),     # row groups, two mask words
-    # past what a cluster takes: tiles on CUDA cores and a merge, and one token on the tensor cores
+    # past what a cluster takes: tiles on CUDA cores and a merge; one token over a long window
     ("f32", 1, 2, 1, 64, [9000], R(26, 30, (5, 3, 2)), 5000, 4, 0),
     ("bf16", 8, 32, 8, 128, [3000, 1, 2950, 0, 130, 2000, 2999, 257], synth.chain(1), 2900, 4, 128),
+    # enough rows for the SM-pair kernel: windows shorter than the tree, itself only, everything
+    ("bf16", 8, 32, 8, 128, [385, 0, 5, 1000, 128, 700, 1, 64], R(27, 60, (10, 4, 3, 2, 2)), 2, 3, 128),
+    ("bf16", 8, 32, 8, 128, [260, 5, 0, 999, 128, 700, 1, 64], R(28, 60, (10, 4, 3, 2, 2)), 1, 0, 0),
+    ("bf16", 8, 56, 8, 128, [260, 5, 0, 999, 128, 700, 1, 64], R(29, 64, (8, 4, 3, 2, 2)), 100000, 9, 128),
+    ("bf16", 8, 24, 8, 64, [260, 5, 0, 999, 128, 700, 1, 64], R(30, 150, (8, 6, 4, 3)), 200, 70, 0),
 ]
 
 
@@ -252,6 +257,87 @@ def test_two_streams_and_a_captured_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(ta["out"], tb["out"])
+
+
+def many(page=0, seed=1, **more):
+    """Enough rows for the SM-pair kernel, with an empty prefix among them."""
+    return Case("bf16", 8, 32, 8, 128, [900, 0, 33, 500, 256, 1000, 700, 64], R(31, 60, (10, 4, 3, 2, 2)), 300, 4,
+                page=page, seed=seed, **more)
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("-inf")])
+@pytest.mark.parametrize("page", [0, 128])
+def test_many_rows_nobody_sees_may_hold_anything(page, fill):
+    c = many(page, fill=(fill, fill))
+    t = c.tensors()
+    c.call(t)
+    c.check(t)
+
+
+def test_many_rows_with_empty_masks_and_depths_out_of_range():
+    c = many()
+    c.mask[:, 4] = False
+    c.depth[:, 7], c.depth[:, 9] = -5, 1 << 30
+    t = c.tensors()
+    c.call(t)
+    c.depth[:, 7], c.depth[:, 9] = 0, c.N - 1
+    c.check(t)
+    assert (host(t["out"])[1, 4] == 0).all()
+
+
+def test_many_rows_report_a_bound_and_a_block():
+    c = many(128)
+    t = c.tensors()
+    c.call(t, mp=950)
+    assert int(t["status"].item()) == sv.DEV_CAPACITY
+    good = [0, 1, 2, 3, 4, 6, 7]
+    c.check(t, rows=good)
+    assert np.isnan(host(t["out"])[5]).all()
+    t = c.tensors()
+    t["table"][5, 2] = 1 << 20            # outside the window: not read
+    c.call(t)
+    assert int(t["status"].item()) == 0
+    c.check(t)
+    t["table"][5, 6] = 1 << 20
+    c.call(t)
+    assert int(t["status"].item()) == sv.DEV_BAD_BLOCK
+    c.check(t, rows=good)
+
+
+def test_many_rows_on_two_streams_and_in_a_graph():
+    a, b = many(128, seed=1), many(128, seed=2)
+    ta, tb = a.tensors(), b.tensors()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            a.call(ta)
+        with torch.cuda.stream(s2):
+            b.call(tb)
+    torch.cuda.synchronize()
+    a.check(ta)
+    b.check(tb)
+    want = ta["out"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.call(ta)
+    ta["out"].zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(ta["out"], want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 4, 5, 16, 17, 70])
+def test_few_rows_of_every_count(dtype, D, n):
+    """Row counts around the groups of 4 and 16, prefixes around the blocks
+    of 16 keys and the CTAs' shares."""
+    c = Case(dtype, 6, 2, 1, D, [0, 1, 15, 16, 129, 777], synth.chain(n), 131, 3, page=128, seed=n)
+    t = c.tensors()
+    c.call(t)
+    assert int(t["status"].item()) == 0
+    c.check(t)
 
 
 def test_paged_equals_contiguous_where_the_tiles_agree():
