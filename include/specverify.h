@@ -392,9 +392,9 @@ int tree_attn_verify_paged(const void *q, const void *k_pages, const void *v_pag
  * Prefix rows that no node sees, [sinks, prefix_len[b] - window], are not
  * read for the result and may hold anything.  One token of ordinary decoding
  * is a tree of one node.
- * The work is that of the visible keys.  Few rows and keys (a decode step, a
- * short chain) run in one launch on CUDA cores, other bf16 calls with up to
- * 128 query heads per KV head on the tensor cores, the rest on CUDA cores in
+ * The work is that of the visible keys.  Few rows (a decode step, a short
+ * chain) run in one launch without a workspace, other bf16 calls with up to
+ * 128 query heads per KV head on pairs of SMs, the rest on CUDA cores in
  * tiles.  Everything else as tree_attn_verify; in addition batch * hkv <=
  * 65535 and batch * hkv * s_max <= 2^30 (SPEC_ERR_UNSUPPORTED).
  *   workspace  device scratch of tree_attn_window_workspace_bytes() bytes

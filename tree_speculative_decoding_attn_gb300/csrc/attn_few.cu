@@ -1,27 +1,37 @@
-// Window tree attention of few rows over few keys, in one launch: a decode
-// step, a short chain, a small tree.
+// Window tree attention of few rows, in one launch: a decode step, a short
+// chain, a small tree.
 //
 // out = sum_k 2^(s_k - M) v_k / sum_k 2^(s_k - M) with s = scale log2(e) q.k
 // over the sinks, the window and the tree's keys that the row's position and
-// ancestor mask show it.  Sums, probabilities and accumulators are float32.
+// ancestor mask show it.  Sums and accumulators are float32, and P is too (bf16
+// inputs: to 2^-17, below).
 //
-// What bounds it: latency.  A decode step (32/8 heads of 128, window 1024,
-// paged) takes 7.6 us from a graph, five float32 nodes of 4 heads over a window
-// of 333 5.3: the launch 2 of it, then prefix length, block table and keys one
-// after another, and a cluster barrier.
+// What bounds it: latency in small calls, the cache's bytes in large ones.  A
+// decode step in bf16 (32/8 heads of 128, window 1024, paged) takes 7.5 us from
+// a graph, five float32 nodes of 4 heads over a window of 333 5.4: the launch
+// 2 of it, then prefix length, block table and keys one after another, and a
+// cluster barrier.  The step at batch 64 takes 53 us (270 MB, 5.1 TB/s), over a
+// window of 4000 166 (1.05 GB, 6.3 TB/s).
 //
 // Work split: one cluster per (16 query rows, KV head, sequence), whose CTAs
 // share its visible keys evenly, key by key (no tiles: every key's row is
-// looked up by itself, so pages and cut windows need no care).  A CTA's keys
-// are few enough to be in flight at once: K into registers (four lanes a key,
-// two keys a lane group), V by asynchronous copies into shared memory.  So the
-// softmax needs one pass and no running max: scores to shared memory, a warp a
-// row for max, exp2 and sum, then P V with two dims and four rows a thread.
-// The partial results are pushed into the shared memory of the CTAs that own
-// slices of the output (one cluster barrier; a pull would add a trip), which
-// weigh and write them.  Measured against this, decode step: 512 threads and
-// eight lanes a key 8.6 to 7.1 us (contiguous cache), partials in a
-// workspace and a second launch (tiles of 32 keys) 22.
+// looked up by itself, so pages and cut windows need no care).  The partial
+// results are pushed into the shared memory of the CTAs that own slices of the
+// output (one cluster barrier; a pull would add a trip), which weigh and write
+// them.
+//
+// float32 (CUDA cores): a CTA's keys are few enough to be in flight at once: K
+// into registers (four lanes a key, two keys a lane group), V by asynchronous
+// copies into shared memory.  So the softmax needs one pass and no running
+// max: scores to shared memory, a warp a row for max, exp2 and sum, then P V
+// with two dims and four rows a thread.  Measured against this, decode step:
+// 512 threads and eight lanes a key 8.6 to 7.1 us, the next round's K ahead in
+// registers 7.7, tiles of 32 keys and a second launch 22.
+//
+// bf16: 16 rows are one operand of the warp-level matrix product, whatever
+// part of them is used; CUDA cores cost 14 us where these take 8 (4 nodes, 16
+// rows), and 92 instead of 53 at batch 64.  The SM-pair kernel's tiles of 256
+// rows take 0.8 us per 128 keys for any number of rows: 15 and 87 us.
 #include <math.h>
 
 #include <atomic>
@@ -40,7 +50,7 @@ constexpr int kLanes = 4;                // that share a key
 constexpr int kGroups = kThreads / kLanes;  // keys taken at once, half of a round
 constexpr int kMaxCtas = 16;
 constexpr int kSms = 152;
-constexpr int kMaxKeys = 264;            // of one CTA: 256 with a few sinks and nodes; two CTAs share an SM
+constexpr int kMaxKeys = 264;            // of a float32 CTA: 256 with a few sinks and nodes
 
 __device__ __forceinline__ void copy16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sv::ptx::smem_u32(dst)), "l"(src) : "memory");
@@ -53,18 +63,6 @@ __device__ __forceinline__ void cluster_arrive() {
 }
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4 &u, float (&f)[16 / sizeof(T)]) {
-  if constexpr (sizeof(T) == 2) {
-    sv::bf16x8_to_f32(u, f);
-  } else {
-    f[0] = __uint_as_float(u.x);
-    f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z);
-    f[3] = __uint_as_float(u.w);
-  }
 }
 
 // The outputs that this CTA owns, from the partial results pushed to it:
@@ -111,18 +109,18 @@ __device__ __forceinline__ void push(float2 *dst, int to, const float2 &x) {
                : "memory");
 }
 
-__device__ __forceinline__ float dot4(const float4 &x, const float *k, float a) {
-  return fmaf(x.x, k[0], fmaf(x.y, k[1], fmaf(x.z, k[2], fmaf(x.w, k[3], a))));
+__device__ __forceinline__ float dot4(const float4 &x, const float4 &y, float a) {
+  return fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, a))));
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
-    attn_few_kernel(const T *__restrict__ q, const T *__restrict__ kc, const T *__restrict__ vc,
-                    const T *__restrict__ kt, const T *__restrict__ vt, const int32_t *__restrict__ prefix_len,
-                    const uint64_t *__restrict__ anc, T *__restrict__ out, int N, int Hq, int Hkv, int s_max,
+    attn_few_kernel(const float *__restrict__ q, const float *__restrict__ kc, const float *__restrict__ vc,
+                    const float *__restrict__ kt, const float *__restrict__ vt, const int32_t *__restrict__ prefix_len,
+                    const uint64_t *__restrict__ anc, float *__restrict__ out, int N, int Hq, int Hkv, int s_max,
                     int max_prefix, int cap, float scale_log2, int32_t *status, const sv::KvPages pg,
                     const sv::Window win) {
-  constexpr int VEC = 16 / (int)sizeof(T);
+  constexpr int VEC = 4;                 // values of a 16-byte piece
   constexpr int LC = D / VEC / kLanes;      // 16-byte pieces of a key that a lane holds
   constexpr int PG = kThreads / (D / 2);  // thread groups of P V
   constexpr int MW = SPEC_MAX_NODES / 64;
@@ -134,8 +132,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ float2 s_own[kRows];
   __shared__ uint64_t s_anc[kRows][MW];
   __shared__ int s_pos[kRows];
-  T *sV = reinterpret_cast<T *>(dyn);                 // [cap][D]
-  float *sS = reinterpret_cast<float *>(sV + (size_t)cap * D);  // [kRows][ld]
+  float *sV = reinterpret_cast<float *>(dyn);         // [cap][D]
+  float *sS = sV + (size_t)cap * D;                   // [kRows][ld]
   const int ld = cap + 4;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -154,10 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // the rows: queries, positions, ancestors
   for (int e = tid; e < nr * (D / VEC); e += kThreads) {
     const int rr = e / (D / VEC), c = e % (D / VEC);
-    float f[VEC];
-    unpack<T>(*reinterpret_cast<const uint4 *>(q + row_at(rr) + c * VEC), f);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) s_q[rr][c * VEC + i] = f[i];
+    *reinterpret_cast<float4 *>(&s_q[rr][c * VEC]) = *reinterpret_cast<const float4 *>(q + row_at(rr) + c * VEC);
   }
   const int nw = (N + 63) >> 6;
   for (int e = tid; e < nr * nw; e += kThreads) {
@@ -175,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int nq = (nr + 3) >> 2;
   bool synced = false;
   for (int base = 0; base < n4; base += 2 * kGroups) {
-    uint4 kv[2][LC];
+    float4 kv[2][LC];
     int pos[2], node[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -183,9 +178,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       pos[h] = 0;
       node[h] = -1;
 #pragma unroll
-      for (int j = 0; j < LC; ++j) kv[h][j] = make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < LC; ++j) kv[h][j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i >= n4) continue;
-      const T *kp = nullptr, *vp = nullptr;
+      const float *kp = nullptr, *vp = nullptr;
       if (i < n && slot < n_prefix) {
         pos[h] = slot < n_sink ? slot : lo + slot - n_sink;
         const int row = sv::kv_row(pg, b, Hkv, kvh, s_max, pos[h], status);
@@ -204,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int j = 0; j < LC; ++j) {
         const int c = (l + kLanes * j) * VEC;
-        if (kp) kv[h][j] = *reinterpret_cast<const uint4 *>(kp + c);
+        if (kp) kv[h][j] = *reinterpret_cast<const float4 *>(kp + c);
       }
 #pragma unroll
       for (int j = 0; j < LC; ++j) {
@@ -212,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (vp)
           copy16(sV + (size_t)i * D + c, vp + c);
         else
-          *reinterpret_cast<uint4 *>(sV + (size_t)i * D + c) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<float4 *>(sV + (size_t)i * D + c) = make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
     if (!synced) __syncthreads();  // the rows are in place
@@ -225,22 +220,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int qd = 0; qd < nq; ++qd) {
         float a[2][4] = {};
 #pragma unroll
-        for (int j = 0; j < LC; ++j) {
-          float k[H][VEC];
-#pragma unroll
-          for (int h = 0; h < H; ++h) unpack<T>(kv[h][j], k[h]);
+        for (int j = 0; j < LC; ++j)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float4 *qp = reinterpret_cast<const float4 *>(&s_q[qd * 4 + r][(l + kLanes * j) * VEC]);
+            const float4 x = *reinterpret_cast<const float4 *>(&s_q[qd * 4 + r][(l + kLanes * j) * VEC]);
 #pragma unroll
-            for (int v = 0; v < VEC / 4; ++v) {
-              const float4 x = qp[v];
-#pragma unroll
-              for (int h = 0; h < H; ++h)
-                a[h][r] = dot4(x, &k[h][4 * v], a[h][r]);
-            }
+            for (int h = 0; h < H; ++h) a[h][r] = dot4(x, kv[h][j], a[h][r]);
           }
-        }
         // sums over the lanes of a key: one row each
         const bool up = l & 2, odd = l & 1;
         const int rr = qd * 4 + l;
@@ -298,13 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4 *>(sp + r * ld + k);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float2 v;
-          if constexpr (sizeof(T) == 2) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(sV + (size_t)(k + i) * D + d);
-            v = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-          } else {
-            v = *reinterpret_cast<const float2 *>(sV + (size_t)(k + i) * D + d);
-          }
+          const float2 v = *reinterpret_cast<const float2 *>(sV + (size_t)(k + i) * D + d);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float w = i == 0 ? p[r].x : i == 1 ? p[r].y : i == 2 ? p[r].z : p[r].w;
@@ -342,11 +322,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncwarp();
   cluster_arrive();
   cluster_wait();
-  join<T, D>(s_in, s_ml, pieces, per, row_at, out);
+  join<float, D>(s_in, s_ml, pieces, per, row_at, out);
 }
 
-// The same in bf16 on the tensor cores, for any number of keys: a CTA's warps
-// stream blocks of 16 keys, each through buffers of its own (no CTA barrier
+// bf16, for any number of keys: a CTA's warps stream blocks of 16 keys, each through buffers of its own (no CTA barrier
 // on the way), with a running max, and their results are weighed at the end.
 // The next block's K is under way from the moment that the scores are done,
 // its V from the end of P V.  P goes into the second product as the sum of
@@ -534,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         s[i][e + 2] *= scale_log2;
         if (whole) continue;
         const int from = (2 * t + e) * 4;
-        const int pos = __shfl_sync(0xffffffffu, keys.pos[i], from), node = __shfl_sync(0xffffffffu, keys.node[i], from);
+        const int pos = __shfl_sync(0xffffffffu, keys.pos[i], from);
+        const int node = __shfl_sync(0xffffffffu, keys.node[i], from);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           bool vis = node != -2 && (pos < win.sinks || at[h] - pos < win.window);
@@ -690,16 +670,17 @@ int launch_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const v
   const sv::KvPages pg{s.block_table, s.block_size, s.max_blocks, s.num_blocks};
   const sv::Window win{s.depth, s.window, s.sinks};
   const float scale_log2 = scale * 1.4426950408889634f;
+  const auto run = [&](auto kern, int bytes, int most_bytes, auto... cap) {
+    return launch_clusters(kern, done, s, p, bytes, most_bytes, stream, (const T *)q, (const T *)kc, (const T *)vc,
+                           (const T *)kt, (const T *)vt, prefix_len, anc, (T *)out, s.n_nodes, s.hq, s.hkv, s.s_max,
+                           s.max_prefix, cap..., scale_log2, status, pg, win);
+  };
   if constexpr (sizeof(T) == 2) {
     constexpr int bytes = kWarps * Stream<D>::kWarpBytes;
-    return launch_clusters(attn_stream_kernel<D>, done, s, p, bytes, bytes, stream, (const T *)q, (const T *)kc,
-                           (const T *)vc, (const T *)kt, (const T *)vt, prefix_len, anc, (T *)out, s.n_nodes, s.hq,
-                           s.hkv, s.s_max, s.max_prefix, scale_log2, status, pg, win);
+    return run(attn_stream_kernel<D>, bytes, bytes);
   } else {
-    const auto bytes = [](int cap) { return cap * D * (int)sizeof(T) + kRows * (cap + 4) * 4; };
-    return launch_clusters(attn_few_kernel<T, D>, done, s, p, bytes(p.chunk), bytes(kMaxKeys), stream, (const T *)q,
-                           (const T *)kc, (const T *)vc, (const T *)kt, (const T *)vt, prefix_len, anc, (T *)out,
-                           s.n_nodes, s.hq, s.hkv, s.s_max, s.max_prefix, p.chunk, scale_log2, status, pg, win);
+    const auto bytes = [](int cap) { return cap * D * 4 + kRows * (cap + 4) * 4; };
+    return run(attn_few_kernel<D>, bytes(p.chunk), bytes(kMaxKeys), p.chunk);
   }
 }
 
@@ -712,7 +693,15 @@ int launch_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const v
 // estimate of both kernels, ns: a wave of clusters costs its start and 21 a
 // key of a CTA; the SM-pair kernel about eight tiles' time beside its tiles
 // (830 each), shared out in parts of eight or more where its row groups are
-// few.  PLACEHOLDER
+// few.  Measured this / the SM-pair kernel, bf16, 32/8 heads of
+// 128, us: one node, batch 1, window 256: 6.0 / 10.5, 1024: 6.9 / 15.3, 4000:
+// 9.9 / 14.5; batch 8: 6.9 / 12.4, 11 / 18, 27 / 39; batch 64: 21 / 60, 53 /
+// 87, 166 / 216; 8 nodes, batch 1: 7.3 / 10.8, 9.9 / 15.6, 15.1 / 15.0; batch
+// 8: 10.3 / 12.3, 16.8 / 17.7 (the estimate errs); 16 nodes, batch 8: 13.9 /
+// 12.4, 26 / 18; 60 nodes, batch 1: 10.1 / 11.2, 17.1 / 15.9, 41 / 21.  f32
+// against the CUDA-core tiles: 5 nodes, 4 heads of 64, window 333: 5.4 / 12.6,
+// 4000: 9.5 / 28; 32/8 heads of 128, window 1024: one node 7.7 / 21.4, 60
+// nodes 72 / 92, batch 64 162 / 362.
 bool sv_attn_few_plan(const SvAttnShape &s, bool pairs, SvAttnPlan *p) {
   const bool stream = s.dtype == SPEC_BF16;
   const long long seen = (long long)s.window - 1 + s.sinks;

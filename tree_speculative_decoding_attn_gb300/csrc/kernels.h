@@ -45,13 +45,13 @@ struct SvAttnPlan {
   int splits;        // KV splits per (sequence, KV head)
   int chunk;         // prefix keys per split (multiple of the key tile)
   size_t ws_bytes;   // partials (0 when splits == 1)
-  bool few;          // the kernel of few rows and keys: splits CTAs a cluster, chunk keys each at most
+  bool few;          // a kernel of few rows: splits CTAs a cluster, chunk keys each at most (f32)
 };
 SvAttnPlan sv_attn_plan(const SvAttnShape &s, int num_splits);
 SvAttnPlan sv_attn_window_plan(const SvAttnShape &s);  // s.window > 0
 bool sv_attn_tc_supported(const SvAttnShape &s);
-// Whether a window call (s.window > 0) is one for the kernel of few rows and keys (pairs: the SM-pair kernel
-// could take it too), and how.
+// Whether a window call (s.window > 0) is one for the kernels of few rows (pairs: the SM-pair kernel could take
+// it too), and how.
 bool sv_attn_few_plan(const SvAttnShape &s, bool pairs, SvAttnPlan *p);
 int sv_attn_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const void *kc, const void *vc,
                 const void *kt, const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out, float scale,
