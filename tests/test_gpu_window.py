@@ -141,6 +141,7 @@ CASES = [
     # past what a cluster takes: tiles on CUDA cores and a merge; one token over a long window
     ("f32", 1, 2, 1, 64, [9000], R(26, 30, (5, 3, 2)), 5000, 4, 0),
     ("bf16", 8, 32, 8, 128, [3000, 1, 2950, 0, 130, 2000, 2999, 257], synth.chain(1), 2900, 4, 128),
+    ("f32", 2, 4, 2, 128, [6000, 0], R(32, 70, (6, 5, 4)), 5000, 40, 128),
     # enough rows for the SM-pair kernel: windows shorter than the tree, itself only, everything
     ("bf16", 8, 32, 8, 128, [385, 0, 5, 1000, 128, 700, 1, 64], R(27, 60, (10, 4, 3, 2, 2)), 2, 3, 128),
     ("bf16", 8, 32, 8, 128, [260, 5, 0, 999, 128, 700, 1, 64], R(28, 60, (10, 4, 3, 2, 2)), 1, 0, 0),
@@ -325,6 +326,29 @@ def test_many_rows_on_two_streams_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(ta["out"], want)
+
+
+def test_a_long_window_in_float32():
+    """More keys than a cluster takes: rows nobody sees, an empty mask, a
+    prefix beyond its bound, a bad block."""
+    c = Case("f32", 3, 4, 2, 64, [5200, 0, 7000], R(33, 20, (4, 3, 2)), 4500, 5, page=128, seed=4,
+             fill=(float("nan"), float("nan")))
+    c.mask[1, 4] = False
+    t = c.tensors()
+    c.call(t)
+    assert int(t["status"].item()) == 0
+    c.check(t)
+    assert (host(t["out"])[1, 4] == 0).all()
+    t = c.tensors()
+    c.call(t, mp=6000)
+    assert int(t["status"].item()) == sv.DEV_CAPACITY
+    c.check(t, rows=slice(0, 2))
+    assert np.isnan(host(t["out"])[2]).all()
+    t = c.tensors()
+    t["table"][2, 40] = 1 << 20
+    c.call(t)
+    assert int(t["status"].item()) == sv.DEV_BAD_BLOCK
+    c.check(t, rows=slice(0, 2))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

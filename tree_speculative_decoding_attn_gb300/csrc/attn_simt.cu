@@ -54,9 +54,10 @@ __device__ __forceinline__ void stage_rows(float *dst, const T *src, int nrows) 
   }
 }
 
-// WIN: only the sinks and the window of the prefix are staged, and each row
-// masks them (and, for windows shorter than the tree, its ancestors) by its
-// own position.  Splits then share out those tiles: chunk keys of them each.
+// WIN (float32, over more keys than attn_few.cu takes): only the sinks and the
+// window of the prefix are staged, and each row masks them (and, for windows
+// shorter than the tree, its ancestors) by its own position.  Splits then
+// share out those tiles: chunk keys of them each.
 template <typename T, int D, int MW, bool WIN>
 __global__ void __launch_bounds__(kWarps * 32)
     attn_simt_kernel(const T *__restrict__ q, const T *__restrict__ kc, const T *__restrict__ vc,
@@ -283,8 +284,10 @@ int launch_simt(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const 
                 cudaStream_t stream) {
   const int R = s.n_nodes * (s.hq / s.hkv);
   dim3 grid((R + kRowsPerCta - 1) / kRowsPerCta, p.splits, s.batch * s.hkv);
-  auto kern = s.window > 0 ? (s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1, true> : attn_simt_kernel<T, D, 4, true>)
-                           : (s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1, false> : attn_simt_kernel<T, D, 4, false>);
+  auto kern = s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1, false> : attn_simt_kernel<T, D, 4, false>;
+  if constexpr (sizeof(T) == 4) {  // (bf16 windows run elsewhere)
+    if (s.window > 0) kern = s.n_nodes <= 64 ? attn_simt_kernel<T, D, 1, true> : attn_simt_kernel<T, D, 4, true>;
+  }
   kern<<<grid, kWarps * 32, 0, stream>>>((const T *)q, (const T *)kc, (const T *)vc, (const T *)kt, (const T *)vt,
                                          prefix_len, anc, (T *)out, s.n_nodes, s.hq, s.hkv, s.s_max, s.max_prefix,
                                          p.splits, p.chunk, scale * 1.4426950408889634f, (float *)ws, status,
