@@ -1597,22 +1597,24 @@ __global__ void __launch_bounds__(256, 4)
   constexpr int PB = kPartialBytes<true>;
   const int rr = blockIdx.y * kWinCombRows + (threadIdx.x >> 4);  // row of the pair
   const int d0 = (threadIdx.x & 15) * 8;                          // first head dim
-  int b, gi, c_lo, c_hi;
+  int b = 0, gi = 0, c_lo = blockIdx.x, c_hi = 0;
   if (s.parts > 0) {
     b = blockIdx.x / s.gpb();
     gi = blockIdx.x % s.gpb();
-    const int k = part_count(s.parts, tiles_of(s, s.prefix_len[b]));
-    if (k == 1) return;  // written by its cluster
-    c_lo = blockIdx.x * s.parts;
-    c_hi = c_lo + k - 1;
-    grid_dep_wait();  // the main kernel's partials are written and visible
+    c_lo *= s.parts;
+    c_hi = c_lo + part_count(s.parts, tiles_of(s, s.prefix_len[b])) - 1;
+  }
+  // The main kernel's partials are written and visible.  Blocks with nothing
+  // to merge wait too: what follows on the stream is ordered after this grid
+  // alone, which so has to end after the main kernel.
+  grid_dep_wait();
+  if (s.parts > 0) {
+    if (c_hi == c_lo) return;  // written by its cluster
   } else {
-    grid_dep_wait();
     const CutDesc d = cut_descs<true>(ws, s.n_clusters)[blockIdx.x + 1];
     if (!d.usable) return;
     b = d.b;
     gi = d.gi;
-    c_lo = blockIdx.x;
     c_hi = d.c_hi;
   }
   const int heads = Hq / s.hkv, R = s.n_nodes * s.gp;
