@@ -313,7 +313,7 @@ SvAttnPlan sv_attn_simt_plan(const SvAttnShape &s, int num_splits) {
   SvAttnPlan p{};
   p.use_tc = 0;
   const int R = s.n_nodes * (s.hq / s.hkv);
-  const int base = ((R + kRowsPerCta - 1) / kRowsPerCta) * s.batch * s.hkv;
+  const long long base = (long long)((R + kRowsPerCta - 1) / kRowsPerCta) * s.batch * s.hkv;  // (passes 32 bits)
   // prefix keys that are read: with a window its own and the sinks, rounded up
   // to the tiles that may hold them (each kind ends in a cut tile of its own)
   const long long sinks = ((long long)s.sinks + kKeyTile - 1) / kKeyTile * kKeyTile;
@@ -321,7 +321,7 @@ SvAttnPlan sv_attn_simt_plan(const SvAttnShape &s, int num_splits) {
   const long long all = s.window > 0 && s.max_prefix > 0 ? (long long)s.max_prefix + kKeyTile : s.max_prefix;
   const int keys = (int)(most < all ? most : all);
   const int max_useful = keys > 0 ? (keys + kKeyTile - 1) / kKeyTile : 1;
-  int splits = num_splits > 0 ? num_splits : (2 * kSms + base - 1) / base;
+  int splits = num_splits > 0 ? num_splits : (int)((2 * kSms + base - 1) / base);
   splits = splits < 1 ? 1 : (splits > max_useful ? max_useful : splits);
   if (splits > 64) splits = 64;
   int chunk = keys > 0 ? (keys + splits - 1) / splits : 0;

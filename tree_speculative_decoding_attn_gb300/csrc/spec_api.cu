@@ -253,16 +253,21 @@ int tree_attn_verify_paged(const void *q, const void *k_pages, const void *v_pag
                      workspace_bytes, dev_status, cs(stream));
 }
 
-// Limits of the window entry points beyond attn_check: 32-bit row indices.
-static int window_check(const SvAttnShape &s) {
+// Limits of the window entry points beyond attn_check: the grid's, and 32-bit
+// row indices.
+static int window_shape_check(const SvAttnShape &s) {
   if (s.window < 1 || s.sinks < 0) return SPEC_ERR_INVALID_ARG;
   const int rc = attn_check(s.dtype, s.batch, s.n_nodes, s.hq, s.hkv, s.head_dim, s.s_max, s.max_prefix);
   if (rc != SPEC_OK) return rc;
   const long long most = 1 << 30;
-  if (s.s_max > most || (long long)s.batch * s.hkv > 65535 || (long long)s.batch * s.hkv * s.n_nodes > most ||
-      (!s.block_table && (long long)s.batch * s.hkv * s.s_max > most))
+  if (s.s_max > most || (long long)s.batch * s.hkv > 65535 || (long long)s.batch * s.hkv * s.n_nodes > most)
     return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
+}
+static int window_check(const SvAttnShape &s) {
+  const int rc = window_shape_check(s);
+  if (rc != SPEC_OK) return rc;
+  return !s.block_table && (long long)s.batch * s.hkv * s.s_max > (1 << 30) ? SPEC_ERR_UNSUPPORTED : SPEC_OK;
 }
 
 size_t tree_attn_window_workspace_bytes(int dtype, int batch, int n_nodes, int hq, int hkv, int head_dim,
@@ -271,8 +276,7 @@ size_t tree_attn_window_workspace_bytes(int dtype, int batch, int n_nodes, int h
   s.window = window;
   s.sinks = sinks;
   // (the cache's own limits are the call's; a paged pool may be smaller than batch * max_prefix)
-  if (window < 1 || sinks < 0 || attn_check(dtype, batch, n_nodes, hq, hkv, head_dim, max_prefix, max_prefix) != SPEC_OK)
-    return 0;
+  if (window_shape_check(s) != SPEC_OK) return 0;
   return sv_attn_window_plan(s).ws_bytes;
 }
 
