@@ -190,9 +190,11 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
       const float mn = fmaxf(m[k], mx[k]);
-      const bool live = mn != -INFINITY;  // something visible so far
-      p[k] = live && sc[k] != -INFINITY ? exp2f(sc[k] - mn) : 0.f;
-      const float corr = live ? exp2f(m[k] - mn) : 1.f;  // 0 when m was -inf
+      // nothing visible so far (or only NaN, which fmaxf passes over and which
+      // p, the sum and the output then keep): p is 0 for the hidden keys
+      const float z = mn == -INFINITY ? 0.f : mn;
+      p[k] = exp2f(sc[k] - z);
+      const float corr = exp2f(m[k] - z);                // 0 when m was -inf
       mx[k] = p[k];                                      // reused for the row sum
       l[k] *= corr;
 #pragma unroll
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(128)
   for (int s = 0; s < splits; ++s) {
     const float *w = w0 + s * sstride;
     const float ms = w[D];
-    if (ms == -INFINITY) continue;
+    if (ms == -INFINITY && w[D + 1] == 0.f) continue;  // (with a sum: of NaN)
     const float f = exp2f(ms - M);
     L = fmaf(f, w[D + 1], L);
 #pragma unroll
