@@ -633,19 +633,61 @@ __global__ void __launch_bounds__(kThreads, 2)
   join<__nv_bfloat16, D>(s_in, s_ml, pieces, per, row_at, out);
 }
 
-// One cluster of p.splits CTAs per 16 rows, KV head and sequence.  done: the
-// devices that know the kernel's cluster and shared-memory sizes.
-template <typename... P, typename... A>
-int launch_clusters(void (*kern)(P...), std::atomic<uint64_t> &done, const SvAttnShape &s, const SvAttnPlan &p,
-                    int bytes, int most_bytes, cudaStream_t stream, A... args) {
+template <int D>
+constexpr int kStreamBytes = kWarps *Stream<D>::kWarpBytes;
+template <int D>
+constexpr int few_bytes(int cap) {
+  return cap * D * 4 + kRows * (cap + 4) * 4;
+}
+
+// Gives a kernel its cluster and shared-memory sizes, once per device, and
+// tells the largest cluster that the device runs: 16 CTAs is more than every
+// device has to take (a partition whose GPCs have fewer SMs does not).
+template <typename K>
+int prepare(K kern, int most_bytes, std::atomic<uint64_t> (&known)[2]) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return SPEC_ERR_CUDA;
-  if (dev > 63 || !(done.load() >> dev & 1)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most_bytes) != cudaSuccess)
-      return SPEC_ERR_CUDA;
-    if (dev <= 63) done.fetch_or(1ull << dev);
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return kMaxCtas;  // (no device: the call's own launch tells)
   }
+  if (dev <= 63 && (known[0].load() >> dev & 1)) return known[1].load() >> dev & 1 ? kMaxCtas : kMaxCtas / 2;
+  bool wide = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most_bytes) == cudaSuccess &&
+              cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  if (wide) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMaxCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = most_bytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    wide = cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0;
+  }
+  if (!wide) (void)cudaGetLastError();
+  if (dev <= 63) {
+    if (wide) known[1].fetch_or(1ull << dev);
+    known[0].fetch_or(1ull << dev);
+  }
+  return wide ? kMaxCtas : kMaxCtas / 2;
+}
+template <typename T, int D>
+int prepare_few() {
+  static std::atomic<uint64_t> known[2];
+  if constexpr (sizeof(T) == 2)
+    return prepare(attn_stream_kernel<D>, kStreamBytes<D>, known);
+  else
+    return prepare(attn_few_kernel<D>, few_bytes<D>(kMaxKeys), known);
+}
+
+// One cluster of p.splits CTAs per 16 rows, KV head and sequence.
+template <typename... P, typename... A>
+int launch_clusters(void (*kern)(P...), const SvAttnShape &s, const SvAttnPlan &p, int bytes, cudaStream_t stream,
+                    A... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = p.splits;
@@ -666,22 +708,18 @@ template <typename T, int D>
 int launch_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const void *kc, const void *vc,
                const void *kt, const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out, float scale,
                int32_t *status, cudaStream_t stream) {
-  static std::atomic<uint64_t> done{0};
   const sv::KvPages pg{s.block_table, s.block_size, s.max_blocks, s.num_blocks};
   const sv::Window win{s.depth, s.window, s.sinks};
   const float scale_log2 = scale * 1.4426950408889634f;
-  const auto run = [&](auto kern, int bytes, int most_bytes, auto... cap) {
-    return launch_clusters(kern, done, s, p, bytes, most_bytes, stream, (const T *)q, (const T *)kc, (const T *)vc,
-                           (const T *)kt, (const T *)vt, prefix_len, anc, (T *)out, s.n_nodes, s.hq, s.hkv, s.s_max,
-                           s.max_prefix, cap..., scale_log2, status, pg, win);
+  const auto run = [&](auto kern, int bytes, auto... cap) {
+    return launch_clusters(kern, s, p, bytes, stream, (const T *)q, (const T *)kc, (const T *)vc, (const T *)kt,
+                           (const T *)vt, prefix_len, anc, (T *)out, s.n_nodes, s.hq, s.hkv, s.s_max, s.max_prefix,
+                           cap..., scale_log2, status, pg, win);
   };
-  if constexpr (sizeof(T) == 2) {
-    constexpr int bytes = kWarps * Stream<D>::kWarpBytes;
-    return run(attn_stream_kernel<D>, bytes, bytes);
-  } else {
-    const auto bytes = [](int cap) { return cap * D * 4 + kRows * (cap + 4) * 4; };
-    return run(attn_few_kernel<D>, bytes(p.chunk), bytes(kMaxKeys), p.chunk);
-  }
+  if constexpr (sizeof(T) == 2)
+    return run(attn_stream_kernel<D>, kStreamBytes<D>);
+  else
+    return run(attn_few_kernel<D>, few_bytes<D>(p.chunk), p.chunk);
 }
 
 }  // namespace
@@ -702,7 +740,12 @@ int launch_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const v
 // against the CUDA-core tiles: 5 nodes, 4 heads of 64, window 333: 5.4 / 12.6,
 // 4000: 9.5 / 28; 32/8 heads of 128, window 1024: one node 7.7 / 21.4, 60
 // nodes 72 / 92, batch 64 162 / 362.
-bool sv_attn_few_plan(const SvAttnShape &s, bool pairs, SvAttnPlan *p) {
+int sv_attn_few_ctas(const SvAttnShape &s) {
+  if (s.dtype == SPEC_BF16) return s.head_dim == 128 ? prepare_few<__nv_bfloat16, 128>() : prepare_few<__nv_bfloat16, 64>();
+  return s.head_dim == 128 ? prepare_few<float, 128>() : prepare_few<float, 64>();
+}
+
+bool sv_attn_few_plan(const SvAttnShape &s, bool pairs, int most_ctas, SvAttnPlan *p) {
   const bool stream = s.dtype == SPEC_BF16;
   const long long seen = (long long)s.window - 1 + s.sinks;
   const long long keys = (seen < s.max_prefix ? seen : s.max_prefix) + s.n_nodes;  // at most
@@ -710,7 +753,7 @@ bool sv_attn_few_plan(const SvAttnShape &s, bool pairs, SvAttnPlan *p) {
   const long long clusters = (long long)s.batch * s.hkv * ((R + kRows - 1) / kRows);
   const auto at_once = [](int c) { return c == kMaxCtas ? kSms : 2 * kSms; };
   int c = 1;
-  while (c < kMaxCtas && (long long)c * (stream ? 64 : 32) < keys) c *= 2;
+  while (c < most_ctas && (long long)c * (stream ? 64 : 32) < keys) c *= 2;
   while (c > 1 && clusters * c > at_once(c) && (stream || keys <= (long long)c / 2 * kMaxKeys)) c /= 2;
   const long long each = (keys + c - 1) / c;
   if (!stream && each > kMaxKeys) return false;

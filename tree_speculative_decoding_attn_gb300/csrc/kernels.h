@@ -51,8 +51,9 @@ SvAttnPlan sv_attn_plan(const SvAttnShape &s, int num_splits);
 SvAttnPlan sv_attn_window_plan(const SvAttnShape &s);  // s.window > 0
 bool sv_attn_tc_supported(const SvAttnShape &s);
 // Whether a window call (s.window > 0) is one for the kernels of few rows (pairs: the SM-pair kernel could take
-// it too), and how.
-bool sv_attn_few_plan(const SvAttnShape &s, bool pairs, SvAttnPlan *p);
+// it too), and how, in clusters of up to most_ctas (8 or 16: what the current device runs).
+bool sv_attn_few_plan(const SvAttnShape &s, bool pairs, int most_ctas, SvAttnPlan *p);
+int sv_attn_few_ctas(const SvAttnShape &s);
 int sv_attn_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const void *kc, const void *vc,
                 const void *kt, const void *vt, const int32_t *prefix_len, const uint64_t *anc, void *out, float scale,
                 int32_t *status, cudaStream_t stream);

@@ -42,7 +42,7 @@ SvAttnPlan sv_attn_plan(const SvAttnShape &s, int num_splits) {
 SvAttnPlan sv_attn_window_plan(const SvAttnShape &s) {
   SvAttnPlan p{};
   const bool pairs = sv_attn_tc2_window_supported(s);
-  if (sv_attn_few_plan(s, pairs, &p)) return p;
+  if (sv_attn_few_plan(s, pairs, sv_attn_few_ctas(s), &p)) return p;
   if (!pairs) return sv_attn_simt_plan(s, 0);
   p = SvAttnPlan{};
   p.use_tc = 2;
