@@ -338,11 +338,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   int turn = 0;
   const u64 *all = nullptr;
   auto cluster_total = [&]() -> u64 {
-    if (turn == 0) cluster_wait();  // every CTA's barriers exist
     const int buf = turn & 1;
     const uint32_t parity = (turn >> 1) & 1;
-    ++turn;
     __syncthreads();
+    if (turn == 0) cluster_wait();  // every CTA's barriers exist
+    ++turn;
     if (warp == 0) {
       const u64 s = warp_sum_u64(lane < kWarps ? sh.wsum[lane] : 0);
       if (lane == 0) mbar_expect_tx(&sh.bar[buf], nc * (uint32_t)sizeof(u64));
@@ -350,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane < nc) send_u64(mapa_cluster(&sh.all[buf][rank], lane), s, mapa_cluster(&sh.bar[buf], lane));
     }
     if (!mbar_wait_cluster(&sh.bar[buf], parity, kWaitLimit)) sv::report(status, SPEC_DEV_TIMEOUT);
+    __syncwarp();  // (the cluster barriers take whole warps)
     all = sh.all[buf];
     u64 s = 0;
     for (int i = 0; i < nc; ++i) s += all[i];
