@@ -68,7 +68,22 @@ __device__ __forceinline__ void send_u64(uint32_t dst, u64 v, uint32_t bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u64 [%0], %1, [%2];" ::"r"(dst), "l"(v), "r"(bar)
                : "memory");
 }
-constexpr uint32_t kWaitLimit = 1u << 22;
+// Waits (bounded) for the 8-byte sums of the other CTAs that a barrier counts:
+// they are read right after, so the wait acquires at the cluster's scope.
+__device__ __forceinline__ bool sums_wait(uint64_t *bar, uint32_t parity) {
+  constexpr uint32_t kWaitLimit = 1u << 22;
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
 
 // The bits of a float in [0, 1] as a number of units of 2^-58, cut: the 24
 // bits of the significand at the top of 64, shifted right by what the
@@ -349,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
       if (lane < nc) send_u64(mapa_cluster(&sh.all[buf][rank], lane), s, mapa_cluster(&sh.bar[buf], lane));
     }
-    if (!mbar_wait_cluster(&sh.bar[buf], parity, kWaitLimit)) sv::report(status, SPEC_DEV_TIMEOUT);
+    if (!sums_wait(&sh.bar[buf], parity)) sv::report(status, SPEC_DEV_TIMEOUT);
     __syncwarp();  // (the cluster barriers take whole warps)
     all = sh.all[buf];
     u64 s = 0;
