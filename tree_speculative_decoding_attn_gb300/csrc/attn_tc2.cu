@@ -472,15 +472,14 @@ struct Ring {
     }
   }
 };
-// f(te, last) for the segments of a cluster's range in order: tiles c.t ..
-// te - 1 of row group (c.b, c.gi); last: the range ends there.  f leaves c.t
-// at te; false ends the walk.
+// f(te) for the segments of a cluster's range in order: tiles c.t .. te - 1
+// of row group (c.b, c.gi).  f leaves c.t at te; false ends the walk.
 template <typename F>
 __device__ __forceinline__ bool for_segments(Cur<true> &c, const Sched<true> &s, int T, F f) {
   while (T > 0) {
     const int te = min(c.n, c.t + T);
     T -= te - c.t;
-    if (!f(te, T == 0)) return false;
+    if (!f(te)) return false;
     if (T > 0) {
       c.t = c.n - 1;
       cur_next(c, s);
@@ -582,11 +581,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bars->n_tiles = live && q < k ? first(q + 1) - first(q) : 0;
       bars->start_raw = raw;
       bars->start_raw_next = 0;  // (not reached)
-      if (rank == 0 && cluster >= 1) {
-        CutDesc d{0, 0, 0, 0};
-        if (live && q == 1 && k > 1) d = CutDesc{1, b, rg % s.gpb(), rg * parts + k - 1};
-        cut_descs<WIN>(ws, s.n_clusters)[cluster] = d;
-      }
     }
   } else if (warp == 0 && whole) {
     // this cluster's row groups [r0, r1): the tiles of their sequences
@@ -735,7 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           r.next();
           return true;
         };
-        for_segments(c, s, T, [&](int te, bool) -> bool {
+        for_segments(c, s, T, [&](int te) -> bool {
           const int kvh = c.gi / pairs, pair = c.gi % pairs;
           const int bh = c.b * s.hkv + kvh;
           if (!is_v) {
@@ -891,7 +885,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Ring<kKS> kr;
         Ring<kSB> sr;
         Ring<kQB> qr;
-        ok = for_segments(c, s, T, [&](int te, bool) -> bool {
+        ok = for_segments(c, s, T, [&](int te) -> bool {
           if (!warp_ready(&bars->qfull[qr.i], qr.parity)) return false;
           const uint64_t qd = smem_desc_sw128(qa + (uint32_t)qr.i * kQBytes, 16, 1024);
           for (; c.t < te; ++c.t) {
@@ -963,7 +957,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Ring<kKS> kr;
         Ring<kQB> qr;
         const uint32_t kfull_even = mapa_cluster(&bars->kfull[0], 0), qfull_even = mapa_cluster(&bars->qfull[0], 0);
-        const bool done = for_segments(c, s, T, [&](int te, bool) -> bool {
+        const bool done = for_segments(c, s, T, [&](int te) -> bool {
           if (!warp_ready(&bars->qland[qr.i], qr.parity) || bars->abort) return false;
           if (lane == 0) mbar_arrive_cluster(qfull_even + (uint32_t)qr.i * (uint32_t)sizeof(uint64_t));
           qr.next();
@@ -1012,7 +1006,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Cur<true> c = cur_begin(bars, s);
         Ring<kVS> vr;
         Ring<kSB> sr;
-        ok = for_segments(c, s, T, [&](int te, bool) -> bool {
+        ok = for_segments(c, s, T, [&](int te) -> bool {
           uint32_t acc = 0;  // the segment's first tile starts O
           for (; c.t < te; ++c.t) {
             if (!warp_ready(&bars->vland[vr.i], vr.parity)) return false;
@@ -1089,7 +1083,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Cur<true> c = cur_begin(bars, s);
         Ring<kVS> vr;
         Ring<kSB> sr;
-        const bool done = for_segments(c, s, T, [&](int te, bool) -> bool {
+        const bool done = for_segments(c, s, T, [&](int te) -> bool {
           for (; c.t < te; ++c.t) {
             if (!warp_ready(&bars->vland[vr.i], vr.parity)) return false;
             if (is_special(c, s)) special_keys(sV + vr.i * kVBytes, c, s);
