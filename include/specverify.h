@@ -390,21 +390,31 @@ int tree_attn_verify_paged(const void *q, const void *k_pages, const void *v_pag
  * (positions of the same number) and its ancestors-or-itself (anc_mask).  A
  * node that sees nothing (an empty anc_mask and an empty prefix) gets zeros.
  * Prefix rows that no node sees, [sinks, prefix_len[b] - window], are not
- * read for the result and may hold anything.  One token of ordinary decoding
+ * read for the result and may hold anything.  A NaN in a query or in a key
+ * makes the rows that see it NaN.  Values that any node of the sequence sees,
+ * tree nodes' among them, have to be finite: they are multiplied by the zero
+ * weight of the nodes that do not see them.  One token of ordinary decoding
  * is a tree of one node.
  * The work is that of the visible keys.  Few rows (a decode step, a short
  * chain) run in one launch without a workspace, other bf16 calls with up to
  * 128 query heads per KV head on pairs of SMs, the rest on CUDA cores in
- * tiles.  Everything else as tree_attn_verify; in addition batch * hkv <=
- * 65535 and batch * hkv * s_max <= 2^30 (SPEC_ERR_UNSUPPORTED).
+ * tiles.  Softmax statistics, sums and accumulators are float32 in all of
+ * them; the SM pairs round each probability to bf16 for the product with V
+ * (half a step, 2^-8, as tree_attn_verify does), the others keep it to 2^-17
+ * or better.  Which kernel runs follows from the arguments on the host (shape,
+ * max_prefix, window, sinks), not from prefix_len, and every call's result is
+ * the same from run to run.  Everything else as tree_attn_verify; in addition
+ * batch * hkv <= 65535 and batch * hkv * s_max <= 2^30
+ * (SPEC_ERR_UNSUPPORTED; the size query answers such shapes with 0).
  *   workspace  device scratch of tree_attn_window_workspace_bytes() bytes
  *            (16-byte aligned, uninitialised; may be NULL when that size is
  *            0; calls that may overlap on the GPU, two captured graphs among
  *            them, need separate ones)
  *
  * tree_attn_verify_window_paged -- the same over a paged prefix cache with
- * the arguments of tree_attn_verify_paged.  Entries of blocks that hold no
- * visible position are not read (kv_pages_free drops them).
+ * the arguments of tree_attn_verify_paged (block_size a multiple of 128).
+ * Entries of blocks that hold no visible position are not read
+ * (kv_pages_free drops them).
  * ------------------------------------------------------------------ */
 size_t tree_attn_window_workspace_bytes(int dtype, int batch, int n_nodes, int hq, int hkv,
                                         int head_dim, int max_prefix, int window, int sinks);
@@ -670,7 +680,8 @@ int kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table, in
  *
  *   block_table [batch, max_blocks] int32: entry j of a sequence names the
  *            block of positions [j * block_size, (j + 1) * block_size);
- *            negative: none.  batch <= SPEC_PAGES_MAX_BATCH
+ *            negative: none.  batch <= SPEC_PAGES_MAX_BATCH.  Any block_size
+ *            here; the attention entry points take multiples of 128
  *   ref_count   [num_blocks] int32: the table entries that name a block, and
  *            whatever else the caller counts (a pinned prompt); <= 0: free
  *   prefix_len  [batch] int32

@@ -325,8 +325,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   join<float, D>(s_in, s_ml, pieces, per, row_at, out);
 }
 
-// bf16, for any number of keys: a CTA's warps stream blocks of 16 keys, each through buffers of its own (no CTA barrier
-// on the way), with a running max, and their results are weighed at the end.
+// bf16, for any number of keys: a CTA's warps stream blocks of 16 keys, each
+// through buffers of its own (no CTA barrier on the way), with a running max,
+// and their results are weighed at the end.
 // The next block's K is under way from the moment that the scores are done,
 // its V from the end of P V.  P goes into the second product as the sum of
 // two bf16 numbers, so that it is rounded to 2^-17 of itself.
@@ -725,7 +726,8 @@ int launch_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const v
 }  // namespace
 
 // CTAs a cluster: enough for 32 keys each (bf16: 64), but no more than run at
-// once (two a SM; clusters of 16 fit a GPC each, so that 256 CTAs in sixteens
+// once (two a SM, in float32 while a CTA's share is below some 150 keys of 128
+// dims; clusters of 16 fit a GPC each, so that 256 CTAs in sixteens
 // took 16 us where eights took 10).  Taken for every shape that the SM-pair
 // kernel does not take, as far as a f32 CTA's keys fit, and else by an
 // estimate of both kernels, ns: a wave of clusters costs its start and 21 a
@@ -736,7 +738,14 @@ int launch_few(const SvAttnShape &s, const SvAttnPlan &p, const void *q, const v
 // 9.9 / 14.5; batch 8: 6.9 / 12.4, 11 / 18, 27 / 39; batch 64: 21 / 60, 53 /
 // 87, 166 / 216; 8 nodes, batch 1: 7.3 / 10.8, 9.9 / 15.6, 15.1 / 15.0; batch
 // 8: 10.3 / 12.3, 16.8 / 17.7 (the estimate errs); 16 nodes, batch 8: 13.9 /
-// 12.4, 26 / 18; 60 nodes, batch 1: 10.1 / 11.2, 17.1 / 15.9, 41 / 21.  f32
+// 12.4, 26 / 18; 60 nodes, batch 1: 10.1 / 11.2, 17.1 / 15.9, 41 / 21.  Other
+// heads of 128, window 1024: 64/8, one node, batch 1: 7.7 / 16.6, batch 64: 57
+// / 90; 32 nodes, batch 1: 18.3 / 16.9; 16/16, 60 nodes, batch 1: 13.1 / 16.6,
+// batch 8: 56 / 30; 28/4, 8 nodes, batch 8: 17.9 / 17.1.  At head_dim 64 a key
+// has half the bytes and the other side's tile costs the same: 32/8, one node,
+// batch 64: 38 / 88, window 4000: 110 / 216.  The estimate is of 128 dims and
+// gives up too early there: 32/8, 8 nodes, batch 8: 13.3 / 18.1 (it takes the
+// SM pairs), batch 64: 74 / 88; 60 nodes, batch 1: 13.1 / 16.7.  f32
 // against the CUDA-core tiles: 5 nodes, 4 heads of 64, window 333: 5.4 / 12.6,
 // 4000: 9.5 / 28; 32/8 heads of 128, window 1024: one node 7.7 / 21.4, 60
 // nodes 72 / 92, batch 64 162 / 362.

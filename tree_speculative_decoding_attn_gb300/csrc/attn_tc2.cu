@@ -1,7 +1,10 @@
 // Tree attention for GQA groups with more than 128 query rows per KV head,
 // or trees of more than 64 nodes (up to 256), bf16 in, float32 softmax and
 // accumulation, head_dim 128, on pairs of SMs: tcgen05.mma.cta_group::2 with
-// M = 256, a persistent grid, and a stream-K split of the work.
+// M = 256, a persistent grid, and a stream-K split of the work.  The WIN
+// instances (a sliding window with sinks) take any number of rows and
+// head_dim 64 too; where they differ from this header, it says so or
+// Sched<true> does.
 //
 // "5.3 Medusa、EAGLE 与 MTP" (infra-guide), sections 3.1 and 8: every node
 // attends to the shared prefix and to its ancestors-or-self; "Medusa,
@@ -21,11 +24,20 @@
 // included, so ranges with more row-group starts hold fewer tiles.  No range
 // starts between two tree tiles, so the first tile of every part of a row
 // group (its first tree tile, holding the root, or a prefix tile) shows
-// every row at least one key.  A row group that lies wholly inside one
-// cluster's range is normalised and written out; the parts of a row group cut by range ends leave partials
-// (unnormalised O in bf16, running max in log2 units and row sum in
-// float32) in workspace slots (2c + 1 for the part cut at cluster c's range
-// end, 2c for the one cut at its start), merged by attn_tc2_combine_kernel.
+// every row at least one key (WIN: it may show a row none, see kUnseen).  A
+// row group that lies wholly inside one cluster's range is normalised and
+// written out; the parts of a row group cut by range ends leave partials
+// (unnormalised O in bf16, WIN: float32; running max in log2 units and row
+// sum in float32) in workspace slots (2c + 1 for the part cut at cluster c's
+// range end, 2c for the one cut at its start), merged by
+// attn_tc2_combine_kernel (WIN: attn_tc2_window_combine_kernel).
+//
+// P.  The second product takes P in V's type, so it is rounded to bf16 (half
+// a step, 2^-8 of each probability, like the output); the row sums take it
+// unrounded, in float32.  Against 64 bits the output is then off by 2.3e-3
+// (relative norm) where its own rounding alone gives 1.7e-3.  P as a sum of
+// two bf16 numbers (attn_few.cu) would take that away for eight more MMAs and
+// 64 more TMEM columns written a tile.
 //
 // Pair MMA.  The even CTA issues every MMA for both.  M = 256: each CTA
 // holds its own 128 query rows (Q in shared memory; S, P and O in its own

@@ -497,10 +497,10 @@ __global__ void __launch_bounds__(kThreads)
 // thread and load; REMAP: also renames the table's entries.  A unit is up to
 // kPiece vectors of one (move, K or V, layer, head); the CTAs take them in
 // turn.  Measured with the plan, eight loads in flight, streaming accesses and
-// up to sixteen CTAs a SM against four loads, plain accesses and eight: a
-// compaction that reads and writes 0.73 GB 113 us (6.5 TB/s, 0.96 of a plain
-// copy's rate) against 121, a reservation whose copies are 0.11 GB 20.6
-// against 23.4.
+// up to sixteen CTAs a SM in the grid (four of them resident: 64 registers a
+// thread) against four loads, plain accesses and eight: a compaction that
+// reads and writes 0.73 GB 113 us (6.5 TB/s, 0.96 of a plain copy's rate)
+// against 121, a reservation whose copies are 0.11 GB 20.6 against 23.4.
 constexpr int kCopyThreads = 256;
 constexpr int kInFlight = 8;
 constexpr int kPiece = kCopyThreads * kInFlight;

@@ -28,14 +28,16 @@
 // 32 nodes over 128256 bf16 tokens 14.7 us (16.8 MB, 1.1 TB/s: the two dependent
 // gathers then miss the TLB, 2.6, and the rows' integer sums, ten 32-bit
 // operations a value, take 3 to 6 where a SM holds two CTAs); eight trees of
-// 60 nodes whose siblings a drafter drew 19.9 (a rejected sibling costs 3.7 us:
-// its row pair 2.2, the exchange 0.6, the next test 0.8; keeping the rows in
-// shared memory from pass to pass gains nothing).  Kept: all the tests
-// that need no row at once, one thread a child (serial float64 tests cost 0.9
-// each); the whole CTA on the piece that holds the bonus (its own warp alone
-// took up to 20).  One cluster per sequence; each warp owns one contiguous piece
-// of the row, so the bonus is found from the per-warp sums by rereading one
-// warp's piece (a few KB, in L2), a vector a thread.
+// 60 nodes whose siblings a drafter drew 19 to 21 with the numbers drawn (a
+// rejected sibling costs 3.7 us: its row pair 2.2, the exchange 0.7, the next
+// test 0.8; keeping the rows in shared memory from pass to pass gains
+// nothing), in bf16 28 (eight products a vector, 132 bytes of them spilled at
+// 64 registers).  Kept: all the tests that need no row at once, one thread a
+// child (serial float64 tests cost 0.9 each); the whole CTA on the piece that
+// holds the bonus (its own warp alone took up to 20).  One cluster per
+// sequence; each warp owns one contiguous piece of the row, so the bonus is
+// found from the per-warp sums by rereading one warp's piece (a few KB, in
+// L2), a vector a thread.
 #include <type_traits>
 
 #include "common.cuh"
