@@ -188,7 +188,8 @@ int spec_build_tree(const int32_t *parents, const int32_t *rank, const int32_t *
  * Outputs as spec_build_tree.  An absent node is nobody's child, has depth
  * 0, position prefix_len, a mask of itself only and no child links, so
  * attention, acceptance and commit never reach it (its attention output is
- * computed but meaningless).
+ * computed but meaningless, and its V has to be finite: the other nodes
+ * multiply it by a weight of 0).
  * ------------------------------------------------------------------ */
 int spec_build_tree_batch(const int32_t *parents, const int32_t *n_valid, const int32_t *tok_in,
                           const int32_t *prefix_len, int batch, int n_nodes, int32_t *tok,
@@ -601,8 +602,11 @@ int spec_accept(int mode, const void *logits, const void *draft_logits, int dtyp
  * accepted, nothing subtracted), SPEC_DEV_BAD_PARENTS (links that disagree
  * with parents[]: the node is taken to have no further child),
  * SPEC_DEV_CAPACITY (a path longer than path_cap: the path ends there),
- * SPEC_DEV_BAD_PROB (a value outside [0, 1], NaN among them: counts as 0; or
- * a row to draw the bonus from whose sum is 0, or 4 and more: token 0).
+ * SPEC_DEV_BAD_PROB (a value outside [0, 1], NaN among them, in a test that
+ * the walk makes or a row that it sums: counts as 0; or a row to draw the
+ * bonus from whose sum is 0, or 4 and more: token 0).  Absent nodes
+ * (spec_build_tree_batch) and nodes that the walk does not get to may hold
+ * anything in tok, parents, the numbers and the rows.
  * ------------------------------------------------------------------ */
 int spec_verify_probs(const void *target_probs, const void *draft_probs, int dtype, int batch,
                       int n_nodes, int vocab, const int32_t *tok, const int32_t *parents,

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nc = gridDim.x, rank = blockIdx.x, b = blockIdx.y;  // the cluster spans x
-  bool bad = false;
+  bool bad = false, odd = false;  // odd: of this thread's node, whether the walk tests it or not
   if (tid == 0) {
     mbar_init(&sh.bar[0], 1);
     mbar_init(&sh.bar[1], 1);
@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     sh.tok[tid] = t;
     if (par >= 0 && par < N && t >= 0 && t < V) {
       const int64_t at = ((int64_t)b * N + par) * V + t;
-      sh.p[tid] = __uint_as_float(checked(__float_as_uint(sv::to_f32(p_all[at])), &bad));
-      sh.q[tid] = DRAFT ? __uint_as_float(checked(__float_as_uint(sv::to_f32(q_all[at])), &bad)) : 1.f;
+      sh.p[tid] = __uint_as_float(checked(__float_as_uint(sv::to_f32(p_all[at])), &odd));
+      sh.q[tid] = DRAFT ? __uint_as_float(checked(__float_as_uint(sv::to_f32(q_all[at])), &odd)) : 1.f;
       // drafter's siblings: the test of a first sibling
       sh.keep[tid] = (double)sh.u[tid] * (double)sh.q[tid] < (double)sh.p[tid];
     }
@@ -518,6 +518,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     for (int i = tid; i < path_cap; i += kThreads) acc_path[(int64_t)b * path_cap + i] = i <= sh.len ? sh.path[i] : -1;
+  }
+  if (odd && rank == 0) {  // reported if the walk has tested the node: a child of the path's, not past the kept one
+    const int par = sh.par[tid];
+    for (int i = 0; i <= sh.len; ++i) {
+      if (sh.path[i] != par) continue;
+      int c = sh.fc[par];
+      for (int n = 0; n < N && c >= 0 && c < N; ++n) {
+        bad = bad || c == tid;
+        if (i < sh.len && c == sh.path[i + 1]) break;
+        c = sh.ns[c];
+      }
+    }
   }
   if (bad) sv::report(status, SPEC_DEV_BAD_PROB);
   __syncwarp();
