@@ -78,3 +78,32 @@ def test_what_follows_the_call_comes_after_all_of_its_work(case, captured):
     assert int(t["status"].item()) == 0
     assert torch.equal(copy, t["out"])
     c.check(t)
+
+
+TOP = 2 ** 31 - 1
+SHAPES = [("bf16", 1, 8, 2, 128, 3), ("bf16", 6, 32, 4, 128, 60), ("bf16", 2, 24, 2, 64, 100), ("bf16", 1, 16, 2, 128, 60),
+          ("f32", 2, 4, 2, 64, 9)]
+
+
+@pytest.mark.parametrize("window,sinks", [(TOP, 0), (TOP, TOP), (1, TOP), (1, 0), (TOP - 1, 1), (40, 1 << 25)])
+@pytest.mark.parametrize("longest", [0, 1, 700, 4500])
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_the_ends_of_the_arguments(shape, longest, window, sinks):
+    """The largest and smallest windows and sinks, empty caches, and a scale
+    of the caller's."""
+    dtype, B, hq, hkv, D, n = SHAPES[shape]
+    prefix = [longest * (B - i) // B for i in range(B)]
+    tree = synth.chain(n) if n < 6 else R(70 + shape, n, (10, 4, 3, 2, 2) if n > 9 else (4, 3, 2))
+    for page in (0, 128):
+        c = Case(dtype, B, hq, hkv, D, prefix, tree, min(window, 10 ** 6), min(sinks, 10 ** 6), page, seed=500 + shape)
+        c.window, c.sinks = window, sinks
+        t = c.tensors()
+        c.call(t)
+        assert int(t["status"].item()) == 0
+        c.check(t)
+        # twice the scale on half the queries: the same products, bit for bit
+        want, t["q"] = t["out"].clone(), t["q"] * 0.5
+        f = sv.tree_attn_verify_window_paged if page else sv.tree_attn_verify_window
+        f(t["q"], t["k"], t["v"], *([t["table"]] if page else []), t["kt"], t["vt"], t["prefix"], t["depth"], t["anc"],
+          t["out"], c.mp, window, sinks=sinks, scale=2 * float(np.float32(1) / np.sqrt(np.float32(D))), workspace=t["ws"])
+        assert torch.equal(t["out"], want)

@@ -146,12 +146,13 @@ __global__ void __launch_bounds__(kWarps * 32)
     int kpos = 0;  // WIN: this lane's key's position
     if constexpr (WIN) {
       kpos = !tree ? t0 + lane : lane < nvalid ? P + sv::win_depth(win, (int64_t)b * N + t0 + lane, N) : 0;
-      // a key of the tile's first block that the root no longer sees: its V
-      // may be anything, and 0 * V has to be 0
-      if (!tree && t0 < span.lo) {
+      // the keys of the tile's first block that the root no longer sees: their
+      // V may be anything, and 0 * V has to be 0 (the rows are compared before
+      // they are scaled: sinks may be any int)
+      const int dead0 = max(t0, win.sinks), dead1 = min(span.lo, t0 + kKeyTile);
+      if (!tree && dead0 < dead1) {
         __syncthreads();
-        for (int e = threadIdx.x; e < (min(span.lo, t0 + kKeyTile) - max(t0, win.sinks)) * D; e += kWarps * 32)
-          sV[(max(t0, win.sinks) - t0) * D + e] = 0.f;
+        for (int e = threadIdx.x; e < (dead1 - dead0) * D; e += kWarps * 32) sV[(dead0 - t0) * D + e] = 0.f;
       }
     }
     __syncthreads();
