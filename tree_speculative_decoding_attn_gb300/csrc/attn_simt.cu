@@ -268,8 +268,7 @@ __global__ void __launch_bounds__(128)
   for (int s = 0; s < splits; ++s) {
     const float *w = w0 + s * sstride;
     const float ms = w[D];
-    if (ms == -INFINITY && w[D + 1] == 0.f) continue;  // (with a sum: of NaN)
-    const float f = exp2f(ms - M);
+    const float f = ms == -INFINITY ? 0.f : exp2f(ms - M);  // (nothing seen: zeros, or NaN and the sum of it)
     L = fmaf(f, w[D + 1], L);
 #pragma unroll
     for (int dd = 0; dd < DL; ++dd) acc[dd] = fmaf(f, w[lane + 32 * dd], acc[dd]);
