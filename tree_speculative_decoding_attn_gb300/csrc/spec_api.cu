@@ -17,6 +17,12 @@ inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
 }
+// Whether a pool has more rows than 32-bit indices count (the product of
+// three ints may pass 64 bits, so two come first).
+inline bool too_many_rows(int num_blocks, int hkv, int block_size) {
+  const long long most = 1 << 30, head = (long long)hkv * block_size;
+  return head > most || head * num_blocks > most;
+}
 // A buffer that may be its own input (the very same address), but not lie across it.
 inline bool same_or_apart(const void *a, const void *b, size_t n) { return a == b || !overlap(a, n, b, n); }
 
@@ -232,7 +238,7 @@ int tree_attn_verify_paged(const void *q, const void *k_pages, const void *v_pag
   if (!q || !k_pages || !v_pages || !block_table || !k_tree || !v_tree || !prefix_len || !anc_mask || !out)
     return SPEC_ERR_INVALID_ARG;
   if (block_size < 128 || block_size % 128 || num_blocks < 1 || max_blocks < 1) return SPEC_ERR_INVALID_ARG;
-  if ((long long)max_blocks * block_size > (1 << 30) || (long long)num_blocks * hkv * block_size > (1 << 30))
+  if ((long long)max_blocks * block_size > (1 << 30) || too_many_rows(num_blocks, hkv, block_size))
     return SPEC_ERR_UNSUPPORTED;
   const int s_max = max_blocks * block_size;
   int rc = attn_check(dtype, batch, n_nodes, hq, hkv, head_dim, s_max, max_prefix);
@@ -319,7 +325,7 @@ int tree_attn_verify_window_paged(const void *q, const void *k_pages, const void
                                   spec_stream_t stream) {
   if (!block_table || block_size < 128 || block_size % 128 || num_blocks < 1 || max_blocks < 1 || hkv < 1)
     return SPEC_ERR_INVALID_ARG;
-  if ((long long)max_blocks * block_size > (1 << 30) || (long long)num_blocks * hkv * block_size > (1 << 30))
+  if ((long long)max_blocks * block_size > (1 << 30) || too_many_rows(num_blocks, hkv, block_size))
     return SPEC_ERR_UNSUPPORTED;
   SvAttnShape s{dtype, batch, n_nodes, hq, hkv, head_dim, max_blocks * block_size, max_prefix};
   s.block_table = block_table;
@@ -502,7 +508,7 @@ int kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table, in
     return SPEC_ERR_INVALID_ARG;
   if (n_nodes > SPEC_MAX_NODES || path_cap > SPEC_MAX_NODES + 1) return SPEC_ERR_UNSUPPORTED;
   if ((head_dim * elem_bytes) % 16) return SPEC_ERR_UNSUPPORTED;
-  if ((long long)max_blocks * block_size > (1 << 30) || (long long)num_blocks * hkv * block_size > (1 << 30))
+  if ((long long)max_blocks * block_size > (1 << 30) || too_many_rows(num_blocks, hkv, block_size))
     return SPEC_ERR_UNSUPPORTED;
   if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_tree) || !aligned16(v_tree))
     return SPEC_ERR_INVALID_ARG;
@@ -559,8 +565,8 @@ static int pool_check(const void *k, const void *v, int elem_bytes, int n_layers
   if (elem_bytes != 2 && elem_bytes != 4) return SPEC_ERR_UNSUPPORTED;
   if (n_layers < 1 || hkv < 1 || head_dim < 1 || block_size < 1) return SPEC_ERR_INVALID_ARG;
   if (((long long)head_dim * elem_bytes) % 16) return SPEC_ERR_UNSUPPORTED;
-  if ((long long)max_blocks * block_size > (1 << 30) || (long long)hkv * block_size > (1 << 30) ||
-      (long long)num_blocks * hkv * block_size > (1 << 30) || head_dim > (1 << 20) || n_layers > (1 << 20))
+  if ((long long)max_blocks * block_size > (1 << 30) || too_many_rows(num_blocks, hkv, block_size) ||
+      head_dim > (1 << 20) || n_layers > (1 << 20))
     return SPEC_ERR_UNSUPPORTED;
   if (!aligned16(k) || !aligned16(v)) return SPEC_ERR_INVALID_ARG;
   return SPEC_OK;
