@@ -436,6 +436,102 @@ int tree_attn_verify_window_paged(const void *q, const void *k_pages, const void
                                   spec_stream_t stream);
 
 /* --------------------------------------------------------------------
+ * tree_attn_verify_latent -- tree_attn_verify for target models whose cache
+ * holds one latent vector a token, shared by all heads (the pages have no
+ * counterpart).  In the absorbed form the key projection is applied to the
+ * query and the value projection to the output, by the caller, so that
+ * queries, keys and outputs live in the latent space:
+ *   x_j = scale * q[b,i,h] . c_j (all latent_dim + rope_dim of them),
+ *   out[b,i,h] = softmax_j(x_j) c_j[0 .. latent_dim - 1] over
+ *   j in { cache rows 0 .. prefix_len[b]-1 } U { tree rows t : bit t of
+ *   anc_mask[b,i] }.
+ *   q        [batch, n_nodes, hq, latent_dim + rope_dim]   dtype
+ *   cache    [batch, s_max, latent_dim + rope_dim]         dtype (rows at and
+ *            past prefix_len are ignored and may hold anything)
+ *   tree     [batch, n_nodes, latent_dim + rope_dim]       dtype: the nodes'
+ *            rows (rotary already applied).  As with tree_attn_verify, their
+ *            latent parts have to be finite, those of absent nodes among them
+ *   out      [batch, n_nodes, hq, latent_dim]              dtype
+ *   scale    > 0 and finite (the head size that it comes from is not known
+ *            here)
+ * Requires latent_dim 256 or 512, rope_dim 64, 1 <= hq <= 128, n_nodes <=
+ * SPEC_MAX_NODES, batch <= 65535, batch * s_max and batch * n_nodes * hq <=
+ * 2^30 (SPEC_ERR_UNSUPPORTED).  A node that sees nothing gets zeros; a NaN
+ * score makes its row NaN.  One token of ordinary decoding is a tree of one
+ * node.  bf16 runs on pairs of SMs: softmax statistics, sums and accumulators
+ * are float32, and each probability is rounded to bf16 for the product with
+ * the values (half a step, 2^-8 of it).  float32 runs on CUDA cores.  Results
+ * are the same from run to run.  A prefix_len outside [0, max_prefix] sets
+ * SPEC_DEV_CAPACITY and that sequence's output is left unwritten.
+ *   workspace  device scratch of tree_attn_latent_workspace_bytes() bytes
+ *            (16-byte aligned, uninitialised; may be NULL when that size is
+ *            0; calls that may overlap on the GPU, two captured graphs among
+ *            them, need separate ones)
+ *
+ * tree_attn_verify_latent_paged -- the same over a paged cache
+ *   pages    [num_blocks, block_size, latent_dim + rope_dim], block_table
+ *            [batch, max_blocks] and block_size as tree_attn_verify_paged.
+ *
+ * The accepted path's rows are committed by kv_commit (kv_commit_paged,
+ * spec_accept_commit) with hkv = 1, head_dim = latent_dim + rope_dim, the
+ * cache as K and NULL for V; kv_pages_reserve and kv_pages_compact take such
+ * a pool the same way.
+ * ------------------------------------------------------------------ */
+size_t tree_attn_latent_workspace_bytes(int dtype, int batch, int n_nodes, int hq, int latent_dim,
+                                        int rope_dim, int max_prefix);
+int tree_attn_verify_latent(const void *q, const void *cache, const void *tree,
+                            const int32_t *prefix_len, const uint64_t *anc_mask, void *out, int dtype,
+                            int batch, int n_nodes, int hq, int latent_dim, int rope_dim, int s_max,
+                            int max_prefix, float scale, void *workspace, size_t workspace_bytes,
+                            int32_t *dev_status, spec_stream_t stream);
+int tree_attn_verify_latent_paged(const void *q, const void *pages, const int32_t *block_table,
+                                  int block_size, int num_blocks, int max_blocks, const void *tree,
+                                  const int32_t *prefix_len, const uint64_t *anc_mask, void *out,
+                                  int dtype, int batch, int n_nodes, int hq, int latent_dim,
+                                  int rope_dim, int max_prefix, float scale, void *workspace,
+                                  size_t workspace_bytes, int32_t *dev_status, spec_stream_t stream);
+
+/* --------------------------------------------------------------------
+ * prompt_attn_latent -- causal attention of prompt tokens in the expanded
+ * form: the caller has expanded the latents into keys and values of every
+ * head (one matrix product), the rotary key stays shared by the heads (the
+ * pages have no counterpart; with many query tokens a sequence this form
+ * needs a third of the absorbed form's operations).
+ * Requests are packed one behind the other: sequence b's queries are rows
+ * q_offsets[b] .. q_offsets[b+1] - 1 of q, its keys rows kv_offsets[b] ..
+ * kv_offsets[b+1] - 1 of k, k_rope and v.  The queries are its last tokens:
+ * query i of n sees keys 0 .. m - n + i of m (the kept beginning of the
+ * prompt, and the chunk up to itself).
+ *   x_j = scale * (q[i,h,0..127] . k[j,h] + q[i,h,128..191] . k_rope[j]),
+ *   out[i,h] = softmax_j(x_j) v[j,h]
+ *   q        [total_q, hq, 192] bf16
+ *   k, v     [total_kv, hq, 128] bf16: element strides k_token, k_head
+ *            (v_token, v_head) between tokens and heads, as of the two halves
+ *            of one projection's output
+ *   k_rope   [total_kv, 64] bf16, rope_token elements between tokens (a
+ *            column range of the latent rows)
+ *   q_offsets, kv_offsets [batch + 1] int32, not decreasing (as
+ *            kv_pages_slots writes them)
+ *   out      [total_q, hq, 128] bf16; rows of no sequence are left as they
+ *            were
+ *   max_q    host bound on a sequence's queries
+ * All strides are positive multiples of 8 (SPEC_ERR_INVALID_ARG), addresses
+ * 16-byte aligned.  head_dim 128 and rope_dim 64 (SPEC_ERR_UNSUPPORTED
+ * otherwise), hq <= 65535, batch <= 65535, total_q * hq <= 2^30, total_kv <=
+ * 2^30, at most 2^23 queries a sequence.  A query before the sequence's first key (n > m) gets zeros.  Offsets
+ * outside [0, total], a decreasing pair, or more than max_q queries set
+ * SPEC_DEV_CAPACITY and that sequence's output is left unwritten.  Values of
+ * a sequence have to be finite from its first key on, also those that a query
+ * does not see (they are multiplied by a weight of 0); rows of other
+ * sequences may hold anything.  Rounding as tree_attn_verify_latent.
+ * ------------------------------------------------------------------ */
+int prompt_attn_latent(const void *q, const void *k, int64_t k_token, int64_t k_head,
+                       const void *k_rope, int64_t rope_token, const void *v, int64_t v_token,
+                       int64_t v_head, const int32_t *q_offsets, const int32_t *kv_offsets, void *out,
+                       int batch, int hq, int head_dim, int rope_dim, int total_q, int total_kv,
+                       int max_q, float scale, int32_t *dev_status, spec_stream_t stream);
+
+/* --------------------------------------------------------------------
  * tree_attn_verify_noalloc -- tree_attn_verify without a caller workspace.
  * The pages have no counterpart to this entry point; it exists for callers
  * that cannot allocate device memory: a plugin inside a host runtime that
@@ -646,6 +742,9 @@ int spec_accept_commit(int mode, const void *logits, const void *draft_logits, i
  *   elem_bytes        2 (bf16) or 4 (f32); head_dim * elem_bytes % 16 == 0
  *   prefix_len_out    may equal prefix_len (each sequence's entry is
  *                     updated in place after its copies); may be NULL
+ *   v_cache, v_tree   both NULL: a cache of one pool (latent rows), of which
+ *                     K alone is copied (here, in kv_commit_paged and in
+ *                     spec_accept_commit)
  * A row past s_max or a path entry outside [0, n_nodes) sets a device
  * status and that sequence is neither copied nor advanced.
  * ------------------------------------------------------------------ */
@@ -733,8 +832,28 @@ int kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table, in
  *            be NULL; for holders outside the table)
  * Both outputs may be their inputs.
  *
+ * kv_pages_slots -- where packed tokens lie in the pool: sequence b brings
+ * new_len[b] tokens (< 0: none), packed one sequence behind the other, for
+ * positions prefix_len[b] .. prefix_len[b] + new_len[b] - 1.
+ *   offsets  [batch + 1] int32 out: first packed token of each sequence, then
+ *            their number (offsets stop at room)
+ *   slots    [room] int32 out: block * block_size + row of each token; -1 for
+ *            tokens that have no block (SPEC_DEV_BAD_BLOCK) or pass the table
+ *            (SPEC_DEV_CAPACITY), and behind the last token
+ *   positions [room] int32 out: each token's position (-1 behind the last and
+ *            past the table; may be NULL)
+ * More tokens than room: those past it are dropped (SPEC_DEV_CAPACITY).
+ * Outputs may not overlap inputs or one another (SPEC_ERR_INVALID_ARG).
+ *
+ * kv_slots_write, kv_slots_read -- rows [n_rows, hkv, head_dim] into their
+ * slots of one pool [num_blocks, hkv, block_size, head_dim] (a layer's K, V or
+ * latents), or out of them.  A negative slot: not written, read as zeros; a
+ * slot past the pool the same (SPEC_DEV_BAD_BLOCK).  A slot that is written
+ * twice in a call ends up with a mixture of its rows.
+ *
  * k_pages, v_pages [n_layers, num_blocks, hkv, block_size, head_dim] (16-byte
- * aligned, elem_bytes 2 or 4, head_dim * elem_bytes % 16 == 0).  workspace:
+ * aligned, elem_bytes 2 or 4, head_dim * elem_bytes % 16 == 0; v_pages NULL: a
+ * cache of one pool, as of latent rows).  workspace:
  * kv_pages_workspace_bytes() bytes, 16-byte aligned, uninitialised; calls
  * that may overlap on the GPU need separate ones.
  * ------------------------------------------------------------------ */
@@ -759,6 +878,16 @@ int kv_pages_compact(void *k_pages, void *v_pages, int elem_bytes, int n_layers,
                      int batch, int max_blocks, const int32_t *ref_count, int32_t *table_out,
                      int32_t *ref_count_out, int32_t *n_used, int32_t *remap, void *workspace,
                      size_t workspace_bytes, int32_t *dev_status, spec_stream_t stream);
+int kv_pages_slots(const int32_t *block_table, const int32_t *prefix_len, const int32_t *new_len,
+                   int batch, int max_blocks, int block_size, int num_blocks, int room,
+                   int32_t *offsets, int32_t *slots, int32_t *positions, int32_t *dev_status,
+                   spec_stream_t stream);
+int kv_slots_write(void *pages, const int32_t *slots, const void *rows, int elem_bytes, int n_rows,
+                   int hkv, int head_dim, int block_size, int num_blocks, int32_t *dev_status,
+                   spec_stream_t stream);
+int kv_slots_read(const void *pages, const int32_t *slots, void *rows, int elem_bytes, int n_rows,
+                  int hkv, int head_dim, int block_size, int num_blocks, int32_t *dev_status,
+                  spec_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -637,17 +637,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (cta == 0 && threadIdx.x == 0 && !fits) sv::report(status, SPEC_DEV_CAPACITY);
     if (fits) {
       const int n = len * cm.vec_per_row;  // vectors of one (layer, head) for K or V
-      const int total = 2 * cm.n_layers * cm.hkv * n;
+      const int total = (cm.vc ? 2 : 1) * cm.n_layers * cm.hkv * n;  // (a cache of one pool: K alone)
       const int nb = (int)gridDim.y;
 #pragma unroll 4
       for (int idx = (int)(cta * kThreads + threadIdx.x); idx < total; idx += nc * kThreads) {
         const int it = idx / n, e = idx - it * n;
         const int j = e / cm.vec_per_row, c = e - j * cm.vec_per_row;
-        const int lh = it >> 1;  // layer * hkv + head
+        const int lh = cm.vc ? it >> 1 : it;  // layer * hkv + head
+        const bool is_v = cm.vc && (it & 1);
         const int layer = lh / cm.hkv, h = lh % cm.hkv;
         const int64_t lb = ((int64_t)layer * nb + b) * cm.hkv + h;
-        const uint4 v = ((it & 1) ? cm.vt : cm.kt)[(lb * N + s_path[j]) * cm.vec_per_row + c];
-        ((it & 1) ? cm.vc : cm.kc)[(lb * cm.s_max + P + j) * cm.vec_per_row + c] = v;
+        const uint4 v = (is_v ? cm.vt : cm.kt)[(lb * N + s_path[j]) * cm.vec_per_row + c];
+        (is_v ? cm.vc : cm.kc)[(lb * cm.s_max + P + j) * cm.vec_per_row + c] = v;
       }
     }
   }

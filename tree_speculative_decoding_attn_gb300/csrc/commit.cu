@@ -55,17 +55,19 @@ __global__ void __launch_bounds__(kThreads)
     // every (K or V, layer, head, row, vector) in one index space, so all
     // of a thread's copies are in flight together
     const int n = (L + 1) * vec_per_row;  // vectors of one (layer, head) for K or V
-    const int total = 2 * n_layers * hkv * n;
+    const int pools = vc ? 2 : 1;  // (a cache of one pool: K alone)
+    const int total = pools * n_layers * hkv * n;
 #pragma unroll 4
     for (int idx = threadIdx.x; idx < total; idx += kThreads) {
       const int it = idx / n, e = idx - it * n;
       const int j = e / vec_per_row, c = e - j * vec_per_row;
-      const int lh = it >> 1;  // layer * hkv + head
+      const int lh = vc ? it >> 1 : it;  // layer * hkv + head
+      const bool is_v = vc && (it & 1);
       const int layer = lh / hkv, h = lh % hkv;
       const int64_t lb = ((int64_t)layer * batch + b) * hkv + h;
-      const uint4 v = ((it & 1) ? vt : kt)[(lb * N + s_path[j]) * vec_per_row + c];
+      const uint4 v = (is_v ? vt : kt)[(lb * N + s_path[j]) * vec_per_row + c];
       const int64_t dst = layer * layer_rows + s_row[j] + h * head_rows;
-      ((it & 1) ? vc : kc)[dst * vec_per_row + c] = v;
+      (is_v ? vc : kc)[dst * vec_per_row + c] = v;
     }
   }
   if (prefix_len_out && threadIdx.x == 0) prefix_len_out[b] = ok ? P + L + 1 : P;

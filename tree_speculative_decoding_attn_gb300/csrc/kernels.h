@@ -181,3 +181,36 @@ int sv_pages_compact(void *k, void *v, int vec_per_row, int n_layers, int hkv, i
                      const int32_t *table, int32_t *table_out, int batch, int max_blocks, const int32_t *ref,
                      int32_t *ref_out, int32_t *n_used, int32_t *remap, void *workspace, int32_t *status,
                      cudaStream_t stream);
+
+// Tree attention over a cache of latent rows (latent_tc.cu: bf16, SM pairs;
+// latent_simt.cu: float32).  A row is latent_dim + 64 elements.
+struct SvLatentShape {
+  int dtype, batch, n_nodes, hq, latent_dim, s_max, max_prefix;
+  // paged cache (block_table null: contiguous [batch, s_max, row])
+  const int32_t *block_table;
+  int block_size, max_blocks, num_blocks;
+};
+size_t sv_latent_simt_ws_bytes(const SvLatentShape &s);
+int sv_latent_simt(const SvLatentShape &s, const void *q, const void *cache, const void *tree,
+                   const int32_t *prefix_len, const uint64_t *anc, void *out, float scale, void *ws, int32_t *status,
+                   cudaStream_t stream);
+size_t sv_latent_tc_ws_bytes(const SvLatentShape &s);
+int sv_latent_tc(const SvLatentShape &s, const void *q, const void *cache, const void *tree, const int32_t *prefix_len,
+                 const uint64_t *anc, void *out, float scale, void *ws, int32_t *status, cudaStream_t stream);
+
+// Causal attention of packed prompt tokens over expanded keys and values
+// (prompt.cu).  Strides in elements.
+struct SvPromptShape {
+  int batch, hq, total_q, total_kv, max_q;
+  int64_t k_token, k_head, v_token, v_head, rope_token;
+};
+int sv_prompt_attn(const SvPromptShape &s, const void *q, const void *k, const void *k_rope, const void *v,
+                   const int32_t *q_offsets, const int32_t *kv_offsets, void *out, float scale, int32_t *status,
+                   cudaStream_t stream);
+
+// Packed tokens' rows of a paged cache (slots.cu).  vec = dim * elem_bytes / 16.
+int sv_pages_slots(const int32_t *table, const int32_t *prefix_len, const int32_t *new_len, int batch, int max_blocks,
+                   int block_size, int num_blocks, int room, int32_t *offsets, int32_t *slots, int32_t *positions,
+                   int32_t *status, cudaStream_t stream);
+int sv_slots_rows(bool write, void *pages, void *rows, const int32_t *slots, int T, int hkv, int block_size,
+                  int num_blocks, int vec, int32_t *status, cudaStream_t stream);

@@ -1,0 +1,221 @@
+// Tree attention over a cache of latent vectors on CUDA cores (float32).
+//
+// Row (node, head) has a query q in the latent space, a key is a cache or
+// tree row c = [latent ; rotary], a value its latent part:
+//   out = sum_j softmax_j(scale q . c_j) c_j[:LAT].
+// One CTA takes 8 rows and a range of the keys, 64 at a time.  Scores: a
+// warp holds one key row in registers (lanes over its dims) and multiplies it
+// with the 8 queries in shared memory.  Softmax: one warp a row, running
+// maximum and sum.  Values: a thread owns one or two of the latent dims for
+// all 8 rows.  Key ranges are joined by a second kernel.  What bounds it is
+// the float32 FMA rate (every key row is read once per 8 rows, from L1 the
+// second time); float32 caches are for exactness, not for speed.
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace {
+
+constexpr int kRows = 8, kKeys = 64, kThreads = 256, kRope = 64;
+constexpr float kLow = -3.0e38f;  // running maximum before the first key
+constexpr int kMaxSplits = 64;
+
+// A partial: LAT unnormalised sums, the maximum (log2 units), the sum of P.
+constexpr int partial_floats(int lat) { return lat + 4; }
+
+template <int LAT>
+__global__ void __launch_bounds__(kThreads)
+    latent_simt_kernel(const float *__restrict__ q, const float *__restrict__ cache, const float *__restrict__ tree,
+                       const int32_t *__restrict__ prefix_len, const uint64_t *__restrict__ anc,
+                       float *__restrict__ out, float *__restrict__ ws, int N, int hq, int s_max, int max_prefix,
+                       int chunk, float scale_log2, int32_t *status, const sv::KvPages pg) {
+  constexpr int D = LAT + kRope, PER = D / 32, VD = LAT / kThreads;
+  __shared__ float s_q[kRows][D];
+  __shared__ float s_p[kRows][kKeys];
+  __shared__ float s_alpha[kRows], s_l[kRows], s_m[kRows];
+  __shared__ int s_row[kKeys];  // cache row of a prefix key, -1 outside the pool
+  const int R = N * hq, b = blockIdx.z, split = blockIdx.y, row0 = blockIdx.x * kRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int P = prefix_len[b];
+  if (P < 0 || P > max_prefix || P > s_max) {
+    if (threadIdx.x == 0) sv::report(status, SPEC_DEV_CAPACITY);
+    return;
+  }
+  for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
+    const int r = e / D, d = e - r * D;
+    s_q[r][d] = row0 + r < R ? q[((int64_t)b * R + row0 + r) * D + d] : 0.f;
+  }
+  const int words = SPEC_MASK_WORDS(N), last = P + N;
+  const int k0 = split * chunk, k1 = min(last, k0 + chunk);
+  float acc[kRows][VD];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+#pragma unroll
+    for (int v = 0; v < VD; ++v) acc[r][v] = 0.f;
+  float m = kLow, l = 0.f;  // of row `warp`
+  for (int j0 = k0; j0 < k1; j0 += kKeys) {
+    const int n = min(kKeys, k1 - j0);
+    __syncthreads();  // the last tile's rows and P have been read
+    if (threadIdx.x < n) {
+      const int j = j0 + threadIdx.x;
+      s_row[threadIdx.x] = j < P ? sv::kv_row(pg, b, 1, 0, s_max, j, status) : 0;
+    }
+    __syncthreads();
+    auto key_row = [&](int j) -> const float * {
+      if (j0 + j >= P) return tree + ((int64_t)b * N + (j0 + j - P)) * D;
+      return s_row[j] < 0 ? nullptr : cache + (int64_t)s_row[j] * D;
+    };
+    for (int j = warp; j < n; j += kThreads / 32) {
+      const float *c = key_row(j);
+      float k[PER], dot[kRows];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) k[i] = c ? c[lane + 32 * i] : 0.f;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) s = fmaf(k[i], s_q[r][lane + 32 * i], s);
+        dot[r] = s;
+      }
+      // eight sums over 32 lanes, one left in each group of four lanes
+#pragma unroll
+      for (int step = 0; step < 3; ++step) {
+        const int o = 16 >> step, half = 4 >> step;
+#pragma unroll
+        for (int r = 0; r < half; ++r) {
+          const bool up = lane & o;
+          const float give = up ? dot[r] : dot[r + half];
+          dot[r] = (up ? dot[r + half] : dot[r]) + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      }
+      dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 2);
+      dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 1);
+      const int r = lane >> 2;
+      if ((lane & 3) == 0) {
+        bool see = row0 + r < R;
+        if (see && j0 + j >= P) {
+          const int t = j0 + j - P, node = (row0 + r) / hq;
+          see = (anc[((int64_t)b * N + node) * words + (t >> 6)] >> (t & 63)) & 1ull;
+        }
+        s_p[r][j] = see ? dot[0] * scale_log2 : -INFINITY;
+      }
+    }
+    __syncthreads();
+    {
+      const float x0 = lane < n ? s_p[warp][lane] : -INFINITY, x1 = lane + 32 < n ? s_p[warp][lane + 32] : -INFINITY;
+      const float mt = fmaxf(sv::warp_max(fmaxf(x0, x1)), m);
+      const float p0 = exp2f(x0 - mt), p1 = exp2f(x1 - mt), a = exp2f(m - mt);
+      l = l * a + sv::warp_sum(p0 + p1);
+      m = mt;
+      s_p[warp][lane] = p0;
+      s_p[warp][lane + 32] = p1;
+      if (lane == 0) s_alpha[warp] = a;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int v = 0; v < VD; ++v) acc[r][v] *= s_alpha[r];
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const float *c = key_row(j);
+#pragma unroll
+      for (int v = 0; v < VD; ++v) {
+        const float x = c ? c[threadIdx.x + v * kThreads] : 0.f;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) acc[r][v] = fmaf(s_p[r][j], x, acc[r][v]);
+      }
+    }
+  }
+  if (lane == 0) {
+    s_l[warp] = l;
+    s_m[warp] = m;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const int64_t row = (int64_t)b * R + row0 + r;
+    if (row0 + r >= R) break;
+    if (gridDim.y == 1) {
+      const float inv = s_l[r] == 0.f ? 0.f : 1.f / s_l[r];  // a row that sees nothing: zeros
+#pragma unroll
+      for (int v = 0; v < VD; ++v) out[row * LAT + threadIdx.x + v * kThreads] = acc[r][v] * inv;
+    } else {
+      float *w = ws + (row * gridDim.y + split) * partial_floats(LAT);
+#pragma unroll
+      for (int v = 0; v < VD; ++v) w[threadIdx.x + v * kThreads] = acc[r][v];
+      if (threadIdx.x == 0) {
+        w[LAT] = s_m[r];
+        w[LAT + 1] = s_l[r];
+      }
+    }
+  }
+}
+
+// One CTA a row: the key ranges' sums, weighted by their maxima.
+template <int LAT>
+__global__ void __launch_bounds__(128)
+    latent_simt_join_kernel(const float *__restrict__ ws, float *__restrict__ out, const int32_t *__restrict__ prefix_len,
+                            int R, int splits, int s_max, int max_prefix) {
+  const int64_t row = blockIdx.x;
+  const int P = prefix_len[row / R];
+  if (P < 0 || P > max_prefix || P > s_max) return;  // reported by the main kernel
+  const float *w = ws + row * splits * partial_floats(LAT);
+  float m = kLow, l = 0.f, acc[LAT / 128];
+#pragma unroll
+  for (int v = 0; v < LAT / 128; ++v) acc[v] = 0.f;
+  for (int s = 0; s < splits; ++s) m = fmaxf(m, w[(int64_t)s * partial_floats(LAT) + LAT]);
+  for (int s = 0; s < splits; ++s) {
+    const float *p = w + (int64_t)s * partial_floats(LAT);
+    const float a = exp2f(p[LAT] - m);
+    l += a * p[LAT + 1];
+#pragma unroll
+    for (int v = 0; v < LAT / 128; ++v) acc[v] = fmaf(a, p[threadIdx.x + 128 * v], acc[v]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int v = 0; v < LAT / 128; ++v) out[row * LAT + threadIdx.x + 128 * v] = acc[v] * inv;
+}
+
+// Ranges of keys: enough CTAs for the GPU's 152 SMs twice, no range under a
+// tile.
+int splits_of(const SvLatentShape &s, int *chunk) {
+  const long long ctas = (long long)s.batch * ((s.n_nodes * s.hq + kRows - 1) / kRows);
+  const int tiles = (s.max_prefix + s.n_nodes + kKeys - 1) / kKeys;
+  long long n = (304 + ctas - 1) / ctas;
+  n = n > tiles ? tiles : n > kMaxSplits ? kMaxSplits : n;
+  *chunk = (tiles + (int)n - 1) / (int)n * kKeys;
+  return (s.max_prefix + s.n_nodes + *chunk - 1) / *chunk;
+}
+
+template <int LAT>
+int launch(const SvLatentShape &s, const void *q, const void *cache, const void *tree, const int32_t *prefix_len,
+           const uint64_t *anc, void *out, float scale, void *ws, int32_t *status, cudaStream_t stream) {
+  int chunk;
+  const int splits = splits_of(s, &chunk), R = s.n_nodes * s.hq;
+  latent_simt_kernel<LAT><<<dim3((R + kRows - 1) / kRows, splits, s.batch), kThreads, 0, stream>>>(
+      (const float *)q, (const float *)cache, (const float *)tree, prefix_len, anc, (float *)out, (float *)ws,
+      s.n_nodes, s.hq, s.s_max, s.max_prefix, chunk, scale * 1.4426950408889634f, status,
+      sv::KvPages{s.block_table, s.block_size, s.max_blocks, s.num_blocks});
+  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  if (splits == 1) return SPEC_OK;
+  latent_simt_join_kernel<LAT><<<s.batch * R, 128, 0, stream>>>((const float *)ws, (float *)out, prefix_len, R, splits,
+                                                               s.s_max, s.max_prefix);
+  return sv_launch_status();
+}
+
+}  // namespace
+
+size_t sv_latent_simt_ws_bytes(const SvLatentShape &s) {
+  int chunk;
+  const int splits = splits_of(s, &chunk);
+  return splits == 1 ? 0 : (size_t)s.batch * s.n_nodes * s.hq * splits * partial_floats(s.latent_dim) * 4;
+}
+
+int sv_latent_simt(const SvLatentShape &s, const void *q, const void *cache, const void *tree,
+                   const int32_t *prefix_len, const uint64_t *anc, void *out, float scale, void *ws, int32_t *status,
+                   cudaStream_t stream) {
+  return (s.latent_dim == 512 ? launch<512> : launch<256>)(s, q, cache, tree, prefix_len, anc, out, scale, ws, status,
+                                                           stream);
+}

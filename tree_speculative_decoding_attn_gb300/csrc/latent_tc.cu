@@ -1,0 +1,762 @@
+// Tree attention over a cache of latent vectors on pairs of SMs (bf16 in,
+// float32 softmax and accumulation).
+//
+// A key is a row c = [latent (LAT) ; rotary (64)], a value its latent part;
+// a query row is (node, head), already in the latent space:
+//   x_j = scale q . c_j over the LAT + 64 dims,  out = sum_j softmax(x)_j c_j[:LAT].
+// All heads and nodes of a sequence share every key, so they are rows of one
+// product: 2 (2 LAT + 64) flops a row and key for 2 (LAT + 64) bytes a key,
+// tensor-bound from about 150 rows a sequence on, HBM-bound below.
+//
+// What fits decides the shape.  LAT = 512 output columns of 128 rows would
+// fill one SM's TMEM and leave nothing for S, and 128 query rows of 576 dims
+// are 144 KB of shared memory.  So a CTA holds 64 rows, and a pair MMA of M =
+// 128 (cta_group::2) gives them the full rate: rows 0-63 of a pair lie in the
+// even CTA, and each CTA's lanes 0-63 hold the columns of the first half of N,
+// lanes 64-127 those of the second.  Measured: M128 N128 K16 33 cycles, M128
+// N256 K16 65 (4096 bf16 multiply-adds a cycle and SM, the peak), issued by
+// one elected thread; the single-CTA M = 64 forms run at half of that.
+//   S(g)  = Q K(g)^T   N = 128 keys (64 in each CTA), K = LAT + 64
+//   O    += P(g) V(g)  N = 256 dims (128 in each CTA), K = 128 keys, LAT/256
+//                      of them; P in shared memory
+// K and V are the same rows, but the pair splits S by keys and O by dims, so
+// V is loaded again (the second time from L2).  Every stage of a tile has a
+// place of its own that the next tile refills as soon as the MMAs that read
+// it are done: a whole tile (2258 cycles of MMAs) for a load to arrive.
+//
+// Shared memory (LAT 512): Q 72 KB, K 72, V 64, P 16.  TMEM: O LAT/2 columns,
+// two S buffers of 64.
+// Roles: warp 0 loads K, 2 V, 3 Q; warp 1 of the even CTA issues all MMAs;
+// warps 4-7 softmax and epilogue: a thread owns 64 keys of one row (lane r and
+// lane r + 64 share row r).  S(g + 1) is issued before P(g) is awaited, so the
+// softmax of a tile runs under the next tile's S and the last one's PV.
+// Work: all (sequence, 128-row tile) units, each its tree tiles and then its
+// prefix tiles of 128 keys, are cut into one equal range a pair; units cut
+// between pairs leave float32 partials that a second kernel joins.
+// Every wait is bounded.
+#include <cuda.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace {
+
+using namespace sv::ptx;
+
+constexpr int kBN = 128, kRope = 64, kThreads = 256, kPairs = 76;
+constexpr uint32_t kPiece = 64 * 128;  // 64 rows (or keys) x 64 elements, 128-byte swizzle
+constexpr uint32_t kStage = 2 * kPiece;
+constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr int kSegW = 3;          // a unit's fixed cost, in tiles
+constexpr float kLow = -3.0e38f;  // running maximum before the first key
+constexpr float kTau = 16.f;      // the maximum moves when a tile exceeds it by more than 2^kTau
+
+template <int LAT> struct Cfg {
+  static constexpr int D = LAT + kRope;
+  static constexpr int KS = LAT / 128 + 1;      // K stages of a tile (the last: rotary dims, half a stage)
+  static constexpr int VS = LAT / 256 * 2;      // V stages
+  static constexpr int NB = LAT == 512 ? 1 : 2; // tiles of stages
+  static constexpr uint32_t q_bytes = (D / 64) * kPiece;
+  static constexpr uint32_t k_bytes = (LAT / 64 + 1) * kPiece;  // of one tile
+  static constexpr uint32_t v_bytes = VS * kStage;
+};
+
+template <int LAT> struct Bars {
+  using C = Cfg<LAT>;
+  // (full, p, ofree: the even CTA's count for both)
+  uint64_t kfull[C::NB * C::KS], kempty[C::NB * C::KS], vfull[C::NB * C::VS], vempty[C::NB * C::VS];
+  uint64_t qfull, qempty, sfull[2], p, pv, ofree, vland, drain;
+  long long lo, hi, b0;
+  int b;
+  uint32_t tmem;
+  volatile int abort;
+  float xmax[2][128];
+};
+template <int LAT> constexpr uint32_t smem_bytes() {
+  using C = Cfg<LAT>;
+  return C::q_bytes + 2 * kPiece + C::NB * (C::k_bytes + C::v_bytes) + sizeof(Bars<LAT>) + 1024;
+}
+static_assert(smem_bytes<512>() <= 232448 && smem_bytes<256>() <= 232448, "shared memory per CTA exceeds 227 KB");
+
+constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // Q, K both K-major
+constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 256, 0, 1);  // V is MN-major (dims contiguous)
+constexpr uint32_t kColS = 256;
+
+// A partial slot: 128 rows of LAT float32 sums, then 128 (maximum, sum) pairs.
+__host__ __device__ constexpr size_t slot_floats(int lat) { return 128 * (size_t)lat + 256; }
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+// TMA load into this CTA whose bytes count on a barrier of the pair's even CTA.
+__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+// Arrive on a barrier of the cluster, after this thread's (and, behind a
+// __syncwarp, its warp's) writes for every CTA of the cluster.
+__device__ __forceinline__ void arrive_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_acquire(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait that also ends once another role of the CTA has given up; its
+// outcome is one for the warp.
+template <class B> __device__ __forceinline__ bool wait(B *bars, uint64_t *bar, uint32_t parity) {
+  bool ok = false;
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if ((ok = try_wait_acquire(bar, parity))) break;
+    if ((i & 63) == 63 && bars->abort) break;
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) bars->abort = 1;
+  return ok;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+
+struct Work {
+  const int32_t *prefix_len;
+  int batch, N, hq, s_max, max_prefix, RT, tree_tiles;
+  __device__ int prefix(int b) const { return __ldg(prefix_len + b); }
+  __device__ bool fits(int P) const { return P >= 0 && P <= max_prefix && P <= s_max; }
+  // tiles of a unit of sequence b (0: its prefix length is refused)
+  __device__ int tiles(int b) const {
+    const int P = prefix(b);
+    return fits(P) ? tree_tiles + (P + kBN - 1) / kBN : 0;
+  }
+};
+// The segments of a pair's range in order: tiles [t0, t1) of T of a unit.
+struct Walk {
+  long long pos, end, b0;
+  int b, rt, t0, t1, T, P;
+  __device__ bool next(const Work &w) {
+    while (pos < end && b < w.batch) {
+      T = w.tiles(b);
+      P = w.prefix(b);
+      const int wu = T + kSegW;
+      rt = (int)((pos - b0) / wu);
+      const long long u0 = b0 + (long long)rt * wu, u1 = u0 + wu, stop = end < u1 ? end : u1;
+      t0 = (int)max(0ll, pos - u0 - kSegW);
+      t1 = T ? (int)max(0ll, stop - u0 - kSegW) : 0;
+      pos = stop;
+      if (stop == u1 && rt == w.RT - 1) {
+        ++b;
+        b0 = u1;
+        if (t1 > t0) {
+          --b;         // the caller reads this unit's sequence; step over it on the next call
+          step = true;
+          return true;
+        }
+        continue;
+      }
+      if (t1 > t0) return true;
+    }
+    return false;
+  }
+  bool step;
+  __device__ bool advance(const Work &w) {
+    if (step) {
+      step = false;
+      ++b;
+    }
+    return next(w);
+  }
+};
+
+template <int LAT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    latent_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
+                     const __grid_constant__ CUtensorMap tm_t, const Work w, const uint64_t *__restrict__ anc,
+                     __nv_bfloat16 *__restrict__ out, float *__restrict__ ws, int4 *__restrict__ desc,
+                     float scale_log2, int row_end, int32_t *status, const sv::KvPages pg) {
+  using C = Cfg<LAT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sQ = smem, *sP = sQ + C::q_bytes, *sK = sP + 2 * kPiece, *sV = sK + C::NB * C::k_bytes;
+  Bars<LAT> *bars = reinterpret_cast<Bars<LAT> *>(sV + C::NB * C::v_bytes);
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int R = w.N * w.hq;
+
+  grid_dep_launch();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NB * C::KS; ++i) {
+      mbar_init(&bars->kfull[i], 1);
+      mbar_init(&bars->kempty[i], 1);
+    }
+    for (int i = 0; i < C::NB * C::VS; ++i) {
+      mbar_init(&bars->vfull[i], 1);
+      mbar_init(&bars->vempty[i], 1);
+    }
+    mbar_init(&bars->qfull, 1);
+    mbar_init(&bars->qempty, 1);
+    mbar_init(&bars->sfull[0], 1);
+    mbar_init(&bars->sfull[1], 1);
+    mbar_init(&bars->p, 8);      // the softmax warps of both CTAs
+    mbar_init(&bars->pv, 1);
+    mbar_init(&bars->ofree, 8);
+    mbar_init(&bars->vland, 1);
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) tmem_alloc_pair(&bars->tmem, 512);
+  if (warp == 0) {
+    // this pair's range of the whole work, and the sequence that it starts in
+    long long total = 0;
+    for (int s = 0; s < w.batch; s += 32) {
+      const int b = s + lane;
+      const int T = b < w.batch ? w.tiles(b) : 0;
+      if (b < w.batch && !w.fits(w.prefix(b)) && blockIdx.x == 0) sv::report(status, SPEC_DEV_CAPACITY);
+      total += b < w.batch ? (long long)w.RT * (T + kSegW) : 0;
+    }
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    // (no more ranges than weight: each that begins inside a unit has a tile)
+    const long long n = total < pairs ? total : pairs;
+    const long long lo = pair < n ? total * pair / n : total, hi = pair < n ? total * (pair + 1) / n : total;
+    if (pair >= n && lane == 0) {
+      bars->lo = bars->hi = bars->b0 = 0;
+      bars->b = 0;
+      if (rank == 0) desc[pair] = make_int4(0, 0, 0, 0);
+    }
+    long long base = 0;
+    for (int s = 0; s < w.batch; s += 32) {
+      const int b = s + lane;
+      const int T = b < w.batch ? w.tiles(b) : 0;
+      const long long mine = b < w.batch ? (long long)w.RT * (T + kSegW) : 0;
+      long long up = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += v;
+      }
+      const long long first = base + up - mine;
+      if (b < w.batch && first <= lo && lo < first + mine) {
+        bars->lo = lo;
+        bars->hi = hi;
+        bars->b0 = first;
+        bars->b = b;
+        if (rank == 0) {
+          // the first range end inside a cut unit names the unit and its parts
+          int4 d = make_int4(0, 0, 0, 0);
+          const int wu = T + kSegW;
+          const int rt = (int)((lo - first) / wu);
+          const long long t_start = first + (long long)rt * wu + kSegW;  // where the unit's first tile weighs
+          if (T > 0 && lo > t_start && total * (pair - 1) / n <= t_start) {
+            int e = pair;
+            while (e + 1 < n && total * (e + 1) / n < t_start + T) ++e;
+            d = make_int4(b, rt, e - pair + 2, 1);
+          }
+          desc[pair] = d;
+        }
+      }
+      base += __shfl_sync(0xffffffffu, up, 31);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  Walk walk;
+  walk.pos = bars->lo;
+  walk.end = bars->hi;
+  walk.b0 = bars->b0;
+  walk.b = bars->b;
+  walk.step = false;
+  bool ok = true;
+
+  // The cache row of prefix key `key` (its 64 keys lie in one block; a bad
+  // block reads rows past the end: zeros).
+  auto cache_row = [&](int b, int key) {
+    const int row = sv::kv_row(pg, b, 1, 0, w.s_max, key, status);
+    return row < 0 ? row_end : row;
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- K
+    const bool me = elect_one();
+    if (me) {
+      tma_prefetch_desc(&tm_c);
+      tma_prefetch_desc(&tm_t);
+    }
+    int g = 0;
+    while (ok && walk.advance(w)) {
+      for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
+        const bool tree = t < w.tree_tiles;
+        const int row = tree ? t * kBN + (int)rank * 64 : cache_row(walk.b, (t - w.tree_tiles) * kBN + (int)rank * 64);
+        const int buf = g % C::NB;
+        const uint32_t par = ((g / C::NB) & 1) ^ 1;
+        for (int i = 0; ok && i < C::KS; ++i) {
+          const int s = buf * C::KS + i;
+          if (!(ok = wait(bars, &bars->kempty[s], par))) break;
+          if (me) {
+            uint8_t *dst = sK + buf * C::k_bytes + i * kStage;
+            const int pieces = i < C::KS - 1 ? 2 : 1;
+            if (rank == 0) mbar_expect_tx(&bars->kfull[s], 2 * pieces * kPiece);
+            const uint32_t bar = mapa_cluster(&bars->kfull[s], 0);
+            for (int h = 0; h < pieces; ++h) {
+              if (tree) load_3d(dst + h * kPiece, &tm_t, i * 128 + h * 64, row, walk.b, bar);
+              else load_2d(dst + h * kPiece, &tm_c, i * 128 + h * 64, row, bar);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- V
+    const bool me = elect_one();
+    int g = 0;
+    while (ok && walk.advance(w)) {
+      for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
+        const bool tree = t < w.tree_tiles;
+        const int row = tree ? t * kBN : cache_row(walk.b, (t - w.tree_tiles) * kBN);
+        const int buf = g % C::NB;
+        const uint32_t par = ((g / C::NB) & 1) ^ 1;
+        for (int i = 0; ok && i < C::VS; ++i) {
+          // stage i: dims [256 (i / 2) + 128 rank, +128) of keys [64 (i % 2), +64)
+          const int s = buf * C::VS + i;
+          if (!(ok = wait(bars, &bars->vempty[s], par))) break;
+          if (me) {
+            uint8_t *dst = sV + buf * C::v_bytes + i * kStage;
+            if (rank == 0) mbar_expect_tx(&bars->vfull[s], 2 * kStage);
+            const uint32_t bar = mapa_cluster(&bars->vfull[s], 0);
+            const int d0 = (i >> 1) * 256 + (int)rank * 128, r0 = row + (i & 1) * 64;
+            for (int h = 0; h < 2; ++h) {
+              if (tree) load_3d(dst + h * kPiece, &tm_t, d0 + h * 64, r0, walk.b, bar);
+              else load_2d(dst + h * kPiece, &tm_c, d0 + h * 64, r0, bar);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- Q
+    const bool me = elect_one();
+    for (int seg = 0; ok && walk.advance(w); ++seg) {
+      if (!(ok = wait(bars, &bars->qempty, (seg & 1) ^ 1))) break;
+      if (me) {
+        if (rank == 0) mbar_expect_tx(&bars->qfull, 2 * C::q_bytes);
+        const uint32_t bar = mapa_cluster(&bars->qfull, 0);
+        for (int i = 0; i < C::D / 64; ++i)
+          load_3d(sQ + i * kPiece, &tm_q, i * 64, walk.rt * 128 + (int)rank * 64, walk.b, bar);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs
+    if (rank == 0) {
+      const uint32_t qa = smem_u32(sQ), ka = smem_u32(sK), va = smem_u32(sV), pa = smem_u32(sP);
+      int g = 0, seg = 0;  // tiles whose S is issued; segments begun
+      bool more = walk.advance(w);
+      int t = walk.t0;
+      // S of tile (walk, t); the last of a segment lets Q go
+      auto issue_s = [&]() -> bool {
+        if (t == walk.t0 && !wait(bars, &bars->qfull, seg & 1)) return false;
+        const int buf = g % C::NB;
+        const uint32_t par = (g / C::NB) & 1, d = tmem + kColS + (g & 1) * 64;
+#pragma unroll
+        for (int i = 0; i < C::KS; ++i) {
+          if (!wait(bars, &bars->kfull[buf * C::KS + i], par)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t kb = ka + buf * C::k_bytes + i * kStage, qb = qa + i * kStage;
+#pragma unroll
+            for (int k = 0; k < (i < C::KS - 1 ? 8 : 4); ++k) {
+              const uint32_t off = (k >> 2) * kPiece + (k & 3) * 32;
+              mma_ss_pair(d, smem_desc_sw128(qb + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024), kIdescS,
+                          i > 0 || k > 0);
+            }
+            mma_commit_pair_mc(&bars->kempty[buf * C::KS + i], 3);
+            if (i == C::KS - 1) {
+              mma_commit_pair_mc(&bars->sfull[g & 1], 3);
+              if (t == walk.t1 - 1) mma_commit_pair_mc(&bars->qempty, 3);
+            }
+          }
+          __syncwarp();
+        }
+        return true;
+      };
+      if (more) ok = issue_s();
+      while (ok && more) {
+        // tile `g`: what PV needs to know of it, then S of the tile after it
+        const bool start = t == walk.t0;
+        const int keys = t < w.tree_tiles ? kBN : min(kBN, walk.P - (t - w.tree_tiles) * kBN);
+        const int cur = g, cur_seg = seg;
+        if (++t >= walk.t1) {
+          more = walk.advance(w);
+          t = walk.t0;
+          ++seg;
+        }
+        ++g;
+        if (more && !(ok = issue_s())) break;
+        const int buf = cur % C::NB;
+        const uint32_t par = (cur / C::NB) & 1;
+        if (keys < kBN) {
+          // the softmax warps clear the V rows past the last key, once they are there
+          for (int i = 0; ok && i < C::VS; ++i) ok = wait(bars, &bars->vfull[buf * C::VS + i], par);
+          if (!ok) break;
+          if (elect_one()) {
+            arrive_release(mapa_cluster(&bars->vland, 0));
+            arrive_release(mapa_cluster(&bars->vland, 1));
+          }
+          __syncwarp();
+        }
+        if (!(ok = wait(bars, &bars->p, cur & 1))) break;
+        // the last segment's O has been read
+        if (start && cur_seg > 0 && !(ok = wait(bars, &bars->ofree, (cur_seg - 1) & 1))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < C::VS; ++i) {
+          if (!(ok = wait(bars, &bars->vfull[buf * C::VS + i], par))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t vb = va + buf * C::v_bytes + i * kStage, pb = pa + (i & 1) * kPiece;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ss_pair(tmem + (i >> 1) * 128, smem_desc_sw128(pb + k * 32, 16, 1024),
+                          smem_desc_sw128(vb + k * 2048, kPiece, 1024), kIdescPV, !start || (i & 1) || k > 0);
+            mma_commit_pair_mc(&bars->vempty[buf * C::VS + i], 3);
+            if (i == C::VS - 1) mma_commit_pair_mc(&bars->pv, 3);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) {  // let issued MMAs finish before TMEM is freed
+        if (elect_one()) mma_commit_pair_mc(&bars->drain, 1);
+        __syncwarp();
+        mbar_wait(&bars->drain, 0, kWaitLimit);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax
+    const int quarter = warp & 3, L = quarter * 32 + lane, r = L & 63, half = L >> 6;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t p_bar = mapa_cluster(&bars->p, 0), ofree_bar = mapa_cluster(&bars->ofree, 0);
+    auto row_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (quarter & 1)) : "memory"); };
+    const int words = SPEC_MASK_WORDS(w.N);
+    int g = 0, ragged = 0;
+    while (walk.advance(w)) {
+      const int row = walk.rt * 128 + (int)rank * 64 + r;
+      const bool row_ok = row < R;
+      const uint64_t *mask = anc + ((int64_t)walk.b * w.N + (row_ok ? row / w.hq : 0)) * words;
+      float m = kLow, l = 0.f;
+      for (int t = walk.t0; t < walk.t1; ++t, ++g) {
+        if (ok) ok = wait(bars, &bars->sfull[g & 1], (g >> 1) & 1);
+        uint32_t x[2][32];
+        if (ok) {
+          tc_fence_after();
+          const uint32_t s = tmem + lane_off + kColS + (g & 1) * 64;
+          tmem_ld32(s, x[0]);
+          tmem_ld32(s + 32, x[1]);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) x[i >> 5][i & 31] = 0;
+        }
+        // which of this thread's 64 keys the row sees
+        const bool tree = t < w.tree_tiles;
+        const int left = (tree ? w.N - t * kBN : walk.P - (t - w.tree_tiles) * kBN) - half * 64;
+        uint64_t vis = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0ull;
+        if (tree && left > 0) vis &= row_ok ? mask[2 * t + half] : 0ull;
+        if (__any_sync(0xffffffffu, vis != ~0ull)) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (!((vis >> i) & 1)) x[i >> 5][i & 31] = 0xff800000u;  // -inf
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          mx[i & 3] = fmax3(mx[i & 3], __uint_as_float(x[i >> 4][(2 * i) & 31]),
+                            __uint_as_float(x[i >> 4][(2 * i + 1) & 31]));
+        mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        bars->xmax[g & 1][L] = mx[0];
+        row_sync();
+        const float mt = fmaxf(mx[0], bars->xmax[g & 1][L ^ 64]) * scale_log2;
+        const bool need = mt > m + kTau;
+        if (__any_sync(0xffffffffu, need)) {
+          const float a = need ? ex2(m - mt) : 1.f;
+          if (need) {
+            m = mt;
+            l *= a;
+          }
+          if (t > walk.t0 && ok && (ok = wait(bars, &bars->pv, (g - 1) & 1))) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < LAT / 2; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tmem + lane_off + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st16(tmem + lane_off + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // P = 2^(x scale - m), rounded to bf16 for the product (2^-8 of each
+        // weight, either way); the row sum takes it unrounded
+        const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m, -m);
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float2 e = fma2(make_float2(__uint_as_float(x[i >> 4][(2 * i) & 31]),
+                                      __uint_as_float(x[i >> 4][(2 * i + 1) & 31])), sc, nm);
+          e = make_float2(ex2(e.x), ex2(e.y));
+          acc[i & 3] = add2(acc[i & 3], e);
+          pk[i] = pack_bf16(e.x, e.y);
+        }
+        const float2 sum = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+        l += sum.x + sum.y;
+        if (g > 0 && ok) ok = wait(bars, &bars->pv, (g - 1) & 1);  // the last P has been read
+        if (ok) {
+          uint8_t *dst = sP + half * kPiece + r * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4 *>(dst + ((c ^ (r & 7)) << 4)) =
+                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        }
+        const int keys = tree ? kBN : min(kBN, walk.P - (t - w.tree_tiles) * kBN);
+        if (keys < kBN) {
+          // rows past the prefix may hold anything, NaN among it: cleared
+          if (ok) ok = wait(bars, &bars->vland, ragged & 1);
+          ++ragged;
+          if (ok) {
+            uint8_t *v = sV + (g % C::NB) * C::v_bytes;
+            const int n = (kBN - keys) * 8 * 2;  // 16-byte pieces of one block of 256 dims
+            for (int e = L; e < n * (LAT / 256); e += 128) {
+              const int j = e / n, f = e - j * n, key = keys + (f >> 4), c = f & 15;
+              *reinterpret_cast<uint4 *>(v + (j * 2 + (key >> 6)) * kStage + (c >> 3) * kPiece + (key & 63) * 128 +
+                                         (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
+        }
+        if (ok) {
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_release(p_bar);
+        }
+      }
+      // the whole row's sum: both halves
+      row_sync();
+      bars->xmax[g & 1][L] = l;
+      row_sync();
+      const float lt = l + bars->xmax[g & 1][L ^ 64];
+      row_sync();
+      if (ok) ok = wait(bars, &bars->pv, (g - 1) & 1);
+      if (ok) {
+        tc_fence_after();
+        const bool whole = walk.t0 == 0 && walk.t1 == walk.T;
+        const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;  // a row that sees nothing: zeros
+        __nv_bfloat16 *o = out + ((int64_t)walk.b * R + row) * LAT + half * 128;
+        float *slot = ws + (size_t)(2 * pair + (walk.t0 > 0 ? 0 : 1)) * slot_floats(LAT);
+        const int lr = (int)rank * 64 + r;
+#pragma unroll 1
+        for (int c = 0; c < LAT / 2; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tmem + lane_off + c, v);
+          tmem_wait_ld();
+          const int d = (c >> 7) * 256 + (c & 127);  // (+ half * 128)
+          if (!row_ok) continue;
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 u;
+              u.x = pack_bf16(__uint_as_float(v[8 * i]) * inv, __uint_as_float(v[8 * i + 1]) * inv);
+              u.y = pack_bf16(__uint_as_float(v[8 * i + 2]) * inv, __uint_as_float(v[8 * i + 3]) * inv);
+              u.z = pack_bf16(__uint_as_float(v[8 * i + 4]) * inv, __uint_as_float(v[8 * i + 5]) * inv);
+              u.w = pack_bf16(__uint_as_float(v[8 * i + 6]) * inv, __uint_as_float(v[8 * i + 7]) * inv);
+              *reinterpret_cast<uint4 *>(o + d + 8 * i) = u;
+            }
+          } else {
+            float *dst = slot + (size_t)lr * LAT + half * 128 + d;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4 *>(dst + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        }
+        if (!whole && row_ok && half == 0)
+          *reinterpret_cast<float2 *>(slot + 128 * (size_t)LAT + 2 * lr) = make_float2(m, lt);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_release(ofree_bar);
+      }
+    }
+  }
+
+  // Nothing leaves while its pair may still copy into it, multiply from it
+  // or arrive on it (after a wait that gave up: copies in flight land long
+  // before the other roles' waits run out).
+  __syncwarp();
+  if (!ok && lane == 0) sv::report(status, SPEC_DEV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// Joins the parts of a unit cut between pairs: block (range end, 4 rows),
+// a thread four (LAT 256: two) of the dims.
+template <int LAT>
+__global__ void __launch_bounds__(128)
+    latent_join_kernel(const float *__restrict__ ws, const int4 *__restrict__ desc, __nv_bfloat16 *__restrict__ out,
+                       int R) {
+  constexpr int V = LAT / 128;
+  grid_dep_wait();
+  const int pair = blockIdx.x + 1;
+  const int4 d = desc[pair];
+  if (d.w == 0) return;
+  // the first part ends its pair's range (slot 1), the others begin theirs (slot 0)
+  auto part = [&](int i) { return ws + (size_t)(i == 0 ? 2 * (pair - 1) + 1 : 2 * (pair - 1 + i)) * slot_floats(LAT); };
+  for (int i = 0; i < 4; ++i) {
+    const int lr = blockIdx.y * 4 + i, row = d.y * 128 + lr;
+    if (row >= R) return;
+    float m = kLow;
+    for (int p = 0; p < d.z; ++p) m = fmaxf(m, part(p)[128 * (size_t)LAT + 2 * lr]);
+    float l = 0.f, acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll 2
+    for (int p = 0; p < d.z; ++p) {
+      const float *s = part(p);
+      const float2 ml = *reinterpret_cast<const float2 *>(s + 128 * (size_t)LAT + 2 * lr);
+      const float a = exp2f(ml.x - m);
+      l = fmaf(a, ml.y, l);
+      float x[V];
+      if constexpr (V == 4) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(s + (size_t)lr * LAT + threadIdx.x * V);
+      else *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(s + (size_t)lr * LAT + threadIdx.x * V);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(a, x[v], acc[v]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t *o = reinterpret_cast<uint32_t *>(out + ((int64_t)d.x * R + row) * LAT + threadIdx.x * V);
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v) o[v] = pack_bf16(acc[2 * v] * inv, acc[2 * v + 1] * inv);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+  }();
+  return fn;
+}
+
+int make_map(CUtensorMap *m, const void *base, cuuint32_t rank, const cuuint64_t *dims, const cuuint64_t *strides) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return SPEC_ERR_CUDA;
+  const cuuint32_t es[3] = {1, 1, 1}, box[3] = {64, 64, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
+}
+
+// Pairs to run: no more than tiles (at max_prefix).
+int pairs_of(const SvLatentShape &s) {
+  const long long units = (long long)s.batch * (((long long)s.n_nodes * s.hq + 127) / 128);
+  const long long tiles = units * ((s.max_prefix + kBN - 1) / kBN + (s.n_nodes + kBN - 1) / kBN);
+  return (int)(tiles < kPairs ? tiles : kPairs);
+}
+
+template <int LAT>
+int launch(const SvLatentShape &s, const void *q, const void *cache, const void *tree, const int32_t *prefix_len,
+           const uint64_t *anc, void *out, float scale, void *ws, int32_t *status, cudaStream_t stream) {
+  using C = Cfg<LAT>;
+  const int pairs = pairs_of(s), R = s.n_nodes * s.hq;
+  const cuuint64_t row = C::D * 2;
+  const long long rows = s.block_table ? (long long)s.num_blocks * s.block_size : (long long)s.batch * s.s_max;
+  CUtensorMap mq, mc, mt;
+  {
+    const cuuint64_t dims[3] = {C::D, (cuuint64_t)R, (cuuint64_t)s.batch}, strides[2] = {row, row * R};
+    if (make_map(&mq, q, 3, dims, strides) != SPEC_OK) return SPEC_ERR_CUDA;
+  }
+  {
+    const cuuint64_t dims[2] = {C::D, (cuuint64_t)(rows > 0 ? rows : 1)}, strides[1] = {row};
+    if (make_map(&mc, cache, 2, dims, strides) != SPEC_OK) return SPEC_ERR_CUDA;
+  }
+  {
+    const cuuint64_t dims[3] = {C::D, (cuuint64_t)s.n_nodes, (cuuint64_t)s.batch}, strides[2] = {row, row * s.n_nodes};
+    if (make_map(&mt, tree, 3, dims, strides) != SPEC_OK) return SPEC_ERR_CUDA;
+  }
+  int4 *desc = static_cast<int4 *>(ws);
+  float *slots = reinterpret_cast<float *>(static_cast<char *>(ws) + kPairs * sizeof(int4));
+  const Work w{prefix_len, s.batch, s.n_nodes, s.hq, s.s_max, s.max_prefix, (R + 127) / 128, (s.n_nodes + kBN - 1) / kBN};
+  if (cudaFuncSetAttribute(latent_tc_kernel<LAT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem_bytes<LAT>()) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  latent_tc_kernel<LAT><<<2 * pairs, kThreads, smem_bytes<LAT>(), stream>>>(
+      mq, mc, mt, w, anc, (__nv_bfloat16 *)out, slots, desc, scale * 1.4426950408889634f, (int)rows, status,
+      sv::KvPages{s.block_table, s.block_size, s.max_blocks, s.num_blocks});
+  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  if (pairs == 1) return SPEC_OK;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(pairs - 1, ((R < 128 ? R : 128) + 3) / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, latent_join_kernel<LAT>, (const float *)slots, (const int4 *)desc,
+                            (__nv_bfloat16 *)out, R) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t sv_latent_tc_ws_bytes(const SvLatentShape &s) {
+  return kPairs * sizeof(int4) + 2 * (size_t)pairs_of(s) * slot_floats(s.latent_dim) * sizeof(float);
+}
+
+int sv_latent_tc(const SvLatentShape &s, const void *q, const void *cache, const void *tree, const int32_t *prefix_len,
+                 const uint64_t *anc, void *out, float scale, void *ws, int32_t *status, cudaStream_t stream) {
+  return (s.latent_dim == 512 ? launch<512> : launch<256>)(s, q, cache, tree, prefix_len, anc, out, scale, ws, status,
+                                                           stream);
+}

@@ -513,7 +513,8 @@ __global__ void __launch_bounds__(kCopyThreads)
   const int n_moves = *ws.n_moves;
   const int64_t page_vec = (int64_t)block_size * vec_per_row;
   const int pieces = (int)((page_vec + kPiece - 1) / kPiece);
-  const int64_t units = (int64_t)n_moves * 2 * n_layers * hkv * pieces;
+  const int pools = v_pages ? 2 : 1;  // (a cache of one pool: K alone)
+  const int64_t units = (int64_t)n_moves * pools * n_layers * hkv * pieces;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int piece = (int)(u % pieces);
     int64_t x = u / pieces;
@@ -521,8 +522,8 @@ __global__ void __launch_bounds__(kCopyThreads)
     x /= hkv;
     const int layer = (int)(x % n_layers);
     x /= n_layers;
-    const int is_v = (int)(x & 1);
-    const Move mv = ws.moves[x >> 1];
+    const bool is_v = v_pages && (x & 1);
+    const Move mv = ws.moves[v_pages ? x >> 1 : x];
     const int64_t n = (int64_t)mv.rows * vec_per_row;
     uint4 *pool = is_v ? v_pages : k_pages;
     const int64_t layer0 = (int64_t)layer * num_blocks;

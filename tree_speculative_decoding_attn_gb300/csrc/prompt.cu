@@ -1,0 +1,402 @@
+// Causal attention of packed prompt tokens over expanded latent keys and
+// values (bf16 in, float32 softmax and accumulation).
+//
+//   x_j = scale (q[0..127] . k_j + q[128..191] . rope_j),  out = sum_j softmax(x)_j v_j
+// for the keys up to the query's own position.  2 (192 + 128) flops a query,
+// key and head: tensor-bound for all but a few queries.
+//
+// A CTA takes 256 queries of one head as two tiles of 128, so that the softmax
+// of one tile runs under the products of the other, and both share every
+// key tile of 128:
+//   S_i(j) = Q_i K(j)^T  (N = 128, K = 192; the rotary columns of K are one
+//            64-column box shared by all heads)   768 cycles
+//   O_i   += P_i(j) V(j) (N = 128 dims, K = 128; P in TMEM over S)  512 cycles
+// in the order S0 S1 PV0 PV1.  P lies where S was, so S_i(j + 1) waits for
+// PV_i(j) to be done: behind the other tile's PV, which covers the wait.
+//   warp 0      loads Q, K (two stages) and V
+//   warp 1      TMEM and all MMAs (an elected thread); clears the V rows past
+//               the sequence's last key
+//   warps 4-7   softmax and output of tile 0, a thread a row; 8-11 tile 1.
+//               S is read twice from TMEM: once for the maximum, once for P
+// TMEM columns: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512).
+// Longest tiles are launched first.  Every wait is bounded.
+#include <cuda.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace {
+
+using namespace sv::ptx;
+
+constexpr int kBN = 128, kD = 128, kRope = 64, kThreads = 384, kTiles = 2;
+constexpr uint32_t kPiece = 128 * 128;  // 128 rows x 64 elements, 128-byte swizzle
+constexpr uint32_t kQBytes = 3 * kPiece, kKBytes = 3 * kPiece, kVBytes = 2 * kPiece;
+constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr float kLow = -3.0e38f;  // running maximum before the first key
+constexpr float kTau = 16.f;      // the maximum moves when a tile exceeds it by more than 2^kTau
+
+struct Bars {
+  uint64_t q[kTiles], kfull[2], kempty[2], vfull, vempty, sfull[kTiles], p[kTiles], pv[kTiles], drain;
+  uint32_t tmem;
+  volatile int abort;
+};
+constexpr uint32_t kSmemBytes = kTiles * kQBytes + 2 * kKBytes + kVBytes + sizeof(Bars) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KB");
+
+constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // Q, K both K-major
+constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, 0, 1);  // V is MN-major (dims contiguous)
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+// Bounded wait that also ends once another role has given up; its outcome is
+// one for the warp.
+__device__ __forceinline__ bool wait(Bars *bars, uint64_t *bar, uint32_t parity) {
+  bool ok = false;
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if ((ok = mbar_try_wait(bar, parity))) break;
+    if ((i & 63) == 63 && bars->abort) break;
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) bars->abort = 1;
+  return ok;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v,
+                  const int32_t *__restrict__ q_off, const int32_t *__restrict__ kv_off, __nv_bfloat16 *__restrict__ out,
+                  int hq, int total_q, int total_kv, int max_q, float scale_log2, int32_t *status) {
+  const int head = blockIdx.x, b = blockIdx.y;
+  const int q_first = q_off[b], q_end = q_off[b + 1], k_first = kv_off[b], k_end = kv_off[b + 1];
+  if (q_first < 0 || k_first < 0 || q_end < q_first || k_end < k_first || q_end > total_q || k_end > total_kv ||
+      q_end - q_first > max_q) {
+    if (threadIdx.x == 0) sv::report(status, SPEC_DEV_CAPACITY);
+    return;
+  }
+  const int n = q_end - q_first, m_keys = k_end - k_first;
+  const int q0 = (int)(gridDim.z - 1 - blockIdx.z) * kTiles * 128;  // first query of this CTA
+  if (q0 >= n) return;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *sQ = smem, *sK = sQ + kTiles * kQBytes, *sV = sK + 2 * kKBytes;
+  Bars *bars = reinterpret_cast<Bars *>(sV + kVBytes);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  // key tiles of each query tile: up to its last query's position
+  int tiles[kTiles], all = 0;
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) {
+    const int last = min(n, q0 + (i + 1) * 128) - 1;  // last query of the tile
+    const int seen = q0 + i * 128 < n ? m_keys - n + last + 1 : 0;
+    tiles[i] = seen > 0 ? (seen + kBN - 1) / kBN : 0;
+    all = max(all, tiles[i]);
+  }
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->q[i], 1);
+      mbar_init(&bars->kfull[i], 1);
+      mbar_init(&bars->kempty[i], 1);
+      mbar_init(&bars->sfull[i], 1);
+      mbar_init(&bars->p[i], 4);
+      mbar_init(&bars->pv[i], 1);
+    }
+    mbar_init(&bars->vfull, 1);
+    mbar_init(&bars->vempty, 1);
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) tmem_alloc(&bars->tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  bool ok = true;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    const bool me = elect_one();
+    if (me && all > 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_r);
+      tma_prefetch_desc(&tm_v);
+    }
+    int k_done = 0, v_done = 0;
+    for (int j = 0; ok && j < all; ++j) {
+      const int row = k_first + j * kBN;
+      if (!(ok = wait(bars, &bars->kempty[j & 1], ((j >> 1) & 1) ^ 1))) break;
+      if (me) {
+        uint64_t *bar = &bars->kfull[j & 1];
+        uint8_t *dst = sK + (j & 1) * kKBytes;
+        if (j == 0) {
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+            if (tiles[i] > 0) {
+              mbar_expect_tx(&bars->q[i], kQBytes);
+              for (int c = 0; c < 3; ++c)
+                tma_load_3d(sQ + i * kQBytes + c * kPiece, &tm_q, c * 64, head, q_first + q0 + i * 128, &bars->q[i]);
+            }
+        }
+        mbar_expect_tx(bar, kKBytes);
+        tma_load_3d(dst, &tm_k, 0, head, row, bar);
+        tma_load_3d(dst + kPiece, &tm_k, 64, head, row, bar);
+        tma_load_2d(dst + 2 * kPiece, &tm_r, 0, row, bar);
+      }
+      ++k_done;
+      __syncwarp();
+      if (!(ok = wait(bars, &bars->vempty, (j & 1) ^ 1))) break;
+      if (me) {
+        mbar_expect_tx(&bars->vfull, kVBytes);
+        tma_load_3d(sV, &tm_v, 0, head, row, &bars->vfull);
+        tma_load_3d(sV + kPiece, &tm_v, 64, head, row, &bars->vfull);
+      }
+      ++v_done;
+      __syncwarp();
+    }
+    if (!ok) {  // let the copies into this CTA land before it exits
+      for (int i = 0; i < kTiles; ++i)
+        if (k_done > 0 && tiles[i] > 0) mbar_wait(&bars->q[i], 0, kWaitLimit);
+      for (int j = k_done > 2 ? k_done - 2 : 0; j < k_done; ++j) mbar_wait(&bars->kfull[j & 1], (j >> 1) & 1, kWaitLimit);
+      if (v_done > 0) mbar_wait(&bars->vfull, (v_done - 1) & 1, kWaitLimit);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs
+    const uint32_t qa = smem_u32(sQ), ka = smem_u32(sK), va = smem_u32(sV);
+    for (int j = 0; ok && j < all; ++j) {
+      if (!(ok = wait(bars, &bars->kfull[j & 1], (j >> 1) & 1))) break;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        if (!ok || j >= tiles[i]) continue;
+        if (j == 0) ok = wait(bars, &bars->q[i], 0);
+        else ok = wait(bars, &bars->pv[i], (j - 1) & 1);  // P(j - 1), where S goes, has been read
+        if (!ok) continue;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 12; ++k) {
+            const uint32_t off = (k >> 2) * kPiece + (k & 3) * 32;
+            mma_ss(tmem + i * 128, smem_desc_sw128(qa + i * kQBytes + off, 16, 1024),
+                   smem_desc_sw128(ka + (j & 1) * kKBytes + off, 16, 1024), kIdescS, k > 0);
+          }
+          mma_commit(&bars->sfull[i]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (elect_one()) mma_commit(&bars->kempty[j & 1]);
+      __syncwarp();
+      if (!(ok = wait(bars, &bars->vfull, j & 1))) break;
+      const int keys = m_keys - j * kBN;
+      if (keys < kBN) {
+        // what follows the sequence's last key belongs to others: cleared
+        for (int e = lane; e < (kBN - keys) * 16; e += 32)
+          *reinterpret_cast<uint4 *>(sV + (e & 8 ? kPiece : 0) + (keys + (e >> 4)) * 128 + (e & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        if (!ok || j >= tiles[i]) continue;
+        if (!(ok = wait(bars, &bars->p[i], j & 1))) continue;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, smem_desc_sw128(va + k * 2048, kPiece, 1024), kIdescPV,
+                   j > 0 || k > 0);
+          mma_commit(&bars->pv[i]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (elect_one()) mma_commit(&bars->vempty);
+      __syncwarp();
+    }
+    if (!ok) {  // let issued MMAs finish before TMEM is freed
+      if (elect_one()) mma_commit(&bars->drain);
+      __syncwarp();
+      mbar_wait(&bars->drain, 0, kWaitLimit);
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax
+    const int i = (warp - 4) >> 2, quarter = warp & 3;
+    const int qi = q0 + i * 128 + quarter * 32 + lane;  // this thread's query
+    const int seen = qi < n ? m_keys - n + qi + 1 : 0;   // keys that it sees (<= 0: none)
+    const uint32_t s_addr = tmem + ((uint32_t)(quarter * 32) << 16) + i * 128;
+    const uint32_t o_addr = s_addr - i * 128 + 256 + i * 128;
+    const int nt = i == 0 ? tiles[0] : tiles[1];
+    float m = kLow, l = 0.f;
+    for (int j = 0; j < nt; ++j) {
+      if (!(ok = wait(bars, &bars->sfull[i], j & 1))) break;
+      tc_fence_after();
+      const int left = seen - j * kBN;  // visible keys of this tile
+      const bool cut = __any_sync(0xffffffffu, left < kBN);
+      auto load = [&](int c, uint32_t (&x)[32]) {
+        tmem_ld32(s_addr + c * 32, x);
+        tmem_wait_ld();
+        if (cut) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (c * 32 + e >= left) x[e] = 0xff800000u;  // -inf
+        }
+      };
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        load(c, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+      }
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
+      const bool need = mt > m + kTau;
+      if (__any_sync(0xffffffffu, need)) {
+        const float a = need ? ex2(m - mt) : 1.f;
+        if (need) {
+          m = mt;
+          l *= a;
+        }
+        if (j > 0) {
+          if (!(ok = wait(bars, &bars->pv[i], (j - 1) & 1))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < kD; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_addr + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+            tmem_st16(o_addr + c, o);
+          }
+        }
+      }
+      // P = 2^(x scale - m) rounded to bf16 for the product, the row sum
+      // takes it unrounded; P's columns lie over S's that have been read
+      const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m, -m);
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32], pk[16];
+        load(c, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float2 v = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc, nm);
+          v = make_float2(ex2(v.x), ex2(v.y));
+          acc[e & 1] = add2(acc[e & 1], v);
+          pk[e] = pack_bf16(v.x, v.y);
+        }
+        tmem_st16(s_addr + c * 16, pk);
+      }
+      const float2 sum = add2(acc[0], acc[1]);
+      l += sum.x + sum.y;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->p[i]);
+    }
+    if (ok && nt > 0) ok = wait(bars, &bars->pv[i], (nt - 1) & 1);
+    if (ok) {
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // a query that sees nothing: zeros
+      uint4 *o = reinterpret_cast<uint4 *>(out + ((int64_t)(q_first + qi) * hq + head) * kD);
+#pragma unroll 1
+      for (int c = 0; c < kD / 32; ++c) {
+        uint32_t v[32];
+        if (nt > 0) {
+          tmem_ld32(o_addr + c * 32, v);
+          tmem_wait_ld();
+        }
+        if (qi >= n) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (nt > 0) {
+            u.x = pack_bf16(__uint_as_float(v[8 * e]) * inv, __uint_as_float(v[8 * e + 1]) * inv);
+            u.y = pack_bf16(__uint_as_float(v[8 * e + 2]) * inv, __uint_as_float(v[8 * e + 3]) * inv);
+            u.z = pack_bf16(__uint_as_float(v[8 * e + 4]) * inv, __uint_as_float(v[8 * e + 5]) * inv);
+            u.w = pack_bf16(__uint_as_float(v[8 * e + 6]) * inv, __uint_as_float(v[8 * e + 7]) * inv);
+          }
+          o[c * 4 + e] = u;
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  if (!ok && lane == 0) sv::report(status, SPEC_DEV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// [tokens, heads, dims] with element strides, in boxes of 128 tokens x 64 dims
+// of one head; heads 0: [tokens, dims].
+int make_map(CUtensorMap *m, const void *base, int dims, int heads, int tokens, int64_t head, int64_t token) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return SPEC_ERR_CUDA;
+  const cuuint32_t es[3] = {1, 1, 1};
+  const cuuint64_t size3[3] = {(cuuint64_t)dims, (cuuint64_t)heads, (cuuint64_t)tokens},
+                   size2[2] = {(cuuint64_t)dims, (cuuint64_t)tokens};
+  const cuuint64_t stride3[2] = {(cuuint64_t)head * 2, (cuuint64_t)token * 2}, stride2[1] = {(cuuint64_t)token * 2};
+  const cuuint32_t box3[3] = {64, 1, 128}, box2[2] = {64, 128};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, heads ? 3 : 2, const_cast<void *>(base), heads ? size3 : size2,
+             heads ? stride3 : stride2, heads ? box3 : box2, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+int sv_prompt_attn(const SvPromptShape &s, const void *q, const void *k, const void *k_rope, const void *v,
+                   const int32_t *q_offsets, const int32_t *kv_offsets, void *out, float scale, int32_t *status,
+                   cudaStream_t stream) {
+  const int longest = s.max_q < s.total_q ? s.max_q : s.total_q;
+  if (longest == 0) return SPEC_OK;
+  CUtensorMap mq, mk, mr, mv;
+  if (make_map(&mq, q, kD + kRope, s.hq, s.total_q, kD + kRope, (int64_t)s.hq * (kD + kRope)) != SPEC_OK ||
+      make_map(&mk, k, kD, s.hq, s.total_kv, s.k_head, s.k_token) != SPEC_OK ||
+      make_map(&mr, k_rope, kRope, 0, s.total_kv, 0, s.rope_token) != SPEC_OK ||
+      make_map(&mv, v, kD, s.hq, s.total_kv, s.v_head, s.v_token) != SPEC_OK)
+    return SPEC_ERR_CUDA;
+  if (cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  prompt_kernel<<<dim3(s.hq, s.batch, (longest + kTiles * 128 - 1) / (kTiles * 128)), kThreads, kSmemBytes, stream>>>(
+      mq, mk, mr, mv, q_offsets, kv_offsets, (__nv_bfloat16 *)out, s.hq, s.total_q, s.total_kv, s.max_q,
+      scale * 1.4426950408889634f, status);
+  return sv_launch_status();
+}

@@ -459,7 +459,7 @@ int spec_accept_commit(int mode, const void *logits, const void *draft_logits, i
   if (mode != SPEC_ACCEPT_GREEDY && !(temperature > 0.f)) return SPEC_ERR_INVALID_ARG;
   if (mode == SPEC_ACCEPT_GREEDY) temperature = 1.f;
   // the commit's arguments, as kv_commit
-  if (!k_cache || !v_cache || !k_tree || !v_tree || !prefix_len) return SPEC_ERR_INVALID_ARG;
+  if (!k_cache || !k_tree || !v_cache != !v_tree || !prefix_len) return SPEC_ERR_INVALID_ARG;
   if (elem_bytes != 2 && elem_bytes != 4) return SPEC_ERR_UNSUPPORTED;
   if (n_layers < 1 || hkv < 1 || s_max < 1 || head_dim < 1) return SPEC_ERR_INVALID_ARG;
   if (path_cap > SPEC_MAX_NODES + 1) return SPEC_ERR_UNSUPPORTED;
@@ -500,7 +500,7 @@ int kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table, in
                     int batch, int hkv, int n_nodes, int head_dim, const int32_t *acc_len,
                     const int32_t *acc_path, int path_cap, const int32_t *prefix_len, int32_t *prefix_len_out,
                     int32_t *dev_status, spec_stream_t stream) {
-  if (!k_pages || !v_pages || !block_table || !k_tree || !v_tree || !acc_len || !acc_path || !prefix_len)
+  if (!k_pages || !block_table || !k_tree || !v_pages != !v_tree || !acc_len || !acc_path || !prefix_len)
     return SPEC_ERR_INVALID_ARG;
   if (elem_bytes != 2 && elem_bytes != 4) return SPEC_ERR_UNSUPPORTED;
   if (block_size < 1 || num_blocks < 1 || max_blocks < 1 || n_layers < 1 || batch < 1 || hkv < 1 ||
@@ -522,8 +522,7 @@ int kv_commit(void *k_cache, void *v_cache, const void *k_tree, const void *v_tr
               const int32_t *acc_len, const int32_t *acc_path, int path_cap,
               const int32_t *prefix_len, int32_t *prefix_len_out, int32_t *dev_status,
               spec_stream_t stream) {
-  if (!k_cache || !v_cache || !k_tree || !v_tree || !acc_len || !acc_path || !prefix_len)
-    return SPEC_ERR_INVALID_ARG;
+  if (!k_cache || !k_tree || !v_cache != !v_tree || !acc_len || !acc_path || !prefix_len) return SPEC_ERR_INVALID_ARG;
   if (elem_bytes != 2 && elem_bytes != 4) return SPEC_ERR_UNSUPPORTED;
   if (n_layers < 1 || batch < 1 || hkv < 1 || s_max < 1 || n_nodes < 1 || head_dim < 1 || path_cap < 1)
     return SPEC_ERR_INVALID_ARG;
@@ -561,7 +560,7 @@ static int pages_check(int batch, int max_blocks, int num_blocks) {
 }
 static int pool_check(const void *k, const void *v, int elem_bytes, int n_layers, int hkv, int head_dim,
                       int block_size, int num_blocks, int max_blocks) {
-  if (!k || !v) return SPEC_ERR_INVALID_ARG;
+  if (!k) return SPEC_ERR_INVALID_ARG;  // (v null: a cache of one pool)
   if (elem_bytes != 2 && elem_bytes != 4) return SPEC_ERR_UNSUPPORTED;
   if (n_layers < 1 || hkv < 1 || head_dim < 1 || block_size < 1) return SPEC_ERR_INVALID_ARG;
   if (((long long)head_dim * elem_bytes) % 16) return SPEC_ERR_UNSUPPORTED;
@@ -647,6 +646,133 @@ int kv_pages_compact(void *k_pages, void *v_pages, int elem_bytes, int n_layers,
   return sv_pages_compact(k_pages, v_pages, head_dim * elem_bytes / 16, n_layers, hkv, block_size, num_blocks,
                           block_table, table_out, batch, max_blocks, ref_count, ref_count_out, n_used, remap,
                           workspace, dev_status, cs(stream));
+}
+
+// Limits of the latent entry points (s.s_max: a sequence's capacity).
+static int latent_check(const SvLatentShape &s, int rope_dim) {
+  const long long most = 1 << 30;
+  if (s.dtype != SPEC_F32 && s.dtype != SPEC_BF16) return SPEC_ERR_UNSUPPORTED;
+  if (s.batch < 1 || s.n_nodes < 1 || s.hq < 1 || s.max_prefix < 0 || s.s_max < 0) return SPEC_ERR_INVALID_ARG;
+  if ((s.latent_dim != 256 && s.latent_dim != 512) || rope_dim != 64 || s.n_nodes > SPEC_MAX_NODES || s.hq > 128 ||
+      s.batch > 65535 || s.max_prefix > most || (long long)s.batch * s.n_nodes * s.hq > most)
+    return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+static size_t latent_ws_bytes(const SvLatentShape &s) {
+  return s.dtype == SPEC_BF16 ? sv_latent_tc_ws_bytes(s) : sv_latent_simt_ws_bytes(s);
+}
+
+size_t tree_attn_latent_workspace_bytes(int dtype, int batch, int n_nodes, int hq, int latent_dim, int rope_dim,
+                                        int max_prefix) {
+  const SvLatentShape s{dtype, batch, n_nodes, hq, latent_dim, max_prefix, max_prefix};
+  return latent_check(s, rope_dim) == SPEC_OK ? latent_ws_bytes(s) : 0;
+}
+
+static int latent_run(const SvLatentShape &s, int rope_dim, const void *q, const void *cache, const void *tree,
+                      const int32_t *prefix_len, const uint64_t *anc_mask, void *out, float scale, void *workspace,
+                      size_t workspace_bytes, int32_t *dev_status, spec_stream_t stream) {
+  if (!q || !cache || !tree || !prefix_len || !anc_mask || !out) return SPEC_ERR_INVALID_ARG;
+  const int rc = latent_check(s, rope_dim);
+  if (rc != SPEC_OK) return rc;
+  if (!s.block_table && (long long)s.batch * s.s_max > (1 << 30)) return SPEC_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(tree) || !aligned16(out)) return SPEC_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale)) return SPEC_ERR_INVALID_ARG;
+  if (s.max_prefix > s.s_max) return SPEC_ERR_CAPACITY;
+  const size_t need = latent_ws_bytes(s);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return SPEC_ERR_CAPACITY;
+  return (s.dtype == SPEC_BF16 ? sv_latent_tc : sv_latent_simt)(s, q, cache, tree, prefix_len, anc_mask, out, scale,
+                                                                workspace, dev_status, cs(stream));
+}
+
+int tree_attn_verify_latent(const void *q, const void *cache, const void *tree, const int32_t *prefix_len,
+                            const uint64_t *anc_mask, void *out, int dtype, int batch, int n_nodes, int hq,
+                            int latent_dim, int rope_dim, int s_max, int max_prefix, float scale, void *workspace,
+                            size_t workspace_bytes, int32_t *dev_status, spec_stream_t stream) {
+  const SvLatentShape s{dtype, batch, n_nodes, hq, latent_dim, s_max, max_prefix};
+  return latent_run(s, rope_dim, q, cache, tree, prefix_len, anc_mask, out, scale, workspace, workspace_bytes,
+                    dev_status, stream);
+}
+
+int tree_attn_verify_latent_paged(const void *q, const void *pages, const int32_t *block_table, int block_size,
+                                  int num_blocks, int max_blocks, const void *tree, const int32_t *prefix_len,
+                                  const uint64_t *anc_mask, void *out, int dtype, int batch, int n_nodes, int hq,
+                                  int latent_dim, int rope_dim, int max_prefix, float scale, void *workspace,
+                                  size_t workspace_bytes, int32_t *dev_status, spec_stream_t stream) {
+  if (!block_table || block_size < 128 || block_size % 128 || num_blocks < 1 || max_blocks < 1)
+    return SPEC_ERR_INVALID_ARG;
+  if ((long long)max_blocks * block_size > (1 << 30) || too_many_rows(num_blocks, 1, block_size))
+    return SPEC_ERR_UNSUPPORTED;
+  const SvLatentShape s{dtype,      batch,       n_nodes,    hq,         latent_dim, max_blocks * block_size,
+                        max_prefix, block_table, block_size, max_blocks, num_blocks};
+  return latent_run(s, rope_dim, q, pages, tree, prefix_len, anc_mask, out, scale, workspace, workspace_bytes,
+                    dev_status, stream);
+}
+
+int kv_pages_slots(const int32_t *block_table, const int32_t *prefix_len, const int32_t *new_len, int batch,
+                   int max_blocks, int block_size, int num_blocks, int room, int32_t *offsets, int32_t *slots,
+                   int32_t *positions, int32_t *dev_status, spec_stream_t stream) {
+  if (!block_table || !prefix_len || !new_len || !offsets || !slots) return SPEC_ERR_INVALID_ARG;
+  const int rc = pages_check(batch, max_blocks, num_blocks);
+  if (rc != SPEC_OK) return rc;
+  if (block_size < 1 || room < 1) return SPEC_ERR_INVALID_ARG;
+  if ((long long)max_blocks * block_size > (1 << 30) || too_many_rows(num_blocks, 1, block_size) || room > (1 << 30))
+    return SPEC_ERR_UNSUPPORTED;
+  const struct { const void *p; size_t n; } in[] = {{block_table, (size_t)batch * max_blocks * 4},
+                                                    {prefix_len, (size_t)batch * 4}, {new_len, (size_t)batch * 4}},
+      o[] = {{offsets, (size_t)(batch + 1) * 4}, {slots, (size_t)room * 4}, {positions, (size_t)room * 4}};
+  for (int i = 0; i < (positions ? 3 : 2); ++i) {
+    for (const auto &x : in)
+      if (overlap(o[i].p, o[i].n, x.p, x.n)) return SPEC_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(o[i].p, o[i].n, o[j].p, o[j].n)) return SPEC_ERR_INVALID_ARG;
+  }
+  return sv_pages_slots(block_table, prefix_len, new_len, batch, max_blocks, block_size, num_blocks, room, offsets,
+                        slots, positions, dev_status, cs(stream));
+}
+
+static int slots_rows(bool write, void *pages, const int32_t *slots, void *rows, int elem_bytes, int n_rows, int hkv,
+                      int head_dim, int block_size, int num_blocks, int32_t *dev_status, spec_stream_t stream) {
+  if (!pages || !slots || !rows) return SPEC_ERR_INVALID_ARG;
+  if (n_rows < 1 || num_blocks < 1) return SPEC_ERR_INVALID_ARG;
+  const int rc = pool_check(pages, nullptr, elem_bytes, 1, hkv, head_dim, block_size, num_blocks, 1);
+  if (rc != SPEC_OK) return rc;
+  if ((long long)n_rows * hkv > (1 << 30)) return SPEC_ERR_UNSUPPORTED;
+  if (!aligned16(rows)) return SPEC_ERR_INVALID_ARG;
+  return sv_slots_rows(write, pages, rows, slots, n_rows, hkv, block_size, num_blocks, head_dim * elem_bytes / 16,
+                       dev_status, cs(stream));
+}
+
+int kv_slots_write(void *pages, const int32_t *slots, const void *rows, int elem_bytes, int n_rows, int hkv,
+                   int head_dim, int block_size, int num_blocks, int32_t *dev_status, spec_stream_t stream) {
+  return slots_rows(true, pages, slots, const_cast<void *>(rows), elem_bytes, n_rows, hkv, head_dim, block_size,
+                    num_blocks, dev_status, stream);
+}
+
+int kv_slots_read(const void *pages, const int32_t *slots, void *rows, int elem_bytes, int n_rows, int hkv,
+                  int head_dim, int block_size, int num_blocks, int32_t *dev_status, spec_stream_t stream) {
+  return slots_rows(false, const_cast<void *>(pages), slots, rows, elem_bytes, n_rows, hkv, head_dim, block_size,
+                    num_blocks, dev_status, stream);
+}
+
+int prompt_attn_latent(const void *q, const void *k, int64_t k_token, int64_t k_head, const void *k_rope,
+                       int64_t rope_token, const void *v, int64_t v_token, int64_t v_head, const int32_t *q_offsets,
+                       const int32_t *kv_offsets, void *out, int batch, int hq, int head_dim, int rope_dim,
+                       int total_q, int total_kv, int max_q, float scale, int32_t *dev_status, spec_stream_t stream) {
+  if (!q || !k || !k_rope || !v || !q_offsets || !kv_offsets || !out) return SPEC_ERR_INVALID_ARG;
+  if (batch < 1 || hq < 1 || total_q < 1 || total_kv < 1 || max_q < 0) return SPEC_ERR_INVALID_ARG;
+  if (head_dim != 128 || rope_dim != 64) return SPEC_ERR_UNSUPPORTED;
+  if (batch > 65535 || hq > 65535 || total_kv > (1 << 30) || (long long)total_q * hq > (1 << 30) ||
+      (max_q < total_q ? max_q : total_q) > (1 << 23))
+    return SPEC_ERR_UNSUPPORTED;
+  // (strides are at least what they step over, and at most what a tensor map takes)
+  const struct { int64_t v; int least; } strides[] = {{k_token, 128}, {k_head, 128}, {rope_token, 64}, {v_token, 128}, {v_head, 128}};
+  for (const auto &x : strides)
+    if (x.v < x.least || x.v % 8 || x.v >= (1ll << 38)) return SPEC_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(k_rope) || !aligned16(v) || !aligned16(out))
+    return SPEC_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale)) return SPEC_ERR_INVALID_ARG;
+  const SvPromptShape s{batch, hq, total_q, total_kv, max_q, k_token, k_head, v_token, v_head, rope_token};
+  return sv_prompt_attn(s, q, k, k_rope, v, q_offsets, kv_offsets, out, scale, dev_status, cs(stream));
 }
 
 }  // extern "C"

@@ -32,7 +32,7 @@ def mask_words(n_nodes):
 
 _lib = None
 
-_vp, _i, _f, _u64, _sz = C.c_void_p, C.c_int, C.c_float, C.c_uint64, C.c_size_t
+_vp, _i, _f, _u64, _i64, _sz = C.c_void_p, C.c_int, C.c_float, C.c_uint64, C.c_int64, C.c_size_t
 _SIGS = {
     "spec_status_string": ([_i], C.c_char_p),
     "spec_abi_version": ([], _i),
@@ -76,6 +76,15 @@ _SIGS = {
     "kv_commit": ([_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp], _i),
     "spec_accept_commit": ([_i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _f, _f, _f, _u64, _u64, _i, _vp, _vp,
                             _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp], _i),
+    "tree_attn_latent_workspace_bytes": ([_i] * 7, _sz),
+    "tree_attn_verify_latent": ([_vp] * 6 + [_i] * 8 + [_f, _vp, _sz, _vp, _vp], _i),
+    "tree_attn_verify_latent_paged": ([_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp] + [_i] * 7 +
+                                      [_f, _vp, _sz, _vp, _vp], _i),
+    "prompt_attn_latent": ([_vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp] + [_i] * 7 +
+                           [_f, _vp, _vp], _i),
+    "kv_pages_slots": ([_vp, _vp, _vp] + [_i] * 5 + [_vp] * 5, _i),
+    "kv_slots_write": ([_vp, _vp, _vp] + [_i] * 6 + [_vp, _vp], _i),
+    "kv_slots_read": ([_vp, _vp, _vp] + [_i] * 6 + [_vp, _vp], _i),
 }
 
 
@@ -573,7 +582,8 @@ def _pool(i, k_pages, v_pages):
     of a pool with or without the layer axis."""
     L, (nb, Hkv, bs, D) = (1, k_pages.shape) if k_pages.dim() == 4 else (k_pages.shape[0], k_pages.shape[1:])
     dt, shape = k_pages.dtype, k_pages.shape
-    return _ptr(k_pages, i, dt, shape), _ptr(v_pages, i, dt, shape), k_pages.element_size(), L, Hkv, D, bs, nb
+    v = None if v_pages is None else _ptr(v_pages, i, dt, shape)    # None: a cache of one pool
+    return _ptr(k_pages, i, dt, shape), v, k_pages.element_size(), L, Hkv, D, bs, nb
 
 
 def kv_pages_reserve(k_pages, v_pages, block_table, prefix_len, need, ref_count, table_out, ref_out, workspace=None,
@@ -610,3 +620,113 @@ def kv_pages_compact(k_pages, v_pages, block_table, ref_count, table_out, ref_ou
         _ptr(table_out, i, i32, (B, mb)), _ptr(ref_out, i, i32, (nb,)), _ptr(n_used, i, i32, (1,)),
         None if remap is None else _ptr(remap, i, i32, (nb,)),
         _sized(workspace, i, torch.uint8), workspace.numel(), _word(dev_status, i), stream))
+
+
+def kv_pages_slots(block_table, prefix_len, new_len, offsets, slots, block_size, num_blocks, positions=None,
+                   dev_status=None):
+    """Rows of the pool where the next new_len[b] tokens of every sequence,
+    packed one sequence behind the other, lie: offsets [B + 1], slots [room]
+    and positions [room] (optional), all int32; -1 behind the last token."""
+    B, mb = block_table.shape
+    i32, room = torch.int32, slots.shape
+    i, stream = _device(block_table)
+    _check("kv_pages_slots", load().kv_pages_slots(
+        _ptr(block_table, i, i32, (B, mb)), _ptr(prefix_len, i, i32, (B,)), _ptr(new_len, i, i32, (B,)), B, mb,
+        int(block_size), int(num_blocks), slots.numel(), _ptr(offsets, i, i32, (B + 1,)), _ptr(slots, i, i32, (slots.numel(),)),
+        None if positions is None else _ptr(positions, i, i32, room), _word(dev_status, i), stream))
+
+
+def _slot_rows(name, pages, slots, rows, dev_status):
+    nb, Hkv, bs, D = pages.shape
+    T, dt = slots.numel(), pages.dtype
+    i, stream = _device(pages)
+    _check(name, getattr(load(), name)(
+        _ptr(pages, i, dt, pages.shape), _ptr(slots, i, torch.int32, (T,)), _ptr(rows, i, dt, (T, Hkv, D)),
+        pages.element_size(), T, Hkv, D, bs, nb, _word(dev_status, i), stream))
+
+
+def kv_slots_write(pages, slots, rows, dev_status=None):
+    """rows [T, Hkv, D] into their slots of one pool [num_blocks, Hkv,
+    block_size, D]; negative slots are left out."""
+    _slot_rows("kv_slots_write", pages, slots, rows, dev_status)
+
+
+def kv_slots_read(pages, slots, rows, dev_status=None):
+    """rows [T, Hkv, D] out of their slots; zeros where a slot is negative."""
+    _slot_rows("kv_slots_read", pages, slots, rows, dev_status)
+
+
+ROPE_DIM = 64    # rotary elements at the end of a latent row
+
+
+def tree_attn_latent_workspace_bytes(dtype, batch, n_nodes, hq, latent_dim, rope_dim, max_prefix):
+    return int(load().tree_attn_latent_workspace_bytes(_DT[dtype], batch, n_nodes, hq, latent_dim, rope_dim, max_prefix))
+
+
+def _latent(q, rows, tree, prefix_len, anc_mask, out, max_prefix, workspace):
+    """Checked arguments that both latent entry points share."""
+    B, N, Hq, D = q.shape
+    dt, i32 = q.dtype, torch.int32
+    i, stream = _device(q)
+    lat = D - ROPE_DIM
+    if workspace is None:
+        workspace = _scratch(tree_attn_latent_workspace_bytes(dt, B, N, Hq, lat, ROPE_DIM, max_prefix), q)
+    return (i, stream, lat, B, N, Hq, _ptr(q, i, dt, (B, N, Hq, D)), _ptr(rows, i, dt, rows.shape[:-1] + (D,)),
+            (_ptr(tree, i, dt, (B, N, D)), _ptr(prefix_len, i, i32, (B,)),
+             _sized(anc_mask, i, torch.int64, B * N * mask_words(N)), _ptr(out, i, dt, (B, N, Hq, lat)), _DT.get(dt, -1)),
+            (_sized(workspace, i, torch.uint8), workspace.numel()))
+
+
+def tree_attn_verify_latent(q, cache, tree, prefix_len, anc_mask, out, max_prefix, scale, workspace=None,
+                            dev_status=None):
+    """Tree attention over a cache of latent rows: q [B, N, Hq, latent + 64],
+    cache [B, s_max, latent + 64], tree [B, N, latent + 64], out [B, N, Hq,
+    latent] (float32 or bf16, latent 256 or 512).  ``workspace`` (uint8,
+    tree_attn_latent_workspace_bytes) is allocated per call when not given."""
+    i, stream, lat, B, N, Hq, pq, pc, rest, ws = _latent(q, cache, tree, prefix_len, anc_mask, out, max_prefix, workspace)
+    if cache.dim() != 3 or cache.shape[0] != B:
+        raise ValueError(f"expected a cache of shape {(B, 's_max', lat + ROPE_DIM)}, not {tuple(cache.shape)}")
+    _check("tree_attn_verify_latent", load().tree_attn_verify_latent(
+        pq, pc, *rest, B, N, Hq, lat, ROPE_DIM, cache.shape[1], int(max_prefix), float(scale), *ws, _word(dev_status, i),
+        stream))
+
+
+def tree_attn_verify_latent_paged(q, pages, block_table, tree, prefix_len, anc_mask, out, max_prefix, scale,
+                                  workspace=None, dev_status=None):
+    """tree_attn_verify_latent over pages [num_blocks, block_size, latent + 64]
+    addressed by block_table [B, max_blocks]."""
+    i, stream, lat, B, N, Hq, pq, pp, rest, ws = _latent(q, pages, tree, prefix_len, anc_mask, out, max_prefix, workspace)
+    if pages.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("expected pages of three dims and a block table of two")
+    nb, bs, _ = pages.shape
+    mb = block_table.shape[1]
+    _check("tree_attn_verify_latent_paged", load().tree_attn_verify_latent_paged(
+        pq, pp, _ptr(block_table, i, torch.int32, (B, mb)), bs, nb, mb, *rest, B, N, Hq, lat, ROPE_DIM, int(max_prefix),
+        float(scale), *ws, _word(dev_status, i), stream))
+
+
+def _strided(t, index, dtype, shape):
+    """Pointer of a tensor whose last dim alone has to be contiguous (a column range of a wider one)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and (t.stride(-1) == 1 or t.shape[-1] == 1):
+        return t.data_ptr()
+    raise _refusal(t, index, dtype, shape)
+
+
+def _step(t, d, least):
+    """Elements between neighbours along dim d (any number where there is one)."""
+    return t.stride(d) if t.shape[d] > 1 else least
+
+
+def prompt_attn_latent(q, k, k_rope, v, q_offsets, kv_offsets, out, max_q, scale, dev_status=None):
+    """Causal attention of packed prompt tokens: q [Tq, Hq, 192], k and v [Tk,
+    Hq, 128], k_rope [Tk, 64] (bf16; k, v and k_rope may be column ranges of
+    wider tensors), offsets [B + 1] int32, out [Tq, Hq, 128]."""
+    (Tq, Hq, _), (Tk, _, D) = q.shape, k.shape
+    bf, i32, B = torch.bfloat16, torch.int32, q_offsets.shape[0] - 1
+    i, stream = _device(q)
+    _check("prompt_attn_latent", load().prompt_attn_latent(
+        _ptr(q, i, bf, (Tq, Hq, D + ROPE_DIM)), _strided(k, i, bf, (Tk, Hq, D)), _step(k, 0, Hq * D), _step(k, 1, D),
+        _strided(k_rope, i, bf, (Tk, ROPE_DIM)), _step(k_rope, 0, ROPE_DIM), _strided(v, i, bf, (Tk, Hq, D)),
+        _step(v, 0, Hq * D), _step(v, 1, D),
+        _ptr(q_offsets, i, i32, (B + 1,)), _ptr(kv_offsets, i, i32, (B + 1,)), _ptr(out, i, bf, (Tq, Hq, D)), B, Hq, D,
+        ROPE_DIM, Tq, Tk, int(max_q), float(scale), _word(dev_status, i), stream))
