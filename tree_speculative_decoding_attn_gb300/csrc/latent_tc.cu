@@ -45,7 +45,7 @@ namespace {
 
 using namespace sv::ptx;
 
-constexpr int kBN = 128, kRope = 64, kThreads = 256, kPairs = 76;
+constexpr int kBN = 128, kRope = 64, kThreads = 384, kPairs = 76;
 constexpr uint32_t kPiece = 64 * 128;  // 64 rows (or keys) x 64 elements, 128-byte swizzle
 constexpr uint32_t kStage = 2 * kPiece;
 constexpr uint32_t kWaitLimit = 1u << 22;
@@ -55,28 +55,30 @@ constexpr float kTau = 16.f;      // the maximum moves when a tile exceeds it by
 
 template <int LAT> struct Cfg {
   static constexpr int D = LAT + kRope;
-  static constexpr int KS = LAT / 128 + 1;      // K stages of a tile (the last: rotary dims, half a stage)
-  static constexpr int VS = LAT / 256 * 2;      // V stages
-  static constexpr int NB = LAT == 512 ? 1 : 2; // tiles of stages
+  static constexpr int KG = LAT == 512 ? 3 : 5;  // 64-element column groups of a K stage
+  static constexpr int KS = D / 64 / KG;         // K stages of a tile
+  static constexpr int VJ = LAT / 256;           // blocks of 256 dims (a V stage: 64 keys of all)
+  static constexpr int NB = LAT == 512 ? 1 : 2;  // tiles of stages
   static constexpr uint32_t q_bytes = (D / 64) * kPiece;
-  static constexpr uint32_t k_bytes = (LAT / 64 + 1) * kPiece;  // of one tile
-  static constexpr uint32_t v_bytes = VS * kStage;
+  static constexpr uint32_t k_bytes = q_bytes;        // of one tile, both stages of V alike
+  static constexpr uint32_t v_bytes = 2 * VJ * kStage;
 };
+static_assert(Cfg<512>::KG * Cfg<512>::KS == 9 && Cfg<256>::KG * Cfg<256>::KS == 5, "K stages cover the row");
 
 template <int LAT> struct Bars {
   using C = Cfg<LAT>;
   // (full, p, ofree: the even CTA's count for both)
-  uint64_t kfull[C::NB * C::KS], kempty[C::NB * C::KS], vfull[C::NB * C::VS], vempty[C::NB * C::VS];
-  uint64_t qfull, qempty, sfull[2], p, pv, ofree, vland, drain;
+  uint64_t kfull[C::NB * C::KS], kempty[C::NB * C::KS], vfull[C::NB * 2], vempty[C::NB * 2];
+  uint64_t qfull, qempty, sfull[2], sread[2], p[2], p_odd[2], pv[2], ofree, vland, drain[2];
   long long lo, hi, b0;
   int b;
   uint32_t tmem;
   volatile int abort;
-  float xmax[2][128];
+  float xmax[2][2][128];
 };
 template <int LAT> constexpr uint32_t smem_bytes() {
   using C = Cfg<LAT>;
-  return C::q_bytes + 2 * kPiece + C::NB * (C::k_bytes + C::v_bytes) + sizeof(Bars<LAT>) + 1024;
+  return C::q_bytes + 2 * kPiece + C::NB * (C::k_bytes + C::v_bytes) + sizeof(Bars<LAT>);
 }
 static_assert(smem_bytes<512>() <= 232448 && smem_bytes<256>() <= 232448, "shared memory per CTA exceeds 227 KB");
 
@@ -93,16 +95,23 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 // TMA load into this CTA whose bytes count on a barrier of the pair's even CTA.
-__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
 __device__ __forceinline__ void load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
       ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_5d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
       : "memory");
 }
 // Arrive on a barrier of the cluster, after this thread's (and, behind a
@@ -121,16 +130,22 @@ __device__ __forceinline__ bool try_wait_acquire(uint64_t *bar, uint32_t parity)
   return ok != 0;
 }
 // Bounded wait that also ends once another role of the CTA has given up; its
-// outcome is one for the warp.
-template <class B> __device__ __forceinline__ bool wait(B *bars, uint64_t *bar, uint32_t parity) {
-  bool ok = false;
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if ((ok = try_wait_acquire(bar, parity))) break;
+// outcome is one for the warp.  CLUSTER: threads of the other CTA arrive.
+template <bool CLUSTER = false, class B> __device__ __forceinline__ bool wait(B *bars, uint64_t *bar, uint32_t parity) {
+  bool ok = !CLUSTER && mbar_test(bar, parity);
+  for (uint32_t i = 0; !ok && i < kWaitLimit; ++i) {
+    if ((ok = CLUSTER ? try_wait_acquire(bar, parity) : mbar_try_wait(bar, parity))) break;
     if ((i & 63) == 63 && bars->abort) break;
   }
   ok = __all_sync(0xffffffffu, ok);
   if (!ok) bars->abort = 1;
   return ok;
+}
+// The same where the phase was tested before (a test that need not suspend
+// the thread, done while other work was left, costs less than a wait that
+// finds its phase complete).
+template <class B> __device__ __forceinline__ bool wait_tested(bool done, B *bars, uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, done) || wait(bars, bar, parity);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -189,13 +204,13 @@ struct Walk {
 
 template <int LAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    latent_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
-                     const __grid_constant__ CUtensorMap tm_t, const Work w, const uint64_t *__restrict__ anc,
+    latent_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_tk,
+                     const __grid_constant__ CUtensorMap tm_tv, const Work w, const uint64_t *__restrict__ anc,
                      __nv_bfloat16 *__restrict__ out, float *__restrict__ ws, int4 *__restrict__ desc,
                      float scale_log2, int row_end, int32_t *status, const sv::KvPages pg) {
   using C = Cfg<LAT>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem, *sP = sQ + C::q_bytes, *sK = sP + 2 * kPiece, *sV = sK + C::NB * C::k_bytes;
   Bars<LAT> *bars = reinterpret_cast<Bars<LAT> *>(sV + C::NB * C::v_bytes);
 
@@ -204,25 +219,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int R = w.N * w.hq;
 
+  // The 128-byte swizzle needs 1024-byte aligned tiles; both CTAs of a
+  // cluster see the same layout, so they leave together.
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) sv::report(status, SPEC_DEV_INTERNAL);
+    return;
+  }
   grid_dep_launch();
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NB * C::KS; ++i) {
       mbar_init(&bars->kfull[i], 1);
       mbar_init(&bars->kempty[i], 1);
     }
-    for (int i = 0; i < C::NB * C::VS; ++i) {
+    for (int i = 0; i < C::NB * 2; ++i) {
       mbar_init(&bars->vfull[i], 1);
       mbar_init(&bars->vempty[i], 1);
     }
     mbar_init(&bars->qfull, 1);
     mbar_init(&bars->qempty, 1);
-    mbar_init(&bars->sfull[0], 1);
-    mbar_init(&bars->sfull[1], 1);
-    mbar_init(&bars->p, 8);      // the softmax warps of both CTAs
-    mbar_init(&bars->pv, 1);
-    mbar_init(&bars->ofree, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->sfull[i], 1);
+      mbar_init(&bars->sread[i], 16);  // the softmax warps of both CTAs
+      mbar_init(&bars->p[i], 4);       // this CTA's softmax warps of 64 keys
+      mbar_init(&bars->p_odd[i], 1);   // the odd CTA's p, forwarded to the even one
+      mbar_init(&bars->pv[i], 1);
+      mbar_init(&bars->drain[i], 1);
+    }
+    mbar_init(&bars->ofree, 16);
     mbar_init(&bars->vland, 1);
-    mbar_init(&bars->drain, 1);
     bars->abort = 0;
     mbar_fence_init();
   }
@@ -299,14 +323,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- K
+    // ---------------------------------------------------------------- Q, K
     const bool me = elect_one();
     if (me) {
-      tma_prefetch_desc(&tm_c);
-      tma_prefetch_desc(&tm_t);
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_tk);
     }
     int g = 0;
-    while (ok && walk.advance(w)) {
+    for (int seg = 0; ok && walk.advance(w); ++seg) {
+      if (!(ok = wait(bars, &bars->qempty, (seg & 1) ^ 1))) break;
+      if (me) {
+        if (rank == 0) mbar_expect_tx(&bars->qfull, 2 * C::q_bytes);
+        const uint32_t bar = mapa_cluster(&bars->qfull, 0);
+        for (int i = 0; i < C::KS; ++i)
+          load_4d(sQ + i * C::KG * kPiece, &tm_q, 0, walk.rt * 128 + (int)rank * 64, i * C::KG, walk.b, bar);
+      }
+      __syncwarp();
       for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
         const bool tree = t < w.tree_tiles;
         const int row = tree ? t * kBN + (int)rank * 64 : cache_row(walk.b, (t - w.tree_tiles) * kBN + (int)rank * 64);
@@ -316,14 +349,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int s = buf * C::KS + i;
           if (!(ok = wait(bars, &bars->kempty[s], par))) break;
           if (me) {
-            uint8_t *dst = sK + buf * C::k_bytes + i * kStage;
-            const int pieces = i < C::KS - 1 ? 2 : 1;
-            if (rank == 0) mbar_expect_tx(&bars->kfull[s], 2 * pieces * kPiece);
+            uint8_t *dst = sK + buf * C::k_bytes + i * C::KG * kPiece;
+            if (rank == 0) mbar_expect_tx(&bars->kfull[s], 2 * C::KG * kPiece);
             const uint32_t bar = mapa_cluster(&bars->kfull[s], 0);
-            for (int h = 0; h < pieces; ++h) {
-              if (tree) load_3d(dst + h * kPiece, &tm_t, i * 128 + h * 64, row, walk.b, bar);
-              else load_2d(dst + h * kPiece, &tm_c, i * 128 + h * 64, row, bar);
-            }
+            if (tree) load_4d(dst, &tm_tk, 0, row, i * C::KG, walk.b, bar);
+            else load_3d(dst, &tm_k, 0, row, i * C::KG, bar);
           }
           __syncwarp();
         }
@@ -339,57 +369,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int row = tree ? t * kBN : cache_row(walk.b, (t - w.tree_tiles) * kBN);
         const int buf = g % C::NB;
         const uint32_t par = ((g / C::NB) & 1) ^ 1;
-        for (int i = 0; ok && i < C::VS; ++i) {
-          // stage i: dims [256 (i / 2) + 128 rank, +128) of keys [64 (i % 2), +64)
-          const int s = buf * C::VS + i;
+        for (int kh = 0; ok && kh < 2; ++kh) {
+          // a stage: keys [64 kh, +64), dims [256 j + 128 rank, +128) of every block j
+          const int s = buf * 2 + kh;
           if (!(ok = wait(bars, &bars->vempty[s], par))) break;
           if (me) {
-            uint8_t *dst = sV + buf * C::v_bytes + i * kStage;
-            if (rank == 0) mbar_expect_tx(&bars->vfull[s], 2 * kStage);
+            uint8_t *dst = sV + buf * C::v_bytes + kh * C::VJ * kStage;
+            if (rank == 0) mbar_expect_tx(&bars->vfull[s], 2 * C::VJ * kStage);
             const uint32_t bar = mapa_cluster(&bars->vfull[s], 0);
-            const int d0 = (i >> 1) * 256 + (int)rank * 128, r0 = row + (i & 1) * 64;
-            for (int h = 0; h < 2; ++h) {
-              if (tree) load_3d(dst + h * kPiece, &tm_t, d0 + h * 64, r0, walk.b, bar);
-              else load_2d(dst + h * kPiece, &tm_c, d0 + h * 64, r0, bar);
-            }
+            if (tree) load_5d(dst, &tm_tv, 0, row + kh * 64, 2 * (int)rank, 0, walk.b, bar);
+            else load_4d(dst, &tm_v, 0, row + kh * 64, 2 * (int)rank, 0, bar);
           }
           __syncwarp();
         }
       }
     }
-  } else if (warp == 3) {
-    // ---------------------------------------------------------------- Q
-    const bool me = elect_one();
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------------------- S
+    // (S and PV are issued by two warps: an MMA waits for room in a short
+    // queue, so the waits of one warp run under the products of the other)
+    const uint32_t qa = smem_u32(sQ), ka = smem_u32(sK);
+    int g = 0;
     for (int seg = 0; ok && walk.advance(w); ++seg) {
-      if (!(ok = wait(bars, &bars->qempty, (seg & 1) ^ 1))) break;
-      if (me) {
-        if (rank == 0) mbar_expect_tx(&bars->qfull, 2 * C::q_bytes);
-        const uint32_t bar = mapa_cluster(&bars->qfull, 0);
-        for (int i = 0; i < C::D / 64; ++i)
-          load_3d(sQ + i * kPiece, &tm_q, i * 64, walk.rt * 128 + (int)rank * 64, walk.b, bar);
-      }
-      __syncwarp();
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMAs
-    if (rank == 0) {
-      const uint32_t qa = smem_u32(sQ), ka = smem_u32(sK), va = smem_u32(sV), pa = smem_u32(sP);
-      int g = 0, seg = 0;  // tiles whose S is issued; segments begun
-      bool more = walk.advance(w);
-      int t = walk.t0;
-      // S of tile (walk, t); the last of a segment lets Q go
-      auto issue_s = [&]() -> bool {
-        if (t == walk.t0 && !wait(bars, &bars->qfull, seg & 1)) return false;
+      if (!(ok = wait(bars, &bars->qfull, seg & 1))) break;
+      for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
         const int buf = g % C::NB;
         const uint32_t par = (g / C::NB) & 1, d = tmem + kColS + (g & 1) * 64;
+        bool there = mbar_test(&bars->kfull[buf * C::KS], par);
+        // the buffer's last S has been read
+        if (g >= 2 && !(ok = wait(bars, &bars->sread[g & 1], ((g >> 1) & 1) ^ 1))) break;
 #pragma unroll
         for (int i = 0; i < C::KS; ++i) {
-          if (!wait(bars, &bars->kfull[buf * C::KS + i], par)) return false;
+          if (!(ok = wait_tested(there, bars, &bars->kfull[buf * C::KS + i], par))) break;
+          if (i + 1 < C::KS) there = mbar_test(&bars->kfull[buf * C::KS + i + 1], par);
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t kb = ka + buf * C::k_bytes + i * kStage, qb = qa + i * kStage;
+            const uint32_t at = i * C::KG * kPiece, kb = ka + buf * C::k_bytes + at, qb = qa + at;
 #pragma unroll
-            for (int k = 0; k < (i < C::KS - 1 ? 8 : 4); ++k) {
+            for (int k = 0; k < C::KG * 4; ++k) {
               const uint32_t off = (k >> 2) * kPiece + (k & 3) * 32;
               mma_ss_pair(d, smem_desc_sw128(qb + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024), kIdescS,
                           i > 0 || k > 0);
@@ -402,26 +419,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        return true;
-      };
-      if (more) ok = issue_s();
-      while (ok && more) {
-        // tile `g`: what PV needs to know of it, then S of the tile after it
+      }
+    }
+    if (!ok) {  // let issued MMAs finish before TMEM is freed
+      if (elect_one()) mma_commit_pair_mc(&bars->drain[0], 1);
+      __syncwarp();
+      mbar_wait(&bars->drain[0], 0, kWaitLimit);
+    }
+  } else if (warp == 3 && rank == 0) {
+    // ---------------------------------------------------------------- PV
+    const uint32_t va = smem_u32(sV), pa = smem_u32(sP);
+    int g = 0;
+    for (int seg = 0; ok && walk.advance(w); ++seg) {
+      for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
         const bool start = t == walk.t0;
         const int keys = t < w.tree_tiles ? kBN : min(kBN, walk.P - (t - w.tree_tiles) * kBN);
-        const int cur = g, cur_seg = seg;
-        if (++t >= walk.t1) {
-          more = walk.advance(w);
-          t = walk.t0;
-          ++seg;
-        }
-        ++g;
-        if (more && !(ok = issue_s())) break;
-        const int buf = cur % C::NB;
-        const uint32_t par = (cur / C::NB) & 1;
+        const int buf = g % C::NB;
+        const uint32_t par = (g / C::NB) & 1;
         if (keys < kBN) {
           // the softmax warps clear the V rows past the last key, once they are there
-          for (int i = 0; ok && i < C::VS; ++i) ok = wait(bars, &bars->vfull[buf * C::VS + i], par);
+          for (int kh = 0; ok && kh < 2; ++kh) ok = wait(bars, &bars->vfull[buf * 2 + kh], par);
           if (!ok) break;
           if (elect_one()) {
             arrive_release(mapa_cluster(&bars->vland, 0));
@@ -429,77 +446,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (!(ok = wait(bars, &bars->p, cur & 1))) break;
         // the last segment's O has been read
-        if (start && cur_seg > 0 && !(ok = wait(bars, &bars->ofree, (cur_seg - 1) & 1))) break;
-        tc_fence_after();
+        if (start && seg > 0 && !(ok = wait<true>(bars, &bars->ofree, (seg - 1) & 1))) break;
 #pragma unroll
-        for (int i = 0; i < C::VS; ++i) {
-          if (!(ok = wait(bars, &bars->vfull[buf * C::VS + i], par))) break;
+        for (int kh = 0; kh < 2; ++kh) {
+          const bool there = mbar_test(&bars->vfull[buf * 2 + kh], par);
+          if (!ok || !(ok = wait(bars, &bars->p[kh], g & 1)) || !(ok = wait<true>(bars, &bars->p_odd[kh], g & 1)) ||
+              !(ok = wait_tested(there, bars, &bars->vfull[buf * 2 + kh], par)))
+            break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t vb = va + buf * C::v_bytes + i * kStage, pb = pa + (i & 1) * kPiece;
+            const uint32_t vb = va + buf * C::v_bytes + kh * C::VJ * kStage, pb = pa + kh * kPiece;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ss_pair(tmem + (i >> 1) * 128, smem_desc_sw128(pb + k * 32, 16, 1024),
-                          smem_desc_sw128(vb + k * 2048, kPiece, 1024), kIdescPV, !start || (i & 1) || k > 0);
-            mma_commit_pair_mc(&bars->vempty[buf * C::VS + i], 3);
-            if (i == C::VS - 1) mma_commit_pair_mc(&bars->pv, 3);
+            for (int j = 0; j < C::VJ; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ss_pair(tmem + j * 128, smem_desc_sw128(pb + k * 32, 16, 1024),
+                            smem_desc_sw128(vb + j * kStage + k * 2048, kPiece, 1024), kIdescPV, !start || kh || k > 0);
+            mma_commit_pair_mc(&bars->vempty[buf * 2 + kh], 3);
+            mma_commit_pair_mc(&bars->pv[kh], 3);
           }
           __syncwarp();
         }
       }
-      if (!ok) {  // let issued MMAs finish before TMEM is freed
-        if (elect_one()) mma_commit_pair_mc(&bars->drain, 1);
-        __syncwarp();
-        mbar_wait(&bars->drain, 0, kWaitLimit);
-      }
     }
+    if (!ok) {
+      if (elect_one()) mma_commit_pair_mc(&bars->drain[1], 1);
+      __syncwarp();
+      mbar_wait(&bars->drain[1], 0, kWaitLimit);
+    }
+  } else if (warp == 1 || warp == 3) {
+    // the odd CTA tells the even one of its P, a warp a half of the keys (so
+    // that the softmax warps need not wait for a release at the cluster's scope)
+    const int kh = warp >> 1;
+    const uint32_t bar = mapa_cluster(&bars->p_odd[kh], 0);
+    int g = 0;
+    while (ok && walk.advance(w))
+      for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
+        if (!(ok = wait(bars, &bars->p[kh], g & 1))) break;
+        if (elect_one()) arrive_release(bar);
+        __syncwarp();
+      }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax
-    const int quarter = warp & 3, L = quarter * 32 + lane, r = L & 63, half = L >> 6;
+    // Lane L of TMEM: row L % 64, keys [64 (L / 64), +64) of a tile; this
+    // warp takes columns [32 h, +32) of its lanes.  The four threads of a row
+    // exchange their maxima at a barrier of the four warps of 32 rows.
+    const int quarter = warp & 3, h = (warp - 4) >> 2, L = quarter * 32 + lane, r = L & 63, half = L >> 6;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t p_bar = mapa_cluster(&bars->p, 0), ofree_bar = mapa_cluster(&bars->ofree, 0);
-    auto row_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (quarter & 1)) : "memory"); };
+    auto row_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + (quarter & 1)) : "memory"); };
+    // the four threads' values of this row, in one order for all of them
+    auto row_put = [&](int buf, float v) { bars->xmax[buf][h][L] = v; };
+    const uint32_t sread_bar = mapa_cluster(&bars->sread[0], 0);
     const int words = SPEC_MASK_WORDS(w.N);
     int g = 0, ragged = 0;
+    bool s_there = false;
     while (walk.advance(w)) {
       const int row = walk.rt * 128 + (int)rank * 64 + r;
       const bool row_ok = row < R;
       const uint64_t *mask = anc + ((int64_t)walk.b * w.N + (row_ok ? row / w.hq : 0)) * words;
       float m = kLow, l = 0.f;
       for (int t = walk.t0; t < walk.t1; ++t, ++g) {
-        if (ok) ok = wait(bars, &bars->sfull[g & 1], (g >> 1) & 1);
-        uint32_t x[2][32];
+        // which of this thread's 32 keys the row sees
+        const bool tree = t < w.tree_tiles;
+        const int first = half * 64 + h * 32;
+        const int left = (tree ? w.N - t * kBN : walk.P - (t - w.tree_tiles) * kBN) - first;
+        uint32_t vis = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0u;
+        if (tree && left > 0) vis &= row_ok ? (uint32_t)(mask[2 * t + half] >> (h * 32)) : 0u;
+        if (ok) ok = wait_tested(s_there, bars, &bars->sfull[g & 1], (g >> 1) & 1);
+        uint32_t x[32];
         if (ok) {
           tc_fence_after();
-          const uint32_t s = tmem + lane_off + kColS + (g & 1) * 64;
-          tmem_ld32(s, x[0]);
-          tmem_ld32(s + 32, x[1]);
+          tmem_ld32(tmem + lane_off + kColS + (g & 1) * 64 + h * 32, x);
           tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(sread_bar + (g & 1) * 8);
         } else {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) x[i >> 5][i & 31] = 0;
+          for (int i = 0; i < 32; ++i) x[i] = 0;
         }
-        // which of this thread's 64 keys the row sees
-        const bool tree = t < w.tree_tiles;
-        const int left = (tree ? w.N - t * kBN : walk.P - (t - w.tree_tiles) * kBN) - half * 64;
-        uint64_t vis = left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0ull;
-        if (tree && left > 0) vis &= row_ok ? mask[2 * t + half] : 0ull;
-        if (__any_sync(0xffffffffu, vis != ~0ull)) {
+        if (__any_sync(0xffffffffu, vis != ~0u)) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (!((vis >> i) & 1)) x[i >> 5][i & 31] = 0xff800000u;  // -inf
+          for (int i = 0; i < 32; ++i)
+            if (!((vis >> i) & 1)) x[i] = 0xff800000u;  // -inf
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          mx[i & 3] = fmax3(mx[i & 3], __uint_as_float(x[i >> 4][(2 * i) & 31]),
-                            __uint_as_float(x[i >> 4][(2 * i + 1) & 31]));
-        mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        bars->xmax[g & 1][L] = mx[0];
+        for (int i = 0; i < 16; ++i)
+          mx[i & 3] = fmax3(mx[i & 3], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+        row_put(g & 1, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
         row_sync();
-        const float mt = fmaxf(mx[0], bars->xmax[g & 1][L ^ 64]) * scale_log2;
+        const bool p_free = g > 0 && mbar_test(&bars->pv[half], (g - 1) & 1);
+        const float mt = fmaxf(fmaxf(bars->xmax[g & 1][0][r], bars->xmax[g & 1][0][r + 64]),
+                               fmaxf(bars->xmax[g & 1][1][r], bars->xmax[g & 1][1][r + 64])) * scale_log2;
         const bool need = mt > m + kTau;
         if (__any_sync(0xffffffffu, need)) {
           const float a = need ? ex2(m - mt) : 1.f;
@@ -507,72 +547,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             m = mt;
             l *= a;
           }
-          if (t > walk.t0 && ok && (ok = wait(bars, &bars->pv, (g - 1) & 1))) {
-            tc_fence_after();
+          if (t > walk.t0) {
+            if (ok && (ok = wait(bars, &bars->pv[1], (g - 1) & 1))) {
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < LAT / 2; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(tmem + lane_off + c, o);
-              tmem_wait_ld();
+              for (int c = h * (LAT / 4); c < (h + 1) * (LAT / 4); c += 16) {
+                uint32_t o[16];
+                tmem_ld16(tmem + lane_off + c, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-              tmem_st16(tmem + lane_off + c, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                tmem_st16(tmem + lane_off + c, o);
+              }
+              tmem_wait_st();
+              tc_fence_before();
             }
-            tmem_wait_st();
+            row_sync();  // PV of the first keys adds to what all four warps scale
           }
         }
         // P = 2^(x scale - m), rounded to bf16 for the product (2^-8 of each
         // weight, either way); the row sum takes it unrounded
         const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m, -m);
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t pk[32];
+        uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float2 e = fma2(make_float2(__uint_as_float(x[i >> 4][(2 * i) & 31]),
-                                      __uint_as_float(x[i >> 4][(2 * i + 1) & 31])), sc, nm);
+        for (int i = 0; i < 16; ++i) {
+          float2 e = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc, nm);
           e = make_float2(ex2(e.x), ex2(e.y));
           acc[i & 3] = add2(acc[i & 3], e);
           pk[i] = pack_bf16(e.x, e.y);
         }
         const float2 sum = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
         l += sum.x + sum.y;
-        if (g > 0 && ok) ok = wait(bars, &bars->pv, (g - 1) & 1);  // the last P has been read
+        if (g > 0 && ok) ok = wait_tested(p_free, bars, &bars->pv[half], (g - 1) & 1);  // the last P has been read
         if (ok) {
           uint8_t *dst = sP + half * kPiece + r * 128;
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4 *>(dst + ((c ^ (r & 7)) << 4)) =
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4 *>(dst + (((h * 4 + c) ^ (r & 7)) << 4)) =
                 make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         }
         const int keys = tree ? kBN : min(kBN, walk.P - (t - w.tree_tiles) * kBN);
         if (keys < kBN) {
           // rows past the prefix may hold anything, NaN among it: cleared
-          if (ok) ok = wait(bars, &bars->vland, ragged & 1);
+          if (ok) ok = wait<true>(bars, &bars->vland, ragged & 1);
           ++ragged;
           if (ok) {
             uint8_t *v = sV + (g % C::NB) * C::v_bytes;
-            const int n = (kBN - keys) * 8 * 2;  // 16-byte pieces of one block of 256 dims
-            for (int e = L; e < n * (LAT / 256); e += 128) {
-              const int j = e / n, f = e - j * n, key = keys + (f >> 4), c = f & 15;
-              *reinterpret_cast<uint4 *>(v + (j * 2 + (key >> 6)) * kStage + (c >> 3) * kPiece + (key & 63) * 128 +
+            const int from = max(keys - half * 64, 0);  // among the 64 keys whose P these warps write
+            const int n = max(64 - from, 0) * 16;        // 16-byte pieces of one block of 256 dims
+            for (int e = h * 64 + r; e < n * C::VJ; e += 128) {
+              const int j = e / n, f = e - j * n, c = f & 15;
+              *reinterpret_cast<uint4 *>(v + (half * C::VJ + j) * kStage + (c >> 3) * kPiece + (from + (f >> 4)) * 128 +
                                          (c & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
           }
         }
+        s_there = mbar_test(&bars->sfull[(g + 1) & 1], ((g + 1) >> 1) & 1);
         if (ok) {
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_release(p_bar);
+          if (lane == 0) mbar_arrive(&bars->p[half]);
         }
       }
-      // the whole row's sum: both halves
+      // the whole row's sum
       row_sync();
-      bars->xmax[g & 1][L] = l;
+      row_put(g & 1, l);
       row_sync();
-      const float lt = l + bars->xmax[g & 1][L ^ 64];
+      const float lt = (bars->xmax[g & 1][0][r] + bars->xmax[g & 1][0][r + 64]) +
+                       (bars->xmax[g & 1][1][r] + bars->xmax[g & 1][1][r + 64]);
       row_sync();
-      if (ok) ok = wait(bars, &bars->pv, (g - 1) & 1);
+      if (ok) ok = wait(bars, &bars->pv[1], (g - 1) & 1);
       if (ok) {
         tc_fence_after();
         const bool whole = walk.t0 == 0 && walk.t1 == walk.T;
@@ -581,7 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float *slot = ws + (size_t)(2 * pair + (walk.t0 > 0 ? 0 : 1)) * slot_floats(LAT);
         const int lr = (int)rank * 64 + r;
 #pragma unroll 1
-        for (int c = 0; c < LAT / 2; c += 32) {
+        for (int c = h * (LAT / 4); c < (h + 1) * (LAT / 4); c += 32) {
           uint32_t v[32];
           tmem_ld32(tmem + lane_off + c, v);
           tmem_wait_ld();
@@ -604,11 +650,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4 *>(dst + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
-        if (!whole && row_ok && half == 0)
+        if (!whole && row_ok && half == 0 && h == 0)
           *reinterpret_cast<float2 *>(slot + 128 * (size_t)LAT + 2 * lr) = make_float2(m, lt);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_release(ofree_bar);
+        if (lane == 0) arrive_release(mapa_cluster(&bars->ofree, 0));
       }
     }
   }
@@ -627,44 +673,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of a unit cut between pairs: block (range end, 4 rows),
-// a thread four (LAT 256: two) of the dims.
+// Joins the parts of a unit cut between pairs: block (row, range end), a
+// thread four (LAT 256: two) of the dims.
 template <int LAT>
 __global__ void __launch_bounds__(128)
     latent_join_kernel(const float *__restrict__ ws, const int4 *__restrict__ desc, __nv_bfloat16 *__restrict__ out,
                        int R) {
   constexpr int V = LAT / 128;
+  __shared__ float s_a[kPairs];
   grid_dep_wait();
-  const int pair = blockIdx.x + 1;
+  const int pair = blockIdx.y + 1, lr = blockIdx.x;
   const int4 d = desc[pair];
-  if (d.w == 0) return;
+  const int row = d.y * 128 + lr;
+  if (d.w == 0 || row >= R) return;
   // the first part ends its pair's range (slot 1), the others begin theirs (slot 0)
   auto part = [&](int i) { return ws + (size_t)(i == 0 ? 2 * (pair - 1) + 1 : 2 * (pair - 1 + i)) * slot_floats(LAT); };
-  for (int i = 0; i < 4; ++i) {
-    const int lr = blockIdx.y * 4 + i, row = d.y * 128 + lr;
-    if (row >= R) return;
-    float m = kLow;
-    for (int p = 0; p < d.z; ++p) m = fmaxf(m, part(p)[128 * (size_t)LAT + 2 * lr]);
-    float l = 0.f, acc[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
-#pragma unroll 2
-    for (int p = 0; p < d.z; ++p) {
-      const float *s = part(p);
-      const float2 ml = *reinterpret_cast<const float2 *>(s + 128 * (size_t)LAT + 2 * lr);
-      const float a = exp2f(ml.x - m);
-      l = fmaf(a, ml.y, l);
-      float x[V];
-      if constexpr (V == 4) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(s + (size_t)lr * LAT + threadIdx.x * V);
-      else *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(s + (size_t)lr * LAT + threadIdx.x * V);
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = fmaf(a, x[v], acc[v]);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t *o = reinterpret_cast<uint32_t *>(out + ((int64_t)d.x * R + row) * LAT + threadIdx.x * V);
-#pragma unroll
-    for (int v = 0; v < V / 2; ++v) o[v] = pack_bf16(acc[2 * v] * inv, acc[2 * v + 1] * inv);
+  float m = kLow;
+  for (int p = threadIdx.x & 31; p < d.z; p += 32) m = fmaxf(m, part(p)[128 * (size_t)LAT + 2 * lr]);
+  m = sv::warp_max(m);  // (every warp for itself)
+  if (threadIdx.x < d.z) {
+    const float2 ml = *reinterpret_cast<const float2 *>(part(threadIdx.x) + 128 * (size_t)LAT + 2 * lr);
+    s_a[threadIdx.x] = exp2f(ml.x - m);
   }
+  float l = 0.f;
+  for (int p = threadIdx.x & 31; p < d.z; p += 32) {
+    const float2 ml = *reinterpret_cast<const float2 *>(part(p) + 128 * (size_t)LAT + 2 * lr);
+    l = fmaf(exp2f(ml.x - m), ml.y, l);
+  }
+  l = sv::warp_sum(l);
+  __syncthreads();
+  float acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll 8
+  for (int p = 0; p < d.z; ++p) {
+    const float *s = part(p) + (size_t)lr * LAT + threadIdx.x * V;
+    float x[V];
+    if constexpr (V == 4) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(s);
+    else *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(s);
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(s_a[p], x[v], acc[v]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t *o = reinterpret_cast<uint32_t *>(out + ((int64_t)d.x * R + row) * LAT + threadIdx.x * V);
+#pragma unroll
+  for (int v = 0; v < V / 2; ++v) o[v] = pack_bf16(acc[2 * v] * inv, acc[2 * v + 1] * inv);
 }
 
 // ---------------------------------------------------------------------------
@@ -685,10 +738,26 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-int make_map(CUtensorMap *m, const void *base, cuuint32_t rank, const cuuint64_t *dims, const cuuint64_t *strides) {
+// Rows of `groups` 64-element column groups in boxes of 64 rows x `boxes`
+// groups, which lie in shared memory group by group (a box of 128 rows of 128
+// bytes: 53 bytes a cycle and SM, measured, against 44 of two boxes of 64;
+// 256: 58).  A dim of size 0 is left out.
+struct MapDim {
+  long long size, stride;  // (bytes)
+  int box;
+};
+int make_map(CUtensorMap *m, const void *base, const MapDim (&d)[5]) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return SPEC_ERR_CUDA;
-  const cuuint32_t es[3] = {1, 1, 1}, box[3] = {64, 64, 1};
+  cuuint64_t dims[5], strides[4];
+  cuuint32_t box[5], es[5] = {1, 1, 1, 1, 1}, rank = 0;
+  for (const MapDim &x : d) {
+    if (x.size == 0) continue;
+    dims[rank] = (cuuint64_t)x.size;
+    box[rank] = (cuuint32_t)x.box;
+    if (rank > 0) strides[rank - 1] = (cuuint64_t)x.stride;
+    ++rank;
+  }
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
@@ -708,21 +777,18 @@ int launch(const SvLatentShape &s, const void *q, const void *cache, const void 
            const uint64_t *anc, void *out, float scale, void *ws, int32_t *status, cudaStream_t stream) {
   using C = Cfg<LAT>;
   const int pairs = pairs_of(s), R = s.n_nodes * s.hq;
-  const cuuint64_t row = C::D * 2;
-  const long long rows = s.block_table ? (long long)s.num_blocks * s.block_size : (long long)s.batch * s.s_max;
-  CUtensorMap mq, mc, mt;
-  {
-    const cuuint64_t dims[3] = {C::D, (cuuint64_t)R, (cuuint64_t)s.batch}, strides[2] = {row, row * R};
-    if (make_map(&mq, q, 3, dims, strides) != SPEC_OK) return SPEC_ERR_CUDA;
-  }
-  {
-    const cuuint64_t dims[2] = {C::D, (cuuint64_t)(rows > 0 ? rows : 1)}, strides[1] = {row};
-    if (make_map(&mc, cache, 2, dims, strides) != SPEC_OK) return SPEC_ERR_CUDA;
-  }
-  {
-    const cuuint64_t dims[3] = {C::D, (cuuint64_t)s.n_nodes, (cuuint64_t)s.batch}, strides[2] = {row, row * s.n_nodes};
-    if (make_map(&mt, tree, 3, dims, strides) != SPEC_OK) return SPEC_ERR_CUDA;
-  }
+  const long long row = C::D * 2, groups = C::D / 64, N = s.n_nodes;
+  const long long cached = s.block_table ? (long long)s.num_blocks * s.block_size : (long long)s.batch * s.s_max;
+  const long long rows = cached > 0 ? cached : 1;
+  CUtensorMap mq, mk, mv, mtk, mtv;
+  const MapDim in{64, 0, 64}, none{0, 0, 0};
+  // (the coordinates: element, row, column group; of V the groups of a block, blocks)
+  if (make_map(&mq, q, {in, {R, row, 64}, {groups, 128, C::KG}, {s.batch, row * R, 1}, none}) != SPEC_OK ||
+      make_map(&mk, cache, {in, {rows, row, 64}, {groups, 128, C::KG}, none, none}) != SPEC_OK ||
+      make_map(&mv, cache, {in, {rows, row, 64}, {4, 128, 2}, {C::VJ, 512, C::VJ}, none}) != SPEC_OK ||
+      make_map(&mtk, tree, {in, {N, row, 64}, {groups, 128, C::KG}, {s.batch, row * N, 1}, none}) != SPEC_OK ||
+      make_map(&mtv, tree, {in, {N, row, 64}, {4, 128, 2}, {C::VJ, 512, C::VJ}, {s.batch, row * N, 1}}) != SPEC_OK)
+    return SPEC_ERR_CUDA;
   int4 *desc = static_cast<int4 *>(ws);
   float *slots = reinterpret_cast<float *>(static_cast<char *>(ws) + kPairs * sizeof(int4));
   const Work w{prefix_len, s.batch, s.n_nodes, s.hq, s.s_max, s.max_prefix, (R + 127) / 128, (s.n_nodes + kBN - 1) / kBN};
@@ -730,7 +796,7 @@ int launch(const SvLatentShape &s, const void *q, const void *cache, const void 
                            (int)smem_bytes<LAT>()) != cudaSuccess)
     return SPEC_ERR_CUDA;
   latent_tc_kernel<LAT><<<2 * pairs, kThreads, smem_bytes<LAT>(), stream>>>(
-      mq, mc, mt, w, anc, (__nv_bfloat16 *)out, slots, desc, scale * 1.4426950408889634f, (int)rows, status,
+      mq, mk, mv, mtk, mtv, w, anc, (__nv_bfloat16 *)out, slots, desc, scale * 1.4426950408889634f, (int)rows, status,
       sv::KvPages{s.block_table, s.block_size, s.max_blocks, s.num_blocks});
   if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
   if (pairs == 1) return SPEC_OK;
@@ -738,7 +804,7 @@ int launch(const SvLatentShape &s, const void *q, const void *cache, const void 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pairs - 1, ((R < 128 ? R : 128) + 3) / 4);
+  cfg.gridDim = dim3(R < 128 ? R : 128, pairs - 1);
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cfg.attrs = attr;
