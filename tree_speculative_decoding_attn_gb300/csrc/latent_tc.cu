@@ -19,17 +19,21 @@
 //   S(g)  = Q K(g)^T   N = 128 keys (64 in each CTA), K = LAT + 64
 //   O    += P(g) V(g)  N = 256 dims (128 in each CTA), K = 128 keys, LAT/256
 //                      of them; P in shared memory
-// K and V are the same rows, but the pair splits S by keys and O by dims, so
-// V is loaded again (the second time from L2).  Every stage of a tile has a
-// place of its own that the next tile refills as soon as the MMAs that read
-// it are done: a whole tile (2258 cycles of MMAs) for a load to arrive.
+// K and V are the same rows, but the pair splits S by keys and O by dims: a
+// CTA needs its own 64 keys whole, and of the other 64 the half of the dims
+// that it multiplies in PV.  Of its own keys the other half of the dims is
+// done with after S, and that is where the other CTA's keys are loaded: each
+// "place" (64 keys, 128 dims of every block of 256) holds in both CTAs what
+// PV reads at one shared-memory offset, as the pair MMA asks.  104 KB a tile
+// and SM instead of 136 with V in a place of its own, which an SM takes in at
+// about 55 bytes a cycle at most (TMA boxes of 256 rows of 128 bytes).
 //
-// Shared memory (LAT 512): Q 72 KB, K 72, V 64, P 16.  TMEM: O LAT/2 columns,
-// two S buffers of 64.
-// Roles: warp 0 loads K, 2 V, 3 Q; warp 1 of the even CTA issues all MMAs;
-// warps 4-7 softmax and epilogue: a thread owns 64 keys of one row (lane r and
-// lane r + 64 share row r).  S(g + 1) is issued before P(g) is awaited, so the
-// softmax of a tile runs under the next tile's S and the last one's PV.
+// Shared memory (LAT 512): Q 72 KB, two tiles of latents 128, rotary columns
+// 8, P 16.  TMEM: O LAT/2 columns, two S buffers of 64.
+// Roles: warp 0 loads Q and K, warp 2 V; of the even CTA warp 1 issues S and
+// warp 3 PV; warps 4-11 softmax and epilogue: a thread owns 32 keys of one row (lanes r and r + 64
+// of two warps share row r).  Two S buffers: the softmax of a tile runs under
+// the next tile's S and the last one's PV.
 // Work: all (sequence, 128-row tile) units, each its tree tiles and then its
 // prefix tiles of 128 keys, are cut into one equal range a pair; units cut
 // between pairs leave float32 partials that a second kernel joins.
@@ -47,7 +51,6 @@ using namespace sv::ptx;
 
 constexpr int kBN = 128, kRope = 64, kThreads = 384, kPairs = 76;
 constexpr uint32_t kPiece = 64 * 128;  // 64 rows (or keys) x 64 elements, 128-byte swizzle
-constexpr uint32_t kStage = 2 * kPiece;
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr int kSegW = 3;          // a unit's fixed cost, in tiles
 constexpr float kLow = -3.0e38f;  // running maximum before the first key
@@ -55,21 +58,21 @@ constexpr float kTau = 16.f;      // the maximum moves when a tile exceeds it by
 
 template <int LAT> struct Cfg {
   static constexpr int D = LAT + kRope;
-  static constexpr int KG = LAT == 512 ? 3 : 5;  // 64-element column groups of a K stage
-  static constexpr int KS = D / 64 / KG;         // K stages of a tile
-  static constexpr int VJ = LAT / 256;           // blocks of 256 dims (a V stage: 64 keys of all)
-  static constexpr int NB = LAT == 512 ? 1 : 2;  // tiles of stages
+  static constexpr int VJ = LAT / 256;           // blocks of 256 dims
+  static constexpr int NB = LAT == 512 ? 2 : 4;  // tiles of latent places
+  static constexpr int NR = LAT == 512 ? 1 : 2;  // tiles of rotary columns
+  static constexpr int QG = LAT == 512 ? 3 : 5;  // column groups of a box of Q
   static constexpr uint32_t q_bytes = (D / 64) * kPiece;
-  static constexpr uint32_t k_bytes = q_bytes;        // of one tile, both stages of V alike
-  static constexpr uint32_t v_bytes = 2 * VJ * kStage;
+  static constexpr uint32_t place = 2 * VJ * kPiece;  // 64 keys x 128 dims of every block
+  static constexpr uint32_t c_bytes = 2 * place;      // of one tile
 };
-static_assert(Cfg<512>::KG * Cfg<512>::KS == 9 && Cfg<256>::KG * Cfg<256>::KS == 5, "K stages cover the row");
+static_assert(Cfg<512>::D / 64 % Cfg<512>::QG == 0 && Cfg<256>::D / 64 % Cfg<256>::QG == 0, "Q's boxes cover the row");
 
 template <int LAT> struct Bars {
   using C = Cfg<LAT>;
   // (full, p, ofree: the even CTA's count for both)
-  uint64_t kfull[C::NB * C::KS], kempty[C::NB * C::KS], vfull[C::NB * 2], vempty[C::NB * 2];
-  uint64_t qfull, qempty, sfull[2], sread[2], p[2], p_odd[2], pv[2], ofree, vland, drain[2];
+  uint64_t kfull[C::NB * 2], kread[C::NB * 2], vfull[C::NB * 2], empty[C::NB * 2], rfull[C::NR], rempty[C::NR];
+  uint64_t qfull, qempty, sfull[2], sread[2], p[2], pv[2], ofree, vland, drain[2];
   long long lo, hi, b0;
   int b;
   uint32_t tmem;
@@ -78,7 +81,7 @@ template <int LAT> struct Bars {
 };
 template <int LAT> constexpr uint32_t smem_bytes() {
   using C = Cfg<LAT>;
-  return C::q_bytes + 2 * kPiece + C::NB * (C::k_bytes + C::v_bytes) + sizeof(Bars<LAT>);
+  return C::q_bytes + 2 * kPiece + C::NB * C::c_bytes + C::NR * kPiece + sizeof(Bars<LAT>);
 }
 static_assert(smem_bytes<512>() <= 232448 && smem_bytes<256>() <= 232448, "shared memory per CTA exceeds 227 KB");
 
@@ -95,6 +98,12 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 // TMA load into this CTA whose bytes count on a barrier of the pair's even CTA.
+__device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -204,15 +213,15 @@ struct Walk {
 
 template <int LAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    latent_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_tk,
-                     const __grid_constant__ CUtensorMap tm_tv, const Work w, const uint64_t *__restrict__ anc,
+    latent_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
+                     const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_tc,
+                     const __grid_constant__ CUtensorMap tm_tr, const Work w, const uint64_t *__restrict__ anc,
                      __nv_bfloat16 *__restrict__ out, float *__restrict__ ws, int4 *__restrict__ desc,
                      float scale_log2, int row_end, int32_t *status, const sv::KvPages pg) {
   using C = Cfg<LAT>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *sQ = smem, *sP = sQ + C::q_bytes, *sK = sP + 2 * kPiece, *sV = sK + C::NB * C::k_bytes;
-  Bars<LAT> *bars = reinterpret_cast<Bars<LAT> *>(sV + C::NB * C::v_bytes);
+  uint8_t *sQ = smem, *sP = sQ + C::q_bytes, *sC = sP + 2 * kPiece, *sR = sC + C::NB * C::c_bytes;
+  Bars<LAT> *bars = reinterpret_cast<Bars<LAT> *>(sR + C::NR * kPiece);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -227,21 +236,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   grid_dep_launch();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NB * C::KS; ++i) {
-      mbar_init(&bars->kfull[i], 1);
-      mbar_init(&bars->kempty[i], 1);
-    }
     for (int i = 0; i < C::NB * 2; ++i) {
+      mbar_init(&bars->kfull[i], 1);
+      mbar_init(&bars->kread[i], 1);
       mbar_init(&bars->vfull[i], 1);
-      mbar_init(&bars->vempty[i], 1);
+      mbar_init(&bars->empty[i], 1);
+    }
+    for (int i = 0; i < C::NR; ++i) {
+      mbar_init(&bars->rfull[i], 1);
+      mbar_init(&bars->rempty[i], 1);
     }
     mbar_init(&bars->qfull, 1);
     mbar_init(&bars->qempty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->sfull[i], 1);
       mbar_init(&bars->sread[i], 16);  // the softmax warps of both CTAs
-      mbar_init(&bars->p[i], 4);       // this CTA's softmax warps of 64 keys
-      mbar_init(&bars->p_odd[i], 1);   // the odd CTA's p, forwarded to the even one
+      mbar_init(&bars->p[i], 8);       // those of 64 keys
       mbar_init(&bars->pv[i], 1);
       mbar_init(&bars->drain[i], 1);
     }
@@ -322,13 +332,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return row < 0 ? row_end : row;
   };
 
+  // 64 rows from `row` on, of every block of 256 dims the half h, into a place.
+  auto load_place = [&](uint8_t *dst, bool tree, int row, int h, int b, uint32_t bar) {
+    if (tree) load_5d(dst, &tm_tc, 0, row, 2 * h, 0, b, bar);
+    else load_4d(dst, &tm_c, 0, row, 2 * h, 0, bar);
+  };
+
   if (warp == 0) {
     // ---------------------------------------------------------------- Q, K
     const bool me = elect_one();
     if (me) {
       tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_tk);
+      tma_prefetch_desc(&tm_c);
+      tma_prefetch_desc(&tm_r);
+      tma_prefetch_desc(&tm_tc);
+      tma_prefetch_desc(&tm_tr);
     }
     int g = 0;
     for (int seg = 0; ok && walk.advance(w); ++seg) {
@@ -336,24 +354,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (me) {
         if (rank == 0) mbar_expect_tx(&bars->qfull, 2 * C::q_bytes);
         const uint32_t bar = mapa_cluster(&bars->qfull, 0);
-        for (int i = 0; i < C::KS; ++i)
-          load_4d(sQ + i * C::KG * kPiece, &tm_q, 0, walk.rt * 128 + (int)rank * 64, i * C::KG, walk.b, bar);
+        for (int i = 0; i < C::D / 64; i += C::QG)
+          load_4d(sQ + i * kPiece, &tm_q, 0, walk.rt * 128 + (int)rank * 64, i, walk.b, bar);
       }
       __syncwarp();
       for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
         const bool tree = t < w.tree_tiles;
         const int row = tree ? t * kBN + (int)rank * 64 : cache_row(walk.b, (t - w.tree_tiles) * kBN + (int)rank * 64);
-        const int buf = g % C::NB;
-        const uint32_t par = ((g / C::NB) & 1) ^ 1;
-        for (int i = 0; ok && i < C::KS; ++i) {
-          const int s = buf * C::KS + i;
-          if (!(ok = wait(bars, &bars->kempty[s], par))) break;
+        const int buf = g % C::NB, rb = g % C::NR;
+        if (!(ok = wait(bars, &bars->rempty[rb], ((g / C::NR) & 1) ^ 1))) break;
+        if (me) {
+          if (rank == 0) mbar_expect_tx(&bars->rfull[rb], 2 * kPiece);
+          const uint32_t bar = mapa_cluster(&bars->rfull[rb], 0);
+          if (tree) load_3d(sR + rb * kPiece, &tm_tr, LAT, row, walk.b, bar);
+          else load_2d(sR + rb * kPiece, &tm_r, LAT, row, bar);
+        }
+        __syncwarp();
+        for (int h = 0; ok && h < 2; ++h) {
+          const int s = buf * 2 + h;
+          if (!(ok = wait(bars, &bars->empty[s], ((g / C::NB) & 1) ^ 1))) break;
           if (me) {
-            uint8_t *dst = sK + buf * C::k_bytes + i * C::KG * kPiece;
-            if (rank == 0) mbar_expect_tx(&bars->kfull[s], 2 * C::KG * kPiece);
-            const uint32_t bar = mapa_cluster(&bars->kfull[s], 0);
-            if (tree) load_4d(dst, &tm_tk, 0, row, i * C::KG, walk.b, bar);
-            else load_3d(dst, &tm_k, 0, row, i * C::KG, bar);
+            if (rank == 0) mbar_expect_tx(&bars->kfull[s], 2 * C::place);
+            load_place(sC + s * C::place, tree, row, h, walk.b, mapa_cluster(&bars->kfull[s], 0));
           }
           __syncwarp();
         }
@@ -361,58 +383,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------------- V
+    // the half of the dims that this CTA multiplies of the other CTA's keys,
+    // over the half that it does not of its own
     const bool me = elect_one();
+    const int h = 1 - (int)rank;
     int g = 0;
     while (ok && walk.advance(w)) {
       for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
         const bool tree = t < w.tree_tiles;
-        const int row = tree ? t * kBN : cache_row(walk.b, (t - w.tree_tiles) * kBN);
-        const int buf = g % C::NB;
-        const uint32_t par = ((g / C::NB) & 1) ^ 1;
-        for (int kh = 0; ok && kh < 2; ++kh) {
-          // a stage: keys [64 kh, +64), dims [256 j + 128 rank, +128) of every block j
-          const int s = buf * 2 + kh;
-          if (!(ok = wait(bars, &bars->vempty[s], par))) break;
-          if (me) {
-            uint8_t *dst = sV + buf * C::v_bytes + kh * C::VJ * kStage;
-            if (rank == 0) mbar_expect_tx(&bars->vfull[s], 2 * C::VJ * kStage);
-            const uint32_t bar = mapa_cluster(&bars->vfull[s], 0);
-            if (tree) load_5d(dst, &tm_tv, 0, row + kh * 64, 2 * (int)rank, 0, walk.b, bar);
-            else load_4d(dst, &tm_v, 0, row + kh * 64, 2 * (int)rank, 0, bar);
+        const int row = (tree ? t * kBN : cache_row(walk.b, (t - w.tree_tiles) * kBN)) + h * 64;
+        const int s = g % C::NB * 2 + h;
+        if (!(ok = wait(bars, &bars->kread[s], (g / C::NB) & 1))) break;
+        if (me) {
+          if (rank == 0) {
+            mbar_expect_tx(&bars->vfull[s], C::place);      // this CTA's load
+            mbar_expect_tx(&bars->vfull[s ^ 1], C::place);  // the odd CTA's
           }
-          __syncwarp();
+          load_place(sC + s * C::place, tree, row, (int)rank, walk.b, mapa_cluster(&bars->vfull[s], 0));
         }
+        __syncwarp();
       }
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------------- S
     // (S and PV are issued by two warps: an MMA waits for room in a short
     // queue, so the waits of one warp run under the products of the other)
-    const uint32_t qa = smem_u32(sQ), ka = smem_u32(sK);
+    const uint32_t qa = smem_u32(sQ), ca = smem_u32(sC), ra = smem_u32(sR);
     int g = 0;
     for (int seg = 0; ok && walk.advance(w); ++seg) {
       if (!(ok = wait(bars, &bars->qfull, seg & 1))) break;
       for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
-        const int buf = g % C::NB;
+        const int s = g % C::NB * 2, rb = g % C::NR;
         const uint32_t par = (g / C::NB) & 1, d = tmem + kColS + (g & 1) * 64;
-        bool there = mbar_test(&bars->kfull[buf * C::KS], par);
+        bool there = mbar_test(&bars->rfull[rb], (g / C::NR) & 1);
         // the buffer's last S has been read
         if (g >= 2 && !(ok = wait(bars, &bars->sread[g & 1], ((g >> 1) & 1) ^ 1))) break;
+        if (!(ok = wait_tested(there, bars, &bars->rfull[rb], (g / C::NR) & 1))) break;
+        there = mbar_test(&bars->kfull[s], par);
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < C::KS; ++i) {
-          if (!(ok = wait_tested(there, bars, &bars->kfull[buf * C::KS + i], par))) break;
-          if (i + 1 < C::KS) there = mbar_test(&bars->kfull[buf * C::KS + i + 1], par);
+          for (int k = 0; k < 4; ++k)
+            mma_ss_pair(d, smem_desc_sw128(qa + LAT / 64 * kPiece + k * 32, 16, 1024),
+                        smem_desc_sw128(ra + rb * kPiece + k * 32, 16, 1024), kIdescS, k > 0);
+          mma_commit_pair_mc(&bars->rempty[rb], 3);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || !(ok = wait_tested(there, bars, &bars->kfull[s + h], par))) break;
+          if (h == 0) there = mbar_test(&bars->kfull[s + 1], par);
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t at = i * C::KG * kPiece, kb = ka + buf * C::k_bytes + at, qb = qa + at;
 #pragma unroll
-            for (int k = 0; k < C::KG * 4; ++k) {
-              const uint32_t off = (k >> 2) * kPiece + (k & 3) * 32;
-              mma_ss_pair(d, smem_desc_sw128(qb + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024), kIdescS,
-                          i > 0 || k > 0);
+            for (int k = 0; k < C::VJ * 8; ++k) {
+              // 16 dims: block k / 8, column group 2 h + (k / 4) % 2 of it
+              const uint32_t qo = ((k >> 3) * 4 + 2 * h + ((k >> 2) & 1)) * kPiece + (k & 3) * 32;
+              mma_ss_pair(d, smem_desc_sw128(qa + qo, 16, 1024),
+                          smem_desc_sw128(ca + (s + h) * C::place + (k >> 2) * kPiece + (k & 3) * 32, 16, 1024), kIdescS, 1);
             }
-            mma_commit_pair_mc(&bars->kempty[buf * C::KS + i], 3);
-            if (i == C::KS - 1) {
+            mma_commit_pair_mc(&bars->kread[s + h], 3);
+            if (h == 1) {
               mma_commit_pair_mc(&bars->sfull[g & 1], 3);
               if (t == walk.t1 - 1) mma_commit_pair_mc(&bars->qempty, 3);
             }
@@ -428,17 +459,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 3 && rank == 0) {
     // ---------------------------------------------------------------- PV
-    const uint32_t va = smem_u32(sV), pa = smem_u32(sP);
+    const uint32_t ca = smem_u32(sC), pa = smem_u32(sP);
     int g = 0;
     for (int seg = 0; ok && walk.advance(w); ++seg) {
       for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
         const bool start = t == walk.t0;
         const int keys = t < w.tree_tiles ? kBN : min(kBN, walk.P - (t - w.tree_tiles) * kBN);
-        const int buf = g % C::NB;
+        const int s = g % C::NB * 2;
         const uint32_t par = (g / C::NB) & 1;
         if (keys < kBN) {
           // the softmax warps clear the V rows past the last key, once they are there
-          for (int kh = 0; ok && kh < 2; ++kh) ok = wait(bars, &bars->vfull[buf * 2 + kh], par);
+          for (int kh = 0; ok && kh < 2; ++kh) ok = wait(bars, &bars->vfull[s + kh], par);
           if (!ok) break;
           if (elect_one()) {
             arrive_release(mapa_cluster(&bars->vland, 0));
@@ -447,23 +478,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         // the last segment's O has been read
-        if (start && seg > 0 && !(ok = wait<true>(bars, &bars->ofree, (seg - 1) & 1))) break;
+        if (start && seg > 0 && !(ok = wait(bars, &bars->ofree, (seg - 1) & 1))) break;
 #pragma unroll
         for (int kh = 0; kh < 2; ++kh) {
-          const bool there = mbar_test(&bars->vfull[buf * 2 + kh], par);
-          if (!ok || !(ok = wait(bars, &bars->p[kh], g & 1)) || !(ok = wait<true>(bars, &bars->p_odd[kh], g & 1)) ||
-              !(ok = wait_tested(there, bars, &bars->vfull[buf * 2 + kh], par)))
+          const bool there = mbar_test(&bars->vfull[s + kh], par);
+          if (!ok || !(ok = wait(bars, &bars->p[kh], g & 1)) ||
+              !(ok = wait_tested(there, bars, &bars->vfull[s + kh], par)))
             break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t vb = va + buf * C::v_bytes + kh * C::VJ * kStage, pb = pa + kh * kPiece;
+            const uint32_t vb = ca + (s + kh) * C::place, pb = pa + kh * kPiece;
 #pragma unroll
             for (int j = 0; j < C::VJ; ++j)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_ss_pair(tmem + j * 128, smem_desc_sw128(pb + k * 32, 16, 1024),
-                            smem_desc_sw128(vb + j * kStage + k * 2048, kPiece, 1024), kIdescPV, !start || kh || k > 0);
-            mma_commit_pair_mc(&bars->vempty[buf * 2 + kh], 3);
+                            smem_desc_sw128(vb + j * 2 * kPiece + k * 2048, kPiece, 1024), kIdescPV, !start || kh || k > 0);
+            mma_commit_pair_mc(&bars->empty[s + kh], 3);
             mma_commit_pair_mc(&bars->pv[kh], 3);
           }
           __syncwarp();
@@ -475,18 +506,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       mbar_wait(&bars->drain[1], 0, kWaitLimit);
     }
-  } else if (warp == 1 || warp == 3) {
-    // the odd CTA tells the even one of its P, a warp a half of the keys (so
-    // that the softmax warps need not wait for a release at the cluster's scope)
-    const int kh = warp >> 1;
-    const uint32_t bar = mapa_cluster(&bars->p_odd[kh], 0);
-    int g = 0;
-    while (ok && walk.advance(w))
-      for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
-        if (!(ok = wait(bars, &bars->p[kh], g & 1))) break;
-        if (elect_one()) arrive_release(bar);
-        __syncwarp();
-      }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax
     // Lane L of TMEM: row L % 64, keys [64 (L / 64), +64) of a tile; this
@@ -497,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto row_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + (quarter & 1)) : "memory"); };
     // the four threads' values of this row, in one order for all of them
     auto row_put = [&](int buf, float v) { bars->xmax[buf][h][L] = v; };
-    const uint32_t sread_bar = mapa_cluster(&bars->sread[0], 0);
+    const uint32_t sread_bar = mapa_cluster(&bars->sread[0], 0), p_bar = mapa_cluster(&bars->p[half], 0);
     const int words = SPEC_MASK_WORDS(w.N);
     int g = 0, ragged = 0;
     bool s_there = false;
@@ -593,12 +612,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (ok) ok = wait<true>(bars, &bars->vland, ragged & 1);
           ++ragged;
           if (ok) {
-            uint8_t *v = sV + (g % C::NB) * C::v_bytes;
+            uint8_t *v = sC + (g % C::NB * 2 + half) * C::place;
             const int from = max(keys - half * 64, 0);  // among the 64 keys whose P these warps write
             const int n = max(64 - from, 0) * 16;        // 16-byte pieces of one block of 256 dims
             for (int e = h * 64 + r; e < n * C::VJ; e += 128) {
               const int j = e / n, f = e - j * n, c = f & 15;
-              *reinterpret_cast<uint4 *>(v + (half * C::VJ + j) * kStage + (c >> 3) * kPiece + (from + (f >> 4)) * 128 +
+              *reinterpret_cast<uint4 *>(v + (j * 2 + (c >> 3)) * kPiece + (from + (f >> 4)) * 128 +
                                          (c & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
           }
@@ -608,7 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->p[half]);
+          if (lane == 0) mbar_arrive_cluster(p_bar);
         }
       }
       // the whole row's sum
@@ -654,7 +673,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float2 *>(slot + 128 * (size_t)LAT + 2 * lr) = make_float2(m, lt);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_release(mapa_cluster(&bars->ofree, 0));
+        if (lane == 0) mbar_arrive_cluster(mapa_cluster(&bars->ofree, 0));
       }
     }
   }
@@ -780,14 +799,14 @@ int launch(const SvLatentShape &s, const void *q, const void *cache, const void 
   const long long row = C::D * 2, groups = C::D / 64, N = s.n_nodes;
   const long long cached = s.block_table ? (long long)s.num_blocks * s.block_size : (long long)s.batch * s.s_max;
   const long long rows = cached > 0 ? cached : 1;
-  CUtensorMap mq, mk, mv, mtk, mtv;
-  const MapDim in{64, 0, 64}, none{0, 0, 0};
-  // (the coordinates: element, row, column group; of V the groups of a block, blocks)
-  if (make_map(&mq, q, {in, {R, row, 64}, {groups, 128, C::KG}, {s.batch, row * R, 1}, none}) != SPEC_OK ||
-      make_map(&mk, cache, {in, {rows, row, 64}, {groups, 128, C::KG}, none, none}) != SPEC_OK ||
-      make_map(&mv, cache, {in, {rows, row, 64}, {4, 128, 2}, {C::VJ, 512, C::VJ}, none}) != SPEC_OK ||
-      make_map(&mtk, tree, {in, {N, row, 64}, {groups, 128, C::KG}, {s.batch, row * N, 1}, none}) != SPEC_OK ||
-      make_map(&mtv, tree, {in, {N, row, 64}, {4, 128, 2}, {C::VJ, 512, C::VJ}, {s.batch, row * N, 1}}) != SPEC_OK)
+  CUtensorMap mq, mc, mr, mtc, mtr;
+  const MapDim in{64, 0, 64}, all{C::D, 0, 64}, none{0, 0, 0};
+  // (the coordinates: element, row, column group; of a place the groups of a block, blocks)
+  if (make_map(&mq, q, {in, {R, row, 64}, {groups, 128, C::QG}, {s.batch, row * R, 1}, none}) != SPEC_OK ||
+      make_map(&mc, cache, {in, {rows, row, 64}, {4, 128, 2}, {C::VJ, 512, C::VJ}, none}) != SPEC_OK ||
+      make_map(&mr, cache, {all, {rows, row, 64}, none, none, none}) != SPEC_OK ||
+      make_map(&mtc, tree, {in, {N, row, 64}, {4, 128, 2}, {C::VJ, 512, C::VJ}, {s.batch, row * N, 1}}) != SPEC_OK ||
+      make_map(&mtr, tree, {all, {N, row, 64}, {s.batch, row * N, 1}, none, none}) != SPEC_OK)
     return SPEC_ERR_CUDA;
   int4 *desc = static_cast<int4 *>(ws);
   float *slots = reinterpret_cast<float *>(static_cast<char *>(ws) + kPairs * sizeof(int4));
@@ -796,7 +815,7 @@ int launch(const SvLatentShape &s, const void *q, const void *cache, const void 
                            (int)smem_bytes<LAT>()) != cudaSuccess)
     return SPEC_ERR_CUDA;
   latent_tc_kernel<LAT><<<2 * pairs, kThreads, smem_bytes<LAT>(), stream>>>(
-      mq, mk, mv, mtk, mtv, w, anc, (__nv_bfloat16 *)out, slots, desc, scale * 1.4426950408889634f, (int)rows, status,
+      mq, mc, mr, mtc, mtr, w, anc, (__nv_bfloat16 *)out, slots, desc, scale * 1.4426950408889634f, (int)rows, status,
       sv::KvPages{s.block_table, s.block_size, s.max_blocks, s.num_blocks});
   if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
   if (pairs == 1) return SPEC_OK;
