@@ -784,11 +784,12 @@ int make_map(CUtensorMap *m, const void *base, const MapDim (&d)[5]) {
              : SPEC_ERR_CUDA;
 }
 
-// Pairs to run: no more than tiles (at max_prefix).
+// Pairs to run: two tiles (at max_prefix) each or more.  5000 keys of one
+// token: 41 pairs 21.8 us, 21: 18.9, 14: 19.4, 11: 18.8 (parts to join).
 int pairs_of(const SvLatentShape &s) {
   const long long units = (long long)s.batch * (((long long)s.n_nodes * s.hq + 127) / 128);
   const long long tiles = units * ((s.max_prefix + kBN - 1) / kBN + (s.n_nodes + kBN - 1) / kBN);
-  return (int)(tiles < kPairs ? tiles : kPairs);
+  return (int)((tiles + 1) / 2 < kPairs ? (tiles + 1) / 2 : kPairs);
 }
 
 template <int LAT>

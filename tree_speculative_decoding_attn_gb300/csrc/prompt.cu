@@ -31,7 +31,7 @@ namespace {
 
 using namespace sv::ptx;
 
-constexpr int kBN = 128, kD = 128, kRope = 64, kThreads = 384, kTiles = 2;
+constexpr int kBN = 128, kD = 128, kRope = 64, kThreads = 640, kTiles = 2;
 constexpr uint32_t kPiece = 128 * 128;  // 128 rows x 64 elements, 128-byte swizzle
 constexpr uint32_t kQBytes = 3 * kPiece, kKBytes = 3 * kPiece, kVBytes = 2 * kPiece;
 constexpr uint32_t kWaitLimit = 1u << 22;
@@ -39,11 +39,13 @@ constexpr float kLow = -3.0e38f;  // running maximum before the first key
 constexpr float kTau = 16.f;      // the maximum moves when a tile exceeds it by more than 2^kTau
 
 struct Bars {
-  uint64_t q[kTiles], kfull[2], kempty[2], vfull, vempty, sfull[kTiles], p[kTiles], pv[kTiles], drain;
+  uint64_t q[kTiles], kfull[2], kempty[2], vfull, vempty, vclear, sfull[kTiles], p[kTiles], pv[kTiles], drain[kTiles];
   uint32_t tmem;
   volatile int abort;
+  // by half of the keys and row (one buffer: S(j + 1) comes after both halves' P(j))
+  float xmax[2][kTiles * 128];
 };
-constexpr uint32_t kSmemBytes = kTiles * kQBytes + 2 * kKBytes + kVBytes + sizeof(Bars) + 1024;
+constexpr uint32_t kSmemBytes = kTiles * kQBytes + 2 * kKBytes + kVBytes + sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KB");
 
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // Q, K both K-major
@@ -87,8 +89,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int q0 = (int)(gridDim.z - 1 - blockIdx.z) * kTiles * 128;  // first query of this CTA
   if (q0 >= n) return;
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // the 128-byte swizzle needs it
+    if (threadIdx.x == 0) sv::report(status, SPEC_DEV_INTERNAL);
+    return;
+  }
   uint8_t *sQ = smem, *sK = sQ + kTiles * kQBytes, *sV = sK + 2 * kKBytes;
   Bars *bars = reinterpret_cast<Bars *>(sV + kVBytes);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -107,14 +112,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q[i], 1);
       mbar_init(&bars->kfull[i], 1);
-      mbar_init(&bars->kempty[i], 1);
+      mbar_init(&bars->kempty[i], kTiles);
       mbar_init(&bars->sfull[i], 1);
-      mbar_init(&bars->p[i], 4);
+      mbar_init(&bars->p[i], 8);
       mbar_init(&bars->pv[i], 1);
+      mbar_init(&bars->drain[i], 1);
     }
     mbar_init(&bars->vfull, 1);
-    mbar_init(&bars->vempty, 1);
-    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->vempty, kTiles);
+    mbar_init(&bars->vclear, 1);
     bars->abort = 0;
     mbar_fence_init();
   }
@@ -166,104 +172,112 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++v_done;
       __syncwarp();
     }
+    if (ok && all > 0 && (ok = wait(bars, &bars->vfull, (all - 1) & 1))) {
+      // what follows the sequence's last key belongs to others: cleared
+      const int keys = m_keys - (all - 1) * kBN;
+      if (keys < kBN) {
+        for (int e = lane; e < (kBN - keys) * 16; e += 32)
+          *reinterpret_cast<uint4 *>(sV + (e & 8 ? kPiece : 0) + (keys + (e >> 4)) * 128 + (e & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (me) mbar_arrive(&bars->vclear);
+      }
+    }
     if (!ok) {  // let the copies into this CTA land before it exits
       for (int i = 0; i < kTiles; ++i)
         if (k_done > 0 && tiles[i] > 0) mbar_wait(&bars->q[i], 0, kWaitLimit);
       for (int j = k_done > 2 ? k_done - 2 : 0; j < k_done; ++j) mbar_wait(&bars->kfull[j & 1], (j >> 1) & 1, kWaitLimit);
       if (v_done > 0) mbar_wait(&bars->vfull, (v_done - 1) & 1, kWaitLimit);
     }
-  } else if (warp == 1) {
+  } else if (warp < 1 + kTiles) {
     // ---------------------------------------------------------------- MMAs
-    const uint32_t qa = smem_u32(sQ), ka = smem_u32(sK), va = smem_u32(sV);
+    // (a warp a tile: an MMA waits for room in a short queue, so the waits of
+    // one warp run under the products of the other)
+    const int i = warp - 1;
+    const uint32_t qa = smem_u32(sQ) + i * kQBytes, ka = smem_u32(sK), va = smem_u32(sV);
+    const uint32_t s_col = tmem + i * 128, o_col = tmem + 256 + i * 128;
+    const int nt = i == 0 ? tiles[0] : tiles[1];
+    if (nt > 0) ok = wait(bars, &bars->q[i], 0);
     for (int j = 0; ok && j < all; ++j) {
       if (!(ok = wait(bars, &bars->kfull[j & 1], (j >> 1) & 1))) break;
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        if (!ok || j >= tiles[i]) continue;
-        if (j == 0) ok = wait(bars, &bars->q[i], 0);
-        else ok = wait(bars, &bars->pv[i], (j - 1) & 1);  // P(j - 1), where S goes, has been read
-        if (!ok) continue;
+      if (j < nt) {
+        // P(j - 1), where S goes, has been read
+        if (j > 0 && !(ok = wait(bars, &bars->pv[i], (j - 1) & 1))) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 12; ++k) {
             const uint32_t off = (k >> 2) * kPiece + (k & 3) * 32;
-            mma_ss(tmem + i * 128, smem_desc_sw128(qa + i * kQBytes + off, 16, 1024),
-                   smem_desc_sw128(ka + (j & 1) * kKBytes + off, 16, 1024), kIdescS, k > 0);
+            mma_ss(s_col, smem_desc_sw128(qa + off, 16, 1024), smem_desc_sw128(ka + (j & 1) * kKBytes + off, 16, 1024),
+                   kIdescS, k > 0);
           }
           mma_commit(&bars->sfull[i]);
+          mma_commit(&bars->kempty[j & 1]);
         }
         __syncwarp();
+      } else if (elect_one()) {
+        mbar_arrive(&bars->kempty[j & 1]);
       }
-      if (!ok) break;
-      if (elect_one()) mma_commit(&bars->kempty[j & 1]);
-      __syncwarp();
       if (!(ok = wait(bars, &bars->vfull, j & 1))) break;
-      const int keys = m_keys - j * kBN;
-      if (keys < kBN) {
-        // what follows the sequence's last key belongs to others: cleared
-        for (int e = lane; e < (kBN - keys) * 16; e += 32)
-          *reinterpret_cast<uint4 *>(sV + (e & 8 ? kPiece : 0) + (keys + (e >> 4)) * 128 + (e & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        if (!ok || j >= tiles[i]) continue;
-        if (!(ok = wait(bars, &bars->p[i], j & 1))) continue;
+      if (j < nt) {
+        if (m_keys - j * kBN < kBN && !(ok = wait(bars, &bars->vclear, 0))) break;
+        if (!(ok = wait(bars, &bars->p[i], j & 1))) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, smem_desc_sw128(va + k * 2048, kPiece, 1024), kIdescPV,
-                   j > 0 || k > 0);
+            mma_ts(o_col, s_col + k * 8, smem_desc_sw128(va + k * 2048, kPiece, 1024), kIdescPV, j > 0 || k > 0);
           mma_commit(&bars->pv[i]);
+          mma_commit(&bars->vempty);
         }
         __syncwarp();
+      } else if (elect_one()) {
+        mbar_arrive(&bars->vempty);
       }
-      if (!ok) break;
-      if (elect_one()) mma_commit(&bars->vempty);
-      __syncwarp();
     }
     if (!ok) {  // let issued MMAs finish before TMEM is freed
-      if (elect_one()) mma_commit(&bars->drain);
+      if (elect_one()) mma_commit(&bars->drain[i]);
       __syncwarp();
-      mbar_wait(&bars->drain, 0, kWaitLimit);
+      mbar_wait(&bars->drain[i], 0, kWaitLimit);
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax
-    const int i = (warp - 4) >> 2, quarter = warp & 3;
-    const int qi = q0 + i * 128 + quarter * 32 + lane;  // this thread's query
-    const int seen = qi < n ? m_keys - n + qi + 1 : 0;   // keys that it sees (<= 0: none)
-    const uint32_t s_addr = tmem + ((uint32_t)(quarter * 32) << 16) + i * 128;
-    const uint32_t o_addr = s_addr - i * 128 + 256 + i * 128;
+    // Warps 4-11 tile 0, 12-19 tile 1; two warps share 32 rows, half h of the
+    // keys (and of the output's dims) each.
+    const int i = (warp - 4) >> 3, h = ((warp - 4) >> 2) & 1, quarter = warp & 3;
+    const int r = quarter * 32 + lane, qi = q0 + i * 128 + r;  // this thread's query
+    const int seen = qi < n ? m_keys - n + qi + 1 : 0;          // keys that it sees (<= 0: none)
+    const uint32_t s_addr = tmem + ((uint32_t)(quarter * 32) << 16) + i * 128, o_addr = s_addr + 256 + h * 64;
     const int nt = i == 0 ? tiles[0] : tiles[1];
+    auto row_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + i * 4 + quarter) : "memory"); };
     float m = kLow, l = 0.f;
     for (int j = 0; j < nt; ++j) {
-      if (!(ok = wait(bars, &bars->sfull[i], j & 1))) break;
-      tc_fence_after();
-      const int left = seen - j * kBN;  // visible keys of this tile
-      const bool cut = __any_sync(0xffffffffu, left < kBN);
-      auto load = [&](int c, uint32_t (&x)[32]) {
-        tmem_ld32(s_addr + c * 32, x);
+      if (ok) ok = wait(bars, &bars->sfull[i], j & 1);
+      uint32_t x[2][32];
+      if (ok) {
+        tc_fence_after();
+        tmem_ld32(s_addr + h * 64, x[0]);
+        tmem_ld32(s_addr + h * 64 + 32, x[1]);
         tmem_wait_ld();
-        if (cut) {
+      } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e >= left) x[e] = 0xff800000u;  // -inf
-        }
-      };
+        for (int e = 0; e < 64; ++e) x[e >> 5][e & 31] = 0;
+      }
+      const int left = seen - j * kBN - h * 64;  // visible keys among this thread's 64
+      if (__any_sync(0xffffffffu, left < 64)) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e >= left) x[e >> 5][e & 31] = 0xff800000u;  // -inf
+      }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32];
-        load(c, x);
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-      }
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
+      for (int e = 0; e < 32; ++e)
+        mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(x[e >> 4][(2 * e) & 31]), __uint_as_float(x[e >> 4][(2 * e + 1) & 31]));
+      mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      bars->xmax[h][i * 128 + r] = mx[0];
+      row_sync();  // also: both halves of S have been read, P may lie over them
+      const float mt = fmaxf(mx[0], bars->xmax[1 - h][i * 128 + r]) * scale_log2;
       const bool need = mt > m + kTau;
       if (__any_sync(0xffffffffu, need)) {
         const float a = need ? ex2(m - mt) : 1.f;
@@ -271,11 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mt;
           l *= a;
         }
-        if (j > 0) {
-          if (!(ok = wait(bars, &bars->pv[i], (j - 1) & 1))) break;
+        if (j > 0 && ok && (ok = wait(bars, &bars->pv[i], (j - 1) & 1))) {
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < kD; c += 16) {
+          for (int c = 0; c < 64; c += 16) {
             uint32_t o[16];
             tmem_ld16(o_addr + c, o);
             tmem_wait_ld();
@@ -285,37 +298,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // P = 2^(x scale - m) rounded to bf16 for the product, the row sum
-      // takes it unrounded; P's columns lie over S's that have been read
+      // P = 2^(x scale - m) rounded to bf16 for the product (2^-8 of each
+      // weight), the row sum takes it unrounded
       const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m, -m);
       float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32], pk[16];
-        load(c, x);
+      for (int c = 0; c < 2; ++c) {
+        uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float2 v = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc, nm);
+          float2 v = fma2(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc, nm);
           v = make_float2(ex2(v.x), ex2(v.y));
           acc[e & 1] = add2(acc[e & 1], v);
           pk[e] = pack_bf16(v.x, v.y);
         }
-        tmem_st16(s_addr + c * 16, pk);
+        if (ok) tmem_st16(s_addr + h * 32 + c * 16, pk);
       }
       const float2 sum = add2(acc[0], acc[1]);
       l += sum.x + sum.y;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->p[i]);
+      if (ok) {
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p[i]);
+      }
     }
+    row_sync();
+    bars->xmax[h][i * 128 + r] = l;
+    row_sync();
+    l = bars->xmax[0][i * 128 + r] + bars->xmax[1][i * 128 + r];
     if (ok && nt > 0) ok = wait(bars, &bars->pv[i], (nt - 1) & 1);
     if (ok) {
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;  // a query that sees nothing: zeros
-      uint4 *o = reinterpret_cast<uint4 *>(out + ((int64_t)(q_first + qi) * hq + head) * kD);
+      uint4 *o = reinterpret_cast<uint4 *>(out + ((int64_t)(q_first + qi) * hq + head) * kD + h * 64);
 #pragma unroll 1
-      for (int c = 0; c < kD / 32; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t v[32];
         if (nt > 0) {
           tmem_ld32(o_addr + c * 32, v);
