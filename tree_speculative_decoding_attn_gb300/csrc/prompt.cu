@@ -39,7 +39,7 @@ constexpr float kLow = -3.0e38f;  // running maximum before the first key
 constexpr float kTau = 16.f;      // the maximum moves when a tile exceeds it by more than 2^kTau
 
 struct Bars {
-  uint64_t q[kTiles], kfull[2], kempty[2], vfull, vempty, vclear, sfull[kTiles], p[kTiles], pv[kTiles], drain[kTiles];
+  uint64_t q[kTiles], kfull[2], kempty[2], vfull, vempty, vclear, sfull[kTiles], p[kTiles], pv[kTiles], turn[kTiles], drain[kTiles];
   uint32_t tmem;
   volatile int abort;
   // by half of the keys and row (one buffer: S(j + 1) comes after both halves' P(j))
@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->sfull[i], 1);
       mbar_init(&bars->p[i], 8);
       mbar_init(&bars->pv[i], 1);
+      mbar_init(&bars->turn[i], 1);
       mbar_init(&bars->drain[i], 1);
     }
     mbar_init(&bars->vfull, 1);
@@ -201,6 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nt > 0) ok = wait(bars, &bars->q[i], 0);
     for (int j = 0; ok && j < all; ++j) {
       if (!(ok = wait(bars, &bars->kfull[j & 1], (j >> 1) & 1))) break;
+      // S in turns: issued side by side, both tiles' products and then both
+      // their softmaxes would run at the same time
+      if (i == 1 ? !(ok = wait(bars, &bars->turn[0], j & 1)) : j > 0 && !(ok = wait(bars, &bars->turn[1], (j - 1) & 1))) break;
       if (j < nt) {
         // P(j - 1), where S goes, has been read
         if (j > 0 && !(ok = wait(bars, &bars->pv[i], (j - 1) & 1))) break;
@@ -214,10 +218,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit(&bars->sfull[i]);
           mma_commit(&bars->kempty[j & 1]);
+          mbar_arrive(&bars->turn[i]);
         }
         __syncwarp();
       } else if (elect_one()) {
         mbar_arrive(&bars->kempty[j & 1]);
+        mbar_arrive(&bars->turn[i]);
       }
       if (!(ok = wait(bars, &bars->vfull, j & 1))) break;
       if (j < nt) {
