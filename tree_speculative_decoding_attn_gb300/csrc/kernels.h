@@ -183,7 +183,7 @@ int sv_pages_compact(void *k, void *v, int vec_per_row, int n_layers, int hkv, i
                      cudaStream_t stream);
 
 // Tree attention over a cache of latent rows (latent_tc.cu: bf16, SM pairs;
-// latent_simt.cu: float32).  A row is latent_dim + 64 elements.
+// latent_few.cu: bf16, few rows; latent_simt.cu: float32).  A row is latent_dim + 64 elements.
 struct SvLatentShape {
   int dtype, batch, n_nodes, hq, latent_dim, s_max, max_prefix;
   // paged cache (block_table null: contiguous [batch, s_max, row])
@@ -194,6 +194,9 @@ size_t sv_latent_simt_ws_bytes(const SvLatentShape &s);
 int sv_latent_simt(const SvLatentShape &s, const void *q, const void *cache, const void *tree,
                    const int32_t *prefix_len, const uint64_t *anc, void *out, float scale, void *ws, int32_t *status,
                    cudaStream_t stream);
+size_t sv_latent_few_ws_bytes(const SvLatentShape &s);
+int sv_latent_few(const SvLatentShape &s, const void *q, const void *cache, const void *tree, const int32_t *prefix_len,
+                  const uint64_t *anc, void *out, float scale, void *ws, int32_t *status, cudaStream_t stream);
 size_t sv_latent_tc_ws_bytes(const SvLatentShape &s);
 int sv_latent_tc(const SvLatentShape &s, const void *q, const void *cache, const void *tree, const int32_t *prefix_len,
                  const uint64_t *anc, void *out, float scale, void *ws, int32_t *status, cudaStream_t stream);

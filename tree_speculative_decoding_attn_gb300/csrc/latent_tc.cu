@@ -43,6 +43,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "latent_work.cuh"
 #include "tc_ptx.cuh"
 
 namespace {
@@ -53,7 +54,7 @@ constexpr int kBN = 128, kRope = 64, kThreads = 384, kPairs = 76;
 constexpr uint32_t kPiece = 64 * 128;  // 64 rows (or keys) x 64 elements, 128-byte swizzle
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr int kSegW = 3;          // a unit's fixed cost, in tiles
-constexpr float kLow = -3.0e38f;  // running maximum before the first key
+using sv::kLow;
 constexpr float kTau = 16.f;      // the maximum moves when a tile exceeds it by more than 2^kTau
 
 template <int LAT> struct Cfg {
@@ -73,8 +74,7 @@ template <int LAT> struct Bars {
   // (full, p, ofree: the even CTA's count for both)
   uint64_t kfull[C::NB * 2], kread[C::NB * 2], vfull[C::NB * 2], empty[C::NB * 2], rfull[C::NR], rempty[C::NR];
   uint64_t qfull, qempty, sfull[2], sread[2], p[2], pv[2], ofree, vland, drain[2];
-  long long lo, hi, b0;
-  int b;
+  sv::LatentRange range;
   uint32_t tmem;
   volatile int abort;
   float xmax[2][2][128];
@@ -88,9 +88,6 @@ static_assert(smem_bytes<512>() <= 232448 && smem_bytes<256>() <= 232448, "share
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // Q, K both K-major
 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 256, 0, 1);  // V is MN-major (dims contiguous)
 constexpr uint32_t kColS = 256;
-
-// A partial slot: 128 rows of LAT float32 sums, then 128 (maximum, sum) pairs.
-__host__ __device__ constexpr size_t slot_floats(int lat) { return 128 * (size_t)lat + 256; }
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -157,59 +154,10 @@ template <class B> __device__ __forceinline__ bool wait_tested(bool done, B *bar
   return __all_sync(0xffffffffu, done) || wait(bars, bar, parity);
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t *>(&v);
-}
+using sv::pack_bf16;
 
-struct Work {
-  const int32_t *prefix_len;
-  int batch, N, hq, s_max, max_prefix, RT, tree_tiles;
-  __device__ int prefix(int b) const { return __ldg(prefix_len + b); }
-  __device__ bool fits(int P) const { return P >= 0 && P <= max_prefix && P <= s_max; }
-  // tiles of a unit of sequence b (0: its prefix length is refused)
-  __device__ int tiles(int b) const {
-    const int P = prefix(b);
-    return fits(P) ? tree_tiles + (P + kBN - 1) / kBN : 0;
-  }
-};
-// The segments of a pair's range in order: tiles [t0, t1) of T of a unit.
-struct Walk {
-  long long pos, end, b0;
-  int b, rt, t0, t1, T, P;
-  __device__ bool next(const Work &w) {
-    while (pos < end && b < w.batch) {
-      T = w.tiles(b);
-      P = w.prefix(b);
-      const int wu = T + kSegW;
-      rt = (int)((pos - b0) / wu);
-      const long long u0 = b0 + (long long)rt * wu, u1 = u0 + wu, stop = end < u1 ? end : u1;
-      t0 = (int)max(0ll, pos - u0 - kSegW);
-      t1 = T ? (int)max(0ll, stop - u0 - kSegW) : 0;
-      pos = stop;
-      if (stop == u1 && rt == w.RT - 1) {
-        ++b;
-        b0 = u1;
-        if (t1 > t0) {
-          --b;         // the caller reads this unit's sequence; step over it on the next call
-          step = true;
-          return true;
-        }
-        continue;
-      }
-      if (t1 > t0) return true;
-    }
-    return false;
-  }
-  bool step;
-  __device__ bool advance(const Work &w) {
-    if (step) {
-      step = false;
-      ++b;
-    }
-    return next(w);
-  }
-};
+using Work = sv::LatentWork<kBN, 128>;
+using Walk = sv::LatentWalk<Work>;
 
 template <int LAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -262,67 +210,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc_pair(&bars->tmem, 512);
   if (warp == 0) {
-    // this pair's range of the whole work, and the sequence that it starts in
-    long long total = 0;
-    for (int s = 0; s < w.batch; s += 32) {
-      const int b = s + lane;
-      const int T = b < w.batch ? w.tiles(b) : 0;
-      if (b < w.batch && !w.fits(w.prefix(b)) && blockIdx.x == 0) sv::report(status, SPEC_DEV_CAPACITY);
-      total += b < w.batch ? (long long)w.RT * (T + kSegW) : 0;
-    }
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    // (no more ranges than weight: each that begins inside a unit has a tile)
-    const long long n = total < pairs ? total : pairs;
-    const long long lo = pair < n ? total * pair / n : total, hi = pair < n ? total * (pair + 1) / n : total;
-    if (pair >= n && lane == 0) {
-      bars->lo = bars->hi = bars->b0 = 0;
-      bars->b = 0;
-      if (rank == 0) desc[pair] = make_int4(0, 0, 0, 0);
-    }
-    long long base = 0;
-    for (int s = 0; s < w.batch; s += 32) {
-      const int b = s + lane;
-      const int T = b < w.batch ? w.tiles(b) : 0;
-      const long long mine = b < w.batch ? (long long)w.RT * (T + kSegW) : 0;
-      long long up = mine;
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, up, o);
-        if (lane >= o) up += v;
-      }
-      const long long first = base + up - mine;
-      if (b < w.batch && first <= lo && lo < first + mine) {
-        bars->lo = lo;
-        bars->hi = hi;
-        bars->b0 = first;
-        bars->b = b;
-        if (rank == 0) {
-          // the first range end inside a cut unit names the unit and its parts
-          int4 d = make_int4(0, 0, 0, 0);
-          const int wu = T + kSegW;
-          const int rt = (int)((lo - first) / wu);
-          const long long t_start = first + (long long)rt * wu + kSegW;  // where the unit's first tile weighs
-          if (T > 0 && lo > t_start && total * (pair - 1) / n <= t_start) {
-            int e = pair;
-            while (e + 1 < n && total * (e + 1) / n < t_start + T) ++e;
-            d = make_int4(b, rt, e - pair + 2, 1);
-          }
-          desc[pair] = d;
-        }
-      }
-      base += __shfl_sync(0xffffffffu, up, 31);
-    }
+    const sv::LatentRange range = sv::latent_range(w, pair, pairs, kSegW, rank == 0 ? desc + pair : nullptr,
+                                                   blockIdx.x == 0 ? status : nullptr);
+    if (lane == 0) bars->range = range;
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
-  Walk walk;
-  walk.pos = bars->lo;
-  walk.end = bars->hi;
-  walk.b0 = bars->b0;
-  walk.b = bars->b;
-  walk.step = false;
+  Walk walk(bars->range, kSegW);
   bool ok = true;
 
   // The cache row of prefix key `key` (its 64 keys lie in one block; a bad
@@ -643,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool whole = walk.t0 == 0 && walk.t1 == walk.T;
         const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;  // a row that sees nothing: zeros
         __nv_bfloat16 *o = out + ((int64_t)walk.b * R + row) * LAT + half * 128;
-        float *slot = ws + (size_t)(2 * pair + (walk.t0 > 0 ? 0 : 1)) * slot_floats(LAT);
+        float *slot = ws + (size_t)(2 * pair + (walk.t0 > 0 ? 0 : 1)) * sv::latent_slot_floats(LAT, 128);
         const int lr = (int)rank * 64 + r;
 #pragma unroll 1
         for (int c = h * (LAT / 4); c < (h + 1) * (LAT / 4); c += 32) {
@@ -692,97 +589,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of a unit cut between pairs: block (row, range end), a
-// thread four (LAT 256: two) of the dims.
-template <int LAT>
-__global__ void __launch_bounds__(128)
-    latent_join_kernel(const float *__restrict__ ws, const int4 *__restrict__ desc, __nv_bfloat16 *__restrict__ out,
-                       int R) {
-  constexpr int V = LAT / 128;
-  __shared__ float s_a[kPairs];
-  grid_dep_wait();
-  const int pair = blockIdx.y + 1, lr = blockIdx.x;
-  const int4 d = desc[pair];
-  const int row = d.y * 128 + lr;
-  if (d.w == 0 || row >= R) return;
-  // the first part ends its pair's range (slot 1), the others begin theirs (slot 0)
-  auto part = [&](int i) { return ws + (size_t)(i == 0 ? 2 * (pair - 1) + 1 : 2 * (pair - 1 + i)) * slot_floats(LAT); };
-  float m = kLow;
-  for (int p = threadIdx.x & 31; p < d.z; p += 32) m = fmaxf(m, part(p)[128 * (size_t)LAT + 2 * lr]);
-  m = sv::warp_max(m);  // (every warp for itself)
-  if (threadIdx.x < d.z) {
-    const float2 ml = *reinterpret_cast<const float2 *>(part(threadIdx.x) + 128 * (size_t)LAT + 2 * lr);
-    s_a[threadIdx.x] = exp2f(ml.x - m);
-  }
-  float l = 0.f;
-  for (int p = threadIdx.x & 31; p < d.z; p += 32) {
-    const float2 ml = *reinterpret_cast<const float2 *>(part(p) + 128 * (size_t)LAT + 2 * lr);
-    l = fmaf(exp2f(ml.x - m), ml.y, l);
-  }
-  l = sv::warp_sum(l);
-  __syncthreads();
-  float acc[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
-#pragma unroll 8
-  for (int p = 0; p < d.z; ++p) {
-    const float *s = part(p) + (size_t)lr * LAT + threadIdx.x * V;
-    float x[V];
-    if constexpr (V == 4) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(s);
-    else *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(s);
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = fmaf(s_a[p], x[v], acc[v]);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t *o = reinterpret_cast<uint32_t *>(out + ((int64_t)d.x * R + row) * LAT + threadIdx.x * V);
-#pragma unroll
-  for (int v = 0; v < V / 2; ++v) o[v] = pack_bf16(acc[2 * v] * inv, acc[2 * v + 1] * inv);
-}
-
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                        cudaSuccess && q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
-  }();
-  return fn;
-}
-
-// Rows of `groups` 64-element column groups in boxes of 64 rows x `boxes`
-// groups, which lie in shared memory group by group (a box of 128 rows of 128
-// bytes: 53 bytes a cycle and SM, measured, against 44 of two boxes of 64;
-// 256: 58).  A dim of size 0 is left out.
-struct MapDim {
-  long long size, stride;  // (bytes)
-  int box;
-};
-int make_map(CUtensorMap *m, const void *base, const MapDim (&d)[5]) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return SPEC_ERR_CUDA;
-  cuuint64_t dims[5], strides[4];
-  cuuint32_t box[5], es[5] = {1, 1, 1, 1, 1}, rank = 0;
-  for (const MapDim &x : d) {
-    if (x.size == 0) continue;
-    dims[rank] = (cuuint64_t)x.size;
-    box[rank] = (cuuint32_t)x.box;
-    if (rank > 0) strides[rank - 1] = (cuuint64_t)x.stride;
-    ++rank;
-  }
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? SPEC_OK
-             : SPEC_ERR_CUDA;
-}
+using sv::MapDim;
 
 // Pairs to run: two tiles (at max_prefix) each or more.  5000 keys of one
 // token: 41 pairs 21.8 us, 21: 18.9, 14: 19.4, 11: 18.8 (parts to join).
@@ -803,15 +613,15 @@ int launch(const SvLatentShape &s, const void *q, const void *cache, const void 
   CUtensorMap mq, mc, mr, mtc, mtr;
   const MapDim in{64, 0, 64}, all{C::D, 0, 64}, none{0, 0, 0};
   // (the coordinates: element, row, column group; of a place the groups of a block, blocks)
-  if (make_map(&mq, q, {in, {R, row, 64}, {groups, 128, C::QG}, {s.batch, row * R, 1}, none}) != SPEC_OK ||
-      make_map(&mc, cache, {in, {rows, row, 64}, {4, 128, 2}, {C::VJ, 512, C::VJ}, none}) != SPEC_OK ||
-      make_map(&mr, cache, {all, {rows, row, 64}, none, none, none}) != SPEC_OK ||
-      make_map(&mtc, tree, {in, {N, row, 64}, {4, 128, 2}, {C::VJ, 512, C::VJ}, {s.batch, row * N, 1}}) != SPEC_OK ||
-      make_map(&mtr, tree, {all, {N, row, 64}, {s.batch, row * N, 1}, none, none}) != SPEC_OK)
+  if (sv::make_map(&mq, q, {in, {R, row, 64}, {groups, 128, C::QG}, {s.batch, row * R, 1}, none}) != SPEC_OK ||
+      sv::make_map(&mc, cache, {in, {rows, row, 64}, {4, 128, 2}, {C::VJ, 512, C::VJ}, none}) != SPEC_OK ||
+      sv::make_map(&mr, cache, {all, {rows, row, 64}, none, none, none}) != SPEC_OK ||
+      sv::make_map(&mtc, tree, {in, {N, row, 64}, {4, 128, 2}, {C::VJ, 512, C::VJ}, {s.batch, row * N, 1}}) != SPEC_OK ||
+      sv::make_map(&mtr, tree, {all, {N, row, 64}, {s.batch, row * N, 1}, none, none}) != SPEC_OK)
     return SPEC_ERR_CUDA;
   int4 *desc = static_cast<int4 *>(ws);
-  float *slots = reinterpret_cast<float *>(static_cast<char *>(ws) + kPairs * sizeof(int4));
-  const Work w{prefix_len, s.batch, s.n_nodes, s.hq, s.s_max, s.max_prefix, (R + 127) / 128, (s.n_nodes + kBN - 1) / kBN};
+  float *slots = reinterpret_cast<float *>(desc + kPairs);
+  const Work w(prefix_len, s.batch, s.n_nodes, s.hq, s.s_max, s.max_prefix);
   if (cudaFuncSetAttribute(latent_tc_kernel<LAT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)smem_bytes<LAT>()) != cudaSuccess)
     return SPEC_ERR_CUDA;
@@ -820,25 +630,13 @@ int launch(const SvLatentShape &s, const void *q, const void *cache, const void 
       sv::KvPages{s.block_table, s.block_size, s.max_blocks, s.num_blocks});
   if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
   if (pairs == 1) return SPEC_OK;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(R < 128 ? R : 128, pairs - 1);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, latent_join_kernel<LAT>, (const float *)slots, (const int4 *)desc,
-                            (__nv_bfloat16 *)out, R) == cudaSuccess
-             ? SPEC_OK
-             : SPEC_ERR_CUDA;
+  return sv::launch_latent_join<LAT, 128>(slots, desc, (__nv_bfloat16 *)out, R, pairs, (long long)s.batch * w.RT, stream);
 }
 
 }  // namespace
 
 size_t sv_latent_tc_ws_bytes(const SvLatentShape &s) {
-  return kPairs * sizeof(int4) + 2 * (size_t)pairs_of(s) * slot_floats(s.latent_dim) * sizeof(float);
+  return kPairs * sizeof(int4) + 2 * (size_t)pairs_of(s) * sv::latent_slot_floats(s.latent_dim, 128) * sizeof(float);
 }
 
 int sv_latent_tc(const SvLatentShape &s, const void *q, const void *cache, const void *tree, const int32_t *prefix_len,

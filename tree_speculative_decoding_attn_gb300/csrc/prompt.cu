@@ -25,6 +25,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "latent_work.cuh"
 #include "tc_ptx.cuh"
 
 namespace {
@@ -35,7 +36,7 @@ constexpr int kBN = 128, kD = 128, kRope = 64, kThreads = 640, kTiles = 2;
 constexpr uint32_t kPiece = 128 * 128;  // 128 rows x 64 elements, 128-byte swizzle
 constexpr uint32_t kQBytes = 3 * kPiece, kKBytes = 3 * kPiece, kVBytes = 2 * kPiece;
 constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr float kLow = -3.0e38f;  // running maximum before the first key
+using sv::kLow;
 constexpr float kTau = 16.f;      // the maximum moves when a tile exceeds it by more than 2^kTau
 
 struct Bars {
@@ -68,10 +69,7 @@ __device__ __forceinline__ bool wait(Bars *bars, uint64_t *bar, uint32_t parity)
   if (!ok) bars->abort = 1;
   return ok;
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t *>(&v);
-}
+using sv::pack_bf16;
 
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -371,39 +369,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                        cudaSuccess && q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
-  }();
-  return fn;
-}
-
-// [tokens, heads, dims] with element strides, in boxes of 128 tokens x 64 dims
-// of one head; heads 0: [tokens, dims].
-int make_map(CUtensorMap *m, const void *base, int dims, int heads, int tokens, int64_t head, int64_t token) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return SPEC_ERR_CUDA;
-  const cuuint32_t es[3] = {1, 1, 1};
-  const cuuint64_t size3[3] = {(cuuint64_t)dims, (cuuint64_t)heads, (cuuint64_t)tokens},
-                   size2[2] = {(cuuint64_t)dims, (cuuint64_t)tokens};
-  const cuuint64_t stride3[2] = {(cuuint64_t)head * 2, (cuuint64_t)token * 2}, stride2[1] = {(cuuint64_t)token * 2};
-  const cuuint32_t box3[3] = {64, 1, 128}, box2[2] = {64, 128};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, heads ? 3 : 2, const_cast<void *>(base), heads ? size3 : size2,
-             heads ? stride3 : stride2, heads ? box3 : box2, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? SPEC_OK
-             : SPEC_ERR_CUDA;
-}
-
 }  // namespace
 
 int sv_prompt_attn(const SvPromptShape &s, const void *q, const void *k, const void *k_rope, const void *v,
@@ -412,10 +377,13 @@ int sv_prompt_attn(const SvPromptShape &s, const void *q, const void *k, const v
   const int longest = s.max_q < s.total_q ? s.max_q : s.total_q;
   if (longest == 0) return SPEC_OK;
   CUtensorMap mq, mk, mr, mv;
-  if (make_map(&mq, q, kD + kRope, s.hq, s.total_q, kD + kRope, (int64_t)s.hq * (kD + kRope)) != SPEC_OK ||
-      make_map(&mk, k, kD, s.hq, s.total_kv, s.k_head, s.k_token) != SPEC_OK ||
-      make_map(&mr, k_rope, kRope, 0, s.total_kv, 0, s.rope_token) != SPEC_OK ||
-      make_map(&mv, v, kD, s.hq, s.total_kv, s.v_head, s.v_token) != SPEC_OK)
+  const sv::MapDim q_dims{kD + kRope, 0, 64}, dims{kD, 0, 64}, rope{kRope, 0, 64}, none{0, 0, 0};
+  const long long q_head = (kD + kRope) * 2;
+  // (the coordinates: element, head, token)
+  if (sv::make_map(&mq, q, {q_dims, {s.hq, q_head, 1}, {s.total_q, s.hq * q_head, 128}, none, none}) != SPEC_OK ||
+      sv::make_map(&mk, k, {dims, {s.hq, s.k_head * 2, 1}, {s.total_kv, s.k_token * 2, 128}, none, none}) != SPEC_OK ||
+      sv::make_map(&mr, k_rope, {rope, {s.total_kv, s.rope_token * 2, 128}, none, none, none}) != SPEC_OK ||
+      sv::make_map(&mv, v, {dims, {s.hq, s.v_head * 2, 1}, {s.total_kv, s.v_token * 2, 128}, none, none}) != SPEC_OK)
     return SPEC_ERR_CUDA;
   if (cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess)
     return SPEC_ERR_CUDA;

@@ -9,6 +9,7 @@
 // as a launch and three dependent loads.
 #include "common.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 namespace {
 
@@ -21,6 +22,7 @@ __global__ void __launch_bounds__(kThreads)
                  int32_t *status) {
   __shared__ int s_off[kMaxBatch + 1];
   __shared__ long long s_warp[kThreads / 32];
+  sv::ptx::grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // lengths of this thread's requests, summed in 64 bits
   const int per = (batch + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
@@ -81,43 +83,71 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Rows [T, hkv, dim] to (WRITE) or from their places in a pool [num_blocks,
-// hkv, block_size, dim], a 16-byte vector a thread, kVecs of them in flight.
-constexpr int kVecs = 4;
+// hkv, block_size, dim].  A CTA takes a run of rows, about 32 KB: their places
+// are looked up once, into shared memory, and then every thread has kVecs
+// 16-byte vectors in flight.  HBM-bound for long runs.  Launched as a
+// programmatic dependent, since it mostly follows slots_kernel.
+constexpr int kVecs = 4, kRun = 256;
 template <bool WRITE>
 __global__ void __launch_bounds__(kThreads)
-    rows_kernel(uint4 *__restrict__ pages, uint4 *__restrict__ rows, const int32_t *__restrict__ slots, int T, int hkv,
-                int block_size, int num_blocks, int vec, int32_t *status) {
-  const int64_t total = (int64_t)T * hkv * vec, step = (int64_t)gridDim.x * kThreads;
-  const int per = hkv * vec;
-  const int limit = num_blocks * block_size;
-  for (int64_t e0 = blockIdx.x * kThreads + threadIdx.x; e0 < total; e0 += kVecs * step) {
+    rows_kernel(uint4 *__restrict__ pages, uint4 *__restrict__ rows, const int32_t *__restrict__ slots, int n_rows,
+                int hkv, int block_size, int num_blocks, int vec, int run, int32_t *status) {
+  __shared__ int64_t s_at[kRun];  // first vector of a row's place, -1: none
+  sv::ptx::grid_dep_wait();
+  const int row0 = blockIdx.x * run, n = min(run, n_rows - row0);
+  if (threadIdx.x < n) {
+    const int row = row0 + threadIdx.x, t = row / hkv, h = row - t * hkv;
+    const int slot = slots[t], blk = slot / block_size;
+    int64_t at = -1;
+    if (slot >= num_blocks * block_size) sv::report(status, SPEC_DEV_BAD_BLOCK);
+    else if (slot >= 0) at = (((int64_t)blk * hkv + h) * block_size + (slot - blk * block_size)) * vec;
+    s_at[threadIdx.x] = at;
+  }
+  __syncthreads();
+  uint4 *mine = rows + (int64_t)row0 * vec;
+  const int total = n * vec;
+  for (int e0 = threadIdx.x; e0 < total; e0 += kVecs * kThreads) {
     uint4 v[kVecs];
-    int64_t at[kVecs];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int64_t e = e0 + i * step;
-      at[i] = -1;
+      const int e = e0 + i * kThreads, r = e / vec;
       v[i] = make_uint4(0, 0, 0, 0);
       if (e >= total) continue;
-      const int t = (int)(e / per), r = (int)(e - (int64_t)t * per), h = r / vec, c = r - h * vec;
-      const int slot = __ldg(slots + t);
-      if (slot >= limit) sv::report(status, SPEC_DEV_BAD_BLOCK);
-      if (slot >= 0 && slot < limit) {
-        const int blk = slot / block_size;
-        at[i] = (((int64_t)blk * hkv + h) * block_size + (slot - blk * block_size)) * vec + c;
-        v[i] = WRITE ? sv::ldg_stream(rows + e) : pages[at[i]];
-      }
+      const int64_t at = s_at[r];
+      if (WRITE) v[i] = __ldcs(mine + e);
+      else if (at >= 0) v[i] = __ldcs(pages + at + (e - r * vec));
     }
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int64_t e = e0 + i * step;
-      if (WRITE) {
-        if (at[i] >= 0) pages[at[i]] = v[i];
-      } else if (e < total) {
-        rows[e] = v[i];
-      }
+      const int e = e0 + i * kThreads, r = e / vec;
+      if (e >= total) continue;
+      const int64_t at = s_at[r];
+      if (!WRITE) mine[e] = v[i];
+      else if (at >= 0) pages[at + (e - r * vec)] = v[i];
     }
   }
+}
+
+template <bool WRITE>
+int launch_rows(void *pages, void *rows, const int32_t *slots, int n_rows, int hkv, int block_size, int num_blocks,
+                int vec, int32_t *status, cudaStream_t stream) {
+  // (few rows: spread over the SMs rather than in long runs)
+  int run = kVecs * kThreads / vec, spread = (n_rows + 303) / 304;
+  run = run > spread ? spread : run;
+  run = run < 1 ? 1 : run > kRun ? kRun : run;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((n_rows + run - 1) / run);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rows_kernel<WRITE>, (uint4 *)pages, (uint4 *)rows, slots, n_rows, hkv, block_size,
+                            num_blocks, vec, run, status) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
 }
 
 }  // namespace
@@ -125,21 +155,14 @@ __global__ void __launch_bounds__(kThreads)
 int sv_pages_slots(const int32_t *table, const int32_t *prefix_len, const int32_t *new_len, int batch, int max_blocks,
                    int block_size, int num_blocks, int room, int32_t *offsets, int32_t *slots, int32_t *positions,
                    int32_t *status, cudaStream_t stream) {
-  const int ctas = (room + 4 * kThreads - 1) / (4 * kThreads);
-  slots_kernel<<<ctas < 1 ? 1 : ctas < 608 ? ctas : 608, kThreads, 0, stream>>>(
+  const int ctas = (room + kThreads - 1) / kThreads;
+  slots_kernel<<<ctas < 608 ? ctas : 608, kThreads, 0, stream>>>(
       table, prefix_len, new_len, batch, max_blocks, block_size, num_blocks, room, offsets, slots, positions, status);
   return sv_launch_status();
 }
 
 int sv_slots_rows(bool write, void *pages, void *rows, const int32_t *slots, int T, int hkv, int block_size,
                   int num_blocks, int vec, int32_t *status, cudaStream_t stream) {
-  const int64_t n = ((int64_t)T * hkv * vec + kThreads * kVecs - 1) / (kThreads * kVecs);
-  const unsigned ctas = (unsigned)(n < 152 * 8 ? n : 152 * 8);
-  if (write)
-    rows_kernel<true><<<ctas, kThreads, 0, stream>>>((uint4 *)pages, (uint4 *)rows, slots, T, hkv, block_size, num_blocks,
-                                                     vec, status);
-  else
-    rows_kernel<false><<<ctas, kThreads, 0, stream>>>((uint4 *)pages, (uint4 *)rows, slots, T, hkv, block_size,
-                                                      num_blocks, vec, status);
-  return sv_launch_status();
+  return (write ? launch_rows<true> : launch_rows<false>)(pages, rows, slots, T * hkv, hkv, block_size, num_blocks, vec,
+                                                          status, stream);
 }

@@ -658,8 +658,11 @@ static int latent_check(const SvLatentShape &s, int rope_dim) {
     return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
 }
+static const int kFewLatentRows = 16;
 static size_t latent_ws_bytes(const SvLatentShape &s) {
-  return s.dtype == SPEC_BF16 ? sv_latent_tc_ws_bytes(s) : sv_latent_simt_ws_bytes(s);
+  return s.dtype != SPEC_BF16                   ? sv_latent_simt_ws_bytes(s)
+         : s.n_nodes * s.hq <= kFewLatentRows ? sv_latent_few_ws_bytes(s)
+                                              : sv_latent_tc_ws_bytes(s);
 }
 
 size_t tree_attn_latent_workspace_bytes(int dtype, int batch, int n_nodes, int hq, int latent_dim, int rope_dim,
@@ -680,8 +683,10 @@ static int latent_run(const SvLatentShape &s, int rope_dim, const void *q, const
   if (s.max_prefix > s.s_max) return SPEC_ERR_CAPACITY;
   const size_t need = latent_ws_bytes(s);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return SPEC_ERR_CAPACITY;
-  return (s.dtype == SPEC_BF16 ? sv_latent_tc : sv_latent_simt)(s, q, cache, tree, prefix_len, anc_mask, out, scale,
-                                                                workspace, dev_status, cs(stream));
+  const auto run = s.dtype != SPEC_BF16                   ? sv_latent_simt
+                   : s.n_nodes * s.hq <= kFewLatentRows ? sv_latent_few
+                                                        : sv_latent_tc;
+  return run(s, q, cache, tree, prefix_len, anc_mask, out, scale, workspace, dev_status, cs(stream));
 }
 
 int tree_attn_verify_latent(const void *q, const void *cache, const void *tree, const int32_t *prefix_len,
