@@ -108,41 +108,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   Walk walk(rest->range, kSegW);
 
-  // Thread 0 loads ahead: its own walk over the tiles.  A tile's row is looked
-  // up when the tile before it is issued, so that nothing waits for the table.
+  // Thread 0 loads ahead: its own walk over the tiles.  A tile's block is looked
+  // up when the tile before it is issued, so that nothing waits for the table,
+  // and divisions are left to a segment's start (they are 300 cycles of the
+  // path from one barrier to the next).
   Walk far(rest->range, kSegW);
-  bool far_more = threadIdx.x == 0 && far.advance(w);
-  int far_t = far.t0, far_g = 0, far_blk = 0;
-  auto look_up = [&]() {
-    if (pg.table && far_more && far_t >= w.tree_tiles)
-      far_blk = __ldg(pg.table + (int64_t)far.b * pg.max_blocks + (far_t - w.tree_tiles) * kBN / pg.block_size);
+  bool far_more = false;
+  int far_t = 0, far_g = 0, far_blk = 0, far_row = 0;  // block, and row in it (contiguous: in the cache)
+  const int32_t *far_table = pg.table;
+  auto far_segment = [&]() {
+    far_more = far.advance(w);
+    far_t = far.t0;
+    const int key = max(0, far_t - w.tree_tiles) * kBN;
+    far_row = far.b * w.s_max + key;
+    if (pg.table && far_more) {
+      far_table = pg.table + (int64_t)far.b * pg.max_blocks + key / pg.block_size;
+      far_row = key % pg.block_size;
+      if (far_t >= w.tree_tiles) far_blk = __ldg(far_table);
+    }
   };
-  look_up();
+  if (threadIdx.x == 0) far_segment();
   auto load_next = [&]() {  // (thread 0)
     if (!far_more) return;
     uint64_t *bar = &rest->full[far_g % C::ST];
     uint8_t *dst = smem + far_g % C::ST * C::tile;
     mbar_expect_tx(bar, C::tile);
-    const int key = (far_t - w.tree_tiles) * kBN;
-    if (key < 0) {
+    if (far_t < w.tree_tiles) {
       tma_load_4d(dst, &tm_t, 0, far_t * kBN, 0, far.b, bar);
     } else {
-      int row = far.b * w.s_max + key;
+      int row = far_row;
       if (pg.table) {
-        row = far_blk * pg.block_size + key % pg.block_size;
+        row += far_blk * pg.block_size;
         if (far_blk < 0 || far_blk >= pg.num_blocks) {
           sv::report(status, SPEC_DEV_BAD_BLOCK);
           row = row_end;  // past the pool: zeros
         }
       }
       tma_load_3d(dst, &tm_c, 0, row, 0, bar);
+      far_row += kBN;
     }
     ++far_g;
     if (++far_t >= far.t1) {
-      far_more = far.advance(w);
-      far_t = far.t0;
+      far_segment();
+    } else if (pg.table && far_t >= w.tree_tiles) {
+      if (far_row >= pg.block_size) {
+        far_row = 0;
+        ++far_table;
+      }
+      far_blk = __ldg(far_table);
     }
-    look_up();
   };
 
   const int r0 = lane >> 2, c2 = (lane & 3) * 2;  // fragment row (and + 8), first of two columns

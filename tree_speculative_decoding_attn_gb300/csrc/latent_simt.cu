@@ -3,9 +3,9 @@
 // Row (node, head) has a query q in the latent space, a key is a cache or
 // tree row c = [latent ; rotary], a value its latent part:
 //   out = sum_j softmax_j(scale q . c_j) c_j[:LAT].
-// One CTA takes 8 rows and a range of the keys, 64 at a time.  Scores: a
-// warp holds one key row in registers (lanes over its dims) and multiplies it
-// with the 8 queries in shared memory.  Softmax: one warp a row, running
+// One CTA takes 8 rows and a range of the keys, 32 at a time.  Scores: a
+// warp holds four key rows in registers (lanes over their dims) and multiplies
+// them with the 8 queries in shared memory.  Softmax: one warp a row, running
 // maximum and sum.  Values: a thread owns one or two of the latent dims for
 // all 8 rows.  Key ranges are joined by a second kernel.  What bounds it is
 // the float32 FMA rate (every key row is read once per 8 rows, from L1 the
@@ -17,7 +17,7 @@
 
 namespace {
 
-constexpr int kRows = 8, kKeys = 64, kThreads = 256, kRope = 64;
+constexpr int kRows = 8, kKeys = 32, kThreads = 256, kRope = 64;
 constexpr float kLow = -3.0e38f;  // running maximum before the first key
 constexpr int kMaxSplits = 64;
 
@@ -66,18 +66,27 @@ __global__ void __launch_bounds__(kThreads)
       if (j0 + j >= P) return tree + ((int64_t)b * N + (j0 + j - P)) * D;
       return s_row[j] < 0 ? nullptr : cache + (int64_t)s_row[j] * D;
     };
-    for (int j = warp; j < n; j += kThreads / 32) {
-      const float *c = key_row(j);
-      float k[PER], dot[kRows];
+    constexpr int KW = kKeys / (kThreads / 32);  // keys of a warp: warp, warp + 8, ..
+    float k[KW][PER], dot[KW][kRows];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) k[i] = c ? c[lane + 32 * i] : 0.f;
+    for (int j = 0; j < KW; ++j) {
+      const float *c = warp + 8 * j < n ? key_row(warp + 8 * j) : nullptr;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        float s = 0.f;
+      for (int i = 0; i < PER; ++i) k[j][i] = c ? c[lane + 32 * i] : 0.f;
+    }
 #pragma unroll
-        for (int i = 0; i < PER; ++i) s = fmaf(k[i], s_q[r][lane + 32 * i], s);
-        dot[r] = s;
+    for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+      for (int j = 0; j < KW; ++j) dot[j][r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float x = s_q[r][lane + 32 * i];
+#pragma unroll
+        for (int j = 0; j < KW; ++j) dot[j][r] = fmaf(k[j][i], x, dot[j][r]);
       }
+    }
+#pragma unroll
+    for (int j = 0; j < KW; ++j) {
       // eight sums over 32 lanes, one left in each group of four lanes
 #pragma unroll
       for (int step = 0; step < 3; ++step) {
@@ -85,31 +94,30 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int r = 0; r < half; ++r) {
           const bool up = lane & o;
-          const float give = up ? dot[r] : dot[r + half];
-          dot[r] = (up ? dot[r + half] : dot[r]) + __shfl_xor_sync(0xffffffffu, give, o);
+          const float give = up ? dot[j][r] : dot[j][r + half];
+          dot[j][r] = (up ? dot[j][r + half] : dot[j][r]) + __shfl_xor_sync(0xffffffffu, give, o);
         }
       }
-      dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 2);
-      dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 1);
-      const int r = lane >> 2;
-      if ((lane & 3) == 0) {
+      dot[j][0] += __shfl_xor_sync(0xffffffffu, dot[j][0], 2);
+      dot[j][0] += __shfl_xor_sync(0xffffffffu, dot[j][0], 1);
+      const int r = lane >> 2, key = warp + 8 * j;
+      if ((lane & 3) == 0 && key < n) {
         bool see = row0 + r < R;
-        if (see && j0 + j >= P) {
-          const int t = j0 + j - P, node = (row0 + r) / hq;
+        if (see && j0 + key >= P) {
+          const int t = j0 + key - P, node = (row0 + r) / hq;
           see = (anc[((int64_t)b * N + node) * words + (t >> 6)] >> (t & 63)) & 1ull;
         }
-        s_p[r][j] = see ? dot[0] * scale_log2 : -INFINITY;
+        s_p[r][key] = see ? dot[j][0] * scale_log2 : -INFINITY;
       }
     }
     __syncthreads();
     {
-      const float x0 = lane < n ? s_p[warp][lane] : -INFINITY, x1 = lane + 32 < n ? s_p[warp][lane + 32] : -INFINITY;
-      const float mt = fmaxf(sv::warp_max(fmaxf(x0, x1)), m);
-      const float p0 = exp2f(x0 - mt), p1 = exp2f(x1 - mt), a = exp2f(m - mt);
-      l = l * a + sv::warp_sum(p0 + p1);
+      const float x = lane < n ? s_p[warp][lane] : -INFINITY;
+      const float mt = fmaxf(sv::warp_max(x), m);
+      const float p = exp2f(x - mt), a = exp2f(m - mt);
+      l = l * a + sv::warp_sum(p);
       m = mt;
-      s_p[warp][lane] = p0;
-      s_p[warp][lane + 32] = p1;
+      s_p[warp][lane] = p;
       if (lane == 0) s_alpha[warp] = a;
     }
     __syncthreads();
@@ -117,7 +125,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int r = 0; r < kRows; ++r)
 #pragma unroll
       for (int v = 0; v < VD; ++v) acc[r][v] *= s_alpha[r];
-#pragma unroll 4
+#pragma unroll 8
     for (int j = 0; j < n; ++j) {
       const float *c = key_row(j);
 #pragma unroll

@@ -145,116 +145,164 @@ template <class Work> struct LatentWalk {
 // for one cut at its end alone.
 __host__ __device__ constexpr size_t latent_slot_floats(int lat, int rows) { return rows * (size_t)(lat + 2); }
 
-// Joins the parts of cut units: block (row, cut unit, dims).  The 128 threads
-// are GROUPS groups, each with its share of the parts, a thread four dims of
-// 512 / GROUPS; all groups' sums go through shared memory.  Many parts (one
-// long sequence) take more groups and blocks of fewer dims.
-template <int LAT, int ROWS, int GROUPS>
+constexpr int kMostParts = 160;
+// The k-th cut unit of those that there are, by its first range end (0: fewer
+// than k + 1).  One warp.
+__device__ __forceinline__ int latent_cut(const int4 *desc, int parts, int k) {
+  const int lane = threadIdx.x & 31;
+  int seen = 0;
+  for (int p = 1; p < parts; p += 32) {
+    const unsigned cut = __ballot_sync(0xffffffffu, p + lane < parts && desc[p + lane].w != 0);
+    if (k < seen + __popc(cut)) return p + __fns(cut, 0, k - seen + 1);
+    seen += __popc(cut);
+  }
+  return 0;
+}
+// What the n parts of a row weigh (into a[]), and the sum of all their sums.
+// One warp.
+template <class Stats>
+__device__ __forceinline__ float latent_weights(int n, float *a, const Stats &stats) {
+  const int lane = threadIdx.x & 31;
+  float2 ml[kMostParts / 32];
+  float m = kLow, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMostParts / 32; ++i) {
+    ml[i] = i * 32 + lane < n ? stats(i * 32 + lane) : make_float2(kLow, 0.f);
+    m = fmaxf(m, ml[i].x);
+  }
+  m = warp_max(m);
+#pragma unroll
+  for (int i = 0; i < kMostParts / 32; ++i) {
+    const float w = exp2f(ml[i].x - m);
+    if (i * 32 + lane < n) a[i * 32 + lane] = w;
+    l = fmaf(w, ml[i].y, l);
+  }
+  return warp_sum(l);
+}
+__device__ __forceinline__ void fma4(float4 &acc, float a, const float4 &x) {
+  acc.x = fmaf(a, x.x, acc.x);
+  acc.y = fmaf(a, x.y, acc.y);
+  acc.z = fmaf(a, x.z, acc.z);
+  acc.w = fmaf(a, x.w, acc.w);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v, float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: zeros
+  *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+}
+
+// Joins the parts of cut units, a thread four dims of a row.
+// FORM 0, many rows: block (8 rows, cut unit), the weights of all its rows
+// first, then four rows (LAT 256: eight) at a time, two parts of each in flight.
+// FORM 1 and 8, fewer: block (row, cut unit, LAT / FORM dims), eight parts in
+// flight, shared out over groups of threads whose sums go through shared memory.
+template <int LAT, int ROWS, int FORM>
 __global__ void __launch_bounds__(128)
     latent_join_kernel(const float *__restrict__ ws, const int4 *__restrict__ desc, int parts,
                        __nv_bfloat16 *__restrict__ out, int R) {
-  constexpr int MOST = 160, PER = 128 / GROUPS, B = 8;  // parts; threads a group; loads in flight
-  __shared__ float s_a[MOST], s_l;
-  __shared__ float4 s_acc[GROUPS][PER];
+  constexpr int RB = FORM ? 1 : 8, SIDE = 512 / LAT;  // rows of a block; rows side by side
+  constexpr int DIMS = FORM ? LAT / FORM : LAT, PER = DIMS / 4, GROUPS = 128 / PER;
+  __shared__ float s_a[RB][kMostParts], s_l[RB];
   __shared__ int s_part;
-  const int lane = threadIdx.x & 31, lr = blockIdx.x;
-  if (threadIdx.x == 0) s_part = 0;
+  const int warp = threadIdx.x >> 5;
   ptx::grid_dep_wait();
-  __syncthreads();
-  // the cut unit blockIdx.y of those that there are, by its first range end
-  if (threadIdx.x < 32) {
-    int seen = 0;
-    for (int p = 1; p < parts; p += 32) {
-      const unsigned cut = __ballot_sync(0xffffffffu, p + lane < parts && desc[p + lane].w != 0);
-      const int mine = seen + __popc(cut & ((1u << lane) - 1));
-      if ((cut >> lane & 1) && mine == (int)blockIdx.y) s_part = p + lane;
-      seen += __popc(cut);
-    }
+  if (warp == 0) {
+    // (as many blocks as range ends: each looks at its own)
+    const int p = (int)gridDim.y < parts - 1            ? latent_cut(desc, parts, blockIdx.y)
+                  : desc[blockIdx.y + 1].w != 0 ? (int)blockIdx.y + 1
+                                                : 0;
+    if (threadIdx.x == 0) s_part = p;
   }
   __syncthreads();
   const int part0 = s_part;
   if (part0 == 0) return;
   const int4 d = desc[part0];
-  const int row = d.y * ROWS + lr;
-  if (row >= R) return;
+  const int lr0 = blockIdx.x * RB, rows = min(min(RB, ROWS - lr0), R - d.y * ROWS - lr0);
+  if (rows <= 0) return;
   // the first part ends its range (slot 1), the others begin theirs (slot 0)
   auto part = [&](int i) {
     return ws + (size_t)(i == 0 ? 2 * (part0 - 1) + 1 : 2 * (part0 - 1 + i)) * latent_slot_floats(LAT, ROWS);
   };
-  if (threadIdx.x < 32) {
-    float2 ml[MOST / 32];
-    float m = kLow, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < MOST / 32; ++i) {
-      const int p = i * 32 + lane;
-      ml[i] = p < d.z ? *reinterpret_cast<const float2 *>(part(p) + ROWS * (size_t)LAT + 2 * lr) : make_float2(kLow, 0.f);
-      m = fmaxf(m, ml[i].x);
-    }
-    m = warp_max(m);
-#pragma unroll
-    for (int i = 0; i < MOST / 32; ++i) {
-      const float a = exp2f(ml[i].x - m);
-      s_a[i * 32 + lane] = a;
-      l = fmaf(a, ml[i].y, l);
-    }
-    l = warp_sum(l);
-    if (lane == 0) s_l = l;
+  for (int r = warp; r < rows; r += 4) {
+    const float l = latent_weights(d.z, s_a[r], [&](int p) {
+      return *reinterpret_cast<const float2 *>(part(p) + ROWS * (size_t)LAT + 2 * (lr0 + r));
+    });
+    if ((threadIdx.x & 31) == 0) s_l[r] = l;
   }
-  const int group = threadIdx.x / PER, at = threadIdx.x % PER, dim = blockIdx.z * (PER * 4) + at * 4;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  bool first = true;
-  for (int p0 = group; p0 < d.z || first; p0 += B * GROUPS) {
-    float4 x[B];
+  __syncthreads();
+  __nv_bfloat16 *o = out + ((int64_t)d.x * R + d.y * ROWS + lr0) * LAT;
+  const int group = threadIdx.x / PER, at = threadIdx.x % PER;
+  auto load = [&](int p, int r, int dim) {
+    return __ldcs(reinterpret_cast<const float4 *>(part(p) + (size_t)(lr0 + r) * LAT + dim));
+  };
+  if constexpr (FORM > 0) {
+    constexpr int B = 8;  // loads in flight
+    __shared__ float4 s_acc[GROUPS][PER];
+    const int dim = blockIdx.z * DIMS + at * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = group; p0 < d.z; p0 += B * GROUPS) {
+      float4 x[B];
 #pragma unroll
-    for (int i = 0; i < B; ++i)
-      x[i] = __ldcs(reinterpret_cast<const float4 *>(part(min(p0 + i * GROUPS, d.z - 1)) + (size_t)lr * LAT + dim));
-    if (first) __syncthreads();  // the weights, behind the first loads
-    first = false;
+      for (int i = 0; i < B; ++i)
+        if (p0 + i * GROUPS < d.z) x[i] = load(p0 + i * GROUPS, 0, dim);
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
-      if (p0 + i * GROUPS >= d.z) continue;
-      const float a = s_a[p0 + i * GROUPS];
-      acc.x = fmaf(a, x[i].x, acc.x);
-      acc.y = fmaf(a, x[i].y, acc.y);
-      acc.z = fmaf(a, x[i].z, acc.z);
-      acc.w = fmaf(a, x[i].w, acc.w);
+      for (int i = 0; i < B; ++i)
+        if (p0 + i * GROUPS < d.z) fma4(acc, s_a[0][p0 + i * GROUPS], x[i]);
+    }
+    if (GROUPS > 1) {
+      s_acc[group][at] = acc;
+      __syncthreads();
+      if (group > 0) return;
+#pragma unroll
+      for (int i = 1; i < GROUPS; ++i) fma4(acc, 1.f, s_acc[i][at]);
+    }
+    store4(o + dim, acc, s_l[0]);
+  } else {
+    constexpr int B = 4;  // rows in flight
+    for (int r0 = group; r0 < rows; r0 += B * SIDE) {
+      float4 acc[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p = 0; p < d.z; p += 2) {
+        float4 x[2][B];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < B; ++i)
+            if (p + h < d.z && r0 + i * SIDE < rows) x[h][i] = load(p + h, r0 + i * SIDE, at * 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < B; ++i)
+            if (p + h < d.z && r0 + i * SIDE < rows) fma4(acc[i], s_a[r0 + i * SIDE][p + h], x[h][i]);
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i)
+        if (r0 + i * SIDE < rows) store4(o + (size_t)(r0 + i * SIDE) * LAT + at * 4, acc[i], s_l[r0 + i * SIDE]);
     }
   }
-  if (GROUPS > 1) {
-    s_acc[group][at] = acc;
-    __syncthreads();
-    if (group > 0) return;
-#pragma unroll
-    for (int i = 1; i < GROUPS; ++i) {
-      const float4 o = s_acc[i][at];
-      acc.x += o.x;
-      acc.y += o.y;
-      acc.z += o.z;
-      acc.w += o.w;
-    }
-  }
-  const float inv = s_l == 0.f ? 0.f : 1.f / s_l;  // a row that sees nothing: zeros
-  *reinterpret_cast<uint2 *>(out + ((int64_t)d.x * R + row) * LAT + dim) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 template <int LAT, int ROWS>
 int launch_latent_join(const float *slots, const int4 *desc, __nv_bfloat16 *out, int R, int parts, long long units,
                        cudaStream_t stream) {
   if (parts == 1) return SPEC_OK;
-  constexpr int FEW = 512 / LAT, MANY = 4 * FEW;
-  const bool many = parts > 4 * units;
+  const int rows = R < ROWS ? R : ROWS, cut = units < parts - 1 ? (int)units : parts - 1;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(R < ROWS ? R : ROWS, units < parts - 1 ? (unsigned)units : parts - 1, many ? 4 : 1);
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = many ? cudaLaunchKernelEx(&cfg, latent_join_kernel<LAT, ROWS, MANY>, slots, desc, parts, out, R)
-                             : cudaLaunchKernelEx(&cfg, latent_join_kernel<LAT, ROWS, FEW>, slots, desc, parts, out, R);
-  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  // (us of the whole call, FORM 8 / 1 / 0: 16 rows of 80 parts 12.2 / 15.4 / -,
+  // 16 units of 128 rows 154 / 130 / 144, 75 units of 128 rows - / 133 / 131)
+  auto run = [&](auto kernel, dim3 grid) {
+    cfg.gridDim = grid;
+    return cudaLaunchKernelEx(&cfg, kernel, slots, desc, parts, out, R) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  };
+  if (rows * cut <= 256) return run(latent_join_kernel<LAT, ROWS, 8>, dim3(rows, cut, 8));
+  if (rows * cut <= 8192) return run(latent_join_kernel<LAT, ROWS, 1>, dim3(rows, cut));
+  return run(latent_join_kernel<LAT, ROWS, 0>, dim3((rows + 7) / 8, cut));
 }
 
 // ---------------------------------------------------------------- tensor maps

@@ -658,6 +658,9 @@ static int latent_check(const SvLatentShape &s, int rope_dim) {
     return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
 }
+// bf16 rows a sequence for the kernel of few rows, whose tile they fill.  us
+// there / on SM pairs (latent 512): 16 rows, 5000 keys 12.2 / 15.6, batch 64
+// over 4096 keys 60 / 71; 32 rows 15.3 / 17.1 and 103 / 75.
 static const int kFewLatentRows = 16;
 static size_t latent_ws_bytes(const SvLatentShape &s) {
   return s.dtype != SPEC_BF16                   ? sv_latent_simt_ws_bytes(s)
