@@ -246,8 +246,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_tr);
     }
     int g = 0;
-    for (int seg = 0; ok && walk.advance(w); ++seg) {
-      if (!(ok = wait(bars, &bars->qempty, (seg & 1) ^ 1))) break;
+    // Q of a segment: behind its first K, which need not wait for the last
+    // segment's S (the first segment's Q first)
+    auto load_q = [&](int seg) -> bool {
+      if (!wait(bars, &bars->qempty, (seg & 1) ^ 1)) return false;
       if (me) {
         if (rank == 0) mbar_expect_tx(&bars->qfull, 2 * C::q_bytes);
         const uint32_t bar = mapa_cluster(&bars->qfull, 0);
@@ -255,6 +257,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           load_4d(sQ + i * kPiece, &tm_q, 0, walk.rt * 128 + (int)rank * 64, i, walk.b, bar);
       }
       __syncwarp();
+      return true;
+    };
+    for (int seg = 0; ok && walk.advance(w); ++seg) {
+      if (seg == 0 && !(ok = load_q(seg))) break;
       for (int t = walk.t0; ok && t < walk.t1; ++t, ++g) {
         const bool tree = t < w.tree_tiles;
         const int row = tree ? t * kBN + (int)rank * 64 : cache_row(walk.b, (t - w.tree_tiles) * kBN + (int)rank * 64);
@@ -276,6 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
+        if (ok && t == walk.t0 && seg > 0) ok = load_q(seg);
       }
     }
   } else if (warp == 2) {
