@@ -524,12 +524,20 @@ int tree_attn_verify_latent_paged(const void *q, const void *pages, const int32_
  * a sequence have to be finite from its first key on, also those that a query
  * does not see (they are multiplied by a weight of 0); rows of other
  * sequences may hold anything.  Rounding as tree_attn_verify_latent.
+ *   workspace  device scratch of prompt_attn_latent_workspace_bytes() bytes
+ *            (16-byte aligned, uninitialised; may be NULL when that size is 0,
+ *            which it is unless the units of (sequence, head, 256 queries) are
+ *            too few for the GPU; calls that may overlap on the GPU need
+ *            separate ones)
  * ------------------------------------------------------------------ */
+size_t prompt_attn_latent_workspace_bytes(int batch, int hq, int head_dim, int rope_dim, int total_q,
+                                          int total_kv, int max_q);
 int prompt_attn_latent(const void *q, const void *k, int64_t k_token, int64_t k_head,
                        const void *k_rope, int64_t rope_token, const void *v, int64_t v_token,
                        int64_t v_head, const int32_t *q_offsets, const int32_t *kv_offsets, void *out,
                        int batch, int hq, int head_dim, int rope_dim, int total_q, int total_kv,
-                       int max_q, float scale, int32_t *dev_status, spec_stream_t stream);
+                       int max_q, float scale, void *workspace, size_t workspace_bytes,
+                       int32_t *dev_status, spec_stream_t stream);
 
 /* --------------------------------------------------------------------
  * tree_attn_verify_noalloc -- tree_attn_verify without a caller workspace.

@@ -207,8 +207,9 @@ struct SvPromptShape {
   int batch, hq, total_q, total_kv, max_q;
   int64_t k_token, k_head, v_token, v_head, rope_token;
 };
+size_t sv_prompt_ws_bytes(const SvPromptShape &s);
 int sv_prompt_attn(const SvPromptShape &s, const void *q, const void *k, const void *k_rope, const void *v,
-                   const int32_t *q_offsets, const int32_t *kv_offsets, void *out, float scale, int32_t *status,
+                   const int32_t *q_offsets, const int32_t *kv_offsets, void *out, float scale, void *ws, int32_t *status,
                    cudaStream_t stream);
 
 // Packed tokens' rows of a paged cache (slots.cu).  vec = dim * elem_bytes / 16.

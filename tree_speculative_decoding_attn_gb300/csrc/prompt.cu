@@ -19,7 +19,9 @@
 //   warps 4-7   softmax and output of tile 0, a thread a row; 8-11 tile 1.
 //               S is read twice from TMEM: once for the maximum, once for P
 // TMEM columns: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512).
-// Longest tiles are launched first.  Every wait is bounded.
+// Longest tiles are launched first.  Where CTAs are fewer than SMs (a chunk of
+// few heads behind a long kept beginning) the keys are cut into parts, a CTA
+// each, whose float32 partials a second kernel joins.  Every wait is bounded.
 #include <cuda.h>
 #include <math.h>
 
@@ -32,7 +34,7 @@ namespace {
 
 using namespace sv::ptx;
 
-constexpr int kBN = 128, kD = 128, kRope = 64, kThreads = 640, kTiles = 2;
+constexpr int kBN = 128, kD = 128, kRope = 64, kThreads = 640, kTiles = 2, kSms = 152;
 constexpr uint32_t kPiece = 128 * 128;  // 128 rows x 64 elements, 128-byte swizzle
 constexpr uint32_t kQBytes = 3 * kPiece, kKBytes = 3 * kPiece, kVBytes = 2 * kPiece;
 constexpr uint32_t kWaitLimit = 1u << 22;
@@ -71,12 +73,18 @@ __device__ __forceinline__ bool wait(Bars *bars, uint64_t *bar, uint32_t parity)
 }
 using sv::pack_bf16;
 
+// A partial: 256 rows of 128 float32 sums, then 256 pairs (maximum in log2
+// units, sum).
+__host__ __device__ constexpr size_t slot_floats() { return 256 * (size_t)(kD + 2); }
+
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v,
                   const int32_t *__restrict__ q_off, const int32_t *__restrict__ kv_off, __nv_bfloat16 *__restrict__ out,
-                  int hq, int total_q, int total_kv, int max_q, float scale_log2, int32_t *status) {
-  const int head = blockIdx.x, b = blockIdx.y;
+                  float *__restrict__ ws, int hq, int parts, int total_q, int total_kv, int max_q, float scale_log2,
+                  int32_t *status) {
+  const int head = blockIdx.x / parts, part = blockIdx.x - head * parts, b = blockIdx.y;
+  if (parts > 1) grid_dep_launch();
   const int q_first = q_off[b], q_end = q_off[b + 1], k_first = kv_off[b], k_end = kv_off[b + 1];
   if (q_first < 0 || k_first < 0 || q_end < q_first || k_end < k_first || q_end > total_q || k_end > total_kv ||
       q_end - q_first > max_q) {
@@ -96,7 +104,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars *bars = reinterpret_cast<Bars *>(sV + kVBytes);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-  // key tiles of each query tile: up to its last query's position
+  // key tiles of each query tile: up to its last query's position; of them
+  // this part's, from tile j0 on
   int tiles[kTiles], all = 0;
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
@@ -105,6 +114,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tiles[i] = seen > 0 ? (seen + kBN - 1) / kBN : 0;
     all = max(all, tiles[i]);
   }
+  const int j0 = (int)((int64_t)all * part / parts);
+  all = (int)((int64_t)all * (part + 1) / parts) - j0;
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) tiles[i] = max(0, min(tiles[i] - j0, all));
+  const int keys_left = m_keys - j0 * kBN;  // from tile j0 on
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -141,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int k_done = 0, v_done = 0;
     for (int j = 0; ok && j < all; ++j) {
-      const int row = k_first + j * kBN;
+      const int row = k_first + (j0 + j) * kBN;
       if (!(ok = wait(bars, &bars->kempty[j & 1], ((j >> 1) & 1) ^ 1))) break;
       if (me) {
         uint64_t *bar = &bars->kfull[j & 1];
@@ -173,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && all > 0 && (ok = wait(bars, &bars->vfull, (all - 1) & 1))) {
       // what follows the sequence's last key belongs to others: cleared
-      const int keys = m_keys - (all - 1) * kBN;
+      const int keys = keys_left - (all - 1) * kBN;
       if (keys < kBN) {
         for (int e = lane; e < (kBN - keys) * 16; e += 32)
           *reinterpret_cast<uint4 *>(sV + (e & 8 ? kPiece : 0) + (keys + (e >> 4)) * 128 + (e & 7) * 16) =
@@ -225,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!(ok = wait(bars, &bars->vfull, j & 1))) break;
       if (j < nt) {
-        if (m_keys - j * kBN < kBN && !(ok = wait(bars, &bars->vclear, 0))) break;
+        if (keys_left - j * kBN < kBN && !(ok = wait(bars, &bars->vclear, 0))) break;
         if (!(ok = wait(bars, &bars->p[i], j & 1))) break;
         tc_fence_after();
         if (elect_one()) {
@@ -251,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // keys (and of the output's dims) each.
     const int i = (warp - 4) >> 3, h = ((warp - 4) >> 2) & 1, quarter = warp & 3;
     const int r = quarter * 32 + lane, qi = q0 + i * 128 + r;  // this thread's query
-    const int seen = qi < n ? m_keys - n + qi + 1 : 0;          // keys that it sees (<= 0: none)
+    const int seen = qi < n ? keys_left - n + qi + 1 : 0;       // keys that it sees from tile j0 on (<= 0: none)
     const uint32_t s_addr = tmem + ((uint32_t)(quarter * 32) << 16) + i * 128, o_addr = s_addr + 256 + h * 64;
     const int nt = i == 0 ? tiles[0] : tiles[1];
     auto row_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + i * 4 + quarter) : "memory"); };
@@ -334,26 +348,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && nt > 0) ok = wait(bars, &bars->pv[i], (nt - 1) & 1);
     if (ok) {
       tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // a query that sees nothing: zeros
-      uint4 *o = reinterpret_cast<uint4 *>(out + ((int64_t)(q_first + qi) * hq + head) * kD + h * 64);
+      if (parts > 1) {
+        // a part that shows the row nothing leaves a sum of 0, and no O
+        float *slot = ws + slot_floats() * (((size_t)blockIdx.z * gridDim.y + b) * gridDim.x + blockIdx.x);
+        const int row = i * 128 + r;
+        if (h == 0 && qi < n) *reinterpret_cast<float2 *>(slot + 256 * kD + 2 * row) = make_float2(m, l);
 #pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[32];
-        if (nt > 0) {
+        for (int c = 0; nt > 0 && c < 2; ++c) {
+          uint32_t v[32];
           tmem_ld32(o_addr + c * 32, v);
           tmem_wait_ld();
-        }
-        if (qi >= n) continue;
+          if (qi >= n) continue;
+          uint4 *dst = reinterpret_cast<uint4 *>(slot + row * kD + h * 64 + c * 32);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4 u = make_uint4(0, 0, 0, 0);
+          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+      } else {
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // a query that sees nothing: zeros
+        uint4 *o = reinterpret_cast<uint4 *>(out + ((int64_t)(q_first + qi) * hq + head) * kD + h * 64);
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32];
           if (nt > 0) {
-            u.x = pack_bf16(__uint_as_float(v[8 * e]) * inv, __uint_as_float(v[8 * e + 1]) * inv);
-            u.y = pack_bf16(__uint_as_float(v[8 * e + 2]) * inv, __uint_as_float(v[8 * e + 3]) * inv);
-            u.z = pack_bf16(__uint_as_float(v[8 * e + 4]) * inv, __uint_as_float(v[8 * e + 5]) * inv);
-            u.w = pack_bf16(__uint_as_float(v[8 * e + 6]) * inv, __uint_as_float(v[8 * e + 7]) * inv);
+            tmem_ld32(o_addr + c * 32, v);
+            tmem_wait_ld();
           }
-          o[c * 4 + e] = u;
+          if (qi >= n) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (nt > 0) {
+              u.x = pack_bf16(__uint_as_float(v[8 * e]) * inv, __uint_as_float(v[8 * e + 1]) * inv);
+              u.y = pack_bf16(__uint_as_float(v[8 * e + 2]) * inv, __uint_as_float(v[8 * e + 3]) * inv);
+              u.z = pack_bf16(__uint_as_float(v[8 * e + 4]) * inv, __uint_as_float(v[8 * e + 5]) * inv);
+              u.w = pack_bf16(__uint_as_float(v[8 * e + 6]) * inv, __uint_as_float(v[8 * e + 7]) * inv);
+            }
+            o[c * 4 + e] = u;
+          }
         }
       }
     }
@@ -369,13 +400,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Joins the parts of a unit: block (8 queries, unit), a warp a query, a lane
+// four dims.
+__global__ void __launch_bounds__(256)
+    prompt_join_kernel(const float *__restrict__ ws, const int32_t *__restrict__ q_off,
+                       const int32_t *__restrict__ kv_off, __nv_bfloat16 *__restrict__ out, int hq, int parts,
+                       int total_q, int total_kv, int max_q) {
+  grid_dep_wait();
+  const int per = 256 / 8;  // blocks of a unit
+  const int unit = blockIdx.x / per, row = (blockIdx.x - unit * per) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int head = unit % hq, b = blockIdx.y;
+  const int q_first = q_off[b], q_end = q_off[b + 1], k_first = kv_off[b], k_end = kv_off[b + 1];
+  if (q_first < 0 || k_first < 0 || q_end < q_first || k_end < k_first || q_end > total_q || k_end > total_kv ||
+      q_end - q_first > max_q)
+    return;  // reported by the main kernel
+  const int z = unit / hq, qi = (int)(gridDim.x / (per * hq) - 1 - z) * kTiles * 128 + row;
+  if (qi >= q_end - q_first) return;
+  const float *slot = ws + slot_floats() * ((((size_t)z * gridDim.y + b) * hq + head) * parts);
+  float m = kLow, l = 0.f;
+  for (int p = lane; p < parts; p += 32) m = fmaxf(m, slot[p * slot_floats() + 256 * kD + 2 * row]);
+  m = sv::warp_max(m);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float2 ml = *reinterpret_cast<const float2 *>(slot + p * slot_floats() + 256 * kD + 2 * row);
+    if (ml.y == 0.f) continue;
+    const float4 x = *reinterpret_cast<const float4 *>(slot + p * slot_floats() + row * kD + lane * 4);
+    const float a = exp2f(ml.x - m);
+    l = fmaf(a, ml.y, l);
+    acc.x = fmaf(a, x.x, acc.x);
+    acc.y = fmaf(a, x.y, acc.y);
+    acc.z = fmaf(a, x.z, acc.z);
+    acc.w = fmaf(a, x.w, acc.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2 *>(out + ((int64_t)(q_first + qi) * hq + head) * kD + lane * 4) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+}
+
+int q_tiles_of(const SvPromptShape &s) {
+  const int longest = s.max_q < s.total_q ? s.max_q : s.total_q;
+  return (longest + kTiles * 128 - 1) / (kTiles * 128);
+}
+// Parts of a unit's keys: as many as fill the SMs, of four tiles at least
+// where sequences have the mean length.
+int parts_of(const SvPromptShape &s) {
+  const long long units = (long long)s.hq * s.batch * q_tiles_of(s);
+  if (units == 0 || 2 * units > kSms) return 1;
+  const long long most = s.total_kv / (4ll * kBN * s.batch), n = kSms / units;
+  return (int)(n < most ? n : most > 1 ? most : 1);
+}
+
 }  // namespace
 
+size_t sv_prompt_ws_bytes(const SvPromptShape &s) {
+  const int parts = parts_of(s);
+  return parts > 1 ? slot_floats() * sizeof(float) * parts * s.hq * s.batch * q_tiles_of(s) : 0;
+}
+
 int sv_prompt_attn(const SvPromptShape &s, const void *q, const void *k, const void *k_rope, const void *v,
-                   const int32_t *q_offsets, const int32_t *kv_offsets, void *out, float scale, int32_t *status,
+                   const int32_t *q_offsets, const int32_t *kv_offsets, void *out, float scale, void *ws, int32_t *status,
                    cudaStream_t stream) {
-  const int longest = s.max_q < s.total_q ? s.max_q : s.total_q;
-  if (longest == 0) return SPEC_OK;
+  const int q_tiles = q_tiles_of(s), parts = parts_of(s);
+  if (q_tiles == 0) return SPEC_OK;
   CUtensorMap mq, mk, mr, mv;
   const sv::MapDim q_dims{kD + kRope, 0, 64}, dims{kD, 0, 64}, rope{kRope, 0, 64}, none{0, 0, 0};
   const long long q_head = (kD + kRope) * 2;
@@ -387,8 +474,22 @@ int sv_prompt_attn(const SvPromptShape &s, const void *q, const void *k, const v
     return SPEC_ERR_CUDA;
   if (cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess)
     return SPEC_ERR_CUDA;
-  prompt_kernel<<<dim3(s.hq, s.batch, (longest + kTiles * 128 - 1) / (kTiles * 128)), kThreads, kSmemBytes, stream>>>(
-      mq, mk, mr, mv, q_offsets, kv_offsets, (__nv_bfloat16 *)out, s.hq, s.total_q, s.total_kv, s.max_q,
-      scale * 1.4426950408889634f, status);
-  return sv_launch_status();
+  prompt_kernel<<<dim3(s.hq * parts, s.batch, q_tiles), kThreads, kSmemBytes, stream>>>(
+      mq, mk, mr, mv, q_offsets, kv_offsets, (__nv_bfloat16 *)out, (float *)ws, s.hq, parts, s.total_q, s.total_kv,
+      s.max_q, scale * 1.4426950408889634f, status);
+  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  if (parts == 1) return SPEC_OK;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(s.hq * q_tiles * (256 / 8), s.batch);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_join_kernel, (const float *)ws, q_offsets, kv_offsets, (__nv_bfloat16 *)out,
+                            s.hq, parts, s.total_q, s.total_kv, s.max_q) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
 }

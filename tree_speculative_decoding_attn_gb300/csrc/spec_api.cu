@@ -762,16 +762,29 @@ int kv_slots_read(const void *pages, const int32_t *slots, void *rows, int elem_
                     num_blocks, dev_status, stream);
 }
 
-int prompt_attn_latent(const void *q, const void *k, int64_t k_token, int64_t k_head, const void *k_rope,
-                       int64_t rope_token, const void *v, int64_t v_token, int64_t v_head, const int32_t *q_offsets,
-                       const int32_t *kv_offsets, void *out, int batch, int hq, int head_dim, int rope_dim,
-                       int total_q, int total_kv, int max_q, float scale, int32_t *dev_status, spec_stream_t stream) {
-  if (!q || !k || !k_rope || !v || !q_offsets || !kv_offsets || !out) return SPEC_ERR_INVALID_ARG;
+static int prompt_check(int batch, int hq, int head_dim, int rope_dim, int total_q, int total_kv, int max_q) {
   if (batch < 1 || hq < 1 || total_q < 1 || total_kv < 1 || max_q < 0) return SPEC_ERR_INVALID_ARG;
   if (head_dim != 128 || rope_dim != 64) return SPEC_ERR_UNSUPPORTED;
   if (batch > 65535 || hq > 65535 || total_kv > (1 << 30) || (long long)total_q * hq > (1 << 30) ||
       (max_q < total_q ? max_q : total_q) > (1 << 23))
     return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+size_t prompt_attn_latent_workspace_bytes(int batch, int hq, int head_dim, int rope_dim, int total_q, int total_kv,
+                                          int max_q) {
+  if (prompt_check(batch, hq, head_dim, rope_dim, total_q, total_kv, max_q) != SPEC_OK) return 0;
+  return sv_prompt_ws_bytes(SvPromptShape{batch, hq, total_q, total_kv, max_q});
+}
+
+int prompt_attn_latent(const void *q, const void *k, int64_t k_token, int64_t k_head, const void *k_rope,
+                       int64_t rope_token, const void *v, int64_t v_token, int64_t v_head, const int32_t *q_offsets,
+                       const int32_t *kv_offsets, void *out, int batch, int hq, int head_dim, int rope_dim,
+                       int total_q, int total_kv, int max_q, float scale, void *workspace, size_t workspace_bytes,
+                       int32_t *dev_status, spec_stream_t stream) {
+  if (!q || !k || !k_rope || !v || !q_offsets || !kv_offsets || !out) return SPEC_ERR_INVALID_ARG;
+  const int rc = prompt_check(batch, hq, head_dim, rope_dim, total_q, total_kv, max_q);
+  if (rc != SPEC_OK) return rc;
   // (strides are at least what they step over, and at most what a tensor map takes)
   const struct { int64_t v; int least; } strides[] = {{k_token, 128}, {k_head, 128}, {rope_token, 64}, {v_token, 128}, {v_head, 128}};
   for (const auto &x : strides)
@@ -780,7 +793,9 @@ int prompt_attn_latent(const void *q, const void *k, int64_t k_token, int64_t k_
     return SPEC_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !isfinite(scale)) return SPEC_ERR_INVALID_ARG;
   const SvPromptShape s{batch, hq, total_q, total_kv, max_q, k_token, k_head, v_token, v_head, rope_token};
-  return sv_prompt_attn(s, q, k, k_rope, v, q_offsets, kv_offsets, out, scale, dev_status, cs(stream));
+  const size_t need = sv_prompt_ws_bytes(s);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return SPEC_ERR_CAPACITY;
+  return sv_prompt_attn(s, q, k, k_rope, v, q_offsets, kv_offsets, out, scale, workspace, dev_status, cs(stream));
 }
 
 }  // extern "C"

@@ -80,8 +80,9 @@ _SIGS = {
     "tree_attn_verify_latent": ([_vp] * 6 + [_i] * 8 + [_f, _vp, _sz, _vp, _vp], _i),
     "tree_attn_verify_latent_paged": ([_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp] + [_i] * 7 +
                                       [_f, _vp, _sz, _vp, _vp], _i),
+    "prompt_attn_latent_workspace_bytes": ([_i] * 7, _sz),
     "prompt_attn_latent": ([_vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp] + [_i] * 7 +
-                           [_f, _vp, _vp], _i),
+                           [_f, _vp, _sz, _vp, _vp], _i),
     "kv_pages_slots": ([_vp, _vp, _vp] + [_i] * 5 + [_vp] * 5, _i),
     "kv_slots_write": ([_vp, _vp, _vp] + [_i] * 6 + [_vp, _vp], _i),
     "kv_slots_read": ([_vp, _vp, _vp] + [_i] * 6 + [_vp, _vp], _i),
@@ -717,16 +718,26 @@ def _step(t, d, least):
     return t.stride(d) if t.shape[d] > 1 else least
 
 
-def prompt_attn_latent(q, k, k_rope, v, q_offsets, kv_offsets, out, max_q, scale, dev_status=None):
+def prompt_attn_latent_workspace_bytes(batch, hq, head_dim, rope_dim, total_q, total_kv, max_q):
+    return int(load().prompt_attn_latent_workspace_bytes(batch, hq, head_dim, rope_dim, total_q, total_kv, max_q))
+
+
+def prompt_attn_latent(q, k, k_rope, v, q_offsets, kv_offsets, out, max_q, scale, workspace=None, dev_status=None):
     """Causal attention of packed prompt tokens: q [Tq, Hq, 192], k and v [Tk,
     Hq, 128], k_rope [Tk, 64] (bf16; k, v and k_rope may be column ranges of
-    wider tensors), offsets [B + 1] int32, out [Tq, Hq, 128]."""
+    wider tensors), offsets [B + 1] int32, out [Tq, Hq, 128].  ``workspace``
+    (uint8, prompt_attn_latent_workspace_bytes) is allocated per call when not
+    given."""
     (Tq, Hq, _), (Tk, _, D) = q.shape, k.shape
     bf, i32, B = torch.bfloat16, torch.int32, q_offsets.shape[0] - 1
     i, stream = _device(q)
+    if workspace is None:
+        size = prompt_attn_latent_workspace_bytes(B, Hq, D, ROPE_DIM, Tq, Tk, int(max_q))
+        workspace = _scratch(size, q) if size else None
+    ws = (None, 0) if workspace is None else (_sized(workspace, i, torch.uint8), workspace.numel())
     _check("prompt_attn_latent", load().prompt_attn_latent(
         _ptr(q, i, bf, (Tq, Hq, D + ROPE_DIM)), _strided(k, i, bf, (Tk, Hq, D)), _step(k, 0, Hq * D), _step(k, 1, D),
         _strided(k_rope, i, bf, (Tk, ROPE_DIM)), _step(k_rope, 0, ROPE_DIM), _strided(v, i, bf, (Tk, Hq, D)),
         _step(v, 0, Hq * D), _step(v, 1, D),
         _ptr(q_offsets, i, i32, (B + 1,)), _ptr(kv_offsets, i, i32, (B + 1,)), _ptr(out, i, bf, (Tq, Hq, D)), B, Hq, D,
-        ROPE_DIM, Tq, Tk, int(max_q), float(scale), _word(dev_status, i), stream))
+        ROPE_DIM, Tq, Tk, int(max_q), float(scale), *ws, _word(dev_status, i), stream))
