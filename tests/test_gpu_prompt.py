@@ -94,3 +94,103 @@ def test_matches_float64(lib, H, new, total):
 def test_layouts_of_keys_and_values(lib, layout):
     c = make(5, 3, [140, 1, 33], [200, 77, 33], layout=layout)
     check(c, *call(c))
+
+
+def test_few_units_are_cut_into_parts(lib):
+    """One head and few queries behind many keys: keys in parts, some of which
+    show some queries nothing."""
+    for new, total, H in (([5], [9000], 1), ([300], [5000], 3), ([256, 1], [700, 6000], 2), ([2000], [2000], 1),
+                          ([400], [390], 1), ([3, 0], [4000, 4000], 2)):
+        assert sv.prompt_attn_latent_workspace_bytes(len(new), H, 128, 64, sum(new), sum(total), max(new)) > 0 \
+            or sum(total) < 1024
+        c = make(len(new) + H, H, new, total, spare=70)
+        check(c, *call(c))
+
+
+def test_scores_that_jump(lib):
+    for H, n in ((2, 700), (40, 300)):
+        c = make(4, H, [n], [n])
+        step = torch.arange(n) // 64
+        step = torch.where(step < 6, step, 11 - step).float()
+        c["q"][..., 128] = 16.0
+        c["rope"][:, 0] = (step * 8).to(BF)
+        check(c, *call(c))
+
+
+def test_not_a_number_and_what_is_not_read(lib):
+    """A NaN query makes its row NaN alone; another sequence's rows may be NaN."""
+    c = make(5, 2, [200, 40, 60], [260, 40, 90])
+    c["q"][17, 1, 150] = float("nan")
+    out, _ = call(c)
+    bad = out.isnan().any(-1).cpu()
+    assert int(bad.sum()) == 1 and bool(bad[17, 1])
+    c = make(5, 2, [200, 40, 60], [260, 40, 90])
+    for x in ("k", "v", "rope"):
+        c[x][260:300] = float("nan")
+    c["q"][200:240] = float("nan")
+    out, st = call(c)
+    assert bool(out[200:240].isnan().all()) and not out[:200].isnan().any() and not out[240:].isnan().any()
+
+
+def test_refused_offsets_leave_their_rows(lib):
+    for H in (2, 30):
+        c = make(6, H, [100, 50, 30], [200, 60, 30])
+        good, _ = call(c)
+        for q_off, kv_off, bad in (([0, 100, 90, 180], [0, 200, 260, 290], (1,)), ([0, 100, 150, 9999], [0, 200, 260, 290], (2,)),
+                                   ([0, 100, 150, 180], [0, 200, 260, 291], (2,)), ([-5, 100, 150, 180], [0, 200, 260, 290], (0,)),
+                                   ([0, 100, 150, 180], [0, 200, 100, 290], (1, 2)),
+                                   ([0, 100, 150, 180], [0, -2 ** 31, 260, 290], (0, 1))):
+            out, st = call(dict(c, q_off=q_off, kv_off=kv_off))
+            assert int(st.item()) == sv.DEV_CAPACITY
+            for b, (lo, hi) in enumerate(((0, 100), (100, 150), (150, 180))):
+                if b not in bad and (b != 2 or q_off[2] == 150) and kv_off[b:b + 2] == c["kv_off"].tolist()[b:b + 2]:
+                    assert torch.equal(out[lo:hi], good[lo:hi])
+            if bad == (2,):
+                assert bool((out[150:] == 7.0).all())
+        out, st = call(c, max_q=60)
+        assert int(st.item()) == sv.DEV_CAPACITY and bool((out[:100] == 7.0).all()) and torch.equal(out[100:], good[100:])
+        out, st = call(c, max_q=10 ** 6)
+        assert int(st.item()) == 0 and torch.equal(out, good)
+        out, st = call(c, max_q=0)
+        assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("H,new,total", [(2, [300, 40], [2000, 90]), (40, [300, 40], [700, 90])])
+def test_captured_on_another_stream_and_two_at_once(lib, H, new, total):
+    cs = [make(30 + i, H, new, total) for i in range(2)]
+    alone = [call(c)[0] for c in cs]
+    args = [(c["q"].cuda(), like(c["k"]), like(c["rope"]), like(c["v"]), i32(c["q_off"]), i32(c["kv_off"])) for c in cs]
+    size = sv.prompt_attn_latent_workspace_bytes(2, H, 128, 64, sum(new), sum(total), max(new))
+    ws = [torch.empty(max(16, size), dtype=torch.uint8, device="cuda") for _ in cs]
+    outs, sts = [torch.empty_like(a) for a in alone], [zeros_i32(1) for _ in cs]
+    graphs, streams = [], [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for a, w, o, t in zip(args, ws, outs, sts):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sv.prompt_attn_latent(*a, o, max(new), SCALE, workspace=w, dev_status=t)
+        graphs.append(g)
+    for _ in range(5):
+        for o in outs:
+            o.fill_(3.0)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for a, o, t in zip(alone, outs, sts):
+            assert int(t.item()) == 0 and torch.equal(a, o)
+
+
+def test_wrapper_refuses(lib):
+    z = lambda *s, dt=BF: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    good = dict(q=z(5, 2, 192), k=z(9, 2, 128), k_rope=z(9, 64), v=z(9, 2, 128), q_offsets=i32([0, 5]), kv_offsets=i32([0, 9]),
+                out=z(5, 2, 128), max_q=5, scale=SCALE)
+    sv.prompt_attn_latent(**good)
+    sv.prompt_attn_latent(**dict(good, v=z(9, 2, 264)[:, :, 8:136]))
+    for kw in (dict(q=z(5, 2, 128)), dict(k=z(9, 3, 128)), dict(k_rope=z(8, 64)), dict(v=z(9, 2, 64)), dict(out=z(5, 2, 192)),
+               dict(kv_offsets=i32([0, 9, 9])), dict(q=z(5, 2, 192, dt=torch.float32)), dict(scale=-1.0), dict(max_q=-1),
+               dict(v=z(9, 2, 132)[:, :, 4:]), dict(v=z(9, 2, 130)[:, :, :128]), dict(k=z(9, 128, 2).transpose(1, 2)),
+               dict(k_rope=z(9, 68)[:, 4:]), dict(v=z(1, 2, 128).expand(9, 2, 128)), dict(q=good["q"].cpu())):
+        with pytest.raises((ValueError, TypeError, sv.SpecError)):
+            sv.prompt_attn_latent(**{**good, **kw})
