@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 namespace {
 
@@ -37,6 +38,7 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ int s_row[kKeys];  // cache row of a prefix key, -1 outside the pool
   const int R = N * hq, b = blockIdx.z, split = blockIdx.y, row0 = blockIdx.x * kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  sv::ptx::grid_dep_launch();
   const int P = prefix_len[b];
   if (P < 0 || P > max_prefix || P > s_max) {
     if (threadIdx.x == 0) sv::report(status, SPEC_DEV_CAPACITY);
@@ -166,6 +168,7 @@ template <int LAT>
 __global__ void __launch_bounds__(128)
     latent_simt_join_kernel(const float *__restrict__ ws, float *__restrict__ out, const int32_t *__restrict__ prefix_len,
                             int R, int splits, int s_max, int max_prefix) {
+  sv::ptx::grid_dep_wait();
   const int64_t row = blockIdx.x;
   const int P = prefix_len[row / R];
   if (P < 0 || P > max_prefix || P > s_max) return;  // reported by the main kernel
@@ -208,9 +211,19 @@ int launch(const SvLatentShape &s, const void *q, const void *cache, const void 
       sv::KvPages{s.block_table, s.block_size, s.max_blocks, s.num_blocks});
   if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
   if (splits == 1) return SPEC_OK;
-  latent_simt_join_kernel<LAT><<<s.batch * R, 128, 0, stream>>>((const float *)ws, (float *)out, prefix_len, R, splits,
-                                                               s.s_max, s.max_prefix);
-  return sv_launch_status();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(s.batch * R);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, latent_simt_join_kernel<LAT>, (const float *)ws, (float *)out, prefix_len, R, splits,
+                            s.s_max, s.max_prefix) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
 }
 
 }  // namespace
