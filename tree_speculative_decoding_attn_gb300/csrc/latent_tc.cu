@@ -31,12 +31,23 @@
 // Shared memory (LAT 512): Q 72 KB, two tiles of latents 128, rotary columns
 // 8, P 16.  TMEM: O LAT/2 columns, two S buffers of 64.
 // Roles: warp 0 loads Q and K, warp 2 V; of the even CTA warp 1 issues S and
-// warp 3 PV; warps 4-11 softmax and epilogue: a thread owns 32 keys of one row (lanes r and r + 64
-// of two warps share row r).  Two S buffers: the softmax of a tile runs under
-// the next tile's S and the last one's PV.
+// warp 3 PV; warps 4-11 softmax and epilogue: a thread owns 32 keys of one row
+// (lanes r and r + 64 of two warps share row r).  Two S buffers: the softmax of
+// a tile runs under the next tile's S and the last one's PV.
 // Work: all (sequence, 128-row tile) units, each its tree tiles and then its
 // prefix tiles of 128 keys, are cut into one equal range a pair; units cut
 // between pairs leave float32 partials that a second kernel joins.
+// What bounds it: a tile's MMAs are 2258 cycles, its shared-memory traffic
+// (operands 245 KB, TMA 104, P 16) 2850 at 128 bytes a cycle, and it takes
+// about 3000; 32 trees of 32 nodes x 64 heads over 4096 rows: 438-485 us, 1.2 to
+// 1.34 PFLOP/s, at 1370 W, where the power limit holds the clock at 1740 MHz.
+// One token of 64 heads, batch 64 over 4096 rows: 84 us, of them 52 at 6 TB/s
+// in the tiles, the rest start, epilogues and the join.
+// Tried and not kept: one warp for all MMAs (4400 cycles a tile: its waits are
+// not covered), P announced through a warp that forwards at the cluster's
+// scope (1400 cycles a hand-off, 540 us), S held back behind the last PV (490
+// to 540), tiles of 64 keys for one row tile (0-4 %, and 46 -> 63 us at LAT
+// 256), the next tiles' keys prefetched into L2 (0-15 % slower: TMA's time).
 // Every wait is bounded.
 #include <cuda.h>
 #include <math.h>
@@ -53,9 +64,9 @@ using namespace sv::ptx;
 constexpr int kBN = 128, kRope = 64, kThreads = 384, kPairs = 76;
 constexpr uint32_t kPiece = 64 * 128;  // 64 rows (or keys) x 64 elements, 128-byte swizzle
 constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr int kSegW = 3;          // a unit's fixed cost, in tiles
+constexpr int kSegW = 3;      // a unit's fixed cost, in tiles (ragged trees: 1 143 us, 2 132, 3 128, 5 129)
 using sv::kLow;
-constexpr float kTau = 16.f;      // the maximum moves when a tile exceeds it by more than 2^kTau
+constexpr float kTau = 16.f;  // the maximum moves when a tile exceeds it by more than 2^kTau
 
 template <int LAT> struct Cfg {
   static constexpr int D = LAT + kRope;

@@ -11,13 +11,19 @@
 //   S_i(j) = Q_i K(j)^T  (N = 128, K = 192; the rotary columns of K are one
 //            64-column box shared by all heads)   768 cycles
 //   O_i   += P_i(j) V(j) (N = 128 dims, K = 128; P in TMEM over S)  512 cycles
-// in the order S0 S1 PV0 PV1.  P lies where S was, so S_i(j + 1) waits for
-// PV_i(j) to be done: behind the other tile's PV, which covers the wait.
-//   warp 0      loads Q, K (two stages) and V
-//   warp 1      TMEM and all MMAs (an elected thread); clears the V rows past
-//               the sequence's last key
-//   warps 4-7   softmax and output of tile 0, a thread a row; 8-11 tile 1.
-//               S is read twice from TMEM: once for the maximum, once for P
+// P lies where S was, so S_i(j + 1) waits for PV_i(j) to be done.
+//   warp 0      loads Q, K (two stages) and V, and clears the V rows past the
+//               sequence's last key
+//   warps 1, 2  the MMAs of tile 0 and 1 (an elected thread each); their S in
+//               turns, or both tiles would multiply and then both wait
+//   warps 4-19  softmax and output, eight warps a tile: a thread half a row
+// What bounds it: two tiles' MMAs are 2560 cycles a key tile (2660 by their
+// shared-memory traffic), the chain S, softmax (1400), PV with its hand-offs
+// 3850.  8192 tokens of 32 heads 480-515 us, 1.34 to 1.43 PFLOP/s, at the power
+// limit (1365 W, 1950 MHz).  Steps: one MMA warp and eight softmax warps 4680
+// cycles, 527 us; a warp a tile 4060, 491; S in turns 3850, 483.  Without the
+// exponentials (timing only) the same: not a limit of the exponential unit.
+// Scalar instead of two-wide float32 arithmetic 508 us.
 // TMEM columns: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512).
 // Longest tiles are launched first.  Where CTAs are fewer than SMs (a chunk of
 // few heads behind a long kept beginning) the keys are cut into parts, a CTA

