@@ -10,8 +10,8 @@
 // all 8 rows.  Key ranges are joined by a second kernel.  What bounds it is
 // the float32 FMA rate (every key row is read once per 8 rows, from L1 the
 // second time); float32 caches are for exactness, not for speed.  A small call
-// is a row's chain of loads, scores and the join: a tree of 7 nodes x 4 heads
-// over a few hundred rows 12 us (18.8 with a warp's keys one after another,
+// is a row's chain of loads, scores and the join: a tree of 5 nodes x 4 heads
+// over 129 rows 12 us (18.8 with a warp's keys one after another,
 // 13.0 with the join as an ordinary launch).
 #include <math.h>
 

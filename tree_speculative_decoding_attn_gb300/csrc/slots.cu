@@ -86,9 +86,10 @@ __global__ void __launch_bounds__(kThreads)
 // Rows [T, hkv, dim] to (WRITE) or from their places in a pool [num_blocks,
 // hkv, block_size, dim].  A CTA takes a run of rows, about 32 KB: their places
 // are looked up once, into shared memory, and then every thread has kVecs
-// 16-byte vectors in flight.  HBM-bound for long runs: 29000 rows of 576
-// bf16 out of a pool 13.4 us, of them 9.7 at the copy rate, the rest the start.  Launched as a
-// programmatic dependent, since it mostly follows slots_kernel.
+// 16-byte vectors in flight.  HBM-bound for long runs: 28400 rows of 576
+// bf16 out of a pool 13.4 us, of them 9.7 at the copy rate, the rest the
+// start.  Launched as a programmatic dependent, since it mostly follows
+// slots_kernel.
 constexpr int kVecs = 4, kRun = 256;
 template <bool WRITE>
 __global__ void __launch_bounds__(kThreads)
