@@ -194,3 +194,11 @@ def test_wrapper_refuses(lib):
                dict(k_rope=z(9, 68)[:, 4:]), dict(v=z(1, 2, 128).expand(9, 2, 128)), dict(q=good["q"].cpu())):
         with pytest.raises((ValueError, TypeError, sv.SpecError)):
             sv.prompt_attn_latent(**{**good, **kw})
+
+
+def test_more_queries_than_none_are_reported(lib):
+    c = make(12, 2, [0, 40, 0], [10, 90, 0])
+    out, st = call(c, max_q=0)
+    assert int(st.item()) == sv.DEV_CAPACITY and bool((out == 7.0).all())
+    out, st = call(make(13, 2, [0, 0], [2000, 7], spare=5), max_q=0)
+    assert int(st.item()) == 0 and bool((out == 7.0).all())

@@ -446,13 +446,13 @@ __global__ void __launch_bounds__(256)
 
 int q_tiles_of(const SvPromptShape &s) {
   const int longest = s.max_q < s.total_q ? s.max_q : s.total_q;
-  return (longest + kTiles * 128 - 1) / (kTiles * 128);
+  return longest ? (longest + kTiles * 128 - 1) / (kTiles * 128) : 1;  // (none allowed: some may be there, to report)
 }
 // Parts of a unit's keys: as many as fill the SMs, of four tiles at least
 // where sequences have the mean length.
 int parts_of(const SvPromptShape &s) {
   const long long units = (long long)s.hq * s.batch * q_tiles_of(s);
-  if (units == 0 || 2 * units > kSms) return 1;
+  if (2 * units > kSms) return 1;
   const long long most = s.total_kv / (4ll * kBN * s.batch), n = kSms / units;
   return (int)(n < most ? n : most > 1 ? most : 1);
 }
@@ -468,7 +468,6 @@ int sv_prompt_attn(const SvPromptShape &s, const void *q, const void *k, const v
                    const int32_t *q_offsets, const int32_t *kv_offsets, void *out, float scale, void *ws, int32_t *status,
                    cudaStream_t stream) {
   const int q_tiles = q_tiles_of(s), parts = parts_of(s);
-  if (q_tiles == 0) return SPEC_OK;
   CUtensorMap mq, mk, mr, mv;
   const sv::MapDim q_dims{kD + kRope, 0, 64}, dims{kD, 0, 64}, rope{kRope, 0, 64}, none{0, 0, 0};
   const long long q_head = (kD + kRope) * 2;
