@@ -518,12 +518,13 @@ int tree_attn_verify_latent_paged(const void *q, const void *pages, const int32_
  * All strides are positive multiples of 8 (SPEC_ERR_INVALID_ARG), addresses
  * 16-byte aligned.  head_dim 128 and rope_dim 64 (SPEC_ERR_UNSUPPORTED
  * otherwise), hq <= 65535, batch <= 65535, total_q * hq <= 2^30, total_kv <=
- * 2^30, at most 2^23 queries a sequence.  A query before the sequence's first key (n > m) gets zeros.  Offsets
- * outside [0, total], a decreasing pair, or more than max_q queries set
- * SPEC_DEV_CAPACITY and that sequence's output is left unwritten.  Values of
- * a sequence have to be finite from its first key on, also those that a query
- * does not see (they are multiplied by a weight of 0); rows of other
- * sequences may hold anything.  Rounding as tree_attn_verify_latent.
+ * 2^30, at most 2^23 queries a sequence.  A query before the sequence's first
+ * key (n > m) gets zeros.  Offsets outside [0, total], a decreasing pair, or
+ * more than max_q queries set SPEC_DEV_CAPACITY and that sequence's output is
+ * left unwritten.  Values of a sequence have to be finite from its first key
+ * on, also those that a query does not see (they are multiplied by a weight of
+ * 0); rows of other sequences may hold anything.  Rounding as
+ * tree_attn_verify_latent.
  *   workspace  device scratch of prompt_attn_latent_workspace_bytes() bytes
  *            (16-byte aligned, uninitialised; may be NULL when that size is 0,
  *            which it is unless the units of (sequence, head, 256 queries) are
@@ -857,7 +858,8 @@ int kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table, in
  * slots of one pool [num_blocks, hkv, block_size, head_dim] (a layer's K, V or
  * latents), or out of them.  A negative slot: not written, read as zeros; a
  * slot past the pool the same (SPEC_DEV_BAD_BLOCK).  A slot that is written
- * twice in a call ends up with a mixture of its rows.
+ * twice in a call ends up with a mixture of its rows.  Rows in the pool, or an
+ * output over the slots, are refused (SPEC_ERR_INVALID_ARG).
  *
  * k_pages, v_pages [n_layers, num_blocks, hkv, block_size, head_dim] (16-byte
  * aligned, elem_bytes 2 or 4, head_dim * elem_bytes % 16 == 0; v_pages NULL: a

@@ -114,3 +114,16 @@ def test_one_pool_wants_no_second_tree(lib):
     assert commit(vc=P) == INV and commit(vt=P) == INV and commit(kt=NULL) == INV and commit() == INV   # (no prefix_len)
     paged = lambda v=NULL, vt=NULL, table=NULL: lib.kv_commit_paged(P, v, table, 128, 8, 4, P, vt, 2, 1, 2, 1, 16, 576, P, P, 8, P, NULL, NULL, NULL)  # noqa: E731
     assert paged(v=P, table=P) == INV and paged(vt=P, table=P) == INV and paged() == INV
+
+
+def test_slots_refuse_rows_in_the_pool(lib):
+    pool, rows, lst = 16 * 16 * 576 * 2, 5 * 576 * 2, 20
+    base = 1 << 34
+    for name, slots_at in (("kv_slots_write", ((base, INV), (base + pool - 4, INV))),
+                           ("kv_slots_read", ((FAR, INV), (FAR + rows - 4, INV)))):
+        def call(r=FAR, s=base - 4096, pages=base):
+            return getattr(lib, name)(pages, s, r, 2, 5, 1, 576, 16, 16, NULL, NULL)
+        for r in (base, base + pool - 16, base - rows + 16):
+            assert call(r=r, s=FAR) == INV
+        for s, code in slots_at:
+            assert call(s=s) == code

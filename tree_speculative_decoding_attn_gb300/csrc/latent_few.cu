@@ -123,8 +123,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     far_more = far.advance(w);
     far_t = far.t0;
     const int key = max(0, far_t - w.tree_tiles) * kBN;
-    far_row = far.b * w.s_max + key;
-    if (pg.table && far_more) {
+    if (!pg.table) {
+      far_row = far.b * w.s_max + key;
+    } else if (far_more) {
       far_table = pg.table + (int64_t)far.b * pg.max_blocks + key / pg.block_size;
       far_row = key % pg.block_size;
       if (far_t >= w.tree_tiles) far_blk = __ldg(far_table);

@@ -746,6 +746,10 @@ static int slots_rows(bool write, void *pages, const int32_t *slots, void *rows,
   if (rc != SPEC_OK) return rc;
   if ((long long)n_rows * hkv > (1 << 30)) return SPEC_ERR_UNSUPPORTED;
   if (!aligned16(rows)) return SPEC_ERR_INVALID_ARG;
+  const size_t row = (size_t)head_dim * elem_bytes, all = row * n_rows * hkv, list = (size_t)n_rows * 4,
+               pool = row * num_blocks * hkv * block_size;
+  if (overlap(pages, pool, rows, all) || overlap(write ? pages : rows, write ? pool : all, slots, list))
+    return SPEC_ERR_INVALID_ARG;
   return sv_slots_rows(write, pages, rows, slots, n_rows, hkv, block_size, num_blocks, head_dim * elem_bytes / 16,
                        dev_status, cs(stream));
 }
