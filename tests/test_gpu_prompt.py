@@ -202,3 +202,13 @@ def test_more_queries_than_none_are_reported(lib):
     assert int(st.item()) == sv.DEV_CAPACITY and bool((out == 7.0).all())
     out, st = call(make(13, 2, [0, 0], [2000, 7], spare=5), max_q=0)
     assert int(st.item()) == 0 and bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("H,new,total", [(24, [1500, 700], [3000, 700]), (2, [200, 129], [9000, 4000])])
+def test_runs_agree_with_one_another(lib, H, new, total):
+    c = make(14, H, new, total)
+    first, st = call(c)
+    check(c, first, st)
+    for _ in range(20):
+        out, st = call(c)
+        assert int(st.item()) == 0 and torch.equal(out, first)

@@ -11,19 +11,26 @@
 //   S_i(j) = Q_i K(j)^T  (N = 128, K = 192; the rotary columns of K are one
 //            64-column box shared by all heads)   768 cycles
 //   O_i   += P_i(j) V(j) (N = 128 dims, K = 128; P in TMEM over S)  512 cycles
-// P lies where S was, so S_i(j + 1) waits for PV_i(j) to be done.
-//   warp 0      loads Q, K (two stages) and V, and clears the V rows past the
-//               sequence's last key
+// P lies where S was, and S_i(j + 1) goes over it right behind PV_i(j).
+//   warp 0      loads Q, K and V, and clears the V rows past the sequence's
+//               last key
 //   warps 1, 2  the MMAs of tile 0 and 1 (an elected thread each); their S in
 //               turns, or both tiles would multiply and then both wait
-//   warps 4-19  softmax and output, eight warps a tile: a thread half a row
+//   warps 4-19  softmax and output, eight warps a tile: a thread half a row;
+//               P is announced in two parts, so that PV starts under the rest
+// Shared memory behind Q holds three pairs of 16 KB pieces, taken in turn by
+// the 128 dims of K(j), K(j + 1) and V(j) (V(j + 1) follows K(j), whose S is the
+// first to be done, K(j + 2) follows V(j)), and two pieces for rotary columns.
 // What bounds it: two tiles' MMAs are 2560 cycles a key tile (2660 by their
-// shared-memory traffic), the chain S, softmax (1400), PV with its hand-offs
-// 3850.  8192 tokens of 32 heads 480-515 us, 1.34 to 1.43 PFLOP/s, at the power
-// limit (1365 W, 1950 MHz).  Steps: one MMA warp and eight softmax warps 4680
-// cycles, 527 us; a warp a tile 4060, 491; S in turns 3850, 483.  Without the
-// exponentials (timing only) the same: not a limit of the exponential unit.
-// Scalar instead of two-wide float32 arithmetic 508 us.
+// shared-memory traffic), the chain S, softmax (1600), PV with its hand-offs
+// 3000 to 3300.  8192 tokens of 32 heads 440 to 465 us, 1.48 to 1.56 PFLOP/s, at
+// the power limit (1365 W).  Steps: one MMA warp and eight softmax warps 4680
+// cycles, 527 us; a warp a tile 4060, 491; S in turns 3850, 483; P in two parts
+// 476; V no longer waiting for its one place 470; PV's end and the next S in
+// one issue 463; one wait for several barriers 440.  Without the exponentials
+// (timing only) the same: not a limit of the exponential unit.  Not kept: scalar
+// instead of two-wide float32 arithmetic (+4 %), P in parts of 48 and 16 or 16
+// and 48 keys (+4 %), S(j + 1) behind a wait for PV(j) (+7 %).
 // TMEM columns: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512).
 // Longest tiles are launched first.  Where CTAs are fewer than SMs (a chunk of
 // few heads behind a long kept beginning) the keys are cut into parts, a CTA
@@ -42,19 +49,19 @@ using namespace sv::ptx;
 
 constexpr int kBN = 128, kD = 128, kRope = 64, kThreads = 640, kTiles = 2, kSms = 152;
 constexpr uint32_t kPiece = 128 * 128;  // 128 rows x 64 elements, 128-byte swizzle
-constexpr uint32_t kQBytes = 3 * kPiece, kKBytes = 3 * kPiece, kVBytes = 2 * kPiece;
+constexpr uint32_t kQBytes = 3 * kPiece, kPair = 2 * kPiece, kRing = 3 * kPair + 2 * kPiece;
 constexpr uint32_t kWaitLimit = 1u << 22;
 using sv::kLow;
-constexpr float kTau = 16.f;      // the maximum moves when a tile exceeds it by more than 2^kTau
+constexpr float kTau = 16.f;  // the maximum moves when a tile exceeds it by more than 2^kTau
 
 struct Bars {
-  uint64_t q[kTiles], kfull[2], kempty[2], vfull, vempty, vclear, sfull[kTiles], p[kTiles], pv[kTiles], turn[kTiles], drain[kTiles];
+  uint64_t q[kTiles], kfull[2], kempty[2], vfull[2], vempty[2], vclear, sfull[kTiles], p[2][kTiles], pv[kTiles], turn[kTiles], drain[kTiles];
   uint32_t tmem;
   volatile int abort;
   // by half of the keys and row (one buffer: S(j + 1) comes after both halves' P(j))
   float xmax[2][kTiles * 128];
 };
-constexpr uint32_t kSmemBytes = kTiles * kQBytes + 2 * kKBytes + kVBytes + sizeof(Bars);
+constexpr uint32_t kSmemBytes = kTiles * kQBytes + kRing + sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory per CTA exceeds 227 KB");
 
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);   // Q, K both K-major
@@ -71,6 +78,25 @@ __device__ __forceinline__ bool wait(Bars *bars, uint64_t *bar, uint32_t parity)
   bool ok = false;
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if ((ok = mbar_try_wait(bar, parity))) break;
+    if ((i & 63) == 63 && bars->abort) break;
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) bars->abort = 1;
+  return ok;
+}
+// The same for several, whose tries overlap (one of a completed barrier takes
+// some 180 cycles beside busy softmax warps).
+struct Phase {
+  uint64_t *bar;
+  uint32_t parity;
+};
+template <int N> __device__ __forceinline__ bool wait(Bars *bars, const Phase (&ph)[N]) {
+  bool ok = false;
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    ok = true;
+#pragma unroll
+    for (int k = 0; k < N; ++k) ok &= mbar_try_wait(ph[k].bar, ph[k].parity);
+    if (ok) break;
     if ((i & 63) == 63 && bars->abort) break;
   }
   ok = __all_sync(0xffffffffu, ok);
@@ -106,8 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) sv::report(status, SPEC_DEV_INTERNAL);
     return;
   }
-  uint8_t *sQ = smem, *sK = sQ + kTiles * kQBytes, *sV = sK + 2 * kKBytes;
-  Bars *bars = reinterpret_cast<Bars *>(sV + kVBytes);
+  uint8_t *sQ = smem, *ring = sQ + kTiles * kQBytes, *sR = ring + 3 * kPair;
+  Bars *bars = reinterpret_cast<Bars *>(ring + kRing);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   // key tiles of each query tile: up to its last query's position; of them
@@ -131,14 +157,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->q[i], 1);
       mbar_init(&bars->kfull[i], 1);
       mbar_init(&bars->kempty[i], kTiles);
+      mbar_init(&bars->vfull[i], 1);
+      mbar_init(&bars->vempty[i], kTiles);
       mbar_init(&bars->sfull[i], 1);
-      mbar_init(&bars->p[i], 8);
+      mbar_init(&bars->p[0][i], 8);
+      mbar_init(&bars->p[1][i], 8);
       mbar_init(&bars->pv[i], 1);
       mbar_init(&bars->turn[i], 1);
       mbar_init(&bars->drain[i], 1);
     }
-    mbar_init(&bars->vfull, 1);
-    mbar_init(&bars->vempty, kTiles);
     mbar_init(&bars->vclear, 1);
     bars->abort = 0;
     mbar_fence_init();
@@ -159,13 +186,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_r);
       tma_prefetch_desc(&tm_v);
     }
-    int k_done = 0, v_done = 0;
+    int k_done = 0, v_done = 0, at = 0;  // at: j mod 3
+    auto rope = [&](int j) {
+      mbar_expect_tx(&bars->kfull[j & 1], 3 * kPiece);
+      tma_load_2d(sR + (j & 1) * kPiece, &tm_r, 0, k_first + (j0 + j) * kBN, &bars->kfull[j & 1]);
+    };
     for (int j = 0; ok && j < all; ++j) {
       const int row = k_first + (j0 + j) * kBN;
-      if (!(ok = wait(bars, &bars->kempty[j & 1], ((j >> 1) & 1) ^ 1))) break;
+      if (j > 1 && !(ok = wait(bars, &bars->vempty[j & 1], ((j >> 1) & 1) ^ 1))) break;
       if (me) {
-        uint64_t *bar = &bars->kfull[j & 1];
-        uint8_t *dst = sK + (j & 1) * kKBytes;
         if (j == 0) {
 #pragma unroll
           for (int i = 0; i < kTiles; ++i)
@@ -175,23 +204,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d(sQ + i * kQBytes + c * kPiece, &tm_q, c * 64, head, q_first + q0 + i * 128, &bars->q[i]);
             }
         }
-        mbar_expect_tx(bar, kKBytes);
-        tma_load_3d(dst, &tm_k, 0, head, row, bar);
-        tma_load_3d(dst + kPiece, &tm_k, 64, head, row, bar);
-        tma_load_2d(dst + 2 * kPiece, &tm_r, 0, row, bar);
+        if (j < 2) rope(j);
+        tma_load_3d(ring + at * kPair, &tm_k, 0, head, row, &bars->kfull[j & 1]);
+        tma_load_3d(ring + at * kPair + kPiece, &tm_k, 64, head, row, &bars->kfull[j & 1]);
       }
       ++k_done;
       __syncwarp();
-      if (!(ok = wait(bars, &bars->vempty, (j & 1) ^ 1))) break;
+      if (j > 0 && !(ok = wait(bars, &bars->kempty[(j - 1) & 1], ((j - 1) >> 1) & 1))) break;
+      at = at == 0 ? 2 : at - 1;  // (j + 2) mod 3
       if (me) {
-        mbar_expect_tx(&bars->vfull, kVBytes);
-        tma_load_3d(sV, &tm_v, 0, head, row, &bars->vfull);
-        tma_load_3d(sV + kPiece, &tm_v, 64, head, row, &bars->vfull);
+        uint64_t *bar = &bars->vfull[j & 1];
+        mbar_expect_tx(bar, kPair);
+        tma_load_3d(ring + at * kPair, &tm_v, 0, head, row, bar);
+        tma_load_3d(ring + at * kPair + kPiece, &tm_v, 64, head, row, bar);
+        if (j > 0 && j + 1 < all) rope(j + 1);
       }
+      at = at == 0 ? 2 : at - 1;  // (j + 1) mod 3
       ++v_done;
       __syncwarp();
     }
-    if (ok && all > 0 && (ok = wait(bars, &bars->vfull, (all - 1) & 1))) {
+    if (ok && all > 0 && (ok = wait(bars, &bars->vfull[(all - 1) & 1], ((all - 1) >> 1) & 1))) {
+      uint8_t *sV = ring + (all + 1) % 3 * kPair;
       // what follows the sequence's last key belongs to others: cleared
       const int keys = keys_left - (all - 1) * kBN;
       if (keys < kBN) {
@@ -207,58 +240,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kTiles; ++i)
         if (k_done > 0 && tiles[i] > 0) mbar_wait(&bars->q[i], 0, kWaitLimit);
       for (int j = k_done > 2 ? k_done - 2 : 0; j < k_done; ++j) mbar_wait(&bars->kfull[j & 1], (j >> 1) & 1, kWaitLimit);
-      if (v_done > 0) mbar_wait(&bars->vfull, (v_done - 1) & 1, kWaitLimit);
+      for (int j = v_done > 2 ? v_done - 2 : 0; j < v_done; ++j) mbar_wait(&bars->vfull[j & 1], (j >> 1) & 1, kWaitLimit);
     }
   } else if (warp < 1 + kTiles) {
     // ---------------------------------------------------------------- MMAs
     // (a warp a tile: an MMA waits for room in a short queue, so the waits of
     // one warp run under the products of the other)
     const int i = warp - 1;
-    const uint32_t qa = smem_u32(sQ) + i * kQBytes, ka = smem_u32(sK), va = smem_u32(sV);
+    const uint32_t qa = smem_u32(sQ) + i * kQBytes, ring_a = smem_u32(ring), ra = smem_u32(sR);
+    uint32_t ka = ring_a, va = ring_a + 2 * kPair;  // K(j) and V(j)
     const uint32_t s_col = tmem + i * 128, o_col = tmem + 256 + i * 128;
     const int nt = i == 0 ? tiles[0] : tiles[1];
     if (nt > 0) ok = wait(bars, &bars->q[i], 0);
-    for (int j = 0; ok && j < all; ++j) {
-      if (!(ok = wait(bars, &bars->kfull[j & 1], (j >> 1) & 1))) break;
-      // S in turns: issued side by side, both tiles' products and then both
-      // their softmaxes would run at the same time
-      if (i == 1 ? !(ok = wait(bars, &bars->turn[0], j & 1)) : j > 0 && !(ok = wait(bars, &bars->turn[1], (j - 1) & 1))) break;
-      if (j < nt) {
-        // P(j - 1), where S goes, has been read
-        if (j > 0 && !(ok = wait(bars, &bars->pv[i], (j - 1) & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
+    auto scores = [&](int j) {  // (the elected thread)
 #pragma unroll
-          for (int k = 0; k < 12; ++k) {
-            const uint32_t off = (k >> 2) * kPiece + (k & 3) * 32;
-            mma_ss(s_col, smem_desc_sw128(qa + off, 16, 1024), smem_desc_sw128(ka + (j & 1) * kKBytes + off, 16, 1024),
-                   kIdescS, k > 0);
-          }
-          mma_commit(&bars->sfull[i]);
-          mma_commit(&bars->kempty[j & 1]);
+      for (int k = 0; k < 12; ++k) {
+        const uint32_t off = (k >> 2) * kPiece + (k & 3) * 32;
+        const uint32_t key = k < 8 ? ka + off : ra + (j & 1) * kPiece + (k & 3) * 32;
+        mma_ss(s_col, smem_desc_sw128(qa + off, 16, 1024), smem_desc_sw128(key, 16, 1024), kIdescS, k > 0);
+      }
+      mma_commit(&bars->sfull[i]);
+      mma_commit(&bars->kempty[j & 1]);
+      mbar_arrive(&bars->turn[i]);
+    };
+    // What S(j) waits for: its keys, and its turn (issued side by side, both
+    // tiles' products and then both their softmaxes would run at the same time).
+    auto keys = [&](int j) { return Phase{&bars->kfull[j & 1], (uint32_t)(j >> 1) & 1}; };
+    auto turn = [&](int j) {  // (of tile 0's first: none, a phase that is over)
+      return Phase{&bars->turn[1 - i], (uint32_t)(i == 1 ? j : j - 1) & 1};
+    };
+    for (int j = -1; ok && j < all; ++j) {
+      // P(j) V(j), and S(j + 1) right behind it.  S goes over P: the same thread
+      // has issued the products that read it before, and a CTA's products of one
+      // shape run one after another, in the order of their issue (the tests
+      // compare with a plain form at every size, and runs with one another).
+      // P comes in two parts, the first 32 keys of each half of 64 and the rest.
+      auto values = [&](int c) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = (e >> 1) * 4 + c * 2 + (e & 1);
+          mma_ts(o_col, s_col + k * 8, smem_desc_sw128(va + k * 2048, kPiece, 1024), kIdescPV, j > 0 || c > 0 || e > 0);
+        }
+      };
+      const bool mine = j >= 0 && j < nt, next = j + 1 < all;
+      if (j >= 0) {
+        const Phase v{&bars->vfull[j & 1], (uint32_t)(j >> 1) & 1};
+        if (mine) {
+          if (keys_left - j * kBN < kBN && !(ok = wait(bars, &bars->vclear, 0))) break;
+          if (!(ok = wait(bars, {v, {&bars->p[0][i], (uint32_t)j & 1}}))) break;
+          tc_fence_after();
+          if (elect_one()) values(0);
+          __syncwarp();
+          const Phase p{&bars->p[1][i], (uint32_t)j & 1};
+          if (!(ok = next ? wait(bars, {keys(j + 1), turn(j + 1), p}) : wait(bars, p.bar, p.parity))) break;
+          tc_fence_after();
+        } else if (!(ok = next ? wait(bars, {v, keys(j + 1), turn(j + 1)}) : wait(bars, v.bar, v.parity))) {
+          break;
+        }
+      } else if (next && !(ok = wait(bars, {keys(0), turn(0)}))) {
+        break;
+      }
+      if (elect_one()) {
+        if (mine) {
+          values(1);
+          mma_commit(&bars->pv[i]);
+          mma_commit(&bars->vempty[j & 1]);
+        } else if (j >= 0) {
+          mbar_arrive(&bars->vempty[j & 1]);
+        }
+        if (j + 1 < nt) {
+          scores(j + 1);
+        } else if (next) {
+          mbar_arrive(&bars->kempty[(j + 1) & 1]);
           mbar_arrive(&bars->turn[i]);
         }
-        __syncwarp();
-      } else if (elect_one()) {
-        mbar_arrive(&bars->kempty[j & 1]);
-        mbar_arrive(&bars->turn[i]);
       }
-      if (!(ok = wait(bars, &bars->vfull, j & 1))) break;
-      if (j < nt) {
-        if (keys_left - j * kBN < kBN && !(ok = wait(bars, &bars->vclear, 0))) break;
-        if (!(ok = wait(bars, &bars->p[i], j & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts(o_col, s_col + k * 8, smem_desc_sw128(va + k * 2048, kPiece, 1024), kIdescPV, j > 0 || k > 0);
-          mma_commit(&bars->pv[i]);
-          mma_commit(&bars->vempty);
-        }
-        __syncwarp();
-      } else if (elect_one()) {
-        mbar_arrive(&bars->vempty);
-      }
+      __syncwarp();
+      if (j >= 0) va = va == ring_a + 2 * kPair ? ring_a : va + kPair;
+      ka = ka == ring_a + 2 * kPair ? ring_a : ka + kPair;
     }
     if (!ok) {  // let issued MMAs finish before TMEM is freed
       if (elect_one()) mma_commit(&bars->drain[i]);
@@ -336,16 +395,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc[e & 1] = add2(acc[e & 1], v);
           pk[e] = pack_bf16(v.x, v.y);
         }
-        if (ok) tmem_st16(s_addr + h * 32 + c * 16, pk);
+        if (ok) {
+          tmem_st16(s_addr + h * 32 + c * 16, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p[c][i]);
+        }
       }
       const float2 sum = add2(acc[0], acc[1]);
       l += sum.x + sum.y;
-      if (ok) {
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p[i]);
-      }
     }
     row_sync();
     bars->xmax[h][i * 128 + r] = l;
