@@ -37,6 +37,7 @@ constexpr int kRows = 16, kBN = 64, kRope = 64, kThreads = 256, kWarps = 8, kCta
 constexpr uint32_t kPiece = 64 * 128;  // 64 keys x 64 elements, 128-byte swizzle
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr int kSegW = 2;  // a unit's fixed cost, in tiles
+constexpr int kJoinW = 4;  // what a join costs, in tiles
 
 using Work = sv::LatentWork<kBN, kRows>;
 using Walk = sv::LatentWalk<Work>;
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 0) {
     const sv::LatentRange r =
-        sv::latent_range(w, blockIdx.x, gridDim.x, kSegW, desc + blockIdx.x, blockIdx.x == 0 ? status : nullptr);
+        sv::latent_range(w, blockIdx.x, gridDim.x, kSegW, kJoinW, desc + blockIdx.x, blockIdx.x == 0 ? status : nullptr);
     if (lane == 0) rest->range = r;
   }
   __syncthreads();

@@ -65,6 +65,7 @@ constexpr int kBN = 128, kRope = 64, kThreads = 384, kPairs = 76;
 constexpr uint32_t kPiece = 64 * 128;  // 64 rows (or keys) x 64 elements, 128-byte swizzle
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr int kSegW = 3;      // a unit's fixed cost, in tiles (ragged trees: 1 143 us, 2 132, 3 128, 5 129)
+constexpr int kJoinW = 16;    // what a join costs, in tiles
 using sv::kLow;
 constexpr float kTau = 16.f;  // the maximum moves when a tile exceeds it by more than 2^kTau
 
@@ -221,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc_pair(&bars->tmem, 512);
   if (warp == 0) {
-    const sv::LatentRange range = sv::latent_range(w, pair, pairs, kSegW, rank == 0 ? desc + pair : nullptr,
+    const sv::LatentRange range = sv::latent_range(w, pair, pairs, kSegW, kJoinW, rank == 0 ? desc + pair : nullptr,
                                                    blockIdx.x == 0 ? status : nullptr);
     if (lane == 0) bars->range = range;
   }

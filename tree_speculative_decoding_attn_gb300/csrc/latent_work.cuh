@@ -50,41 +50,79 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // One warp: the range of part `part` of `parts`.  desc (may be null): the
 // first range end inside a cut unit names it and its parts (sequence, unit,
 // parts, 1).  status (may be null): refused prefix lengths are reported.
+// Where whole units share out nearly as evenly, none is cut: the longest part
+// is then no more than `join` weights (about what partials and their join cost)
+// and 1/32 above the mean.  us cut / whole: one token of 64 heads, batch 64, 4096
+// keys 84 / 74, 500 keys 35 / 23; 64 heads x 32 nodes, 4 trees over 4096 keys 80
+// / 65, 32 trees 439 / 416, over 8192 keys 902 / 782 (whole units of a sequence
+// run side by side, in L2); one token of 16 heads, batch 140, 2048 keys 68 / 63.
+// Not whole: 64 heads x 9 nodes, 8 trees over 6000 keys 73 / 89; one token of 64
+// heads, 64 sequences of 1000 to 8000 keys 91 / 98.
 template <class Work>
-__device__ __forceinline__ LatentRange latent_range(const Work &w, int part, int parts, int fixed, int4 *desc,
+__device__ __forceinline__ LatentRange latent_range(const Work &w, int part, int parts, int fixed, int join, int4 *desc,
                                                     int32_t *status) {
   const int lane = threadIdx.x & 31;
   long long total = 0;
-  int T0 = 0;  // of sequence `lane`
+  int T0 = 0, most = 0;  // tiles of sequence `lane`, of the longest
   for (int s = 0; s < w.batch; s += 32) {
     const int b = s + lane;
     if (b < w.batch) {
       const int T = w.tiles(b);
       if (s == 0) T0 = T;
+      most = max(most, T);
       total += (long long)w.RT * (T + fixed);
       if (T == 0) report(status, SPEC_DEV_CAPACITY);
     }
   }
+  most = __reduce_max_sync(0xffffffffu, most) + fixed;
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  // (no more ranges than weight: each that begins inside a unit has a tile)
-  const long long n = total < parts ? total : parts;
   LatentRange r{0, 0, 0, 0};
-  if (part >= n) {
-    if (desc && lane == 0) *desc = make_int4(0, 0, 0, 0);
-    return r;
-  }
-  const long long lo = quotient(total * part, n), hi = quotient(total * (part + 1), n);
-  long long base = 0;
-  for (int s = 0; s < w.batch; s += 32) {
+  long long base = 0;  // weight of the sequences before the 32 that are looked at
+  // sequence b = s + lane: its tiles, its weight, and where it begins
+  auto look = [&](int s, int &T, long long &mine, long long &first) {
     const int b = s + lane;
-    const int T = b >= w.batch ? 0 : s == 0 ? T0 : w.tiles(b);
-    const long long mine = b < w.batch ? (long long)w.RT * (T + fixed) : 0;
+    T = b >= w.batch ? 0 : s == 0 ? T0 : w.tiles(b);
+    mine = b < w.batch ? (long long)w.RT * (T + fixed) : 0;
     long long up = mine;
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, up, o);
       if (lane >= o) up += v;
     }
-    const long long first = base + up - mine;
+    first = base + up - mine;
+    base += __shfl_sync(0xffffffffu, up, 31);
+  };
+  int T;
+  long long mine, first;
+  const long long units = (long long)w.batch * w.RT, each = units <= parts ? 1 : quotient(units + parts - 1, parts);
+  if (each * most * parts <= total + (total >> 5) + (long long)join * parts) {  // whole units, `each` a part
+    const long long i0 = each * part, i1 = i0 + each;
+    if (desc && lane == 0) *desc = make_int4(0, 0, 0, 0);
+    if (i0 >= units) return r;
+    const int b0 = (int)quotient(i0, w.RT), b1 = (int)quotient(i1, w.RT);
+    r.b = b0;
+    r.hi = total;
+    for (int s = 0; s < w.batch && s <= b1; s += 32) {
+      look(s, T, mine, first);
+      const long long lo = first + (i0 - (long long)b0 * w.RT) * (T + fixed);
+      const long long hi = first + (i1 - (long long)b1 * w.RT) * (T + fixed);
+      if (b0 >> 5 == s >> 5) {
+        r.b0 = __shfl_sync(0xffffffffu, first, b0 & 31);
+        r.lo = __shfl_sync(0xffffffffu, lo, b0 & 31);
+      }
+      if (b1 < w.batch && b1 >> 5 == s >> 5) r.hi = __shfl_sync(0xffffffffu, hi, b1 & 31);
+    }
+    return r;
+  }
+  // (no more ranges than weight: each that begins inside a unit has a tile)
+  const long long n = total < parts ? total : parts;
+  if (part >= n) {
+    if (desc && lane == 0) *desc = make_int4(0, 0, 0, 0);
+    return r;
+  }
+  const long long lo = quotient(total * part, n), hi = quotient(total * (part + 1), n);
+  for (int s = 0; s < w.batch; s += 32) {
+    const int b = s + lane;
+    look(s, T, mine, first);
     const bool here = b < w.batch && first <= lo && lo < first + mine;
     if (here && desc) {
       int4 d = make_int4(0, 0, 0, 0);
@@ -107,7 +145,6 @@ __device__ __forceinline__ LatentRange latent_range(const Work &w, int part, int
       r.b = s + l;
       return r;
     }
-    base += __shfl_sync(0xffffffffu, up, 31);
   }
   return r;
 }
