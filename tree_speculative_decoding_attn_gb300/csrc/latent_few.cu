@@ -372,7 +372,7 @@ int launch(const SvLatentShape &s, const void *q, const void *cache, const void 
     return SPEC_ERR_CUDA;
   int4 *desc = static_cast<int4 *>(ws);
   float *slots = reinterpret_cast<float *>(desc + kCtas);
-  const Work w(prefix_len, s.batch, s.n_nodes, s.hq, s.s_max, s.max_prefix);
+  const Work w(prefix_len, s.batch, s.n_nodes, s.hq, s.s_max, s.max_prefix, C::D * 2);
   if (cudaFuncSetAttribute(latent_few_kernel<LAT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)smem_bytes<LAT>()) != cudaSuccess)
     return SPEC_ERR_CUDA;

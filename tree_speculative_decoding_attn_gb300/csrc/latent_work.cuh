@@ -24,9 +24,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 template <int TILE, int ROWS> struct LatentWork {
   const int32_t *prefix_len;
   int batch, N, hq, s_max, max_prefix, RT, tree_tiles;
-  LatentWork(const int32_t *prefix_len, int batch, int N, int hq, int s_max, int max_prefix)
+  int far;  // so many tiles of all sequences together do not stay in L2
+  LatentWork(const int32_t *prefix_len, int batch, int N, int hq, int s_max, int max_prefix, int row_bytes)
       : prefix_len(prefix_len), batch(batch), N(N), hq(hq), s_max(s_max), max_prefix(max_prefix),
-        RT((N * hq + ROWS - 1) / ROWS), tree_tiles((N + TILE - 1) / TILE) {}
+        RT((N * hq + ROWS - 1) / ROWS), tree_tiles((N + TILE - 1) / TILE), far((100 << 20) / (TILE * row_bytes)) {}
   __device__ int prefix(int b) const { return __ldg(prefix_len + b); }
   __device__ bool fits(int P) const { return P >= 0 && P <= max_prefix && P <= s_max; }
   // tiles of a unit of sequence b (0: its prefix length is refused)
@@ -114,7 +115,14 @@ __device__ __forceinline__ LatentRange latent_range(const Work &w, int part, int
     return r;
   }
   // (no more ranges than weight: each that begins inside a unit has a tile)
-  const long long n = total < parts ? total : parts;
+  long long n = total < parts ? total : parts;
+  // The units of a sequence read the same rows.  Where those do not stay in L2,
+  // parts in halves of a unit let pairs of units read them at the same time: 4
+  // sequences of 4 units over 32768 keys, 76 parts 130 us, 72 (4.5 a unit) 117.
+  if (w.RT > 1 && units * most == total && (long long)most * w.batch > w.far) {
+    const long long even = quotient(2ll * parts, units) * units / 2;
+    if (10 * even >= 9ll * parts && even < n) n = even;
+  }
   if (part >= n) {
     if (desc && lane == 0) *desc = make_int4(0, 0, 0, 0);
     return r;
