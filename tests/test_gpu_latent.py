@@ -312,3 +312,28 @@ def test_wrapper_refuses(lib):
                dict(block_table=torch.zeros(B + 1, 2, dtype=torch.int32, device="cuda"))):
         with pytest.raises((ValueError, TypeError, sv.SpecError)):
             sv.tree_attn_verify_latent_paged(**{**paged, **kw})
+
+
+@pytest.mark.parametrize("B,N,H,lat,lo,hi", [(70, 1, 64, 256, 300, 340), (66, 1, 33, 256, 700, 700), (30, 6, 64, 256, 128, 140),
+                                             (45, 2, 100, 512, 0, 60), (140, 1, 16, 256, 200, 256), (33, 1, 16, 512, 0, 130)])
+def test_units_that_are_not_cut(lib, B, N, H, lat, lo, hi):
+    """Whole units a part, one or several, with sequences that are refused among them."""
+    prefix = [lo + (31 * i) % (hi - lo + 1) for i in range(B)]
+    c = make(21, B, N, H, lat, prefix, BF, 128)
+    out, st = call(c)
+    check(c, out, st)
+    refused = [b for b in (0, 31, 32, B - 1) if b < B]
+    other = list(prefix)
+    for b in refused:
+        other[b] = -1 if b % 2 else max(prefix) + 1
+    again, st = call(c, prefix=i32(other))
+    assert int(st.item()) == sv.DEV_CAPACITY
+    check(c, again, zeros_i32(1), skip=refused)
+    for b in refused:
+        assert bool((again[b] == 7.0).all())
+
+
+def test_parts_in_halves_of_a_unit(lib):
+    """Six units over more rows than L2 holds: 75 parts instead of 76."""
+    c = make(22, 2, 3, 90, 256, [82000, 82000], BF, 0)
+    check(c, *call(c))
