@@ -567,8 +567,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_ld32(tmem + lane_off + c, v);
           tmem_wait_ld();
           const int d = (c >> 7) * 256 + (c & 127);  // (+ half * 128)
-          if (!row_ok) continue;
           if (whole) {
+            // rows to pieces of 64 bytes of a row (lanes of 32 rows would touch 32
+            // lines with each store), over the part of P that the four warps of
+            // these rows write next behind a barrier of theirs
+            uint8_t *st = sP + half * kPiece + (quarter & 1) * 4096 + h * 2048;
+            __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint4 u;
@@ -576,13 +580,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               u.y = pack_bf16(__uint_as_float(v[8 * i + 2]) * inv, __uint_as_float(v[8 * i + 3]) * inv);
               u.z = pack_bf16(__uint_as_float(v[8 * i + 4]) * inv, __uint_as_float(v[8 * i + 5]) * inv);
               u.w = pack_bf16(__uint_as_float(v[8 * i + 6]) * inv, __uint_as_float(v[8 * i + 7]) * inv);
-              *reinterpret_cast<uint4 *>(o + d + 8 * i) = u;
+              *reinterpret_cast<uint4 *>(st + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = u;
             }
-          } else {
-            float *dst = slot + (size_t)lr * LAT + half * 128 + d;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int to = i * 8 + (lane >> 2), piece = lane & 3;  // row among the warp's 32
+              if (row - lane + to < R)
+                *reinterpret_cast<uint4 *>(o + (to - lane) * LAT + d + 8 * piece) =
+                    *reinterpret_cast<const uint4 *>(st + to * 64 + ((piece ^ ((to >> 1) & 3)) << 4));
+            }
+          } else if (row_ok) {
+            float *dst = slot + sv::latent_at<LAT, 128>(lr, half * 128 + d);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4 *>(dst + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              *reinterpret_cast<uint4 *>(dst + i * 4 * 128) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
         if (!whole && row_ok && half == 0 && h == 0)

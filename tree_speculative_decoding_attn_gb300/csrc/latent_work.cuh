@@ -189,6 +189,12 @@ template <class Work> struct LatentWalk {
 // log2 units, sum).  Part p has two: 2p for a segment cut at its start, 2p + 1
 // for one cut at its end alone.
 __host__ __device__ constexpr size_t latent_slot_floats(int lat, int rows) { return rows * (size_t)(lat + 2); }
+// Where dim `dim` of row `row` lies in it.  128 rows: [LAT / 4][128][4], since a
+// thread that writes them holds a row, and a warp's store is 512 bytes in one
+// piece (a row after another: 32 lines; 6.5 us for a pair's partial instead of 3).
+template <int LAT, int ROWS> __host__ __device__ constexpr size_t latent_at(int row, int dim) {
+  return ROWS == 128 ? ((size_t)(dim >> 2) * ROWS + row) * 4 + (dim & 3) : row * (size_t)LAT + dim;
+}
 
 constexpr int kMostParts = 160;
 // The k-th cut unit of those that there are, by its first range end (0: fewer
@@ -235,17 +241,17 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v, float 
   *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
 }
 
-// Joins the parts of cut units, a thread four dims of a row.
-// FORM 0, many rows: block (8 rows, cut unit), the weights of all its rows
-// first, then four rows (LAT 256: eight) at a time, two parts of each in flight.
-// FORM 1 and 8, fewer: block (row, cut unit, LAT / FORM dims), eight parts in
-// flight, shared out over groups of threads whose sums go through shared memory.
+// Joins the parts of cut units, a thread four dims of a row at a time.
+// BY_ROW (FORM 8, and partials of 16 rows): block (row, cut unit, LAT / FORM
+// dims), eight parts in flight, shared out over groups of threads whose sums go
+// through shared memory.  Otherwise block (8 rows, cut unit, FORM 1: 64 dims, FORM
+// 0: all), the rows side by side as they lie.
 template <int LAT, int ROWS, int FORM>
 __global__ void __launch_bounds__(128)
     latent_join_kernel(const float *__restrict__ ws, const int4 *__restrict__ desc, int parts,
                        __nv_bfloat16 *__restrict__ out, int R) {
-  constexpr int RB = FORM ? 1 : 8, SIDE = 512 / LAT;  // rows of a block; rows side by side
-  constexpr int DIMS = FORM ? LAT / FORM : LAT, PER = DIMS / 4, GROUPS = 128 / PER;
+  constexpr bool BY_ROW = FORM == 8 || ROWS == 16;
+  constexpr int RB = BY_ROW ? 1 : 8;  // rows of a block
   __shared__ float s_a[RB][kMostParts], s_l[RB];
   __shared__ int s_part;
   const int warp = threadIdx.x >> 5;
@@ -275,14 +281,13 @@ __global__ void __launch_bounds__(128)
   }
   __syncthreads();
   __nv_bfloat16 *o = out + ((int64_t)d.x * R + d.y * ROWS + lr0) * LAT;
-  const int group = threadIdx.x / PER, at = threadIdx.x % PER;
   auto load = [&](int p, int r, int dim) {
-    return __ldcs(reinterpret_cast<const float4 *>(part(p) + (size_t)(lr0 + r) * LAT + dim));
+    return __ldcs(reinterpret_cast<const float4 *>(part(p) + latent_at<LAT, ROWS>(lr0 + r, dim)));
   };
-  if constexpr (FORM > 0) {
-    constexpr int B = 8;  // loads in flight
+  if constexpr (BY_ROW) {
+    constexpr int DIMS = LAT / FORM, PER = DIMS / 4, GROUPS = 128 / PER, B = 8;  // B: loads in flight
     __shared__ float4 s_acc[GROUPS][PER];
-    const int dim = blockIdx.z * DIMS + at * 4;
+    const int group = threadIdx.x / PER, at = threadIdx.x % PER, dim = blockIdx.z * DIMS + at * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p0 = group; p0 < d.z; p0 += B * GROUPS) {
       float4 x[B];
@@ -302,28 +307,27 @@ __global__ void __launch_bounds__(128)
     }
     store4(o + dim, acc, s_l[0]);
   } else {
-    constexpr int B = 4;  // rows in flight
-    for (int r0 = group; r0 < rows; r0 += B * SIDE) {
-      float4 acc[B];
+    constexpr int NI = FORM == 1 ? 1 : LAT / 64, B = FORM == 1 ? 8 : 2;  // pieces of a thread; parts in flight
+    const int r = threadIdx.x & 7, dim0 = blockIdx.z * 64 + (threadIdx.x >> 3) * 4;
+    if (r >= rows) return;
+    float4 acc[NI];
 #pragma unroll
-      for (int i = 0; i < B; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int p = 0; p < d.z; p += 2) {
-        float4 x[2][B];
+    for (int i = 0; i < NI; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < d.z; p += B) {
+      float4 x[B][NI];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < B; ++h)
 #pragma unroll
-          for (int i = 0; i < B; ++i)
-            if (p + h < d.z && r0 + i * SIDE < rows) x[h][i] = load(p + h, r0 + i * SIDE, at * 4);
+        for (int i = 0; i < NI; ++i)
+          if (p + h < d.z) x[h][i] = load(p + h, r, dim0 + i * 64);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < B; ++h)
 #pragma unroll
-          for (int i = 0; i < B; ++i)
-            if (p + h < d.z && r0 + i * SIDE < rows) fma4(acc[i], s_a[r0 + i * SIDE][p + h], x[h][i]);
-      }
-#pragma unroll
-      for (int i = 0; i < B; ++i)
-        if (r0 + i * SIDE < rows) store4(o + (size_t)(r0 + i * SIDE) * LAT + at * 4, acc[i], s_l[r0 + i * SIDE]);
+        for (int i = 0; i < NI; ++i)
+          if (p + h < d.z) fma4(acc[i], s_a[r][p + h], x[h][i]);
     }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) store4(o + (size_t)r * LAT + dim0 + i * 64, acc[i], s_l[r]);
   }
 }
 template <int LAT, int ROWS>
@@ -339,15 +343,19 @@ int launch_latent_join(const float *slots, const int4 *desc, __nv_bfloat16 *out,
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // (us of the whole call, FORM 8 / 1 / 0: 16 rows of 80 parts 12.2 / 15.4 / -,
-  // 16 units of 128 rows 154 / 130 / 144, 75 units of 128 rows - / 133 / 131)
+  // (us of the whole call, FORM 8 / 1 / 0: 128 rows of 76 parts 38 / 60 / -, 512
+  // rows of 19 parts 57 / 52 / -, 75 units of 128 rows - / 128 / 124)
   auto run = [&](auto kernel, dim3 grid) {
     cfg.gridDim = grid;
     return cudaLaunchKernelEx(&cfg, kernel, slots, desc, parts, out, R) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
   };
   if (rows * cut <= 256) return run(latent_join_kernel<LAT, ROWS, 8>, dim3(rows, cut, 8));
-  if (rows * cut <= 8192) return run(latent_join_kernel<LAT, ROWS, 1>, dim3(rows, cut));
-  return run(latent_join_kernel<LAT, ROWS, 0>, dim3((rows + 7) / 8, cut));
+  if constexpr (ROWS == 16) {
+    return run(latent_join_kernel<LAT, ROWS, 1>, dim3(rows, cut));
+  } else {
+    if (rows * cut <= 4096) return run(latent_join_kernel<LAT, ROWS, 1>, dim3((rows + 7) / 8, cut, LAT / 64));
+    return run(latent_join_kernel<LAT, ROWS, 0>, dim3((rows + 7) / 8, cut));
+  }
 }
 
 // ---------------------------------------------------------------- tensor maps
