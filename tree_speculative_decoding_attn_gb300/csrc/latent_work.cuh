@@ -197,17 +197,28 @@ template <int LAT, int ROWS> __host__ __device__ constexpr size_t latent_at(int 
 }
 
 constexpr int kMostParts = 160;
-// The k-th cut unit of those that there are, by its first range end (0: fewer
-// than k + 1).  One warp.
-__device__ __forceinline__ int latent_cut(const int4 *desc, int parts, int k) {
+// The k-th cut unit of those that there are, by its first range end (part 0:
+// fewer than k + 1).  One warp; all entries in flight at once.
+__device__ __forceinline__ void latent_cut(const int4 *desc, int parts, int k, int *part, int4 *d) {
   const int lane = threadIdx.x & 31;
+  int4 e[kMostParts / 32];
+#pragma unroll
+  for (int i = 0; i < kMostParts / 32; ++i) {
+    const int p = 1 + i * 32 + lane;
+    e[i] = p < parts ? desc[p] : make_int4(0, 0, 0, 0);
+  }
+  if (lane == 0) *part = 0;
+  __syncwarp();
   int seen = 0;
-  for (int p = 1; p < parts; p += 32) {
-    const unsigned cut = __ballot_sync(0xffffffffu, p + lane < parts && desc[p + lane].w != 0);
-    if (k < seen + __popc(cut)) return p + __fns(cut, 0, k - seen + 1);
+#pragma unroll
+  for (int i = 0; i < kMostParts / 32; ++i) {
+    const unsigned cut = __ballot_sync(0xffffffffu, e[i].w != 0);
+    if (e[i].w != 0 && seen + __popc(cut & ((1u << lane) - 1)) == k) {
+      *part = 1 + i * 32 + lane;
+      *d = e[i];
+    }
     seen += __popc(cut);
   }
-  return 0;
 }
 // What the n parts of a row weigh (into a[]), and the sum of all their sums.
 // One warp.
@@ -254,19 +265,19 @@ __global__ void __launch_bounds__(128)
   constexpr int RB = BY_ROW ? 1 : 8;  // rows of a block
   __shared__ float s_a[RB][kMostParts], s_l[RB];
   __shared__ int s_part;
+  __shared__ int4 s_desc;
   const int warp = threadIdx.x >> 5;
   ptx::grid_dep_wait();
-  if (warp == 0) {
-    // (as many blocks as range ends: each looks at its own)
-    const int p = (int)gridDim.y < parts - 1            ? latent_cut(desc, parts, blockIdx.y)
-                  : desc[blockIdx.y + 1].w != 0 ? (int)blockIdx.y + 1
-                                                : 0;
-    if (threadIdx.x == 0) s_part = p;
+  if ((int)gridDim.y < parts - 1) {
+    if (warp == 0) latent_cut(desc, parts, blockIdx.y, &s_part, &s_desc);
+  } else if (threadIdx.x == 0) {  // as many blocks as range ends: each looks at its own
+    s_desc = desc[blockIdx.y + 1];
+    s_part = s_desc.w != 0 ? (int)blockIdx.y + 1 : 0;
   }
   __syncthreads();
   const int part0 = s_part;
   if (part0 == 0) return;
-  const int4 d = desc[part0];
+  const int4 d = s_desc;
   const int lr0 = blockIdx.x * RB, rows = min(min(RB, ROWS - lr0), R - d.y * ROWS - lr0);
   if (rows <= 0) return;
   // the first part ends its range (slot 1), the others begin theirs (slot 0)
