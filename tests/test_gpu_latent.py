@@ -337,3 +337,9 @@ def test_parts_in_halves_of_a_unit(lib):
     """Six units over more rows than L2 holds: 75 parts instead of 76."""
     c = make(22, 2, 3, 90, 256, [82000, 82000], BF, 0)
     check(c, *call(c))
+
+
+@pytest.mark.parametrize("H,lat,P", [(4, 512, 3200), (9, 256, 9001), (16, 512, 2047)])
+def test_float32_in_many_ranges(lib, H, lat, P):
+    c = make(23, 1, 1, H, lat, [P], F32, 0)
+    check(c, *call(c))

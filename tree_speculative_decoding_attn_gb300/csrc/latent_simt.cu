@@ -11,19 +11,21 @@
 // the float32 FMA rate (every key row is read once per 8 rows, from L1 the
 // second time); float32 caches are for exactness, not for speed.  A small call
 // is a row's chain of loads, scores and the join: a tree of 5 nodes x 4 heads
-// over 129 rows 12 us (18.8 with a warp's keys one after another,
-// 13.0 with the join as an ordinary launch).
+// over 129 rows 8.3 us (18.8 with a warp's keys one after another, 13.0 with the
+// join as an ordinary launch, 11.9 with the queries loaded behind the length, the
+// join's ranges one after another and ranges of 32 keys).
 #include <math.h>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "latent_work.cuh"
 #include "tc_ptx.cuh"
 
 namespace {
 
 constexpr int kRows = 8, kKeys = 32, kThreads = 256, kRope = 64;
-constexpr float kLow = -3.0e38f;  // running maximum before the first key
-constexpr int kMaxSplits = 64;
+using sv::kLow;
+constexpr int kMaxSplits = 128, kGrain = 16;  // ranges of keys, and what their lengths are multiples of
 
 // A partial: LAT unnormalised sums, the maximum (log2 units), the sum of P.
 constexpr int partial_floats(int lat) { return lat + 4; }
@@ -35,7 +37,7 @@ __global__ void __launch_bounds__(kThreads)
                        float *__restrict__ out, float *__restrict__ ws, int N, int hq, int s_max, int max_prefix,
                        int chunk, float scale_log2, int32_t *status, const sv::KvPages pg) {
   constexpr int D = LAT + kRope, PER = D / 32, VD = LAT / kThreads;
-  __shared__ float s_q[kRows][D];
+  __shared__ alignas(16) float s_q[kRows][D];
   __shared__ float s_p[kRows][kKeys];
   __shared__ float s_alpha[kRows], s_l[kRows], s_m[kRows];
   __shared__ int s_row[kKeys];  // cache row of a prefix key, -1 outside the pool
@@ -43,13 +45,17 @@ __global__ void __launch_bounds__(kThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   sv::ptx::grid_dep_launch();
   const int P = prefix_len[b];
+  // (the queries before anything waits for the length)
+#pragma unroll
+  for (int i = 0; i < kRows * D / 4 / kThreads + 1; ++i) {
+    const int e = threadIdx.x + i * kThreads, r = e / (D / 4);
+    if (r >= kRows) break;
+    reinterpret_cast<float4 *>(&s_q[0][0])[e] =
+        row0 + r < R ? reinterpret_cast<const float4 *>(q + ((int64_t)b * R + row0) * D)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   if (P < 0 || P > max_prefix || P > s_max) {
     if (threadIdx.x == 0) sv::report(status, SPEC_DEV_CAPACITY);
     return;
-  }
-  for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
-    const int r = e / D, d = e - r * D;
-    s_q[r][d] = row0 + r < R ? q[((int64_t)b * R + row0 + r) * D + d] : 0.f;
   }
   const int words = SPEC_MASK_WORDS(N), last = P + N;
   const int k0 = split * chunk, k1 = min(last, k0 + chunk);
@@ -166,40 +172,57 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// One CTA a row: the key ranges' sums, weighted by their maxima.
+// One CTA a row: the key ranges' sums, weighted by their maxima; eight in
+// flight (a loop of one after another: 12 us more with 63 ranges).
 template <int LAT>
 __global__ void __launch_bounds__(128)
     latent_simt_join_kernel(const float *__restrict__ ws, float *__restrict__ out, const int32_t *__restrict__ prefix_len,
                             int R, int splits, int s_max, int max_prefix) {
+  __shared__ float s_a[kMaxSplits], s_l;
   sv::ptx::grid_dep_wait();
   const int64_t row = blockIdx.x;
   const int P = prefix_len[row / R];
-  if (P < 0 || P > max_prefix || P > s_max) return;  // reported by the main kernel
   const float *w = ws + row * splits * partial_floats(LAT);
-  float m = kLow, l = 0.f, acc[LAT / 128];
-#pragma unroll
-  for (int v = 0; v < LAT / 128; ++v) acc[v] = 0.f;
-  for (int s = 0; s < splits; ++s) m = fmaxf(m, w[(int64_t)s * partial_floats(LAT) + LAT]);
-  for (int s = 0; s < splits; ++s) {
-    const float *p = w + (int64_t)s * partial_floats(LAT);
-    const float a = exp2f(p[LAT] - m);
-    l += a * p[LAT + 1];
-#pragma unroll
-    for (int v = 0; v < LAT / 128; ++v) acc[v] = fmaf(a, p[threadIdx.x + 128 * v], acc[v]);
+  if (threadIdx.x < 32) {
+    const float l = sv::latent_weights<kMaxSplits>(splits, s_a, [&](int s) {
+      return *reinterpret_cast<const float2 *>(w + (int64_t)s * partial_floats(LAT) + LAT);
+    });
+    if (threadIdx.x == 0) s_l = l;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __syncthreads();
+  if (P < 0 || P > max_prefix || P > s_max) return;  // reported by the main kernel
+  constexpr int V = LAT / 128, B = 8;
+  float acc[V];
 #pragma unroll
-  for (int v = 0; v < LAT / 128; ++v) out[row * LAT + threadIdx.x + 128 * v] = acc[v] * inv;
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int s0 = 0; s0 < splits; s0 += B) {
+    float x[B][V];
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (s0 + i < splits) x[i][v] = w[(int64_t)(s0 + i) * partial_floats(LAT) + threadIdx.x + 128 * v];
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (s0 + i < splits) acc[v] = fmaf(s_a[s0 + i], x[i][v], acc[v]);
+  }
+  const float inv = s_l == 0.f ? 0.f : 1.f / s_l;
+#pragma unroll
+  for (int v = 0; v < V; ++v) out[row * LAT + threadIdx.x + 128 * v] = acc[v] * inv;
 }
 
-// Ranges of keys: enough CTAs for the GPU's 152 SMs twice, no range under a
-// tile.
+// Ranges of keys: as many as fill the GPU's 152 SMs once (LAT 256: two CTAs an
+// SM, by their registers; a few more than that would run a second time round:
+// 16 heads, 2000 keys 15 us in 126 CTAs, 27 in 252).
 int splits_of(const SvLatentShape &s, int *chunk) {
   const long long ctas = (long long)s.batch * ((s.n_nodes * s.hq + kRows - 1) / kRows);
-  const int tiles = (s.max_prefix + s.n_nodes + kKeys - 1) / kKeys;
-  long long n = (304 + ctas - 1) / ctas;
-  n = n > tiles ? tiles : n > kMaxSplits ? kMaxSplits : n;
-  *chunk = (tiles + (int)n - 1) / (int)n * kKeys;
+  const int tiles = (s.max_prefix + s.n_nodes + kGrain - 1) / kGrain;
+  long long n = (s.latent_dim == 512 ? 152 : 304) / ctas;
+  n = n > tiles ? tiles : n;
+  n = n > kMaxSplits ? kMaxSplits : n < 1 ? 1 : n;  // (what the join holds)
+  *chunk = (tiles + (int)n - 1) / (int)n * kGrain;
   return (s.max_prefix + s.n_nodes + *chunk - 1) / *chunk;
 }
 

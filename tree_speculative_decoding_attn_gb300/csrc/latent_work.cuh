@@ -221,20 +221,20 @@ __device__ __forceinline__ void latent_cut(const int4 *desc, int parts, int k, i
   }
 }
 // What the n parts of a row weigh (into a[]), and the sum of all their sums.
-// One warp.
-template <class Stats>
+// One warp; n <= MOST.
+template <int MOST, class Stats>
 __device__ __forceinline__ float latent_weights(int n, float *a, const Stats &stats) {
   const int lane = threadIdx.x & 31;
-  float2 ml[kMostParts / 32];
+  float2 ml[MOST / 32];
   float m = kLow, l = 0.f;
 #pragma unroll
-  for (int i = 0; i < kMostParts / 32; ++i) {
+  for (int i = 0; i < MOST / 32; ++i) {
     ml[i] = i * 32 + lane < n ? stats(i * 32 + lane) : make_float2(kLow, 0.f);
     m = fmaxf(m, ml[i].x);
   }
   m = warp_max(m);
 #pragma unroll
-  for (int i = 0; i < kMostParts / 32; ++i) {
+  for (int i = 0; i < MOST / 32; ++i) {
     const float w = exp2f(ml[i].x - m);
     if (i * 32 + lane < n) a[i * 32 + lane] = w;
     l = fmaf(w, ml[i].y, l);
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(128)
     return ws + (size_t)(i == 0 ? 2 * (part0 - 1) + 1 : 2 * (part0 - 1 + i)) * latent_slot_floats(LAT, ROWS);
   };
   for (int r = warp; r < rows; r += 4) {
-    const float l = latent_weights(d.z, s_a[r], [&](int p) {
+    const float l = latent_weights<kMostParts>(d.z, s_a[r], [&](int p) {
       return *reinterpret_cast<const float2 *>(part(p) + ROWS * (size_t)LAT + 2 * (lr0 + r));
     });
     if ((threadIdx.x & 31) == 0) s_l[r] = l;
