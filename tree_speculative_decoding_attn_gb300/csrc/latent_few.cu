@@ -1,5 +1,6 @@
-// Tree attention over a cache of latent vectors for few rows a sequence (bf16
-// in, float32 softmax and accumulation): a token of a few heads, a short chain.
+// Tree attention over a cache of latent vectors for few rows a sequence, or few
+// tiles in all (bf16 in, float32 softmax and accumulation): a token of a few
+// heads, a short chain, a short cache.
 //
 //   x_j = scale q . c_j over the LAT + 64 dims,  out = sum_j softmax(x)_j c_j[:LAT].
 // With 16 rows a key's 1152 bytes meet 35 kflop: HBM-bound, and a tcgen05 tile
@@ -15,11 +16,11 @@
 //   PV: warp i takes dims [64 i, +64) (LAT 256: 32), 64 keys deep
 // Two barriers a tile; the load of the tile after next is issued behind the
 // first, when every warp is done with the tile before.  A tile takes 2700 to
-// 3000 cycles, HBM's share of one 3150: batch 64 of 16 heads over 4096 rows 60
-// us (5.0 TB/s; 55 without the join), one sequence of 5000 rows 12.2 (start,
-// one tile a CTA, join).
-// Work: equal ranges of all (sequence, 16 rows) units, a CTA each; cut units
-// leave float32 partials for a second kernel.  Every wait is bounded.
+// 3000 cycles, HBM's share of one 3150: batch 64 of 16 heads over 4096 rows 59
+// us (5.1 TB/s), one sequence of 5000 rows 12.2 to 12.7 (start 4, one tile a CTA
+// 2, partial 1, join 4).
+// Work: equal ranges of all (sequence, 16 rows) units, or whole units, a CTA each;
+// cut units leave float32 partials for a second kernel.  Every wait is bounded.
 #include <math.h>
 
 #include "common.cuh"

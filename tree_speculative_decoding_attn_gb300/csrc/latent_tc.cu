@@ -35,14 +35,15 @@
 // (lanes r and r + 64 of two warps share row r).  Two S buffers: the softmax of
 // a tile runs under the next tile's S and the last one's PV.
 // Work: all (sequence, 128-row tile) units, each its tree tiles and then its
-// prefix tiles of 128 keys, are cut into one equal range a pair; units cut
-// between pairs leave float32 partials that a second kernel joins.
+// prefix tiles of 128 keys, go whole to the pairs or are cut into one equal
+// range a pair; units cut between pairs leave float32 partials that a second
+// kernel joins.
 // What bounds it: a tile's MMAs are 2258 cycles, its shared-memory traffic
 // (operands 245 KB, TMA 104, P 16) 2850 at 128 bytes a cycle, and it takes
-// about 3000; 32 trees of 32 nodes x 64 heads over 4096 rows: 438-485 us, 1.2 to
-// 1.34 PFLOP/s, at 1370 W, where the power limit holds the clock at 1740 MHz.
-// One token of 64 heads, batch 64 over 4096 rows: 84 us, of them 52 at 6 TB/s
-// in the tiles, the rest start, epilogues and the join.
+// 2800 to 3200; 32 trees of 32 nodes x 64 heads over 4096 rows: 405-445 us, 1.32
+// to 1.46 PFLOP/s, at 1370 W, where the power limit holds the clock at 1740 MHz.
+// One token of 64 heads, batch 64 over 4096 rows: 73 us, of them 58 at 5.2 TB/s
+// in the tiles of 64 pairs, the rest start (6.5) and epilogue (3.5).
 // Tried and not kept: one warp for all MMAs (4400 cycles a tile: its waits are
 // not covered), P announced through a warp that forwards at the cluster's
 // scope (1400 cycles a hand-off, 540 us), S held back behind the last PV (490
@@ -65,7 +66,7 @@ constexpr int kBN = 128, kRope = 64, kThreads = 384, kPairs = 76;
 constexpr uint32_t kPiece = 64 * 128;  // 64 rows (or keys) x 64 elements, 128-byte swizzle
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr int kSegW = 3;      // a unit's fixed cost, in tiles (ragged trees: 1 143 us, 2 132, 3 128, 5 129)
-constexpr int kJoinW = 16;    // what a join costs, in tiles
+constexpr int kJoinW = 6;     // what a join costs, in tiles
 using sv::kLow;
 constexpr float kTau = 16.f;  // the maximum moves when a tile exceeds it by more than 2^kTau
 

@@ -52,13 +52,14 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // first range end inside a cut unit names it and its parts (sequence, unit,
 // parts, 1).  status (may be null): refused prefix lengths are reported.
 // Where whole units share out nearly as evenly, none is cut: the longest part
-// is then no more than `join` weights (about what partials and their join cost)
-// and 1/32 above the mean.  us cut / whole: one token of 64 heads, batch 64, 4096
-// keys 84 / 74, 500 keys 35 / 23; 64 heads x 32 nodes, 4 trees over 4096 keys 80
-// / 65, 32 trees 439 / 416, over 8192 keys 902 / 782 (whole units of a sequence
-// run side by side, in L2); one token of 16 heads, batch 140, 2048 keys 68 / 63.
-// Not whole: 64 heads x 9 nodes, 8 trees over 6000 keys 73 / 89; one token of 64
-// heads, 64 sequences of 1000 to 8000 keys 91 / 98.
+// is then no more than a fifth and `join` weights (about what partials and their
+// join cost) above the mean.  us cut / whole: one token of 64 heads, batch 64, 4096
+// keys 84 / 72, 500 keys 35 / 21; 64 heads x 32 nodes, 4 trees over 4096 keys 80
+// / 60, 32 trees 439 / 406, over 8192 keys 902 / 790 (whole units of a sequence
+// run side by side, in L2); one token of 16 heads, batch 140, 2048 keys 68 / 61.
+// Not whole: 64 heads x 9 nodes, 8 trees over 6000 keys 68 / 89; one token of 64
+// heads, 64 sequences of 1000 to 8000 keys 86 / 98; 32 heads, 16 sequences of
+// 1000 keys 19 / 23.
 template <class Work>
 __device__ __forceinline__ LatentRange latent_range(const Work &w, int part, int parts, int fixed, int join, int4 *desc,
                                                     int32_t *status) {
@@ -95,7 +96,7 @@ __device__ __forceinline__ LatentRange latent_range(const Work &w, int part, int
   int T;
   long long mine, first;
   const long long units = (long long)w.batch * w.RT, each = units <= parts ? 1 : quotient(units + parts - 1, parts);
-  if (each * most * parts <= total + (total >> 5) + (long long)join * parts) {  // whole units, `each` a part
+  if (5 * each * most * parts <= 6 * total + 5ll * join * parts) {  // whole units, `each` a part
     const long long i0 = each * part, i1 = i0 + each;
     if (desc && lane == 0) *desc = make_int4(0, 0, 0, 0);
     if (i0 >= units) return r;

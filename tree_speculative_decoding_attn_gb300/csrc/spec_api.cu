@@ -658,14 +658,24 @@ static int latent_check(const SvLatentShape &s, int rope_dim) {
     return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
 }
-// bf16 rows a sequence for the kernel of few rows, whose tile they fill.  us
-// there / on SM pairs (latent 512): 16 rows, 5000 keys 12.2 / 15.6, batch 64
-// over 4096 keys 60 / 71; 32 rows 15.3 / 17.1 and 103 / 75.
-static const int kFewLatentRows = 16;
+// The kernel of few rows takes bf16 calls of up to 16 rows a sequence, whose tile
+// they fill, and calls of few tiles (16 rows x 64 keys, at max_prefix: seven a CTA,
+// three at latent 256, in no more units than CTAs), whose steps wait for one another
+// less there.  us there / on SM pairs (latent 512): 16 rows over 4096 keys, batch 64
+// 59 / 70; 64 rows over 300 11 / 16, 128 over 5000 (640 tiles) 17 / 20, 32 over
+// 32768 (1026) 23 / 35; 128 over 1500, batch 4 (800) 19 / 18; 32 over 500, batch
+// 64 (1152) 22 / 20, over 4096 102 / 71; 1920 over 64, batch 4 (480 units) 27 / 15;
+// latent 256, 128 over 2000 (264) 11 / 14, 960 over 500 (540) 14 / 13.
+static bool few_latent_rows(const SvLatentShape &s) {
+  const int rows = s.n_nodes * s.hq;
+  const long long units = (long long)s.batch * ((rows + 15) / 16);
+  const long long tiles = units * ((s.max_prefix + 63) / 64 + (s.n_nodes + 63) / 64);
+  return rows <= 16 || (units <= 152 && tiles <= (s.latent_dim == 512 ? 1064 : 456));
+}
 static size_t latent_ws_bytes(const SvLatentShape &s) {
-  return s.dtype != SPEC_BF16                   ? sv_latent_simt_ws_bytes(s)
-         : s.n_nodes * s.hq <= kFewLatentRows ? sv_latent_few_ws_bytes(s)
-                                              : sv_latent_tc_ws_bytes(s);
+  return s.dtype != SPEC_BF16   ? sv_latent_simt_ws_bytes(s)
+         : few_latent_rows(s) ? sv_latent_few_ws_bytes(s)
+                              : sv_latent_tc_ws_bytes(s);
 }
 
 size_t tree_attn_latent_workspace_bytes(int dtype, int batch, int n_nodes, int hq, int latent_dim, int rope_dim,
@@ -686,9 +696,7 @@ static int latent_run(const SvLatentShape &s, int rope_dim, const void *q, const
   if (s.max_prefix > s.s_max) return SPEC_ERR_CAPACITY;
   const size_t need = latent_ws_bytes(s);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return SPEC_ERR_CAPACITY;
-  const auto run = s.dtype != SPEC_BF16                   ? sv_latent_simt
-                   : s.n_nodes * s.hq <= kFewLatentRows ? sv_latent_few
-                                                        : sv_latent_tc;
+  const auto run = s.dtype != SPEC_BF16 ? sv_latent_simt : few_latent_rows(s) ? sv_latent_few : sv_latent_tc;
   return run(s, q, cache, tree, prefix_len, anc_mask, out, scale, workspace, dev_status, cs(stream));
 }
 
