@@ -629,32 +629,35 @@ def kv_pages_slots(block_table, prefix_len, new_len, offsets, slots, block_size,
     packed one sequence behind the other, lie: offsets [B + 1], slots [room]
     and positions [room] (optional), all int32; -1 behind the last token."""
     B, mb = block_table.shape
-    i32, room = torch.int32, slots.shape
+    i32, room, each = torch.int32, slots.numel(), (B,)
     i, stream = _device(block_table)
-    _check("kv_pages_slots", load().kv_pages_slots(
-        _ptr(block_table, i, i32, (B, mb)), _ptr(prefix_len, i, i32, (B,)), _ptr(new_len, i, i32, (B,)), B, mb,
-        int(block_size), int(num_blocks), slots.numel(), _ptr(offsets, i, i32, (B + 1,)), _ptr(slots, i, i32, (slots.numel(),)),
-        None if positions is None else _ptr(positions, i, i32, room), _word(dev_status, i), stream))
+    code = load().kv_pages_slots(
+        _ptr(block_table, i, i32, (B, mb)), _ptr(prefix_len, i, i32, each), _ptr(new_len, i, i32, each), B, mb, block_size,
+        num_blocks, room, _ptr(offsets, i, i32, (B + 1,)), _ptr(slots, i, i32, (room,)),
+        None if positions is None else _ptr(positions, i, i32, (room,)), _word(dev_status, i), stream)
+    if code != OK:
+        raise SpecError("kv_pages_slots", code)
 
 
-def _slot_rows(name, pages, slots, rows, dev_status):
-    nb, Hkv, bs, D = pages.shape
-    T, dt = slots.numel(), pages.dtype
+def _slot_rows(name, call, pages, slots, rows, dev_status):
+    shape, T, dt = pages.shape, slots.numel(), pages.dtype
+    nb, Hkv, bs, D = shape
     i, stream = _device(pages)
-    _check(name, getattr(load(), name)(
-        _ptr(pages, i, dt, pages.shape), _ptr(slots, i, torch.int32, (T,)), _ptr(rows, i, dt, (T, Hkv, D)),
-        pages.element_size(), T, Hkv, D, bs, nb, _word(dev_status, i), stream))
+    code = call(_ptr(pages, i, dt, shape), _ptr(slots, i, torch.int32, (T,)), _ptr(rows, i, dt, (T, Hkv, D)),
+                pages.element_size(), T, Hkv, D, bs, nb, _word(dev_status, i), stream)
+    if code != OK:
+        raise SpecError(name, code)
 
 
 def kv_slots_write(pages, slots, rows, dev_status=None):
     """rows [T, Hkv, D] into their slots of one pool [num_blocks, Hkv,
     block_size, D]; negative slots are left out."""
-    _slot_rows("kv_slots_write", pages, slots, rows, dev_status)
+    _slot_rows("kv_slots_write", load().kv_slots_write, pages, slots, rows, dev_status)
 
 
 def kv_slots_read(pages, slots, rows, dev_status=None):
     """rows [T, Hkv, D] out of their slots; zeros where a slot is negative."""
-    _slot_rows("kv_slots_read", pages, slots, rows, dev_status)
+    _slot_rows("kv_slots_read", load().kv_slots_read, pages, slots, rows, dev_status)
 
 
 ROPE_DIM = 64    # rotary elements at the end of a latent row
