@@ -482,22 +482,32 @@ __global__ void __launch_bounds__(256)
   const int z = unit / hq, qi = (int)(gridDim.x / (per * hq) - 1 - z) * kTiles * 128 + row;
   if (qi >= q_end - q_first) return;
   const float *slot = ws + slot_floats() * ((((size_t)z * gridDim.y + b) * hq + head) * parts);
+  auto stat = [&](int p) {  // maximum, sum
+    return p < parts ? *reinterpret_cast<const float2 *>(slot + p * slot_floats() + 256 * kD + 2 * row) : make_float2(kLow, 0.f);
+  };
   float m = kLow, l = 0.f;
-  for (int p = lane; p < parts; p += 32) m = fmaxf(m, slot[p * slot_floats() + 256 * kD + 2 * row]);
+  for (int p = lane; p < parts; p += 32) m = fmaxf(m, stat(p).x);
   m = sv::warp_max(m);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int p = 0; p < parts; ++p) {
-    const float2 ml = *reinterpret_cast<const float2 *>(slot + p * slot_floats() + 256 * kD + 2 * row);
-    if (ml.y == 0.f) continue;
-    const float4 x = *reinterpret_cast<const float4 *>(slot + p * slot_floats() + row * kD + lane * 4);
-    const float a = exp2f(ml.x - m);
-    l = fmaf(a, ml.y, l);
-    acc.x = fmaf(a, x.x, acc.x);
-    acc.y = fmaf(a, x.y, acc.y);
-    acc.z = fmaf(a, x.z, acc.z);
-    acc.w = fmaf(a, x.w, acc.w);
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    const float2 ml = stat(p0 + lane);
+    const float a = ml.y == 0.f ? 0.f : exp2f(ml.x - m);  // (a part of nothing has no sums)
+    l += a * ml.y;
+    constexpr int B = 8;  // parts in flight
+    for (int i0 = 0; i0 < min(32, parts - p0); i0 += B) {
+      float4 x[B];
+      float w[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        w[i] = __shfl_sync(0xffffffffu, a, i0 + i);
+        if (w[i] != 0.f) x[i] = *reinterpret_cast<const float4 *>(slot + (p0 + i0 + i) * slot_floats() + row * kD + lane * 4);
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i)
+        if (w[i] != 0.f) sv::fma4(acc, w[i], x[i]);
+    }
   }
+  l = sv::warp_sum(l);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint2 *>(out + ((int64_t)(q_first + qi) * hq + head) * kD + lane * 4) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
