@@ -23,11 +23,12 @@
 // first to be done, K(j + 2) follows V(j)), and two pieces for rotary columns.
 // What bounds it: two tiles' MMAs are 2560 cycles a key tile (2660 by their
 // shared-memory traffic), the chain S, softmax (1600), PV with its hand-offs
-// 3000 to 3300.  8192 tokens of 32 heads 440 to 465 us, 1.48 to 1.56 PFLOP/s, at
+// 3000 to 3300.  8192 tokens of 32 heads 432 to 465 us, 1.48 to 1.59 PFLOP/s, at
 // the power limit (1365 W).  Steps: one MMA warp and eight softmax warps 4680
 // cycles, 527 us; a warp a tile 4060, 491; S in turns 3850, 483; P in two parts
 // 476; V no longer waiting for its one place 470; PV's end and the next S in
-// one issue 463; one wait for several barriers 440.  Without the exponentials
+// one issue 463; one wait for several barriers 440; outputs through shared memory
+// 432.  Without the exponentials
 // (timing only) the same: not a limit of the exponential unit.  Not kept: scalar
 // instead of two-wide float32 arithmetic (+4 %), P in parts of 48 and 16 or 16
 // and 48 keys (+4 %), S(j + 1) behind a wait for PV(j) (+7 %).
@@ -105,9 +106,11 @@ template <int N> __device__ __forceinline__ bool wait(Bars *bars, const Phase (&
 }
 using sv::pack_bf16;
 
-// A partial: 256 rows of 128 float32 sums, then 256 pairs (maximum in log2
-// units, sum).
+// A partial: 256 rows of 128 float32 sums, four dims by four ([32][256][4]: a
+// thread that writes them holds a row, and a warp's store is one piece), then
+// 256 pairs (maximum in log2 units, sum).
 __host__ __device__ constexpr size_t slot_floats() { return 256 * (size_t)(kD + 2); }
+__device__ __forceinline__ int slot_at(int row, int dim) { return ((dim >> 2) * 256 + row) * 4; }
 
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -424,13 +427,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(o_addr + c * 32, v);
           tmem_wait_ld();
           if (qi >= n) continue;
-          uint4 *dst = reinterpret_cast<uint4 *>(slot + row * kD + h * 64 + c * 32);
+          float *dst = slot + slot_at(row, h * 64 + c * 32);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4 *>(dst + e * 4 * 256) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
       } else {
         const float inv = l == 0.f ? 0.f : 1.f / l;  // a query that sees nothing: zeros
-        uint4 *o = reinterpret_cast<uint4 *>(out + ((int64_t)(q_first + qi) * hq + head) * kD + h * 64);
+        // rows to pieces of 128 bytes of a row (32 lanes of 32 rows would touch 32
+        // lines with each store), where this tile's Q lay
+        uint8_t *st = sQ + i * kQBytes + ((warp - 4) & 7) * 4096;
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           uint32_t v[32];
@@ -438,7 +444,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(o_addr + c * 32, v);
             tmem_wait_ld();
           }
-          if (qi >= n) continue;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint4 u = make_uint4(0, 0, 0, 0);
@@ -448,8 +453,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               u.z = pack_bf16(__uint_as_float(v[8 * e + 4]) * inv, __uint_as_float(v[8 * e + 5]) * inv);
               u.w = pack_bf16(__uint_as_float(v[8 * e + 6]) * inv, __uint_as_float(v[8 * e + 7]) * inv);
             }
-            o[c * 4 + e] = u;
+            *reinterpret_cast<uint4 *>(st + lane * 128 + (((c * 4 + e) ^ (lane & 7)) << 4)) = u;
           }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int to = e * 4 + (lane >> 3), piece = lane & 7, qt = qi - lane + to;  // row among the warp's 32
+          if (qt < n)
+            *reinterpret_cast<uint4 *>(out + ((int64_t)(q_first + qt) * hq + head) * kD + h * 64 + piece * 8) =
+                *reinterpret_cast<const uint4 *>(st + to * 128 + ((piece ^ (to & 7)) << 4));
         }
       }
     }
@@ -465,52 +478,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of a unit: block (8 queries, unit), a warp a query, a lane
-// four dims.
+// Joins the parts of a unit: block (8 queries, unit), the queries side by side as
+// they lie, a thread four dims of one.
 __global__ void __launch_bounds__(256)
     prompt_join_kernel(const float *__restrict__ ws, const int32_t *__restrict__ q_off,
                        const int32_t *__restrict__ kv_off, __nv_bfloat16 *__restrict__ out, int hq, int parts,
                        int total_q, int total_kv, int max_q) {
+  __shared__ float s_a[8][sv::kMostParts], s_l[8];
+  static_assert(sv::kMostParts >= kSms, "a part a CTA at most");
   grid_dep_wait();
   const int per = 256 / 8;  // blocks of a unit
-  const int unit = blockIdx.x / per, row = (blockIdx.x - unit * per) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int head = unit % hq, b = blockIdx.y;
+  const int unit = blockIdx.x / per, row0 = (blockIdx.x - unit * per) * 8, head = unit % hq, b = blockIdx.y;
   const int q_first = q_off[b], q_end = q_off[b + 1], k_first = kv_off[b], k_end = kv_off[b + 1];
   if (q_first < 0 || k_first < 0 || q_end < q_first || k_end < k_first || q_end > total_q || k_end > total_kv ||
       q_end - q_first > max_q)
     return;  // reported by the main kernel
-  const int z = unit / hq, qi = (int)(gridDim.x / (per * hq) - 1 - z) * kTiles * 128 + row;
-  if (qi >= q_end - q_first) return;
+  const int z = unit / hq, qi0 = (int)(gridDim.x / (per * hq) - 1 - z) * kTiles * 128 + row0;
+  if (qi0 >= q_end - q_first) return;
   const float *slot = ws + slot_floats() * ((((size_t)z * gridDim.y + b) * hq + head) * parts);
-  auto stat = [&](int p) {  // maximum, sum
-    return p < parts ? *reinterpret_cast<const float2 *>(slot + p * slot_floats() + 256 * kD + 2 * row) : make_float2(kLow, 0.f);
-  };
-  float m = kLow, l = 0.f;
-  for (int p = lane; p < parts; p += 32) m = fmaxf(m, stat(p).x);
-  m = sv::warp_max(m);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p0 = 0; p0 < parts; p0 += 32) {
-    const float2 ml = stat(p0 + lane);
-    const float a = ml.y == 0.f ? 0.f : exp2f(ml.x - m);  // (a part of nothing has no sums)
-    l += a * ml.y;
-    constexpr int B = 8;  // parts in flight
-    for (int i0 = 0; i0 < min(32, parts - p0); i0 += B) {
-      float4 x[B];
-      float w[B];
-#pragma unroll
-      for (int i = 0; i < B; ++i) {
-        w[i] = __shfl_sync(0xffffffffu, a, i0 + i);
-        if (w[i] != 0.f) x[i] = *reinterpret_cast<const float4 *>(slot + (p0 + i0 + i) * slot_floats() + row * kD + lane * 4);
-      }
-#pragma unroll
-      for (int i = 0; i < B; ++i)
-        if (w[i] != 0.f) sv::fma4(acc, w[i], x[i]);
-    }
+  {
+    const int r = threadIdx.x >> 5;
+    const bool there = qi0 + r < q_end - q_first;
+    const float l = sv::latent_weights<sv::kMostParts>(parts, s_a[r], [&](int p) {
+      const float2 ml = there ? *reinterpret_cast<const float2 *>(slot + p * slot_floats() + 256 * kD + 2 * (row0 + r))
+                              : make_float2(0.f, 0.f);
+      return ml.y == 0.f ? make_float2(-INFINITY, 0.f) : ml;  // (a part of nothing: no weight, and no sums to read)
+    });
+    if ((threadIdx.x & 31) == 0) s_l[r] = l;
   }
-  l = sv::warp_sum(l);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2 *>(out + ((int64_t)(q_first + qi) * hq + head) * kD + lane * 4) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  __syncthreads();
+  const int r = threadIdx.x & 7, dim = (threadIdx.x >> 3) * 4;
+  if (qi0 + r >= q_end - q_first) return;
+  constexpr int B = 8;  // parts in flight
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = 0; p0 < parts; p0 += B) {
+    float4 x[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+      if (p0 + i < parts && s_a[r][p0 + i] != 0.f)
+        x[i] = *reinterpret_cast<const float4 *>(slot + (p0 + i) * slot_floats() + slot_at(row0 + r, dim));
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+      if (p0 + i < parts && s_a[r][p0 + i] != 0.f) sv::fma4(acc, s_a[r][p0 + i], x[i]);
+  }
+  sv::store4(out + ((int64_t)(q_first + qi0 + r) * hq + head) * kD + dim, acc, s_l[r]);
 }
 
 int q_tiles_of(const SvPromptShape &s) {
