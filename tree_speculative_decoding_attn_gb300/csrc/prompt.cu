@@ -28,10 +28,10 @@
 // cycles, 527 us; a warp a tile 4060, 491; S in turns 3850, 483; P in two parts
 // 476; V no longer waiting for its one place 470; PV's end and the next S in
 // one issue 463; one wait for several barriers 440; outputs through shared memory
-// 432.  Without the exponentials
-// (timing only) the same: not a limit of the exponential unit.  Not kept: scalar
-// instead of two-wide float32 arithmetic (+4 %), P in parts of 48 and 16 or 16
-// and 48 keys (+4 %), S(j + 1) behind a wait for PV(j) (+7 %).
+// 432.  Without the exponentials (timing only) the same: not a limit of the
+// exponential unit.  Not kept: scalar instead of two-wide float32 arithmetic (+4
+// %), P in parts of 48 and 16 or 16 and 48 keys (+4 %), S(j + 1) behind a wait
+// for PV(j) (+7 %).
 // TMEM columns: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512).
 // Longest tiles are launched first.  Where CTAs are fewer than SMs (a chunk of
 // few heads behind a long kept beginning) the keys are cut into parts, a CTA
