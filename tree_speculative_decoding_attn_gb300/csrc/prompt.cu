@@ -194,22 +194,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_expect_tx(&bars->kfull[j & 1], 3 * kPiece);
       tma_load_2d(sR + (j & 1) * kPiece, &tm_r, 0, k_first + (j0 + j) * kBN, &bars->kfull[j & 1]);
     };
+    auto load_q = [&](int i) {
+      if (tiles[i] == 0) return;
+      mbar_expect_tx(&bars->q[i], kQBytes);
+      for (int c = 0; c < 3; ++c)
+        tma_load_3d(sQ + i * kQBytes + c * kPiece, &tm_q, c * 64, head, q_first + q0 + i * 128, &bars->q[i]);
+    };
     for (int j = 0; ok && j < all; ++j) {
       const int row = k_first + (j0 + j) * kBN;
       if (j > 1 && !(ok = wait(bars, &bars->vempty[j & 1], ((j >> 1) & 1) ^ 1))) break;
       if (me) {
-        if (j == 0) {
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i)
-            if (tiles[i] > 0) {
-              mbar_expect_tx(&bars->q[i], kQBytes);
-              for (int c = 0; c < 3; ++c)
-                tma_load_3d(sQ + i * kQBytes + c * kPiece, &tm_q, c * 64, head, q_first + q0 + i * 128, &bars->q[i]);
-            }
-        }
+        if (j == 0) load_q(0);
         if (j < 2) rope(j);
         tma_load_3d(ring + at * kPair, &tm_k, 0, head, row, &bars->kfull[j & 1]);
         tma_load_3d(ring + at * kPair + kPiece, &tm_k, 64, head, row, &bars->kfull[j & 1]);
+        if (j == 0) load_q(1);  // (S of tile 0 is first)
       }
       ++k_done;
       __syncwarp();
