@@ -17,8 +17,8 @@
 // Two barriers a tile; the load of the tile after next is issued behind the
 // first, when every warp is done with the tile before.  A tile takes 2700 to
 // 3000 cycles, HBM's share of one 3150: batch 64 of 16 heads over 4096 rows 59
-// us (5.1 TB/s), one sequence of 5000 rows 12.2 to 12.7 (start 4, one tile a CTA
-// 2, partial 1, join 4).
+// us (5.1 TB/s), one sequence of 5000 rows 11.4 (start 4, one tile a CTA 2, partial
+// 1, join 3).
 // Work: equal ranges of all (sequence, 16 rows) units, or whole units, a CTA each;
 // cut units leave float32 partials for a second kernel.  Every wait is bounded.
 #include <math.h>

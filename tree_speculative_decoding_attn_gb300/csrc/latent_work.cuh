@@ -255,7 +255,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v, float 
 
 // Joins the parts of cut units, a thread four dims of a row at a time.
 // BY_ROW (FORM 8, and partials of 16 rows): block (row, cut unit, LAT / FORM
-// dims), eight parts in flight, shared out over groups of threads whose sums go
+// dims), ten parts in flight, shared out over groups of threads whose sums go
 // through shared memory.  Otherwise block (8 rows, cut unit, FORM 1: 64 dims, FORM
 // 0: all), the rows side by side as they lie.
 template <int LAT, int ROWS, int FORM>
@@ -285,27 +285,35 @@ __global__ void __launch_bounds__(128)
   auto part = [&](int i) {
     return ws + (size_t)(i == 0 ? 2 * (part0 - 1) + 1 : 2 * (part0 - 1 + i)) * latent_slot_floats(LAT, ROWS);
   };
-  for (int r = warp; r < rows; r += 4) {
-    const float l = latent_weights<kMostParts>(d.z, s_a[r], [&](int p) {
-      return *reinterpret_cast<const float2 *>(part(p) + ROWS * (size_t)LAT + 2 * (lr0 + r));
-    });
-    if ((threadIdx.x & 31) == 0) s_l[r] = l;
-  }
-  __syncthreads();
+  // (beside the first of the sums)
+  auto weights = [&]() {
+    for (int r = warp; r < rows; r += 4) {
+      const float l = latent_weights<kMostParts>(d.z, s_a[r], [&](int p) {
+        return *reinterpret_cast<const float2 *>(part(p) + ROWS * (size_t)LAT + 2 * (lr0 + r));
+      });
+      if ((threadIdx.x & 31) == 0) s_l[r] = l;
+    }
+    __syncthreads();
+  };
   __nv_bfloat16 *o = out + ((int64_t)d.x * R + d.y * ROWS + lr0) * LAT;
   auto load = [&](int p, int r, int dim) {
     return __ldcs(reinterpret_cast<const float4 *>(part(p) + latent_at<LAT, ROWS>(lr0 + r, dim)));
   };
   if constexpr (BY_ROW) {
-    constexpr int DIMS = LAT / FORM, PER = DIMS / 4, GROUPS = 128 / PER, B = 8;  // B: loads in flight
+    constexpr int DIMS = LAT / FORM, PER = DIMS / 4, GROUPS = 128 / PER, B = 10;  // B: loads in flight
     __shared__ float4 s_acc[GROUPS][PER];
     const int group = threadIdx.x / PER, at = threadIdx.x % PER, dim = blockIdx.z * DIMS + at * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = group; p0 < d.z; p0 += B * GROUPS) {
-      float4 x[B];
+    float4 x[B];
+    auto fetch = [&](int p0) {
 #pragma unroll
       for (int i = 0; i < B; ++i)
         if (p0 + i * GROUPS < d.z) x[i] = load(p0 + i * GROUPS, 0, dim);
+    };
+    fetch(group);
+    weights();
+    for (int p0 = group; p0 < d.z; p0 += B * GROUPS) {
+      if (p0 != group) fetch(p0);
 #pragma unroll
       for (int i = 0; i < B; ++i)
         if (p0 + i * GROUPS < d.z) fma4(acc, s_a[0][p0 + i * GROUPS], x[i]);
@@ -321,17 +329,21 @@ __global__ void __launch_bounds__(128)
   } else {
     constexpr int NI = FORM == 1 ? 1 : LAT / 64, B = FORM == 1 ? 8 : 2;  // pieces of a thread; parts in flight
     const int r = threadIdx.x & 7, dim0 = blockIdx.z * 64 + (threadIdx.x >> 3) * 4;
-    if (r >= rows) return;
-    float4 acc[NI];
+    float4 acc[NI], x[B][NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p = 0; p < d.z; p += B) {
-      float4 x[B][NI];
+    auto fetch = [&](int p) {
 #pragma unroll
       for (int h = 0; h < B; ++h)
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-          if (p + h < d.z) x[h][i] = load(p + h, r, dim0 + i * 64);
+          if (p + h < d.z && r < rows) x[h][i] = load(p + h, r, dim0 + i * 64);
+    };
+    fetch(0);
+    weights();
+    if (r >= rows) return;
+    for (int p = 0; p < d.z; p += B) {
+      if (p > 0) fetch(p);
 #pragma unroll
       for (int h = 0; h < B; ++h)
 #pragma unroll
