@@ -40,7 +40,7 @@
 // kernel joins.
 // What bounds it: a tile's MMAs are 2258 cycles, its shared-memory traffic
 // (operands 245 KB, TMA 104, P 16) 2850 at 128 bytes a cycle, and it takes
-// 2800 to 3200; 32 trees of 32 nodes x 64 heads over 4096 rows: 405-445 us, 1.32
+// 2800 to 3200; 32 trees of 32 nodes x 64 heads over 4096 rows: 405-455 us, 1.29
 // to 1.46 PFLOP/s, at 1370 W, where the power limit holds the clock at 1740 MHz.
 // One token of 64 heads, batch 64 over 4096 rows: 73 us, of them 58 at 5.2 TB/s
 // in the tiles of 64 pairs, the rest start (6.5) and epilogue (3.5).
