@@ -11,7 +11,7 @@
 //   S_i(j) = Q_i K(j)^T  (N = 128, K = 192; the rotary columns of K are one
 //            64-column box shared by all heads)   768 cycles
 //   O_i   += P_i(j) V(j) (N = 128 dims, K = 128; P in TMEM over S)  512 cycles
-// P lies where S was, and S_i(j + 1) goes over it right behind PV_i(j).
+// P lies where S was, and S_i(j + 1) goes over it once PV_i(j) is done.
 //   warp 0      loads Q, K and V, and clears the V rows past the sequence's
 //               last key
 //   warps 1, 2  the MMAs of tile 0 and 1 (an elected thread each); their S in
@@ -23,15 +23,15 @@
 // first to be done, K(j + 2) follows V(j)), and two pieces for rotary columns.
 // What bounds it: two tiles' MMAs are 2560 cycles a key tile (2660 by their
 // shared-memory traffic), the chain S, softmax (1600), PV with its hand-offs
-// 3000 to 3300.  8192 tokens of 32 heads 432 to 465 us, 1.48 to 1.59 PFLOP/s, at
-// the power limit (1365 W).  Steps: one MMA warp and eight softmax warps 4680
-// cycles, 527 us; a warp a tile 4060, 491; S in turns 3850, 483; P in two parts
-// 476; V no longer waiting for its one place 470; PV's end and the next S in
-// one issue 463; one wait for several barriers 440; outputs through shared memory
-// 432.  Without the exponentials (timing only) the same: not a limit of the
-// exponential unit.  Not kept: scalar instead of two-wide float32 arithmetic (+4
-// %), P in parts of 48 and 16 or 16 and 48 keys (+4 %), S(j + 1) behind a wait
-// for PV(j) (+7 %).
+// 3100 to 3400.  8192 tokens of 32 heads 450 us, 1.53 PFLOP/s, 491 (1.40) under
+// sustained load, at the power limit (1365 W).  Steps: one MMA warp and eight
+// softmax warps 4680 cycles, 527 us; a warp a tile 4060, 491; S in turns 3850,
+// 483; P in two parts 476; V no longer waiting for its one place 470; one wait
+// for several barriers, outputs through shared memory, and S(j + 1) behind a
+// wait for PV(j) (without it 3 % less, 432 to 465, by an order of products that
+// nothing promises) 450.  Without the exponentials (timing only) the same: not a
+// limit of the exponential unit.  Not kept: scalar instead of two-wide float32
+// arithmetic (+4 %), P in parts of 48 and 16 or 16 and 48 keys (+4 %).
 // TMEM columns: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512).
 // Longest tiles are launched first.  Where CTAs are fewer than SMs (a chunk of
 // few heads behind a long kept beginning) the keys are cut into parts, a CTA
@@ -272,10 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return Phase{&bars->turn[1 - i], (uint32_t)(i == 1 ? j : j - 1) & 1};
     };
     for (int j = -1; ok && j < all; ++j) {
-      // P(j) V(j), and S(j + 1) right behind it.  S goes over P: the same thread
-      // has issued the products that read it before, and a CTA's products of one
-      // shape run one after another, in the order of their issue (the tests
-      // compare with a plain form at every size, and runs with one another).
+      // P(j) V(j), then S(j + 1) over P(j), behind a wait for the products that
+      // read it: products with different accumulators have no order that the
+      // instruction set promises, although one thread issues both.
       // P comes in two parts, the first 32 keys of each half of 64 and the rest.
       auto values = [&](int c) {
 #pragma unroll
@@ -285,36 +284,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       const bool mine = j >= 0 && j < nt, next = j + 1 < all;
-      if (j >= 0) {
-        const Phase v{&bars->vfull[j & 1], (uint32_t)(j >> 1) & 1};
-        if (mine) {
-          if (keys_left - j * kBN < kBN && !(ok = wait(bars, &bars->vclear, 0))) break;
-          if (!(ok = wait(bars, {v, {&bars->p[0][i], (uint32_t)j & 1}}))) break;
-          tc_fence_after();
-          if (elect_one()) values(0);
-          __syncwarp();
-          const Phase p{&bars->p[1][i], (uint32_t)j & 1};
-          if (!(ok = next ? wait(bars, {keys(j + 1), turn(j + 1), p}) : wait(bars, p.bar, p.parity))) break;
-          tc_fence_after();
-        } else if (!(ok = next ? wait(bars, {v, keys(j + 1), turn(j + 1)}) : wait(bars, v.bar, v.parity))) {
-          break;
-        }
-      } else if (next && !(ok = wait(bars, {keys(0), turn(0)}))) {
-        break;
-      }
-      if (elect_one()) {
-        if (mine) {
+      if (mine) {
+        if (keys_left - j * kBN < kBN && !(ok = wait(bars, &bars->vclear, 0))) break;
+        if (!(ok = wait(bars, {{&bars->vfull[j & 1], (uint32_t)(j >> 1) & 1}, {&bars->p[0][i], (uint32_t)j & 1}}))) break;
+        tc_fence_after();
+        if (elect_one()) values(0);
+        __syncwarp();
+        if (!(ok = wait(bars, &bars->p[1][i], j & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
           values(1);
           mma_commit(&bars->pv[i]);
           mma_commit(&bars->vempty[j & 1]);
-        } else if (j >= 0) {
-          mbar_arrive(&bars->vempty[j & 1]);
         }
-        if (j + 1 < nt) {
-          scores(j + 1);
-        } else if (next) {
-          mbar_arrive(&bars->kempty[(j + 1) & 1]);
-          mbar_arrive(&bars->turn[i]);
+        __syncwarp();
+      } else if (j >= 0) {
+        if (!(ok = wait(bars, &bars->vfull[j & 1], (j >> 1) & 1))) break;
+        if (elect_one()) mbar_arrive(&bars->vempty[j & 1]);
+        __syncwarp();
+      }
+      if (next) {
+        if (j >= 0 && j + 1 < nt) ok = wait(bars, {keys(j + 1), turn(j + 1), {&bars->pv[i], (uint32_t)j & 1}});
+        else ok = wait(bars, {keys(j + 1), turn(j + 1)});
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (j + 1 < nt) {
+            scores(j + 1);
+          } else {
+            mbar_arrive(&bars->kempty[(j + 1) & 1]);
+            mbar_arrive(&bars->turn[i]);
+          }
         }
       }
       __syncwarp();
