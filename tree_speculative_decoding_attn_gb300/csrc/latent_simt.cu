@@ -222,8 +222,9 @@ int splits_of(const SvLatentShape &s, int *chunk) {
   long long n = (s.latent_dim == 512 ? 152 : 304) / ctas;
   n = n > tiles ? tiles : n;
   n = n > kMaxSplits ? kMaxSplits : n < 1 ? 1 : n;  // (what the join holds)
-  *chunk = (tiles + (int)n - 1) / (int)n * kGrain;
-  return (s.max_prefix + s.n_nodes + *chunk - 1) / *chunk;
+  const int each = (tiles + (int)n - 1) / (int)n;  // tiles of a range
+  *chunk = each * kGrain;
+  return (tiles + each - 1) / each;  // (in tiles: keys and a range's length together may pass 32 bits)
 }
 
 template <int LAT>
