@@ -664,7 +664,8 @@ ROPE_DIM = 64    # rotary elements at the end of a latent row
 
 
 def tree_attn_latent_workspace_bytes(dtype, batch, n_nodes, hq, latent_dim, rope_dim, max_prefix):
-    return int(load().tree_attn_latent_workspace_bytes(_DT[dtype], batch, n_nodes, hq, latent_dim, rope_dim, max_prefix))
+    code = _DT.get(dtype, -1) if isinstance(dtype, torch.dtype) else int(dtype)     # (0 bytes for other types, as in C)
+    return int(load().tree_attn_latent_workspace_bytes(code, batch, n_nodes, hq, latent_dim, rope_dim, max_prefix))
 
 
 def tree_attn_verify_latent(q, cache, tree, prefix_len, anc_mask, out, max_prefix, scale, workspace=None,
