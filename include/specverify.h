@@ -515,8 +515,11 @@ int tree_attn_verify_latent_paged(const void *q, const void *pages, const int32_
  *   out      [total_q, hq, 128] bf16; rows of no sequence are left as they
  *            were
  *   max_q    host bound on a sequence's queries
- * All strides are positive multiples of 8 (SPEC_ERR_INVALID_ARG), addresses
- * 16-byte aligned.  head_dim 128 and rope_dim 64 (SPEC_ERR_UNSUPPORTED
+ * Strides are multiples of 8 below 2^38, no less than what they step over (128,
+ * rope_token 64), so that tokens and heads do not overlap; a head stride where
+ * hq is 1 and a token stride where total_kv is 1 may be anything.  Addresses are
+ * 16-byte aligned; total_q and total_kv are 1 or more (SPEC_ERR_INVALID_ARG; a
+ * batch without tokens is no call).  head_dim 128 and rope_dim 64 (SPEC_ERR_UNSUPPORTED
  * otherwise), hq <= 65535, batch <= 65535, total_q * hq <= 2^30, total_kv <=
  * 2^30, at most 2^23 queries a sequence.  A query before the sequence's first
  * key (n > m) gets zeros.  Offsets outside [0, total], a decreasing pair, or

@@ -797,7 +797,10 @@ int prompt_attn_latent(const void *q, const void *k, int64_t k_token, int64_t k_
   if (!q || !k || !k_rope || !v || !q_offsets || !kv_offsets || !out) return SPEC_ERR_INVALID_ARG;
   const int rc = prompt_check(batch, hq, head_dim, rope_dim, total_q, total_kv, max_q);
   if (rc != SPEC_OK) return rc;
-  // (strides are at least what they step over, and at most what a tensor map takes)
+  // strides that nothing steps by may be anything; the others are at least what
+  // they step over, and at most what a tensor map takes
+  if (hq == 1) k_head = v_head = 128;
+  if (total_kv == 1) k_token = v_token = 128, rope_token = 64;
   const struct { int64_t v; int least; } strides[] = {{k_token, 128}, {k_head, 128}, {rope_token, 64}, {v_token, 128}, {v_head, 128}};
   for (const auto &x : strides)
     if (x.v < x.least || x.v % 8 || x.v >= (1ll << 38)) return SPEC_ERR_INVALID_ARG;
