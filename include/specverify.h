@@ -458,10 +458,14 @@ int tree_attn_verify_window_paged(const void *q, const void *k_pages, const void
  * SPEC_MAX_NODES, batch <= 65535, batch * s_max and batch * n_nodes * hq <=
  * 2^30 (SPEC_ERR_UNSUPPORTED).  A node that sees nothing gets zeros; a NaN
  * score makes its row NaN.  One token of ordinary decoding is a tree of one
- * node.  bf16 runs on pairs of SMs: softmax statistics, sums and accumulators
- * are float32, and each probability is rounded to bf16 for the product with
- * the values (half a step, 2^-8 of it).  float32 runs on CUDA cores.  Results
- * are the same from run to run.  A prefix_len outside [0, max_prefix] sets
+ * node.  bf16 runs on tensor cores, on pairs of SMs or, with up to 16 rows
+ * (node, head) a sequence or few key tiles in all, on one SM a range of keys:
+ * softmax statistics, sums and accumulators are float32, and each probability
+ * is rounded to bf16 for the product with the values (half a step, 2^-8 of
+ * it).  float32 runs on CUDA cores.  Results are the same from run to run.
+ * max_prefix bounds the lengths and chooses the kernel: one far above them
+ * costs time, not more (64 rows over 300 keys: 11 us, 16 with a bound past
+ * which calls go to the pairs).  A prefix_len outside [0, max_prefix] sets
  * SPEC_DEV_CAPACITY and that sequence's output is left unwritten.
  *   workspace  device scratch of tree_attn_latent_workspace_bytes() bytes
  *            (16-byte aligned, uninitialised; may be NULL when that size is
@@ -496,7 +500,8 @@ int tree_attn_verify_latent_paged(const void *q, const void *pages, const int32_
  * form: the caller has expanded the latents into keys and values of every
  * head (one matrix product), the rotary key stays shared by the heads (the
  * pages have no counterpart; with many query tokens a sequence this form
- * needs a third of the absorbed form's operations).
+ * needs a third of the absorbed form's operations).  bf16 alone: prompts of a
+ * float32 cache go through tree_attn_verify_latent, 256 tokens a call.
  * Requests are packed one behind the other: sequence b's queries are rows
  * q_offsets[b] .. q_offsets[b+1] - 1 of q, its keys rows kv_offsets[b] ..
  * kv_offsets[b+1] - 1 of k, k_rope and v.  The queries are its last tokens:
@@ -861,12 +866,14 @@ int kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table, in
  * slots of one pool [num_blocks, hkv, block_size, head_dim] (a layer's K, V or
  * latents), or out of them.  A negative slot: not written, read as zeros; a
  * slot past the pool the same (SPEC_DEV_BAD_BLOCK).  A slot that is written
- * twice in a call ends up with a mixture of its rows.  Rows in the pool, or an
- * output over the slots, are refused (SPEC_ERR_INVALID_ARG).
+ * twice in a call ends up with a mixture of its rows.  No rows (n_rows < 1),
+ * rows in the pool, or an output over the slots, are refused
+ * (SPEC_ERR_INVALID_ARG).
  *
  * k_pages, v_pages [n_layers, num_blocks, hkv, block_size, head_dim] (16-byte
  * aligned, elem_bytes 2 or 4, head_dim * elem_bytes % 16 == 0; v_pages NULL: a
- * cache of one pool, as of latent rows).  workspace:
+ * cache of one pool, as of latent rows: nothing notices a V pool that is left
+ * out by mistake, K's pages alone are then moved).  workspace:
  * kv_pages_workspace_bytes() bytes, 16-byte aligned, uninitialised; calls
  * that may overlap on the GPU need separate ones.
  * ------------------------------------------------------------------ */

@@ -15,10 +15,12 @@
 //      outputs are scaled by
 //   PV: warp i takes dims [64 i, +64) (LAT 256: 32), 64 keys deep
 // Two barriers a tile; the load of the tile after next is issued behind the
-// first, when every warp is done with the tile before.  A tile takes 2700 to
-// 3000 cycles, HBM's share of one 3150: batch 64 of 16 heads over 4096 rows 59
-// us (5.1 TB/s), one sequence of 5000 rows 11.4 (start 4, one tile a CTA 2, partial
-// 1, join 3).
+// first, when every warp is done with the tile before.  A tile whose data are
+// there is 2700 to 3000 cycles of work; in a long stream a CTA takes 1.53 to 1.63
+// us a tile (3200 to 3400 cycles at 2.07 GHz), which is HBM's read rate (6.9 to 7.3
+// TB/s in all).  Batch 64 of 16 heads over 4096 rows 59 us: 27 tiles a CTA 44, the
+// rest start, partials and the join; one sequence of 5000 rows 11.4 (start 4, one
+// tile a CTA 2, partial 1, join 3).
 // Work: equal ranges of all (sequence, 16 rows) units, or whole units, a CTA each;
 // cut units leave float32 partials for a second kernel.  Every wait is bounded.
 #include <math.h>

@@ -118,8 +118,12 @@ __device__ __forceinline__ LatentRange latent_range(const Work &w, int part, int
   // (no more ranges than weight: each that begins inside a unit has a tile)
   long long n = total < parts ? total : parts;
   // The units of a sequence read the same rows.  Where those do not stay in L2,
-  // parts in halves of a unit let pairs of units read them at the same time: 4
-  // sequences of 4 units over 32768 keys, 76 parts 130 us, 72 (4.5 a unit) 117.
+  // parts in halves of a unit let pairs of units read them at the same time.  us
+  // with all parts / in halves: 4 sequences of 4 units over 32768 keys 127 / 115
+  // (76 and 72 parts, 4.5 a unit), 1 of 3 over 93000 80 / 75, 3 of 5 over 40000 125
+  // / 120, 2 of 8 over 50000 163 / 157, 16 of 3 over 8000 105 / 103, 2 of 2 over
+  // 60000 the same; 8 of 2 over 16384 72 / 78.  Lengths that differ (4 of 32000 to
+  // 32768: 123) put the cuts elsewhere in each sequence.
   if (w.RT > 1 && units * most == total && (long long)most * w.batch > w.far) {
     const long long even = quotient(2ll * parts, units) * units / 2;
     if (10 * even >= 9ll * parts && even < n) n = even;

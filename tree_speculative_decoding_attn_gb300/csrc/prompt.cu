@@ -23,13 +23,13 @@
 // first to be done, K(j + 2) follows V(j)), and two pieces for rotary columns.
 // What bounds it: two tiles' MMAs are 2560 cycles a key tile (2660 by their
 // shared-memory traffic), the chain S, softmax (1600), PV with its hand-offs
-// 3100 to 3400.  8192 tokens of 32 heads 450 us, 1.53 PFLOP/s, 491 (1.40) under
-// sustained load, at the power limit (1365 W).  Steps: one MMA warp and eight
-// softmax warps 4680 cycles, 527 us; a warp a tile 4060, 491; S in turns 3850,
-// 483; P in two parts 476; V no longer waiting for its one place 470; one wait
-// for several barriers, outputs through shared memory, and S(j + 1) behind a
-// wait for PV(j) (without it 3 % less, 432 to 465, by an order of products that
-// nothing promises) 450.  Without the exponentials (timing only) the same: not a
+// 3100 to 3400.  8192 tokens of 32 heads 449 to 472 us, 1.46 to 1.53 PFLOP/s, 491
+// (1.40) under sustained load, at the power limit (1365 W).  Steps: one MMA warp
+// and eight softmax warps 4680 cycles, 527 us; a warp a tile 4060, 491; S in
+// turns 3850, 483; P in two parts 476; V no longer waiting for its one place
+// 470; one wait for several barriers, outputs through shared memory, and S(j + 1)
+// behind a wait for PV(j) (without it 3 % less, 432 to 465, by an order of
+// products that nothing promises) 450.  Without the exponentials (timing only) the same: not a
 // limit of the exponential unit.  Not kept: scalar instead of two-wide float32
 // arithmetic (+4 %), P in parts of 48 and 16 or 16 and 48 keys (+4 %).
 // TMEM columns: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512).
