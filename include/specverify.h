@@ -464,7 +464,7 @@ int tree_attn_verify_window_paged(const void *q, const void *k_pages, const void
  * is rounded to bf16 for the product with the values (half a step, 2^-8 of
  * it).  float32 runs on CUDA cores.  Results are the same from run to run.
  * max_prefix bounds the lengths and chooses the kernel: one far above them
- * costs time, not more (64 rows over 300 keys: 11 us, 16 with a bound past
+ * may cost time (64 rows over 300 keys take 11 us, and 16 with a bound past
  * which calls go to the pairs).  A prefix_len outside [0, max_prefix] sets
  * SPEC_DEV_CAPACITY and that sequence's output is left unwritten.
  *   workspace  device scratch of tree_attn_latent_workspace_bytes() bytes
@@ -501,7 +501,7 @@ int tree_attn_verify_latent_paged(const void *q, const void *pages, const int32_
  * head (one matrix product), the rotary key stays shared by the heads (the
  * pages have no counterpart; with many query tokens a sequence this form
  * needs a third of the absorbed form's operations).  bf16 alone: prompts of a
- * float32 cache go through tree_attn_verify_latent, 256 tokens a call.
+ * float32 cache go through tree_attn_verify_latent, as chains of 256 nodes.
  * Requests are packed one behind the other: sequence b's queries are rows
  * q_offsets[b] .. q_offsets[b+1] - 1 of q, its keys rows kv_offsets[b] ..
  * kv_offsets[b+1] - 1 of k, k_rope and v.  The queries are its last tokens:
